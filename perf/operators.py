@@ -355,7 +355,7 @@ def run(state):
                                       s["scale"], out=s["out"], workspace=s["workspace"])
         if s["kind"] == "prefill":
             if "workspace" not in s:
-                s["workspace"] = pkv.prefill_fp8_workspace(s["batch"], s["hq"], s["hkv"], D, s["block"], s["max_q"], s["total_k"])
+                s["workspace"] = pkv.prefill_fp8_workspace(s["batch"], s["hq"], s["hkv"], D, s["max_q"], s["max_k"], s["total_k"])
             return pkv.pkv_prefill_varlen_fp8(s["q"], s["k_cache"], s["v_cache"], s["k_scale"], s["v_scale"], s["cu_q"], s["cu_k"], s["tables"],
                                               s["max_q"], s["max_k"], s["total_k"], s["scale"], out=s["out"], workspace=s["workspace"])
         return pkv.pkv_sample_filtered(s["logits"], s["t"], s["top_k"], s["top_p"], s["min_p"], s["seed"], s["offset"], out_ids=s["ids"])
