@@ -11,6 +11,10 @@
  *   a5  pkv_sample           temperature sampling by exponential race
  *   f2  pkv_rope_store_kvcache  rotary embedding of Q/K fused into the a2 write
  *
+ * and, beside them, the same writes and attentions on an 8-bit KV cache
+ * (pkv_*_fp8) and sampling among the tokens that top-k, top-p and min-p keep
+ * (pkv_sample_filtered).
+ *
  * Conventions shared by every call
  * --------------------------------
  * - Every pointer argument is DEVICE memory owned by the caller, unless stated.
@@ -56,6 +60,8 @@ extern "C" {
 #endif
 
 typedef uint16_t pkv_bf16;     /* raw bfloat16 bits */
+typedef uint8_t pkv_e4m3;      /* raw 8-bit float: sign, 4 exponent bits, 3 mantissa bits, no infinities */
+typedef uint8_t pkv_e8m0;      /* power of two: byte b stands for 2^(b - 127), 255 for NaN */
 typedef void *pkv_stream_t;    /* cudaStream_t */
 
 typedef enum {
@@ -75,7 +81,8 @@ enum {
     PKV_DEVERR_TEMPERATURE = 4,  /* temperature <= 0, inf or NaN */
     PKV_DEVERR_TIMEOUT = 5,      /* an mbarrier wait exceeded its limit */
     PKV_DEVERR_BLOCK_TABLE = 6,  /* a position past max_blocks_per_seq * block_size */
-    PKV_DEVERR_PLAN = 7          /* the prefill workspace holds no plan for these arguments */
+    PKV_DEVERR_PLAN = 7,         /* the prefill workspace holds no plan for these arguments */
+    PKV_DEVERR_FILTER = 8        /* top_p outside (0, 1], min_p outside [0, 1], or either NaN */
 };
 
 /* ABI version; bumped on any signature change. */
@@ -333,6 +340,101 @@ PKV_API pkv_status pkv_decode_noalloc(const pkv_bf16 *q, const pkv_bf16 *k_cache
                               pkv_bf16 *out, pkv_stream_t stream);
 
 /*
+ * 8-bit KV cache.  The pools keep the block layout, one byte per number, and
+ * every row (one token of one KV head) has a scale:
+ *
+ *   k_cache, v_cache  e4m3 [num_blocks, block_size, num_kv_heads, 128]
+ *   k_scale, v_scale  e8m0 [num_blocks, num_kv_heads, block_size]
+ *
+ * A row x of 128 numbers is held as codes e4m3(x * 2^-e), rounded to nearest
+ * even, with e the smallest exponent >= -126 for which max|x| <= 448 * 2^e, and
+ * the scale byte e + 127.  It reads as code * 2^e.  A row with an infinity or a
+ * NaN gets the scale byte 255 and codes 0 and reads as NaN.  (A floating-point
+ * code gains no relative precision from a finer scale, and a power of two makes
+ * the value read exact in bf16.)  Half the cache's bytes, so half the time of a
+ * long context's decode step; a stored number is off by at most 2^-4 of itself
+ * plus 2^(e - 10).
+ * Pools need 16-byte aligned bases (PKV_ERR_UNSUPPORTED otherwise), scale
+ * pools too.  head_dim = 128, block sizes and group sizes as everywhere.
+ */
+
+/*
+ * Append rows to an 8-bit cache: the scatter of pkv_store_kvcache with the
+ * rounding above.  Arguments, skipped rows (slot < 0), errors (a slot past the
+ * pool: PKV_DEVERR_SLOT, skipped) and races of equal slots as there.  Exact: the
+ * codes and scales are those of the definition, bit for bit.
+ */
+PKV_API pkv_status pkv_store_kvcache_fp8(const pkv_bf16 *k, const pkv_bf16 *v, int64_t n_tokens,
+                                 int64_t k_token_stride, int64_t v_token_stride,
+                                 const int32_t *slot_mapping, pkv_e4m3 *k_cache, pkv_e4m3 *v_cache,
+                                 pkv_e8m0 *k_scale, pkv_e8m0 *v_scale, int32_t num_blocks,
+                                 int32_t block_size, int32_t num_kv_heads, int32_t head_dim,
+                                 pkv_stream_t stream);
+
+/*
+ * pkv_rope_store_kvcache into an 8-bit cache: Q rotated into q_out (bf16), K
+ * rotated and V unchanged rounded into the pools.  The rotated K is rounded once,
+ * from fp32.  q and q_out both NULL (rotate and store K only) or both non-NULL;
+ * q_out may equal q (equal strides).  head_dim must be 128.
+ */
+PKV_API pkv_status pkv_rope_store_kvcache_fp8(const pkv_bf16 *q, int64_t q_token_stride, pkv_bf16 *q_out,
+                                      int64_t q_out_token_stride, const pkv_bf16 *k, int64_t k_token_stride,
+                                      const pkv_bf16 *v, int64_t v_token_stride, const int32_t *positions,
+                                      int64_t n_tokens, int32_t num_heads, int32_t num_kv_heads,
+                                      int32_t head_dim, double rope_base, const int32_t *slot_mapping,
+                                      pkv_e4m3 *k_cache, pkv_e4m3 *v_cache, pkv_e8m0 *k_scale,
+                                      pkv_e8m0 *v_scale, int32_t num_blocks, int32_t block_size,
+                                      pkv_stream_t stream);
+
+/*
+ * pkv_decode over an 8-bit cache.  Arguments, errors, empty sequences and the
+ * workspace rules as pkv_decode, with a workspace of
+ * pkv_decode_fp8_workspace_size bytes, 256-byte aligned.  Results are
+ * deterministic.  Scores and the softmax sum are fp32; the weight of each key,
+ * times its value's scale relative to the largest such product seen, is rounded
+ * to f16 (relative error 2^-11) for the product with the values.
+ */
+PKV_API size_t pkv_decode_fp8_workspace_size(int32_t batch, int32_t num_heads, int32_t num_kv_heads,
+                                     int32_t head_dim);
+
+PKV_API pkv_status pkv_decode_fp8(const pkv_bf16 *q, const pkv_e4m3 *k_cache, const pkv_e4m3 *v_cache,
+                          const pkv_e8m0 *k_scale, const pkv_e8m0 *v_scale, const int32_t *block_tables,
+                          int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t batch,
+                          int32_t max_context_len, int32_t num_heads, int32_t num_kv_heads,
+                          int32_t head_dim, int32_t block_size, int32_t num_blocks, float softmax_scale,
+                          pkv_bf16 *out, void *workspace, size_t workspace_bytes, pkv_stream_t stream);
+
+/*
+ * pkv_prefill_varlen over an 8-bit cache.  Arguments and errors as
+ * pkv_prefill_varlen, and
+ *
+ *   total_k    bound on the keys of all sequences together (host-known)
+ *   workspace  >= pkv_prefill_fp8_workspace_size(num_seqs, num_heads, num_kv_heads,
+ *              head_dim, max_seqlen_q, max_seqlen_k, total_k) bytes, 256-byte
+ *              aligned: the work list, and the keys and values the batch attends
+ *              to as bf16 (512 bytes per key and KV head).  Scratch, needs no
+ *              initialisation; calls that may overlap need one each.
+ *
+ * A sequence that does not fit total_k or max_seqlen_k records
+ * PKV_DEVERR_SEQLENS; its output rows are unspecified.  The result is bit for
+ * bit that of pkv_prefill_varlen over a bf16 cache that holds the values read
+ * (exact for exponents e >= -117; below that bf16 is subnormal and rounds).
+ */
+PKV_API size_t pkv_prefill_fp8_workspace_size(int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads,
+                                      int32_t head_dim, int32_t max_seqlen_q, int32_t max_seqlen_k,
+                                      int64_t total_k);
+
+PKV_API pkv_status pkv_prefill_varlen_fp8(const pkv_bf16 *q, const pkv_e4m3 *k_cache, const pkv_e4m3 *v_cache,
+                                  const pkv_e8m0 *k_scale, const pkv_e8m0 *v_scale,
+                                  const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                                  const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                  int32_t num_seqs, int32_t total_q, int32_t max_seqlen_q,
+                                  int32_t max_seqlen_k, int64_t total_k, int32_t num_heads,
+                                  int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                  int32_t num_blocks, float softmax_scale, pkv_bf16 *out, void *workspace,
+                                  size_t workspace_bytes, pkv_stream_t stream);
+
+/*
  * a5. Temperature sampling by exponential race.
  * Visual atlas fig. 23: the engine samples with temperature only, as an
  * exponential race: winner = argmax_v p_v / e_v (= argmin e_v / p_v), with
@@ -365,6 +467,41 @@ PKV_API pkv_status pkv_sample(const float *logits, int32_t batch, int32_t vocab,
 PKV_API pkv_status pkv_sample_dev(const float *logits, int32_t batch, int32_t vocab, int64_t row_stride,
                           const float *temperatures, const uint64_t *seed_offset, int64_t *out_ids,
                           pkv_stream_t stream);
+
+/*
+ * Sampling among the tokens that a row's filters keep.  With z_v =
+ * (logits_v - max logits) / T, tokens ordered by logit (equal logits: the lower
+ * index first), a row keeps, in this sequence,
+ *
+ *   top_k  int32 [batch]  the first top_k tokens; top_k <= 0: all
+ *   top_p  fp32 [batch]   in (0, 1]: of those, every token before which the
+ *          weights e^z in the order sum to less than top_p times the weights of
+ *          all of those (the first one always); 1: all
+ *   min_p  fp32 [batch]   in [0, 1]: of those, the tokens with z_v >= ln(min_p),
+ *          i.e. at least min_p times as likely as the most likely one; 0: all
+ *
+ * and out_ids is the race of pkv_sample among the kept tokens: argmax z_v -
+ * ln e_v with the noise of the same seed, offset, row and column.  With every
+ * filter off the winner is pkv_sample's.  Each of top_k, top_p and min_p may be
+ * NULL (off for every row).  A -inf or NaN logit is never kept and counts
+ * nowhere; a +inf logit wins, the lowest index among several.  A row with no
+ * logit above -inf gets -1; a row with an invalid temperature or filter gets -1 and
+ * records PKV_DEVERR_TEMPERATURE or PKV_DEVERR_FILTER with info = row.
+ * vocab <= 2^24.  Other arguments as pkv_sample; pkv_sample_filtered_dev reads
+ * {seed, offset} from device memory as pkv_sample_dev does.
+ * Weights are fp32 and their sums fp32 within a thread, fp64 across threads: a
+ * token is decided as in exact arithmetic unless top_p * sum lies within about
+ * 1e-7 of a running sum.  Results do not depend on timing.
+ */
+PKV_API pkv_status pkv_sample_filtered(const float *logits, int32_t batch, int32_t vocab, int64_t row_stride,
+                               const float *temperatures, const int32_t *top_k, const float *top_p,
+                               const float *min_p, uint64_t seed, uint64_t offset, int64_t *out_ids,
+                               pkv_stream_t stream);
+
+PKV_API pkv_status pkv_sample_filtered_dev(const float *logits, int32_t batch, int32_t vocab, int64_t row_stride,
+                                   const float *temperatures, const int32_t *top_k, const float *top_p,
+                                   const float *min_p, const uint64_t *seed_offset, int64_t *out_ids,
+                                   pkv_stream_t stream);
 
 /*
  * Read (and optionally clear) the current device's error word.  HOST output

@@ -20,5 +20,9 @@ sampler
     temperature sampler's exponential race.
 rope
     rotary position embedding of Q and K before the KV write (V untouched).
+fp8_cache
+    the 8-bit cache's row format (e4m3 codes, a power-of-two scale) and its scatter.
+filtered
+    top-k, top-p and min-p before the race.
 """
-from . import paged_attention, rope, sampler  # noqa: F401
+from . import filtered, fp8_cache, paged_attention, rope, sampler  # noqa: F401

@@ -16,6 +16,10 @@ Functions carry the C names:
 ``pkv_prefill_varlen``     varlen prefill attention with the offset causal mask
 ``pkv_decode``             single-token decode attention over block tables
 ``pkv_sample``             temperature sampling by exponential race
+``pkv_sample_filtered``    the same race among what top-k, top-p and min-p keep
+``pkv_*_fp8``              the writes and attentions on an 8-bit KV cache: e4m3
+                           pools (``torch.float8_e4m3fn``) with one power-of-two
+                           scale per row (``torch.float8_e8m0fnu``)
 =========================  ================================================
 """
 from __future__ import annotations
@@ -33,6 +37,9 @@ __all__ = [
     "pkv_decode_workspace_size", "pkv_decode", "pkv_sample", "pkv_get_device_error", "pkv_check_wait_timeout",
     "WAIT_CHECK_INFO",
     "decode_workspace", "pkv_decode_append", "pkv_decode_noalloc", "pkv_sample_dev", "pkv_rope_store_kvcache", "DecodeAppendCall", "DEVERR",
+    "pkv_store_kvcache_fp8", "pkv_rope_store_kvcache_fp8", "pkv_decode_fp8_workspace_size", "decode_fp8_workspace",
+    "pkv_decode_fp8", "pkv_prefill_fp8_workspace_size", "prefill_fp8_workspace", "pkv_prefill_varlen_fp8",
+    "pkv_sample_filtered", "pkv_sample_filtered_dev",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -41,7 +48,7 @@ _lib: Optional[ctypes.CDLL] = None
 
 DEVERR = {0: "none", 1: "block id outside pool", 2: "slot outside pool", 3: "sequence lengths",
           4: "temperature", 5: "pipeline wait timed out", 6: "position past block table",
-          7: "no prefill plan for these arguments in the workspace"}
+          7: "no prefill plan for these arguments in the workspace", 8: "sampling filter"}
 
 _c_int32 = ctypes.c_int32
 _c_int64 = ctypes.c_int64
@@ -103,6 +110,22 @@ def load() -> ctypes.CDLL:
         "pkv_sample": (ctypes.c_int, [_c_ptr, _c_int32, _c_int32, _c_int64, _c_ptr, _c_u64, _c_u64, _c_ptr,
                                       _c_ptr]),
         "pkv_sample_dev": (ctypes.c_int, [_c_ptr, _c_int32, _c_int32, _c_int64, _c_ptr, _c_ptr, _c_ptr, _c_ptr]),
+        "pkv_store_kvcache_fp8": (ctypes.c_int, [_c_ptr, _c_ptr, _c_int64, _c_int64, _c_int64, _c_ptr, _c_ptr, _c_ptr,
+                                                 _c_ptr, _c_ptr, _c_int32, _c_int32, _c_int32, _c_int32, _c_ptr]),
+        "pkv_rope_store_kvcache_fp8": (ctypes.c_int, [_c_ptr, _c_int64, _c_ptr, _c_int64, _c_ptr, _c_int64, _c_ptr,
+                                                      _c_int64, _c_ptr, _c_int64, _c_int32, _c_int32, _c_int32,
+                                                      ctypes.c_double, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr,
+                                                      _c_int32, _c_int32, _c_ptr]),
+        "pkv_decode_fp8_workspace_size": (_c_size, [_c_int32] * 4),
+        "pkv_decode_fp8": (ctypes.c_int, [_c_ptr] * 6 + [_c_int32, _c_ptr] + [_c_int32] * 7 + [_c_float, _c_ptr, _c_ptr,
+                                                                                              _c_size, _c_ptr]),
+        "pkv_prefill_fp8_workspace_size": (_c_size, [_c_int32] * 6 + [_c_int64]),
+        "pkv_prefill_varlen_fp8": (ctypes.c_int, [_c_ptr] * 8 + [_c_int32] * 5 + [_c_int64] + [_c_int32] * 5 +
+                                   [_c_float, _c_ptr, _c_ptr, _c_size, _c_ptr]),
+        "pkv_sample_filtered": (ctypes.c_int, [_c_ptr, _c_int32, _c_int32, _c_int64, _c_ptr, _c_ptr, _c_ptr, _c_ptr,
+                                               _c_u64, _c_u64, _c_ptr, _c_ptr]),
+        "pkv_sample_filtered_dev": (ctypes.c_int, [_c_ptr, _c_int32, _c_int32, _c_int64, _c_ptr, _c_ptr, _c_ptr, _c_ptr,
+                                                   _c_ptr, _c_ptr, _c_ptr]),
         "pkv_get_device_error": (ctypes.c_int, [ctypes.POINTER(_c_int32), ctypes.POINTER(_c_int32), _c_int32]),
         "pkv_check_wait_timeout": (ctypes.c_int, [ctypes.c_void_p]),
     }
@@ -540,6 +563,239 @@ def pkv_sample_dev(logits: torch.Tensor, temperatures: torch.Tensor, seed_offset
         _raise(load().pkv_sample_dev(_ptr(logits), batch, vocab, _row_stride(logits), _ptr(temperatures),
                                      _ptr(seed_offset),
                                      _ptr(out_ids), _stream(stream)), "pkv_sample_dev")
+    return out_ids
+
+
+# ---------------------------------------------------------------------------
+# 8-bit KV cache
+# ---------------------------------------------------------------------------
+
+def _pools_fp8(k_cache, v_cache, k_scale, v_scale):
+    """Shape (num_blocks, block_size, num_kv_heads, head_dim) of an 8-bit cache, checked."""
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _check(t, name, torch.float8_e4m3fn, 4)
+    nb, bs, hkv, d = k_cache.shape
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache shapes differ")
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        _check(t, name, torch.float8_e8m0fnu, 3)
+        if tuple(t.shape) != (nb, hkv, bs):
+            raise ValueError(f"{name} must be [{nb}, {hkv}, {bs}] (num_blocks, num_kv_heads, block_size)")
+    return nb, bs, hkv, d
+
+
+def _rows(t, name, hkv, d):
+    _check(t, name, torch.bfloat16, 3, contiguous=False)
+    if tuple(t.shape[1:]) != (hkv, d) or t.stride(2) != 1 or (hkv > 1 and t.stride(1) != d):
+        raise ValueError(f"{name} must be [n, {hkv}, {d}] with contiguous rows")
+
+
+def _token_stride(t: torch.Tensor) -> int:
+    """Elements between tokens; a single token's stride is meaningless (it may be 0), so use its length."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def pkv_store_kvcache_fp8(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
+                          v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor, stream=None) -> None:
+    """Round every row of k and v to e4m3 codes with a power-of-two scale and write both to its slot
+    of the 8-bit pools; slot < 0 skips."""
+    nb, bs, hkv, d = _pools_fp8(k_cache, v_cache, k_scale, v_scale)
+    _rows(k, "k", hkv, d)
+    _rows(v, "v", hkv, d)
+    _check(slot_mapping, "slot_mapping", torch.int32, 1)
+    n = k.shape[0]
+    if v.shape[0] != n or slot_mapping.shape[0] != n:
+        raise ValueError("k, v and slot_mapping disagree on the token count")
+    with _on_device(k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale, stream=stream):
+        _raise(load().pkv_store_kvcache_fp8(_ptr(k), _ptr(v), n, _token_stride(k), _token_stride(v), _ptr(slot_mapping),
+                                            _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), nb, bs, hkv, d,
+                                            _stream(stream)), "pkv_store_kvcache_fp8")
+
+
+def pkv_rope_store_kvcache_fp8(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                               slot_mapping: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                               k_scale: torch.Tensor, v_scale: torch.Tensor, rope_base: float,
+                               q_out: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """Rotate q and k by `positions`; write rotated k and plain v, rounded to 8 bits, to the pools.
+
+    Returns the rotated q in bf16 (a new tensor, or `q_out`; pass ``q_out=q`` to rotate in place)."""
+    nb, bs, hkv, d = _pools_fp8(k_cache, v_cache, k_scale, v_scale)
+    _rows(k, "k", hkv, d)
+    _rows(v, "v", hkv, d)
+    _check(positions, "positions", torch.int32, 1)
+    _check(slot_mapping, "slot_mapping", torch.int32, 1)
+    n = k.shape[0]
+    if v.shape[0] != n or slot_mapping.shape[0] != n or positions.shape[0] != n:
+        raise ValueError("k, v, positions and slot_mapping disagree on the token count")
+    hq = 0
+    if q is not None:
+        _check(q, "q", torch.bfloat16, 3, contiguous=False)
+        hq = q.shape[1]
+        _rows(q, "q", hq, d)
+        if q.shape[0] != n:
+            raise ValueError("q and k disagree on the token count")
+        if q_out is None:
+            q_out = torch.empty(n, hq, d, dtype=torch.bfloat16, device=q.device)
+        _rows(q_out, "q_out", hq, d)
+        if q_out.shape[0] != n:
+            raise ValueError("q_out must match q's shape")
+    elif q_out is not None:
+        raise ValueError("q_out given without q")
+    with _on_device(q, q_out, k, v, positions, slot_mapping, k_cache, v_cache, k_scale, v_scale, stream=stream):
+        _raise(load().pkv_rope_store_kvcache_fp8(_ptr(q), _token_stride(q) if q is not None else 0, _ptr(q_out),
+                                                 _token_stride(q_out) if q_out is not None else 0, _ptr(k),
+                                                 _token_stride(k), _ptr(v), _token_stride(v), _ptr(positions), n, hq,
+                                                 hkv, d, float(rope_base), _ptr(slot_mapping), _ptr(k_cache),
+                                                 _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), nb, bs, _stream(stream)),
+               "pkv_rope_store_kvcache_fp8")
+    return q_out
+
+
+def pkv_decode_fp8_workspace_size(batch: int, num_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    return int(load().pkv_decode_fp8_workspace_size(batch, num_heads, num_kv_heads, head_dim))
+
+
+def decode_fp8_workspace(batch: int, num_heads: int, num_kv_heads: int, head_dim: int, device=None) -> torch.Tensor:
+    """A uint8 device buffer of the size pkv_decode_fp8 needs (256-byte aligned by the allocator)."""
+    n = pkv_decode_fp8_workspace_size(batch, num_heads, num_kv_heads, head_dim)
+    if n == 0:
+        raise PkvError(2, "pkv_decode_fp8_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def pkv_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                   v_scale: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor, max_context_len: int,
+                   softmax_scale: float, out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """Decode attention over an 8-bit cache: one query token per sequence, context_lens[b] keys."""
+    nb, bs, hkv, d = _pools_fp8(k_cache, v_cache, k_scale, v_scale)
+    _check(q, "q", torch.bfloat16, 3)
+    _check(block_tables, "block_tables", torch.int32, 2)
+    _check(context_lens, "context_lens", torch.int32, 1)
+    batch, hq, dq = q.shape
+    if dq != d or context_lens.shape[0] != batch or block_tables.shape[0] != batch:
+        raise ValueError("q, context_lens and block_tables disagree")
+    if out is None:
+        out = torch.empty_like(q)
+    _check(out, "out", torch.bfloat16, 3)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if workspace is None:
+        with _on_device(q):
+            workspace = decode_fp8_workspace(batch, hq, hkv, d, q.device)
+    _check(workspace, "workspace", torch.uint8, 1)
+    with _on_device(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, out, workspace, stream=stream):
+        _raise(load().pkv_decode_fp8(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                                     _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), batch,
+                                     int(max_context_len), hq, hkv, d, bs, nb, float(softmax_scale), _ptr(out),
+                                     _ptr(workspace), workspace.numel(), _stream(stream)), "pkv_decode_fp8")
+    return out
+
+
+def pkv_prefill_fp8_workspace_size(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int, max_seqlen_q: int,
+                                   max_seqlen_k: int, total_k: int) -> int:
+    return int(load().pkv_prefill_fp8_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, max_seqlen_q,
+                                                     max_seqlen_k, total_k))
+
+
+def prefill_fp8_workspace(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int, max_seqlen_q: int,
+                          max_seqlen_k: int, total_k: int, device=None) -> torch.Tensor:
+    """A uint8 device buffer of the size pkv_prefill_varlen_fp8 needs for these bounds."""
+    n = pkv_prefill_fp8_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, int(max_seqlen_q),
+                                       int(max_seqlen_k), int(total_k))
+    if n == 0:
+        raise PkvError(2, "pkv_prefill_fp8_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def pkv_prefill_varlen_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                           v_scale: torch.Tensor, cu_seqlens_q: torch.Tensor, cu_seqlens_k: torch.Tensor,
+                           block_tables: torch.Tensor, max_seqlen_q: int, max_seqlen_k: int, total_k: int,
+                           softmax_scale: float, out: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Varlen prefill attention over an 8-bit cache (the new tokens' K/V already stored).  `total_k`
+    bounds the keys of all sequences together."""
+    nb, bs, hkv, d = _pools_fp8(k_cache, v_cache, k_scale, v_scale)
+    _check(q, "q", torch.bfloat16, 3)
+    _check(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1)
+    _check(cu_seqlens_k, "cu_seqlens_k", torch.int32, 1)
+    _check(block_tables, "block_tables", torch.int32, 2)
+    total_q, hq, dq = q.shape
+    if dq != d:
+        raise ValueError("q head_dim differs from the pool's")
+    num_seqs = cu_seqlens_q.shape[0] - 1
+    if cu_seqlens_k.shape[0] != num_seqs + 1 or block_tables.shape[0] != num_seqs:
+        raise ValueError("cu_seqlens_q, cu_seqlens_k and block_tables disagree on the sequence count")
+    if out is None:
+        out = torch.empty_like(q)
+    _check(out, "out", torch.bfloat16, 3)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if workspace is None:
+        workspace = prefill_fp8_workspace(num_seqs, hq, hkv, d, max_seqlen_q, max_seqlen_k, total_k, q.device)
+    _check(workspace, "workspace", torch.uint8, 1)
+    with _on_device(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, cu_seqlens_k, block_tables, out, workspace,
+                    stream=stream):
+        _raise(load().pkv_prefill_varlen_fp8(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                                             _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), _ptr(block_tables),
+                                             block_tables.shape[1], num_seqs, total_q, int(max_seqlen_q),
+                                             int(max_seqlen_k), int(total_k), hq, hkv, d, bs, nb, float(softmax_scale),
+                                             _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream)),
+               "pkv_prefill_varlen_fp8")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# sampling with filters
+# ---------------------------------------------------------------------------
+
+def _filter_args(logits, temperatures, top_k, top_p, min_p, out_ids):
+    """Checked arguments of a filtered sampling call; allocates out_ids if None."""
+    _check(logits, "logits", torch.float32, 2, contiguous=False)
+    if logits.stride(1) != 1 and logits.shape[1] > 1:
+        raise ValueError("logits rows must be contiguous")
+    batch = logits.shape[0]
+    if out_ids is None:
+        out_ids = torch.empty(batch, dtype=torch.int64, device=logits.device)
+    for name, t, dtype in (("temperatures", temperatures, torch.float32), ("top_k", top_k, torch.int32),
+                           ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32),
+                           ("out_ids", out_ids, torch.int64)):
+        if t is None and name in ("top_k", "top_p", "min_p"):
+            continue
+        _check(t, name, dtype, 1)
+        if t.shape[0] != batch:
+            raise ValueError(f"{name} must have one entry per row of logits ({batch}), got {t.shape[0]}")
+    return out_ids
+
+
+def pkv_sample_filtered(logits: torch.Tensor, temperatures: torch.Tensor, top_k: Optional[torch.Tensor],
+                        top_p: Optional[torch.Tensor], min_p: Optional[torch.Tensor], seed: int, offset: int = 0,
+                        out_ids: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The exponential race among the tokens that top-k, then top-p, then min-p keep (one setting per
+    row; None: off for every row); returns int64 ids [batch].  All off: pkv_sample's winners."""
+    out_ids = _filter_args(logits, temperatures, top_k, top_p, min_p, out_ids)
+    batch, vocab = logits.shape
+    with _on_device(logits, temperatures, top_k, top_p, min_p, out_ids, stream=stream):
+        _raise(load().pkv_sample_filtered(_ptr(logits), batch, vocab, _row_stride(logits), _ptr(temperatures),
+                                          _ptr(top_k), _ptr(top_p), _ptr(min_p), int(seed) & (2 ** 64 - 1),
+                                          int(offset) & (2 ** 64 - 1), _ptr(out_ids), _stream(stream)),
+               "pkv_sample_filtered")
+    return out_ids
+
+
+def pkv_sample_filtered_dev(logits: torch.Tensor, temperatures: torch.Tensor, top_k: Optional[torch.Tensor],
+                            top_p: Optional[torch.Tensor], min_p: Optional[torch.Tensor], seed_offset: torch.Tensor,
+                            out_ids: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """pkv_sample_filtered with {seed, offset} read from a device int64 tensor of 2 elements."""
+    out_ids = _filter_args(logits, temperatures, top_k, top_p, min_p, out_ids)
+    _check(seed_offset, "seed_offset", torch.int64, 1)
+    if seed_offset.numel() != 2:
+        raise ValueError("seed_offset holds {seed, offset}")
+    batch, vocab = logits.shape
+    with _on_device(logits, temperatures, top_k, top_p, min_p, seed_offset, out_ids, stream=stream):
+        _raise(load().pkv_sample_filtered_dev(_ptr(logits), batch, vocab, _row_stride(logits), _ptr(temperatures),
+                                              _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(seed_offset), _ptr(out_ids),
+                                              _stream(stream)), "pkv_sample_filtered_dev")
     return out_ids
 
 

@@ -71,6 +71,15 @@ bool supported_shape(int num_heads, int num_kv_heads, int head_dim, int block_si
            block_size % kBlockQuantum == 0;
 }
 
+// Pair i advances base^(-2i/d) radians per position: the fraction of a turn in 64-bit fixed
+// point (whole turns change no angle).
+void rope_turns(double rope_base, int head_dim, uint64_t* turns) {
+    for (int i = 0; i < head_dim / 2; ++i) {
+        const double t = pow(rope_base, -2.0 * i / head_dim) / 6.283185307179586;
+        turns[i] = static_cast<uint64_t>(ldexp(t - floor(t), 64));   // t - floor(t) < 1: in range
+    }
+}
+
 // One thread waits on a barrier that nothing completes, through the bounded wait all the
 // kernels use; it gives up after the limit, records the timeout and the kernel returns.
 __global__ void wait_check_kernel(int* err) {
@@ -235,12 +244,7 @@ pkv_status pkv_rope_store_kvcache(const pkv_bf16* q, int64_t q_token_stride, pkv
     a.num_heads = num_heads;
     a.num_kv_heads = num_kv_heads;
     a.head_dim = head_dim;
-    // pair i advances base^(-2i/d) radians per position: store the fraction of a
-    // turn in 64-bit fixed point (whole turns change no angle)
-    for (int i = 0; i < head_dim / 2; ++i) {
-        const double t = pow(rope_base, -2.0 * i / head_dim) / 6.283185307179586;
-        a.turns[i] = static_cast<uint64_t>(ldexp(t - floor(t), 64));   // t - floor(t) < 1: in range
-    }
+    rope_turns(rope_base, head_dim, a.turns);
     if (rope_store_threads(a) == 0) return PKV_ERR_UNSUPPORTED;
     int* err = device_error_word();
     if (!err) return PKV_ERR_CUDA;
@@ -435,6 +439,187 @@ pkv_status pkv_decode_append(const pkv_bf16* q, const pkv_bf16* k_new, const pkv
     return launch_decode(a, err, as_stream(stream));
 }
 
+namespace {
+
+bool misaligned16(const void* a, const void* b = nullptr, const void* c = nullptr, const void* d = nullptr) {
+    return ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) | reinterpret_cast<uintptr_t>(c) |
+             reinterpret_cast<uintptr_t>(d)) & 15) != 0;
+}
+
+// Host checks and argument packing shared by the two appends; positions and rope_base are the
+// rotating one's (rotate: positions must be given).
+pkv_status store_fp8_call(const pkv_bf16* q, int64_t q_token_stride, pkv_bf16* q_out, int64_t q_out_token_stride,
+                          const pkv_bf16* k, int64_t k_token_stride, const pkv_bf16* v, int64_t v_token_stride,
+                          const int32_t* positions, bool rotate, int64_t n_tokens, int32_t num_heads,
+                          int32_t num_kv_heads, int32_t head_dim, double rope_base, const int32_t* slot_mapping,
+                          pkv_e4m3* k_cache, pkv_e4m3* v_cache, pkv_e8m0* k_scale, pkv_e8m0* v_scale,
+                          int32_t num_blocks, int32_t block_size, pkv_stream_t stream) {
+    if (n_tokens < 0 || num_heads < 0 || num_kv_heads <= 0 || head_dim <= 0 || num_blocks <= 0 || block_size <= 0)
+        return PKV_ERR_INVALID_ARG;
+    if (rotate && (!(rope_base > 0.0) || rope_base == INFINITY)) return PKV_ERR_INVALID_ARG;
+    if ((q == nullptr) != (q_out == nullptr) || (q != nullptr && num_heads == 0)) return PKV_ERR_INVALID_ARG;
+    if (head_dim != kHeadDim || block_size % kBlockQuantum) return PKV_ERR_UNSUPPORTED;
+    if (num_heads > 4096 || num_kv_heads > 4096) return PKV_ERR_UNSUPPORTED;
+    const int64_t kv_row = static_cast<int64_t>(num_kv_heads) * head_dim;
+    const int64_t q_row = static_cast<int64_t>(num_heads) * head_dim;
+    if (k_token_stride < kv_row || v_token_stride < kv_row) return PKV_ERR_INVALID_ARG;
+    if (q && (q_token_stride < q_row || q_out_token_stride < q_row)) return PKV_ERR_INVALID_ARG;
+    if (q && q == q_out && q_token_stride != q_out_token_stride) return PKV_ERR_INVALID_ARG;
+    if (n_tokens == 0) return PKV_OK;
+    if (!k || !v || (rotate && !positions) || !slot_mapping || !k_cache || !v_cache || !k_scale || !v_scale)
+        return PKV_ERR_INVALID_ARG;
+    if (k_token_stride % 8 || v_token_stride % 8 || (q && (q_token_stride % 8 || q_out_token_stride % 8)))
+        return PKV_ERR_UNSUPPORTED;
+    if (misaligned16(q, q_out, k, v) || misaligned16(k_cache, v_cache, k_scale, v_scale)) return PKV_ERR_UNSUPPORTED;
+    if (n_tokens > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
+    StoreFp8Args a{};
+    a.q = q;
+    a.q_out = q_out;
+    a.k = k;
+    a.v = v;
+    a.positions = rotate ? positions : nullptr;
+    a.slots = slot_mapping;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.q_stride = q_token_stride;
+    a.q_out_stride = q_out_token_stride;
+    a.k_stride = k_token_stride;
+    a.v_stride = v_token_stride;
+    a.num_slots = static_cast<int64_t>(num_blocks) * block_size;
+    a.num_heads = q ? num_heads : 0;
+    a.num_kv_heads = num_kv_heads;
+    a.block_size = block_size;
+    if (rotate) rope_turns(rope_base, head_dim, a.turns);
+    int* err = device_error_word();
+    if (!err) return PKV_ERR_CUDA;
+    return launch_store_fp8(a, n_tokens, err, as_stream(stream)) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+}  // namespace
+
+pkv_status pkv_store_kvcache_fp8(const pkv_bf16* k, const pkv_bf16* v, int64_t n_tokens, int64_t k_token_stride,
+                                 int64_t v_token_stride, const int32_t* slot_mapping, pkv_e4m3* k_cache,
+                                 pkv_e4m3* v_cache, pkv_e8m0* k_scale, pkv_e8m0* v_scale, int32_t num_blocks,
+                                 int32_t block_size, int32_t num_kv_heads, int32_t head_dim, pkv_stream_t stream) {
+    return store_fp8_call(nullptr, 0, nullptr, 0, k, k_token_stride, v, v_token_stride, nullptr, false, n_tokens, 0,
+                          num_kv_heads, head_dim, 0.0, slot_mapping, k_cache, v_cache, k_scale, v_scale, num_blocks,
+                          block_size, stream);
+}
+
+pkv_status pkv_rope_store_kvcache_fp8(const pkv_bf16* q, int64_t q_token_stride, pkv_bf16* q_out,
+                                      int64_t q_out_token_stride, const pkv_bf16* k, int64_t k_token_stride,
+                                      const pkv_bf16* v, int64_t v_token_stride, const int32_t* positions,
+                                      int64_t n_tokens, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                      double rope_base, const int32_t* slot_mapping, pkv_e4m3* k_cache,
+                                      pkv_e4m3* v_cache, pkv_e8m0* k_scale, pkv_e8m0* v_scale, int32_t num_blocks,
+                                      int32_t block_size, pkv_stream_t stream) {
+    return store_fp8_call(q, q_token_stride, q_out, q_out_token_stride, k, k_token_stride, v, v_token_stride, positions,
+                          true, n_tokens, num_heads, num_kv_heads, head_dim, rope_base, slot_mapping, k_cache, v_cache,
+                          k_scale, v_scale, num_blocks, block_size, stream);
+}
+
+size_t pkv_decode_fp8_workspace_size(int32_t batch, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim) {
+    if (batch < 0 || !supported_shape(num_heads, num_kv_heads, head_dim, kBlockQuantum)) return 0;
+    if (sm_count() <= 0) return 0;
+    return decode_fp8_workspace_bytes(batch, num_kv_heads, group_log2(num_heads, num_kv_heads));
+}
+
+pkv_status pkv_decode_fp8(const pkv_bf16* q, const pkv_e4m3* k_cache, const pkv_e4m3* v_cache, const pkv_e8m0* k_scale,
+                          const pkv_e8m0* v_scale, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                          const int32_t* context_lens, int32_t batch, int32_t max_context_len, int32_t num_heads,
+                          int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t num_blocks,
+                          float softmax_scale, pkv_bf16* out, void* workspace, size_t workspace_bytes,
+                          pkv_stream_t stream) {
+    if (batch < 0 || max_blocks_per_seq <= 0 || num_blocks <= 0 || max_context_len < 0 || !(softmax_scale > 0.f) ||
+        softmax_scale == INFINITY)
+        return PKV_ERR_INVALID_ARG;
+    if (!supported_shape(num_heads, num_kv_heads, head_dim, block_size)) return PKV_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(max_blocks_per_seq) * block_size > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
+    if (batch == 0) return PKV_OK;
+    if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !block_tables || !context_lens || !out)
+        return PKV_ERR_INVALID_ARG;
+    if (misaligned16(q, out) || misaligned16(k_cache, v_cache, k_scale, v_scale)) return PKV_ERR_UNSUPPORTED;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255) return PKV_ERR_WORKSPACE;
+    int* err = device_error_word();
+    if (!err) return PKV_ERR_CUDA;
+    DecodeFp8Args a;
+    a.q = q;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.out = out;
+    a.max_blocks = max_blocks_per_seq;
+    a.batch = batch;
+    a.num_heads = num_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.block_size = block_size;
+    a.num_blocks = num_blocks;
+    a.softmax_scale = softmax_scale;
+    a.workspace = workspace;
+    a.workspace_bytes = workspace_bytes;
+    return launch_decode_fp8(a, err, as_stream(stream));
+}
+
+size_t pkv_prefill_fp8_workspace_size(int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                      int32_t max_seqlen_q, int32_t max_seqlen_k, int64_t total_k) {
+    if (num_seqs < 0 || max_seqlen_q < 0 || max_seqlen_k < 0 || total_k < 0 ||
+        !supported_shape(num_heads, num_kv_heads, head_dim, kBlockQuantum))
+        return 0;
+    return prefill_fp8_workspace_bytes(num_seqs, num_kv_heads, max_seqlen_q, max_seqlen_k, total_k,
+                                       group_log2(num_heads, num_kv_heads));
+}
+
+pkv_status pkv_prefill_varlen_fp8(const pkv_bf16* q, const pkv_e4m3* k_cache, const pkv_e4m3* v_cache,
+                                  const pkv_e8m0* k_scale, const pkv_e8m0* v_scale, const int32_t* cu_seqlens_q,
+                                  const int32_t* cu_seqlens_k, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                  int32_t num_seqs, int32_t total_q, int32_t max_seqlen_q, int32_t max_seqlen_k,
+                                  int64_t total_k, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                  int32_t block_size, int32_t num_blocks, float softmax_scale, pkv_bf16* out,
+                                  void* workspace, size_t workspace_bytes, pkv_stream_t stream) {
+    if (num_seqs < 0 || total_q < 0 || max_seqlen_q < 0 || max_seqlen_k < 0 || total_k < 0 || max_blocks_per_seq <= 0 ||
+        num_blocks <= 0 || !(softmax_scale > 0.f) || softmax_scale == INFINITY)
+        return PKV_ERR_INVALID_ARG;
+    if (!supported_shape(num_heads, num_kv_heads, head_dim, block_size)) return PKV_ERR_UNSUPPORTED;
+    if (max_seqlen_q > max_seqlen_k) return PKV_ERR_INVALID_ARG;
+    if (num_seqs == 0 || total_q == 0 || max_seqlen_q == 0) return PKV_OK;
+    if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !cu_seqlens_q || !cu_seqlens_k || !block_tables || !out)
+        return PKV_ERR_INVALID_ARG;
+    if (misaligned16(q, out) || misaligned16(k_cache, v_cache, k_scale, v_scale)) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs > 65535 || total_k > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255) return PKV_ERR_WORKSPACE;
+    int* err = device_error_word();
+    if (!err) return PKV_ERR_CUDA;
+    PrefillFp8Args a;
+    a.q = q;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.cu_q = cu_seqlens_q;
+    a.cu_k = cu_seqlens_k;
+    a.block_tables = block_tables;
+    a.out = out;
+    a.max_blocks = max_blocks_per_seq;
+    a.num_seqs = num_seqs;
+    a.total_q = total_q;
+    a.total_k = total_k;
+    a.max_seqlen_q = max_seqlen_q;
+    a.max_seqlen_k = max_seqlen_k;
+    a.num_heads = num_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.block_size = block_size;
+    a.num_blocks = num_blocks;
+    a.softmax_scale = softmax_scale;
+    a.workspace = workspace;
+    a.workspace_bytes = workspace_bytes;
+    return launch_prefill_fp8(a, err, as_stream(stream));
+}
+
 pkv_status pkv_sample(const float* logits, int32_t batch, int32_t vocab, int64_t row_stride,
                       const float* temperatures, uint64_t seed, uint64_t offset, int64_t* out_ids,
                       pkv_stream_t stream) {
@@ -462,6 +647,53 @@ pkv_status pkv_sample_dev(const float* logits, int32_t batch, int32_t vocab, int
     const cudaError_t e = launch_sample(logits, batch, vocab, row_stride, temperatures, 0, 0, seed_offset, out_ids,
                                         err, as_stream(stream));
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+namespace {
+
+pkv_status sample_filtered_call(const float* logits, int32_t batch, int32_t vocab, int64_t row_stride,
+                                const float* temperatures, const int32_t* top_k, const float* top_p, const float* min_p,
+                                uint64_t seed, uint64_t offset, bool dev, const uint64_t* seed_offset, int64_t* out_ids,
+                                pkv_stream_t stream) {
+    if (batch < 0 || vocab <= 0 || row_stride < vocab) return PKV_ERR_INVALID_ARG;
+    if (batch == 0) return PKV_OK;
+    if (!logits || !temperatures || !out_ids || (dev && !seed_offset)) return PKV_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(seed_offset) & 7) return PKV_ERR_INVALID_ARG;
+    if (batch > 65535 || vocab > (1 << 24)) return PKV_ERR_UNSUPPORTED;
+    int* err = device_error_word();
+    if (!err) return PKV_ERR_CUDA;
+    SampleFilteredArgs a;
+    a.logits = logits;
+    a.temperatures = temperatures;
+    a.top_k = top_k;
+    a.top_p = top_p;
+    a.min_p = min_p;
+    a.seed_offset = seed_offset;
+    a.out_ids = out_ids;
+    a.row_stride = row_stride;
+    a.seed = seed;
+    a.offset = offset;
+    a.batch = batch;
+    a.vocab = vocab;
+    return launch_sample_filtered(a, err, as_stream(stream));
+}
+
+}  // namespace
+
+pkv_status pkv_sample_filtered(const float* logits, int32_t batch, int32_t vocab, int64_t row_stride,
+                               const float* temperatures, const int32_t* top_k, const float* top_p,
+                               const float* min_p, uint64_t seed, uint64_t offset, int64_t* out_ids,
+                               pkv_stream_t stream) {
+    return sample_filtered_call(logits, batch, vocab, row_stride, temperatures, top_k, top_p, min_p, seed, offset, false,
+                                nullptr, out_ids, stream);
+}
+
+pkv_status pkv_sample_filtered_dev(const float* logits, int32_t batch, int32_t vocab, int64_t row_stride,
+                                   const float* temperatures, const int32_t* top_k, const float* top_p,
+                                   const float* min_p, const uint64_t* seed_offset, int64_t* out_ids,
+                                   pkv_stream_t stream) {
+    return sample_filtered_call(logits, batch, vocab, row_stride, temperatures, top_k, top_p, min_p, 0, 0, true,
+                                seed_offset, out_ids, stream);
 }
 
 pkv_status pkv_check_wait_timeout(pkv_stream_t stream) {

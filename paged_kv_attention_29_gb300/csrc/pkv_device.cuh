@@ -362,4 +362,44 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(uint32_t M, uint32_t N, ui
            ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
+// ---------------------------------------------------------------------------
+// Rotary angles
+// ---------------------------------------------------------------------------
+// Angles in fixed-point turns.  The host passes, per pair i, the fraction
+// F_i / 2^64 = frac(inv_freq_i / (2 pi)) of a turn per position step.  For
+// 0 <= p <= 2^31, p * F_i mod 2^64 is the angle's fraction of a turn; its top
+// 32 bits are exactly umulhi(p, F_lo) + p * F_hi (mod 2^32), and dropping the
+// low word truncates by less than 2^-32 turn.  Read as a signed int32 that
+// is the angle reduced to [-pi, pi) in units of 2^-32 turn, exact whatever the
+// position -- so no floating-point range reduction and no fp64 arithmetic,
+// which runs at a small fraction of the fp32 rate on this part.  A negative
+// position is |p| turned the other way.  On [-pi, pi] the hardware sine and
+// cosine approximation is within 4e-7 absolute, a few fp32 roundings of the
+// rotated value, and keeps the table off the CTA's critical path.
+__device__ __forceinline__ float reduced_angle(int pos, uint32_t f_lo, uint32_t f_hi) {
+    const uint32_t m = pos < 0 ? 0u - static_cast<uint32_t>(pos) : static_cast<uint32_t>(pos);
+    uint32_t turns = __umulhi(m, f_lo) + m * f_hi;
+    if (pos < 0) turns = 0u - turns;
+    return static_cast<float>(static_cast<int32_t>(turns)) * 1.4629180792671596e-9f;   // 2 pi / 2^32
+}
+
+// ---------------------------------------------------------------------------
+// 8-bit cache rows: e4m3 codes and an E8M0 scale byte
+// ---------------------------------------------------------------------------
+// Four e4m3 codes -> two f16 pairs (codes 0, 1 and codes 2, 3), exactly.
+__device__ __forceinline__ void f16_of_codes(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(w));
+}
+
+// An E8M0 byte's exponent as fp32 (NaN for 255), and its value 2^exponent.
+__device__ __forceinline__ float e8m0_exponent(uint32_t byte) {
+    return byte == 255u ? __uint_as_float(0x7fc00000u) : static_cast<float>(static_cast<int>(byte) - 127);
+}
+__device__ __forceinline__ float e8m0_value(uint32_t byte) {
+    return byte == 255u ? __uint_as_float(0x7fc00000u)
+                        : __uint_as_float(byte ? byte << 23 : 0x00400000u);      // byte 0: 2^-127, subnormal
+}
+
 }  // namespace pkv

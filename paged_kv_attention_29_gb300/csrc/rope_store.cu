@@ -18,24 +18,6 @@ namespace {
 
 constexpr int kMaxThreads = 1024;
 
-// Angles in fixed-point turns.  The host passes, per pair i, the fraction
-// F_i / 2^64 = frac(inv_freq_i / (2 pi)) of a turn per position step.  For
-// 0 <= p <= 2^31, p * F_i mod 2^64 is the angle's fraction of a turn; its top
-// 32 bits are exactly umulhi(p, F_lo) + p * F_hi (mod 2^32), and dropping the
-// low word truncates by less than 2^-32 turn.  Read as a signed int32 that
-// is the angle reduced to [-pi, pi) in units of 2^-32 turn, exact whatever the
-// position -- so no floating-point range reduction and no fp64 arithmetic,
-// which runs at a small fraction of the fp32 rate on this part.  A negative
-// position is |p| turned the other way.  On [-pi, pi] the hardware sine and
-// cosine approximation is within 4e-7 absolute, a few fp32 roundings of the
-// rotated value, and keeps the table off the CTA's critical path.
-__device__ __forceinline__ float reduced_angle(int pos, uint32_t f_lo, uint32_t f_hi) {
-    const uint32_t m = pos < 0 ? 0u - static_cast<uint32_t>(pos) : static_cast<uint32_t>(pos);
-    uint32_t turns = __umulhi(m, f_lo) + m * f_hi;
-    if (pos < 0) turns = 0u - turns;
-    return static_cast<float>(static_cast<int32_t>(turns)) * 1.4629180792671596e-9f;   // 2 pi / 2^32
-}
-
 // One CTA per token, one work item per thread: item (row, j) of a Q or K head
 // row holds vectors j and j + d/16 (8 pairs, 16 B each side); the items after
 // them copy the V row in 16-byte vectors.  Each thread issues its loads first;
