@@ -11,27 +11,34 @@
 // -ln e_v lies in (-2.82, 16.64), a token more than 19.6 below the maximum cannot beat the
 // maximum's own key: it counts in the sums but takes no part in the race.
 //
-// One cluster of 8 CTAs takes a row: each CTA copies its eighth of the row into shared memory
-// once (151,936 logits: 76 KB, two CTAs per SM) and every later step reads that copy, so HBM sees
-// each logit once.  A kept set is an upper set of the order, so top-k and top-p each come down to
-// one threshold (logit, column):
+// One cluster of CTAs takes a row, each an equal slice of it; HBM sees each logit once (pass 1),
+// later sweeps find the row in L2 and skip a quad of logits at one comparison of its maximum.
+// The work below pass 1 is bound by latency (cluster barriers, dependent shared-memory steps), so
+// each kind of row takes the shortest way that is exact for it:
 //
-//   1  Histogram of z over 2048 bins of width 0.01 (integer counts, so the order of the atomics
-//      does not matter), summed over the cluster.
-//   2  Top-k: the bin where the count reaches k.  Top-p: a bin holds weights within 1% of one
-//      another, so the counts bound the running sum from both sides and leave a few bins where
-//      it may reach its goal.
-//   3  One sweep sums the weights above those bins (fixed order: threads, then CTAs in rank order)
-//      and collects the bins' members, at most 1024, in the first CTA, which sorts them and finds
-//      the threshold.  More members than that (a flat row, thousands of equal logits) are first
-//      halved, by (logit bits, column), as often as it takes.
+//   pass 1  every thread's maximum and, for top-p, its sum of weights relative to that maximum;
+//           one exchange gives every CTA the row's first token (top_k = 1 ends here) and the sum Z.
+//   top-k   (k at most half the threads, and 1024.)  The k-th largest of the threads' maxima bounds
+//           the k-th logit from below: a 128-bin histogram of the maxima gives the bound, a sweep
+//           collects what reaches it (a little over k tokens) in the first CTA, which sorts them,
+//           cuts them by k, then by p and min-p, and runs the race.
+//   top-p   A token lighter than (1 - p) Z / vocab is outside (all of those together weigh less
+//           than 1 - p of Z).  The others are counted into 2048 bins of 1/64 octave of weight.
+//           A bin's weights lie within 1.1% of one another, so the counts bound the running sum
+//           from both sides and leave a few bins where it may reach p Z.  One sweep sums and races
+//           the tokens above those bins and collects the bins' members in the first CTA, which
+//           sorts them, finds the border by their running sum and races what is above it.
+//   else    (a larger k, or more members than fit: a flat row, thousands of equal logits.)  The
+//           same histogram over every token, and the range of candidates halved, by (logit bits,
+//           column), until it fits; the race then sweeps the slices once more.
 //
-// Sums: weights in fp32 (ex2.approx), a thread's share (37 of 151,936 terms) in fp32, everything
-// across threads in fp64: a running sum is within about 1e-7 of itself, so the token at the
-// border is decided as in exact arithmetic except when a border lies that near to it.
+// Counts are integers and sums across threads 64-bit fixed point (2^-38), so neither atomics nor
+// the order of the list can change a result.  A thread's share of a sum (a few dozen weights) is
+// fp32: a running sum is within about 1e-6 of itself, and the token at the border is decided as in
+// exact arithmetic except when a border lies that near to it.
 //
-// The race's keys are fp32 with an error below 2e-5; when the two best are within 1e-4 the
-// candidates are ranked again in fp64.
+// The race's keys are fp32 with an error below 2e-5; when the two best are within 1e-4 they are
+// ranked again in fp64.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -45,41 +52,42 @@ namespace cg = cooperative_groups;
 namespace pkv {
 namespace {
 
-constexpr int CLUSTER = 8;
-constexpr int THREADS = 512;
-constexpr int WARPS = THREADS / 32;
 constexpr int BINS = 2048;
-constexpr int BINS_PER_THREAD = BINS / THREADS;
-constexpr int BINS_PER_RANK = BINS / CLUSTER;
-constexpr int TAIL = BINS - 1;               // the last bin: everything from z = -20.47 down
-constexpr float BINS_PER_UNIT = 100.f;
-constexpr float TAIL_Z = 20.47f;
-constexpr int CAP = 1024;                    // members sorted at once
-constexpr float RACE_Z = 19.6f;              // reach of the race (see above)
+constexpr int TAIL = BINS - 1;               // the last bin: everything from 2047/64 octaves down
+constexpr int COARSE = 128;                  // bins of the threads' maxima, 16 fine bins each
+constexpr int CAP = 2048;                    // members collected at once
+constexpr int RANK_MAX = 256;                // members sorted by counting
+constexpr int MAX_CLUSTER = 16;
+constexpr int kWideRows = 8;                 // rows that get a wide cluster each (see the launch)
+constexpr float BINS_PER_OCTAVE = 64.f;
+constexpr float RACE_Z = 19.6f;              // reach of the race (see above): 28.3 octaves, inside the fine bins
 constexpr float NEAR = 1e-4f;
-constexpr int kMaxResident = 22016;          // logits of a slice in shared memory: 2 CTAs per SM
 constexpr float LOG2E = 1.4426950408889634f;
-static_assert(BINS_PER_RANK <= THREADS && 2 * THREADS >= CAP, "one element per thread in the reductions and the sort");
+constexpr float FIX = 274877906944.f;        // 2^38: a weight of 1 in fixed point
 
 struct Shared {
     uint32_t hist[BINS];         // this CTA's counts
     uint32_t tot[BINS];          // the cluster's counts
     uint64_t list[CAP];          // first CTA: members, as composites
-    double slot[2][CLUSTER];     // cluster-wide sums, alternating
-    uint64_t lo[CLUSTER], hi[CLUSTER];
+    uint64_t sorted[RANK_MAX];
+    uint64_t slot[2][MAX_CLUSTER];             // cluster-wide sums, alternating
+    uint64_t lo[2][MAX_CLUSTER], hi[2][MAX_CLUSTER];   // cluster-wide ranges, alternating
+    uint64_t top[MAX_CLUSTER];   // pass 1: first token and sum of each CTA
+    float z[MAX_CLUSTER];
+    uint32_t coarse[MAX_CLUSTER][COARSE];
+    float2 win[MAX_CLUSTER];     // race: best and second best key of each CTA
+    int2 win_col[MAX_CLUSTER];
     uint64_t threshold;
-    double list_sum;
-    double wred[WARPS];
-    uint64_t wlo[WARPS], whi[WARPS];
-    float2 wscan[WARPS];
-    float2 win[CLUSTER];         // race: best and second best key of each CTA
-    int win_col[CLUSTER];
-    float wbest[WARPS], wsecond[WARPS];
-    int wcol[WARPS];
-    float min_x;                 // smallest logit that min-p keeps
-    int first[2];
+    uint64_t list_sum;
+    uint64_t wred[32];           // per warp
+    uint64_t wlo[32], whi[32];
+    float2 wscan[32];
+    float2 wwin[32];
+    int2 wwin_col[32];
+    int first[3];
     uint32_t list_n;
 };
+static_assert(sizeof(Shared) <= 48 * 1024, "no opt-in to more shared memory");
 
 // Order of the tokens as an unsigned number: larger = earlier.  -0 and +0 are one logit.
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -92,11 +100,33 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 __device__ __forceinline__ uint64_t composite(float x, int col) {
     return (static_cast<uint64_t>(key_of(x)) << 32) | (0xffffffffu - static_cast<uint32_t>(col));
 }
+__device__ __forceinline__ float composite_x(uint64_t c) { return value_of(static_cast<uint32_t>(c >> 32)); }
+__device__ __forceinline__ int composite_col(uint64_t c) { return static_cast<int>(0xffffffffu - static_cast<uint32_t>(c)); }
 
-__device__ __forceinline__ int bin_of(float d) {   // d = max z - z; non-decreasing in d
-    return d < TAIL_Z ? min(static_cast<int>(d * BINS_PER_UNIT), TAIL - 1) : TAIL;
+// Depth below the maximum in bins; non-decreasing as the logit falls, inf for -inf.
+__device__ __forceinline__ int bin_of(float depth) { return static_cast<int>(fminf(depth, static_cast<float>(TAIL))); }
+__device__ __forceinline__ float weight_of(float depth) { return ex2_ftz(depth * (-1.f / BINS_PER_OCTAVE)); }
+__device__ __forceinline__ uint64_t fixed_of(float w) { return __float2ull_rn(w * FIX); }
+
+__device__ __forceinline__ uint64_t shfl_xor64(uint64_t v, int off) {
+    return static_cast<uint64_t>(__shfl_xor_sync(0xffffffffu, static_cast<unsigned long long>(v), off));
 }
-__device__ __forceinline__ float weight_of(float d) { return ex2_ftz(-d * LOG2E); }
+
+// The two best of a race: larger key first, then lower column.
+struct Best {
+    float k1, k2;
+    int c1, c2;                  // -1: none
+    __device__ __forceinline__ void clear() { k1 = k2 = -INFINITY; c1 = c2 = -1; }
+    __device__ __forceinline__ void add(float k, int c) {
+        if (c < 0) return;
+        if (c1 < 0 || k > k1 || (k == k1 && c < c1)) {
+            k2 = k1; c2 = c1;
+            k1 = k; c1 = c;
+        } else if (c2 < 0 || k > k2 || (k == k2 && c < c2)) {
+            k2 = k; c2 = c;
+        }
+    }
+};
 
 struct Args {
     SampleFilteredArgs a;
@@ -104,19 +134,22 @@ struct Args {
     int* err;
 };
 
-template <bool kResident>
-__global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, 2) sample_filtered_kernel(const Args args) {
+template <int CLUSTER, int THREADS, int LOADS, int MIN_CTAS>
+__global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_CTAS) sample_filtered_kernel(const Args args) {
+    constexpr int WARPS = THREADS / 32;
+    constexpr int BINS_PER_THREAD = BINS / THREADS;
+    constexpr int BINS_PER_RANK = BINS / CLUSTER;
+    constexpr int FAST_K = CLUSTER * THREADS / 2 < CAP / 2 ? CLUSTER * THREADS / 2 : CAP / 2;
+    static_assert(BINS % THREADS == 0 && CLUSTER <= MAX_CLUSTER && WARPS <= 32 && COARSE <= THREADS, "tables fit");
     const SampleFilteredArgs& a = args.a;
-    extern __shared__ __align__(16) uint8_t smem_raw[];
-    Shared& sh = *reinterpret_cast<Shared*>(smem_raw);
-    float* slice = reinterpret_cast<float*>(smem_raw + (sizeof(Shared) + 15) / 16 * 16);
+    __shared__ Shared sh;
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = static_cast<int>(cluster.block_rank());
     const int row = blockIdx.y;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     const float T = __ldg(a.temperatures + row);
-    int k = a.top_k ? __ldg(a.top_k + row) : 0;
+    const int k = a.top_k ? __ldg(a.top_k + row) : 0;
     const float p = a.top_p ? __ldg(a.top_p + row) : 1.f;
     const float mp = a.min_p ? __ldg(a.min_p + row) : 0.f;
     const bool t_ok = T > 0.f && T < INFINITY;
@@ -128,88 +161,181 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, 2) sa
         }
         return;
     }
+    const bool need_k = k > 0 && k < a.vocab;
+    const bool need_p = p < 1.f;
+    const bool fast_k = need_k && k <= FAST_K;
     const float inv_t = fminf(1.0f / T, 3.4028235e38f);
+    const float per_logit = fminf(inv_t * (LOG2E * BINS_PER_OCTAVE), 3.4028235e38f);    // bins per unit of logit
 
-    // ---- this CTA's slice: whole quads [q0, q1) of the row; absent columns read as NaN
+    // ---- this CTA's slice: whole quads [q0, q1) of the row; absent columns and NaN read as -inf
     const float* lrow = a.logits + static_cast<int64_t>(row) * a.row_stride;
     const int nquads = (a.vocab + 3) >> 2;
     const int per = (nquads + CLUSTER - 1) / CLUSTER;
     const int q0 = min(nquads, rank * per), q1 = min(nquads, q0 + per);
     auto load_quad = [&](int qd) -> float4 {
         const int col = qd * 4;
-        if (args.vec_ok && col + 3 < a.vocab) return __ldg(reinterpret_cast<const float4*>(lrow + col));
-        const float none = __uint_as_float(0x7fc00000u);
         float4 v;
-        v.x = __ldg(lrow + col);
-        v.y = col + 1 < a.vocab ? __ldg(lrow + col + 1) : none;
-        v.z = col + 2 < a.vocab ? __ldg(lrow + col + 2) : none;
-        v.w = col + 3 < a.vocab ? __ldg(lrow + col + 3) : none;
-        return v;
-    };
-    // f(column, logit) for every logit of the slice that is above -inf (not NaN)
-    auto sweep = [&](auto f) {
-        for (int qd = q0 + tid; qd < q1; qd += THREADS) {
-            const float4 v = kResident ? reinterpret_cast<const float4*>(slice)[qd - q0] : load_quad(qd);
-            if (v.x > -INFINITY) f(4 * qd, v.x);
-            if (v.y > -INFINITY) f(4 * qd + 1, v.y);
-            if (v.z > -INFINITY) f(4 * qd + 2, v.z);
-            if (v.w > -INFINITY) f(4 * qd + 3, v.w);
+        if (args.vec_ok && col + 3 < a.vocab) {
+            v = __ldg(reinterpret_cast<const float4*>(lrow + col));
+        } else {
+            v.x = __ldg(lrow + col);
+            v.y = col + 1 < a.vocab ? __ldg(lrow + col + 1) : -INFINITY;
+            v.z = col + 2 < a.vocab ? __ldg(lrow + col + 2) : -INFINITY;
+            v.w = col + 3 < a.vocab ? __ldg(lrow + col + 3) : -INFINITY;
         }
+        return make_float4(fmaxf(v.x, -INFINITY), fmaxf(v.y, -INFINITY), fmaxf(v.z, -INFINITY), fmaxf(v.w, -INFINITY));
     };
+    auto max_of = [](const float4& v) { return fmaxf(fmax3(v.x, v.y, v.z), v.w); };
+    // f(quad, its logits) over the slice, LOADS loads in flight per thread
+    auto sweep_quads = [&](auto f) {
+        int qd = q0 + tid;
+        for (; qd + (LOADS - 1) * THREADS < q1; qd += LOADS * THREADS) {
+            float4 v[LOADS];
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) v[i] = load_quad(qd + i * THREADS);
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) f(qd + i * THREADS, v[i]);
+        }
+        for (; qd < q1; qd += THREADS) f(qd, load_quad(qd));
+    };
+    // f(column, logit) for every logit of the slice from x_min up, and above -inf
+    auto sweep_from = [&](float x_min, auto f) {
+        sweep_quads([&](int qd, const float4& v) {
+            const float m = max_of(v);
+            if (!(m >= x_min && m > -INFINITY)) return;
+            const float l[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (l[e] >= x_min && l[e] > -INFINITY) f(4 * qd + e, l[e]);
+        });
+    };
+
+    // ---- pass 1
     for (int b = tid; b < BINS; b += THREADS) sh.hist[b] = 0u;
+    if (tid < COARSE) sh.tot[tid] = 0u;                   // the coarse counts, first
     if (tid == 0) sh.list_n = 0u;
-    float mx = -INFINITY;
-#pragma unroll 4
-    for (int qd = q0 + tid; qd < q1; qd += THREADS) {
-        const float4 v = load_quad(qd);
-        if (kResident) reinterpret_cast<float4*>(slice)[qd - q0] = v;
-        mx = fmaxf(fmax3(mx, v.x, v.y), fmaxf(v.z, v.w));     // NaN loses
+    float mx = -INFINITY, zs = 0.f;
+    int mx_quad = q0;                                     // the first quad that holds this thread's maximum
+    const bool online = need_p && !fast_k;
+    const float l2 = fminf(inv_t * LOG2E, 3.4028235e38f);
+    if (online) {
+        sweep_quads([&](int qd, const float4& v) {
+            const float m4 = max_of(v);
+            if (m4 > mx) {
+                zs *= ex2_ftz((mx - m4) * l2);            // 0 for the first
+                mx = m4;
+                mx_quad = qd;
+            }
+            if (mx > -INFINITY)
+                zs += (ex2_ftz((v.x - mx) * l2) + ex2_ftz((v.y - mx) * l2)) + (ex2_ftz((v.z - mx) * l2) + ex2_ftz((v.w - mx) * l2));
+        });
+    } else {
+        sweep_quads([&](int qd, const float4& v) {
+            const float m4 = max_of(v);
+            if (m4 > mx) { mx = m4; mx_quad = qd; }
+        });
     }
+    uint64_t top = 0;                                     // the first token: largest logit, lowest column
+    if (mx > -INFINITY) {
+        const float4 v = load_quad(mx_quad);
+        const int e = v.x == mx ? 0 : v.y == mx ? 1 : v.z == mx ? 2 : 3;
+        top = composite(mx, 4 * mx_quad + e);
+    }
+    {
+        uint64_t t = top;
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) t = max(t, shfl_xor64(t, off));
+        if (lane == 0) sh.whi[warp] = t;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) t = max(t, sh.whi[w]);
+        const float m_cta = t ? composite_x(t) : 0.f;
+        uint64_t zf = 0;
+        if (online) {
+            // infinite maxima end the row below, whatever their sum
+            zf = mx > -INFINITY && m_cta < INFINITY ? fixed_of(zs * ex2_ftz((mx - m_cta) * l2)) : 0ull;
+#pragma unroll
+            for (int off = 16; off >= 1; off >>= 1) zf += shfl_xor64(zf, off);
+            if (lane == 0) sh.wred[warp] = zf;
+            __syncthreads();
+            zf = 0;
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) zf += sh.wred[w];
+        }
+        if (tid < CLUSTER) {
+            *cluster.map_shared_rank(&sh.top[rank], tid) = t;
+            *cluster.map_shared_rank(&sh.slot[0][rank], tid) = zf;
+        }
+    }
+    cluster.sync();                                       // also publishes the cleared tables
+    uint64_t first_token = 0, Z = 0;
+#pragma unroll
+    for (int r = 0; r < CLUSTER; ++r) first_token = max(first_token, sh.top[r]);
+    const float M = composite_x(first_token);
+    if (first_token == 0 || k == 1 || M == INFINITY) {    // nothing above -inf; or no choice: infinite logits win
+        if (rank == 0 && tid == 0) a.out_ids[row] = first_token == 0 ? -1 : static_cast<int64_t>(composite_col(first_token));
+        return;
+    }
+    if (online) {
+        float z = 0.f;                                    // in units of 2^-38
+#pragma unroll
+        for (int r = 0; r < CLUSTER; ++r)
+            if (sh.top[r]) z = fmaf(__ull2float_rn(sh.slot[0][r]), ex2_ftz((composite_x(sh.top[r]) - M) * l2), z);
+        Z = __float2ull_rn(z);
+    }
+    // the smallest logit in the race: min-p's limit, and the race's reach
+    const float min_x = fmaxf(mp > 0.f ? fmaf(T, logf(mp), M) : -INFINITY, M - RACE_Z * T);
+    auto depth = [&](float x) { return (M - x) * per_logit; };
+    // a logit not above any whose bin is <= b: M minus b + 1 bins and a margin for its own rounding
+    auto x_at_end_of = [&](int b) {
+        const float x = M - static_cast<float>(b + 1) / per_logit;
+        return x - (fabsf(M) + fabsf(x)) * 1e-6f;
+    };
 
     // ---- cluster-wide reductions; every CTA ends with the same values
-    int phase = 0;
-    auto cluster_sum = [&](double v) -> double {
+    int phase = 1;
+    auto cluster_sum = [&](uint64_t v) -> uint64_t {
 #pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+        for (int off = 16; off >= 1; off >>= 1) v += shfl_xor64(v, off);
         if (lane == 0) sh.wred[warp] = v;
         __syncthreads();
-        double* mine = &sh.slot[phase][rank];
         if (tid < CLUSTER) {
-            double s = 0.0;
+            uint64_t s = 0;
             for (int w = 0; w < WARPS; ++w) s += sh.wred[w];
-            *cluster.map_shared_rank(mine, tid) = s;
+            *cluster.map_shared_rank(&sh.slot[phase][rank], tid) = s;
         }
         cluster.sync();
-        double s = 0.0;
+        uint64_t s = 0;
+#pragma unroll
         for (int r = 0; r < CLUSTER; ++r) s += sh.slot[phase][r];
         phase ^= 1;
         return s;
     };
-    // smallest and largest of two 64-bit numbers
-    auto cluster_range = [&](uint64_t& lo, uint64_t& hi) {
+    int rphase = 0;
+    auto cluster_range = [&](uint64_t& lo, uint64_t& hi) {   // the smallest and the largest
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) {
-            lo = min(lo, static_cast<uint64_t>(__shfl_xor_sync(0xffffffffu, static_cast<unsigned long long>(lo), off)));
-            hi = max(hi, static_cast<uint64_t>(__shfl_xor_sync(0xffffffffu, static_cast<unsigned long long>(hi), off)));
+            lo = min(lo, shfl_xor64(lo, off));
+            hi = max(hi, shfl_xor64(hi, off));
         }
         if (lane == 0) { sh.wlo[warp] = lo; sh.whi[warp] = hi; }
         __syncthreads();
         if (tid < CLUSTER) {
             for (int w = 0; w < WARPS; ++w) { lo = min(lo, sh.wlo[w]); hi = max(hi, sh.whi[w]); }
-            *cluster.map_shared_rank(&sh.lo[rank], tid) = lo;
-            *cluster.map_shared_rank(&sh.hi[rank], tid) = hi;
+            *cluster.map_shared_rank(&sh.lo[rphase][rank], tid) = lo;
+            *cluster.map_shared_rank(&sh.hi[rphase][rank], tid) = hi;
         }
         cluster.sync();
-        lo = sh.lo[0];
-        hi = sh.hi[0];
-        for (int r = 1; r < CLUSTER; ++r) { lo = min(lo, sh.lo[r]); hi = max(hi, sh.hi[r]); }
-        cluster.sync();                                   // read before anyone writes them again
+        lo = sh.lo[rphase][0];
+        hi = sh.hi[rphase][0];
+        for (int r = 1; r < CLUSTER; ++r) { lo = min(lo, sh.lo[rphase][r]); hi = max(hi, sh.hi[rphase][r]); }
+        rphase ^= 1;
     };
-    // the cluster's histogram from every CTA's, which is cleared for its next use
+    // the cluster's counts from every CTA's (complete before the call's first barrier)
     auto cluster_hist = [&]() {
         cluster.sync();
-        if (tid < BINS_PER_RANK) {
-            const int b = rank * BINS_PER_RANK + tid;
+        for (int i = tid; i < BINS_PER_RANK; i += THREADS) {
+            const int b = rank * BINS_PER_RANK + i;
             uint32_t s = 0;
 #pragma unroll
             for (int r = 0; r < CLUSTER; ++r) s += *cluster.map_shared_rank(&sh.hist[b], r);
@@ -217,7 +343,6 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, 2) sa
             for (int r = 0; r < CLUSTER; ++r) *cluster.map_shared_rank(&sh.tot[b], r) = s;
         }
         cluster.sync();
-        for (int b = tid; b < BINS; b += THREADS) sh.hist[b] = 0u;
     };
     // exclusive prefix over the CTA's threads of two fp32 numbers
     auto scan2 = [&](float2 v) -> float2 {
@@ -235,45 +360,245 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, 2) sa
         return make_float2(before.x + s.x - v.x, before.y + s.y - v.y);
     };
 
-    uint64_t lo64 = 0, hi64 = (mx > -INFINITY) ? key_of(mx) : 0u;
-    cluster_range(lo64, hi64);                            // its barriers also publish the slice and the cleared histogram
-    if (hi64 == 0) {                                      // nothing above -inf
-        if (rank == 0 && tid == 0) a.out_ids[row] = -1;
-        return;
+    // ---- noise and keys
+    uint64_t seed = a.seed, offset = a.offset;
+    if (a.seed_offset) {
+        seed = __ldg(a.seed_offset);
+        offset = __ldg(a.seed_offset + 1);
     }
-    const float M = value_of(static_cast<uint32_t>(hi64));
-    if (M == INFINITY) {                                  // infinite logits win; the lowest column among them
-        uint64_t first = ~0ull, none = 0;
-        sweep([&](int col, float x) { if (x == INFINITY) first = min(first, static_cast<uint64_t>(col)); });
-        cluster_range(first, none);
-        if (rank == 0 && tid == 0) a.out_ids[row] = static_cast<int64_t>(first);
-        return;
-    }
-    if (tid == 0)
-        sh.min_x = mp > 0.f ? __double2float_ru(static_cast<double>(M) + static_cast<double>(T) * log(static_cast<double>(mp)))
-                            : -INFINITY;
-    auto depth = [&](float x) { return (M - x) * inv_t; };
+    const uint64_t rr = static_cast<uint64_t>(row) + offset;
+    const PhiloxRow prow = philox_row(static_cast<uint32_t>(rr), static_cast<uint32_t>(rr >> 32), static_cast<uint32_t>(seed),
+                                      static_cast<uint32_t>(seed >> 32));
+    const RoundKeys unused = {};
+    auto noise_of = [&](int col) -> uint32_t {
+        const uint4 w = philox_row_at<false>(static_cast<uint32_t>(col) >> 2, prow, unused);
+        const int e = col & 3;
+        return e == 0 ? w.x : e == 1 ? w.y : e == 2 ? w.z : w.w;
+    };
+    auto key32 = [&](float x, uint32_t noise) {
+        // e = -ln u from the exact w = 1 - u where u is near 1, from the hardware logarithm elsewhere
+        const float w = one_minus_u_of(noise);
+        const float e = w < 0.015625f ? w * fmaf(w, fmaf(w, fmaf(w, 0.25f, 0.333333343f), 0.5f), 1.0f)
+                                      : -__logf(__uint2float_rn(2u * (noise >> 9) + 1u) * 5.9604644775390625e-08f);
+        return (x - M) * inv_t - __logf(e);
+    };
+    auto key64 = [&](int col) {
+        const double e = -log1p(-static_cast<double>(one_minus_u_of(noise_of(col))));
+        return (static_cast<double>(__ldg(lrow + col)) - static_cast<double>(M)) / static_cast<double>(T) - log(e);
+    };
+    Best best;
+    best.clear();
+    // The tokens of a quad that are from x_min up and pass `in`, raced.  A token can beat the warp's best
+    // `bar` only if 1 - u < e^(z - bar) (since -ln u >= 1 - u), which spares most keys: the quad's smallest
+    // 1 - u against the bound of its largest logit, then each token's; the bound carries a margin of 1e-3.
+    auto race_quad = [&](int qd, const float (&l)[4], float lmax, float bar) {
+        const uint4 w = philox_row_at<false>(static_cast<uint32_t>(qd), prow, unused);
+        const float cb = (1e-3f - bar) * LOG2E + 1.4419741739064e-3f;                  // + log2 1.001
+        const uint32_t wmax = max(max(w.x, w.y), max(w.z, w.w));
+        if (one_minus_u_of(wmax) < ex2_ftz(fmaf(lmax - M, l2, cb))) {
+            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (one_minus_u_of(ws[e]) < ex2_ftz(fmaf(l[e] - M, l2, cb))) best.add(key32(l[e], ws[e]), 4 * qd + e);
+        }
+    };
+    auto share_best = [&]() -> float {                    // the warp's best key so far
+        float b;
+        asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(b) : "f"(best.k1));
+        return b;
+    };
+    // the CTA's two best, in every thread
+    auto block_best = [&]() {
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) {
+            const float k1 = __shfl_xor_sync(0xffffffffu, best.k1, off), k2 = __shfl_xor_sync(0xffffffffu, best.k2, off);
+            const int c1 = __shfl_xor_sync(0xffffffffu, best.c1, off), c2 = __shfl_xor_sync(0xffffffffu, best.c2, off);
+            best.add(k1, c1);
+            best.add(k2, c2);
+        }
+        if (lane == 0) {
+            sh.wwin[warp] = make_float2(best.k1, best.k2);
+            sh.wwin_col[warp] = make_int2(best.c1, best.c2);
+        }
+        __syncthreads();
+        best.clear();
+        for (int w = 0; w < WARPS; ++w) {
+            best.add(sh.wwin[w].x, sh.wwin_col[w].x);
+            best.add(sh.wwin[w].y, sh.wwin_col[w].y);
+        }
+        __syncthreads();
+    };
+    // every CTA's two best to the first CTA (the caller's next barrier completes it)
+    auto send_best = [&]() {
+        block_best();
+        if (tid == 0) {
+            *cluster.map_shared_rank(&sh.win[rank], 0) = make_float2(best.k1, best.k2);
+            *cluster.map_shared_rank(&sh.win_col[rank], 0) = make_int2(best.c1, best.c2);
+        }
+    };
+    auto gather_best = [&]() {
+        best.clear();
+        for (int r = 0; r < CLUSTER; ++r) {
+            best.add(sh.win[r].x, sh.win_col[r].x);
+            best.add(sh.win[r].y, sh.win_col[r].y);
+        }
+    };
+    // by one thread
+    auto write_winner = [&]() {
+        if (best.c2 >= 0 && best.k1 - best.k2 <= NEAR) {  // too near in fp32
+            const double d1 = key64(best.c1), d2 = key64(best.c2);
+            if (d2 > d1 || (d2 == d1 && best.c2 < best.c1)) best.c1 = best.c2;
+        }
+        a.out_ids[row] = static_cast<int64_t>(best.c1);
+    };
 
-    // ---- thresholds
+    // ---- the list in the first CTA
+    uint64_t* list0 = cluster.map_shared_rank(sh.list, 0);
+    uint32_t* n0 = cluster.map_shared_rank(&sh.list_n, 0);
+    auto collect = [&](uint64_t c) {
+        const uint32_t at = atomicAdd(n0, 1u);
+        if (at < CAP) list0[at] = c;
+    };
+    // n members sorted, earliest first, by the CTA
+    auto sort_list = [&](int n) {
+        if (n <= RANK_MAX) {
+            for (int i = tid; i < n; i += THREADS) {
+                const uint64_t c = sh.list[i];
+                int at = 0;
+#pragma unroll 4
+                for (int j = 0; j < n; ++j) at += sh.list[j] > c ? 1 : 0;
+                sh.sorted[at] = c;
+            }
+            __syncthreads();
+            for (int i = tid; i < n; i += THREADS) sh.list[i] = sh.sorted[i];
+            __syncthreads();
+            return;
+        }
+        int n2 = RANK_MAX;
+        while (n2 < n) n2 <<= 1;
+        for (int i = n + tid; i < n2; i += THREADS) sh.list[i] = 0ull;
+        __syncthreads();
+        for (int size = 2; size <= n2; size <<= 1)
+            for (int half = size >> 1; half >= 1; half >>= 1) {
+                for (int i = tid; i < (n2 >> 1); i += THREADS) {
+                    const int x = (i & ~(half - 1)) * 2 + (i & (half - 1)), y = x + half;
+                    const uint64_t cx = sh.list[x], cy = sh.list[y];
+                    if ((x & size) == 0 ? cx < cy : cx > cy) {
+                        sh.list[x] = cy;
+                        sh.list[y] = cx;
+                    }
+                }
+                __syncthreads();
+            }
+    };
+    // How many of the first n members of the sorted list have less than `goal` weight before them, `above`
+    // in front; *sum: their weight (without `above`).
+    auto kept_by_weight = [&](int n, uint64_t above, uint64_t goal, uint64_t* sum) -> int {
+        const int each = (n + THREADS - 1) / THREADS, i0 = tid * each, i1 = min(n, i0 + each);
+        uint64_t mine = 0;
+        for (int i = i0; i < i1; ++i) mine += fixed_of(weight_of(depth(composite_x(sh.list[i]))));
+        uint64_t s = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const uint64_t x = static_cast<uint64_t>(__shfl_up_sync(0xffffffffu, static_cast<unsigned long long>(s), off));
+            if (lane >= off) s += x;
+        }
+        __syncthreads();
+        if (lane == 31) sh.wred[warp] = s;
+        __syncthreads();
+        uint64_t before = above + s - mine;
+        for (int w = 0; w < warp; ++w) before += sh.wred[w];
+        int count = 0;
+        uint64_t part = 0;
+        for (int i = i0; i < i1; ++i) {
+            const uint64_t w = fixed_of(weight_of(depth(composite_x(sh.list[i]))));
+            if (before < goal) {
+                ++count;
+                part += w;
+            }
+            before += w;
+        }
+        count = __reduce_add_sync(0xffffffffu, count);
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) part += shfl_xor64(part, off);
+        __syncthreads();
+        if (lane == 0) { sh.wred[warp] = part; sh.wlo[warp] = static_cast<uint64_t>(count); }
+        __syncthreads();
+        count = 0;
+        part = 0;
+        for (int w = 0; w < WARPS; ++w) { count += static_cast<int>(sh.wlo[w]); part += sh.wred[w]; }
+        __syncthreads();
+        *sum = part;
+        return count;
+    };
+    // p z, at least the smallest weight (the first token is always kept); p 2^63 is exact
+    auto goal_of = [&](uint64_t z) { return max(__umul64hi(z, __float2ull_rz(p * 9223372036854775808.f)) << 1, static_cast<unsigned long long>(1)); };
+    auto race_list = [&](int n) {
+        for (int i = tid; i < n; i += THREADS) {
+            const uint64_t c = sh.list[i];
+            if (composite_x(c) < min_x) break;
+            best.add(key32(composite_x(c), noise_of(composite_col(c))), composite_col(c));
+        }
+    };
+
+    // ---- top-k
+    if (fast_k) {
+        if (mx > -INFINITY) atomicAdd(&sh.tot[bin_of(depth(mx)) / (BINS / COARSE)], 1u);
+        __syncthreads();
+        if (tid < COARSE) {
+            const uint32_t cnt = sh.tot[tid];
+#pragma unroll
+            for (int r = 0; r < CLUSTER; ++r) *cluster.map_shared_rank(&sh.coarse[rank][tid], r) = cnt;
+        }
+        cluster.sync();
+        float2 mine = make_float2(0.f, 0.f);
+        if (tid < COARSE)
+            for (int r = 0; r < CLUSTER; ++r) mine.x += static_cast<float>(sh.coarse[r][tid]);
+        if (tid == 0) sh.first[0] = COARSE;
+        const float2 run = scan2(mine);
+        if (tid < COARSE && run.x < static_cast<float>(k) && run.x + mine.x >= static_cast<float>(k)) sh.first[0] = tid;
+        __syncthreads();
+        const int bound = sh.first[0];                    // COARSE: fewer than k maxima
+        const int last_bin = bound < COARSE - 1 ? (bound + 1) * (BINS / COARSE) - 1 : BINS;
+        // Collected by their bins, exactly; a row with fewer than k maxima above -inf, or with the k-th in the
+        // last bins, collects everything it has (which fits if the vocabulary does).
+        if (last_bin < BINS || a.vocab <= CAP) {
+            sweep_from(last_bin < BINS ? x_at_end_of(last_bin) : -INFINITY, [&](int col, float x) {
+                if (last_bin == BINS || bin_of(depth(x)) <= last_bin) collect(composite(x, col));
+            });
+            cluster.sync();
+            const int n = static_cast<int>(*n0);
+            if (n <= CAP) {
+                if (rank != 0) { cluster.sync(); return; }            // the first CTA's counter has been read
+                cluster.sync();
+                sort_list(n);
+                int kept = min(k, n);
+                if (need_p) {
+                    uint64_t sum;
+                    kept_by_weight(kept, 0, ~0ull, &sum);
+                    kept = kept_by_weight(kept, 0, goal_of(sum), &sum);
+                }
+                race_list(kept);
+                block_best();
+                if (tid == 0) write_winner();
+                return;
+            }
+            cluster.sync();
+            if (rank == 0 && tid == 0) sh.list_n = 0u;
+        }
+    }
+
+    // ---- thresholds by histogram
     uint64_t keep = 0;                                    // a token is kept if its composite is >= keep
-    bool need_k = k > 0 && k < a.vocab;
-    const bool need_p = p < 1.f;
-
     // From a range of members (bins [b_lo, b_hi] and composites >= keep, n of them) to the threshold.
     // By count: the goal-th member, in order.  By weight: the last member before which the weights,
     // those above the range in front, sum to less than the goal.  Sets `keep`; returns the weight of
     // every kept token (weigh: also when selecting by count).
-    auto select = [&](bool by_weight, bool weigh, int b_lo, int b_hi, uint32_t n, double goal) -> double {
+    auto select = [&](bool by_weight, bool weigh, int b_lo, int b_hi, uint32_t n, uint64_t goal) -> uint64_t {
         float ws = 0.f;
         uint64_t cmin = ~0ull, cmax = 0ull;
-        uint64_t* list0 = cluster.map_shared_rank(sh.list, 0);
-        uint32_t* n0 = cluster.map_shared_rank(&sh.list_n, 0);
-        auto collect = [&](uint64_t c) {
-            const uint32_t at = atomicAdd(n0, 1u);
-            if (at < CAP) list0[at] = c;
-        };
         const bool fits = n <= CAP;
-        sweep([&](int col, float x) {
+        sweep_from(b_hi < TAIL ? x_at_end_of(b_hi) : -INFINITY, [&](int col, float x) {
             const float d = depth(x);
             const int b = bin_of(d);
             if (b < b_lo) {
@@ -286,89 +611,48 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, 2) sa
                 cmax = max(cmax, c);
             }
         });
-        double above = cluster_sum(static_cast<double>(ws));
+        uint64_t above = cluster_sum(fixed_of(ws));
         if (!fits) {
             cluster_range(cmin, cmax);
-            for (int half = 0; half < 64 && n > CAP; ++half) {       // composites differ: 64 halvings leave one
+            for (int half = 0; half < 64 && n > CAP; ++half) {          // composites differ: 64 halvings leave one
                 const uint64_t mid = cmin + ((cmax - cmin) >> 1);       // upper half: (mid, cmax]
                 ws = 0.f;
                 uint32_t cnt = 0;
-                sweep([&](int col, float x) {
+                sweep_from(composite_x(mid), [&](int col, float x) {
                     const uint64_t c = composite(x, col);
                     if (c <= mid || c > cmax) return;
                     ++cnt;
                     if (weigh) ws += weight_of(depth(x));
                 });
-                const uint32_t upper = static_cast<uint32_t>(cluster_sum(static_cast<double>(cnt)));
-                const double w_upper = weigh ? cluster_sum(static_cast<double>(ws)) : 0.0;
-                if (by_weight ? above + w_upper >= goal : static_cast<double>(upper) >= goal) {
+                const uint32_t upper = static_cast<uint32_t>(cluster_sum(cnt));
+                const uint64_t w_upper = weigh ? cluster_sum(fixed_of(ws)) : 0ull;
+                if (by_weight ? above + w_upper >= goal : upper >= goal) {
                     cmin = mid + 1;
                     n = upper;
                 } else {
                     above += w_upper;
-                    if (!by_weight) goal -= static_cast<double>(upper);
+                    if (!by_weight) goal -= upper;
                     cmax = mid;
                     n -= upper;
                 }
             }
-            sweep([&](int col, float x) {
+            sweep_from(composite_x(cmin), [&](int col, float x) {
                 const uint64_t c = composite(x, col);
                 if (c >= cmin && c <= cmax) collect(c);
             });
             n = min(n, static_cast<uint32_t>(CAP));
             cluster.sync();
         }
-        // the first CTA sorts the members, earliest first, and finds the threshold
         if (rank == 0) {
-            int n2 = 32;
-            while (n2 < static_cast<int>(n)) n2 <<= 1;
-            for (int i = static_cast<int>(n) + tid; i < n2; i += THREADS) sh.list[i] = 0ull;
-            __syncthreads();
-            for (int size = 2; size <= n2; size <<= 1)
-                for (int half = size >> 1; half >= 1; half >>= 1) {
-                    for (int i = tid; i < (n2 >> 1); i += THREADS) {
-                        const int x = (i / half) * 2 * half + (i % half), y = x + half;
-                        const uint64_t cx = sh.list[x], cy = sh.list[y];
-                        const bool down = (x & size) == 0;
-                        if (down ? cx < cy : cx > cy) {
-                            sh.list[x] = cy;
-                            sh.list[y] = cx;
-                        }
-                    }
-                    __syncthreads();
-                }
-            // weights of members 2 tid, 2 tid + 1 and the sum before them
-            const int i0 = 2 * tid, i1 = i0 + 1;
-            double w0 = 0.0, w1 = 0.0;
-            if (weigh) {
-                if (i0 < static_cast<int>(n)) w0 = weight_of(depth(value_of(static_cast<uint32_t>(sh.list[i0] >> 32))));
-                if (i1 < static_cast<int>(n)) w1 = weight_of(depth(value_of(static_cast<uint32_t>(sh.list[i1] >> 32))));
-            }
-            double s = w0 + w1;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const double x = __shfl_up_sync(0xffffffffu, s, off);
-                if (lane >= off) s += x;
-            }
-            if (lane == 31) sh.wred[warp] = s;
-            __syncthreads();
-            double before = above;
-            for (int w = 0; w < warp; ++w) before += sh.wred[w];
-            before += s - w0 - w1;
-            const bool in0 = i0 < static_cast<int>(n) && (by_weight ? before < goal : i0 < goal);
-            const bool in1 = i1 < static_cast<int>(n) && (by_weight ? before + w0 < goal : i1 < goal);
-            const int kept = __syncthreads_count(in0) + __syncthreads_count(in1);
-            double part = (in0 ? w0 : 0.0) + (in1 ? w1 : 0.0);
-#pragma unroll
-            for (int off = 16; off >= 1; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
-            if (lane == 0) sh.wred[warp] = part;
-            __syncthreads();
+            sort_list(static_cast<int>(n));
+            uint64_t sum = 0;
+            int kept = static_cast<int>(min(goal, static_cast<uint64_t>(n)));
+            if (by_weight) kept = kept_by_weight(static_cast<int>(n), above, goal, &sum);
+            else if (weigh) kept_by_weight(kept, 0, ~0ull, &sum);
             if (tid < CLUSTER) {
-                double sum = above;
-                for (int w = 0; w < WARPS; ++w) sum += sh.wred[w];
                 // none kept: just above the range
                 *cluster.map_shared_rank(&sh.threshold, tid) = kept > 0 ? sh.list[kept - 1] : n > 0 ? sh.list[0] + 1 : cmax + 1;
-                *cluster.map_shared_rank(&sh.list_sum, tid) = sum;
+                *cluster.map_shared_rank(&sh.list_sum, tid) = above + sum;
             }
             if (tid == 0) sh.list_n = 0u;
         }
@@ -378,22 +662,23 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, 2) sa
     };
 
     if (need_k || need_p) {
-        float ws = 0.f;
-        uint32_t tail = 0;
-        sweep([&](int, float x) {
-            const float d = depth(x);
-            const int b = bin_of(d);
-            if (b == TAIL) ++tail; else atomicAdd(&sh.hist[b], 1u);
-            if (need_p) ws += weight_of(d);
-        });
-        tail = __reduce_add_sync(0xffffffffu, tail);
-        if (lane == 0 && tail) atomicAdd(&sh.hist[TAIL], tail);
-        double Z = cluster_sum(static_cast<double>(ws));
-        cluster_hist();
         int k_bin = BINS;                                 // the bin of the last token top-k keeps
         uint32_t k_left = 0;                              // tokens it keeps in that bin
+        int end = TAIL;                                   // bins that top-p's border can lie in, or that the race reaches
         if (need_k) {
-            // counts are below 2^24 in fp32 where it matters: the vocabulary is limited to that
+            float ws = 0.f;
+            uint32_t tail = 0;
+            sweep_from(-INFINITY, [&](int, float x) {
+                const float d = depth(x);
+                const int b = bin_of(d);
+                if (b == TAIL) ++tail; else atomicAdd(&sh.hist[b], 1u);
+                if (need_p) ws += weight_of(d);
+            });
+            tail = __reduce_add_sync(0xffffffffu, tail);
+            if (lane == 0 && tail) atomicAdd(&sh.hist[TAIL], tail);
+            Z = cluster_sum(fixed_of(ws));
+            cluster_hist();
+            // exact in fp32: the vocabulary is limited to 2^24
             float2 mine = make_float2(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < BINS_PER_THREAD; ++i) mine.x += static_cast<float>(sh.tot[tid * BINS_PER_THREAD + i]);
@@ -416,20 +701,31 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, 2) sa
             __syncthreads();
             // every token of the tail is out of the race's reach: without top-p its order does not matter
             if (k_bin < TAIL || (k_bin == TAIL && need_p))
-                Z = select(false, need_p, k_bin, k_bin, sh.tot[k_bin], static_cast<double>(k_left));
+                Z = select(false, need_p, k_bin, k_bin, sh.tot[k_bin], k_left);
+        } else {
+            // tokens lighter than (1 - p) Z / vocab are outside; the limit in bins, with a margin
+            const float z_f = static_cast<float>(Z) * (1.f / FIX);
+            const float limit = (log2f(static_cast<float>(a.vocab)) - log2f((1.f - p) * z_f)) * BINS_PER_OCTAVE * 1.00001f + 2.f;
+            end = limit < static_cast<float>(TAIL) ? max(1, static_cast<int>(limit)) : TAIL;
+            sweep_from(x_at_end_of(end), [&](int, float x) {
+                const int b = bin_of(depth(x));
+                if (b < end) atomicAdd(&sh.hist[b], 1u);
+            });
+            cluster_hist();
         }
         if (need_p) {
-            const double goal = static_cast<double>(p) * Z;
+            const uint64_t goal = goal_of(Z);
+            const float goal_f = static_cast<float>(goal) * (1.f / FIX);
             auto kept_in = [&](int b) { return b < k_bin ? sh.tot[b] : b == k_bin ? k_left : 0u; };   // after top-k
-            // bounds of the running sum at the end of each bin
+            // bounds of the running sum at the end of each bin; thread t holds bins BINS_PER_THREAD t ...
             float up[BINS_PER_THREAD], dn[BINS_PER_THREAD];
             float2 mine = make_float2(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < BINS_PER_THREAD; ++i) {
                 const int b = tid * BINS_PER_THREAD + i;
                 const float cnt = static_cast<float>(kept_in(b));
-                up[i] = cnt * weight_of(b / BINS_PER_UNIT);
-                dn[i] = b == TAIL ? 0.f : cnt * weight_of((b + 1) / BINS_PER_UNIT);
+                up[i] = cnt * weight_of(static_cast<float>(b));
+                dn[i] = b == TAIL ? 0.f : cnt * weight_of(static_cast<float>(b + 1));
                 mine.x += up[i];
                 mine.y += dn[i];
             }
@@ -440,135 +736,112 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, 2) sa
             for (int i = 0; i < BINS_PER_THREAD; ++i) {
                 run.x += up[i];
                 run.y += dn[i];
-                if (run.x >= static_cast<float>(goal) * (1.f - 1e-4f)) atomicMin(&sh.first[0], tid * BINS_PER_THREAD + i);
-                if (run.y >= static_cast<float>(goal) * (1.f + 1e-4f)) atomicMin(&sh.first[1], tid * BINS_PER_THREAD + i);
+                if (run.x >= goal_f * (1.f - 1e-4f)) atomicMin(&sh.first[0], tid * BINS_PER_THREAD + i);
+                if (run.y >= goal_f * (1.f + 1e-4f)) atomicMin(&sh.first[1], tid * BINS_PER_THREAD + i);
             }
             __syncthreads();
-            const int b_lo = sh.first[0], b_hi = sh.first[1];
+            const int b_lo = sh.first[0], b_hi = min(max(b_lo, sh.first[1]), end - 1);
+            uint32_t n_in = 0;
+            for (int b = b_lo + lane; b <= b_hi; b += 32) n_in += kept_in(b);
+            n_in = __reduce_add_sync(0xffffffffu, n_in);
             __syncthreads();
-            if (b_lo < TAIL) {
-                uint32_t n = 0;
-                for (int b = b_lo + lane; b <= b_hi; b += 32) n += kept_in(b);
-                n = __reduce_add_sync(0xffffffffu, n);
-                select(true, true, b_lo, b_hi, n, goal);
+            if (b_lo <= b_hi && !need_k && n_in <= CAP) {
+                // the usual case: sum and race what is above the range, collect the range
+                float ws = 0.f, bar = -INFINITY;
+                const float x_end = x_at_end_of(b_hi);
+                const int iters = (q1 - q0 + THREADS - 1) / THREADS;        // uniform
+                for (int it = 0; it < iters; ++it) {
+                    const int qd = q0 + it * THREADS + tid;
+                    bool raced = false;
+                    if (qd < q1) {
+                        const float4 v = load_quad(qd);
+                        if (max_of(v) >= x_end) {
+                            float l[4] = {v.x, v.y, v.z, v.w}, lmax = -INFINITY;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float d = depth(l[e]);
+                                const int b = bin_of(d);
+                                const bool sure = b < b_lo;
+                                if (sure) ws += weight_of(d);
+                                else if (b <= b_hi) collect(composite(l[e], 4 * qd + e));
+                                if (!(sure && l[e] >= min_x)) l[e] = -INFINITY;
+                                lmax = fmaxf(lmax, l[e]);
+                            }
+                            if (lmax > -INFINITY) {
+                                race_quad(qd, l, lmax, bar);
+                                raced = true;
+                            }
+                        }
+                    }
+                    if (__any_sync(0xffffffffu, raced)) bar = share_best();
+                }
+                send_best();
+                const uint64_t above = cluster_sum(fixed_of(ws));
+                if (rank != 0) return;
+                sort_list(static_cast<int>(n_in));
+                uint64_t sum;
+                const int kept = kept_by_weight(static_cast<int>(n_in), above, goal, &sum);
+                best.clear();
+                race_list(kept);
+                block_best();
+                if (tid == 0) {
+                    const Best mine2 = best;
+                    gather_best();
+                    best.add(mine2.k1, mine2.c1);
+                    best.add(mine2.k2, mine2.c2);
+                    write_winner();
+                }
+                return;
             }
+            if (b_lo <= b_hi) select(true, true, b_lo, b_hi, n_in, goal);
         }
     }
 
-    // ---- the race
-    __syncthreads();                                      // min_x
-    const float min_x = fmaxf(sh.min_x, M - RACE_Z * T);
-    uint64_t seed = a.seed, offset = a.offset;
-    if (a.seed_offset) {
-        seed = __ldg(a.seed_offset);
-        offset = __ldg(a.seed_offset + 1);
-    }
-    const uint64_t rr = static_cast<uint64_t>(row) + offset;
-    const PhiloxRow prow = philox_row(static_cast<uint32_t>(rr), static_cast<uint32_t>(rr >> 32), static_cast<uint32_t>(seed),
-                                      static_cast<uint32_t>(seed >> 32));
-    const RoundKeys unused = {};
-    auto in_race = [&](float x, int col) { return x >= min_x && composite(x, col) >= keep; };
-    auto race = [&](auto f) {                             // f(column, logit, noise word) for every token in the race
-        for (int qd = q0 + tid; qd < q1; qd += THREADS) {
-            const float4 v = kResident ? reinterpret_cast<const float4*>(slice)[qd - q0] : load_quad(qd);
-            const float l[4] = {v.x, v.y, v.z, v.w};
-            bool in[4];
+    // ---- the race over the slices
+    const float x_keep = keep ? composite_x(keep) : -INFINITY, x_from = fmaxf(min_x, x_keep);
+    const uint32_t col_keep = keep ? static_cast<uint32_t>(composite_col(keep)) : 0xffffffffu;    // at x_keep itself: columns up to this
+    float bar = -INFINITY;
+    const int iters = (q1 - q0 + THREADS - 1) / THREADS;                    // uniform
+    for (int it = 0; it < iters; ++it) {
+        const int qd = q0 + it * THREADS + tid;
+        if (qd < q1) {
+            const float4 v = load_quad(qd);
+            if (max_of(v) >= x_from) {
+                float l[4] = {v.x, v.y, v.z, v.w}, lmax = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) in[e] = in_race(l[e], 4 * qd + e);
-            if (!(in[0] || in[1] || in[2] || in[3])) continue;
-            const uint4 w = philox_row_at<false>(static_cast<uint32_t>(qd), prow, unused);
-            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (in[e]) f(4 * qd + e, l[e], ws[e]);
+                for (int e = 0; e < 4; ++e) {
+                    if (!(l[e] >= x_from && (l[e] > x_keep || static_cast<uint32_t>(4 * qd + e) <= col_keep))) l[e] = -INFINITY;
+                    lmax = fmaxf(lmax, l[e]);
+                }
+                if (lmax > -INFINITY) race_quad(qd, l, lmax, bar);
+            }
         }
-    };
-    auto key32 = [&](float x, uint32_t noise) {
-        // e = -ln u from the exact w = 1 - u where u is near 1, from the hardware logarithm elsewhere
-        const float w = one_minus_u_of(noise);
-        const float e = w < 0.015625f ? w * fmaf(w, fmaf(w, fmaf(w, 0.25f, 0.333333343f), 0.5f), 1.0f)
-                                      : -__logf(__uint2float_rn(2u * (noise >> 9) + 1u) * 5.9604644775390625e-08f);
-        return -depth(x) - __logf(e);
-    };
-    float best = -INFINITY, second = -INFINITY;
-    int col_of = -1;
-    auto take = [&](float kb, int cb, float k2) {         // merge another (best, column, second best)
-        if (cb < 0) return;
-        if (col_of < 0 || kb > best || (kb == best && cb < col_of)) {
-            second = fmaxf(fmaxf(best, k2), second);
-            best = kb;
-            col_of = cb;
-        } else {
-            second = fmaxf(second, kb);
-        }
-    };
-    race([&](int col, float x, uint32_t noise) { take(key32(x, noise), col, -INFINITY); });
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) {
-        const float ob = __shfl_xor_sync(0xffffffffu, best, off), os = __shfl_xor_sync(0xffffffffu, second, off);
-        const int oc = __shfl_xor_sync(0xffffffffu, col_of, off);
-        take(ob, oc, os);
+        bar = share_best();
     }
-    if (lane == 0) { sh.wbest[warp] = best; sh.wsecond[warp] = second; sh.wcol[warp] = col_of; }
-    __syncthreads();
-    if (tid < CLUSTER) {
-        best = second = -INFINITY;
-        col_of = -1;
-        for (int w = 0; w < WARPS; ++w) take(sh.wbest[w], sh.wcol[w], sh.wsecond[w]);
-        *cluster.map_shared_rank(&sh.win[rank], tid) = make_float2(best, second);
-        *cluster.map_shared_rank(&sh.win_col[rank], tid) = col_of;
-    }
+    send_best();
     cluster.sync();
-    best = second = -INFINITY;
-    col_of = -1;
-    for (int r = 0; r < CLUSTER; ++r) take(sh.win[r].x, sh.win_col[r], sh.win[r].y);
-    if (best - second > NEAR) {
-        if (rank == 0 && tid == 0) a.out_ids[row] = static_cast<int64_t>(col_of);
-        return;
+    if (rank == 0 && tid == 0) {
+        gather_best();
+        write_winner();
     }
-    // ---- too near in fp32: the same keys in fp64, as an order-preserving integer and the column
-    double kd = 0.0;
-    int cd = -1;
-    const float bar = best - NEAR;
-    race([&](int col, float x, uint32_t noise) {
-        if (key32(x, noise) < bar) return;
-        const double e = -log1p(-static_cast<double>(one_minus_u_of(noise)));
-        const double key = (static_cast<double>(x) - static_cast<double>(M)) / static_cast<double>(T) - log(e);
-        if (cd < 0 || key > kd) { kd = key; cd = col; }   // columns come in rising order
-    });
-    uint64_t none = ~0ull, top = 0ull;
-    if (cd >= 0) {
-        const uint64_t b = static_cast<uint64_t>(__double_as_longlong(kd));
-        top = (b >> 63) ? ~b : b | 0x8000000000000000ull;
-    }
-    const uint64_t mine = top;
-    cluster_range(none, top);
-    uint64_t col_min = (cd >= 0 && mine == top) ? static_cast<uint64_t>(cd) : ~0ull, zero = 0ull;
-    cluster_range(col_min, zero);
-    if (rank == 0 && tid == 0) a.out_ids[row] = static_cast<int64_t>(col_min);
 }
-
-size_t smem_bytes(int slice) { return (sizeof(Shared) + 15) / 16 * 16 + static_cast<size_t>(slice) * 4; }
 
 }  // namespace
 
 pkv_status launch_sample_filtered(const SampleFilteredArgs& a, int* err, cudaStream_t stream) {
     if (a.batch == 0) return PKV_OK;
     if (!setup_once(kSetupSampleFiltered, [] {
-            return cudaFuncSetAttribute(sample_filtered_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        static_cast<int>(smem_bytes(kMaxResident))) == cudaSuccess;
+            return cudaFuncSetAttribute(sample_filtered_kernel<16, 512, 4, 1>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
         }))
         return PKV_ERR_CUDA;
     Args args;
     args.a = a;
     args.vec_ok = (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0 && a.row_stride % 4 == 0;
     args.err = err;
-    const int slice = ((a.vocab + 3) / 4 + CLUSTER - 1) / CLUSTER * 4;
-    const dim3 grid(CLUSTER, a.batch);
-    if (slice <= kMaxResident)
-        sample_filtered_kernel<true><<<grid, THREADS, smem_bytes(slice), stream>>>(args);
+    if (a.batch <= kWideRows)
+        sample_filtered_kernel<16, 512, 4, 1><<<dim3(16, a.batch), 512, 0, stream>>>(args);
     else
-        sample_filtered_kernel<false><<<grid, THREADS, smem_bytes(0), stream>>>(args);
+        sample_filtered_kernel<8, 256, 4, 4><<<dim3(8, a.batch), 256, 0, stream>>>(args);
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
