@@ -568,31 +568,65 @@ def pkv_sample_dev(logits: torch.Tensor, temperatures: torch.Tensor, seed_offset
 
 # ---------------------------------------------------------------------------
 # 8-bit KV cache
+#
+# A step of a small batch takes a few microseconds on the GPU, less than checking and marshalling a
+# call's arguments does with the helpers above; the calls below test every tensor in one expression
+# that passes when all is well (and otherwise hands over to _check for its message), pass raw integers
+# to ctypes and ask for the current device and stream once.
 # ---------------------------------------------------------------------------
+
+def _want(t, name, dtype, ndim):
+    """_check, at the cost of a few attribute reads when it passes."""
+    if not (type(t) is torch.Tensor and t.dtype is dtype and t.dim() == ndim and t.is_cuda and t.is_contiguous()):
+        _check(t, name, dtype, ndim)
+
+
+def _launch(name: str, fn, stream, tensors, args):
+    """fn(*args, stream) with the tensors' device current (see _on_device)."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != dev:
+            raise ValueError(f"all tensors of a call must be on one device (got cuda:{dev} and {t.device})")
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"stream is on cuda:{stream.device.index}, tensors on cuda:{dev}")
+    else:
+        s = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, s)
+    if status:
+        raise PkvError(status, name)
+
 
 def _pools_fp8(k_cache, v_cache, k_scale, v_scale):
     """Shape (num_blocks, block_size, num_kv_heads, head_dim) of an 8-bit cache, checked."""
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _check(t, name, torch.float8_e4m3fn, 4)
-    nb, bs, hkv, d = k_cache.shape
-    if v_cache.shape != k_cache.shape:
+    _want(k_cache, "k_cache", torch.float8_e4m3fn, 4)
+    _want(v_cache, "v_cache", torch.float8_e4m3fn, 4)
+    _want(k_scale, "k_scale", torch.float8_e8m0fnu, 3)
+    _want(v_scale, "v_scale", torch.float8_e8m0fnu, 3)
+    shape = k_cache.shape
+    if v_cache.shape != shape:
         raise ValueError("k_cache and v_cache shapes differ")
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        _check(t, name, torch.float8_e8m0fnu, 3)
-        if tuple(t.shape) != (nb, hkv, bs):
-            raise ValueError(f"{name} must be [{nb}, {hkv}, {bs}] (num_blocks, num_kv_heads, block_size)")
+    nb, bs, hkv, d = shape
+    want = (nb, hkv, bs)
+    if k_scale.shape != want or v_scale.shape != want:
+        raise ValueError(f"k_scale and v_scale must be [{nb}, {hkv}, {bs}] (num_blocks, num_kv_heads, block_size)")
     return nb, bs, hkv, d
 
 
-def _rows(t, name, hkv, d):
-    _check(t, name, torch.bfloat16, 3, contiguous=False)
-    if tuple(t.shape[1:]) != (hkv, d) or t.stride(2) != 1 or (hkv > 1 and t.stride(1) != d):
-        raise ValueError(f"{name} must be [n, {hkv}, {d}] with contiguous rows")
-
-
-def _token_stride(t: torch.Tensor) -> int:
-    """Elements between tokens; a single token's stride is meaningless (it may be 0), so use its length."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+def _rows(t, name, n, heads, d):
+    """Rows [n, heads, d] that are contiguous within a token; returns the elements between tokens (a single
+    token's own stride is meaningless, so its length)."""
+    if not (type(t) is torch.Tensor and t.dtype is torch.bfloat16 and t.dim() == 3 and t.is_cuda):
+        _check(t, name, torch.bfloat16, 3, contiguous=False)
+    token, head, element = t.stride()
+    if t.shape != (n, heads, d) or element != 1 or (heads > 1 and head != d):
+        raise ValueError(f"{name} must be [{n}, {heads}, {d}] with contiguous rows")
+    return token if n > 1 else heads * d
 
 
 def pkv_store_kvcache_fp8(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
@@ -600,16 +634,13 @@ def pkv_store_kvcache_fp8(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.
     """Round every row of k and v to e4m3 codes with a power-of-two scale and write both to its slot
     of the 8-bit pools; slot < 0 skips."""
     nb, bs, hkv, d = _pools_fp8(k_cache, v_cache, k_scale, v_scale)
-    _rows(k, "k", hkv, d)
-    _rows(v, "v", hkv, d)
-    _check(slot_mapping, "slot_mapping", torch.int32, 1)
-    n = k.shape[0]
-    if v.shape[0] != n or slot_mapping.shape[0] != n:
-        raise ValueError("k, v and slot_mapping disagree on the token count")
-    with _on_device(k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale, stream=stream):
-        _raise(load().pkv_store_kvcache_fp8(_ptr(k), _ptr(v), n, _token_stride(k), _token_stride(v), _ptr(slot_mapping),
-                                            _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), nb, bs, hkv, d,
-                                            _stream(stream)), "pkv_store_kvcache_fp8")
+    _want(slot_mapping, "slot_mapping", torch.int32, 1)
+    n = slot_mapping.shape[0]
+    ks, vs = _rows(k, "k", n, hkv, d), _rows(v, "v", n, hkv, d)
+    _launch("pkv_store_kvcache_fp8", load().pkv_store_kvcache_fp8, stream,
+            (k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale),
+            (k.data_ptr(), v.data_ptr(), n, ks, vs, slot_mapping.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+             k_scale.data_ptr(), v_scale.data_ptr(), nb, bs, hkv, d))
 
 
 def pkv_rope_store_kvcache_fp8(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
@@ -620,34 +651,30 @@ def pkv_rope_store_kvcache_fp8(q: Optional[torch.Tensor], k: torch.Tensor, v: to
 
     Returns the rotated q in bf16 (a new tensor, or `q_out`; pass ``q_out=q`` to rotate in place)."""
     nb, bs, hkv, d = _pools_fp8(k_cache, v_cache, k_scale, v_scale)
-    _rows(k, "k", hkv, d)
-    _rows(v, "v", hkv, d)
-    _check(positions, "positions", torch.int32, 1)
-    _check(slot_mapping, "slot_mapping", torch.int32, 1)
-    n = k.shape[0]
-    if v.shape[0] != n or slot_mapping.shape[0] != n or positions.shape[0] != n:
-        raise ValueError("k, v, positions and slot_mapping disagree on the token count")
-    hq = 0
-    if q is not None:
+    _want(positions, "positions", torch.int32, 1)
+    _want(slot_mapping, "slot_mapping", torch.int32, 1)
+    n = slot_mapping.shape[0]
+    if positions.shape[0] != n:
+        raise ValueError("positions and slot_mapping disagree on the token count")
+    ks, vs = _rows(k, "k", n, hkv, d), _rows(v, "v", n, hkv, d)
+    tensors = (k, v, positions, slot_mapping, k_cache, v_cache, k_scale, v_scale)
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out given without q")
+        head = (None, 0, None, 0)
+        hq = 0
+    else:
         _check(q, "q", torch.bfloat16, 3, contiguous=False)
         hq = q.shape[1]
-        _rows(q, "q", hq, d)
-        if q.shape[0] != n:
-            raise ValueError("q and k disagree on the token count")
+        qs = _rows(q, "q", n, hq, d)
         if q_out is None:
             q_out = torch.empty(n, hq, d, dtype=torch.bfloat16, device=q.device)
-        _rows(q_out, "q_out", hq, d)
-        if q_out.shape[0] != n:
-            raise ValueError("q_out must match q's shape")
-    elif q_out is not None:
-        raise ValueError("q_out given without q")
-    with _on_device(q, q_out, k, v, positions, slot_mapping, k_cache, v_cache, k_scale, v_scale, stream=stream):
-        _raise(load().pkv_rope_store_kvcache_fp8(_ptr(q), _token_stride(q) if q is not None else 0, _ptr(q_out),
-                                                 _token_stride(q_out) if q_out is not None else 0, _ptr(k),
-                                                 _token_stride(k), _ptr(v), _token_stride(v), _ptr(positions), n, hq,
-                                                 hkv, d, float(rope_base), _ptr(slot_mapping), _ptr(k_cache),
-                                                 _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), nb, bs, _stream(stream)),
-               "pkv_rope_store_kvcache_fp8")
+        head = (q.data_ptr(), qs, q_out.data_ptr(), _rows(q_out, "q_out", n, hq, d))
+        tensors += (q, q_out)
+    _launch("pkv_rope_store_kvcache_fp8", load().pkv_rope_store_kvcache_fp8, stream, tensors,
+            head + (k.data_ptr(), ks, v.data_ptr(), vs, positions.data_ptr(), n, hq, hkv, d, float(rope_base),
+                    slot_mapping.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                    v_scale.data_ptr(), nb, bs))
     return q_out
 
 
@@ -657,10 +684,12 @@ def pkv_decode_fp8_workspace_size(batch: int, num_heads: int, num_kv_heads: int,
 
 def decode_fp8_workspace(batch: int, num_heads: int, num_kv_heads: int, head_dim: int, device=None) -> torch.Tensor:
     """A uint8 device buffer of the size pkv_decode_fp8 needs (256-byte aligned by the allocator)."""
-    n = pkv_decode_fp8_workspace_size(batch, num_heads, num_kv_heads, head_dim)
+    device = torch.device(device or "cuda")
+    with torch.cuda.device(device):
+        n = pkv_decode_fp8_workspace_size(batch, num_heads, num_kv_heads, head_dim)
     if n == 0:
         raise PkvError(2, "pkv_decode_fp8_workspace_size")
-    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    return torch.empty(n, dtype=torch.uint8, device=device)
 
 
 def pkv_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
@@ -669,26 +698,26 @@ def pkv_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
                    stream=None) -> torch.Tensor:
     """Decode attention over an 8-bit cache: one query token per sequence, context_lens[b] keys."""
     nb, bs, hkv, d = _pools_fp8(k_cache, v_cache, k_scale, v_scale)
-    _check(q, "q", torch.bfloat16, 3)
-    _check(block_tables, "block_tables", torch.int32, 2)
-    _check(context_lens, "context_lens", torch.int32, 1)
+    _want(q, "q", torch.bfloat16, 3)
+    _want(block_tables, "block_tables", torch.int32, 2)
+    _want(context_lens, "context_lens", torch.int32, 1)
     batch, hq, dq = q.shape
-    if dq != d or context_lens.shape[0] != batch or block_tables.shape[0] != batch:
+    rows, width = block_tables.shape
+    if dq != d or context_lens.shape[0] != batch or rows != batch:
         raise ValueError("q, context_lens and block_tables disagree")
     if out is None:
         out = torch.empty_like(q)
-    _check(out, "out", torch.bfloat16, 3)
-    if out.shape != q.shape:
+    _want(out, "out", torch.bfloat16, 3)
+    if out.shape != (batch, hq, d):
         raise ValueError("out must have q's shape")
     if workspace is None:
-        with _on_device(q):
-            workspace = decode_fp8_workspace(batch, hq, hkv, d, q.device)
-    _check(workspace, "workspace", torch.uint8, 1)
-    with _on_device(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, out, workspace, stream=stream):
-        _raise(load().pkv_decode_fp8(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-                                     _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), batch,
-                                     int(max_context_len), hq, hkv, d, bs, nb, float(softmax_scale), _ptr(out),
-                                     _ptr(workspace), workspace.numel(), _stream(stream)), "pkv_decode_fp8")
+        workspace = decode_fp8_workspace(batch, hq, hkv, d, q.device)
+    _want(workspace, "workspace", torch.uint8, 1)
+    _launch("pkv_decode_fp8", load().pkv_decode_fp8, stream,
+            (q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, out, workspace),
+            (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+             block_tables.data_ptr(), width, context_lens.data_ptr(), batch, int(max_context_len), hq, hkv, d, bs, nb,
+             float(softmax_scale), out.data_ptr(), workspace.data_ptr(), workspace.numel()))
     return out
 
 
@@ -716,32 +745,30 @@ def pkv_prefill_varlen_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
     """Varlen prefill attention over an 8-bit cache (the new tokens' K/V already stored).  `total_k`
     bounds the keys of all sequences together."""
     nb, bs, hkv, d = _pools_fp8(k_cache, v_cache, k_scale, v_scale)
-    _check(q, "q", torch.bfloat16, 3)
-    _check(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1)
-    _check(cu_seqlens_k, "cu_seqlens_k", torch.int32, 1)
-    _check(block_tables, "block_tables", torch.int32, 2)
+    _want(q, "q", torch.bfloat16, 3)
+    _want(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1)
+    _want(cu_seqlens_k, "cu_seqlens_k", torch.int32, 1)
+    _want(block_tables, "block_tables", torch.int32, 2)
     total_q, hq, dq = q.shape
     if dq != d:
         raise ValueError("q head_dim differs from the pool's")
-    num_seqs = cu_seqlens_q.shape[0] - 1
-    if cu_seqlens_k.shape[0] != num_seqs + 1 or block_tables.shape[0] != num_seqs:
+    num_seqs, width = block_tables.shape
+    if cu_seqlens_q.shape[0] != num_seqs + 1 or cu_seqlens_k.shape[0] != num_seqs + 1:
         raise ValueError("cu_seqlens_q, cu_seqlens_k and block_tables disagree on the sequence count")
     if out is None:
         out = torch.empty_like(q)
-    _check(out, "out", torch.bfloat16, 3)
-    if out.shape != q.shape:
+    _want(out, "out", torch.bfloat16, 3)
+    if out.shape != (total_q, hq, d):
         raise ValueError("out must have q's shape")
     if workspace is None:
         workspace = prefill_fp8_workspace(num_seqs, hq, hkv, d, max_seqlen_q, max_seqlen_k, total_k, q.device)
-    _check(workspace, "workspace", torch.uint8, 1)
-    with _on_device(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, cu_seqlens_k, block_tables, out, workspace,
-                    stream=stream):
-        _raise(load().pkv_prefill_varlen_fp8(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-                                             _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), _ptr(block_tables),
-                                             block_tables.shape[1], num_seqs, total_q, int(max_seqlen_q),
-                                             int(max_seqlen_k), int(total_k), hq, hkv, d, bs, nb, float(softmax_scale),
-                                             _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream)),
-               "pkv_prefill_varlen_fp8")
+    _want(workspace, "workspace", torch.uint8, 1)
+    _launch("pkv_prefill_varlen_fp8", load().pkv_prefill_varlen_fp8, stream,
+            (q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, cu_seqlens_k, block_tables, out, workspace),
+            (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+             cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), block_tables.data_ptr(), width, num_seqs, total_q,
+             int(max_seqlen_q), int(max_seqlen_k), int(total_k), hq, hkv, d, bs, nb, float(softmax_scale),
+             out.data_ptr(), workspace.data_ptr(), workspace.numel()))
     return out
 
 
@@ -749,22 +776,34 @@ def pkv_prefill_varlen_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
 # sampling with filters
 # ---------------------------------------------------------------------------
 
-def _filter_args(logits, temperatures, top_k, top_p, min_p, out_ids):
-    """Checked arguments of a filtered sampling call; allocates out_ids if None."""
-    _check(logits, "logits", torch.float32, 2, contiguous=False)
-    if logits.stride(1) != 1 and logits.shape[1] > 1:
+def _sample_filtered(name, logits, temperatures, top_k, top_p, min_p, noise, out_ids, stream):
+    if not (type(logits) is torch.Tensor and logits.dtype is torch.float32 and logits.dim() == 2 and logits.is_cuda):
+        _check(logits, "logits", torch.float32, 2, contiguous=False)
+    batch, vocab = logits.shape
+    row, element = logits.stride()
+    if element != 1 and vocab > 1:
         raise ValueError("logits rows must be contiguous")
-    batch = logits.shape[0]
     if out_ids is None:
         out_ids = torch.empty(batch, dtype=torch.int64, device=logits.device)
-    for name, t, dtype in (("temperatures", temperatures, torch.float32), ("top_k", top_k, torch.int32),
-                           ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32),
-                           ("out_ids", out_ids, torch.int64)):
-        if t is None and name in ("top_k", "top_p", "min_p"):
-            continue
-        _check(t, name, dtype, 1)
+    tensors, filters = [logits, temperatures, out_ids], []
+    _want(temperatures, "temperatures", torch.float32, 1)
+    _want(out_ids, "out_ids", torch.int64, 1)
+    for what, t, dtype in (("top_k", top_k, torch.int32), ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
+        if t is None:
+            filters.append(None)
+        else:
+            _want(t, what, dtype, 1)
+            tensors.append(t)
+            filters.append(t.data_ptr())
+    for t in tensors[1:]:
         if t.shape[0] != batch:
-            raise ValueError(f"{name} must have one entry per row of logits ({batch}), got {t.shape[0]}")
+            raise ValueError(f"temperatures, filters and out_ids need one entry per row of logits ({batch}), got {t.shape[0]}")
+    if isinstance(noise, torch.Tensor):
+        tensors.append(noise)
+        noise = (noise.data_ptr(),)
+    _launch(name, getattr(load(), name), stream, tensors,
+            (logits.data_ptr(), batch, vocab, row if batch > 1 else vocab, temperatures.data_ptr(), *filters, *noise,
+             out_ids.data_ptr()))
     return out_ids
 
 
@@ -773,30 +812,19 @@ def pkv_sample_filtered(logits: torch.Tensor, temperatures: torch.Tensor, top_k:
                         out_ids: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The exponential race among the tokens that top-k, then top-p, then min-p keep (one setting per
     row; None: off for every row); returns int64 ids [batch].  All off: pkv_sample's winners."""
-    out_ids = _filter_args(logits, temperatures, top_k, top_p, min_p, out_ids)
-    batch, vocab = logits.shape
-    with _on_device(logits, temperatures, top_k, top_p, min_p, out_ids, stream=stream):
-        _raise(load().pkv_sample_filtered(_ptr(logits), batch, vocab, _row_stride(logits), _ptr(temperatures),
-                                          _ptr(top_k), _ptr(top_p), _ptr(min_p), int(seed) & (2 ** 64 - 1),
-                                          int(offset) & (2 ** 64 - 1), _ptr(out_ids), _stream(stream)),
-               "pkv_sample_filtered")
-    return out_ids
+    return _sample_filtered("pkv_sample_filtered", logits, temperatures, top_k, top_p, min_p,
+                            (int(seed) & (2 ** 64 - 1), int(offset) & (2 ** 64 - 1)), out_ids, stream)
 
 
 def pkv_sample_filtered_dev(logits: torch.Tensor, temperatures: torch.Tensor, top_k: Optional[torch.Tensor],
                             top_p: Optional[torch.Tensor], min_p: Optional[torch.Tensor], seed_offset: torch.Tensor,
                             out_ids: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """pkv_sample_filtered with {seed, offset} read from a device int64 tensor of 2 elements."""
-    out_ids = _filter_args(logits, temperatures, top_k, top_p, min_p, out_ids)
     _check(seed_offset, "seed_offset", torch.int64, 1)
     if seed_offset.numel() != 2:
         raise ValueError("seed_offset holds {seed, offset}")
-    batch, vocab = logits.shape
-    with _on_device(logits, temperatures, top_k, top_p, min_p, seed_offset, out_ids, stream=stream):
-        _raise(load().pkv_sample_filtered_dev(_ptr(logits), batch, vocab, _row_stride(logits), _ptr(temperatures),
-                                              _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(seed_offset), _ptr(out_ids),
-                                              _stream(stream)), "pkv_sample_filtered_dev")
-    return out_ids
+    return _sample_filtered("pkv_sample_filtered_dev", logits, temperatures, top_k, top_p, min_p, seed_offset, out_ids,
+                            stream)
 
 
 WAIT_CHECK_INFO = 0x5741
