@@ -127,13 +127,13 @@ bool setup_once(SetupKey key, bool (*setup)()) {
 
 CUresult encode_tiled(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t rank, void* base,
                       const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
-                      CUtensorMapSwizzle swizzle) {
+                      CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promotion) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return CUDA_ERROR_NOT_SUPPORTED;
     cuuint32_t elem_strides[5] = {1, 1, 1, 1, 1};
     return fn(map, dtype, rank, base, reinterpret_cast<const cuuint64_t*>(dims),
               reinterpret_cast<const cuuint64_t*>(strides_bytes), reinterpret_cast<const cuuint32_t*>(box),
-              elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promotion,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 

@@ -27,10 +27,13 @@
 // * Both references move only when a score exceeds them by a margin (w <= 2^8 stays far below
 //   f16's 65504, l's terms below 2^64), found by one vote per chunk; the rescale is a rare branch.
 //
-// Work split, as in the bf16 decode kernel: the batch's KV in 32-token chunks ordered (sequence,
-// KV head, chunk), every warp of a persistent grid taking one contiguous run of equal length; a
-// run that crosses a (sequence, KV head) border writes a piece (m, l, o) for each side, and a
-// second kernel merges each head's pieces in run order, so results do not depend on timing.
+// Work split: the batch's tokens in 32-token chunks, sequence after sequence, are cut into equal
+// contiguous runs, one for each group of num_kv_heads warps of a persistent grid; warp h of the
+// group walks its run for KV head h.  A token's rows of all heads are contiguous in the pool, so
+// the warps of a group, which advance together, read whole DRAM pages between them: a head's row
+// alone is 128 bytes at a stride of a token.  A run that crosses a sequence border writes a piece
+// (m, l, o) for each side, and a second kernel merges each head's pieces in run order, so results
+// do not depend on timing.
 // Each warp owns a ring of shared-memory stages, each holding a chunk's K and V codes (TMA tiles
 // with 128-byte swizzle: conflict-free 16-byte loads below) and its 2 x 32 scale bytes, all
 // landing on one mbarrier.
@@ -51,7 +54,7 @@ constexpr int TILE_BYTES = CHUNK * D;        // one e4m3 tile
 constexpr int STAGE_BYTES = 2 * TILE_BYTES;  // K, V
 constexpr int SCALE_BYTES = 2 * CHUNK;       // a stage's K scales, V scales
 constexpr int MAX_BATCH = 4096;
-constexpr int KMIN = 4;                      // chunks a warp takes at least, where the batch allows it
+constexpr int KMIN = 2;                      // chunks a warp takes at least, where the batch allows it
 constexpr float kMarginT = 8.f;              // log2 headroom of the weights over their reference
 constexpr float kMarginM = 64.f;             // and of the softmax terms over theirs
 static_assert(TILE_BYTES % 1024 == 0, "swizzled tiles start on 1 KiB");
@@ -68,50 +71,39 @@ struct Params {
     int block_size;
     int num_blocks;
     float scale_log2;      // softmax scale * log2(e)
-    int total_warps;
-    int32_t* plan;         // [batch + 1] chunk prefix per sequence (per KV head)
-    float* part_ml;        // [pieces][G][2]  (m, l); piece = (sequence, KV head) + run
+    int groups;            // groups of num_kv_heads warps in the grid
+    int32_t* plan;         // [batch + 1] chunks before each sequence
+    float* part_ml;        // [pieces][G][2]  (m, l); piece = (sequence + run) * num_kv_heads + KV head
     float* part_o;         // [pieces][G][D]
     int* err;
 };
 
-// Runs the work is cut over: every warp, unless that left fewer than KMIN chunks to a run.
-__device__ __forceinline__ int runs_of(int total_warps, int64_t total) {
-    const int64_t w = (total + KMIN - 1) / KMIN;
-    return static_cast<int>(w < total_warps ? (w > 0 ? w : 1) : total_warps);
+// Runs the `total` chunks are cut into: one for each group, unless that left fewer than KMIN chunks to a run.
+__device__ __forceinline__ int runs_of(int groups, int total) {
+    return max(1, min(groups, (total + KMIN - 1) / KMIN));
 }
 
-// floor(a b / c) of non-negative numbers; `narrow`: a b is known to fit in 32 bits.
-__device__ __forceinline__ int64_t mul_div(int64_t a, int64_t b, int64_t c, bool narrow) {
-    if (narrow)
-        return static_cast<int64_t>(static_cast<uint32_t>(a) * static_cast<uint32_t>(b) / static_cast<uint32_t>(c));
-    return a * b / c;
+// First chunk of run r.
+__device__ __forceinline__ int run_begin(int r, int total, int runs) {
+    return static_cast<int>(static_cast<uint64_t>(r) * static_cast<uint32_t>(total) / static_cast<uint32_t>(runs));
 }
 
 struct Cursor {
-    int b, g, c, n;   // sequence, KV head, chunk within it, chunks of the sequence
+    int b, c, n;      // sequence, chunk within it, chunks of the sequence
 };
 
-__device__ __forceinline__ Cursor cursor_at(const int32_t* prefix, int batch, int hkv, int64_t i) {
-    int lo = 0, hi = batch;          // hkv * prefix[lo] <= i < hkv * prefix[hi]
+__device__ __forceinline__ Cursor cursor_at(const int32_t* prefix, int batch, int i) {
+    int lo = 0, hi = batch;          // prefix[lo] <= i < prefix[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (static_cast<int64_t>(hkv) * prefix[mid] <= i) lo = mid; else hi = mid;
+        if (prefix[mid] <= i) lo = mid; else hi = mid;
     }
-    Cursor cu;
-    cu.b = lo;
-    cu.n = prefix[lo + 1] - prefix[lo];
-    const int64_t rem = i - static_cast<int64_t>(hkv) * prefix[lo];
-    cu.g = static_cast<int>(rem / cu.n);
-    cu.c = static_cast<int>(rem - static_cast<int64_t>(cu.g) * cu.n);
-    return cu;
+    return Cursor{lo, i - prefix[lo], prefix[lo + 1] - prefix[lo]};
 }
 
-__device__ __forceinline__ void cursor_next(Cursor& cu, const int32_t* prefix, int batch, int hkv) {
+__device__ __forceinline__ void cursor_next(Cursor& cu, const int32_t* prefix, int batch) {
     if (++cu.c < cu.n) return;
     cu.c = 0;
-    if (++cu.g < hkv) return;
-    cu.g = 0;
     do { ++cu.b; } while (cu.b < batch && prefix[cu.b + 1] == prefix[cu.b]);
     cu.n = cu.b < batch ? prefix[cu.b + 1] - prefix[cu.b] : 0;
 }
@@ -143,12 +135,12 @@ __device__ __forceinline__ uint32_t ld_shared_u8(uint32_t addr) {
 
 // The raw query words of this lane: head g = lane / 4 of the group, dims 32 (lane % 4) ... + 31.
 template <int G>
-__device__ __forceinline__ void load_q(const Params& p, const Cursor& cu, int lane, uint4 (&w)[4]) {
+__device__ __forceinline__ void load_q(const Params& p, int b, int kv_head, int lane, uint4 (&w)[4]) {
     const int h = lane >> 2;
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = make_uint4(0, 0, 0, 0);
     if (h < G) {
-        const uint16_t* row = p.q + (static_cast<int64_t>(cu.b) * p.num_kv_heads + cu.g) * (G * D) + h * D + 32 * (lane & 3);
+        const uint16_t* row = p.q + (static_cast<int64_t>(b) * p.num_kv_heads + kv_head) * (G * D) + h * D + 32 * (lane & 3);
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(row) + i);
     }
@@ -228,14 +220,14 @@ decode_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     if (blockIdx.x == 0)
         for (int b = tid; b <= p.batch; b += THREADS) p.plan[b] = prefix[b];
 
-    // ---- this warp's run of chunks
+    // ---- this warp's run of chunks and KV head
     const int gw = blockIdx.x * WARPS + warp;
-    const int64_t total = static_cast<int64_t>(hkv) * prefix[p.batch];
-    const int W = runs_of(p.total_warps, total);
-    if (gw >= W) return;
-    const bool narrow = total * W <= 0xffffffffll;
-    const int64_t begin = mul_div(gw, total, W, narrow);
-    const int n_mine = static_cast<int>(mul_div(gw + 1, total, W, narrow) - begin);
+    const int run_id = gw / hkv, head = gw - run_id * hkv;
+    const int total = prefix[p.batch];
+    const int W = runs_of(p.groups, total);
+    if (run_id >= W) return;
+    const int begin = run_begin(run_id, total, W);
+    const int n_mine = run_begin(run_id + 1, total, W) - begin;
     if (n_mine <= 0) return;
 
     const uint32_t stage0 = smem_u32(smem) + warp * STAGES * STAGE_BYTES;
@@ -250,15 +242,13 @@ decode_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     __syncwarp();
     const uint64_t policy = l2_policy_evict_first();
 
-    // ---- copies: a cursor of their own and a window of 32 block-table entries
-    Cursor pc = cursor_at(prefix, p.batch, hkv, begin);
+    // ---- copies: a cursor of their own, the block it is in, and a window of 32 block-table entries
+    Cursor pc = cursor_at(prefix, p.batch, begin);
     Cursor cc = pc;
+    int blk = pc.c * CHUNK / p.block_size, off = pc.c * CHUNK - blk * p.block_size;
     int bt_b = -1, bt_base = 0, bt_lane = -1;
-    int issued = 0;
+    int issued = 0, put = 0;         // chunks issued; the stage the next one goes to
     auto issue_next = [&]() {
-        const int s = issued % STAGES;
-        const int tok = pc.c * CHUNK;
-        const int blk = tok / p.block_size;
         if (pc.b != bt_b || blk < bt_base || blk >= bt_base + 32) {
             bt_b = pc.b;
             bt_base = blk;
@@ -269,19 +259,22 @@ decode_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         if (lane == 0) {
             const bool known = phys >= 0 && phys < p.num_blocks;
             if (!known) record_error(p.err, PKV_DEVERR_BLOCK_ID, pc.b);
-            const uint32_t bar = bar0 + 8 * s;
-            const uint32_t dst = stage0 + s * STAGE_BYTES, sdst = scale0 + s * SCALE_BYTES;
-            const int off = tok - blk * p.block_size;
+            const uint32_t bar = bar0 + 8 * put;
+            const uint32_t dst = stage0 + put * STAGE_BYTES, sdst = scale0 + put * SCALE_BYTES;
             // the tensor copies fill a block outside the pool with zeros; its scales come from block 0
-            const int64_t srow = (static_cast<int64_t>(known ? phys : 0) * hkv + pc.g) * p.block_size + off;
+            const int64_t srow = (static_cast<int64_t>(known ? phys : 0) * hkv + head) * p.block_size + off;
             mbar_arrive_expect_tx(bar, STAGE_BYTES + SCALE_BYTES);
-            tma_load_4d_hint(dst, &tm_k, bar, 0, pc.g, off, phys, policy);
-            tma_load_4d_hint(dst + TILE_BYTES, &tm_v, bar, 0, pc.g, off, phys, policy);
+            tma_load_4d_hint(dst, &tm_k, bar, 0, head, off, phys, policy);
+            tma_load_4d_hint(dst + TILE_BYTES, &tm_v, bar, 0, head, off, phys, policy);
             bulk_load(sdst, p.k_scale + srow, CHUNK, bar);
             bulk_load(sdst + CHUNK, p.v_scale + srow, CHUNK, bar);
         }
         ++issued;
-        cursor_next(pc, prefix, p.batch, hkv);
+        put = put + 1 == STAGES ? 0 : put + 1;
+        off += CHUNK;
+        if (off == p.block_size) { off = 0; ++blk; }
+        cursor_next(pc, prefix, p.batch);
+        if (pc.c == 0) blk = off = 0;
     };
     for (int i = 0; i < min(n_mine, STAGES); ++i) issue_next();
 
@@ -291,7 +284,7 @@ decode_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     uint32_t qb[16];
     float qf[2];
     uint4 qw[4];
-    load_q<G>(p, cc, lane, qw);
+    load_q<G>(p, cc.b, head, lane, qw);
     make_q(qw, p.scale_log2, lane, qb, qf);
     int L = length_of(cc.b);
     // the next segment's query rows and length, loaded while this one streams
@@ -300,8 +293,8 @@ decode_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         if (n_mine - done <= cc.n - cc.c) return;
         Cursor nx = cc;
         nx.c = nx.n - 1;
-        cursor_next(nx, prefix, p.batch, hkv);
-        load_q<G>(p, nx, lane, qw);
+        cursor_next(nx, prefix, p.batch);
+        load_q<G>(p, nx.b, head, lane, qw);
         L_next = length_of(nx.b);
     };
     prefetch_next(0);
@@ -319,14 +312,15 @@ decode_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     };
     reset();
 
-    int k = 0;
+    int k = 0, st = 0;               // chunk of the run; its stage
+    uint32_t parity = 0;
     bool failed = false;
     for (; k < n_mine; ++k) {
-        const int s = k % STAGES;
-        const bool ok = mbar_wait(bar0 + 8 * s, (k / STAGES) & 1, p.err, gw);
+        const bool ok = mbar_wait(bar0 + 8 * st, parity, p.err, gw);
         if (__any_sync(0xffffffffu, !ok)) { failed = true; break; }
-        const uint32_t kb = stage0 + s * STAGE_BYTES, vb = kb + TILE_BYTES;
-        const uint32_t sb = scale0 + s * SCALE_BYTES;
+        const uint32_t kb = stage0 + st * STAGE_BYTES, vb = kb + TILE_BYTES;
+        const uint32_t sb = scale0 + st * SCALE_BYTES;
+        if (++st == STAGES) { st = 0; parity ^= 1u; }
         const int valid = min(CHUNK, L - cc.c * CHUNK);
         if (valid < CHUNK) {
             // slots past the sequence's end may hold anything (a freed block is not cleared); their
@@ -335,6 +329,8 @@ decode_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vb + valid * D + i * 16), "r"(0) : "memory");
             __syncwarp();
         }
+        // this lane's key's scales (key = lane), as a factor and an exponent
+        const float kf_lane = e8m0_value(ld_shared_u8(sb + lane)), ev_lane = e8m0_exponent(ld_shared_u8(sb + CHUNK + lane));
         // ---- scores: S^T = K Q^T, 16 keys per tile; step e takes dims 32t + 4e .. + 3 of this lane's piece
         float c[2][4];
 #pragma unroll
@@ -353,52 +349,62 @@ decode_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 mma_f16(c[i], a0, a1, a2, a3, qb[2 * e], qb[2 * e + 1]);
             }
         }
-        // ---- log2-domain scores; this lane: keys g + 8 r, heads 2t, 2t + 1
-        float sc[4][2], ms[2] = {-INFINITY, -INFINITY};
+        // ---- log2-domain scores relative to m; this lane: keys g + 8 r, heads 2t, 2t + 1
+        float d[4][2], w[4][2];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int key = g + 8 * r;
-            const float kf = e8m0_value(ld_shared_u8(sb + key));
+            const float kf = __shfl_sync(0xffffffffu, kf_lane, g + 8 * r);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) d[r][h] = fmaf(c[r >> 1][(r & 1) * 2 + h] * qf[h], kf, -m[h]);
+        }
+        if (valid < CHUNK) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (g + 8 * r >= valid) d[r][0] = d[r][1] = -INFINITY;
+        }
+        const float d_max = fmax3(fmax3(d[0][0], d[0][1], d[1][0]), fmax3(d[1][1], d[2][0], d[2][1]), fmaxf(d[3][0], d[3][1]));
+        if (__any_sync(0xffffffffu, fresh || d_max > kMarginM)) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                sc[r][h] = key < valid ? (c[r >> 1][(r & 1) * 2 + h] * qf[h]) * kf : -INFINITY;
-                ms[h] = fmaxf(ms[h], sc[r][h]);
+                float up = fmaxf(fmaxf(d[0][h], d[1][h]), fmaxf(d[2][h], d[3][h]));
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, x));
+                if (!fresh) up = fmaxf(up, 0.f);
+                if (!(fabsf(up) < INFINITY)) up = 0.f;   // no finite score: any reference does
+                m[h] += up;
+                l[h] *= fresh ? 1.f : ex2_ftz(-up);      // a fresh l is 0, and up may be any score
+                // o keeps its units; below 2^-256 it is nothing beside the new maximum's weight (>= 2^-126), and a
+                // larger T would cost the next weights their low bits
+                T[h] = fresh ? 0.f : fmaxf(T[h] - up, -256.f);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) d[r][h] -= up;
             }
         }
-        if (__any_sync(0xffffffffu, fresh || ms[0] > m[0] + kMarginM || ms[1] > m[1] + kMarginM)) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                for (int off = 4; off < 32; off <<= 1) ms[h] = fmaxf(ms[h], __shfl_xor_sync(0xffffffffu, ms[h], off));
-                float m_new = fresh ? ms[h] : fmaxf(m[h], ms[h]);
-                if (!(fabsf(m_new) < INFINITY)) m_new = fresh ? 0.f : m[h];   // no finite score: any reference does
-                l[h] *= ex2_ftz(m[h] - m_new);
-                T[h] += m[h] - m_new;                 // o keeps its units
-                m[h] = m_new;
-            }
-        }
-        // ---- exponents of the weights, relative to m: s - m + ev
-        float wt[4][2], mw[2] = {-INFINITY, -INFINITY};
+        // ---- exponents of the weights over their reference: s - m + ev - T
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int key = g + 8 * r;
-            const float ev = e8m0_exponent(ld_shared_u8(sb + CHUNK + key));
+            const float ev = __shfl_sync(0xffffffffu, ev_lane, g + 8 * r);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                sc[r][h] -= m[h];
-                wt[r][h] = key < valid ? sc[r][h] + ev : -INFINITY;
-                mw[h] = fmaxf(mw[h], wt[r][h]);
-            }
+            for (int h = 0; h < 2; ++h) w[r][h] = (d[r][h] + ev) - T[h];
         }
-        if (__any_sync(0xffffffffu, fresh || mw[0] > T[0] + kMarginT || mw[1] > T[1] + kMarginT)) {
+        if (valid < CHUNK) {                             // whatever scale a slot past the end has
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (g + 8 * r >= valid) w[r][0] = w[r][1] = -INFINITY;
+        }
+        const float w_max = fmax3(fmax3(w[0][0], w[0][1], w[1][0]), fmax3(w[1][1], w[2][0], w[2][1]), fmaxf(w[3][0], w[3][1]));
+        if (__any_sync(0xffffffffu, fresh || w_max > kMarginT)) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
+                float up = fmaxf(fmaxf(w[0][h], w[1][h]), fmaxf(w[2][h], w[3][h]));
 #pragma unroll
-                for (int off = 4; off < 32; off <<= 1) mw[h] = fmaxf(mw[h], __shfl_xor_sync(0xffffffffu, mw[h], off));
-                float T_new = fresh ? mw[h] : fmaxf(T[h], mw[h]);
-                if (!(fabsf(T_new) < INFINITY)) T_new = fresh ? 0.f : T[h];
-                const float f = fresh ? 1.f : ex2_ftz(T[h] - T_new);          // a fresh o is 0
-                T[h] = T_new;
+                for (int x = 4; x < 32; x <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, x));
+                if (!fresh) up = fmaxf(up, 0.f);
+                if (!(fabsf(up) < INFINITY)) up = 0.f;
+                T[h] += up;
+                const float f = fresh ? 1.f : ex2_ftz(-up);          // a fresh o is 0
+#pragma unroll
+                for (int r = 0; r < 4; ++r) w[r][h] -= up;
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
                     o[u][h] *= f;
@@ -410,9 +416,9 @@ decode_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         uint32_t pb[4];               // P^T operand: key pairs of this lane's head g
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            l[0] += ex2_ftz(sc[r][0]);
-            l[1] += ex2_ftz(sc[r][1]);
-            pb[r] = transposed_8x8(pack_f16x2(ex2_ftz(wt[r][0] - T[0]), ex2_ftz(wt[r][1] - T[1])));
+            l[0] += ex2_ftz(d[r][0]);
+            l[1] += ex2_ftz(d[r][1]);
+            pb[r] = transposed_8x8(pack_f16x2(ex2_ftz(w[r][0]), ex2_ftz(w[r][1])));
         }
         // ---- O^T += V^T P^T, 16 keys per step; row g of tile u: dim 16g + 2u, row g + 8: dim 16g + 2u + 1
 #pragma unroll
@@ -438,28 +444,28 @@ decode_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         __syncwarp();
         if (issued < n_mine) issue_next();
 
-        // ---- end of the (sequence, KV head) segment or of the run: write the piece
+        // ---- end of the sequence or of the run: write the piece
         if (cc.c == cc.n - 1 || k == n_mine - 1) {
-            const int64_t piece = static_cast<int64_t>(cc.b) * hkv + cc.g + gw;
+            const int64_t piece = static_cast<int64_t>(cc.b + run_id) * hkv + head;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], off);
-                const int head = 2 * t + h;
-                if (head < G) {
+                const int hq = 2 * t + h;                      // query head of the group
+                if (hq < G) {
                     const float f = ex2_ftz(T[h]);             // from the weights' reference to the sum's
-                    float4* dst = reinterpret_cast<float4*>(p.part_o + (piece * G + head) * D + 16 * g);
+                    float4* dst = reinterpret_cast<float4*>(p.part_o + (piece * G + hq) * D + 16 * g);
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
                         dst[u] = make_float4(o[2 * u][h] * f, o[2 * u][2 + h] * f, o[2 * u + 1][h] * f, o[2 * u + 1][2 + h] * f);
                     if (g == 0) {
-                        p.part_ml[(piece * G + head) * 2] = m[h];
-                        p.part_ml[(piece * G + head) * 2 + 1] = l[h];
+                        p.part_ml[(piece * G + hq) * 2] = m[h];
+                        p.part_ml[(piece * G + hq) * 2 + 1] = l[h];
                     }
                 }
             }
             if (k != n_mine - 1) {
-                cursor_next(cc, prefix, p.batch, hkv);
+                cursor_next(cc, prefix, p.batch);
                 make_q(qw, p.scale_log2, lane, qb, qf);
                 L = L_next;
                 prefetch_next(k + 1);
@@ -470,20 +476,24 @@ decode_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         }
     }
     if (failed)       // copies in flight land before the CTA's shared memory goes away
-        for (int i = k; i < issued; ++i) {
-            const bool ok = mbar_wait(bar0 + 8 * (i % STAGES), (i / STAGES) & 1, p.err, gw);
+        for (; k < issued; ++k) {
+            const bool ok = mbar_wait(bar0 + 8 * st, parity, p.err, gw);
+            if (++st == STAGES) { st = 0; parity ^= 1u; }
             if (__any_sync(0xffffffffu, !ok)) break;
         }
 }
 
-// One warp per (sequence, query head) merges its pieces in run order.
-template <int G>
+// Merge the pieces of each (sequence, query head): SPLIT warps take every SPLIT-th piece in run order
+// each, and their sums are added in warp order.
+template <int G, int SPLIT>
 __global__ void __launch_bounds__(128) decode_fp8_combine_kernel(const Params p, int num_heads, uint16_t* __restrict__ out) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int lane = threadIdx.x & 31;
-    const int idx = blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (idx >= p.batch * num_heads) return;
+    __shared__ float4 part[4][32];
+    __shared__ float2 part_ml[4];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int idx = blockIdx.x * (4 / SPLIT) + warp / SPLIT, sub = warp % SPLIT;
+    if (idx >= p.batch * num_heads) return;               // whole CTAs only if SPLIT > 1
     const int b = idx / num_heads;
     const int h = idx - b * num_heads;
     const int g = h / G, hh = h - g * G;
@@ -491,48 +501,67 @@ __global__ void __launch_bounds__(128) decode_fp8_combine_kernel(const Params p,
     const int first = p.plan[b], n = p.plan[b + 1] - first, all = p.plan[p.batch];
     uint2* dst = reinterpret_cast<uint2*>(out + static_cast<int64_t>(idx) * D + 4 * lane);
     if (n == 0) {
-        *dst = make_uint2(0u, 0u);
+        if (sub == 0) *dst = make_uint2(0u, 0u);
         return;
     }
-    const int64_t total = static_cast<int64_t>(hkv) * all;
-    const int64_t W = runs_of(p.total_warps, total);
-    const int64_t start = static_cast<int64_t>(hkv) * first + static_cast<int64_t>(g) * n;
-    const bool narrow = total * W <= 0xffffffffll;
-    // the run that holds chunk i is floor(((i + 1) W - 1) / total); W <= total, so every run holds a chunk
-    auto run_of = [&](int64_t i) -> int {
-        return narrow ? static_cast<int>((static_cast<uint32_t>(i + 1) * static_cast<uint32_t>(W) - 1u) / static_cast<uint32_t>(total))
-                      : static_cast<int>(((i + 1) * W - 1) / total);
+    const int W = runs_of(p.groups, all);
+    // the run that holds chunk i is floor(((i + 1) W - 1) / all); W <= all, so every run holds a chunk
+    auto run_of = [&](int i) {
+        return static_cast<int>((static_cast<uint64_t>(i + 1) * static_cast<uint32_t>(W) - 1) / static_cast<uint32_t>(all));
     };
-    const int wf = run_of(start), wl = run_of(start + n - 1);
-    const int64_t piece0 = static_cast<int64_t>(b) * hkv + g;
+    const int wf = run_of(first), wl = run_of(first + n - 1);
     constexpr int BATCH = 4;        // pieces whose loads are issued together
-    float M = -INFINITY;
-    for (int w0 = wf; w0 <= wl; w0 += 32)
-        if (w0 + lane <= wl) M = fmaxf(M, p.part_ml[((piece0 + w0 + lane) * G + hh) * 2]);
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    float L = 0.f;
+    float M = -INFINITY, L = 0.f;   // sums relative to the running maximum
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int w0 = wf; w0 <= wl; w0 += BATCH) {
+    for (int w0 = wf + sub; w0 <= wl; w0 += BATCH * SPLIT) {
         float2 ml[BATCH];
         float4 v[BATCH];
 #pragma unroll
         for (int i = 0; i < BATCH; ++i)
-            if (w0 + i <= wl) {
-                const int64_t at = (piece0 + w0 + i) * G + hh;
+            if (w0 + i * SPLIT <= wl) {
+                const int64_t at = (static_cast<int64_t>(b + w0 + i * SPLIT) * hkv + g) * G + hh;
                 ml[i] = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
                 v[i] = *reinterpret_cast<const float4*>(p.part_o + at * D + 4 * lane);
+            } else {
+                ml[i] = make_float2(-INFINITY, 0.f);
+                v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             }
+        const float m_new = fmax3(M, fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));   // finite: a piece's m is
+        const float keep = ex2_ftz(M - m_new);
+        L *= keep;
+        acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
+        M = m_new;
 #pragma unroll
-        for (int i = 0; i < BATCH; ++i)
-            if (w0 + i <= wl) {
-                const float f = exp2f(ml[i].x - M);
-                L = fmaf(f, ml[i].y, L);
-                acc.x = fmaf(f, v[i].x, acc.x);
-                acc.y = fmaf(f, v[i].y, acc.y);
-                acc.z = fmaf(f, v[i].z, acc.z);
-                acc.w = fmaf(f, v[i].w, acc.w);
-            }
+        for (int i = 0; i < BATCH; ++i) {
+            const float f = exp2f(ml[i].x - M);
+            L = fmaf(f, ml[i].y, L);
+            acc.x = fmaf(f, v[i].x, acc.x);
+            acc.y = fmaf(f, v[i].y, acc.y);
+            acc.z = fmaf(f, v[i].z, acc.z);
+            acc.w = fmaf(f, v[i].w, acc.w);
+        }
+    }
+    if (SPLIT > 1) {
+        part[warp][lane] = acc;
+        if (lane == 0) part_ml[warp] = make_float2(M, L);
+        __syncthreads();
+        if (sub != 0) return;
+        float m_all = M;
+#pragma unroll
+        for (int i = 1; i < SPLIT; ++i) m_all = fmaxf(m_all, part_ml[warp + i].x);
+        L = 0.f;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < SPLIT; ++i) {
+            const float2 ml = part_ml[warp + i];
+            const float4 v = part[warp + i][lane];
+            const float f = exp2f(ml.x - m_all);          // 0 for a warp without a piece
+            L = fmaf(f, ml.y, L);
+            acc.x = fmaf(f, v.x, acc.x);
+            acc.y = fmaf(f, v.y, acc.y);
+            acc.z = fmaf(f, v.z, acc.z);
+            acc.w = fmaf(f, v.w, acc.w);
+        }
     }
     const float inv = 1.f / L;
     *dst = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
@@ -551,25 +580,28 @@ bool set_smem_attr(int bytes) {
 
 template <int G>
 pkv_status launch_pair(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Params& p, int num_heads, uint16_t* out,
-                       cudaStream_t stream) {
+                       int sms, cudaStream_t stream) {
     // both launches are programmatic dependents of what precedes them in the stream; each kernel waits
     // for its predecessor's completion before touching global memory
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.total_warps / WARPS);
+    cfg.gridDim = dim3(sms);
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = dynamic_smem_bytes(p.batch);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, decode_fp8_kernel<G>, tm_k, tm_v, p) != cudaSuccess) return PKV_ERR_CUDA;
-    cfg.gridDim = dim3((p.batch * num_heads + 3) / 4);
+    // a sequence is cut into about groups / batch pieces: with four or more, four warps share a head's merge
+    const bool split = p.groups >= 4 * p.batch;
+    cfg.gridDim = dim3(split ? p.batch * num_heads : (p.batch * num_heads + 3) / 4);
     cfg.blockDim = dim3(128);
     cfg.dynamicSmemBytes = 0;
-    if (cudaLaunchKernelEx(&cfg, decode_fp8_combine_kernel<G>, p, num_heads, out) != cudaSuccess) return PKV_ERR_CUDA;
-    return PKV_OK;
+    const cudaError_t e = split ? cudaLaunchKernelEx(&cfg, decode_fp8_combine_kernel<G, 4>, p, num_heads, out)
+                                : cudaLaunchKernelEx(&cfg, decode_fp8_combine_kernel<G, 1>, p, num_heads, out);
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 }  // namespace
@@ -589,6 +621,9 @@ pkv_status launch_decode_fp8(const DecodeFp8Args& a, int* err, cudaStream_t stre
     if (a.workspace == nullptr || a.workspace_bytes < decode_fp8_workspace_bytes(a.batch, a.num_kv_heads, lg))
         return PKV_ERR_WORKSPACE;
     if (a.batch == 0) return PKV_OK;
+    // the chunks of a batch are counted in 32 bits
+    if (static_cast<int64_t>(a.batch) * ((static_cast<int64_t>(a.max_blocks) * a.block_size + CHUNK - 1) / CHUNK) > 0x7fffffffLL)
+        return PKV_ERR_UNSUPPORTED;
 
     CUtensorMap tm_k, tm_v;
     const uint64_t dims[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(a.num_kv_heads),
@@ -597,9 +632,9 @@ pkv_status launch_decode_fp8(const DecodeFp8Args& a, int* err, cudaStream_t stre
                                  static_cast<uint64_t>(a.block_size) * a.num_kv_heads * D};
     const uint32_t box[4] = {static_cast<uint32_t>(D), 1u, static_cast<uint32_t>(CHUNK), 1u};
     if (encode_tiled(&tm_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(a.k_cache), dims, strides, box,
-                     CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B) != CUDA_SUCCESS ||
         encode_tiled(&tm_v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(a.v_cache), dims, strides, box,
-                     CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B) != CUDA_SUCCESS)
         return PKV_ERR_INVALID_ARG;
 
     if (!setup_once(kSetupDecodeFp8, [] {
@@ -621,8 +656,9 @@ pkv_status launch_decode_fp8(const DecodeFp8Args& a, int* err, cudaStream_t stre
     p.block_size = a.block_size;
     p.num_blocks = a.num_blocks;
     p.scale_log2 = a.softmax_scale * 1.4426950408889634f;
-    p.total_warps = sms * WARPS;
-    const size_t pieces = static_cast<size_t>(a.batch) * a.num_kv_heads + p.total_warps;
+    p.groups = sms * WARPS / a.num_kv_heads;
+    if (p.groups < 1) return PKV_ERR_UNSUPPORTED;
+    const size_t pieces = static_cast<size_t>(a.batch + p.groups) * a.num_kv_heads;
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     p.plan = reinterpret_cast<int32_t*>(ws);
     ws += align256(static_cast<size_t>(a.batch + 1) * 4);
@@ -631,10 +667,10 @@ pkv_status launch_decode_fp8(const DecodeFp8Args& a, int* err, cudaStream_t stre
     p.part_o = reinterpret_cast<float*>(ws);
     p.err = err;
     switch (lg) {
-        case 0: return launch_pair<1>(tm_k, tm_v, p, a.num_heads, a.out, stream);
-        case 1: return launch_pair<2>(tm_k, tm_v, p, a.num_heads, a.out, stream);
-        case 2: return launch_pair<4>(tm_k, tm_v, p, a.num_heads, a.out, stream);
-        default: return launch_pair<8>(tm_k, tm_v, p, a.num_heads, a.out, stream);
+        case 0: return launch_pair<1>(tm_k, tm_v, p, a.num_heads, a.out, sms, stream);
+        case 1: return launch_pair<2>(tm_k, tm_v, p, a.num_heads, a.out, sms, stream);
+        case 2: return launch_pair<4>(tm_k, tm_v, p, a.num_heads, a.out, sms, stream);
+        default: return launch_pair<8>(tm_k, tm_v, p, a.num_heads, a.out, sms, stream);
     }
 }
 

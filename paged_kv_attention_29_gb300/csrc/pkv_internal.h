@@ -32,7 +32,8 @@ bool setup_once(SetupKey key, bool (*setup)());
 // cuTensorMapEncodeTiled through the runtime's driver entry point.
 CUresult encode_tiled(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t rank, void* base,
                       const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
-                      CUtensorMapSwizzle swizzle);
+                      CUtensorMapSwizzle swizzle,
+                      CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 
 // ---- a1 / a2 --------------------------------------------------------------
 cudaError_t launch_slot_mapping(const int32_t* cu_q, const int32_t* cu_k, const int32_t* ctx,
