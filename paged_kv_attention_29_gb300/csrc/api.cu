@@ -491,7 +491,16 @@ pkv_status store_fp8_call(const pkv_bf16* q, int64_t q_token_stride, pkv_bf16* q
     a.num_heads = q ? num_heads : 0;
     a.num_kv_heads = num_kv_heads;
     a.block_size = block_size;
-    if (rotate) rope_turns(rope_base, head_dim, a.turns);
+    if (rotate) {
+        // 64 powers, the same for every call of a model: kept for the thread's last base
+        static thread_local double base = 0.0;
+        static thread_local uint64_t turns[kHeadDim / 2];
+        if (base != rope_base) {
+            rope_turns(rope_base, kHeadDim, turns);
+            base = rope_base;
+        }
+        for (int i = 0; i < kHeadDim / 2; ++i) a.turns[i] = turns[i];
+    }
     int* err = device_error_word();
     if (!err) return PKV_ERR_CUDA;
     return launch_store_fp8(a, n_tokens, err, as_stream(stream)) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;

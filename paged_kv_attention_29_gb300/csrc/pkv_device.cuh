@@ -376,11 +376,13 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(uint32_t M, uint32_t N, ui
 // position is |p| turned the other way.  On [-pi, pi] the hardware sine and
 // cosine approximation is within 4e-7 absolute, a few fp32 roundings of the
 // rotated value, and keeps the table off the CTA's critical path.
-__device__ __forceinline__ float reduced_angle(int pos, uint32_t f_lo, uint32_t f_hi) {
+__device__ __forceinline__ uint32_t turns_of(int pos, uint32_t f_lo, uint32_t f_hi) {
     const uint32_t m = pos < 0 ? 0u - static_cast<uint32_t>(pos) : static_cast<uint32_t>(pos);
-    uint32_t turns = __umulhi(m, f_lo) + m * f_hi;
-    if (pos < 0) turns = 0u - turns;
-    return static_cast<float>(static_cast<int32_t>(turns)) * 1.4629180792671596e-9f;   // 2 pi / 2^32
+    const uint32_t turns = __umulhi(m, f_lo) + m * f_hi;
+    return pos < 0 ? 0u - turns : turns;
+}
+__device__ __forceinline__ float reduced_angle(int pos, uint32_t f_lo, uint32_t f_hi) {
+    return static_cast<float>(static_cast<int32_t>(turns_of(pos, f_lo, f_hi))) * 1.4629180792671596e-9f;   // 2 pi / 2^32
 }
 
 // ---------------------------------------------------------------------------

@@ -26,6 +26,7 @@ namespace {
 constexpr int THREADS = 256;
 constexpr int ROW_LANES = 8;
 constexpr int GROUP = 32 / ROW_LANES;    // rows a warp holds at a time
+constexpr int CTAS_PER_SM = 2;
 
 // The E8M0 byte of a row whose largest |x| has these fp32 bits (largest as an integer, so an
 // infinity or a NaN in the row shows as an exponent of 255).  448 = 1.75 * 2^8: with
@@ -46,106 +47,148 @@ __device__ __forceinline__ uint2 to_codes(const float (&x)[8], float inv) {
     return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
+// (cos, sin) of the angle that is turns / 2^32 of a turn.  The quadrant is taken off in integers, so
+// what reaches the functions is at most an eighth of a turn, rounded to 2^-25 of itself, and the
+// result is within a few 2^-24 -- which decides fewer roundings to e4m3 otherwise than exact values
+// would than the hardware's approximation over a whole turn (4e-7) does.
+__device__ __forceinline__ float2 cos_sin_of(uint32_t turns) {
+    const uint32_t quadrant = (turns + 0x20000000u) >> 30;
+    const int32_t rest = static_cast<int32_t>(turns - (quadrant << 30));
+    float s, c;
+    sincospif(static_cast<float>(rest) * 4.656612873077393e-10f, &s, &c);      // 2 / 2^32
+    const float x = (quadrant & 1u) ? s : c, y = (quadrant & 1u) ? c : s;
+    return make_float2(((quadrant + 1u) & 2u) ? -x : x, (quadrant & 2u) ? -y : y);
+}
+
+// Items are (token, group of 4U rows); a warp walks items with the grid's stride and issues the next
+// item's loads before it works on the current one.
 template <bool kRope, int U>
 __global__ void __launch_bounds__(THREADS) store_fp8_kernel(const StoreFp8Args a, int64_t n_tokens, int chunks, int* err) {
     const int lane = threadIdx.x & 31;
     const int j = lane & (ROW_LANES - 1);
     const int sub = lane / ROW_LANES;
-    const int rows = a.num_heads + 2 * a.num_kv_heads;      // num_heads is 0 without q
+    const int hq = kRope ? a.num_heads : 0;                 // 0 without q
+    const int rows = hq + 2 * a.num_kv_heads;
     const int64_t items = n_tokens * chunks;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * (THREADS / 32);
-    for (int64_t it = static_cast<int64_t>(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5); it < items; it += stride) {
-        const int64_t t = it / chunks;
-        const int chunk = static_cast<int>(it - t * chunks);
-        const int slot = __ldg(a.slots + t);
-        const bool in_pool = slot >= 0 && slot < a.num_slots;
-        if (slot >= a.num_slots && chunk == 0 && lane == 0) record_error(err, PKV_DEVERR_SLOT, static_cast<int>(t));
+    int64_t it = static_cast<int64_t>(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5);
+    if (it >= items) return;
+    uint64_t f0 = 0, f1 = 0;                                // this lane's two pairs: 2 lane, 2 lane + 1
+    if (kRope) {
+        f0 = a.turns[2 * lane];
+        f1 = a.turns[2 * lane + 1];
+    }
+    struct Item {
+        int64_t t;
+        int chunk, slot, pos;
         uint4 lo[U], hi[U];
-        const int r0 = chunk * (GROUP * U) + sub;
+    };
+    auto load = [&](int64_t i, Item& x) {
+        x.t = i / chunks;
+        x.chunk = static_cast<int>(i - x.t * chunks);
+        x.slot = __ldg(a.slots + x.t);
+        if (kRope) x.pos = __ldg(a.positions + x.t);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int r = r0 + u * GROUP;
-            lo[u] = hi[u] = make_uint4(0, 0, 0, 0);
-            if (r < rows && (r < a.num_heads || in_pool)) {
+            const int r = x.chunk * (GROUP * U) + u * GROUP + sub;
+            x.lo[u] = x.hi[u] = make_uint4(0, 0, 0, 0);
+            if (r < rows) {                                 // a skipped row is read too: its slot is not known yet
                 const uint16_t* src;
-                if (kRope && r < a.num_heads)
-                    src = a.q + t * a.q_stride + static_cast<int64_t>(r) * kHeadDim;
-                else if (r < a.num_heads + a.num_kv_heads)
-                    src = a.k + t * a.k_stride + static_cast<int64_t>(r - a.num_heads) * kHeadDim;
+                if (kRope && r < hq)
+                    src = a.q + x.t * a.q_stride + static_cast<int64_t>(r) * kHeadDim;
+                else if (r < hq + a.num_kv_heads)
+                    src = a.k + x.t * a.k_stride + static_cast<int64_t>(r - hq) * kHeadDim;
                 else
-                    src = a.v + t * a.v_stride + static_cast<int64_t>(r - a.num_heads - a.num_kv_heads) * kHeadDim;
-                lo[u] = __ldcs(reinterpret_cast<const uint4*>(src) + j);
-                hi[u] = __ldcs(reinterpret_cast<const uint4*>(src) + ROW_LANES + j);
+                    src = a.v + x.t * a.v_stride + static_cast<int64_t>(r - hq - a.num_kv_heads) * kHeadDim;
+                x.lo[u] = __ldcs(reinterpret_cast<const uint4*>(src) + j);
+                x.hi[u] = __ldcs(reinterpret_cast<const uint4*>(src) + ROW_LANES + j);
             }
         }
+    };
+    auto work = [&](const Item& x) {
+        const bool in_pool = x.slot >= 0 && x.slot < a.num_slots;
+        if (x.slot >= a.num_slots && x.chunk == 0 && lane == 0) record_error(err, PKV_DEVERR_SLOT, static_cast<int>(x.t));
         float cs[8], sn[8];
         if (kRope) {
-            const int pos = __ldg(a.positions + t);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint64_t f = a.turns[8 * j + e];
-                __sincosf(reduced_angle(pos, static_cast<uint32_t>(f), static_cast<uint32_t>(f >> 32)), &sn[e], &cs[e]);
-            }
-        }
-        const int64_t blk = in_pool ? slot / a.block_size : 0;
-        const int off = in_pool ? slot - static_cast<int>(blk) * a.block_size : 0;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int r = r0 + u * GROUP;
-            const bool is_q = r < a.num_heads;
-            const bool is_k = !is_q && r < a.num_heads + a.num_kv_heads;
-            const uint32_t wl[4] = {lo[u].x, lo[u].y, lo[u].z, lo[u].w};
-            const uint32_t wh[4] = {hi[u].x, hi[u].y, hi[u].z, hi[u].w};
-            float x[8], y[8];
+            // two pairs per lane; lane j's eight come from lanes 4j .. 4j + 3
+            const float2 p0 = cos_sin_of(turns_of(x.pos, static_cast<uint32_t>(f0), static_cast<uint32_t>(f0 >> 32)));
+            const float2 p1 = cos_sin_of(turns_of(x.pos, static_cast<uint32_t>(f1), static_cast<uint32_t>(f1 >> 32)));
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                x[2 * e] = bf16_lo(wl[e]);
-                x[2 * e + 1] = bf16_hi(wl[e]);
-                y[2 * e] = bf16_lo(wh[e]);
-                y[2 * e + 1] = bf16_hi(wh[e]);
+                cs[2 * e] = __shfl_sync(0xffffffffu, p0.x, 4 * j + e);
+                sn[2 * e] = __shfl_sync(0xffffffffu, p0.y, 4 * j + e);
+                cs[2 * e + 1] = __shfl_sync(0xffffffffu, p1.x, 4 * j + e);
+                sn[2 * e + 1] = __shfl_sync(0xffffffffu, p1.y, 4 * j + e);
+            }
+        }
+        const int blk = in_pool ? x.slot / a.block_size : 0;
+        const int off = in_pool ? x.slot - blk * a.block_size : 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = x.chunk * (GROUP * U) + u * GROUP + sub;
+            const bool is_q = r < hq;
+            const bool is_k = !is_q && r < hq + a.num_kv_heads;
+            const uint32_t wl[4] = {x.lo[u].x, x.lo[u].y, x.lo[u].z, x.lo[u].w};
+            const uint32_t wh[4] = {x.hi[u].x, x.hi[u].y, x.hi[u].z, x.hi[u].w};
+            float y[8], z[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                y[2 * e] = bf16_lo(wl[e]);
+                y[2 * e + 1] = bf16_hi(wl[e]);
+                z[2 * e] = bf16_lo(wh[e]);
+                z[2 * e + 1] = bf16_hi(wh[e]);
             }
             if (kRope && (is_q || is_k)) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float p = x[e], q = y[e];
-                    x[e] = fmaf(p, cs[e], -q * sn[e]);
-                    y[e] = fmaf(q, cs[e], p * sn[e]);
+                    const float p = y[e], q = z[e];
+                    y[e] = fmaf(p, cs[e], -q * sn[e]);
+                    z[e] = fmaf(q, cs[e], p * sn[e]);
                 }
+            }
+            if (kRope && is_q) {
+                uint4* dst = reinterpret_cast<uint4*>(a.q_out + x.t * a.q_out_stride + static_cast<int64_t>(r) * kHeadDim);
+                dst[j] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                                    pack_bf16x2(y[6], y[7]));
+                dst[ROW_LANES + j] = make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]),
+                                                pack_bf16x2(z[4], z[5]), pack_bf16x2(z[6], z[7]));
             }
             uint32_t amax = 0;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                amax = max(amax, __float_as_uint(x[e]) & 0x7fffffffu);
                 amax = max(amax, __float_as_uint(y[e]) & 0x7fffffffu);
+                amax = max(amax, __float_as_uint(z[e]) & 0x7fffffffu);
             }
 #pragma unroll
             for (int d = 1; d < ROW_LANES; d <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-            if (kRope && is_q) {
-                uint4* dst = reinterpret_cast<uint4*>(a.q_out + t * a.q_out_stride + static_cast<int64_t>(r) * kHeadDim);
-                dst[j] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                                    pack_bf16x2(x[6], x[7]));
-                dst[ROW_LANES + j] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
-                                                pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
-            } else if (r < rows && in_pool) {
-                const int h = r - a.num_heads - (is_k ? 0 : a.num_kv_heads);
+            if (!is_q && r < rows && in_pool) {
+                const int h = r - hq - (is_k ? 0 : a.num_kv_heads);
                 const int byte = scale_byte(amax);
                 uint2 c0 = make_uint2(0, 0), c1 = c0;
                 if (byte != 255) {
-                    // 2^-(byte - 127), a normal number: the byte is at most 248
+                    // 2^-(byte - 127), a normal number: the byte is at most 247
                     const float inv = __uint_as_float(static_cast<uint32_t>(254 - byte) << 23);
-                    c0 = to_codes(x, inv);
-                    c1 = to_codes(y, inv);
+                    c0 = to_codes(y, inv);
+                    c1 = to_codes(z, inv);
                 }
                 uint8_t* dst = (is_k ? a.k_cache : a.v_cache) +
-                               (static_cast<int64_t>(slot) * a.num_kv_heads + h) * kHeadDim;
+                               (static_cast<int64_t>(x.slot) * a.num_kv_heads + h) * kHeadDim;
                 *reinterpret_cast<uint2*>(dst + 8 * j) = c0;
                 *reinterpret_cast<uint2*>(dst + 64 + 8 * j) = c1;
                 if (j == 0)
-                    (is_k ? a.k_scale : a.v_scale)[(blk * a.num_kv_heads + h) * a.block_size + off] =
+                    (is_k ? a.k_scale : a.v_scale)[(static_cast<int64_t>(blk) * a.num_kv_heads + h) * a.block_size + off] =
                         static_cast<uint8_t>(byte);
             }
         }
+    };
+    Item cur, next;
+    load(it, cur);
+    for (; it + stride < items; it += stride) {
+        load(it + stride, next);
+        work(cur);
+        cur = next;
     }
+    work(cur);
 }
 
 template <bool kRope, int U>
@@ -153,8 +196,8 @@ cudaError_t launch(const StoreFp8Args& a, int64_t n_tokens, int* err, cudaStream
     const int rows = a.num_heads + 2 * a.num_kv_heads;
     const int chunks = (rows + GROUP * U - 1) / (GROUP * U);
     const int64_t ctas = (n_tokens * chunks + THREADS / 32 - 1) / (THREADS / 32);
-    store_fp8_kernel<kRope, U><<<static_cast<unsigned>(std::min<int64_t>(ctas, 1 << 20)), THREADS, 0, stream>>>(
-        a, n_tokens, chunks, err);
+    const int64_t resident = static_cast<int64_t>(sm_count()) * CTAS_PER_SM;
+    store_fp8_kernel<kRope, U><<<static_cast<unsigned>(std::min(ctas, resident)), THREADS, 0, stream>>>(a, n_tokens, chunks, err);
     return cudaGetLastError();
 }
 

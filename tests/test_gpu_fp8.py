@@ -205,9 +205,10 @@ def test_rope_store_in_place_and_without_q(pkv):
     here = q.clone()
     assert pkv.pkv_rope_store_kvcache_fp8(here, k, v, pos, slots, *b, 1e4, q_out=here) is here
     assert torch.equal(here, ref)
-    # the same rotation as the bf16 append's
+    # the same rotation as the bf16 append's, to a rounding
     kc = torch.zeros(1, 256, 8, D, dtype=torch.bfloat16, device="cuda")
-    assert torch.equal(ref, pkv.pkv_rope_store_kvcache(q, k, v, pos, slots, kc, torch.zeros_like(kc), 1e4))
+    other = pkv.pkv_rope_store_kvcache(q, k, v, pos, slots, kc, torch.zeros_like(kc), 1e4).double()
+    assert torch.all((ref.double() - other).abs() <= 2.0 ** -7 * other.abs() + 2e-6 * q.double().abs().amax())
 
 
 def test_store_slot_past_the_pool_is_skipped_and_recorded(pkv):
