@@ -19,15 +19,19 @@
 //   pass 1  every thread's maximum and, for top-p, its sum of weights relative to that maximum;
 //           one exchange gives every CTA the row's first token (top_k = 1 ends here) and the sum Z.
 //   top-k   (k at most half the threads, and 1024.)  The k-th largest of the threads' maxima bounds
-//           the k-th logit from below: a 128-bin histogram of the maxima gives the bound, a sweep
-//           collects what reaches it (a little over k tokens) in the first CTA, which sorts them,
-//           cuts them by k, then by p and min-p, and runs the race.
+//           the k-th logit from below: a 128-bin histogram of the maxima gives the bound.  A
+//           thread has kept its two largest quads of logits and the third's maximum, so what
+//           reaches the bound (a little over k tokens) is collected from those, rarely by another
+//           look at a thread's share, in the first CTA, which sorts them, cuts them by k, then by p
+//           and min-p, and runs the race.
 //   top-p   A token lighter than (1 - p) Z / vocab is outside (all of those together weigh less
-//           than 1 - p of Z).  The others are counted into 2048 bins of 1/64 octave of weight.
-//           A bin's weights lie within 1.1% of one another, so the counts bound the running sum
-//           from both sides and leave a few bins where it may reach p Z.  One sweep sums and races
-//           the tokens above those bins and collects the bins' members in the first CTA, which
-//           sorts them, finds the border by their running sum and races what is above it.
+//           than 1 - p of Z).  Each warp lists its quads that hold others (so the work below runs
+//           on full warps), and those are counted into 2048 bins of 1/64 octave of weight.  A bin's
+//           weights lie within 1.1% of one another, so the counts bound the running sum from both
+//           sides and leave a few bins where it may reach p Z (if they hold too many, they are
+//           counted once more, into 2048 bins of their own).  The tokens above those bins are
+//           summed and raced, the bins' members collected in the first CTA, which sorts them, finds
+//           the border by their running sum and races what is above it.
 //   else    (a larger k, or more members than fit: a flat row, thousands of equal logits.)  The
 //           same histogram over every token, and the range of candidates halved, by (logit bits,
 //           column), until it fits; the race then sweeps the slices once more.
@@ -41,7 +45,7 @@
 // ranked again in fp64.
 #include <cooperative_groups.h>
 
-#include <algorithm>
+#include <utility>
 
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
@@ -56,6 +60,8 @@ constexpr int BINS = 2048;
 constexpr int TAIL = BINS - 1;               // the last bin: everything from 2047/64 octaves down
 constexpr int COARSE = 128;                  // bins of the threads' maxima, 16 fine bins each
 constexpr int CAP = 2048;                    // members collected at once
+constexpr int BORDER = 1024;                 // of those, around top-p's border
+constexpr int LISTED = 8192;                 // quads of a CTA's warps' lists
 constexpr int RANK_MAX = 256;                // members sorted by counting
 constexpr int MAX_CLUSTER = 16;
 constexpr int kWideRows = 8;                 // rows that get a wide cluster each (see the launch)
@@ -66,15 +72,19 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr float FIX = 274877906944.f;        // 2^38: a weight of 1 in fixed point
 
 struct Shared {
-    uint32_t hist[BINS];         // this CTA's counts
+    uint32_t hist[BINS];         // this CTA's counts; top-k: every CTA's coarse counts
     uint32_t tot[BINS];          // the cluster's counts
-    uint64_t list[CAP];          // first CTA: members, as composites
+    union {
+        uint64_t list[CAP];      // first CTA: members, as composites
+        uint16_t quads[LISTED];  // top-p and races: each warp's quads, from the slice's first
+    };
+    uint64_t border[BORDER];     // first CTA, top-p: members
     uint64_t sorted[RANK_MAX];
     uint64_t slot[2][MAX_CLUSTER];             // cluster-wide sums, alternating
     uint64_t lo[2][MAX_CLUSTER], hi[2][MAX_CLUSTER];   // cluster-wide ranges, alternating
     uint64_t top[MAX_CLUSTER];   // pass 1: first token and sum of each CTA
     float z[MAX_CLUSTER];
-    uint32_t coarse[MAX_CLUSTER][COARSE];
+    float wz[32];
     float2 win[MAX_CLUSTER];     // race: best and second best key of each CTA
     int2 win_col[MAX_CLUSTER];
     uint64_t threshold;
@@ -87,6 +97,7 @@ struct Shared {
     int first[3];
     uint32_t list_n;
 };
+static_assert(MAX_CLUSTER * COARSE <= BINS, "the coarse counts fit the histogram");
 static_assert(sizeof(Shared) <= 48 * 1024, "no opt-in to more shared memory");
 
 // Order of the tokens as an unsigned number: larger = earlier.  -0 and +0 are one logit.
@@ -172,29 +183,42 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
     const int nquads = (a.vocab + 3) >> 2;
     const int per = (nquads + CLUSTER - 1) / CLUSTER;
     const int q0 = min(nquads, rank * per), q1 = min(nquads, q0 + per);
+    auto clean = [](const float4& v) {
+        return make_float4(fmaxf(v.x, -INFINITY), fmaxf(v.y, -INFINITY), fmaxf(v.z, -INFINITY), fmaxf(v.w, -INFINITY));
+    };
+    // quads below `whole` are one aligned 16-byte load
+    const int whole = args.vec_ok ? a.vocab >> 2 : 0;
+    auto load_whole = [&](int qd) -> float4 { return clean(__ldg(reinterpret_cast<const float4*>(lrow) + qd)); };
     auto load_quad = [&](int qd) -> float4 {
+        if (qd < whole) return load_whole(qd);
         const int col = qd * 4;
         float4 v;
-        if (args.vec_ok && col + 3 < a.vocab) {
-            v = __ldg(reinterpret_cast<const float4*>(lrow + col));
-        } else {
-            v.x = __ldg(lrow + col);
-            v.y = col + 1 < a.vocab ? __ldg(lrow + col + 1) : -INFINITY;
-            v.z = col + 2 < a.vocab ? __ldg(lrow + col + 2) : -INFINITY;
-            v.w = col + 3 < a.vocab ? __ldg(lrow + col + 3) : -INFINITY;
-        }
-        return make_float4(fmaxf(v.x, -INFINITY), fmaxf(v.y, -INFINITY), fmaxf(v.z, -INFINITY), fmaxf(v.w, -INFINITY));
+        v.x = __ldg(lrow + col);
+        v.y = col + 1 < a.vocab ? __ldg(lrow + col + 1) : -INFINITY;
+        v.z = col + 2 < a.vocab ? __ldg(lrow + col + 2) : -INFINITY;
+        v.w = col + 3 < a.vocab ? __ldg(lrow + col + 3) : -INFINITY;
+        return clean(v);
     };
     auto max_of = [](const float4& v) { return fmaxf(fmax3(v.x, v.y, v.z), v.w); };
     // f(quad, its logits) over the slice, LOADS loads in flight per thread
     auto sweep_quads = [&](auto f) {
         int qd = q0 + tid;
-        for (; qd + (LOADS - 1) * THREADS < q1; qd += LOADS * THREADS) {
+        const int end = min(q1, whole);
+        for (; qd + (LOADS - 1) * THREADS < end; qd += LOADS * THREADS) {
             float4 v[LOADS];
 #pragma unroll
-            for (int i = 0; i < LOADS; ++i) v[i] = load_quad(qd + i * THREADS);
+            for (int i = 0; i < LOADS; ++i) v[i] = load_whole(qd + i * THREADS);
 #pragma unroll
             for (int i = 0; i < LOADS; ++i) f(qd + i * THREADS, v[i]);
+        }
+        if (qd < end) {                                   // the rest of the whole quads, together as well
+            float4 v[LOADS];
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) v[i] = load_whole(min(qd + i * THREADS, end - 1));
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i)
+                if (qd + i * THREADS < end) f(qd + i * THREADS, v[i]);
+            qd += ((end - qd + THREADS - 1) / THREADS) * THREADS;
         }
         for (; qd < q1; qd += THREADS) f(qd, load_quad(qd));
     };
@@ -216,6 +240,8 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
     if (tid == 0) sh.list_n = 0u;
     float mx = -INFINITY, zs = 0.f;
     int mx_quad = q0;                                     // the first quad that holds this thread's maximum
+    float m2 = -INFINITY, m3 = -INFINITY;                 // top-k: the second and third largest quads' maxima
+    int m2_quad = q0;
     const bool online = need_p && !fast_k;
     const float l2 = fminf(inv_t * LOG2E, 3.4028235e38f);
     if (online) {
@@ -228,6 +254,16 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
             }
             if (mx > -INFINITY)
                 zs += (ex2_ftz((v.x - mx) * l2) + ex2_ftz((v.y - mx) * l2)) + (ex2_ftz((v.z - mx) * l2) + ex2_ftz((v.w - mx) * l2));
+        });
+    } else if (fast_k) {
+        sweep_quads([&](int qd, const float4& v) {
+            const float m4 = max_of(v);
+            const bool a1 = m4 > mx, a2 = m4 > m2;
+            m3 = a2 ? m2 : fmaxf(m3, m4);
+            m2_quad = a1 ? mx_quad : a2 ? qd : m2_quad;
+            m2 = a1 ? mx : a2 ? m4 : m2;
+            mx_quad = a1 ? qd : mx_quad;
+            mx = a1 ? m4 : mx;
         });
     } else {
         sweep_quads([&](int qd, const float4& v) {
@@ -249,22 +285,22 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) t = max(t, sh.whi[w]);
-        const float m_cta = t ? composite_x(t) : 0.f;
-        uint64_t zf = 0;
+        float z = 0.f;
         if (online) {
-            // infinite maxima end the row below, whatever their sum
-            zf = mx > -INFINITY && m_cta < INFINITY ? fixed_of(zs * ex2_ftz((mx - m_cta) * l2)) : 0ull;
+            // fixed trees of fp32 sums; infinite maxima end the row below, whatever their sum
+            const float m_cta = t ? composite_x(t) : 0.f;
+            z = mx > -INFINITY && m_cta < INFINITY ? zs * ex2_ftz((mx - m_cta) * l2) : 0.f;
 #pragma unroll
-            for (int off = 16; off >= 1; off >>= 1) zf += shfl_xor64(zf, off);
-            if (lane == 0) sh.wred[warp] = zf;
+            for (int off = 16; off >= 1; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
+            if (lane == 0) sh.wz[warp] = z;
             __syncthreads();
-            zf = 0;
+            z = 0.f;
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) zf += sh.wred[w];
+            for (int w = 0; w < WARPS; ++w) z += sh.wz[w];
         }
         if (tid < CLUSTER) {
             *cluster.map_shared_rank(&sh.top[rank], tid) = t;
-            *cluster.map_shared_rank(&sh.slot[0][rank], tid) = zf;
+            *cluster.map_shared_rank(&sh.z[rank], tid) = z;
         }
     }
     cluster.sync();                                       // also publishes the cleared tables
@@ -277,11 +313,11 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
         return;
     }
     if (online) {
-        float z = 0.f;                                    // in units of 2^-38
+        float z = 0.f;
 #pragma unroll
         for (int r = 0; r < CLUSTER; ++r)
-            if (sh.top[r]) z = fmaf(__ull2float_rn(sh.slot[0][r]), ex2_ftz((composite_x(sh.top[r]) - M) * l2), z);
-        Z = __float2ull_rn(z);
+            if (sh.top[r]) z = fmaf(sh.z[r], ex2_ftz((composite_x(sh.top[r]) - M) * l2), z);
+        Z = fixed_of(z);
     }
     // the smallest logit in the race: min-p's limit, and the race's reach
     const float min_x = fmaxf(mp > 0.f ? fmaf(T, logf(mp), M) : -INFINITY, M - RACE_Z * T);
@@ -293,7 +329,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
     };
 
     // ---- cluster-wide reductions; every CTA ends with the same values
-    int phase = 1;
+    int phase = 0;
     auto cluster_sum = [&](uint64_t v) -> uint64_t {
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) v += shfl_xor64(v, off);
@@ -452,6 +488,80 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
         a.out_ids[row] = static_cast<int64_t>(best.c1);
     };
 
+    // ---- each warp's list of its quads that reach x_min; f(quad, its logits) over the warp's list, 32 at a
+    // time.  Order and shares are fixed.  A slice too long for the lists is walked instead.
+    constexpr int PER_WARP = LISTED / WARPS;
+    const int iters = (q1 - q0 + THREADS - 1) / THREADS;  // uniform
+    const bool listable = iters * 32 <= PER_WARP && q1 - q0 <= 65536;
+    int n_quads = 0;
+    float listed_x = -INFINITY;
+    auto list_quads = [&](float x_min) {
+        listed_x = x_min;
+        if (!listable) return;
+        n_quads = 0;
+        uint16_t* mine = sh.quads + warp * PER_WARP;
+        auto put = [&](int at, const float4& v) {         // quad q0 + at; by whole warps
+            const float m = max_of(v);
+            const uint32_t in = __ballot_sync(0xffffffffu, m >= x_min && m > -INFINITY);
+            if ((in >> lane) & 1u) mine[n_quads + __popc(in & ((1u << lane) - 1u))] = static_cast<uint16_t>(at);
+            n_quads += __popc(in);
+        };
+        const float4 none = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        int i0 = 0;
+        for (; q0 + (i0 + LOADS) * THREADS <= min(q1, whole); i0 += LOADS) {
+            float4 v[LOADS];
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) v[i] = load_whole(q0 + (i0 + i) * THREADS + tid);
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) put((i0 + i) * THREADS + tid, v[i]);
+        }
+        for (; i0 < iters; i0 += LOADS) {
+            float4 v[LOADS];
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) {
+                const int qd = q0 + (i0 + i) * THREADS + tid;
+                v[i] = whole > 0 ? load_whole(min(qd, whole - 1)) : none;
+                if (qd >= q1) v[i] = none;
+                else if (qd >= whole) v[i] = load_quad(qd);
+            }
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) put((i0 + i) * THREADS + tid, v[i]);
+        }
+        __syncwarp();
+    };
+    // f is called by whole warps (quad -1 and -inf logits for lanes without one)
+    auto for_quads = [&](auto f) {
+        const float4 none = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (!listable) {
+            for (int i = 0; i < iters; ++i) {
+                const int qd = q0 + i * THREADS + tid;
+                const float4 v = qd < q1 ? load_quad(qd) : none;
+                f(max_of(v) >= listed_x ? qd : -1, v);
+            }
+            return;
+        }
+        const uint16_t* mine = sh.quads + warp * PER_WARP;
+        for (int i0 = 0; i0 < n_quads; i0 += 32 * LOADS) {
+            float4 v[LOADS];
+            int qd[LOADS];
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) {
+                const int at = i0 + i * 32 + lane;
+                qd[i] = q0 + mine[min(at, n_quads - 1)];
+                v[i] = whole > 0 ? load_whole(min(qd[i], whole - 1)) : none;
+                if (at >= n_quads) {
+                    qd[i] = -1;
+                    v[i] = none;
+                } else if (qd[i] >= whole) {
+                    v[i] = load_quad(qd[i]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i)
+                if (i0 + i * 32 < n_quads) f(qd[i], v[i]);
+        }
+    };
+
     // ---- the list in the first CTA
     uint64_t* list0 = cluster.map_shared_rank(sh.list, 0);
     uint32_t* n0 = cluster.map_shared_rank(&sh.list_n, 0);
@@ -460,32 +570,32 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
         if (at < CAP) list0[at] = c;
     };
     // n members sorted, earliest first, by the CTA
-    auto sort_list = [&](int n) {
+    auto sort_list = [&](uint64_t* list, int n) {
         if (n <= RANK_MAX) {
             for (int i = tid; i < n; i += THREADS) {
-                const uint64_t c = sh.list[i];
+                const uint64_t c = list[i];
                 int at = 0;
 #pragma unroll 4
-                for (int j = 0; j < n; ++j) at += sh.list[j] > c ? 1 : 0;
+                for (int j = 0; j < n; ++j) at += list[j] > c ? 1 : 0;
                 sh.sorted[at] = c;
             }
             __syncthreads();
-            for (int i = tid; i < n; i += THREADS) sh.list[i] = sh.sorted[i];
+            for (int i = tid; i < n; i += THREADS) list[i] = sh.sorted[i];
             __syncthreads();
             return;
         }
         int n2 = RANK_MAX;
         while (n2 < n) n2 <<= 1;
-        for (int i = n + tid; i < n2; i += THREADS) sh.list[i] = 0ull;
+        for (int i = n + tid; i < n2; i += THREADS) list[i] = 0ull;
         __syncthreads();
         for (int size = 2; size <= n2; size <<= 1)
             for (int half = size >> 1; half >= 1; half >>= 1) {
                 for (int i = tid; i < (n2 >> 1); i += THREADS) {
                     const int x = (i & ~(half - 1)) * 2 + (i & (half - 1)), y = x + half;
-                    const uint64_t cx = sh.list[x], cy = sh.list[y];
+                    const uint64_t cx = list[x], cy = list[y];
                     if ((x & size) == 0 ? cx < cy : cx > cy) {
-                        sh.list[x] = cy;
-                        sh.list[y] = cx;
+                        list[x] = cy;
+                        list[y] = cx;
                     }
                 }
                 __syncthreads();
@@ -493,10 +603,10 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
     };
     // How many of the first n members of the sorted list have less than `goal` weight before them, `above`
     // in front; *sum: their weight (without `above`).
-    auto kept_by_weight = [&](int n, uint64_t above, uint64_t goal, uint64_t* sum) -> int {
+    auto kept_by_weight = [&](const uint64_t* list, int n, uint64_t above, uint64_t goal, uint64_t* sum) -> int {
         const int each = (n + THREADS - 1) / THREADS, i0 = tid * each, i1 = min(n, i0 + each);
         uint64_t mine = 0;
-        for (int i = i0; i < i1; ++i) mine += fixed_of(weight_of(depth(composite_x(sh.list[i]))));
+        for (int i = i0; i < i1; ++i) mine += fixed_of(weight_of(depth(composite_x(list[i]))));
         uint64_t s = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -511,7 +621,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
         int count = 0;
         uint64_t part = 0;
         for (int i = i0; i < i1; ++i) {
-            const uint64_t w = fixed_of(weight_of(depth(composite_x(sh.list[i]))));
+            const uint64_t w = fixed_of(weight_of(depth(composite_x(list[i]))));
             if (before < goal) {
                 ++count;
                 part += w;
@@ -533,9 +643,9 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
     };
     // p z, at least the smallest weight (the first token is always kept); p 2^63 is exact
     auto goal_of = [&](uint64_t z) { return max(__umul64hi(z, __float2ull_rz(p * 9223372036854775808.f)) << 1, static_cast<unsigned long long>(1)); };
-    auto race_list = [&](int n) {
+    auto race_list = [&](const uint64_t* list, int n) {
         for (int i = tid; i < n; i += THREADS) {
-            const uint64_t c = sh.list[i];
+            const uint64_t c = list[i];
             if (composite_x(c) < min_x) break;
             best.add(key32(composite_x(c), noise_of(composite_col(c))), composite_col(c));
         }
@@ -548,12 +658,12 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
         if (tid < COARSE) {
             const uint32_t cnt = sh.tot[tid];
 #pragma unroll
-            for (int r = 0; r < CLUSTER; ++r) *cluster.map_shared_rank(&sh.coarse[rank][tid], r) = cnt;
+            for (int r = 0; r < CLUSTER; ++r) *cluster.map_shared_rank(&sh.hist[rank * COARSE + tid], r) = cnt;
         }
         cluster.sync();
         float2 mine = make_float2(0.f, 0.f);
         if (tid < COARSE)
-            for (int r = 0; r < CLUSTER; ++r) mine.x += static_cast<float>(sh.coarse[r][tid]);
+            for (int r = 0; r < CLUSTER; ++r) mine.x += static_cast<float>(sh.hist[r * COARSE + tid]);
         if (tid == 0) sh.first[0] = COARSE;
         const float2 run = scan2(mine);
         if (tid < COARSE && run.x < static_cast<float>(k) && run.x + mine.x >= static_cast<float>(k)) sh.first[0] = tid;
@@ -563,29 +673,47 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
         // Collected by their bins, exactly; a row with fewer than k maxima above -inf, or with the k-th in the
         // last bins, collects everything it has (which fits if the vocabulary does).
         if (last_bin < BINS || a.vocab <= CAP) {
-            sweep_from(last_bin < BINS ? x_at_end_of(last_bin) : -INFINITY, [&](int col, float x) {
-                if (last_bin == BINS || bin_of(depth(x)) <= last_bin) collect(composite(x, col));
-            });
+            const float x_end = last_bin < BINS ? x_at_end_of(last_bin) : -INFINITY;
+            auto collect_quad = [&](int qd, const float4& v) {
+                const float l[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (l[e] > -INFINITY && (last_bin == BINS || bin_of(depth(l[e])) <= last_bin)) collect(composite(l[e], 4 * qd + e));
+            };
+            const bool two = m2 >= x_end && m2 > -INFINITY;
+            if (mx >= x_end && mx > -INFINITY) {
+                const float4 v1 = load_quad(mx_quad);
+                const float4 v2 = load_quad(two ? m2_quad : mx_quad);
+                collect_quad(mx_quad, v1);
+                if (two) collect_quad(m2_quad, v2);
+            }
+            if (m3 >= x_end && m3 > -INFINITY)            // a third quad: this thread's share again
+                sweep_quads([&](int qd, const float4& v) {
+                    if (qd != mx_quad && qd != m2_quad && max_of(v) >= x_end) collect_quad(qd, v);
+                });
             cluster.sync();
             const int n = static_cast<int>(*n0);
             if (n <= CAP) {
-                if (rank != 0) { cluster.sync(); return; }            // the first CTA's counter has been read
-                cluster.sync();
-                sort_list(n);
+                if (rank != 0) return;
+                auto read = cluster.barrier_arrive();     // the others leave once they have read the counter
+                sort_list(sh.list, n);
                 int kept = min(k, n);
                 if (need_p) {
                     uint64_t sum;
-                    kept_by_weight(kept, 0, ~0ull, &sum);
-                    kept = kept_by_weight(kept, 0, goal_of(sum), &sum);
+                    kept_by_weight(sh.list, kept, 0, ~0ull, &sum);
+                    kept = kept_by_weight(sh.list, kept, 0, goal_of(sum), &sum);
                 }
-                race_list(kept);
+                race_list(sh.list, kept);
                 block_best();
                 if (tid == 0) write_winner();
+                cluster.barrier_wait(std::move(read));
                 return;
             }
             cluster.sync();
             if (rank == 0 && tid == 0) sh.list_n = 0u;
         }
+        for (int b = tid; b < BINS; b += THREADS) sh.hist[b] = 0u;
+        cluster.sync();
     }
 
     // ---- thresholds by histogram
@@ -644,11 +772,11 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
             cluster.sync();
         }
         if (rank == 0) {
-            sort_list(static_cast<int>(n));
+            sort_list(sh.list, static_cast<int>(n));
             uint64_t sum = 0;
             int kept = static_cast<int>(min(goal, static_cast<uint64_t>(n)));
-            if (by_weight) kept = kept_by_weight(static_cast<int>(n), above, goal, &sum);
-            else if (weigh) kept_by_weight(kept, 0, ~0ull, &sum);
+            if (by_weight) kept = kept_by_weight(sh.list, static_cast<int>(n), above, goal, &sum);
+            else if (weigh) kept_by_weight(sh.list, kept, 0, ~0ull, &sum);
             if (tid < CLUSTER) {
                 // none kept: just above the range
                 *cluster.map_shared_rank(&sh.threshold, tid) = kept > 0 ? sh.list[kept - 1] : n > 0 ? sh.list[0] + 1 : cmax + 1;
@@ -707,9 +835,14 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
             const float z_f = static_cast<float>(Z) * (1.f / FIX);
             const float limit = (log2f(static_cast<float>(a.vocab)) - log2f((1.f - p) * z_f)) * BINS_PER_OCTAVE * 1.00001f + 2.f;
             end = limit < static_cast<float>(TAIL) ? max(1, static_cast<int>(limit)) : TAIL;
-            sweep_from(x_at_end_of(end), [&](int, float x) {
-                const int b = bin_of(depth(x));
-                if (b < end) atomicAdd(&sh.hist[b], 1u);
+            list_quads(x_at_end_of(end));
+            for_quads([&](int, const float4& v) {
+                const float l[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int b = bin_of(depth(l[e]));
+                    if (b < end) atomicAdd(&sh.hist[b], 1u);
+                }
             });
             cluster_hist();
         }
@@ -717,81 +850,124 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
             const uint64_t goal = goal_of(Z);
             const float goal_f = static_cast<float>(goal) * (1.f / FIX);
             auto kept_in = [&](int b) { return b < k_bin ? sh.tot[b] : b == k_bin ? k_left : 0u; };   // after top-k
-            // bounds of the running sum at the end of each bin; thread t holds bins BINS_PER_THREAD t ...
-            float up[BINS_PER_THREAD], dn[BINS_PER_THREAD];
-            float2 mine = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int i = 0; i < BINS_PER_THREAD; ++i) {
-                const int b = tid * BINS_PER_THREAD + i;
-                const float cnt = static_cast<float>(kept_in(b));
-                up[i] = cnt * weight_of(static_cast<float>(b));
-                dn[i] = b == TAIL ? 0.f : cnt * weight_of(static_cast<float>(b + 1));
-                mine.x += up[i];
-                mine.y += dn[i];
-            }
-            float2 run = scan2(mine);
-            if (tid == 0) sh.first[0] = sh.first[1] = TAIL;
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < BINS_PER_THREAD; ++i) {
-                run.x += up[i];
-                run.y += dn[i];
-                if (run.x >= goal_f * (1.f - 1e-4f)) atomicMin(&sh.first[0], tid * BINS_PER_THREAD + i);
-                if (run.y >= goal_f * (1.f + 1e-4f)) atomicMin(&sh.first[1], tid * BINS_PER_THREAD + i);
-            }
-            __syncthreads();
-            const int b_lo = sh.first[0], b_hi = min(max(b_lo, sh.first[1]), end - 1);
+            // The bins [b_lo, b_hi] in which the running sum may reach what is left of the goal, from counts(b) and
+            // the largest and smallest weight of a bin; thread t holds bins BINS_PER_THREAD t ...; and their members.
+            int b_lo = 0, b_hi = 0;
             uint32_t n_in = 0;
-            for (int b = b_lo + lane; b <= b_hi; b += 32) n_in += kept_in(b);
-            n_in = __reduce_add_sync(0xffffffffu, n_in);
-            __syncthreads();
-            if (b_lo <= b_hi && !need_k && n_in <= CAP) {
-                // the usual case: sum and race what is above the range, collect the range
-                float ws = 0.f, bar = -INFINITY;
-                const float x_end = x_at_end_of(b_hi);
-                const int iters = (q1 - q0 + THREADS - 1) / THREADS;        // uniform
-                for (int it = 0; it < iters; ++it) {
-                    const int qd = q0 + it * THREADS + tid;
-                    bool raced = false;
-                    if (qd < q1) {
-                        const float4 v = load_quad(qd);
-                        if (max_of(v) >= x_end) {
-                            float l[4] = {v.x, v.y, v.z, v.w}, lmax = -INFINITY;
+            auto find = [&](float left, int last, auto counts, auto weight_at) {
+                float up[BINS_PER_THREAD], dn[BINS_PER_THREAD];
+                float2 mine = make_float2(0.f, 0.f);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float d = depth(l[e]);
-                                const int b = bin_of(d);
-                                const bool sure = b < b_lo;
-                                if (sure) ws += weight_of(d);
-                                else if (b <= b_hi) collect(composite(l[e], 4 * qd + e));
-                                if (!(sure && l[e] >= min_x)) l[e] = -INFINITY;
-                                lmax = fmaxf(lmax, l[e]);
-                            }
-                            if (lmax > -INFINITY) {
-                                race_quad(qd, l, lmax, bar);
-                                raced = true;
-                            }
+                for (int i = 0; i < BINS_PER_THREAD; ++i) {
+                    const int b = tid * BINS_PER_THREAD + i;
+                    const float cnt = static_cast<float>(counts(b));
+                    up[i] = cnt * weight_at(b);
+                    dn[i] = cnt * weight_at(b + 1);
+                    mine.x += up[i];
+                    mine.y += dn[i];
+                }
+                float2 run = scan2(mine);
+                if (tid == 0) sh.first[0] = sh.first[1] = BINS;
+                __syncthreads();
+                const float at_up = left * (1.f - 1e-4f), at_dn = left * (1.f + 1e-4f);
+                // one thread sees each sum reach its mark
+                int b_up = BINS, b_dn = BINS;
+                const bool mine_up = run.x < at_up, mine_dn = run.y < at_dn;
+#pragma unroll
+                for (int i = 0; i < BINS_PER_THREAD; ++i) {
+                    run.x += up[i];
+                    run.y += dn[i];
+                    if (run.x >= at_up) b_up = min(b_up, tid * BINS_PER_THREAD + i);
+                    if (run.y >= at_dn) b_dn = min(b_dn, tid * BINS_PER_THREAD + i);
+                }
+                if ((mine_up || tid == 0) && b_up < BINS) atomicMin(&sh.first[0], b_up);
+                if ((mine_dn || tid == 0) && b_dn < BINS) atomicMin(&sh.first[1], b_dn);
+                __syncthreads();
+                b_lo = sh.first[0];
+                b_hi = min(max(b_lo, sh.first[1]), last);
+                n_in = 0;
+                for (int b = b_lo + lane; b <= b_hi; b += 32) n_in += counts(b);
+                n_in = __reduce_add_sync(0xffffffffu, n_in);
+                __syncthreads();
+            };
+            find(goal_f, end - 1, kept_in, [&](int b) { return b > TAIL ? 0.f : weight_of(static_cast<float>(b)); });
+            if (b_lo <= b_hi && !need_k) {
+                // the depths of the range, and what lies above it; a second histogram if the range holds too many
+                float d_lo = static_cast<float>(b_lo), d_hi = static_cast<float>(b_hi + 1), sub = 0.f;
+                const uint32_t n_range = n_in;
+                int s_lo = 0, s_hi = 0;
+                if (n_in > BORDER) {
+                    for (int b = tid; b < BINS; b += THREADS) sh.hist[b] = 0u;
+                    __syncthreads();
+                    sub = static_cast<float>(BINS) / (d_hi - d_lo);
+                    auto sub_of = [&](float d) { return min(static_cast<int>((d - d_lo) * sub), BINS - 1); };
+                    float ws = 0.f;
+                    for_quads([&](int, const float4& v) {
+                        const float l[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float d = depth(l[e]);
+                            if (d < d_lo) ws += weight_of(d);
+                            else if (d < d_hi) atomicAdd(&sh.hist[sub_of(d)], 1u);
                         }
+                    });
+                    const uint64_t above = cluster_sum(fixed_of(ws));
+                    cluster_hist();
+                    const float left = (static_cast<float>(goal) - static_cast<float>(above)) * (1.f / FIX);
+                    // (a sum that rounding puts past the goal already leaves the first members as the range)
+                    find(fmaxf(left, 1e-30f), BINS - 1, [&](int b) { return sh.tot[b]; },
+                         [&](int b) { return weight_of(d_lo + static_cast<float>(b) / sub); });
+                    s_lo = b_lo;
+                    s_hi = b_hi;
+                }
+                if (n_in <= BORDER && b_lo <= b_hi) {
+                    // sum and race what is above the range, collect the range
+                    uint64_t* border0 = cluster.map_shared_rank(sh.border, 0);
+                    float ws = 0.f, bar = -INFINITY;
+                    for_quads([&](int qd, const float4& v) {
+                        float l[4] = {v.x, v.y, v.z, v.w}, lmax = -INFINITY;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float d = depth(l[e]);
+                            bool sure = d < d_lo, in = !sure && d < d_hi;
+                            if (in && sub > 0.f) {
+                                const int b = min(static_cast<int>((d - d_lo) * sub), BINS - 1);
+                                sure = b < s_lo;
+                                in = b >= s_lo && b <= s_hi;
+                            }
+                            if (sure) ws += weight_of(d);
+                            if (in) {
+                                const uint32_t at = atomicAdd(n0, 1u);
+                                if (at < BORDER) border0[at] = composite(l[e], 4 * qd + e);
+                            }
+                            if (!(sure && l[e] >= min_x)) l[e] = -INFINITY;
+                            lmax = fmaxf(lmax, l[e]);
+                        }
+                        if (lmax > -INFINITY) race_quad(qd, l, lmax, bar);
+                        bar = share_best();
+                    });
+                    send_best();
+                    const uint64_t above = cluster_sum(fixed_of(ws));
+                    if (rank != 0) return;
+                    sort_list(sh.border, static_cast<int>(n_in));
+                    uint64_t sum;
+                    const int kept = kept_by_weight(sh.border, static_cast<int>(n_in), above, goal, &sum);
+                    best.clear();
+                    race_list(sh.border, kept);
+                    block_best();
+                    if (tid == 0) {
+                        const Best last = best;
+                        gather_best();
+                        best.add(last.k1, last.c1);
+                        best.add(last.k2, last.c2);
+                        write_winner();
                     }
-                    if (__any_sync(0xffffffffu, raced)) bar = share_best();
+                    return;
                 }
-                send_best();
-                const uint64_t above = cluster_sum(fixed_of(ws));
-                if (rank != 0) return;
-                sort_list(static_cast<int>(n_in));
-                uint64_t sum;
-                const int kept = kept_by_weight(static_cast<int>(n_in), above, goal, &sum);
-                best.clear();
-                race_list(kept);
-                block_best();
-                if (tid == 0) {
-                    const Best mine2 = best;
-                    gather_best();
-                    best.add(mine2.k1, mine2.c1);
-                    best.add(mine2.k2, mine2.c2);
-                    write_winner();
-                }
-                return;
+                // thousands of equal logits at the border: halve it
+                b_lo = static_cast<int>(d_lo);
+                b_hi = static_cast<int>(d_hi) - 1;
+                n_in = n_range;
             }
             if (b_lo <= b_hi) select(true, true, b_lo, b_hi, n_in, goal);
         }
@@ -801,23 +977,17 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
     const float x_keep = keep ? composite_x(keep) : -INFINITY, x_from = fmaxf(min_x, x_keep);
     const uint32_t col_keep = keep ? static_cast<uint32_t>(composite_col(keep)) : 0xffffffffu;    // at x_keep itself: columns up to this
     float bar = -INFINITY;
-    const int iters = (q1 - q0 + THREADS - 1) / THREADS;                    // uniform
-    for (int it = 0; it < iters; ++it) {
-        const int qd = q0 + it * THREADS + tid;
-        if (qd < q1) {
-            const float4 v = load_quad(qd);
-            if (max_of(v) >= x_from) {
-                float l[4] = {v.x, v.y, v.z, v.w}, lmax = -INFINITY;
+    list_quads(x_from);
+    for_quads([&](int qd, const float4& v) {
+        float l[4] = {v.x, v.y, v.z, v.w}, lmax = -INFINITY;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (!(l[e] >= x_from && (l[e] > x_keep || static_cast<uint32_t>(4 * qd + e) <= col_keep))) l[e] = -INFINITY;
-                    lmax = fmaxf(lmax, l[e]);
-                }
-                if (lmax > -INFINITY) race_quad(qd, l, lmax, bar);
-            }
+        for (int e = 0; e < 4; ++e) {
+            if (!(l[e] >= x_from && (l[e] > x_keep || static_cast<uint32_t>(4 * qd + e) <= col_keep))) l[e] = -INFINITY;
+            lmax = fmaxf(lmax, l[e]);
         }
+        if (lmax > -INFINITY) race_quad(qd, l, lmax, bar);
         bar = share_best();
-    }
+    });
     send_best();
     cluster.sync();
     if (rank == 0 && tid == 0) {
