@@ -45,6 +45,7 @@
 // ranked again in fp64.
 #include <cooperative_groups.h>
 
+#include <type_traits>
 #include <utility>
 
 #include "pkv_device.cuh"
@@ -63,6 +64,7 @@ constexpr int CAP = 2048;                    // members collected at once
 constexpr int BORDER = 1024;                 // of those, around top-p's border
 constexpr int LISTED = 8192;                 // quads of a CTA's warps' lists
 constexpr int RANK_MAX = 256;                // members sorted by counting
+constexpr int LOADS = 4;                     // 16-byte loads in flight per thread of a sweep (pass 1, from HBM: LOADS1)
 constexpr int MAX_CLUSTER = 16;
 constexpr int kWideRows = 8;                 // rows that get a wide cluster each (see the launch)
 constexpr float BINS_PER_OCTAVE = 64.f;
@@ -139,13 +141,103 @@ struct Best {
     }
 };
 
+// Steps that several ways share are functions, not inlined: a row runs most of this kernel's code once, so its
+// time is in good part that of fetching it.
+
+// n members sorted, earliest first, by the CTA.
+template <int THREADS>
+__device__ __noinline__ void sort_members(Shared& sh, uint64_t* list, int n) {
+    const int tid = threadIdx.x;
+    if (n <= RANK_MAX) {
+        for (int i = tid; i < n; i += THREADS) {
+            const uint64_t c = list[i];
+            int at = 0;
+#pragma unroll 4
+            for (int j = 0; j < n; ++j) at += list[j] > c ? 1 : 0;
+            sh.sorted[at] = c;
+        }
+        __syncthreads();
+        for (int i = tid; i < n; i += THREADS) list[i] = sh.sorted[i];
+        __syncthreads();
+        return;
+    }
+    int n2 = RANK_MAX;
+    while (n2 < n) n2 <<= 1;
+    for (int i = n + tid; i < n2; i += THREADS) list[i] = 0ull;
+    __syncthreads();
+    for (int size = 2; size <= n2; size <<= 1)
+        for (int half = size >> 1; half >= 1; half >>= 1) {
+            for (int i = tid; i < (n2 >> 1); i += THREADS) {
+                const int x = (i & ~(half - 1)) * 2 + (i & (half - 1)), y = x + half;
+                const uint64_t cx = list[x], cy = list[y];
+                if ((x & size) == 0 ? cx < cy : cx > cy) {
+                    list[x] = cy;
+                    list[y] = cx;
+                }
+            }
+            __syncthreads();
+        }
+}
+
+// How many of the first n members of a sorted list have less than `goal` weight before them, `above` in
+// front, and their weight (without `above`).  By every thread of the CTA.
+struct Kept {
+    uint64_t sum;
+    int count;
+};
+template <int THREADS>
+__device__ __noinline__ Kept kept_members(Shared& sh, const uint64_t* list, int n, uint64_t above, uint64_t goal, float M,
+                                          float per_logit) {
+    constexpr int WARPS = THREADS / 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int each = (n + THREADS - 1) / THREADS, i0 = tid * each, i1 = min(n, i0 + each);
+    auto weight = [&](int i) { return fixed_of(weight_of((M - composite_x(list[i])) * per_logit)); };
+    uint64_t mine = 0;
+    for (int i = i0; i < i1; ++i) mine += weight(i);
+    uint64_t s = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const uint64_t x = static_cast<uint64_t>(__shfl_up_sync(0xffffffffu, static_cast<unsigned long long>(s), off));
+        if (lane >= off) s += x;
+    }
+    __syncthreads();
+    if (lane == 31) sh.wred[warp] = s;
+    __syncthreads();
+    uint64_t before = above + s - mine;
+    for (int w = 0; w < warp; ++w) before += sh.wred[w];
+    Kept r{0, 0};
+    for (int i = i0; i < i1; ++i) {
+        const uint64_t w = weight(i);
+        if (before < goal) {
+            ++r.count;
+            r.sum += w;
+        }
+        before += w;
+    }
+    r.count = __reduce_add_sync(0xffffffffu, r.count);
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) r.sum += shfl_xor64(r.sum, off);
+    __syncthreads();
+    if (lane == 0) { sh.wred[warp] = r.sum; sh.wlo[warp] = static_cast<uint64_t>(r.count); }
+    __syncthreads();
+    r = Kept{0, 0};
+    for (int w = 0; w < WARPS; ++w) { r.count += static_cast<int>(sh.wlo[w]); r.sum += sh.wred[w]; }
+    __syncthreads();
+    return r;
+}
+
+__device__ __noinline__ uint4 noise_quad(uint32_t quad, PhiloxRow row) {
+    const RoundKeys unused = {};
+    return philox_row_at<false>(quad, row, unused);
+}
+
 struct Args {
     SampleFilteredArgs a;
     int vec_ok;
     int* err;
 };
 
-template <int CLUSTER, int THREADS, int LOADS, int MIN_CTAS>
+template <int CLUSTER, int THREADS, int LOADS1, int MIN_CTAS>
 __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_CTAS) sample_filtered_kernel(const Args args) {
     constexpr int WARPS = THREADS / 32;
     constexpr int BINS_PER_THREAD = BINS / THREADS;
@@ -156,8 +248,8 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
     __shared__ Shared sh;
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = static_cast<int>(cluster.block_rank());
-    const int row = blockIdx.y;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int row = blockIdx.y;
 
     const float T = __ldg(a.temperatures + row);
     const int k = a.top_k ? __ldg(a.top_k + row) : 0;
@@ -201,27 +293,29 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
     };
     auto max_of = [](const float4& v) { return fmaxf(fmax3(v.x, v.y, v.z), v.w); };
     // f(quad, its logits) over the slice, LOADS loads in flight per thread
-    auto sweep_quads = [&](auto f) {
+    auto sweep_quads_by = [&](auto in_flight, auto f) {
+        constexpr int N = decltype(in_flight)::value;
         int qd = q0 + tid;
         const int end = min(q1, whole);
-        for (; qd + (LOADS - 1) * THREADS < end; qd += LOADS * THREADS) {
-            float4 v[LOADS];
+        for (; qd + (N - 1) * THREADS < end; qd += N * THREADS) {
+            float4 v[N];
 #pragma unroll
-            for (int i = 0; i < LOADS; ++i) v[i] = load_whole(qd + i * THREADS);
+            for (int i = 0; i < N; ++i) v[i] = load_whole(qd + i * THREADS);
 #pragma unroll
-            for (int i = 0; i < LOADS; ++i) f(qd + i * THREADS, v[i]);
+            for (int i = 0; i < N; ++i) f(qd + i * THREADS, v[i]);
         }
         if (qd < end) {                                   // the rest of the whole quads, together as well
-            float4 v[LOADS];
+            float4 v[N];
 #pragma unroll
-            for (int i = 0; i < LOADS; ++i) v[i] = load_whole(min(qd + i * THREADS, end - 1));
+            for (int i = 0; i < N; ++i) v[i] = load_whole(min(qd + i * THREADS, end - 1));
 #pragma unroll
-            for (int i = 0; i < LOADS; ++i)
+            for (int i = 0; i < N; ++i)
                 if (qd + i * THREADS < end) f(qd + i * THREADS, v[i]);
             qd += ((end - qd + THREADS - 1) / THREADS) * THREADS;
         }
         for (; qd < q1; qd += THREADS) f(qd, load_quad(qd));
     };
+    auto sweep_quads = [&](auto f) { sweep_quads_by(std::integral_constant<int, LOADS>{}, f); };
     // f(column, logit) for every logit of the slice from x_min up, and above -inf
     auto sweep_from = [&](float x_min, auto f) {
         sweep_quads([&](int qd, const float4& v) {
@@ -245,7 +339,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
     const bool online = need_p && !fast_k;
     const float l2 = fminf(inv_t * LOG2E, 3.4028235e38f);
     if (online) {
-        sweep_quads([&](int qd, const float4& v) {
+        sweep_quads_by(std::integral_constant<int, LOADS1>{}, [&](int qd, const float4& v) {
             const float m4 = max_of(v);
             if (m4 > mx) {
                 zs *= ex2_ftz((mx - m4) * l2);            // 0 for the first
@@ -256,7 +350,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
                 zs += (ex2_ftz((v.x - mx) * l2) + ex2_ftz((v.y - mx) * l2)) + (ex2_ftz((v.z - mx) * l2) + ex2_ftz((v.w - mx) * l2));
         });
     } else if (fast_k) {
-        sweep_quads([&](int qd, const float4& v) {
+        sweep_quads_by(std::integral_constant<int, LOADS1>{}, [&](int qd, const float4& v) {
             const float m4 = max_of(v);
             const bool a1 = m4 > mx, a2 = m4 > m2;
             m3 = a2 ? m2 : fmaxf(m3, m4);
@@ -266,7 +360,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
             mx = a1 ? m4 : mx;
         });
     } else {
-        sweep_quads([&](int qd, const float4& v) {
+        sweep_quads_by(std::integral_constant<int, LOADS1>{}, [&](int qd, const float4& v) {
             const float m4 = max_of(v);
             if (m4 > mx) { mx = m4; mx_quad = qd; }
         });
@@ -405,9 +499,8 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
     const uint64_t rr = static_cast<uint64_t>(row) + offset;
     const PhiloxRow prow = philox_row(static_cast<uint32_t>(rr), static_cast<uint32_t>(rr >> 32), static_cast<uint32_t>(seed),
                                       static_cast<uint32_t>(seed >> 32));
-    const RoundKeys unused = {};
     auto noise_of = [&](int col) -> uint32_t {
-        const uint4 w = philox_row_at<false>(static_cast<uint32_t>(col) >> 2, prow, unused);
+        const uint4 w = noise_quad(static_cast<uint32_t>(col) >> 2, prow);
         const int e = col & 3;
         return e == 0 ? w.x : e == 1 ? w.y : e == 2 ? w.z : w.w;
     };
@@ -428,7 +521,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
     // `bar` only if 1 - u < e^(z - bar) (since -ln u >= 1 - u), which spares most keys: the quad's smallest
     // 1 - u against the bound of its largest logit, then each token's; the bound carries a margin of 1e-3.
     auto race_quad = [&](int qd, const float (&l)[4], float lmax, float bar) {
-        const uint4 w = philox_row_at<false>(static_cast<uint32_t>(qd), prow, unused);
+        const uint4 w = noise_quad(static_cast<uint32_t>(qd), prow);
         const float cb = (1e-3f - bar) * LOG2E + 1.4419741739064e-3f;                  // + log2 1.001
         const uint32_t wmax = max(max(w.x, w.y), max(w.z, w.w));
         if (one_minus_u_of(wmax) < ex2_ftz(fmaf(lmax - M, l2, cb))) {
@@ -445,7 +538,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
     };
     // the CTA's two best, in every thread
     auto block_best = [&]() {
-#pragma unroll
+#pragma unroll 1
         for (int off = 16; off >= 1; off >>= 1) {
             const float k1 = __shfl_xor_sync(0xffffffffu, best.k1, off), k2 = __shfl_xor_sync(0xffffffffu, best.k2, off);
             const int c1 = __shfl_xor_sync(0xffffffffu, best.c1, off), c2 = __shfl_xor_sync(0xffffffffu, best.c2, off);
@@ -569,79 +662,12 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
         const uint32_t at = atomicAdd(n0, 1u);
         if (at < CAP) list0[at] = c;
     };
-    // n members sorted, earliest first, by the CTA
-    auto sort_list = [&](uint64_t* list, int n) {
-        if (n <= RANK_MAX) {
-            for (int i = tid; i < n; i += THREADS) {
-                const uint64_t c = list[i];
-                int at = 0;
-#pragma unroll 4
-                for (int j = 0; j < n; ++j) at += list[j] > c ? 1 : 0;
-                sh.sorted[at] = c;
-            }
-            __syncthreads();
-            for (int i = tid; i < n; i += THREADS) list[i] = sh.sorted[i];
-            __syncthreads();
-            return;
-        }
-        int n2 = RANK_MAX;
-        while (n2 < n) n2 <<= 1;
-        for (int i = n + tid; i < n2; i += THREADS) list[i] = 0ull;
-        __syncthreads();
-        for (int size = 2; size <= n2; size <<= 1)
-            for (int half = size >> 1; half >= 1; half >>= 1) {
-                for (int i = tid; i < (n2 >> 1); i += THREADS) {
-                    const int x = (i & ~(half - 1)) * 2 + (i & (half - 1)), y = x + half;
-                    const uint64_t cx = list[x], cy = list[y];
-                    if ((x & size) == 0 ? cx < cy : cx > cy) {
-                        list[x] = cy;
-                        list[y] = cx;
-                    }
-                }
-                __syncthreads();
-            }
-    };
-    // How many of the first n members of the sorted list have less than `goal` weight before them, `above`
-    // in front; *sum: their weight (without `above`).
+    auto sort_list = [&](uint64_t* list, int n) { sort_members<THREADS>(sh, list, n); };
     auto kept_by_weight = [&](const uint64_t* list, int n, uint64_t above, uint64_t goal, uint64_t* sum) -> int {
-        const int each = (n + THREADS - 1) / THREADS, i0 = tid * each, i1 = min(n, i0 + each);
-        uint64_t mine = 0;
-        for (int i = i0; i < i1; ++i) mine += fixed_of(weight_of(depth(composite_x(list[i]))));
-        uint64_t s = mine;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const uint64_t x = static_cast<uint64_t>(__shfl_up_sync(0xffffffffu, static_cast<unsigned long long>(s), off));
-            if (lane >= off) s += x;
-        }
-        __syncthreads();
-        if (lane == 31) sh.wred[warp] = s;
-        __syncthreads();
-        uint64_t before = above + s - mine;
-        for (int w = 0; w < warp; ++w) before += sh.wred[w];
-        int count = 0;
-        uint64_t part = 0;
-        for (int i = i0; i < i1; ++i) {
-            const uint64_t w = fixed_of(weight_of(depth(composite_x(list[i]))));
-            if (before < goal) {
-                ++count;
-                part += w;
-            }
-            before += w;
-        }
-        count = __reduce_add_sync(0xffffffffu, count);
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) part += shfl_xor64(part, off);
-        __syncthreads();
-        if (lane == 0) { sh.wred[warp] = part; sh.wlo[warp] = static_cast<uint64_t>(count); }
-        __syncthreads();
-        count = 0;
-        part = 0;
-        for (int w = 0; w < WARPS; ++w) { count += static_cast<int>(sh.wlo[w]); part += sh.wred[w]; }
-        __syncthreads();
-        *sum = part;
-        return count;
+        const Kept r = kept_members<THREADS>(sh, list, n, above, goal, M, per_logit);
+        *sum = r.sum;
+        return r.count;
     };
-    // p z, at least the smallest weight (the first token is always kept); p 2^63 is exact
     auto goal_of = [&](uint64_t z) { return max(__umul64hi(z, __float2ull_rz(p * 9223372036854775808.f)) << 1, static_cast<unsigned long long>(1)); };
     auto race_list = [&](const uint64_t* list, int n) {
         for (int i = tid; i < n; i += THREADS) {
@@ -1001,7 +1027,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
 pkv_status launch_sample_filtered(const SampleFilteredArgs& a, int* err, cudaStream_t stream) {
     if (a.batch == 0) return PKV_OK;
     if (!setup_once(kSetupSampleFiltered, [] {
-            return cudaFuncSetAttribute(sample_filtered_kernel<16, 512, 4, 1>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+            return cudaFuncSetAttribute(sample_filtered_kernel<16, 512, 5, 1>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
         }))
         return PKV_ERR_CUDA;
     Args args;
@@ -1009,9 +1035,9 @@ pkv_status launch_sample_filtered(const SampleFilteredArgs& a, int* err, cudaStr
     args.vec_ok = (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0 && a.row_stride % 4 == 0;
     args.err = err;
     if (a.batch <= kWideRows)
-        sample_filtered_kernel<16, 512, 4, 1><<<dim3(16, a.batch), 512, 0, stream>>>(args);
+        sample_filtered_kernel<16, 512, 5, 1><<<dim3(16, a.batch), 512, 0, stream>>>(args);
     else
-        sample_filtered_kernel<8, 256, 4, 4><<<dim3(8, a.batch), 256, 0, stream>>>(args);
+        sample_filtered_kernel<8, 256, 8, 4><<<dim3(8, a.batch), 256, 0, stream>>>(args);
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
