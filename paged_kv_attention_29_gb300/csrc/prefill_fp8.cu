@@ -27,11 +27,16 @@ constexpr int D = kHeadDim;
 constexpr int TILE = 128;         // tokens per workspace tile (a prefill KV tile)
 constexpr int PART = 32;          // tokens one CTA decodes at a time
 constexpr int THREADS = 256;
+constexpr int BATCH = 8;
+constexpr int CTAS_PER_SM = 3;
 
 struct DecodeTilesParams {
-    const uint8_t* codes[2];      // K, V
-    const uint8_t* scale[2];
-    uint16_t* tiles[2];           // [num_tiles][TILE][num_kv_heads][D] bf16
+    const uint8_t* k_codes;
+    const uint8_t* v_codes;
+    const uint8_t* k_scale;
+    const uint8_t* v_scale;
+    uint16_t* k_tiles;            // [num_tiles][TILE][num_kv_heads][D] bf16
+    uint16_t* v_tiles;
     const int32_t* cu_k;
     const int32_t* block_tables;
     int32_t* tile_tables;         // [num_seqs][max_tiles]
@@ -63,7 +68,10 @@ __device__ __forceinline__ uint2 bf16_of_codes(uint32_t w, float f) {
     return make_uint2(pack_bf16x2(lo.x * f, lo.y * f), pack_bf16x2(hi.x * f, hi.y * f));
 }
 
+// Started beside the plan (which it does not read) by programmatic launch; it ends after the plan has, so
+// the attention kernel, which waits for this one, finds both done.
 __global__ void __launch_bounds__(THREADS) decode_tiles_kernel(const DecodeTilesParams p) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x;
     // the tables the attention kernel walks: tile j of sequence s
     const int64_t entries = static_cast<int64_t>(p.num_seqs) * p.max_tiles;
@@ -73,12 +81,11 @@ __global__ void __launch_bounds__(THREADS) decode_tiles_kernel(const DecodeTiles
         if (kl < 0 && j == 0) record_error(p.err, PKV_DEVERR_SEQLENS, s);
         p.tile_tables[i] = j * TILE < kl ? static_cast<int32_t>(first_tile(p.cu_k, s) + j) : -1;
     }
-    const int64_t items = p.num_tiles * (TILE / PART) * 2;
-    const int vecs = PART * p.num_kv_heads * (D / 16);        // 16 codes each
+    const int64_t items = p.num_tiles * (TILE / PART);
+    const int row_vecs = p.num_kv_heads * (D / 8);            // 8 codes each (a warp stores 512 bytes in a row): a token's
     for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-        const int which = static_cast<int>(it & 1);
-        const int64_t tile = (it >> 1) / (TILE / PART);
-        const int part = static_cast<int>((it >> 1) - tile * (TILE / PART));
+        const int64_t tile = it / (TILE / PART);
+        const int part = static_cast<int>(it - tile * (TILE / PART));
         int lo = 0, hi = p.num_seqs;                          // the last sequence whose first tile is not behind
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -93,22 +100,40 @@ __global__ void __launch_bounds__(THREADS) decode_tiles_kernel(const DecodeTiles
         const int phys = __ldg(p.block_tables + static_cast<int64_t>(lo) * p.max_blocks + blk);
         const bool known = phys >= 0 && phys < p.num_blocks;
         if (!known && tid == 0) record_error(p.err, PKV_DEVERR_BLOCK_ID, lo);
-        const int64_t src_row = (static_cast<int64_t>(known ? phys : 0) * p.block_size + off0) * p.num_kv_heads;
-        const uint4* src = reinterpret_cast<const uint4*>(p.codes[which] + src_row * D);
-        uint4* dst = reinterpret_cast<uint4*>(p.tiles[which] + (tile * TILE + part * PART) * p.num_kv_heads * D);
-        const uint8_t* scale = p.scale[which] + static_cast<int64_t>(known ? phys : 0) * p.num_kv_heads * p.block_size + off0;
-        for (int v = tid; v < vecs; v += THREADS) {
-            const int row = v / (D / 16);
-            const int tok = row / p.num_kv_heads, h = row - tok * p.num_kv_heads;
-            if (tok >= n) break;
-            const uint32_t byte = __ldg(scale + static_cast<int64_t>(h) * p.block_size + tok);
-            const float f = !known ? 0.f : e8m0_value(byte);
-            const uint4 w = known ? __ldcs(src + v) : make_uint4(0, 0, 0, 0);
-            const uint2 a = bf16_of_codes(w.x, f), b = bf16_of_codes(w.y, f), c = bf16_of_codes(w.z, f), d = bf16_of_codes(w.w, f);
-            dst[2 * v] = make_uint4(a.x, a.y, b.x, b.y);
-            dst[2 * v + 1] = make_uint4(c.x, c.y, d.x, d.y);
+        const int64_t block = known ? phys : 0;
+        const int64_t src0 = (block * p.block_size + off0) * row_vecs;
+        const int64_t dst0 = (tile * TILE + part * PART) * row_vecs;
+        const int64_t scale0 = block * p.num_kv_heads * p.block_size + off0;
+        const int vecs = n * row_vecs;
+        // K and V of BATCH vectors at a time, loads first
+        for (int v0 = tid; v0 < vecs; v0 += BATCH * THREADS) {
+            uint2 w[2][BATCH];
+            float f[2][BATCH];
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                const int v = min(v0 + i * THREADS, vecs - 1);
+                const int tok = v / row_vecs, h = (v - tok * row_vecs) / (D / 8);
+                const int64_t at = scale0 + static_cast<int64_t>(h) * p.block_size + tok;
+                w[0][i] = __ldcs(reinterpret_cast<const uint2*>(p.k_codes) + src0 + v);
+                w[1][i] = __ldcs(reinterpret_cast<const uint2*>(p.v_codes) + src0 + v);
+                f[0][i] = e8m0_value(__ldg(p.k_scale + at));
+                f[1][i] = e8m0_value(__ldg(p.v_scale + at));
+            }
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                const int v = v0 + i * THREADS;
+                if (v >= vecs) break;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint2 c = known ? w[x][i] : make_uint2(0, 0);
+                    const float g = known ? f[x][i] : 0.f;
+                    const uint2 a = bf16_of_codes(c.x, g), b = bf16_of_codes(c.y, g);
+                    (reinterpret_cast<uint4*>(x ? p.v_tiles : p.k_tiles) + dst0)[v] = make_uint4(a.x, a.y, b.x, b.y);
+                }
+            }
         }
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 constexpr size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -140,12 +165,12 @@ pkv_status launch_prefill_fp8(const PrefillFp8Args& a, int* err, cudaStream_t st
     uint8_t* k_tiles = ws + align256(plan_bytes) + align256(static_cast<size_t>(a.num_seqs) * max_tiles * 4);
 
     DecodeTilesParams p;
-    p.codes[0] = a.k_cache;
-    p.codes[1] = a.v_cache;
-    p.scale[0] = a.k_scale;
-    p.scale[1] = a.v_scale;
-    p.tiles[0] = reinterpret_cast<uint16_t*>(k_tiles);
-    p.tiles[1] = reinterpret_cast<uint16_t*>(k_tiles + align256(pool));
+    p.k_codes = a.k_cache;
+    p.v_codes = a.v_cache;
+    p.k_scale = a.k_scale;
+    p.v_scale = a.v_scale;
+    p.k_tiles = reinterpret_cast<uint16_t*>(k_tiles);
+    p.v_tiles = reinterpret_cast<uint16_t*>(k_tiles + align256(pool));
     p.cu_k = a.cu_k;
     p.block_tables = a.block_tables;
     p.tile_tables = tables;
@@ -158,14 +183,10 @@ pkv_status launch_prefill_fp8(const PrefillFp8Args& a, int* err, cudaStream_t st
     p.num_tiles = num_tiles;
     p.total_k = a.total_k;
     p.err = err;
-    const int64_t items = num_tiles * (TILE / PART) * 2;
-    decode_tiles_kernel<<<static_cast<unsigned>(std::min<int64_t>(items, 8LL * sm_count())), THREADS, 0, stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
-
     PrefillArgs f;
     f.q = a.q;
-    f.k_cache = p.tiles[0];
-    f.v_cache = p.tiles[1];
+    f.k_cache = p.k_tiles;
+    f.v_cache = p.v_tiles;
     f.cu_q = a.cu_q;
     f.cu_k = a.cu_k;
     f.block_tables = tables;
@@ -182,7 +203,20 @@ pkv_status launch_prefill_fp8(const PrefillFp8Args& a, int* err, cudaStream_t st
     f.softmax_scale = a.softmax_scale;
     f.workspace = a.workspace;
     f.workspace_bytes = plan_bytes;
-    return launch_prefill(f, err, stream, kPrefillPlanAndRun);
+    // the plan; the tiles beside it; the attention after both
+    pkv_status st = launch_prefill(f, err, stream, kPrefillPlanOnly);
+    if (st != PKV_OK) return st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(num_tiles * (TILE / PART), static_cast<int64_t>(CTAS_PER_SM) * sm_count())));
+    cfg.blockDim = dim3(THREADS);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, decode_tiles_kernel, p) != cudaSuccess) return PKV_ERR_CUDA;
+    return launch_prefill(f, err, stream, kPrefillRunOnly);
 }
 
 }  // namespace pkv
