@@ -87,15 +87,13 @@ struct Shared {
     uint64_t top[MAX_CLUSTER];   // pass 1: first token and sum of each CTA
     float z[MAX_CLUSTER];
     float wz[32];
-    float2 win[MAX_CLUSTER];     // race: best and second best key of each CTA
-    int2 win_col[MAX_CLUSTER];
+    uint64_t win[MAX_CLUSTER][2];   // race: the two best of each CTA
     uint64_t threshold;
     uint64_t list_sum;
     uint64_t wred[32];           // per warp
     uint64_t wlo[32], whi[32];
     float2 wscan[32];
-    float2 wwin[32];
-    int2 wwin_col[32];
+    uint64_t wwin[32][2];
     int first[3];
     uint32_t list_n;
 };
@@ -125,20 +123,19 @@ __device__ __forceinline__ uint64_t shfl_xor64(uint64_t v, int off) {
     return static_cast<uint64_t>(__shfl_xor_sync(0xffffffffu, static_cast<unsigned long long>(v), off));
 }
 
-// The two best of a race: larger key first, then lower column.
+// The two best of a race, as composites of key and column (larger key first, then lower column); 0: none.
 struct Best {
-    float k1, k2;
-    int c1, c2;                  // -1: none
-    __device__ __forceinline__ void clear() { k1 = k2 = -INFINITY; c1 = c2 = -1; }
-    __device__ __forceinline__ void add(float k, int c) {
-        if (c < 0) return;
-        if (c1 < 0 || k > k1 || (k == k1 && c < c1)) {
-            k2 = k1; c2 = c1;
-            k1 = k; c1 = c;
-        } else if (c2 < 0 || k > k2 || (k == k2 && c < c2)) {
-            k2 = k; c2 = c;
-        }
+    uint64_t b1, b2;
+    __device__ __forceinline__ void clear() { b1 = b2 = 0; }
+    __device__ __forceinline__ void add(uint64_t c) {
+        b2 = max(b2, min(b1, c));
+        b1 = max(b1, c);
     }
+    __device__ __forceinline__ void merge(uint64_t o1, uint64_t o2) {
+        b2 = max(max(b2, o2), min(b1, o1));
+        b1 = max(b1, o1);
+    }
+    __device__ __forceinline__ float key() const { return b1 ? composite_x(b1) : -INFINITY; }
 };
 
 // Steps that several ways share are functions, not inlined: a row runs most of this kernel's code once, so its
@@ -528,57 +525,51 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
             const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (one_minus_u_of(ws[e]) < ex2_ftz(fmaf(l[e] - M, l2, cb))) best.add(key32(l[e], ws[e]), 4 * qd + e);
+                if (one_minus_u_of(ws[e]) < ex2_ftz(fmaf(l[e] - M, l2, cb))) best.add(composite(key32(l[e], ws[e]), 4 * qd + e));
         }
     };
     auto share_best = [&]() -> float {                    // the warp's best key so far
         float b;
-        asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(b) : "f"(best.k1));
+        asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(b) : "f"(best.key()));
         return b;
     };
-    // the CTA's two best, in every thread
+    // the CTA's two best, in the lanes of its first warp
     auto block_best = [&]() {
-#pragma unroll 1
-        for (int off = 16; off >= 1; off >>= 1) {
-            const float k1 = __shfl_xor_sync(0xffffffffu, best.k1, off), k2 = __shfl_xor_sync(0xffffffffu, best.k2, off);
-            const int c1 = __shfl_xor_sync(0xffffffffu, best.c1, off), c2 = __shfl_xor_sync(0xffffffffu, best.c2, off);
-            best.add(k1, c1);
-            best.add(k2, c2);
-        }
-        if (lane == 0) {
-            sh.wwin[warp] = make_float2(best.k1, best.k2);
-            sh.wwin_col[warp] = make_int2(best.c1, best.c2);
-        }
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) best.merge(shfl_xor64(best.b1, off), shfl_xor64(best.b2, off));
+        if (lane == 0) { sh.wwin[warp][0] = best.b1; sh.wwin[warp][1] = best.b2; }
         __syncthreads();
-        best.clear();
-        for (int w = 0; w < WARPS; ++w) {
-            best.add(sh.wwin[w].x, sh.wwin_col[w].x);
-            best.add(sh.wwin[w].y, sh.wwin_col[w].y);
+        if (warp == 0) {
+            best.clear();
+            if (lane < WARPS) best.merge(sh.wwin[lane][0], sh.wwin[lane][1]);
+#pragma unroll
+            for (int off = WARPS / 2; off >= 1; off >>= 1) best.merge(shfl_xor64(best.b1, off), shfl_xor64(best.b2, off));
         }
-        __syncthreads();
     };
     // every CTA's two best to the first CTA (the caller's next barrier completes it)
     auto send_best = [&]() {
         block_best();
         if (tid == 0) {
-            *cluster.map_shared_rank(&sh.win[rank], 0) = make_float2(best.k1, best.k2);
-            *cluster.map_shared_rank(&sh.win_col[rank], 0) = make_int2(best.c1, best.c2);
+            uint64_t* to = cluster.map_shared_rank(&sh.win[rank][0], 0);
+            to[0] = best.b1;
+            to[1] = best.b2;
         }
     };
+    // adds every CTA's two best; by the first warp, the result in its lanes
     auto gather_best = [&]() {
-        best.clear();
-        for (int r = 0; r < CLUSTER; ++r) {
-            best.add(sh.win[r].x, sh.win_col[r].x);
-            best.add(sh.win[r].y, sh.win_col[r].y);
-        }
+        if (lane < CLUSTER) best.merge(sh.win[lane][0], sh.win[lane][1]);
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) best.merge(shfl_xor64(best.b1, off), shfl_xor64(best.b2, off));
     };
     // by one thread
     auto write_winner = [&]() {
-        if (best.c2 >= 0 && best.k1 - best.k2 <= NEAR) {  // too near in fp32
-            const double d1 = key64(best.c1), d2 = key64(best.c2);
-            if (d2 > d1 || (d2 == d1 && best.c2 < best.c1)) best.c1 = best.c2;
+        int c1 = composite_col(best.b1);
+        if (best.b2 && composite_x(best.b1) - composite_x(best.b2) <= NEAR) {   // too near in fp32
+            const int c2 = composite_col(best.b2);
+            const double d1 = key64(c1), d2 = key64(c2);
+            if (d2 > d1 || (d2 == d1 && c2 < c1)) c1 = c2;
         }
-        a.out_ids[row] = static_cast<int64_t>(best.c1);
+        a.out_ids[row] = static_cast<int64_t>(c1);
     };
 
     // ---- each warp's list of its quads that reach x_min; f(quad, its logits) over the warp's list, 32 at a
@@ -673,7 +664,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
         for (int i = tid; i < n; i += THREADS) {
             const uint64_t c = list[i];
             if (composite_x(c) < min_x) break;
-            best.add(key32(composite_x(c), noise_of(composite_col(c))), composite_col(c));
+            best.add(composite(key32(composite_x(c), noise_of(composite_col(c))), composite_col(c)));
         }
     };
 
@@ -981,12 +972,10 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
                     best.clear();
                     race_list(sh.border, kept);
                     block_best();
-                    if (tid == 0) {
-                        const Best last = best;
+                    if (warp == 0) {
+                        if (lane != 0) best.clear();      // the border's best counts once
                         gather_best();
-                        best.add(last.k1, last.c1);
-                        best.add(last.k2, last.c2);
-                        write_winner();
+                        if (lane == 0) write_winner();
                     }
                     return;
                 }
@@ -1016,9 +1005,10 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
     });
     send_best();
     cluster.sync();
-    if (rank == 0 && tid == 0) {
+    if (rank == 0 && warp == 0) {
+        best.clear();
         gather_best();
-        write_winner();
+        if (lane == 0) write_winner();
     }
 }
 
