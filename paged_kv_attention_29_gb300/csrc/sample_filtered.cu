@@ -18,10 +18,9 @@
 //
 //   pass 1  every thread's maximum and, for top-p, its sum of weights relative to that maximum;
 //           one exchange gives every CTA the row's first token (top_k = 1 ends here) and the sum Z.
-//   top-k   (k at most half the threads, and 1024.)  The k-th largest of the threads' maxima bounds
-//           the k-th logit from below: a 128-bin histogram of the maxima gives the bound.  A
-//           thread has kept its two largest quads of logits and the third's maximum, so what
-//           reaches the bound (a little over k tokens) is collected from those, rarely by another
+//   top-k   (k at most the threads, and 1024.)  A thread keeps its two largest quads of logits and
+//           the third's maximum.  The k-th largest of those quads' maxima bounds the k-th logit
+//           from below: a 128-bin histogram of the maxima gives the bound, and what reaches the bound (a little over k tokens) is collected from those, rarely by another
 //           look at a thread's share, in the first CTA, which sorts them, cuts them by k, then by p
 //           and min-p, and runs the race.
 //   top-p   A token lighter than (1 - p) Z / vocab is outside (all of those together weigh less
@@ -61,12 +60,11 @@ constexpr int BINS = 2048;
 constexpr int TAIL = BINS - 1;               // the last bin: everything from 2047/64 octaves down
 constexpr int COARSE = 128;                  // bins of the threads' maxima, 16 fine bins each
 constexpr int CAP = 2048;                    // members collected at once
-constexpr int BORDER = 1024;                 // of those, around top-p's border
-constexpr int LISTED = 8192;                 // quads of a CTA's warps' lists
+constexpr int BORDER = 512;                  // of those, around top-p's border
+constexpr int LISTED = 10240;                // quads of a CTA's warps' lists
 constexpr int RANK_MAX = 256;                // members sorted by counting
 constexpr int LOADS = 4;                     // 16-byte loads in flight per thread of a sweep (pass 1, from HBM: LOADS1)
 constexpr int MAX_CLUSTER = 16;
-constexpr int kWideRows = 8;                 // rows that get a wide cluster each (see the launch)
 constexpr float BINS_PER_OCTAVE = 64.f;
 constexpr float RACE_Z = 19.6f;              // reach of the race (see above): 28.3 octaves, inside the fine bins
 constexpr float NEAR = 1e-4f;
@@ -239,7 +237,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
     constexpr int WARPS = THREADS / 32;
     constexpr int BINS_PER_THREAD = BINS / THREADS;
     constexpr int BINS_PER_RANK = BINS / CLUSTER;
-    constexpr int FAST_K = CLUSTER * THREADS / 2 < CAP / 2 ? CLUSTER * THREADS / 2 : CAP / 2;
+    constexpr int FAST_K = CLUSTER * THREADS < CAP / 2 ? CLUSTER * THREADS : CAP / 2;
     static_assert(BINS % THREADS == 0 && CLUSTER <= MAX_CLUSTER && WARPS <= 32 && COARSE <= THREADS, "tables fit");
     const SampleFilteredArgs& a = args.a;
     __shared__ Shared sh;
@@ -671,6 +669,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
     // ---- top-k
     if (fast_k) {
         if (mx > -INFINITY) atomicAdd(&sh.tot[bin_of(depth(mx)) / (BINS / COARSE)], 1u);
+        if (m2 > -INFINITY) atomicAdd(&sh.tot[bin_of(depth(m2)) / (BINS / COARSE)], 1u);
         __syncthreads();
         if (tid < COARSE) {
             const uint32_t cnt = sh.tot[tid];
@@ -1012,23 +1011,36 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
     }
 }
 
+template <int CLUSTER, int THREADS, int LOADS1, int MIN_CTAS>
+struct Rows {
+    static constexpr auto kernel = sample_filtered_kernel<CLUSTER, THREADS, LOADS1, MIN_CTAS>;
+    static cudaError_t launch(const Args& args, cudaStream_t stream) {
+        kernel<<<dim3(CLUSTER, args.a.batch), THREADS, 0, stream>>>(args);
+        return cudaGetLastError();
+    }
+};
+using FewRows = Rows<16, 512, 5, 1>;
+using ManyRows = Rows<8, 256, 8, 4>;
+
 }  // namespace
 
 pkv_status launch_sample_filtered(const SampleFilteredArgs& a, int* err, cudaStream_t stream) {
     if (a.batch == 0) return PKV_OK;
     if (!setup_once(kSetupSampleFiltered, [] {
-            return cudaFuncSetAttribute(sample_filtered_kernel<16, 512, 5, 1>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+            return cudaFuncSetAttribute(FewRows::kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
         }))
         return PKV_ERR_CUDA;
     Args args;
     args.a = a;
     args.vec_ok = (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0 && a.row_stride % 4 == 0;
     args.err = err;
-    if (a.batch <= kWideRows)
-        sample_filtered_kernel<16, 512, 5, 1><<<dim3(16, a.batch), 512, 0, stream>>>(args);
-    else
-        sample_filtered_kernel<8, 256, 8, 4><<<dim3(8, a.batch), 256, 0, stream>>>(args);
-    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    // Up to 9 clusters of 16 CTAs run at once; a row on 16 x 512 threads takes about two thirds of the time it
+    // takes on 8 x 256 (top-p, one row of 151,936: 26 and 40 us), and with more rows than that it is throughput
+    // that counts: 8 x 256 at four CTAs to an SM took 111 us for 256 rows, 4 x 256 took 130, five CTAs to an SM 123.
+    constexpr int kWideRows = 8;
+    const cudaError_t e = a.batch <= kWideRows ? FewRows::launch(args, stream)
+                                               : ManyRows::launch(args, stream);
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 }  // namespace pkv

@@ -180,3 +180,19 @@ def test_captured_with_fresh_noise_and_settings(pkv):
         graph.replay()
         assert torch.equal(ids, pkv.pkv_sample_filtered(gx, T, k, p, m, 3, 32 * step))
     check(pkv, x, 0.8, 10, np.float32(0.5), 0.0, seed=3, offset=64)
+
+
+@pytest.mark.parametrize("B,vocab", [(9, 3001), (77, 12007), (160, 30011), (300, 129)])
+def test_batches_of_every_size(pkv, B, vocab):
+    """Few, some and many rows run as clusters of different sizes; every kind of row in each."""
+    k, p, m = (np.array([SETTINGS[i % len(SETTINGS)][j] for i in range(B)]) for j in range(3))
+    T = np.random.default_rng(B).uniform(0.4, 1.3, B)
+    check(pkv, rows(B, vocab, B + 3, 2.5, rounded=B % 2 == 0), T, k, p, m, most_unclear=2)
+
+
+def test_many_rows_of_a_vocabulary_beyond_the_lists(pkv):
+    """Slices too long for the warps' lists of quads are walked instead."""
+    B = 80
+    x = rows(B, 180001, 41, 2.0)
+    k, p = np.where(np.arange(B) % 4 == 0, 30, 0), np.where(np.arange(B) % 4 == 1, 1.0, 0.85)
+    check(pkv, x, 0.9, k, p, 0.0, most_unclear=2)
