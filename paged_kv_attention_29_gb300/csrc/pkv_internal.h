@@ -26,7 +26,8 @@ int sm_count();
 // One-time set-up of kernel attributes, per device.  Runs `setup` with the
 // current device once (thread-safe; a failed set-up is retried on the next
 // call) and returns whether the set-up for `key` has succeeded on this device.
-enum SetupKey { kSetupDecode = 0, kSetupPrefill, kSetupRopeStore, kSetupDecodeFp8, kSetupSampleFiltered, kNumSetupKeys };
+enum SetupKey { kSetupDecode = 0, kSetupPrefill, kSetupRopeStore, kSetupDecodeFp8, kSetupSampleFiltered, kSetupStoreFp8,
+                kSetupStoreFp8Rope, kNumSetupKeys };
 bool setup_once(SetupKey key, bool (*setup)());
 
 // cuTensorMapEncodeTiled through the runtime's driver entry point.

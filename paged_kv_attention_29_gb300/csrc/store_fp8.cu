@@ -60,24 +60,94 @@ __device__ __forceinline__ float2 cos_sin_of(uint32_t turns) {
     return make_float2(((quadrant + 1u) & 2u) ? -x : x, (quadrant & 2u) ? -y : y);
 }
 
-// Items are (token, group of 4U rows); a warp walks items with the grid's stride and issues the next
+// Eight lanes' share of a row: its loads' bits, rotated (q, k), rounded and written.  r >= rows: nothing.
+// The warp calls it together.
+template <bool kRope>
+__device__ __forceinline__ void put_row(const StoreFp8Args& a, int64_t t, int slot, int blk, int off, int r, int j, const uint4& lo,
+                                        const uint4& hi, const float (&cs)[8], const float (&sn)[8]) {
+    const int hq = kRope ? a.num_heads : 0;                 // 0 without q
+    const bool in_pool = slot >= 0 && slot < a.num_slots;
+    const bool is_q = r < hq;
+    const bool is_k = !is_q && r < hq + a.num_kv_heads;
+    const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w};
+    const uint32_t wh[4] = {hi.x, hi.y, hi.z, hi.w};
+    float y[8], z[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        y[2 * e] = bf16_lo(wl[e]);
+        y[2 * e + 1] = bf16_hi(wl[e]);
+        z[2 * e] = bf16_lo(wh[e]);
+        z[2 * e + 1] = bf16_hi(wh[e]);
+    }
+    if (kRope && (is_q || is_k)) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float p = y[e], q = z[e];
+            y[e] = fmaf(p, cs[e], -q * sn[e]);
+            z[e] = fmaf(q, cs[e], p * sn[e]);
+        }
+    }
+    if (kRope && is_q) {
+        uint4* dst = reinterpret_cast<uint4*>(a.q_out + t * a.q_out_stride + static_cast<int64_t>(r) * kHeadDim);
+        dst[j] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+        dst[ROW_LANES + j] = make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]), pack_bf16x2(z[4], z[5]),
+                                        pack_bf16x2(z[6], z[7]));
+    }
+    uint32_t amax = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        amax = max(amax, __float_as_uint(y[e]) & 0x7fffffffu);
+        amax = max(amax, __float_as_uint(z[e]) & 0x7fffffffu);
+    }
+#pragma unroll
+    for (int d = 1; d < ROW_LANES; d <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+    if (!is_q && r < hq + 2 * a.num_kv_heads && in_pool) {
+        const int h = r - hq - (is_k ? 0 : a.num_kv_heads);
+        const int byte = scale_byte(amax);
+        uint2 c0 = make_uint2(0, 0), c1 = c0;
+        if (byte != 255) {
+            // 2^-(byte - 127), a normal number: the byte is at most 247
+            const float inv = __uint_as_float(static_cast<uint32_t>(254 - byte) << 23);
+            c0 = to_codes(y, inv);
+            c1 = to_codes(z, inv);
+        }
+        uint8_t* dst = (is_k ? a.k_cache : a.v_cache) + (static_cast<int64_t>(slot) * a.num_kv_heads + h) * kHeadDim;
+        *reinterpret_cast<uint2*>(dst + 8 * j) = c0;
+        *reinterpret_cast<uint2*>(dst + 64 + 8 * j) = c1;
+        if (j == 0)
+            (is_k ? a.k_scale : a.v_scale)[(static_cast<int64_t>(blk) * a.num_kv_heads + h) * a.block_size + off] =
+                static_cast<uint8_t>(byte);
+    }
+}
+
+// (cos, sin) of this lane's eight pairs 8j .. 8j + 7 at a position: two pairs per lane, the lane's own
+// fractions of a turn f0 and f1 (pairs 2 lane, 2 lane + 1), handed on by shuffles.
+__device__ __forceinline__ void pairs_of(int pos, uint64_t f0, uint64_t f1, int j, float (&cs)[8], float (&sn)[8]) {
+    const float2 p0 = cos_sin_of(turns_of(pos, static_cast<uint32_t>(f0), static_cast<uint32_t>(f0 >> 32)));
+    const float2 p1 = cos_sin_of(turns_of(pos, static_cast<uint32_t>(f1), static_cast<uint32_t>(f1 >> 32)));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        cs[2 * e] = __shfl_sync(0xffffffffu, p0.x, 4 * j + e);
+        sn[2 * e] = __shfl_sync(0xffffffffu, p0.y, 4 * j + e);
+        cs[2 * e + 1] = __shfl_sync(0xffffffffu, p1.x, 4 * j + e);
+        sn[2 * e + 1] = __shfl_sync(0xffffffffu, p1.y, 4 * j + e);
+    }
+}
+
+// Few tokens: items are (token, 4U rows); a warp walks items with the grid's stride and issues the next
 // item's loads before it works on the current one.
 template <bool kRope, int U>
 __global__ void __launch_bounds__(THREADS) store_fp8_kernel(const StoreFp8Args a, int64_t n_tokens, int chunks, int* err) {
     const int lane = threadIdx.x & 31;
     const int j = lane & (ROW_LANES - 1);
     const int sub = lane / ROW_LANES;
-    const int hq = kRope ? a.num_heads : 0;                 // 0 without q
+    const int hq = kRope ? a.num_heads : 0;
     const int rows = hq + 2 * a.num_kv_heads;
     const int64_t items = n_tokens * chunks;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * (THREADS / 32);
     int64_t it = static_cast<int64_t>(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5);
     if (it >= items) return;
-    uint64_t f0 = 0, f1 = 0;                                // this lane's two pairs: 2 lane, 2 lane + 1
-    if (kRope) {
-        f0 = a.turns[2 * lane];
-        f1 = a.turns[2 * lane + 1];
-    }
+    const uint64_t f0 = kRope ? a.turns[2 * lane] : 0, f1 = kRope ? a.turns[2 * lane + 1] : 0;
     struct Item {
         int64_t t;
         int chunk, slot, pos;
@@ -106,80 +176,13 @@ __global__ void __launch_bounds__(THREADS) store_fp8_kernel(const StoreFp8Args a
         }
     };
     auto work = [&](const Item& x) {
-        const bool in_pool = x.slot >= 0 && x.slot < a.num_slots;
         if (x.slot >= a.num_slots && x.chunk == 0 && lane == 0) record_error(err, PKV_DEVERR_SLOT, static_cast<int>(x.t));
         float cs[8], sn[8];
-        if (kRope) {
-            // two pairs per lane; lane j's eight come from lanes 4j .. 4j + 3
-            const float2 p0 = cos_sin_of(turns_of(x.pos, static_cast<uint32_t>(f0), static_cast<uint32_t>(f0 >> 32)));
-            const float2 p1 = cos_sin_of(turns_of(x.pos, static_cast<uint32_t>(f1), static_cast<uint32_t>(f1 >> 32)));
+        if (kRope) pairs_of(x.pos, f0, f1, j, cs, sn);
+        const int blk = max(x.slot, 0) / a.block_size, off = max(x.slot, 0) - blk * a.block_size;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                cs[2 * e] = __shfl_sync(0xffffffffu, p0.x, 4 * j + e);
-                sn[2 * e] = __shfl_sync(0xffffffffu, p0.y, 4 * j + e);
-                cs[2 * e + 1] = __shfl_sync(0xffffffffu, p1.x, 4 * j + e);
-                sn[2 * e + 1] = __shfl_sync(0xffffffffu, p1.y, 4 * j + e);
-            }
-        }
-        const int blk = in_pool ? x.slot / a.block_size : 0;
-        const int off = in_pool ? x.slot - blk * a.block_size : 0;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int r = x.chunk * (GROUP * U) + u * GROUP + sub;
-            const bool is_q = r < hq;
-            const bool is_k = !is_q && r < hq + a.num_kv_heads;
-            const uint32_t wl[4] = {x.lo[u].x, x.lo[u].y, x.lo[u].z, x.lo[u].w};
-            const uint32_t wh[4] = {x.hi[u].x, x.hi[u].y, x.hi[u].z, x.hi[u].w};
-            float y[8], z[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                y[2 * e] = bf16_lo(wl[e]);
-                y[2 * e + 1] = bf16_hi(wl[e]);
-                z[2 * e] = bf16_lo(wh[e]);
-                z[2 * e + 1] = bf16_hi(wh[e]);
-            }
-            if (kRope && (is_q || is_k)) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float p = y[e], q = z[e];
-                    y[e] = fmaf(p, cs[e], -q * sn[e]);
-                    z[e] = fmaf(q, cs[e], p * sn[e]);
-                }
-            }
-            if (kRope && is_q) {
-                uint4* dst = reinterpret_cast<uint4*>(a.q_out + x.t * a.q_out_stride + static_cast<int64_t>(r) * kHeadDim);
-                dst[j] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                                    pack_bf16x2(y[6], y[7]));
-                dst[ROW_LANES + j] = make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]),
-                                                pack_bf16x2(z[4], z[5]), pack_bf16x2(z[6], z[7]));
-            }
-            uint32_t amax = 0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                amax = max(amax, __float_as_uint(y[e]) & 0x7fffffffu);
-                amax = max(amax, __float_as_uint(z[e]) & 0x7fffffffu);
-            }
-#pragma unroll
-            for (int d = 1; d < ROW_LANES; d <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-            if (!is_q && r < rows && in_pool) {
-                const int h = r - hq - (is_k ? 0 : a.num_kv_heads);
-                const int byte = scale_byte(amax);
-                uint2 c0 = make_uint2(0, 0), c1 = c0;
-                if (byte != 255) {
-                    // 2^-(byte - 127), a normal number: the byte is at most 247
-                    const float inv = __uint_as_float(static_cast<uint32_t>(254 - byte) << 23);
-                    c0 = to_codes(y, inv);
-                    c1 = to_codes(z, inv);
-                }
-                uint8_t* dst = (is_k ? a.k_cache : a.v_cache) +
-                               (static_cast<int64_t>(x.slot) * a.num_kv_heads + h) * kHeadDim;
-                *reinterpret_cast<uint2*>(dst + 8 * j) = c0;
-                *reinterpret_cast<uint2*>(dst + 64 + 8 * j) = c1;
-                if (j == 0)
-                    (is_k ? a.k_scale : a.v_scale)[(static_cast<int64_t>(blk) * a.num_kv_heads + h) * a.block_size + off] =
-                        static_cast<uint8_t>(byte);
-            }
-        }
+        for (int u = 0; u < U; ++u)
+            put_row<kRope>(a, x.t, x.slot, blk, off, x.chunk * (GROUP * U) + u * GROUP + sub, j, x.lo[u], x.hi[u], cs, sn);
     };
     Item cur, next;
     load(it, cur);
@@ -191,13 +194,120 @@ __global__ void __launch_bounds__(THREADS) store_fp8_kernel(const StoreFp8Args a
     work(cur);
 }
 
-template <bool kRope, int U>
+// Many tokens: items are (token, RING_ROWS rows); each warp of a persistent grid keeps a ring of RING stages of
+// shared memory filled by bulk copies (up to three an item: its q, k and v rows), which holds far more bytes in
+// flight than registers do.
+constexpr int RING = 2;
+constexpr int RING_ROWS = 16;
+constexpr int RING_STAGE = RING_ROWS * kHeadDim * 2;
+constexpr int RING_CTAS_PER_SM = 2;
+constexpr size_t kRingSmem = static_cast<size_t>(THREADS / 32) * RING * (RING_STAGE + 8);
+
+template <bool kRope>
+__global__ void __launch_bounds__(THREADS, RING_CTAS_PER_SM)
+store_fp8_ring_kernel(const StoreFp8Args a, int64_t n_tokens, int chunks, int* err) {
+    extern __shared__ __align__(128) uint8_t ring_smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int j = lane & (ROW_LANES - 1);
+    const int sub = lane / ROW_LANES;
+    const int hq = kRope ? a.num_heads : 0;
+    const int rows = hq + 2 * a.num_kv_heads;
+    const int64_t items = n_tokens * chunks;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * (THREADS / 32);
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * (THREADS / 32) + warp;
+    if (first >= items) return;
+    const int64_t n_mine = (items - first + stride - 1) / stride;
+    const uint32_t stage0 = smem_u32(ring_smem) + warp * RING * RING_STAGE;
+    const uint32_t bar0 = smem_u32(ring_smem) + (THREADS / 32) * RING * RING_STAGE + warp * RING * 8;
+    if (lane == 0) {
+        for (int s = 0; s < RING; ++s) mbar_init(bar0 + 8 * s, 1);
+        fence_barrier_init();
+    }
+    __syncwarp();
+    const uint64_t f0 = kRope ? a.turns[2 * lane] : 0, f1 = kRope ? a.turns[2 * lane + 1] : 0;
+    int slot[RING], pos[RING];
+    int64_t issued = 0;
+    auto issue = [&](int s) {                               // item `issued` into stage s
+        const int64_t it = first + issued * stride;
+        const int64_t t = it / chunks;
+        const int r0 = static_cast<int>(it - t * chunks) * RING_ROWS, r1 = min(rows, r0 + RING_ROWS);
+        slot[s] = __ldg(a.slots + t);
+        pos[s] = kRope ? __ldg(a.positions + t) : 0;
+        if (lane == 0) {
+            const uint32_t bar = bar0 + 8 * s, dst = stage0 + s * RING_STAGE;
+            mbar_arrive_expect_tx(bar, static_cast<uint32_t>(r1 - r0) * (kHeadDim * 2));
+            auto part = [&](const uint16_t* src, int64_t token_stride, int begin, int end) {      // rows [begin, end) of the token
+                const int x0 = max(r0, begin), x1 = min(r1, end);
+                if (x0 < x1)
+                    bulk_load(dst + (x0 - r0) * (kHeadDim * 2), src + t * token_stride + static_cast<int64_t>(x0 - begin) * kHeadDim,
+                              static_cast<uint32_t>(x1 - x0) * (kHeadDim * 2), bar);
+            };
+            if (kRope) part(a.q, a.q_stride, 0, hq);
+            part(a.k, a.k_stride, hq, hq + a.num_kv_heads);
+            part(a.v, a.v_stride, hq + a.num_kv_heads, rows);
+        }
+        ++issued;
+    };
+#pragma unroll
+    for (int s = 0; s < RING; ++s)
+        if (issued < n_mine) issue(s);
+    bool ok = true;
+    int64_t done = 0;
+    uint32_t parity = 0;
+    while (done < n_mine && ok) {
+#pragma unroll
+        for (int s = 0; s < RING; ++s) {
+            if (done >= n_mine || !ok) break;
+            ok = __all_sync(0xffffffffu, mbar_wait(bar0 + 8 * s, parity, err, 5));
+            if (!ok) break;
+            const int64_t it = first + done * stride;
+            const int64_t t = it / chunks;
+            const int chunk = static_cast<int>(it - t * chunks);
+            const int sl = slot[s];
+            if (sl >= a.num_slots && chunk == 0 && lane == 0) record_error(err, PKV_DEVERR_SLOT, static_cast<int>(t));
+            float cs[8], sn[8];
+            if (kRope) pairs_of(pos[s], f0, f1, j, cs, sn);
+            const int blk = max(sl, 0) / a.block_size, off = max(sl, 0) - blk * a.block_size;
+            const uint32_t at = stage0 + s * RING_STAGE + sub * (kHeadDim * 2) + 16 * j;
+#pragma unroll
+            for (int u = 0; u < RING_ROWS / GROUP; ++u) {
+                const int r = chunk * RING_ROWS + u * GROUP;
+                if (r >= rows) break;                       // whole groups past the token's rows (uniform)
+                const uint4 lo = ld_shared_v4(at + u * GROUP * (kHeadDim * 2)), hi = ld_shared_v4(at + u * GROUP * (kHeadDim * 2) + 128);
+                put_row<kRope>(a, t, sl, blk, off, r + sub, j, lo, hi, cs, sn);
+            }
+            ++done;
+            __syncwarp();                                   // every lane has read the stage
+            if (issued < n_mine) issue(s);
+        }
+        parity ^= 1u;
+    }
+    // copies still in flight (a wait above gave up) land before the CTA's shared memory goes away
+    if (!ok)
+        for (int64_t i = done; i < issued; ++i) mbar_wait(bar0 + 8 * static_cast<int>(i % RING), static_cast<uint32_t>((i / RING) & 1), err, 6);
+}
+
+template <bool kRope>
 cudaError_t launch(const StoreFp8Args& a, int64_t n_tokens, int* err, cudaStream_t stream) {
     const int rows = a.num_heads + 2 * a.num_kv_heads;
+    auto ctas_for = [&](int chunks) { return (n_tokens * chunks + THREADS / 32 - 1) / (THREADS / 32); };
+    const int64_t sms = sm_count();
+    // The ring pays once every warp of its grid walks a few items.
+    const int ring_chunks = (rows + RING_ROWS - 1) / RING_ROWS;
+    if (ctas_for(ring_chunks) >= 2 * RING_CTAS_PER_SM * sms) {
+        if (!setup_once(kRope ? kSetupStoreFp8Rope : kSetupStoreFp8, [] {
+                return cudaFuncSetAttribute(store_fp8_ring_kernel<kRope>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            static_cast<int>(kRingSmem)) == cudaSuccess;
+            }))
+            return cudaErrorUnknown;
+        store_fp8_ring_kernel<kRope><<<static_cast<unsigned>(RING_CTAS_PER_SM * sms), THREADS, kRingSmem, stream>>>(a, n_tokens,
+                                                                                                                     ring_chunks, err);
+        return cudaGetLastError();
+    }
+    constexpr int U = 2;
     const int chunks = (rows + GROUP * U - 1) / (GROUP * U);
-    const int64_t ctas = (n_tokens * chunks + THREADS / 32 - 1) / (THREADS / 32);
-    const int64_t resident = static_cast<int64_t>(sm_count()) * CTAS_PER_SM;
-    store_fp8_kernel<kRope, U><<<static_cast<unsigned>(std::min(ctas, resident)), THREADS, 0, stream>>>(a, n_tokens, chunks, err);
+    const int64_t ctas = std::min<int64_t>(ctas_for(chunks), CTAS_PER_SM * sms);
+    store_fp8_kernel<kRope, U><<<static_cast<unsigned>(ctas), THREADS, 0, stream>>>(a, n_tokens, chunks, err);
     return cudaGetLastError();
 }
 
@@ -205,7 +315,7 @@ cudaError_t launch(const StoreFp8Args& a, int64_t n_tokens, int* err, cudaStream
 
 cudaError_t launch_store_fp8(const StoreFp8Args& a, int64_t n_tokens, int* err, cudaStream_t stream) {
     if (n_tokens == 0) return cudaSuccess;
-    return a.positions ? launch<true, 2>(a, n_tokens, err, stream) : launch<false, 2>(a, n_tokens, err, stream);
+    return a.positions ? launch<true>(a, n_tokens, err, stream) : launch<false>(a, n_tokens, err, stream);
 }
 
 }  // namespace pkv

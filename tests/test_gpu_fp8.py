@@ -211,6 +211,40 @@ def test_rope_store_in_place_and_without_q(pkv):
     assert torch.all((ref.double() - other).abs() <= 2.0 ** -7 * other.abs() + 2e-6 * q.double().abs().amax())
 
 
+@pytest.mark.parametrize("n,hq,hkv", [(2500, 16, 8), (5001, 8, 1), (1700, 32, 8), (5003, 3, 2), (4900, 0, 8)])
+def test_many_tokens_at_once_are_the_same_as_a_few_at_a_time(pkv, n, hq, hkv):
+    """Large appends take a kernel of their own (more work than four items for every warp of the GPU): bit for
+    bit what appends of 400 tokens write, from views of a fused projection, with skipped rows."""
+    g = torch.Generator().manual_seed(n)
+    width = (hq + 2 * hkv) * D
+    qkv = (torch.randn(n, width + 24, generator=g) * 3).bfloat16().cuda()[:, :width].unflatten(1, (hq + 2 * hkv, D))
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+    pos = torch.randint(0, 2 ** 20, (n,), generator=g, dtype=torch.int32).cuda()
+    nb = -(-n // 256) + 1
+    slots = torch.from_numpy(slots_for(n, nb, 256, n + 1, skip=True)).cuda()
+    pool = make_pool(nb, 256, hkv, n + 2)
+    a, b = on_gpu(pool), on_gpu(pool)
+    parts = [slice(i, i + 400) for i in range(0, n, 400)]
+    if hq:
+        once = pkv.pkv_rope_store_kvcache_fp8(q, k, v, pos, slots, *a, 1e6)
+        few = torch.cat([pkv.pkv_rope_store_kvcache_fp8(q[x], k[x], v[x], pos[x], slots[x], *b, 1e6) for x in parts])
+        assert torch.equal(once, few)
+    else:
+        pkv.pkv_store_kvcache_fp8(k, v, slots, *a)
+        for x in parts:
+            pkv.pkv_store_kvcache_fp8(k[x], v[x], slots[x], *b)
+    for x, y, old in zip(a, b, pool):
+        assert np.array_equal(raw(x), raw(y)) and not np.array_equal(raw(x), old)
+    if hq:                                                # and without q, and in place
+        c = on_gpu(pool)
+        assert pkv.pkv_rope_store_kvcache_fp8(None, k, v, pos, slots, *c, 1e6) is None
+        for x, y in zip(a, c):
+            assert np.array_equal(raw(x), raw(y))
+        pkv.pkv_rope_store_kvcache_fp8(q, k, v, pos, slots, *c, 1e6, q_out=q)
+        assert torch.equal(once, q)
+    expect_no_device_error(pkv)
+
+
 def test_store_slot_past_the_pool_is_skipped_and_recorded(pkv):
     k = randn_bf16((3, 8, D), 31).cuda()
     pool = make_pool(1, 256, 8, 32)
