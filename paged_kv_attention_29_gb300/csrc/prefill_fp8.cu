@@ -41,6 +41,7 @@ struct DecodeTilesParams {
     const int32_t* block_tables;
     int32_t* tile_tables;         // [num_seqs][max_tiles]
     int max_blocks, num_seqs, num_kv_heads, block_size, num_blocks, max_tiles;
+    uint32_t heads_magic;         // ceil(2^32 / num_kv_heads), which divides a part's rows by umulhi; 0 for one head
     int64_t num_tiles, total_k;
     int* err;
 };
@@ -70,7 +71,7 @@ __device__ __forceinline__ uint2 bf16_of_codes(uint32_t w, float f) {
 
 // Started beside the plan (which it does not read) by programmatic launch; it ends after the plan has, so
 // the attention kernel, which waits for this one, finds both done.
-__global__ void __launch_bounds__(THREADS) decode_tiles_kernel(const DecodeTilesParams p) {
+__global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_tiles_kernel(const DecodeTilesParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x;
     // the tables the attention kernel walks: tile j of sequence s
@@ -112,7 +113,8 @@ __global__ void __launch_bounds__(THREADS) decode_tiles_kernel(const DecodeTiles
 #pragma unroll
             for (int i = 0; i < BATCH; ++i) {
                 const int v = min(v0 + i * THREADS, vecs - 1);
-                const int tok = v / row_vecs, h = (v - tok * row_vecs) / (D / 8);
+                const int row = v / (D / 8), tok = p.heads_magic ? static_cast<int>(__umulhi(row, p.heads_magic)) : row;
+                const int h = row - tok * p.num_kv_heads;
                 const int64_t at = scale0 + static_cast<int64_t>(h) * p.block_size + tok;
                 w[0][i] = __ldcs(reinterpret_cast<const uint2*>(p.k_codes) + src0 + v);
                 w[1][i] = __ldcs(reinterpret_cast<const uint2*>(p.v_codes) + src0 + v);
@@ -177,6 +179,7 @@ pkv_status launch_prefill_fp8(const PrefillFp8Args& a, int* err, cudaStream_t st
     p.max_blocks = a.max_blocks;
     p.num_seqs = a.num_seqs;
     p.num_kv_heads = a.num_kv_heads;
+    p.heads_magic = a.num_kv_heads > 1 ? static_cast<uint32_t>(((1ull << 32) + a.num_kv_heads - 1) / a.num_kv_heads) : 0u;
     p.block_size = a.block_size;
     p.num_blocks = a.num_blocks;
     p.max_tiles = max_tiles;

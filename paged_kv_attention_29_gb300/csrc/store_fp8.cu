@@ -42,9 +42,12 @@ __device__ __forceinline__ int scale_byte(uint32_t amax_bits) {
 __device__ __forceinline__ uint2 to_codes(const float (&x)[8], float inv) {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] * inv, x[2 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-    return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+    for (int i = 0; i < 4; ++i) {
+        float2 v;
+        fmul2(v.x, v.y, x[2 * i], x[2 * i + 1], inv, inv);
+        w[i] = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+    }
+    return make_uint2(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410));
 }
 
 // (cos, sin) of the angle that is turns / 2^32 of a turn.  The quadrant is taken off in integers, so
@@ -60,13 +63,13 @@ __device__ __forceinline__ float2 cos_sin_of(uint32_t turns) {
     return make_float2(((quadrant + 1u) & 2u) ? -x : x, (quadrant & 2u) ? -y : y);
 }
 
-// Eight lanes' share of a row: its loads' bits, rotated (q, k), rounded and written.  r >= rows: nothing.
-// The warp calls it together.
+// Eight lanes' share of row r0 + sub of a token: its loads' bits, rotated (q, k), rounded and written.  The
+// warp calls it together for rows r0 .. r0 + 3; what none of the four needs is skipped by all.
 template <bool kRope>
-__device__ __forceinline__ void put_row(const StoreFp8Args& a, int64_t t, int slot, int blk, int off, int r, int j, const uint4& lo,
-                                        const uint4& hi, const float (&cs)[8], const float (&sn)[8]) {
+__device__ __forceinline__ void put_row(const StoreFp8Args& a, int64_t t, int slot, int blk, int off, int r0, int sub, int j,
+                                        const uint4& lo, const uint4& hi, const float (&cs)[8], const float (&sn)[8]) {
     const int hq = kRope ? a.num_heads : 0;                 // 0 without q
-    const bool in_pool = slot >= 0 && slot < a.num_slots;
+    const int r = r0 + sub;
     const bool is_q = r < hq;
     const bool is_k = !is_q && r < hq + a.num_kv_heads;
     const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w};
@@ -79,12 +82,14 @@ __device__ __forceinline__ void put_row(const StoreFp8Args& a, int64_t t, int sl
         z[2 * e] = bf16_lo(wh[e]);
         z[2 * e + 1] = bf16_hi(wh[e]);
     }
-    if (kRope && (is_q || is_k)) {
+    if (kRope && r0 < hq + a.num_kv_heads && (is_q || is_k)) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float p = y[e], q = z[e];
-            y[e] = fmaf(p, cs[e], -q * sn[e]);
-            z[e] = fmaf(q, cs[e], p * sn[e]);
+        for (int e = 0; e < 8; e += 2) {
+            float u0, u1, v0, v1;
+            fmul2(u0, u1, z[e], z[e + 1], -sn[e], -sn[e + 1]);
+            fmul2(v0, v1, y[e], y[e + 1], sn[e], sn[e + 1]);
+            ffma2(y[e], y[e + 1], y[e], y[e + 1], cs[e], cs[e + 1], u0, u1);
+            ffma2(z[e], z[e + 1], z[e], z[e + 1], cs[e], cs[e + 1], v0, v1);
         }
     }
     if (kRope && is_q) {
@@ -93,17 +98,15 @@ __device__ __forceinline__ void put_row(const StoreFp8Args& a, int64_t t, int sl
         dst[ROW_LANES + j] = make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]), pack_bf16x2(z[4], z[5]),
                                         pack_bf16x2(z[6], z[7]));
     }
-    uint32_t amax = 0;
+    if (r0 + GROUP <= hq) return;
+    // the largest magnitude; a NaN anywhere shows as one, which is an exponent of 255 like an infinity's
+    float m = amax3_nan(amax3_nan(amax3_nan(y[0], y[1], y[2]), y[3], y[4]), amax3_nan(y[5], y[6], y[7]),
+                        amax3_nan(amax3_nan(z[0], z[1], z[2]), amax3_nan(z[3], z[4], z[5]), amax3_nan(z[6], z[7], 0.f)));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        amax = max(amax, __float_as_uint(y[e]) & 0x7fffffffu);
-        amax = max(amax, __float_as_uint(z[e]) & 0x7fffffffu);
-    }
-#pragma unroll
-    for (int d = 1; d < ROW_LANES; d <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-    if (!is_q && r < hq + 2 * a.num_kv_heads && in_pool) {
+    for (int d = 1; d < ROW_LANES; d <<= 1) m = amax3_nan(m, __shfl_xor_sync(0xffffffffu, m, d), 0.f);
+    if (!is_q && r < hq + 2 * a.num_kv_heads && slot >= 0 && slot < a.num_slots) {
         const int h = r - hq - (is_k ? 0 : a.num_kv_heads);
-        const int byte = scale_byte(amax);
+        const int byte = scale_byte(__float_as_uint(m) & 0x7fffffffu);
         uint2 c0 = make_uint2(0, 0), c1 = c0;
         if (byte != 255) {
             // 2^-(byte - 127), a normal number: the byte is at most 247
@@ -182,7 +185,7 @@ __global__ void __launch_bounds__(THREADS) store_fp8_kernel(const StoreFp8Args a
         const int blk = max(x.slot, 0) / a.block_size, off = max(x.slot, 0) - blk * a.block_size;
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            put_row<kRope>(a, x.t, x.slot, blk, off, x.chunk * (GROUP * U) + u * GROUP + sub, j, x.lo[u], x.hi[u], cs, sn);
+            put_row<kRope>(a, x.t, x.slot, blk, off, x.chunk * (GROUP * U) + u * GROUP, sub, j, x.lo[u], x.hi[u], cs, sn);
     };
     Item cur, next;
     load(it, cur);
@@ -274,7 +277,7 @@ store_fp8_ring_kernel(const StoreFp8Args a, int64_t n_tokens, int chunks, int* e
                 const int r = chunk * RING_ROWS + u * GROUP;
                 if (r >= rows) break;                       // whole groups past the token's rows (uniform)
                 const uint4 lo = ld_shared_v4(at + u * GROUP * (kHeadDim * 2)), hi = ld_shared_v4(at + u * GROUP * (kHeadDim * 2) + 128);
-                put_row<kRope>(a, t, sl, blk, off, r + sub, j, lo, hi, cs, sn);
+                put_row<kRope>(a, t, sl, blk, off, r, sub, j, lo, hi, cs, sn);
             }
             ++done;
             __syncwarp();                                   // every lane has read the stage
