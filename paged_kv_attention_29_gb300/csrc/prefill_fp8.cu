@@ -25,10 +25,11 @@ namespace {
 
 constexpr int D = kHeadDim;
 constexpr int TILE = 128;         // tokens per workspace tile (a prefill KV tile)
-constexpr int PART = 32;          // tokens one CTA decodes at a time
+constexpr int PART = 16;          // tokens one CTA decodes at a time
 constexpr int THREADS = 256;
-constexpr int BATCH = 8;
-constexpr int CTAS_PER_SM = 3;
+constexpr int BATCH = 4;
+constexpr int CTAS_PER_SM = 4;
+constexpr int MAX_NEAR = 1023;
 
 struct DecodeTilesParams {
     const uint8_t* k_codes;
@@ -47,16 +48,16 @@ struct DecodeTilesParams {
 };
 
 __device__ __forceinline__ int64_t first_tile(const int32_t* cu_k, int s) {
-    return (static_cast<int64_t>(__ldg(cu_k + s)) - __ldg(cu_k) + static_cast<int64_t>(TILE - 1) * s) / TILE;
+    return (static_cast<int64_t>(cu_k[s]) - cu_k[0] + static_cast<int64_t>(TILE - 1) * s) / TILE;
 }
 
 // Keys of sequence s, or -1 where its tiles do not fit (the lengths break the call's bounds).
-__device__ __forceinline__ int keys_of(const DecodeTilesParams& p, int s) {
-    const int64_t kl = static_cast<int64_t>(__ldg(p.cu_k + s + 1)) - __ldg(p.cu_k + s);
-    const int64_t first = first_tile(p.cu_k, s);
+__device__ __forceinline__ int keys_of(const DecodeTilesParams& p, const int32_t* cu_k, int s) {
+    const int64_t kl = static_cast<int64_t>(cu_k[s + 1]) - cu_k[s];
+    const int64_t first = first_tile(cu_k, s);
     if (kl < 0 || kl > static_cast<int64_t>(p.max_blocks) * p.block_size || first < 0) return -1;
     const int64_t need = (kl + TILE - 1) / TILE;
-    const bool within = static_cast<int64_t>(__ldg(p.cu_k + s + 1)) - __ldg(p.cu_k) <= p.total_k;
+    const bool within = static_cast<int64_t>(cu_k[s + 1]) - cu_k[0] <= p.total_k;
     return within && need <= p.max_tiles && first + need <= p.num_tiles ? static_cast<int>(kl) : -1;
 }
 
@@ -74,13 +75,20 @@ __device__ __forceinline__ uint2 bf16_of_codes(uint32_t w, float f) {
 __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_tiles_kernel(const DecodeTilesParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x;
+    // the running key counts, searched for every item: in shared memory where they fit
+    __shared__ int32_t cu_near[MAX_NEAR + 1];
+    const bool near = p.num_seqs <= MAX_NEAR;
+    if (near)
+        for (int i = tid; i <= p.num_seqs; i += THREADS) cu_near[i] = __ldg(p.cu_k + i);
+    __syncthreads();
+    const int32_t* cu_k = near ? cu_near : p.cu_k;
     // the tables the attention kernel walks: tile j of sequence s
     const int64_t entries = static_cast<int64_t>(p.num_seqs) * p.max_tiles;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * THREADS + tid; i < entries; i += static_cast<int64_t>(gridDim.x) * THREADS) {
         const int s = static_cast<int>(i / p.max_tiles), j = static_cast<int>(i - static_cast<int64_t>(s) * p.max_tiles);
-        const int kl = keys_of(p, s);
+        const int kl = keys_of(p, cu_k, s);
         if (kl < 0 && j == 0) record_error(p.err, PKV_DEVERR_SEQLENS, s);
-        p.tile_tables[i] = j * TILE < kl ? static_cast<int32_t>(first_tile(p.cu_k, s) + j) : -1;
+        p.tile_tables[i] = j * TILE < kl ? static_cast<int32_t>(first_tile(cu_k, s) + j) : -1;
     }
     const int64_t items = p.num_tiles * (TILE / PART);
     const int row_vecs = p.num_kv_heads * (D / 8);            // 8 codes each (a warp stores 512 bytes in a row): a token's
@@ -90,10 +98,10 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_tiles_kernel(cons
         int lo = 0, hi = p.num_seqs;                          // the last sequence whose first tile is not behind
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (first_tile(p.cu_k, mid) <= tile) lo = mid; else hi = mid;
+            if (first_tile(cu_k, mid) <= tile) lo = mid; else hi = mid;
         }
-        const int kl = keys_of(p, lo);
-        const int64_t tok0 = (tile - first_tile(p.cu_k, lo)) * TILE + part * PART;
+        const int kl = keys_of(p, cu_k, lo);
+        const int64_t tok0 = (tile - first_tile(cu_k, lo)) * TILE + part * PART;
         if (tok0 < 0 || tok0 >= kl) continue;
         const int n = min(PART, static_cast<int>(kl - tok0));
         const int blk = static_cast<int>(tok0 / p.block_size);
