@@ -155,13 +155,14 @@ int64_t tiles_of(int num_seqs, int64_t total_k) { return (total_k + static_cast<
 size_t prefill_fp8_workspace_bytes(int num_seqs, int num_kv_heads, int max_seqlen_q, int max_seqlen_k, int64_t total_k,
                                    int log_group) {
     const size_t pool = static_cast<size_t>(tiles_of(num_seqs, total_k)) * TILE * num_kv_heads * D * 2;
-    const size_t tables = static_cast<size_t>(num_seqs) * ((max_seqlen_k + TILE - 1) / TILE) * 4;
+    const size_t tables = static_cast<size_t>(num_seqs) * ((static_cast<int64_t>(max_seqlen_k) + TILE - 1) / TILE) * 4;
     return align256(prefill_workspace_bytes(num_seqs, max_seqlen_q, log_group)) + align256(tables) + 2 * align256(pool);
 }
 
 pkv_status launch_prefill_fp8(const PrefillFp8Args& a, int* err, cudaStream_t stream) {
     const int lg = group_log2(a.num_heads, a.num_kv_heads);
     if (lg < 0) return PKV_ERR_UNSUPPORTED;
+    if (a.max_seqlen_k > (1 << 24)) return PKV_ERR_UNSUPPORTED;     // (the plan's own limit is lower)
     const int64_t num_tiles = tiles_of(a.num_seqs, a.total_k);
     const int max_tiles = (a.max_seqlen_k + TILE - 1) / TILE;
     if (num_tiles > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;

@@ -464,6 +464,80 @@ def test_prefill_bad_block_is_recorded(pkv):
 
 
 # ---------------------------------------------------------------------------
+# sharing, sizes and streams
+# ---------------------------------------------------------------------------
+
+def test_calls_of_different_batches_share_a_workspace_in_stream_order(pkv):
+    """Two batches of other lengths, tables and sizes in turn on one workspace with nothing waited for between
+    them: each call's plan, tiles and pieces are its own."""
+    a = prefill_case(pkv, [60, 200, 1], [300, 200, 513], 16, 8, seed=91)
+    b = prefill_case(pkv, [257, 3], [257, 1000], 16, 8, seed=92)
+    n = max(pkv.pkv_prefill_fp8_workspace_size(len(x[0][5]) - 1, 16, 8, D, *x[0][8:11]) for x in (a, b))
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    got = [pkv.pkv_prefill_varlen_fp8(*x[0], workspace=ws) for _ in range(10) for x in (a, b)]
+    for i, o in enumerate(got):
+        assert torch.equal(o, (a, b)[i % 2][1])
+    c = decode_case(pkv, [900, 17, 0, 2500, 333], 16, 8, seed=93)
+    d = decode_case(pkv, [31] * 40, 16, 8, seed=94, check=[0])
+    ws = pkv.decode_fp8_workspace(40, 16, 8, D)
+    got = [pkv.pkv_decode_fp8(*x[0], workspace=ws) for _ in range(10) for x in (c, d)]
+    for i, o in enumerate(got):
+        assert torch.equal(o, (c, d)[i % 2][1])
+
+
+def test_calls_on_two_streams_at_once_with_their_own_workspaces(pkv):
+    a = decode_case(pkv, [3000, 17, 0, 2500, 333], 16, 8, seed=95)
+    b = prefill_case(pkv, [257, 300], [257, 1000], 16, 8, seed=96)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(10):                                   # workspaces and outputs allocated by the calls themselves
+        outs.append((pkv.pkv_decode_fp8(*a[0], stream=s1), pkv.pkv_prefill_varlen_fp8(*b[0], stream=s2)))
+    torch.cuda.synchronize()
+    for x, y in outs:
+        assert torch.equal(x, a[1]) and torch.equal(y, b[1])
+
+
+def test_decode_largest_batch(pkv):
+    """4096 sequences of 0 to 3 tokens sharing one block; one more is refused."""
+    c = Cache([3], 2, seed=97)
+    B = 4096
+    lens = np.arange(B) % 4
+    q = randn_bf16((B, 4, D), 98)
+    args = (*c.gpu(), torch.full((B + 1, 1), int(c.tables[0, 0]), dtype=torch.int32).cuda())
+    out = pkv.pkv_decode_fp8(q.cuda(), *args[:4], args[4][:B], torch.from_numpy(lens.astype(np.int32)).cuda(), 3, D ** -0.5)
+    k, v = c.read(0)
+    got = out.double().cpu().numpy()
+    for n in (1, 2, 3):
+        rows = np.nonzero(lens == n)[0]
+        ref, A = attention64(q[rows].double().numpy(), k[:n], v[:n], D ** -0.5)
+        assert np.all(np.abs(got[rows] - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -11 + 2.0 ** -13) * A)
+    assert not got[lens == 0].any()
+    with pytest.raises(pkv.PkvError):
+        pkv.pkv_decode_fp8(torch.cat([q, q[:1]]).cuda(), *args, torch.ones(B + 1, dtype=torch.int32).cuda(), 3, D ** -0.5)
+    expect_no_device_error(pkv)
+
+
+def test_empty_calls_do_nothing(pkv):
+    pool = on_gpu(make_pool(1, 256, 8, 99))
+    z = torch.zeros(0, 8, D, dtype=torch.bfloat16, device="cuda")
+    zq = torch.zeros(0, 16, D, dtype=torch.bfloat16, device="cuda")
+    zi = torch.zeros(0, dtype=torch.int32, device="cuda")
+    pkv.pkv_store_kvcache_fp8(z, z, zi, *pool)
+    assert pkv.pkv_rope_store_kvcache_fp8(zq, z, z, zi, zi, *pool, 1e4).shape == (0, 16, D)
+    assert pkv.pkv_decode_fp8(zq, *pool, torch.zeros(0, 1, dtype=torch.int32, device="cuda"), zi, 0, 0.1).shape == (0, 16, D)
+    cu = torch.zeros(3, dtype=torch.int32, device="cuda")
+    assert pkv.pkv_prefill_varlen_fp8(zq, *pool, cu, cu, torch.zeros(2, 1, dtype=torch.int32, device="cuda"), 0, 0, 0, 0.1).shape == (0, 16, D)
+    assert pkv.pkv_sample_filtered(torch.zeros(0, 50, device="cuda"), torch.zeros(0, device="cuda"), None, None, None, 1).shape == (0,)
+    expect_no_device_error(pkv)
+
+
+def test_prefill_of_more_sequences_than_fit_near(pkv):
+    """1100 one-token prompts: more running counts than the decoding kernel keeps in shared memory."""
+    prefill_case(pkv, [1] * 1100, [1 + i % 3 for i in range(1100)], 8, 1, seed=90, check=list(range(0, 1100, 97)))
+
+
+# ---------------------------------------------------------------------------
 # together: a prompt with a cached prefix, then decode steps, then sampling
 # ---------------------------------------------------------------------------
 
