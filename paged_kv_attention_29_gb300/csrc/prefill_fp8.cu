@@ -11,6 +11,10 @@
 // would save in traffic it would pay back in conversions repeated for every query tile, on the
 // softmax warps' issue slots, which already bound that kernel.
 //
+// Measured: 32 prompts, 18,000 keys of 8 KV heads, 25 us for the tiles (37 MB in, 74 MB out) beside 54 us of
+// attention; a prompt of 8192 tokens 11 us beside 160.  Eight codes per lane, so that a warp stores
+// whole lines: sixteen took 31 us.
+//
 // Tile j of sequence s lives at tile floor((cu_k[s] - cu_k[0] + 127 s) / 128) + j: consecutive
 // sequences' ranges cannot overlap (ceil(k / 128) <= (k + 127) / 128), so no scan is needed.
 #include <cuda_fp16.h>

@@ -40,6 +40,12 @@
 // fp32: a running sum is within about 1e-6 of itself, and the token at the border is decided as in
 // exact arithmetic except when a border lies that near to it.
 //
+// Measured on rows of 151,936 logits: 256 rows with settings of their own 110 us (156 MB, 1.4 TB/s; 41% of issue
+// slots), all top-k = 50 62 us, all top-p = 0.9 161 us, no filter 119 us; one row 15, 26 and 17 us (top-p 41 us
+// when its code has to come from DRAM).  What was tried: the slices kept in shared memory (435 us for the mixed
+// rows), one loop for every sweep instead of a batched and a last one (138), clusters of 4 (130), five CTAs to
+// an SM (123), long rows first (124).
+//
 // The race's keys are fp32 with an error below 2e-5; when the two best are within 1e-4 they are
 // ranked again in fp64.
 #include <cooperative_groups.h>

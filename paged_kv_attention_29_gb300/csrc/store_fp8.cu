@@ -11,8 +11,12 @@
 //
 // The step is bound by HBM: 256 bytes in and 129 out per K or V row, 512 per Q row.  Eight lanes
 // hold a row, lane j elements [8j, 8j+8) and [64+8j, 64+8j+8): both halves of its rotary pairs,
-// 16-byte loads, a row maximum by three shuffles.  A warp takes 4 rows at a time and U such
-// groups of one token, so its (cos, sin) of the lane's 8 pairs are computed once for 4U rows.
+// 16-byte loads, a row maximum by three shuffles.  A warp takes 4 rows at a time and several such
+// groups of one token, so the (cos, sin) of its pairs are computed once for all of them.
+//
+// Measured on 10,814 tokens of 16 Q and 8 KV heads, 155 MB: 31.3 us = 4.97 TB/s through the ring of
+// bulk copies, 38 us with the next item's loads in registers, 50 us without (one item per warp).
+// 3 stages 33.2 us, 3 CTAs per SM 33.0, items of 8 rows 39.8, of 32 rows 37.0.
 #include <cuda_fp8.h>
 
 #include <algorithm>
