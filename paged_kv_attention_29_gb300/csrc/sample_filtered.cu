@@ -20,9 +20,10 @@
 //           one exchange gives every CTA the row's first token (top_k = 1 ends here) and the sum Z.
 //   top-k   (k at most the threads, and 1024.)  A thread keeps its two largest quads of logits and
 //           the third's maximum.  The k-th largest of those quads' maxima bounds the k-th logit
-//           from below: a 128-bin histogram of the maxima gives the bound, and what reaches the bound (a little over k tokens) is collected from those, rarely by another
-//           look at a thread's share, in the first CTA, which sorts them, cuts them by k, then by p
-//           and min-p, and runs the race.
+//           from below: a 128-bin histogram of the maxima gives the bound, and what reaches the
+//           bound (a little over k tokens) is collected from those, rarely by another look at a
+//           thread's share, in the first CTA, which sorts them, cuts them by k, then by p and
+//           min-p, and runs the race.
 //   top-p   A token lighter than (1 - p) Z / vocab is outside (all of those together weigh less
 //           than 1 - p of Z).  Each warp lists its quads that hold others (so the work below runs
 //           on full warps), and those are counted into 2048 bins of 1/64 octave of weight.  A bin's
@@ -35,9 +36,9 @@
 //           same histogram over every token, and the range of candidates halved, by (logit bits,
 //           column), until it fits; the race then sweeps the slices once more.
 //
-// Counts are integers and sums across threads 64-bit fixed point (2^-38), so neither atomics nor
-// the order of the list can change a result.  A thread's share of a sum (a few dozen weights) is
-// fp32: a running sum is within about 1e-6 of itself, and the token at the border is decided as in
+// Counts are integers, the weights of every thread are summed in a fixed tree (Z) or in 64-bit fixed
+// point (2^-38), so neither atomics nor the order of the list can change a result.  A thread's share
+// of a sum (a few dozen weights) is fp32: a running sum is within about 1e-6 of itself, and the token at the border is decided as in
 // exact arithmetic except when a border lies that near to it.
 //
 // Measured on rows of 151,936 logits: 256 rows with settings of their own 110 us (156 MB, 1.4 TB/s; 41% of issue
@@ -88,9 +89,9 @@ struct Shared {
     uint64_t sorted[RANK_MAX];
     uint64_t slot[2][MAX_CLUSTER];             // cluster-wide sums, alternating
     uint64_t lo[2][MAX_CLUSTER], hi[2][MAX_CLUSTER];   // cluster-wide ranges, alternating
-    uint64_t top[MAX_CLUSTER];   // pass 1: first token and sum of each CTA
+    uint64_t top[MAX_CLUSTER];   // pass 1: first token of each CTA, and its sum of weights relative to it
     float z[MAX_CLUSTER];
-    float wz[32];
+    float wz[32];                // per warp
     uint64_t win[MAX_CLUSTER][2];   // race: the two best of each CTA
     uint64_t threshold;
     uint64_t list_sum;
@@ -265,6 +266,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
         }
         return;
     }
+    auto started = cluster.barrier_arrive();              // waited for before the first access to another CTA
     const bool need_k = k > 0 && k < a.vocab;
     const bool need_p = p < 1.f;
     const bool fast_k = need_k && k <= FAST_K;
@@ -393,6 +395,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
 #pragma unroll
             for (int w = 0; w < WARPS; ++w) z += sh.wz[w];
         }
+        cluster.barrier_wait(std::move(started));
         if (tid < CLUSTER) {
             *cluster.map_shared_rank(&sh.top[rank], tid) = t;
             *cluster.map_shared_rank(&sh.z[rank], tid) = z;
@@ -518,7 +521,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
     };
     Best best;
     best.clear();
-    // The tokens of a quad that are from x_min up and pass `in`, raced.  A token can beat the warp's best
+    // The tokens of a quad that are above -inf, raced.  A token can beat the warp's best
     // `bar` only if 1 - u < e^(z - bar) (since -ln u >= 1 - u), which spares most keys: the quad's smallest
     // 1 - u against the bound of its largest logit, then each token's; the bound carries a margin of 1e-3.
     auto race_quad = [&](int qd, const float (&l)[4], float lmax, float bar) {
@@ -790,10 +793,11 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
                 const uint64_t c = composite(x, col);
                 if (c >= cmin && c <= cmax) collect(c);
             });
-            n = min(n, static_cast<uint32_t>(CAP));
             cluster.sync();
         }
         if (rank == 0) {
+            n = min(sh.list_n, static_cast<uint32_t>(CAP));              // as counted
+            __syncthreads();
             sort_list(sh.list, static_cast<int>(n));
             uint64_t sum = 0;
             int kept = static_cast<int>(min(goal, static_cast<uint64_t>(n)));
@@ -892,9 +896,10 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
                 if (tid == 0) sh.first[0] = sh.first[1] = BINS;
                 __syncthreads();
                 const float at_up = left * (1.f - 1e-4f), at_dn = left * (1.f + 1e-4f);
-                // one thread sees each sum reach its mark
+                // the threads whose sums reach a mark from below it, or from so little above that rounding may be
+                // what put the prefix there
                 int b_up = BINS, b_dn = BINS;
-                const bool mine_up = run.x < at_up, mine_dn = run.y < at_dn;
+                const bool mine_up = run.x < at_up * 1.0001f, mine_dn = run.y < at_dn * 1.0001f;
 #pragma unroll
                 for (int i = 0; i < BINS_PER_THREAD; ++i) {
                     run.x += up[i];
@@ -902,8 +907,8 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
                     if (run.x >= at_up) b_up = min(b_up, tid * BINS_PER_THREAD + i);
                     if (run.y >= at_dn) b_dn = min(b_dn, tid * BINS_PER_THREAD + i);
                 }
-                if ((mine_up || tid == 0) && b_up < BINS) atomicMin(&sh.first[0], b_up);
-                if ((mine_dn || tid == 0) && b_dn < BINS) atomicMin(&sh.first[1], b_dn);
+                if (mine_up && b_up < BINS) atomicMin(&sh.first[0], b_up);
+                if (mine_dn && b_dn < BINS) atomicMin(&sh.first[1], b_dn);
                 __syncthreads();
                 b_lo = sh.first[0];
                 b_hi = min(max(b_lo, sh.first[1]), last);
@@ -935,8 +940,8 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
                     });
                     const uint64_t above = cluster_sum(fixed_of(ws));
                     cluster_hist();
-                    const float left = (static_cast<float>(goal) - static_cast<float>(above)) * (1.f / FIX);
                     // (a sum that rounding puts past the goal already leaves the first members as the range)
+                    const float left = goal > above ? static_cast<float>(goal - above) * (1.f / FIX) : 0.f;
                     find(fmaxf(left, 1e-30f), BINS - 1, [&](int b) { return sh.tot[b]; },
                          [&](int b) { return weight_of(d_lo + static_cast<float>(b) / sub); });
                     s_lo = b_lo;
@@ -971,9 +976,10 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
                     send_best();
                     const uint64_t above = cluster_sum(fixed_of(ws));
                     if (rank != 0) return;
-                    sort_list(sh.border, static_cast<int>(n_in));
+                    const int members = static_cast<int>(min(sh.list_n, static_cast<uint32_t>(BORDER)));     // n_in
+                    sort_list(sh.border, members);
                     uint64_t sum;
-                    const int kept = kept_by_weight(sh.border, static_cast<int>(n_in), above, goal, &sum);
+                    const int kept = kept_by_weight(sh.border, members, above, goal, &sum);
                     best.clear();
                     race_list(sh.border, kept);
                     block_best();
@@ -1038,7 +1044,7 @@ pkv_status launch_sample_filtered(const SampleFilteredArgs& a, int* err, cudaStr
         return PKV_ERR_CUDA;
     Args args;
     args.a = a;
-    args.vec_ok = (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0 && a.row_stride % 4 == 0;
+    args.vec_ok = (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0 && (a.batch == 1 || a.row_stride % 4 == 0);
     args.err = err;
     // Up to 9 clusters of 16 CTAs run at once; a row on 16 x 512 threads takes about two thirds of the time it
     // takes on 8 x 256 (top-p, one row of 151,936: 26 and 40 us), and with more rows than that it is throughput

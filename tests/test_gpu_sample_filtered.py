@@ -2,7 +2,7 @@
 
 Ids must be the oracle's on every row whose outcome is decided by more than rounding: a race
 margin above 1e-9 (near races are ranked in fp64) and a winner that does not change when top_p
-moves by 1e-6 of itself (sums are good to 1e-7).  Nearly every row is; each test bounds the others."""
+moves by 1e-6 of itself (what the sums are good to).  Nearly every row is; each test bounds the others."""
 import numpy as np
 import pytest
 import torch
@@ -196,3 +196,19 @@ def test_many_rows_of_a_vocabulary_beyond_the_lists(pkv):
     x = rows(B, 180001, 41, 2.0)
     k, p = np.where(np.arange(B) % 4 == 0, 30, 0), np.where(np.arange(B) % 4 == 1, 1.0, 0.85)
     check(pkv, x, 0.9, k, p, 0.0, most_unclear=2)
+
+
+@pytest.mark.parametrize("vocab", [5, 1001, 30011])
+def test_one_row_of_an_odd_vocabulary(pkv, vocab):
+    for i, (k, p, m) in enumerate(SETTINGS):
+        check(pkv, rows(1, vocab, 60 + i), 0.8, k, p, m)
+
+
+@pytest.mark.parametrize("B", [8, 400])
+def test_top_p_borders_anywhere_in_a_row(pkv, B):
+    """One row under many p, so that borders lie in every part of the order, on histogram bins' and
+    threads' limits too."""
+    x = rows(1, 20011, 71, 1.5)
+    p = np.linspace(0.0005, 0.9995, 400)
+    for i in range(0, 400, B):
+        check(pkv, x.expand(B, -1).contiguous(), 0.9, 0, p[i:i + B], 0.0, offset=i)
