@@ -361,7 +361,8 @@ PKV_API pkv_status pkv_decode_noalloc(const pkv_bf16 *q, const pkv_bf16 *k_cache
 /*
  * Append rows to an 8-bit cache: the scatter of pkv_store_kvcache with the
  * rounding above.  Arguments, skipped rows (slot < 0), errors (a slot past the
- * pool: PKV_DEVERR_SLOT, skipped) and races of equal slots as there.  Exact: the
+ * pool: PKV_DEVERR_SLOT, skipped) as there.  Slots >= 0 of a call must differ: of
+ * rows with equal slots, one's codes may end beside another's scale.  Exact: the
  * codes and scales are those of the definition, bit for bit.
  */
 PKV_API pkv_status pkv_store_kvcache_fp8(const pkv_bf16 *k, const pkv_bf16 *v, int64_t n_tokens,
@@ -489,9 +490,10 @@ PKV_API pkv_status pkv_sample_dev(const float *logits, int32_t batch, int32_t vo
  * records PKV_DEVERR_TEMPERATURE or PKV_DEVERR_FILTER with info = row.
  * vocab <= 2^24.  Other arguments as pkv_sample; pkv_sample_filtered_dev reads
  * {seed, offset} from device memory as pkv_sample_dev does.
- * Weights are fp32 and their sums fp32 within a thread, fp64 across threads: a
- * token is decided as in exact arithmetic unless top_p * sum lies within about
- * 1e-7 of a running sum.  Results do not depend on timing.
+ * Weights and a thread's sums of them are fp32, joined across threads in a fixed
+ * order or in 64-bit fixed point: a token is decided as in exact arithmetic unless
+ * top_p * sum lies within about 1e-6 of a running sum.  Results do not depend on
+ * timing.
  */
 PKV_API pkv_status pkv_sample_filtered(const float *logits, int32_t batch, int32_t vocab, int64_t row_stride,
                                const float *temperatures, const int32_t *top_k, const float *top_p,
