@@ -71,9 +71,12 @@ constexpr int BORDER = 512;                  // of those, around top-p's border
 constexpr int LISTED = 10240;                // quads of a CTA's warps' lists
 constexpr int RANK_MAX = 256;                // members sorted by counting
 constexpr int LOADS = 4;                     // 16-byte loads in flight per thread of a sweep (pass 1, from HBM: LOADS1)
+constexpr int RACE_LOADS = 2;                // and of a race over all tokens
 constexpr int MAX_CLUSTER = 16;
 constexpr float BINS_PER_OCTAVE = 64.f;
 constexpr float RACE_Z = 19.6f;              // reach of the race (see above): 28.3 octaves, inside the fine bins
+constexpr float REF_REACH = 32.f;            // how far a race's reference may lie below a logit, in units of T
+constexpr int TRIES = 3;                     // winners of top-p races examined before the border is looked for
 constexpr float NEAR = 1e-4f;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float FIX = 274877906944.f;        // 2^38: a weight of 1 in fixed point
@@ -87,7 +90,8 @@ struct Shared {
     };
     uint64_t border[BORDER];     // first CTA, top-p: members
     uint64_t sorted[RANK_MAX];
-    uint64_t slot[2][MAX_CLUSTER];             // cluster-wide sums, alternating
+    uint64_t slot[2][MAX_CLUSTER];             // cluster-wide sums and counts, alternating
+    uint32_t slot_n[2][MAX_CLUSTER];
     uint64_t lo[2][MAX_CLUSTER], hi[2][MAX_CLUSTER];   // cluster-wide ranges, alternating
     uint64_t top[MAX_CLUSTER];   // pass 1: first token of each CTA, and its sum of weights relative to it
     float z[MAX_CLUSTER];
@@ -139,6 +143,11 @@ struct Best {
     __device__ __forceinline__ void merge(uint64_t o1, uint64_t o2) {
         b2 = max(max(b2, o2), min(b1, o1));
         b1 = max(b1, o1);
+    }
+    // keys shifted by d
+    __device__ __forceinline__ void rebase(float d) {
+        if (b1) b1 = composite(composite_x(b1) + d, composite_col(b1));
+        if (b2) b2 = composite(composite_x(b2) + d, composite_col(b2));
     }
     __device__ __forceinline__ float key() const { return b1 ? composite_x(b1) : -INFINITY; }
 };
@@ -233,6 +242,277 @@ __device__ __noinline__ uint4 noise_quad(uint32_t quad, PhiloxRow row) {
     return philox_row_at<false>(quad, row, unused);
 }
 
+__device__ __forceinline__ float warp_max(float x) {
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+    return m;
+}
+
+// The key of a token whose logit exceeds the reference's by d, relative to a key of 0 there.
+__device__ __forceinline__ float key_of_token(float d, float inv_t, uint32_t noise) {
+    // e = -ln u from the exact w = 1 - u where u is near 1, from the hardware logarithm elsewhere
+    const float w = one_minus_u_of(noise);
+    const float e = w < 0.015625f ? w * fmaf(w, fmaf(w, fmaf(w, 0.25f, 0.333333343f), 0.5f), 1.0f)
+                                  : -__logf(__uint2float_rn(2u * (noise >> 9) + 1u) * 5.9604644775390625e-08f);
+    return d * inv_t - __logf(e);
+}
+
+// The tokens of a quad that are above -inf, raced, with keys relative to `base`.  A token can beat the warp's
+// best `bar` only if 1 - u < e^(z - bar) (since -ln u >= 1 - u), which spares most keys: the quad's smallest
+// 1 - u against the bound of its largest logit, then each token's; the bound carries a margin of 1e-3.
+__device__ __forceinline__ void race_quad(Best& best, int qd, const float (&l)[4], float lmax, float base, float bar, float inv_t,
+                                          float l2, const uint4& w) {
+    const float cb = (1e-3f - bar) * LOG2E + 1.4419741739064e-3f;                      // + log2 1.001
+    const uint32_t wmax = max(max(w.x, w.y), max(w.z, w.w));
+    if (one_minus_u_of(wmax) < ex2_ftz(fmaf(lmax - base, l2, cb))) {
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (one_minus_u_of(ws[e]) < ex2_ftz(fmaf(l[e] - base, l2, cb)))
+                best.add(composite(key_of_token(l[e] - base, inv_t, ws[e]), 4 * qd + e));
+    }
+}
+
+// Whole quads are one aligned 16-byte load; absent columns and NaN read as -inf.
+__device__ __forceinline__ float4 clean(const float4& v) {
+    return make_float4(fmaxf(v.x, -INFINITY), fmaxf(v.y, -INFINITY), fmaxf(v.z, -INFINITY), fmaxf(v.w, -INFINITY));
+}
+__device__ __forceinline__ float4 load_whole_quad(const float* row, int qd) {
+    return clean(__ldg(reinterpret_cast<const float4*>(row) + qd));
+}
+__device__ __forceinline__ float4 load_columns(const float* row, int qd, int vocab) {
+    const int col = qd * 4;
+    float4 v;
+    v.x = __ldg(row + col);
+    v.y = col + 1 < vocab ? __ldg(row + col + 1) : -INFINITY;
+    v.z = col + 2 < vocab ? __ldg(row + col + 2) : -INFINITY;
+    v.w = col + 3 < vocab ? __ldg(row + col + 3) : -INFINITY;
+    return clean(v);
+}
+__device__ __forceinline__ float max_of(const float4& v) { return fmaxf(fmax3(v.x, v.y, v.z), v.w); }
+
+// f(quad, its logits) over quads [q0, q1) of a row by whole warps, N loads in flight; lanes without a quad get -inf.
+template <int THREADS, int N, typename F>
+__device__ __forceinline__ void sweep_warps(const float* row, int q0, int q1, int whole, int vocab, F f) {
+    const float4 none = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    const int tid = threadIdx.x;
+    int base = q0;
+    for (; base + N * THREADS <= min(q1, whole); base += N * THREADS) {
+        float4 v[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = load_whole_quad(row, base + i * THREADS + tid);
+#pragma unroll
+        for (int i = 0; i < N; ++i) f(base + i * THREADS + tid, v[i]);
+    }
+    for (; base < q1; base += N * THREADS) {
+        float4 v[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int qd = base + i * THREADS + tid;
+            v[i] = whole > 0 ? load_whole_quad(row, min(qd, whole - 1)) : none;
+            if (qd >= q1) v[i] = none;
+            else if (qd >= whole) v[i] = load_columns(row, qd, vocab);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (base + i * THREADS < q1) f(base + i * THREADS + tid, v[i]);
+    }
+}
+
+// A race among all tokens of a slice, read once, with its maximum and (kSum) the sum of its weights.  Sums and
+// keys are relative to a reference the warp shares, which moves when a logit exceeds it by REF_REACH.
+struct RaceAll {
+    Best best;
+    float mx, zs, ref;
+    int mx_quad;
+};
+template <bool kSum, int THREADS>
+__device__ __noinline__ RaceAll race_all_of(const float* row, int q0, int q1, int whole, int vocab, float T, float inv_t,
+                                            PhiloxRow prow) {
+    RaceAll r;
+    r.best.clear();
+    r.mx = r.ref = -INFINITY;
+    r.zs = 0.f;
+    r.mx_quad = q0;
+    const float l2 = fminf(inv_t * LOG2E, 3.4028235e38f);
+    const RoundKeys unused = {};
+    float ref_end = -INFINITY, bar = -INFINITY;
+    sweep_warps<THREADS, RACE_LOADS>(row, q0, q1, whole, vocab, [&](int qd, const float4& v) {
+        const float m4 = max_of(v);
+        if (m4 > r.mx) { r.mx = m4; r.mx_quad = qd; }
+        if (__any_sync(0xffffffffu, m4 > ref_end)) {
+            const float up = warp_max(m4), d = r.ref - up;
+            if (r.ref > -INFINITY) {
+                r.zs *= ex2_ftz(d * l2);
+                r.best.rebase(d * inv_t);
+                bar += d * inv_t;
+            }
+            r.ref = up;
+            ref_end = up + REF_REACH * T;
+        }
+        if (r.ref > -INFINITY) {
+            if (kSum)
+                r.zs += (ex2_ftz((v.x - r.ref) * l2) + ex2_ftz((v.y - r.ref) * l2)) +
+                        (ex2_ftz((v.z - r.ref) * l2) + ex2_ftz((v.w - r.ref) * l2));
+            const float l[4] = {v.x, v.y, v.z, v.w};
+            race_quad(r.best, qd, l, m4, r.ref, bar, inv_t, l2, philox_row_at<false>(static_cast<uint32_t>(qd), prow, unused));
+            bar = warp_max(r.best.key());
+        }
+    });
+    return r;
+}
+
+__device__ __forceinline__ uint32_t noise_of(int col, const PhiloxRow& prow) {
+    const uint4 w = noise_quad(static_cast<uint32_t>(col) >> 2, prow);
+    const int e = col & 3;
+    return e == 0 ? w.x : e == 1 ? w.y : e == 2 ? w.z : w.w;
+}
+
+// The column that wins among the two best: their fp64 keys decide where fp32 ones are too near.
+__device__ __noinline__ int winner_of(Best best, const float* row, float M, float T, PhiloxRow prow) {
+    int c1 = best.b1 ? composite_col(best.b1) : -1;       // (a row that changes under the call may have none)
+    if (best.b2 && composite_x(best.b1) - composite_x(best.b2) <= NEAR) {
+        const int c2 = composite_col(best.b2);
+        double d[2];
+        for (int i = 0; i < 2; ++i) {
+            const int col = i ? c2 : c1;
+            const double e = -log1p(-static_cast<double>(one_minus_u_of(noise_of(col, prow))));
+            d[i] = (static_cast<double>(__ldg(row + col)) - static_cast<double>(M)) / static_cast<double>(T) - log(e);
+        }
+        if (d[1] > d[0] || (d[1] == d[0] && c2 < c1)) c1 = c2;
+    }
+    return c1;
+}
+
+// top_p of a fixed-point sum (p < 1), at least 1.
+__device__ __forceinline__ uint64_t goal_of_sum(uint64_t z, float p) {
+    return max(__umul64hi(z, __float2ull_rz(p * 9223372036854775808.f)) << 1, static_cast<unsigned long long>(1));
+}
+
+// The winner among the n members of the list, which begins the row's order: their first `count`, and (by_weight)
+// of those the ones before which the weights sum to less than the goal (goal 0: p of the `count` ones' sum).
+// By every thread of the CTA; each holds its members in registers.  The members are not sorted: the
+// count-th is selected, and a race's winner stands if the weights before it are less than the goal; if they
+// are not, neither it nor what comes after it is a member, and the rest is raced again.
+template <int THREADS>
+__device__ __noinline__ int list_winner(Shared& sh, const float* row, int n, int count, bool by_weight, uint64_t goal, float p, float M,
+                                        float T, float inv_t, float per_logit, float min_x, PhiloxRow prow) {
+    constexpr int WARPS = THREADS / 32, PER = CAP / THREADS, DIGITS = 256;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint64_t c[PER], keep = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) c[i] = tid + i * THREADS < n ? sh.list[tid + i * THREADS] : 0;      // no member's is 0
+    if (count < n) {
+        uint64_t lo = ~0ull, hi = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (c[i]) { lo = min(lo, c[i]); hi = max(hi, c[i]); }
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) {
+            lo = min(lo, shfl_xor64(lo, off));
+            hi = max(hi, shfl_xor64(hi, off));
+        }
+        __syncthreads();
+        if (lane == 0) { sh.wlo[warp] = lo; sh.whi[warp] = hi; }
+        __syncthreads();
+        for (int w = 0; w < WARPS; ++w) { lo = min(lo, sh.wlo[w]); hi = max(hi, sh.whi[w]); }
+        // the need-th, from the top, of the `in` members in [lo, hi]; 256 equal parts at a time
+        int need = count, in = n;
+        while (in > RANK_MAX) {
+            const int shift = max(0, 56 - __clzll(static_cast<long long>(hi - lo)));
+            if (tid < DIGITS) sh.hist[tid] = 0u;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (c[i] >= lo && c[i] <= hi) atomicAdd(&sh.hist[(c[i] - lo) >> shift], 1u);
+            __syncthreads();
+            const int digit = DIGITS - 1 - tid, mine = tid < DIGITS ? static_cast<int>(sh.hist[digit]) : 0;
+            int upto = mine;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, upto, off);
+                if (lane >= off) upto += x;
+            }
+            if (lane == 31) sh.wlo[warp] = static_cast<uint64_t>(upto);
+            __syncthreads();
+            for (int w = 0; w < warp; ++w) upto += static_cast<int>(sh.wlo[w]);
+            if (upto - mine < need && upto >= need) { sh.first[0] = digit; sh.first[1] = need - (upto - mine); sh.first[2] = mine; }
+            __syncthreads();
+            lo += static_cast<uint64_t>(sh.first[0]) << shift;
+            hi = min(hi, lo + ((static_cast<uint64_t>(1) << shift) - 1));
+            need = sh.first[1];
+            in = sh.first[2];
+            __syncthreads();
+        }
+        if (tid == 0) sh.first[0] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (c[i] >= lo && c[i] <= hi) {
+                const int at = atomicAdd(&sh.first[0], 1);
+                if (at < RANK_MAX) sh.sorted[at] = c[i];
+            }
+        __syncthreads();
+        for (int i = tid; i < in; i += THREADS) {
+            const uint64_t x = sh.sorted[i];
+            int before = 0;
+#pragma unroll 4
+            for (int j = 0; j < in; ++j) before += sh.sorted[j] > x ? 1 : 0;
+            if (before == need - 1) sh.threshold = x;
+        }
+        __syncthreads();
+        keep = sh.threshold;
+    }
+    auto block_sum = [&](uint64_t v) -> uint64_t {
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) v += shfl_xor64(v, off);
+        __syncthreads();
+        if (lane == 0) sh.wred[warp] = v;
+        __syncthreads();
+        v = 0;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) v += sh.wred[w];
+        return v;
+    };
+    auto weight = [&](uint64_t m) { return fixed_of(weight_of((M - composite_x(m)) * per_logit)); };
+    auto weights_from = [&](uint64_t first) {              // of the members from `first` up
+        uint64_t s = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (c[i] && c[i] >= first) s += weight(c[i]);
+        return block_sum(s);
+    };
+    float key[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        if (c[i] < keep || !(composite_x(c[i]) >= min_x)) key[i] = -INFINITY;      // (an absent member's x is NaN)
+        else key[i] = key_of_token(composite_x(c[i]) - M, inv_t, noise_of(composite_col(c[i]), prow));
+    }
+    if (by_weight && goal == 0) goal = goal_of_sum(weights_from(keep), p);
+    for (;;) {
+        Best best;
+        best.clear();
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (c[i] >= keep && key[i] > -INFINITY) best.add(composite(key[i], composite_col(c[i])));
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) best.merge(shfl_xor64(best.b1, off), shfl_xor64(best.b2, off));
+        if (lane == 0) { sh.wwin[warp][0] = best.b1; sh.wwin[warp][1] = best.b2; }
+        __syncthreads();
+        best.clear();
+        if (lane < WARPS) best.merge(sh.wwin[lane][0], sh.wwin[lane][1]);
+#pragma unroll
+        for (int off = WARPS / 2; off >= 1; off >>= 1) best.merge(shfl_xor64(best.b1, off), shfl_xor64(best.b2, off));
+        best.b1 = static_cast<uint64_t>(__shfl_sync(0xffffffffu, static_cast<unsigned long long>(best.b1), 0));
+        best.b2 = static_cast<uint64_t>(__shfl_sync(0xffffffffu, static_cast<unsigned long long>(best.b2), 0));
+        const int col = winner_of(best, row, M, T, prow);
+        if (!by_weight || col < 0) return col;
+        const uint64_t w = composite(__ldg(row + col), col) + 1;
+        if (weights_from(w) < goal) return col;
+        keep = w;
+    }
+}
+
 struct Args {
     SampleFilteredArgs a;
     int vec_ok;
@@ -245,7 +525,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
     constexpr int BINS_PER_THREAD = BINS / THREADS;
     constexpr int BINS_PER_RANK = BINS / CLUSTER;
     constexpr int FAST_K = CLUSTER * THREADS < CAP / 2 ? CLUSTER * THREADS : CAP / 2;
-    static_assert(BINS % THREADS == 0 && CLUSTER <= MAX_CLUSTER && WARPS <= 32 && COARSE <= THREADS, "tables fit");
+    static_assert(BINS % THREADS == 0 && CLUSTER <= MAX_CLUSTER && CLUSTER <= WARPS && WARPS <= 32 && COARSE <= THREADS, "tables fit");
     const SampleFilteredArgs& a = args.a;
     __shared__ Shared sh;
     cg::cluster_group cluster = cg::this_cluster();
@@ -271,6 +551,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
     const bool need_p = p < 1.f;
     const bool fast_k = need_k && k <= FAST_K;
     const float inv_t = fminf(1.0f / T, 3.4028235e38f);
+    const float l2 = fminf(inv_t * LOG2E, 3.4028235e38f);
     const float per_logit = fminf(inv_t * (LOG2E * BINS_PER_OCTAVE), 3.4028235e38f);    // bins per unit of logit
 
     // ---- this CTA's slice: whole quads [q0, q1) of the row; absent columns and NaN read as -inf
@@ -278,23 +559,10 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
     const int nquads = (a.vocab + 3) >> 2;
     const int per = (nquads + CLUSTER - 1) / CLUSTER;
     const int q0 = min(nquads, rank * per), q1 = min(nquads, q0 + per);
-    auto clean = [](const float4& v) {
-        return make_float4(fmaxf(v.x, -INFINITY), fmaxf(v.y, -INFINITY), fmaxf(v.z, -INFINITY), fmaxf(v.w, -INFINITY));
-    };
-    // quads below `whole` are one aligned 16-byte load
-    const int whole = args.vec_ok ? a.vocab >> 2 : 0;
-    auto load_whole = [&](int qd) -> float4 { return clean(__ldg(reinterpret_cast<const float4*>(lrow) + qd)); };
-    auto load_quad = [&](int qd) -> float4 {
-        if (qd < whole) return load_whole(qd);
-        const int col = qd * 4;
-        float4 v;
-        v.x = __ldg(lrow + col);
-        v.y = col + 1 < a.vocab ? __ldg(lrow + col + 1) : -INFINITY;
-        v.z = col + 2 < a.vocab ? __ldg(lrow + col + 2) : -INFINITY;
-        v.w = col + 3 < a.vocab ? __ldg(lrow + col + 3) : -INFINITY;
-        return clean(v);
-    };
-    auto max_of = [](const float4& v) { return fmaxf(fmax3(v.x, v.y, v.z), v.w); };
+    const int whole = args.vec_ok ? a.vocab >> 2 : 0;     // quads below it are whole
+    const float4 none = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    auto load_whole = [&](int qd) -> float4 { return load_whole_quad(lrow, qd); };
+    auto load_quad = [&](int qd) -> float4 { return qd < whole ? load_whole(qd) : load_columns(lrow, qd, a.vocab); };
     // f(quad, its logits) over the slice, LOADS loads in flight per thread
     auto sweep_quads_by = [&](auto in_flight, auto f) {
         constexpr int N = decltype(in_flight)::value;
@@ -319,6 +587,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
         for (; qd < q1; qd += THREADS) f(qd, load_quad(qd));
     };
     auto sweep_quads = [&](auto f) { sweep_quads_by(std::integral_constant<int, LOADS>{}, f); };
+    const int iters = (q1 - q0 + THREADS - 1) / THREADS;  // uniform
     // f(column, logit) for every logit of the slice from x_min up, and above -inf
     auto sweep_from = [&](float x_min, auto f) {
         sweep_quads([&](int qd, const float4& v) {
@@ -331,6 +600,39 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
         });
     };
 
+    // ---- noise and keys
+    uint64_t seed = a.seed, offset = a.offset;
+    if (a.seed_offset) {
+        seed = __ldg(a.seed_offset);
+        offset = __ldg(a.seed_offset + 1);
+    }
+    const uint64_t rr = static_cast<uint64_t>(row) + offset;
+    const PhiloxRow prow = philox_row(static_cast<uint32_t>(rr), static_cast<uint32_t>(rr >> 32), static_cast<uint32_t>(seed),
+                                      static_cast<uint32_t>(seed >> 32));
+    Best best;
+    best.clear();
+    auto warp_best = [&]() {                              // of the warp's lanes, in each of them
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) best.merge(shfl_xor64(best.b1, off), shfl_xor64(best.b2, off));
+    };
+    // the CTA's two best, in the lanes of its first warp
+    auto block_best = [&]() {
+        warp_best();
+        if (lane == 0) { sh.wwin[warp][0] = best.b1; sh.wwin[warp][1] = best.b2; }
+        __syncthreads();
+        if (warp == 0) {
+            best.clear();
+            if (lane < WARPS) best.merge(sh.wwin[lane][0], sh.wwin[lane][1]);
+#pragma unroll
+            for (int off = WARPS / 2; off >= 1; off >>= 1) best.merge(shfl_xor64(best.b1, off), shfl_xor64(best.b2, off));
+        }
+    };
+    auto put_best = [&](int to) {                         // by a lane of the first warp, after block_best
+        uint64_t* w = cluster.map_shared_rank(&sh.win[rank][0], to);
+        w[0] = best.b1;
+        w[1] = best.b2;
+    };
+
     // ---- pass 1
     for (int b = tid; b < BINS; b += THREADS) sh.hist[b] = 0u;
     if (tid < COARSE) sh.tot[tid] = 0u;                   // the coarse counts, first
@@ -340,8 +642,17 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
     float m2 = -INFINITY, m3 = -INFINITY;                 // top-k: the second and third largest quads' maxima
     int m2_quad = q0;
     const bool online = need_p && !fast_k;
-    const float l2 = fminf(inv_t * LOG2E, 3.4028235e38f);
-    if (online) {
+    const bool race_all = !need_k && mp == 0.f;           // every token is raced as it is read
+    float ref = -INFINITY;                                // race_all: what the warp's sums and keys are relative to
+    if (race_all) {
+        const RaceAll r = online ? race_all_of<true, THREADS>(lrow, q0, q1, whole, a.vocab, T, inv_t, prow)
+                                 : race_all_of<false, THREADS>(lrow, q0, q1, whole, a.vocab, T, inv_t, prow);
+        mx = r.mx;
+        mx_quad = r.mx_quad;
+        zs = r.zs;
+        ref = r.ref;
+        best = r.best;
+    } else if (online) {
         sweep_quads_by(std::integral_constant<int, LOADS1>{}, [&](int qd, const float4& v) {
             const float m4 = max_of(v);
             if (m4 > mx) {
@@ -385,8 +696,8 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
         float z = 0.f;
         if (online) {
             // fixed trees of fp32 sums; infinite maxima end the row below, whatever their sum
-            const float m_cta = t ? composite_x(t) : 0.f;
-            z = mx > -INFINITY && m_cta < INFINITY ? zs * ex2_ftz((mx - m_cta) * l2) : 0.f;
+            const float m_cta = t ? composite_x(t) : 0.f, m_own = race_all ? ref : mx;
+            z = m_own > -INFINITY && m_cta < INFINITY ? zs * ex2_ftz((m_own - m_cta) * l2) : 0.f;
 #pragma unroll
             for (int off = 16; off >= 1; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
             if (lane == 0) sh.wz[warp] = z;
@@ -395,10 +706,15 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
 #pragma unroll
             for (int w = 0; w < WARPS; ++w) z += sh.wz[w];
         }
+        if (race_all) {
+            best.rebase((ref - composite_x(t)) * inv_t);
+            block_best();
+        }
         cluster.barrier_wait(std::move(started));
         if (tid < CLUSTER) {
             *cluster.map_shared_rank(&sh.top[rank], tid) = t;
             *cluster.map_shared_rank(&sh.z[rank], tid) = z;
+            if (race_all) put_best(tid);
         }
     }
     cluster.sync();                                       // also publishes the cleared tables
@@ -428,20 +744,24 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
 
     // ---- cluster-wide reductions; every CTA ends with the same values
     int phase = 0;
-    auto cluster_sum = [&](uint64_t v) -> uint64_t {
+    uint32_t summed = 0;                                  // the counts given with the last sum
+    auto cluster_sum = [&](uint64_t v, uint32_t cnt = 0) -> uint64_t {
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) v += shfl_xor64(v, off);
-        if (lane == 0) sh.wred[warp] = v;
+        cnt = __reduce_add_sync(0xffffffffu, cnt);
+        if (lane == 0) { sh.wred[warp] = v; sh.wlo[warp] = cnt; }
         __syncthreads();
         if (tid < CLUSTER) {
-            uint64_t s = 0;
-            for (int w = 0; w < WARPS; ++w) s += sh.wred[w];
+            uint64_t s = 0, n = 0;
+            for (int w = 0; w < WARPS; ++w) { s += sh.wred[w]; n += sh.wlo[w]; }
             *cluster.map_shared_rank(&sh.slot[phase][rank], tid) = s;
+            *cluster.map_shared_rank(&sh.slot_n[phase][rank], tid) = static_cast<uint32_t>(n);
         }
         cluster.sync();
         uint64_t s = 0;
+        summed = 0;
 #pragma unroll
-        for (int r = 0; r < CLUSTER; ++r) s += sh.slot[phase][r];
+        for (int r = 0; r < CLUSTER; ++r) { s += sh.slot[phase][r]; summed += sh.slot_n[phase][r]; }
         phase ^= 1;
         return s;
     };
@@ -494,95 +814,11 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
         return make_float2(before.x + s.x - v.x, before.y + s.y - v.y);
     };
 
-    // ---- noise and keys
-    uint64_t seed = a.seed, offset = a.offset;
-    if (a.seed_offset) {
-        seed = __ldg(a.seed_offset);
-        offset = __ldg(a.seed_offset + 1);
-    }
-    const uint64_t rr = static_cast<uint64_t>(row) + offset;
-    const PhiloxRow prow = philox_row(static_cast<uint32_t>(rr), static_cast<uint32_t>(rr >> 32), static_cast<uint32_t>(seed),
-                                      static_cast<uint32_t>(seed >> 32));
-    auto noise_of = [&](int col) -> uint32_t {
-        const uint4 w = noise_quad(static_cast<uint32_t>(col) >> 2, prow);
-        const int e = col & 3;
-        return e == 0 ? w.x : e == 1 ? w.y : e == 2 ? w.z : w.w;
-    };
-    auto key32 = [&](float x, uint32_t noise) {
-        // e = -ln u from the exact w = 1 - u where u is near 1, from the hardware logarithm elsewhere
-        const float w = one_minus_u_of(noise);
-        const float e = w < 0.015625f ? w * fmaf(w, fmaf(w, fmaf(w, 0.25f, 0.333333343f), 0.5f), 1.0f)
-                                      : -__logf(__uint2float_rn(2u * (noise >> 9) + 1u) * 5.9604644775390625e-08f);
-        return (x - M) * inv_t - __logf(e);
-    };
-    auto key64 = [&](int col) {
-        const double e = -log1p(-static_cast<double>(one_minus_u_of(noise_of(col))));
-        return (static_cast<double>(__ldg(lrow + col)) - static_cast<double>(M)) / static_cast<double>(T) - log(e);
-    };
-    Best best;
-    best.clear();
-    // The tokens of a quad that are above -inf, raced.  A token can beat the warp's best
-    // `bar` only if 1 - u < e^(z - bar) (since -ln u >= 1 - u), which spares most keys: the quad's smallest
-    // 1 - u against the bound of its largest logit, then each token's; the bound carries a margin of 1e-3.
-    auto race_quad = [&](int qd, const float (&l)[4], float lmax, float bar) {
-        const uint4 w = noise_quad(static_cast<uint32_t>(qd), prow);
-        const float cb = (1e-3f - bar) * LOG2E + 1.4419741739064e-3f;                  // + log2 1.001
-        const uint32_t wmax = max(max(w.x, w.y), max(w.z, w.w));
-        if (one_minus_u_of(wmax) < ex2_ftz(fmaf(lmax - M, l2, cb))) {
-            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (one_minus_u_of(ws[e]) < ex2_ftz(fmaf(l[e] - M, l2, cb))) best.add(composite(key32(l[e], ws[e]), 4 * qd + e));
-        }
-    };
-    auto share_best = [&]() -> float {                    // the warp's best key so far
-        float b;
-        asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(b) : "f"(best.key()));
-        return b;
-    };
-    // the CTA's two best, in the lanes of its first warp
-    auto block_best = [&]() {
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) best.merge(shfl_xor64(best.b1, off), shfl_xor64(best.b2, off));
-        if (lane == 0) { sh.wwin[warp][0] = best.b1; sh.wwin[warp][1] = best.b2; }
-        __syncthreads();
-        if (warp == 0) {
-            best.clear();
-            if (lane < WARPS) best.merge(sh.wwin[lane][0], sh.wwin[lane][1]);
-#pragma unroll
-            for (int off = WARPS / 2; off >= 1; off >>= 1) best.merge(shfl_xor64(best.b1, off), shfl_xor64(best.b2, off));
-        }
-    };
-    // every CTA's two best to the first CTA (the caller's next barrier completes it)
-    auto send_best = [&]() {
-        block_best();
-        if (tid == 0) {
-            uint64_t* to = cluster.map_shared_rank(&sh.win[rank][0], 0);
-            to[0] = best.b1;
-            to[1] = best.b2;
-        }
-    };
-    // adds every CTA's two best; by the first warp, the result in its lanes
-    auto gather_best = [&]() {
-        if (lane < CLUSTER) best.merge(sh.win[lane][0], sh.win[lane][1]);
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) best.merge(shfl_xor64(best.b1, off), shfl_xor64(best.b2, off));
-    };
-    // by one thread
-    auto write_winner = [&]() {
-        int c1 = composite_col(best.b1);
-        if (best.b2 && composite_x(best.b1) - composite_x(best.b2) <= NEAR) {   // too near in fp32
-            const int c2 = composite_col(best.b2);
-            const double d1 = key64(c1), d2 = key64(c2);
-            if (d2 > d1 || (d2 == d1 && c2 < c1)) c1 = c2;
-        }
-        a.out_ids[row] = static_cast<int64_t>(c1);
-    };
+    auto winner = [&]() -> int { return winner_of(best, lrow, M, T, prow); };
 
     // ---- each warp's list of its quads that reach x_min; f(quad, its logits) over the warp's list, 32 at a
     // time.  Order and shares are fixed.  A slice too long for the lists is walked instead.
     constexpr int PER_WARP = LISTED / WARPS;
-    const int iters = (q1 - q0 + THREADS - 1) / THREADS;  // uniform
     const bool listable = iters * 32 <= PER_WARP && q1 - q0 <= 65536;
     int n_quads = 0;
     float listed_x = -INFINITY;
@@ -591,38 +827,17 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
         if (!listable) return;
         n_quads = 0;
         uint16_t* mine = sh.quads + warp * PER_WARP;
-        auto put = [&](int at, const float4& v) {         // quad q0 + at; by whole warps
+        auto put = [&](int qd, const float4& v) {
             const float m = max_of(v);
             const uint32_t in = __ballot_sync(0xffffffffu, m >= x_min && m > -INFINITY);
-            if ((in >> lane) & 1u) mine[n_quads + __popc(in & ((1u << lane) - 1u))] = static_cast<uint16_t>(at);
+            if ((in >> lane) & 1u) mine[n_quads + __popc(in & ((1u << lane) - 1u))] = static_cast<uint16_t>(qd - q0);
             n_quads += __popc(in);
         };
-        const float4 none = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        int i0 = 0;
-        for (; q0 + (i0 + LOADS) * THREADS <= min(q1, whole); i0 += LOADS) {
-            float4 v[LOADS];
-#pragma unroll
-            for (int i = 0; i < LOADS; ++i) v[i] = load_whole(q0 + (i0 + i) * THREADS + tid);
-#pragma unroll
-            for (int i = 0; i < LOADS; ++i) put((i0 + i) * THREADS + tid, v[i]);
-        }
-        for (; i0 < iters; i0 += LOADS) {
-            float4 v[LOADS];
-#pragma unroll
-            for (int i = 0; i < LOADS; ++i) {
-                const int qd = q0 + (i0 + i) * THREADS + tid;
-                v[i] = whole > 0 ? load_whole(min(qd, whole - 1)) : none;
-                if (qd >= q1) v[i] = none;
-                else if (qd >= whole) v[i] = load_quad(qd);
-            }
-#pragma unroll
-            for (int i = 0; i < LOADS; ++i) put((i0 + i) * THREADS + tid, v[i]);
-        }
+        sweep_warps<THREADS, LOADS>(lrow, q0, q1, whole, a.vocab, put);
         __syncwarp();
     };
     // f is called by whole warps (quad -1 and -inf logits for lanes without one)
     auto for_quads = [&](auto f) {
-        const float4 none = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
         if (!listable) {
             for (int i = 0; i < iters; ++i) {
                 const int qd = q0 + i * THREADS + tid;
@@ -666,12 +881,12 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
         *sum = r.sum;
         return r.count;
     };
-    auto goal_of = [&](uint64_t z) { return max(__umul64hi(z, __float2ull_rz(p * 9223372036854775808.f)) << 1, static_cast<unsigned long long>(1)); };
+    auto goal_of = [&](uint64_t z) { return goal_of_sum(z, p); };
     auto race_list = [&](const uint64_t* list, int n) {
         for (int i = tid; i < n; i += THREADS) {
             const uint64_t c = list[i];
             if (composite_x(c) < min_x) break;
-            best.add(composite(key32(composite_x(c), noise_of(composite_col(c))), composite_col(c)));
+            best.add(composite(key_of_token(composite_x(c) - M, inv_t, noise_of(composite_col(c), prow)), composite_col(c)));
         }
     };
 
@@ -721,16 +936,8 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
             if (n <= CAP) {
                 if (rank != 0) return;
                 auto read = cluster.barrier_arrive();     // the others leave once they have read the counter
-                sort_list(sh.list, n);
-                int kept = min(k, n);
-                if (need_p) {
-                    uint64_t sum;
-                    kept_by_weight(sh.list, kept, 0, ~0ull, &sum);
-                    kept = kept_by_weight(sh.list, kept, 0, goal_of(sum), &sum);
-                }
-                race_list(sh.list, kept);
-                block_best();
-                if (tid == 0) write_winner();
+                const int col = list_winner<THREADS>(sh, lrow, n, min(k, n), need_p, 0, p, M, T, inv_t, per_logit, min_x, prow);
+                if (tid == 0) a.out_ids[row] = static_cast<int64_t>(col);
                 cluster.barrier_wait(std::move(read));
                 return;
             }
@@ -815,211 +1022,260 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
         return sh.list_sum;
     };
 
-    if (need_k || need_p) {
-        int k_bin = BINS;                                 // the bin of the last token top-k keeps
-        uint32_t k_left = 0;                              // tokens it keeps in that bin
-        int end = TAIL;                                   // bins that top-p's border can lie in, or that the race reaches
-        if (need_k) {
-            float ws = 0.f;
-            uint32_t tail = 0;
-            sweep_from(-INFINITY, [&](int, float x) {
-                const float d = depth(x);
-                const int b = bin_of(d);
-                if (b == TAIL) ++tail; else atomicAdd(&sh.hist[b], 1u);
-                if (need_p) ws += weight_of(d);
-            });
-            tail = __reduce_add_sync(0xffffffffu, tail);
-            if (lane == 0 && tail) atomicAdd(&sh.hist[TAIL], tail);
-            Z = cluster_sum(fixed_of(ws));
-            cluster_hist();
-            // exact in fp32: the vocabulary is limited to 2^24
-            float2 mine = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int i = 0; i < BINS_PER_THREAD; ++i) mine.x += static_cast<float>(sh.tot[tid * BINS_PER_THREAD + i]);
-            float2 run = scan2(mine);
-            if (tid == 0) { sh.first[0] = BINS; sh.first[1] = 0; }
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < BINS_PER_THREAD; ++i) {
-                const int b = tid * BINS_PER_THREAD + i;
-                const float before = run.x;
-                run.x += static_cast<float>(sh.tot[b]);
-                if (before < static_cast<float>(k) && run.x >= static_cast<float>(k)) {
-                    sh.first[0] = b;
-                    sh.first[1] = k - static_cast<int>(before);
-                }
-            }
-            __syncthreads();
-            k_bin = sh.first[0];
-            k_left = static_cast<uint32_t>(sh.first[1]);
-            __syncthreads();
-            // every token of the tail is out of the race's reach: without top-p its order does not matter
-            if (k_bin < TAIL || (k_bin == TAIL && need_p))
-                Z = select(false, need_p, k_bin, k_bin, sh.tot[k_bin], k_left);
-        } else {
-            // tokens lighter than (1 - p) Z / vocab are outside; the limit in bins, with a margin
-            const float z_f = static_cast<float>(Z) * (1.f / FIX);
-            const float limit = (log2f(static_cast<float>(a.vocab)) - log2f((1.f - p) * z_f)) * BINS_PER_OCTAVE * 1.00001f + 2.f;
-            end = limit < static_cast<float>(TAIL) ? max(1, static_cast<int>(limit)) : TAIL;
-            list_quads(x_at_end_of(end));
-            for_quads([&](int, const float4& v) {
-                const float l[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int b = bin_of(depth(l[e]));
-                    if (b < end) atomicAdd(&sh.hist[b], 1u);
-                }
-            });
-            cluster_hist();
-        }
-        if (need_p) {
-            const uint64_t goal = goal_of(Z);
-            const float goal_f = static_cast<float>(goal) * (1.f / FIX);
-            auto kept_in = [&](int b) { return b < k_bin ? sh.tot[b] : b == k_bin ? k_left : 0u; };   // after top-k
-            // The bins [b_lo, b_hi] in which the running sum may reach what is left of the goal, from counts(b) and
-            // the largest and smallest weight of a bin; thread t holds bins BINS_PER_THREAD t ...; and their members.
-            int b_lo = 0, b_hi = 0;
-            uint32_t n_in = 0;
-            auto find = [&](float left, int last, auto counts, auto weight_at) {
-                float up[BINS_PER_THREAD], dn[BINS_PER_THREAD];
+    // ---- races.  `exact`: `keep` is where the filters end, but for min-p's.  Until then a winner is one of the
+    // filters' if the weights before it are less than the goal, and if it is not, neither is what comes after it.
+    bool exact = !need_k && !need_p;
+    int tries = need_k ? 0 : TRIES;
+    bool raced = race_all;
+    for (;; raced = false) {
+        if (!exact && tries == 0) {
+            keep = 0;
+            best.clear();
+            int k_bin = BINS;                                 // the bin of the last token top-k keeps
+            uint32_t k_left = 0;                              // tokens it keeps in that bin
+            int end = TAIL;                                   // bins that top-p's border can lie in, or that the race reaches
+            if (need_k) {
+                float ws = 0.f;
+                uint32_t tail = 0;
+                sweep_from(-INFINITY, [&](int, float x) {
+                    const float d = depth(x);
+                    const int b = bin_of(d);
+                    if (b == TAIL) ++tail; else atomicAdd(&sh.hist[b], 1u);
+                    if (need_p) ws += weight_of(d);
+                });
+                tail = __reduce_add_sync(0xffffffffu, tail);
+                if (lane == 0 && tail) atomicAdd(&sh.hist[TAIL], tail);
+                Z = cluster_sum(fixed_of(ws));
+                cluster_hist();
+                // exact in fp32: the vocabulary is limited to 2^24
                 float2 mine = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < BINS_PER_THREAD; ++i) mine.x += static_cast<float>(sh.tot[tid * BINS_PER_THREAD + i]);
+                float2 run = scan2(mine);
+                if (tid == 0) { sh.first[0] = BINS; sh.first[1] = 0; }
+                __syncthreads();
 #pragma unroll
                 for (int i = 0; i < BINS_PER_THREAD; ++i) {
                     const int b = tid * BINS_PER_THREAD + i;
-                    const float cnt = static_cast<float>(counts(b));
-                    up[i] = cnt * weight_at(b);
-                    dn[i] = cnt * weight_at(b + 1);
-                    mine.x += up[i];
-                    mine.y += dn[i];
-                }
-                float2 run = scan2(mine);
-                if (tid == 0) sh.first[0] = sh.first[1] = BINS;
-                __syncthreads();
-                const float at_up = left * (1.f - 1e-4f), at_dn = left * (1.f + 1e-4f);
-                // the threads whose sums reach a mark from below it, or from so little above that rounding may be
-                // what put the prefix there
-                int b_up = BINS, b_dn = BINS;
-                const bool mine_up = run.x < at_up * 1.0001f, mine_dn = run.y < at_dn * 1.0001f;
-#pragma unroll
-                for (int i = 0; i < BINS_PER_THREAD; ++i) {
-                    run.x += up[i];
-                    run.y += dn[i];
-                    if (run.x >= at_up) b_up = min(b_up, tid * BINS_PER_THREAD + i);
-                    if (run.y >= at_dn) b_dn = min(b_dn, tid * BINS_PER_THREAD + i);
-                }
-                if (mine_up && b_up < BINS) atomicMin(&sh.first[0], b_up);
-                if (mine_dn && b_dn < BINS) atomicMin(&sh.first[1], b_dn);
-                __syncthreads();
-                b_lo = sh.first[0];
-                b_hi = min(max(b_lo, sh.first[1]), last);
-                n_in = 0;
-                for (int b = b_lo + lane; b <= b_hi; b += 32) n_in += counts(b);
-                n_in = __reduce_add_sync(0xffffffffu, n_in);
-                __syncthreads();
-            };
-            find(goal_f, end - 1, kept_in, [&](int b) { return b > TAIL ? 0.f : weight_of(static_cast<float>(b)); });
-            if (b_lo <= b_hi && !need_k) {
-                // the depths of the range, and what lies above it; a second histogram if the range holds too many
-                float d_lo = static_cast<float>(b_lo), d_hi = static_cast<float>(b_hi + 1), sub = 0.f;
-                const uint32_t n_range = n_in;
-                int s_lo = 0, s_hi = 0;
-                if (n_in > BORDER) {
-                    for (int b = tid; b < BINS; b += THREADS) sh.hist[b] = 0u;
-                    __syncthreads();
-                    sub = static_cast<float>(BINS) / (d_hi - d_lo);
-                    auto sub_of = [&](float d) { return min(static_cast<int>((d - d_lo) * sub), BINS - 1); };
-                    float ws = 0.f;
-                    for_quads([&](int, const float4& v) {
-                        const float l[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float d = depth(l[e]);
-                            if (d < d_lo) ws += weight_of(d);
-                            else if (d < d_hi) atomicAdd(&sh.hist[sub_of(d)], 1u);
-                        }
-                    });
-                    const uint64_t above = cluster_sum(fixed_of(ws));
-                    cluster_hist();
-                    // (a sum that rounding puts past the goal already leaves the first members as the range)
-                    const float left = goal > above ? static_cast<float>(goal - above) * (1.f / FIX) : 0.f;
-                    find(fmaxf(left, 1e-30f), BINS - 1, [&](int b) { return sh.tot[b]; },
-                         [&](int b) { return weight_of(d_lo + static_cast<float>(b) / sub); });
-                    s_lo = b_lo;
-                    s_hi = b_hi;
-                }
-                if (n_in <= BORDER && b_lo <= b_hi) {
-                    // sum and race what is above the range, collect the range
-                    uint64_t* border0 = cluster.map_shared_rank(sh.border, 0);
-                    float ws = 0.f, bar = -INFINITY;
-                    for_quads([&](int qd, const float4& v) {
-                        float l[4] = {v.x, v.y, v.z, v.w}, lmax = -INFINITY;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float d = depth(l[e]);
-                            bool sure = d < d_lo, in = !sure && d < d_hi;
-                            if (in && sub > 0.f) {
-                                const int b = min(static_cast<int>((d - d_lo) * sub), BINS - 1);
-                                sure = b < s_lo;
-                                in = b >= s_lo && b <= s_hi;
-                            }
-                            if (sure) ws += weight_of(d);
-                            if (in) {
-                                const uint32_t at = atomicAdd(n0, 1u);
-                                if (at < BORDER) border0[at] = composite(l[e], 4 * qd + e);
-                            }
-                            if (!(sure && l[e] >= min_x)) l[e] = -INFINITY;
-                            lmax = fmaxf(lmax, l[e]);
-                        }
-                        if (lmax > -INFINITY) race_quad(qd, l, lmax, bar);
-                        bar = share_best();
-                    });
-                    send_best();
-                    const uint64_t above = cluster_sum(fixed_of(ws));
-                    if (rank != 0) return;
-                    const int members = static_cast<int>(min(sh.list_n, static_cast<uint32_t>(BORDER)));     // n_in
-                    sort_list(sh.border, members);
-                    uint64_t sum;
-                    const int kept = kept_by_weight(sh.border, members, above, goal, &sum);
-                    best.clear();
-                    race_list(sh.border, kept);
-                    block_best();
-                    if (warp == 0) {
-                        if (lane != 0) best.clear();      // the border's best counts once
-                        gather_best();
-                        if (lane == 0) write_winner();
+                    const float before = run.x;
+                    run.x += static_cast<float>(sh.tot[b]);
+                    if (before < static_cast<float>(k) && run.x >= static_cast<float>(k)) {
+                        sh.first[0] = b;
+                        sh.first[1] = k - static_cast<int>(before);
                     }
+                }
+                __syncthreads();
+                k_bin = sh.first[0];
+                k_left = static_cast<uint32_t>(sh.first[1]);
+                __syncthreads();
+                // every token of the tail is out of the race's reach: without top-p its order does not matter
+                if (k_bin < TAIL || (k_bin == TAIL && need_p))
+                    Z = select(false, need_p, k_bin, k_bin, sh.tot[k_bin], k_left);
+            } else {
+                // tokens lighter than (1 - p) Z / vocab are outside; the limit in bins, with a margin
+                const float z_f = static_cast<float>(Z) * (1.f / FIX);
+                const float limit = (log2f(static_cast<float>(a.vocab)) - log2f((1.f - p) * z_f)) * BINS_PER_OCTAVE * 1.00001f + 2.f;
+                end = limit < static_cast<float>(TAIL) ? max(1, static_cast<int>(limit)) : TAIL;
+                list_quads(x_at_end_of(end));
+                for_quads([&](int, const float4& v) {
+                    const float l[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int b = bin_of(depth(l[e]));
+                        if (b < end) atomicAdd(&sh.hist[b], 1u);
+                    }
+                });
+                cluster_hist();
+            }
+            if (need_p) {
+                const uint64_t goal = goal_of(Z);
+                const float goal_f = static_cast<float>(goal) * (1.f / FIX);
+                auto kept_in = [&](int b) { return b < k_bin ? sh.tot[b] : b == k_bin ? k_left : 0u; };   // after top-k
+                // The bins [b_lo, b_hi] in which the running sum may reach what is left of the goal, from counts(b) and
+                // the largest and smallest weight of a bin; thread t holds bins BINS_PER_THREAD t ...; and their members.
+                int b_lo = 0, b_hi = 0;
+                uint32_t n_in = 0;
+                auto find = [&](float left, int last, auto counts, auto weight_at) {
+                    float up[BINS_PER_THREAD], dn[BINS_PER_THREAD];
+                    float2 mine = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int i = 0; i < BINS_PER_THREAD; ++i) {
+                        const int b = tid * BINS_PER_THREAD + i;
+                        const float cnt = static_cast<float>(counts(b));
+                        up[i] = cnt * weight_at(b);
+                        dn[i] = cnt * weight_at(b + 1);
+                        mine.x += up[i];
+                        mine.y += dn[i];
+                    }
+                    float2 run = scan2(mine);
+                    if (tid == 0) sh.first[0] = sh.first[1] = BINS;
+                    __syncthreads();
+                    const float at_up = left * (1.f - 1e-4f), at_dn = left * (1.f + 1e-4f);
+                    // the threads whose sums reach a mark from below it, or from so little above that rounding may be
+                    // what put the prefix there
+                    int b_up = BINS, b_dn = BINS;
+                    const bool mine_up = run.x < at_up * 1.0001f, mine_dn = run.y < at_dn * 1.0001f;
+#pragma unroll
+                    for (int i = 0; i < BINS_PER_THREAD; ++i) {
+                        run.x += up[i];
+                        run.y += dn[i];
+                        if (run.x >= at_up) b_up = min(b_up, tid * BINS_PER_THREAD + i);
+                        if (run.y >= at_dn) b_dn = min(b_dn, tid * BINS_PER_THREAD + i);
+                    }
+                    if (mine_up && b_up < BINS) atomicMin(&sh.first[0], b_up);
+                    if (mine_dn && b_dn < BINS) atomicMin(&sh.first[1], b_dn);
+                    __syncthreads();
+                    b_lo = sh.first[0];
+                    b_hi = min(max(b_lo, sh.first[1]), last);
+                    n_in = 0;
+                    for (int b = b_lo + lane; b <= b_hi; b += 32) n_in += counts(b);
+                    n_in = __reduce_add_sync(0xffffffffu, n_in);
+                    __syncthreads();
+                };
+                find(goal_f, end - 1, kept_in, [&](int b) { return b > TAIL ? 0.f : weight_of(static_cast<float>(b)); });
+                if (b_lo <= b_hi && !need_k) {
+                    // the depths of the range, and what lies above it; a second histogram if the range holds too many
+                    float d_lo = static_cast<float>(b_lo), d_hi = static_cast<float>(b_hi + 1), sub = 0.f;
+                    const uint32_t n_range = n_in;
+                    int s_lo = 0, s_hi = 0;
+                    if (n_in > BORDER) {
+                        for (int b = tid; b < BINS; b += THREADS) sh.hist[b] = 0u;
+                        __syncthreads();
+                        sub = static_cast<float>(BINS) / (d_hi - d_lo);
+                        auto sub_of = [&](float d) { return min(static_cast<int>((d - d_lo) * sub), BINS - 1); };
+                        float ws = 0.f;
+                        for_quads([&](int, const float4& v) {
+                            const float l[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float d = depth(l[e]);
+                                if (d < d_lo) ws += weight_of(d);
+                                else if (d < d_hi) atomicAdd(&sh.hist[sub_of(d)], 1u);
+                            }
+                        });
+                        const uint64_t above = cluster_sum(fixed_of(ws));
+                        cluster_hist();
+                        // (a sum that rounding puts past the goal already leaves the first members as the range)
+                        const float left = goal > above ? static_cast<float>(goal - above) * (1.f / FIX) : 0.f;
+                        find(fmaxf(left, 1e-30f), BINS - 1, [&](int b) { return sh.tot[b]; },
+                             [&](int b) { return weight_of(d_lo + static_cast<float>(b) / sub); });
+                        s_lo = b_lo;
+                        s_hi = b_hi;
+                    }
+                    if (n_in <= BORDER && b_lo <= b_hi) {
+                        // sum and race what is above the range, collect the range
+                        uint64_t* border0 = cluster.map_shared_rank(sh.border, 0);
+                        float ws = 0.f, bar = -INFINITY;
+                        for_quads([&](int qd, const float4& v) {
+                            float l[4] = {v.x, v.y, v.z, v.w}, lmax = -INFINITY;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float d = depth(l[e]);
+                                bool sure = d < d_lo, in = !sure && d < d_hi;
+                                if (in && sub > 0.f) {
+                                    const int b = min(static_cast<int>((d - d_lo) * sub), BINS - 1);
+                                    sure = b < s_lo;
+                                    in = b >= s_lo && b <= s_hi;
+                                }
+                                if (sure) ws += weight_of(d);
+                                if (in) {
+                                    const uint32_t at = atomicAdd(n0, 1u);
+                                    if (at < BORDER) border0[at] = composite(l[e], 4 * qd + e);
+                                }
+                                if (!(sure && l[e] >= min_x)) l[e] = -INFINITY;
+                                lmax = fmaxf(lmax, l[e]);
+                            }
+                            if (lmax > -INFINITY) race_quad(best, qd, l, lmax, M, bar, inv_t, l2, noise_quad(static_cast<uint32_t>(qd), prow));
+                            bar = warp_max(best.key());
+                        });
+                        block_best();
+                        if (tid == 0) put_best(0);
+                        const uint64_t above = cluster_sum(fixed_of(ws));
+                        if (rank != 0) return;
+                        const int members = static_cast<int>(min(sh.list_n, static_cast<uint32_t>(BORDER)));     // n_in
+                        sort_list(sh.border, members);
+                        uint64_t sum;
+                        const int kept = kept_by_weight(sh.border, members, above, goal, &sum);
+                        best.clear();
+                        race_list(sh.border, kept);
+                        block_best();
+                        if (warp == 0) {
+                            if (lane != 0) best.clear();      // the border's best counts once
+                            if (lane < CLUSTER) best.merge(sh.win[lane][0], sh.win[lane][1]);
+                            warp_best();
+                            if (lane == 0) a.out_ids[row] = winner();
+                        }
+                        return;
+                    }
+                    // thousands of equal logits at the border: halve it
+                    b_lo = static_cast<int>(d_lo);
+                    b_hi = static_cast<int>(d_hi) - 1;
+                    n_in = n_range;
+                }
+                if (b_lo <= b_hi) select(true, true, b_lo, b_hi, n_in, goal);
+            }
+            exact = true;
+        }
+        if (!raced) {
+            const float x_keep = keep ? composite_x(keep) : -INFINITY, x_from = fmaxf(min_x, x_keep);
+            const uint32_t col_keep = keep ? static_cast<uint32_t>(composite_col(keep)) : 0xffffffffu;    // at x_keep itself: columns up to this
+            float bar = -INFINITY;
+            best.clear();
+            list_quads(x_from);
+            for_quads([&](int qd, const float4& v) {
+                float l[4] = {v.x, v.y, v.z, v.w}, lmax = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (!(l[e] >= x_from && (l[e] > x_keep || static_cast<uint32_t>(4 * qd + e) <= col_keep))) l[e] = -INFINITY;
+                    lmax = fmaxf(lmax, l[e]);
+                }
+                if (lmax > -INFINITY) race_quad(best, qd, l, lmax, M, bar, inv_t, l2, noise_quad(static_cast<uint32_t>(qd), prow));
+                bar = warp_max(best.key());
+            });
+            block_best();
+            if (tid < CLUSTER) put_best(tid);
+            cluster.sync();
+        }
+        // every warp of every CTA: the cluster's two best
+        best.clear();
+        if (lane < CLUSTER) {
+            best.merge(sh.win[lane][0], sh.win[lane][1]);
+            if (raced) best.rebase((composite_x(sh.top[lane]) - M) * inv_t);
+        }
+        warp_best();
+        const int col = winner();
+        if (!exact && col >= 0) {
+            const uint64_t c = composite(__ldg(lrow + col), col);
+            const float x_c = composite_x(c);
+            float ws = 0.f;
+            uint32_t before = 0;
+            sweep_quads_by(std::integral_constant<int, 8>{}, [&](int qd, const float4& v) {
+                if (!(max_of(v) >= x_c)) return;
+                const float l[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (l[e] > x_c || (l[e] == x_c && 4 * qd + e < col)) { ws += weight_of(depth(l[e])); ++before; }
+            });
+            const uint64_t goal = goal_of(Z);
+            if (cluster_sum(fixed_of(ws), before) >= goal) {
+                keep = c + 1;
+                if (summed <= CAP) {                      // the first CTA ends it
+                    sweep_from(x_c, [&](int other, float x) {
+                        if (composite(x, other) > c) collect(composite(x, other));
+                    });
+                    cluster.sync();
+                    if (rank != 0) return;
+                    const int n = static_cast<int>(min(sh.list_n, static_cast<uint32_t>(CAP)));
+                    const int last = list_winner<THREADS>(sh, lrow, n, n, true, goal, p, M, T, inv_t, per_logit, min_x, prow);
+                    if (tid == 0) a.out_ids[row] = static_cast<int64_t>(last);
                     return;
                 }
-                // thousands of equal logits at the border: halve it
-                b_lo = static_cast<int>(d_lo);
-                b_hi = static_cast<int>(d_hi) - 1;
-                n_in = n_range;
+                --tries;
+                continue;
             }
-            if (b_lo <= b_hi) select(true, true, b_lo, b_hi, n_in, goal);
         }
-    }
-
-    // ---- the race over the slices
-    const float x_keep = keep ? composite_x(keep) : -INFINITY, x_from = fmaxf(min_x, x_keep);
-    const uint32_t col_keep = keep ? static_cast<uint32_t>(composite_col(keep)) : 0xffffffffu;    // at x_keep itself: columns up to this
-    float bar = -INFINITY;
-    list_quads(x_from);
-    for_quads([&](int qd, const float4& v) {
-        float l[4] = {v.x, v.y, v.z, v.w}, lmax = -INFINITY;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (!(l[e] >= x_from && (l[e] > x_keep || static_cast<uint32_t>(4 * qd + e) <= col_keep))) l[e] = -INFINITY;
-            lmax = fmaxf(lmax, l[e]);
-        }
-        if (lmax > -INFINITY) race_quad(qd, l, lmax, bar);
-        bar = share_best();
-    });
-    send_best();
-    cluster.sync();
-    if (rank == 0 && warp == 0) {
-        best.clear();
-        gather_best();
-        if (lane == 0) write_winner();
+        if (rank == 0 && tid == 0) a.out_ids[row] = static_cast<int64_t>(col);
+        return;
     }
 }
 
