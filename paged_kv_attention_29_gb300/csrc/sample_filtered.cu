@@ -16,22 +16,29 @@
 // The work below pass 1 is bound by latency (cluster barriers, dependent shared-memory steps), so
 // each kind of row takes the shortest way that is exact for it:
 //
-//   pass 1  every thread's maximum and, for top-p, its sum of weights relative to that maximum;
-//           one exchange gives every CTA the row's first token (top_k = 1 ends here) and the sum Z.
+//   pass 1  every thread's maximum and, for top-p, its sum of weights relative to a maximum; one
+//           exchange gives every CTA the row's first token (top_k = 1 ends here) and the sum Z.
+//           Without top-k and min-p the pass races every token too, so the exchange has the winner.
 //   top-k   (k at most the threads, and 1024.)  A thread keeps its two largest quads of logits and
 //           the third's maximum.  The k-th largest of those quads' maxima bounds the k-th logit
 //           from below: a 128-bin histogram of the maxima gives the bound, and what reaches the
 //           bound (a little over k tokens) is collected from those, rarely by another look at a
-//           thread's share, in the first CTA, which sorts them, cuts them by k, then by p and
-//           min-p, and runs the race.
-//   top-p   A token lighter than (1 - p) Z / vocab is outside (all of those together weigh less
-//           than 1 - p of Z).  Each warp lists its quads that hold others (so the work below runs
-//           on full warps), and those are counted into 2048 bins of 1/64 octave of weight.  A bin's
-//           weights lie within 1.1% of one another, so the counts bound the running sum from both
-//           sides and leave a few bins where it may reach p Z (if they hold too many, they are
-//           counted once more, into 2048 bins of their own).  The tokens above those bins are
-//           summed and raced, the bins' members collected in the first CTA, which sorts them, finds
-//           the border by their running sum and races what is above it.
+//           thread's share, in the first CTA, which ends the row on that list: one warp if it is
+//           short.
+//   top-p   The winner of a race among all tokens that min-p allows is the filters' winner if it is
+//           one of their tokens: if the weights before it in the order sum to less than p Z, one
+//           sweep.  It is with probability p (of the weight min-p allows).  Otherwise it and what
+//           comes after it are out; the tokens before it are collected in the first CTA, which ends
+//           the row, or raced again, if they are more than fit.  Where that fails TRIES times, the
+//           border itself is looked for:
+//   border  A token lighter than (1 - p) Z / vocab is outside (all of those together weigh less
+//           than 1 - p of Z).  Each warp lists its quads that hold others, and those are counted
+//           into 2048 bins of 1/64 octave of weight.  A bin's weights lie within 1.1% of one
+//           another, so the counts bound the running sum from both sides and leave a few bins where
+//           it may reach p Z (if they hold too many, they are counted once more, into 2048 bins of
+//           their own).  The tokens above those bins are summed and raced, the bins' members
+//           collected in the first CTA, which sorts them, finds the border by their running sum and
+//           races what is above it.
 //   else    (a larger k, or more members than fit: a flat row, thousands of equal logits.)  The
 //           same histogram over every token, and the range of candidates halved, by (logit bits,
 //           column), until it fits; the race then sweeps the slices once more.
@@ -41,11 +48,11 @@
 // of a sum (a few dozen weights) is fp32: a running sum is within about 1e-6 of itself, and the token at the border is decided as in
 // exact arithmetic except when a border lies that near to it.
 //
-// Measured on rows of 151,936 logits: 256 rows with settings of their own 110 us (156 MB, 1.4 TB/s; 41% of issue
-// slots), all top-k = 50 62 us, all top-p = 0.9 161 us, no filter 119 us; one row 15, 26 and 17 us (top-p 41 us
-// when its code has to come from DRAM).  What was tried: the slices kept in shared memory (435 us for the mixed
-// rows), one loop for every sweep instead of a batched and a last one (138), clusters of 4 (130), five CTAs to
-// an SM (123), long rows first (124).
+// Measured on rows of 151,936 logits: 256 rows with settings of their own 86 us (156 MB, 1.8 TB/s), all top-k = 50
+// 58 us, all top-p = 0.9 125 us, no filter 78 us; one row 14, 24 and 15 us (top-p 35 us when its code has to come
+// from DRAM).  With the border looked for in every top-p row and lists sorted: 111 us, all top-p 161 us, one 20.5 us.
+// What else was tried: the slices kept in shared memory (435 us for the mixed rows), one loop for every sweep
+// instead of a batched and a last one, five CTAs to an SM, long rows first (all slower).
 //
 // The race's keys are fp32 with an error below 2e-5; when the two best are within 1e-4 they are
 // ranked again in fp64.
@@ -69,6 +76,7 @@ constexpr int COARSE = 128;                  // bins of the threads' maxima, 16 
 constexpr int CAP = 2048;                    // members collected at once
 constexpr int BORDER = 512;                  // of those, around top-p's border
 constexpr int LISTED = 10240;                // quads of a CTA's warps' lists
+constexpr int WARP_LIST = 128;               // members that one warp ends a row with
 constexpr int RANK_MAX = 256;                // members sorted by counting
 constexpr int LOADS = 4;                     // 16-byte loads in flight per thread of a sweep (pass 1, from HBM: LOADS1)
 constexpr int RACE_LOADS = 2;                // and of a race over all tokens
@@ -391,84 +399,90 @@ __device__ __forceinline__ uint64_t goal_of_sum(uint64_t z, float p) {
 
 // The winner among the n members of the list, which begins the row's order: their first `count`, and (by_weight)
 // of those the ones before which the weights sum to less than the goal (goal 0: p of the `count` ones' sum).
-// By every thread of the CTA; each holds its members in registers.  The members are not sorted: the
-// count-th is selected, and a race's winner stands if the weights before it are less than the goal; if they
-// are not, neither it nor what comes after it is a member, and the rest is raced again.
-template <int THREADS>
+// By GROUP threads, a warp or the whole CTA; each holds its share of up to CAPACITY members in registers.  The
+// members are not sorted: the count-th is selected, and a race's winner stands if the weights before it are less
+// than the goal; if they are not, neither it nor what comes after it is a member, and the rest is raced again.
+template <int GROUP, int CAPACITY>
 __device__ __noinline__ int list_winner(Shared& sh, const float* row, int n, int count, bool by_weight, uint64_t goal, float p, float M,
                                         float T, float inv_t, float per_logit, float min_x, PhiloxRow prow) {
-    constexpr int WARPS = THREADS / 32, PER = CAP / THREADS, DIGITS = 256;
+    constexpr int WARPS = GROUP / 32, PER = CAPACITY / GROUP, DIGITS = 256;
+    auto sync = [] { if (WARPS == 1) __syncwarp(); else __syncthreads(); };
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint64_t c[PER], keep = 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) c[i] = tid + i * THREADS < n ? sh.list[tid + i * THREADS] : 0;      // no member's is 0
+    for (int i = 0; i < PER; ++i) c[i] = tid + i * GROUP < n ? sh.list[tid + i * GROUP] : 0;      // no member's is 0
     if (count < n) {
-        uint64_t lo = ~0ull, hi = 0;
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (c[i]) { lo = min(lo, c[i]); hi = max(hi, c[i]); }
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) {
-            lo = min(lo, shfl_xor64(lo, off));
-            hi = max(hi, shfl_xor64(hi, off));
-        }
-        __syncthreads();
-        if (lane == 0) { sh.wlo[warp] = lo; sh.whi[warp] = hi; }
-        __syncthreads();
-        for (int w = 0; w < WARPS; ++w) { lo = min(lo, sh.wlo[w]); hi = max(hi, sh.whi[w]); }
-        // the need-th, from the top, of the `in` members in [lo, hi]; 256 equal parts at a time
+        // the need-th, from the top, of `in` members that are compared with one another
+        const uint64_t* among = sh.list;
         int need = count, in = n;
-        while (in > RANK_MAX) {
-            const int shift = max(0, 56 - __clzll(static_cast<long long>(hi - lo)));
-            if (tid < DIGITS) sh.hist[tid] = 0u;
-            __syncthreads();
+        if (CAPACITY > RANK_MAX && n > RANK_MAX) {
+            uint64_t lo = ~0ull, hi = 0;
 #pragma unroll
             for (int i = 0; i < PER; ++i)
-                if (c[i] >= lo && c[i] <= hi) atomicAdd(&sh.hist[(c[i] - lo) >> shift], 1u);
-            __syncthreads();
-            const int digit = DIGITS - 1 - tid, mine = tid < DIGITS ? static_cast<int>(sh.hist[digit]) : 0;
-            int upto = mine;
+                if (c[i]) { lo = min(lo, c[i]); hi = max(hi, c[i]); }
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int x = __shfl_up_sync(0xffffffffu, upto, off);
-                if (lane >= off) upto += x;
+            for (int off = 16; off >= 1; off >>= 1) {
+                lo = min(lo, shfl_xor64(lo, off));
+                hi = max(hi, shfl_xor64(hi, off));
             }
-            if (lane == 31) sh.wlo[warp] = static_cast<uint64_t>(upto);
-            __syncthreads();
-            for (int w = 0; w < warp; ++w) upto += static_cast<int>(sh.wlo[w]);
-            if (upto - mine < need && upto >= need) { sh.first[0] = digit; sh.first[1] = need - (upto - mine); sh.first[2] = mine; }
-            __syncthreads();
-            lo += static_cast<uint64_t>(sh.first[0]) << shift;
-            hi = min(hi, lo + ((static_cast<uint64_t>(1) << shift) - 1));
-            need = sh.first[1];
-            in = sh.first[2];
-            __syncthreads();
+            sync();
+            if (lane == 0) { sh.wlo[warp] = lo; sh.whi[warp] = hi; }
+            sync();
+            for (int w = 0; w < WARPS; ++w) { lo = min(lo, sh.wlo[w]); hi = max(hi, sh.whi[w]); }
+            // [lo, hi] holds it; 256 equal parts at a time
+            while (in > RANK_MAX) {
+                const int shift = max(0, 56 - __clzll(static_cast<long long>(hi - lo)));
+                if (tid < DIGITS) sh.hist[tid] = 0u;
+                sync();
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+                    if (c[i] >= lo && c[i] <= hi) atomicAdd(&sh.hist[(c[i] - lo) >> shift], 1u);
+                sync();
+                const int digit = DIGITS - 1 - tid, mine = tid < DIGITS ? static_cast<int>(sh.hist[digit]) : 0;
+                int upto = mine;
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const int x = __shfl_up_sync(0xffffffffu, upto, off);
+                    if (lane >= off) upto += x;
+                }
+                if (lane == 31) sh.wlo[warp] = static_cast<uint64_t>(upto);
+                sync();
+                for (int w = 0; w < warp; ++w) upto += static_cast<int>(sh.wlo[w]);
+                if (upto - mine < need && upto >= need) { sh.first[0] = digit; sh.first[1] = need - (upto - mine); sh.first[2] = mine; }
+                sync();
+                lo += static_cast<uint64_t>(sh.first[0]) << shift;
+                hi = min(hi, lo + ((static_cast<uint64_t>(1) << shift) - 1));
+                need = sh.first[1];
+                in = sh.first[2];
+                sync();
+            }
+            if (tid == 0) sh.first[0] = 0;
+            sync();
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (c[i] >= lo && c[i] <= hi) {
+                    const int at = atomicAdd(&sh.first[0], 1);
+                    if (at < RANK_MAX) sh.sorted[at] = c[i];
+                }
+            sync();
+            among = sh.sorted;
         }
-        if (tid == 0) sh.first[0] = 0;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (c[i] >= lo && c[i] <= hi) {
-                const int at = atomicAdd(&sh.first[0], 1);
-                if (at < RANK_MAX) sh.sorted[at] = c[i];
-            }
-        __syncthreads();
-        for (int i = tid; i < in; i += THREADS) {
-            const uint64_t x = sh.sorted[i];
+        for (int i = tid; i < in; i += GROUP) {
+            const uint64_t x = among[i];
             int before = 0;
 #pragma unroll 4
-            for (int j = 0; j < in; ++j) before += sh.sorted[j] > x ? 1 : 0;
+            for (int j = 0; j < in; ++j) before += among[j] > x ? 1 : 0;
             if (before == need - 1) sh.threshold = x;
         }
-        __syncthreads();
+        sync();
         keep = sh.threshold;
     }
     auto block_sum = [&](uint64_t v) -> uint64_t {
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) v += shfl_xor64(v, off);
-        __syncthreads();
+        sync();
         if (lane == 0) sh.wred[warp] = v;
-        __syncthreads();
+        sync();
         v = 0;
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) v += sh.wred[w];
@@ -498,7 +512,7 @@ __device__ __noinline__ int list_winner(Shared& sh, const float* row, int n, int
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) best.merge(shfl_xor64(best.b1, off), shfl_xor64(best.b2, off));
         if (lane == 0) { sh.wwin[warp][0] = best.b1; sh.wwin[warp][1] = best.b2; }
-        __syncthreads();
+        sync();
         best.clear();
         if (lane < WARPS) best.merge(sh.wwin[lane][0], sh.wwin[lane][1]);
 #pragma unroll
@@ -507,9 +521,12 @@ __device__ __noinline__ int list_winner(Shared& sh, const float* row, int n, int
         best.b2 = static_cast<uint64_t>(__shfl_sync(0xffffffffu, static_cast<unsigned long long>(best.b2), 0));
         const int col = winner_of(best, row, M, T, prow);
         if (!by_weight || col < 0) return col;
-        const uint64_t w = composite(__ldg(row + col), col) + 1;
-        if (weights_from(w) < goal) return col;
-        keep = w;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (c[i] && composite_col(c[i]) == col) sh.threshold = c[i];
+        sync();
+        keep = sh.threshold + 1;
+        if (weights_from(keep) < goal) return col;
     }
 }
 
@@ -936,7 +953,11 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
             if (n <= CAP) {
                 if (rank != 0) return;
                 auto read = cluster.barrier_arrive();     // the others leave once they have read the counter
-                const int col = list_winner<THREADS>(sh, lrow, n, min(k, n), need_p, 0, p, M, T, inv_t, per_logit, min_x, prow);
+                int col = 0;
+                if (n > WARP_LIST)
+                    col = list_winner<THREADS, CAP>(sh, lrow, n, min(k, n), need_p, 0, p, M, T, inv_t, per_logit, min_x, prow);
+                else if (warp == 0)
+                    col = list_winner<32, WARP_LIST>(sh, lrow, n, min(k, n), need_p, 0, p, M, T, inv_t, per_logit, min_x, prow);
                 if (tid == 0) a.out_ids[row] = static_cast<int64_t>(col);
                 cluster.barrier_wait(std::move(read));
                 return;
@@ -1266,7 +1287,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
                     cluster.sync();
                     if (rank != 0) return;
                     const int n = static_cast<int>(min(sh.list_n, static_cast<uint32_t>(CAP)));
-                    const int last = list_winner<THREADS>(sh, lrow, n, n, true, goal, p, M, T, inv_t, per_logit, min_x, prow);
+                    const int last = list_winner<THREADS, CAP>(sh, lrow, n, n, true, goal, p, M, T, inv_t, per_logit, min_x, prow);
                     if (tid == 0) a.out_ids[row] = static_cast<int64_t>(last);
                     return;
                 }
@@ -1288,7 +1309,8 @@ struct Rows {
     }
 };
 using FewRows = Rows<16, 512, 5, 1>;
-using ManyRows = Rows<8, 256, 8, 4>;
+using SomeRows = Rows<8, 256, 8, 4>;
+using ManyRows = Rows<4, 256, 8, 4>;
 
 }  // namespace
 
@@ -1302,12 +1324,15 @@ pkv_status launch_sample_filtered(const SampleFilteredArgs& a, int* err, cudaStr
     args.a = a;
     args.vec_ok = (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0 && (a.batch == 1 || a.row_stride % 4 == 0);
     args.err = err;
-    // Up to 9 clusters of 16 CTAs run at once; a row on 16 x 512 threads takes about two thirds of the time it
-    // takes on 8 x 256 (top-p, one row of 151,936: 26 and 40 us), and with more rows than that it is throughput
-    // that counts: 8 x 256 at four CTAs to an SM took 111 us for 256 rows, 4 x 256 took 130, five CTAs to an SM 123.
-    constexpr int kWideRows = 8;
-    const cudaError_t e = a.batch <= kWideRows ? FewRows::launch(args, stream)
-                                               : ManyRows::launch(args, stream);
+    // The more CTAs to a row, the sooner it is done; the fewer, the less of its time goes into their barriers.  7
+    // clusters of 16 x 512 threads run at once, half as many rows as there are SMs on clusters of 8 x 256 (four CTAs to
+    // an SM), as many rows as SMs on clusters of 4.  Rows of 151,936 with settings of their own, us: 8 rows 22 on 16 and
+    // 28 on 8, 10 rows 22 and 28, 12 rows 35 and 29; 77 rows 54 on 8 and 65 on 4, 120 rows 64 and 70, 180 rows 76
+    // and 78, 228 rows 88 and 79, 512 rows 158 and 140 (256 rows without filters 99 and 78).
+    constexpr int kWideRows = 10;
+    const cudaError_t e = a.batch <= kWideRows             ? FewRows::launch(args, stream)
+                          : 4 * a.batch <= 5 * sm_count()  ? SomeRows::launch(args, stream)
+                                                           : ManyRows::launch(args, stream);
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 

@@ -212,3 +212,13 @@ def test_top_p_borders_anywhere_in_a_row(pkv, B):
     p = np.linspace(0.0005, 0.9995, 400)
     for i in range(0, 400, B):
         check(pkv, x.expand(B, -1).contiguous(), 0.9, 0, p[i:i + B], 0.0, offset=i)
+
+
+@pytest.mark.parametrize("B", [40, 200])
+def test_full_vocabulary_in_larger_batches(pkv, B):
+    """Rows of one batch from flat to peaked, with settings that end a row in each of its ways: a race's
+    winner that stands, one that does not with few or with many tokens before it, a border looked for."""
+    x = rows(B, W.VOCAB_QWEN3, 81, 1.0) * torch.logspace(-2, 1, B)[torch.randperm(B, generator=torch.Generator().manual_seed(82))][:, None]
+    more = SETTINGS + [(0, 0.02, 0.0), (0, 0.5, 0.0), (0, 0.5, 0.02), (1000, 0.7, 0.0), (300, 1.0, 0.0)]
+    k, p, m = (np.array([more[i % len(more)][j] for i in range(B)]) for j in range(3))
+    check(pkv, x, np.random.default_rng(83).uniform(0.4, 1.5, B), k, p, m, most_unclear=3)
