@@ -572,12 +572,16 @@ def pkv_sample_dev(logits: torch.Tensor, temperatures: torch.Tensor, seed_offset
 # A step of a small batch takes a few microseconds on the GPU, less than checking and marshalling a
 # call's arguments does with the helpers above; the calls below test every tensor in one expression
 # that passes when all is well (and otherwise hands over to _check for its message), pass raw integers
-# to ctypes and ask for the current device and stream once.
+# to ctypes and ask for the current device and stream once.  A call tests its first tensor for being a
+# CUDA tensor, and _launch all others for being on that one's device.
 # ---------------------------------------------------------------------------
 
+_Tensor = torch.Tensor
+
+
 def _want(t, name, dtype, ndim):
-    """_check, at the cost of a few attribute reads when it passes."""
-    if not (type(t) is torch.Tensor and t.dtype is dtype and t.dim() == ndim and t.is_cuda and t.is_contiguous()):
+    """_check, but for the device, at the cost of a few attribute reads when it passes."""
+    if not (type(t) is _Tensor and t.dtype is dtype and t.ndim == ndim and t.is_contiguous()):
         _check(t, name, dtype, ndim)
 
 
@@ -613,7 +617,7 @@ def _used_on(stream, *tensors):
 
 def _pools_fp8(k_cache, v_cache, k_scale, v_scale):
     """Shape (num_blocks, block_size, num_kv_heads, head_dim) of an 8-bit cache, checked."""
-    _want(k_cache, "k_cache", torch.float8_e4m3fn, 4)
+    _check(k_cache, "k_cache", torch.float8_e4m3fn, 4)
     _want(v_cache, "v_cache", torch.float8_e4m3fn, 4)
     _want(k_scale, "k_scale", torch.float8_e8m0fnu, 3)
     _want(v_scale, "v_scale", torch.float8_e8m0fnu, 3)
@@ -630,7 +634,7 @@ def _pools_fp8(k_cache, v_cache, k_scale, v_scale):
 def _rows(t, name, n, heads, d):
     """Rows [n, heads, d] that are contiguous within a token; returns the elements between tokens (a single
     token's own stride is meaningless, so its length)."""
-    if not (type(t) is torch.Tensor and t.dtype is torch.bfloat16 and t.dim() == 3 and t.is_cuda):
+    if not (type(t) is _Tensor and t.dtype is torch.bfloat16 and t.ndim == 3):
         _check(t, name, torch.bfloat16, 3, contiguous=False)
     token, head, element = t.stride()
     if t.shape != (n, heads, d) or element != 1 or (heads > 1 and head != d):
@@ -674,7 +678,8 @@ def pkv_rope_store_kvcache_fp8(q: Optional[torch.Tensor], k: torch.Tensor, v: to
         head = (None, 0, None, 0)
         hq = 0
     else:
-        _check(q, "q", torch.bfloat16, 3, contiguous=False)
+        if not (type(q) is _Tensor and q.ndim == 3):
+            _check(q, "q", torch.bfloat16, 3, contiguous=False)
         hq = q.shape[1]
         qs = _rows(q, "q", n, hq, d)
         if q_out is None:
@@ -723,7 +728,7 @@ def pkv_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     if out.shape != (batch, hq, d):
         raise ValueError("out must have q's shape")
     if workspace is None:
-        workspace = own_ws = decode_fp8_workspace(batch, hq, hkv, d, q.device)
+        workspace = own_ws = decode_fp8_workspace(batch, hq, hkv, d, k_cache.device)
     _want(workspace, "workspace", torch.uint8, 1)
     _launch("pkv_decode_fp8", load().pkv_decode_fp8, stream,
             (q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, out, workspace),
@@ -775,7 +780,7 @@ def pkv_prefill_varlen_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
     if out.shape != (total_q, hq, d):
         raise ValueError("out must have q's shape")
     if workspace is None:
-        workspace = own_ws = prefill_fp8_workspace(num_seqs, hq, hkv, d, max_seqlen_q, max_seqlen_k, total_k, q.device)
+        workspace = own_ws = prefill_fp8_workspace(num_seqs, hq, hkv, d, max_seqlen_q, max_seqlen_k, total_k, k_cache.device)
     _want(workspace, "workspace", torch.uint8, 1)
     _launch("pkv_prefill_varlen_fp8", load().pkv_prefill_varlen_fp8, stream,
             (q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, cu_seqlens_k, block_tables, out, workspace),
@@ -792,7 +797,7 @@ def pkv_prefill_varlen_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
 # ---------------------------------------------------------------------------
 
 def _sample_filtered(name, logits, temperatures, top_k, top_p, min_p, noise, out_ids, stream):
-    if not (type(logits) is torch.Tensor and logits.dtype is torch.float32 and logits.dim() == 2 and logits.is_cuda):
+    if not (type(logits) is _Tensor and logits.dtype is torch.float32 and logits.ndim == 2 and logits.is_cuda):
         _check(logits, "logits", torch.float32, 2, contiguous=False)
     batch, vocab = logits.shape
     row, element = logits.stride()

@@ -600,3 +600,23 @@ def test_a_serving_run_on_the_8_bit_cache(pkv):
         assert np.array_equal(ids.cpu().numpy()[clear], ref[clear]) and clear.sum() >= 2
         done = ctx
     expect_no_device_error(pkv)
+
+
+def test_a_tensor_on_another_device_is_refused_wherever_it_is(pkv):
+    c = Cache([40], 2, seed=91)
+    k, v, ks, vs = c.gpu()
+    bt, ln = torch.from_numpy(c.tables).cuda(), torch.from_numpy(c.kv_lens).cuda()
+    q, kv = randn_bf16((1, 4, D), 92).cuda(), randn_bf16((1, 2, D), 93).cuda()
+    one, cu_q, cu_k = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.tensor([0, 1]).int().cuda(), torch.tensor([0, 40]).int().cuda()
+    logits, row = torch.zeros(1, 9, device="cuda"), torch.ones(1, device="cuda")
+    calls = [(pkv.pkv_store_kvcache_fp8, [kv, kv, one, k, v, ks, vs], []),
+             (pkv.pkv_rope_store_kvcache_fp8, [q, kv, kv, one, one, k, v, ks, vs], [1e4]),
+             (pkv.pkv_decode_fp8, [q, k, v, ks, vs, bt, ln], [40, 0.1]),
+             (pkv.pkv_prefill_varlen_fp8, [q, k, v, ks, vs, cu_q, cu_k, bt], [1, 40, 40, 0.1]),
+             (pkv.pkv_sample_filtered, [logits, row, one, row, row], [1])]
+    for f, tensors, rest in calls:
+        f(*tensors, *rest)
+        for i in range(len(tensors)):
+            with pytest.raises(ValueError):
+                f(*(t.cpu() if j == i else t for j, t in enumerate(tensors)), *rest)
+    expect_no_device_error(pkv)
