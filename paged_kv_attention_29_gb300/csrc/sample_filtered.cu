@@ -25,12 +25,14 @@
 //           bound (a little over k tokens) is collected from those, rarely by another look at a
 //           thread's share, in the first CTA, which ends the row on that list: one warp if it is
 //           short.
-//   top-p   The winner of a race among all tokens that min-p allows is the filters' winner if it is
-//           one of their tokens: if the weights before it in the order sum to less than p Z, one
-//           sweep.  It is with probability p (of the weight min-p allows).  Otherwise it and what
-//           comes after it are out; the tokens before it are collected in the first CTA, which ends
-//           the row, or raced again, if they are more than fit.  Where that fails TRIES times, the
-//           border itself is looked for:
+//   top-p   A token that wins a race among all that min-p allows is the filters' winner if it is one
+//           of their tokens: if the weights before it in the order sum to less than p Z.  If it is
+//           not, it and what comes after it are out, and the race's next token is the candidate, so
+//           long as it is known: every warp brings its two best.  One sweep sums the weights before
+//           the best CANDS tokens (one of them is in with probability 1 - (1 - p)^CANDS; a single
+//           row, for which the wait counts, examines one).  If none is, the tokens before them are
+//           collected in the first CTA, which ends the row, or raced again, if they are more than
+//           fit.  Where that fails TRIES times, the border itself is looked for:
 //   border  A token lighter than (1 - p) Z / vocab is outside (all of those together weigh less
 //           than 1 - p of Z).  Each warp lists its quads that hold others, and those are counted
 //           into 2048 bins of 1/64 octave of weight.  A bin's weights lie within 1.1% of one
@@ -48,11 +50,15 @@
 // of a sum (a few dozen weights) is fp32: a running sum is within about 1e-6 of itself, and the token at the border is decided as in
 // exact arithmetic except when a border lies that near to it.
 //
-// Measured on rows of 151,936 logits: 256 rows with settings of their own 86 us (156 MB, 1.8 TB/s), all top-k = 50
-// 58 us, all top-p = 0.9 125 us, no filter 78 us; one row 14, 24 and 15 us (top-p 35 us when its code has to come
-// from DRAM).  With the border looked for in every top-p row and lists sorted: 111 us, all top-p 161 us, one 20.5 us.
-// What else was tried: the slices kept in shared memory (435 us for the mixed rows), one loop for every sweep
-// instead of a batched and a last one, five CTAs to an SM, long rows first (all slower).
+// Rows that cannot all run at once are taken in an order that starts the longest first (row_in_order).
+//
+// Measured on rows of 151,936 logits: 256 rows with settings of their own 80 us (156 MB, 1.9 TB/s; over sixteen
+// seeds 90 on average and 109 at most), all top-k = 50 62 us, all top-p = 0.9 127 us, no filter 82 us; one row 14,
+// 16 and 14 us (top-p 18 us when its code has to come from DRAM).  The same batch of 256 before: with the border
+// looked for in every top-p row and lists sorted 111 us; with one candidate examined 105 us on average and 179 at
+// most; with rows in their own order 94.  What else was tried: the slices kept in shared memory (435 us), one loop
+// for every sweep instead of a batched and a last one, five CTAs to an SM, a repeated race by only those warps
+// whose best tokens are out, the last rows on larger clusters beside the others (all slower).
 //
 // The race's keys are fp32 with an error below 2e-5; when the two best are within 1e-4 they are
 // ranked again in fp64.
@@ -80,11 +86,13 @@ constexpr int WARP_LIST = 128;               // members that one warp ends a row
 constexpr int RANK_MAX = 256;                // members sorted by counting
 constexpr int LOADS = 4;                     // 16-byte loads in flight per thread of a sweep (pass 1, from HBM: LOADS1)
 constexpr int RACE_LOADS = 2;                // and of a race over all tokens
+constexpr int CHECK_LOADS = 8;               // and of the check of a race's winner
 constexpr int MAX_CLUSTER = 16;
 constexpr float BINS_PER_OCTAVE = 64.f;
 constexpr float RACE_Z = 19.6f;              // reach of the race (see above): 28.3 octaves, inside the fine bins
+constexpr int CANDS = 3;                     // best tokens of a race that are examined, at most (TRIED)
 constexpr float REF_REACH = 32.f;            // how far a race's reference may lie below a logit, in units of T
-constexpr int TRIES = 3;                     // winners of top-p races examined before the border is looked for
+constexpr int TRIES = 6;                     // winners of top-p races examined before the border is looked for
 constexpr float NEAR = 1e-4f;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float FIX = 274877906944.f;        // 2^38: a weight of 1 in fixed point
@@ -96,7 +104,10 @@ struct Shared {
         uint64_t list[CAP];      // first CTA: members, as composites
         uint16_t quads[LISTED];  // top-p and races: each warp's quads, from the slice's first
     };
-    uint64_t border[BORDER];     // first CTA, top-p: members
+    union {
+        uint64_t border[BORDER];                     // first CTA, top-p: members
+        uint64_t parts[MAX_CLUSTER * 8][2];          // races: the two best of every part
+    };
     uint64_t sorted[RANK_MAX];
     uint64_t slot[2][MAX_CLUSTER];             // cluster-wide sums and counts, alternating
     uint32_t slot_n[2][MAX_CLUSTER];
@@ -104,7 +115,16 @@ struct Shared {
     uint64_t top[MAX_CLUSTER];   // pass 1: first token of each CTA, and its sum of weights relative to it
     float z[MAX_CLUSTER];
     float wz[32];                // per warp
-    uint64_t win[MAX_CLUSTER][2];   // race: the two best of each CTA
+    uint64_t win[MAX_CLUSTER][2];   // border: the two best of each CTA
+    uint64_t lists[MAX_CLUSTER][CANDS + 1];
+    int list_part[MAX_CLUSTER][CANDS + 1];
+    uint64_t cand[CANDS + 1];       // the race's best, in the order of their keys, with their parts and logits
+    int cand_part[CANDS + 1];
+    float cand_x[CANDS];
+    uint64_t cand_at[CANDS];        // their places in the row's order
+    uint64_t wsum[32][CANDS];       // weights before each of them: per warp, per CTA
+    uint64_t csum[MAX_CLUSTER][CANDS];
+    uint32_t ccnt[MAX_CLUSTER];
     uint64_t threshold;
     uint64_t list_sum;
     uint64_t wred[32];           // per warp
@@ -138,6 +158,12 @@ __device__ __forceinline__ uint64_t fixed_of(float w) { return __float2ull_rn(w 
 
 __device__ __forceinline__ uint64_t shfl_xor64(uint64_t v, int off) {
     return static_cast<uint64_t>(__shfl_xor_sync(0xffffffffu, static_cast<unsigned long long>(v), off));
+}
+
+__device__ __forceinline__ uint64_t warp_max64(uint64_t v) {
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(v >> 32));
+    const uint32_t lo = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
+    return (static_cast<uint64_t>(hi) << 32) | lo;
 }
 
 // The two best of a race, as composites of key and column (larger key first, then lower column); 0: none.
@@ -267,18 +293,27 @@ __device__ __forceinline__ float key_of_token(float d, float inv_t, uint32_t noi
 
 // The tokens of a quad that are above -inf, raced, with keys relative to `base`.  A token can beat the warp's
 // best `bar` only if 1 - u < e^(z - bar) (since -ln u >= 1 - u), which spares most keys: the quad's smallest
-// 1 - u against the bound of its largest logit, then each token's; the bound carries a margin of 1e-3.
-__device__ __forceinline__ void race_quad(Best& best, int qd, const float (&l)[4], float lmax, float base, float bar, float inv_t,
+// 1 - u against the bound of its largest logit, then each token's; the bound carries a margin of 1e-3.  False:
+// nothing was added.
+__device__ __forceinline__ bool race_quad(Best& best, int qd, const float (&l)[4], float lmax, float base, float bar, float inv_t,
                                           float l2, const uint4& w) {
     const float cb = (1e-3f - bar) * LOG2E + 1.4419741739064e-3f;                      // + log2 1.001
     const uint32_t wmax = max(max(w.x, w.y), max(w.z, w.w));
-    if (one_minus_u_of(wmax) < ex2_ftz(fmaf(lmax - base, l2, cb))) {
+    const bool any = one_minus_u_of(wmax) < ex2_ftz(fmaf(lmax - base, l2, cb));
+    if (any) {
         const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             if (one_minus_u_of(ws[e]) < ex2_ftz(fmaf(l[e] - base, l2, cb)))
                 best.add(composite(key_of_token(l[e] - base, inv_t, ws[e]), 4 * qd + e));
     }
+    return any;
+}
+
+// A key that at least two tokens of the warp reach: what is pruned against it is not among the warp's two best.
+__device__ __forceinline__ float warp_second(const Best& best) {
+    const float k1 = best.key(), m = warp_max(k1);
+    return warp_max(k1 == m ? (best.b2 ? composite_x(best.b2) : -INFINITY) : k1);
 }
 
 // Whole quads are one aligned 16-byte load; absent columns and NaN read as -inf.
@@ -334,7 +369,7 @@ struct RaceAll {
     float mx, zs, ref;
     int mx_quad;
 };
-template <bool kSum, int THREADS>
+template <bool kSum, bool kTwo, int THREADS>
 __device__ __noinline__ RaceAll race_all_of(const float* row, int q0, int q1, int whole, int vocab, float T, float inv_t,
                                             PhiloxRow prow) {
     RaceAll r;
@@ -363,11 +398,32 @@ __device__ __noinline__ RaceAll race_all_of(const float* row, int q0, int q1, in
                 r.zs += (ex2_ftz((v.x - r.ref) * l2) + ex2_ftz((v.y - r.ref) * l2)) +
                         (ex2_ftz((v.z - r.ref) * l2) + ex2_ftz((v.w - r.ref) * l2));
             const float l[4] = {v.x, v.y, v.z, v.w};
-            race_quad(r.best, qd, l, m4, r.ref, bar, inv_t, l2, philox_row_at<false>(static_cast<uint32_t>(qd), prow, unused));
-            bar = warp_max(r.best.key());
+            const uint4 w = philox_row_at<false>(static_cast<uint32_t>(qd), prow, unused);
+            const bool any = race_quad(r.best, qd, l, m4, r.ref, bar, inv_t, l2, w);
+            if (!kTwo) bar = warp_max(r.best.key());
+            else if (__any_sync(0xffffffffu, any)) bar = warp_second(r.best);
         }
     });
     return r;
+}
+
+// A quad's weights added to the sums of those that come before each candidate, and its tokens before `top_c` counted.
+struct Before {
+    float w[CANDS];
+    uint32_t count;
+};
+__device__ __noinline__ Before add_before(Before s, const Shared& sh, float4 v, int qd, float M, float per_logit, uint64_t top_c) {
+    const float l[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint64_t c = composite(l[e], 4 * qd + e);
+        const float w = weight_of((M - l[e]) * per_logit);
+#pragma unroll
+        for (int j = 0; j < CANDS; ++j)
+            if (c > sh.cand_at[j]) s.w[j] += w;
+        if (c > top_c) ++s.count;
+    }
+    return s;
 }
 
 __device__ __forceinline__ uint32_t noise_of(int col, const PhiloxRow& prow) {
@@ -533,22 +589,63 @@ __device__ __noinline__ int list_winner(Shared& sh, const float* row, int n, int
 struct Args {
     SampleFilteredArgs a;
     int vec_ok;
+    int ordered;             // rows that take long first
     int* err;
 };
 
-template <int CLUSTER, int THREADS, int LOADS1, int MIN_CTAS>
+// The row that the i-th cluster takes where rows do not all run at once: those that take long first, so that the
+// batch does not end with one of them: without top-k and with top-p, without both, with a large k, a small one, 1.
+constexpr int ORDERED_ROWS = 4095;           // counted in 12 bits each
+template <int THREADS>
+__device__ __noinline__ int row_in_order(Shared& sh, const SampleFilteredArgs& a, int i) {
+    constexpr int WARPS = THREADS / 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    auto field = [&](int b) {
+        const int k = a.top_k ? __ldg(a.top_k + b) : 0;
+        const float p = a.top_p ? __ldg(a.top_p + b) : 1.f;
+        if (k <= 0 || k >= a.vocab) return p < 1.f ? 0 : 12;
+        return k > WARP_LIST ? 24 : k > 1 ? 36 : 48;
+    };
+    const int per = (a.batch + THREADS - 1) / THREADS, b0 = tid * per, b1 = min(a.batch, b0 + per);
+    uint64_t mine = 0;
+    for (int b = b0; b < b1; ++b) mine += static_cast<uint64_t>(1) << field(b);
+    uint64_t upto = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const uint64_t x = static_cast<uint64_t>(__shfl_up_sync(0xffffffffu, static_cast<unsigned long long>(upto), off));
+        if (lane >= off) upto += x;
+    }
+    if (lane == 31) sh.wred[warp] = upto;
+    __syncthreads();
+    uint64_t all = 0;
+    for (int w = 0; w < WARPS; ++w) {
+        if (w < warp) upto += sh.wred[w];
+        all += sh.wred[w];
+    }
+    int f = 0;
+    for (; f < 48 && i >= static_cast<int>((all >> f) & 4095u); f += 12) i -= static_cast<int>((all >> f) & 4095u);
+    i -= static_cast<int>(((upto - mine) >> f) & 4095u);
+    if (i >= 0 && i < static_cast<int>((mine >> f) & 4095u))
+        for (int b = b0; b < b1; ++b)
+            if (field(b) == f && i-- == 0) sh.first[2] = b;
+    __syncthreads();
+    return sh.first[2];
+}
+
+template <int CLUSTER, int THREADS, int LOADS1, int MIN_CTAS, int TRIED>
 __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_CTAS) sample_filtered_kernel(const Args args) {
     constexpr int WARPS = THREADS / 32;
     constexpr int BINS_PER_THREAD = BINS / THREADS;
     constexpr int BINS_PER_RANK = BINS / CLUSTER;
     constexpr int FAST_K = CLUSTER * THREADS < CAP / 2 ? CLUSTER * THREADS : CAP / 2;
-    static_assert(BINS % THREADS == 0 && CLUSTER <= MAX_CLUSTER && CLUSTER <= WARPS && WARPS <= 32 && COARSE <= THREADS, "tables fit");
+    static_assert(BINS % THREADS == 0 && CLUSTER <= MAX_CLUSTER && CLUSTER <= WARPS && WARPS <= 32 && TRIED <= CANDS &&
+                      CLUSTER * (TRIED > 1 ? WARPS : 1) <= MAX_CLUSTER * 8 && COARSE <= THREADS, "tables fit");
     const SampleFilteredArgs& a = args.a;
     __shared__ Shared sh;
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = static_cast<int>(cluster.block_rank());
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int row = blockIdx.y;
+    const int row = args.ordered ? row_in_order<THREADS>(sh, a, blockIdx.y) : static_cast<int>(blockIdx.y);
 
     const float T = __ldg(a.temperatures + row);
     const int k = a.top_k ? __ldg(a.top_k + row) : 0;
@@ -649,6 +746,17 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
         w[0] = best.b1;
         w[1] = best.b2;
     };
+    // what the race's best are taken from, to every CTA
+    constexpr int PUT = TRIED > 1 ? WARPS : 1;            // parts of a CTA whose two best are known
+    auto gather_best = [&]() {
+        if (PUT == 1) block_best();
+        else warp_best();
+        if (PUT == 1 ? tid < CLUSTER : lane < CLUSTER) {
+            uint64_t* w = cluster.map_shared_rank(&sh.parts[rank * PUT + (PUT == 1 ? 0 : warp)][0], lane);
+            w[0] = best.b1;
+            w[1] = best.b2;
+        }
+    };
 
     // ---- pass 1
     for (int b = tid; b < BINS; b += THREADS) sh.hist[b] = 0u;
@@ -662,8 +770,8 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
     const bool race_all = !need_k && mp == 0.f;           // every token is raced as it is read
     float ref = -INFINITY;                                // race_all: what the warp's sums and keys are relative to
     if (race_all) {
-        const RaceAll r = online ? race_all_of<true, THREADS>(lrow, q0, q1, whole, a.vocab, T, inv_t, prow)
-                                 : race_all_of<false, THREADS>(lrow, q0, q1, whole, a.vocab, T, inv_t, prow);
+        const RaceAll r = online ? race_all_of<true, (TRIED > 1), THREADS>(lrow, q0, q1, whole, a.vocab, T, inv_t, prow)
+                                 : race_all_of<false, false, THREADS>(lrow, q0, q1, whole, a.vocab, T, inv_t, prow);
         mx = r.mx;
         mx_quad = r.mx_quad;
         zs = r.zs;
@@ -723,15 +831,12 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
 #pragma unroll
             for (int w = 0; w < WARPS; ++w) z += sh.wz[w];
         }
-        if (race_all) {
-            best.rebase((ref - composite_x(t)) * inv_t);
-            block_best();
-        }
+        if (race_all) best.rebase((ref - composite_x(t)) * inv_t);
         cluster.barrier_wait(std::move(started));
+        if (race_all) gather_best();
         if (tid < CLUSTER) {
             *cluster.map_shared_rank(&sh.top[rank], tid) = t;
             *cluster.map_shared_rank(&sh.z[rank], tid) = z;
-            if (race_all) put_best(tid);
         }
     }
     cluster.sync();                                       // also publishes the cleared tables
@@ -1250,67 +1355,158 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
                     if (!(l[e] >= x_from && (l[e] > x_keep || static_cast<uint32_t>(4 * qd + e) <= col_keep))) l[e] = -INFINITY;
                     lmax = fmaxf(lmax, l[e]);
                 }
-                if (lmax > -INFINITY) race_quad(best, qd, l, lmax, M, bar, inv_t, l2, noise_quad(static_cast<uint32_t>(qd), prow));
-                bar = warp_max(best.key());
+                bool any = false;
+                if (lmax > -INFINITY) any = race_quad(best, qd, l, lmax, M, bar, inv_t, l2, noise_quad(static_cast<uint32_t>(qd), prow));
+                if (__any_sync(0xffffffffu, any)) bar = TRIED > 1 ? warp_second(best) : warp_max(best.key());
             });
-            block_best();
-            if (tid < CLUSTER) put_best(tid);
+            gather_best();
             cluster.sync();
         }
-        // every warp of every CTA: the cluster's two best
-        best.clear();
-        if (lane < CLUSTER) {
-            best.merge(sh.win[lane][0], sh.win[lane][1]);
-            if (raced) best.rebase((composite_x(sh.top[lane]) - M) * inv_t);
+        // the race's best tokens: the best of 32 by a warp each, of those by the first
+        constexpr int LISTS = CLUSTER * PUT * 2 / 32, EACH = (LISTS * (TRIED + 1) + 31) / 32;
+        const int wanted = exact ? 2 : TRIED + 1;
+        if (warp < LISTS) {
+            const int at = warp * 32 + lane;
+            uint64_t e = sh.parts[at >> 1][at & 1];
+            if (raced && e) e = composite(composite_x(e) + (composite_x(sh.top[at / (2 * PUT)]) - M) * inv_t, composite_col(e));
+#pragma unroll 1
+            for (int j = 0; j < wanted; ++j) {
+                const uint64_t m = warp_max64(e);
+                if (e == m) {
+                    (LISTS > 1 ? sh.lists[warp] : sh.cand)[j] = m;
+                    (LISTS > 1 ? sh.list_part[warp] : sh.cand_part)[j] = at >> 1;
+                    e = 0;
+                }
+            }
         }
-        warp_best();
-        const int col = winner();
-        if (!exact && col >= 0) {
-            const uint64_t c = composite(__ldg(lrow + col), col);
-            const float x_c = composite_x(c);
-            float ws = 0.f;
-            uint32_t before = 0;
-            sweep_quads_by(std::integral_constant<int, 8>{}, [&](int qd, const float4& v) {
-                if (!(max_of(v) >= x_c)) return;
-                const float l[4] = {v.x, v.y, v.z, v.w};
+        if (LISTS > 1) __syncthreads();
+        else __syncwarp();
+        if (warp == 0) {
+            if (LISTS > 1) {
+                uint64_t e[EACH];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (l[e] > x_c || (l[e] == x_c && 4 * qd + e < col)) { ws += weight_of(depth(l[e])); ++before; }
+                for (int i = 0; i < EACH; ++i) {
+                    const int at = i * 32 + lane;
+                    e[i] = at < LISTS * (TRIED + 1) && at % (TRIED + 1) < wanted ? sh.lists[at / (TRIED + 1)][at % (TRIED + 1)] : 0;
+                }
+#pragma unroll 1
+                for (int j = 0; j < wanted; ++j) {
+                    uint64_t m = e[0];
+#pragma unroll
+                    for (int i = 1; i < EACH; ++i) m = max(m, e[i]);
+                    m = warp_max64(m);
+                    if (lane == 0) sh.cand[j] = m;
+#pragma unroll
+                    for (int i = 0; i < EACH; ++i)
+                        if (m && e[i] == m) {
+                            e[i] = 0;
+                            sh.cand_part[j] = sh.list_part[(i * 32 + lane) / (TRIED + 1)][(i * 32 + lane) % (TRIED + 1)];
+                        }
+                }
+                __syncwarp();
+            }
+            if (lane < CANDS && !exact) {
+                const int col = composite_col(sh.cand[lane]);
+                const float x = lane < TRIED && sh.cand[lane] ? __ldg(lrow + col) : -INFINITY;
+                sh.cand_x[lane] = x;
+                sh.cand_at[lane] = x > -INFINITY ? composite(x, col) : ~0ull;
+            }
+        }
+        __syncthreads();
+        int first = 0, next = 1;                          // the first candidate that stands, and the next
+        if (!exact) {
+            float x_low = INFINITY;
+            uint64_t top_c = 0;                           // the candidate that comes first in the order
+#pragma unroll 1
+            for (int j = 0; j < TRIED && sh.cand[j]; ++j) {
+                x_low = fminf(x_low, sh.cand_x[j]);
+                top_c = max(top_c, sh.cand_at[j]);
+            }
+            Before sums = {};                             // before each of them; and the tokens before that one
+            sweep_quads_by(std::integral_constant<int, CHECK_LOADS>{}, [&](int qd, const float4& v) {
+                if (max_of(v) >= x_low) sums = add_before(sums, sh, v, qd, M, per_logit, top_c);
             });
+            const uint32_t before = __reduce_add_sync(0xffffffffu, sums.count);
+#pragma unroll
+            for (int j = 0; j < TRIED; ++j) {
+                uint64_t f = fixed_of(sums.w[j]);
+#pragma unroll
+                for (int off = 16; off >= 1; off >>= 1) f += shfl_xor64(f, off);
+                if (lane == 0) sh.wsum[warp][j] = f;
+            }
+            if (lane == 0) sh.wlo[warp] = before;
+            __syncthreads();
+            if (tid < CLUSTER * TRIED) {
+                const int to = tid / TRIED, j = tid % TRIED;
+                uint64_t f = 0, n = 0;
+                for (int w = 0; w < WARPS; ++w) { f += sh.wsum[w][j]; n += sh.wlo[w]; }
+                *cluster.map_shared_rank(&sh.csum[rank][j], to) = f;
+                if (j == 0) *cluster.map_shared_rank(&sh.ccnt[rank], to) = static_cast<uint32_t>(n);
+            }
+            cluster.sync();
             const uint64_t goal = goal_of(Z);
-            if (cluster_sum(fixed_of(ws), before) >= goal) {
-                keep = c + 1;
-                if (summed <= CAP) {                      // the first CTA ends it
-                    sweep_from(x_c, [&](int other, float x) {
-                        if (composite(x, other) > c) collect(composite(x, other));
+            uint64_t out = 0;                             // the excluded candidate that comes first in the order
+            bool known = true;                            // no part had both of its two best excluded
+            int stands[2] = {-1, -1};
+#pragma unroll 1
+            for (int j = 0; j < TRIED && sh.cand[j]; ++j) {
+                uint64_t f = 0;
+#pragma unroll
+                for (int r = 0; r < CLUSTER; ++r) f += sh.csum[r][j];
+                if (f < goal) {
+                    if (stands[0] < 0) stands[0] = j;
+                    else if (stands[1] < 0) stands[1] = j;
+                } else if (stands[0] < 0) {
+                    for (int i = 0; i < j; ++i) known = known && sh.cand_part[i] != sh.cand_part[j];
+                    out = max(out, sh.cand_at[j]);
+                }
+            }
+            first = stands[0];
+            next = stands[1] < 0 ? TRIED + 1 : stands[1];
+            // none stands, or a token of a part whose two best are out might beat it: race again what is left; or one
+            // that was not examined is too near it: the border decides
+            const bool near = first >= 0 && stands[1] < 0 && sh.cand[TRIED] &&
+                              composite_x(sh.cand[first]) - composite_x(sh.cand[TRIED]) <= NEAR;
+            if (first < 0 || !known || near) {
+                uint32_t n = 0;
+                for (int r = 0; r < CLUSTER; ++r) n += sh.ccnt[r];
+                keep = out + 1;
+                if (out == top_c && n <= CAP) {           // the first CTA ends it
+                    sweep_from(composite_x(out), [&](int other, float x) {
+                        if (composite(x, other) > out) collect(composite(x, other));
                     });
                     cluster.sync();
                     if (rank != 0) return;
-                    const int n = static_cast<int>(min(sh.list_n, static_cast<uint32_t>(CAP)));
-                    const int last = list_winner<THREADS, CAP>(sh, lrow, n, n, true, goal, p, M, T, inv_t, per_logit, min_x, prow);
+                    n = min(sh.list_n, static_cast<uint32_t>(CAP));
+                    const int last = list_winner<THREADS, CAP>(sh, lrow, static_cast<int>(n), static_cast<int>(n), true, goal, p, M, T,
+                                                               inv_t, per_logit, min_x, prow);
                     if (tid == 0) a.out_ids[row] = static_cast<int64_t>(last);
                     return;
                 }
-                --tries;
+                tries = near ? 0 : tries - 1;
                 continue;
             }
         }
-        if (rank == 0 && tid == 0) a.out_ids[row] = static_cast<int64_t>(col);
+        if (rank == 0 && tid == 0) {
+            best.b1 = sh.cand[first];
+            best.b2 = next <= TRIED ? sh.cand[next] : 0;
+            a.out_ids[row] = static_cast<int64_t>(winner());
+        }
         return;
     }
 }
 
-template <int CLUSTER, int THREADS, int LOADS1, int MIN_CTAS>
+template <int CLUSTER, int THREADS, int LOADS1, int MIN_CTAS, int TRIED>
 struct Rows {
-    static constexpr auto kernel = sample_filtered_kernel<CLUSTER, THREADS, LOADS1, MIN_CTAS>;
+    static constexpr auto kernel = sample_filtered_kernel<CLUSTER, THREADS, LOADS1, MIN_CTAS, TRIED>;
     static cudaError_t launch(const Args& args, cudaStream_t stream) {
         kernel<<<dim3(CLUSTER, args.a.batch), THREADS, 0, stream>>>(args);
         return cudaGetLastError();
     }
 };
-using FewRows = Rows<16, 512, 5, 1>;
-using SomeRows = Rows<8, 256, 8, 4>;
-using ManyRows = Rows<4, 256, 8, 4>;
+using FewRows = Rows<16, 512, 5, 1, 1>;
+using SomeRows = Rows<8, 256, 8, 4, CANDS>;
+using ManyRows = Rows<4, 256, 8, 4, CANDS>;
 
 }  // namespace
 
@@ -1327,12 +1523,14 @@ pkv_status launch_sample_filtered(const SampleFilteredArgs& a, int* err, cudaStr
     // The more CTAs to a row, the sooner it is done; the fewer, the less of its time goes into their barriers.  7
     // clusters of 16 x 512 threads run at once, half as many rows as there are SMs on clusters of 8 x 256 (four CTAs to
     // an SM), as many rows as SMs on clusters of 4.  Rows of 151,936 with settings of their own, us: 8 rows 22 on 16 and
-    // 28 on 8, 10 rows 22 and 28, 12 rows 35 and 29; 77 rows 54 on 8 and 65 on 4, 120 rows 64 and 70, 180 rows 76
-    // and 78, 228 rows 88 and 79, 512 rows 158 and 140 (256 rows without filters 99 and 78).
+    // 28 on 8, 10 rows 22 and 28, 12 rows 35 and 29; 120 rows 53 on 8 and 70 on 4, 228 rows 84 and 78, 512 rows 162 and
+    // 119 (256 rows without filters 109 and 82).  Their order: 120 rows 61 without it, 512 rows 136; equal rows lose
+    // 3 us to it.
     constexpr int kWideRows = 10;
-    const cudaError_t e = a.batch <= kWideRows             ? FewRows::launch(args, stream)
-                          : 4 * a.batch <= 5 * sm_count()  ? SomeRows::launch(args, stream)
-                                                           : ManyRows::launch(args, stream);
+    const int sms = sm_count();
+    const bool wide = a.batch <= kWideRows, some = 4 * a.batch <= 5 * sms;
+    args.ordered = !wide && a.batch > (some ? sms / 2 : sms) && a.batch <= ORDERED_ROWS;
+    const cudaError_t e = wide ? FewRows::launch(args, stream) : some ? SomeRows::launch(args, stream) : ManyRows::launch(args, stream);
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 

@@ -222,3 +222,11 @@ def test_full_vocabulary_in_larger_batches(pkv, B):
     more = SETTINGS + [(0, 0.02, 0.0), (0, 0.5, 0.0), (0, 0.5, 0.02), (1000, 0.7, 0.0), (300, 1.0, 0.0)]
     k, p, m = (np.array([more[i % len(more)][j] for i in range(B)]) for j in range(3))
     check(pkv, x, np.random.default_rng(83).uniform(0.4, 1.5, B), k, p, m, most_unclear=3)
+
+
+@pytest.mark.parametrize("B", [1000, 4097])
+def test_every_row_of_a_large_batch_is_sampled(pkv, B):
+    """Batches whose rows do not all run at once take them in another order than the rows'."""
+    rng = np.random.default_rng(B)
+    k, p, m = (np.array([SETTINGS[i][j] for i in rng.integers(0, len(SETTINGS), B)]) for j in range(3))
+    check(pkv, rows(B, 129, 91), 0.9, k, p, m, most_unclear=5)
