@@ -11,8 +11,8 @@
 // -ln e_v lies in (-2.82, 16.64), a token more than 19.6 below the maximum cannot beat the
 // maximum's own key: it counts in the sums but takes no part in the race.
 //
-// One cluster of CTAs takes a row, each an equal slice of it; HBM sees each logit once (pass 1),
-// later sweeps find the row in L2 and skip a quad of logits at one comparison of its maximum.
+// One cluster of CTAs takes a row, each an equal slice of it; pass 1 reads it from HBM, later
+// sweeps mostly find it in L2 and skip a quad of logits at one comparison of its maximum.
 // The work below pass 1 is bound by latency (cluster barriers, dependent shared-memory steps), so
 // each kind of row takes the shortest way that is exact for it:
 //
@@ -53,8 +53,8 @@
 //
 // Rows that cannot all run at once are taken in an order that starts the longest first (row_in_order).
 //
-// Measured on rows of 151,936 logits: 256 rows with settings of their own 80 us (156 MB, 1.9 TB/s; over sixteen
-// seeds 90 on average and 109 at most), all top-k = 50 62 us, all top-p = 0.9 127 us, no filter 82 us; one row 14,
+// Measured on rows of 151,936 logits: 256 rows with settings of their own 87 us (156 MB, 1.8 TB/s; the average
+// of sixteen seeds, 103 at most), all top-k = 50 62 us, all top-p = 0.9 127 us, no filter 82 us; one row 14,
 // 16 and 14 us (top-p 18 us when its code has to come from DRAM).  The same batch of 256 before: with the border
 // looked for in every top-p row and lists sorted 111 us; with one candidate examined 105 us on average and 179 at
 // most; with rows in their own order 94.  What else was tried: the slices kept in shared memory (435 us), one loop
@@ -321,8 +321,12 @@ __device__ __forceinline__ float warp_second(const Best& best) {
 __device__ __forceinline__ float4 clean(const float4& v) {
     return make_float4(fmaxf(v.x, -INFINITY), fmaxf(v.y, -INFINITY), fmaxf(v.z, -INFINITY), fmaxf(v.w, -INFINITY));
 }
+// kOnce: the row is not swept again, so its lines may leave L2 first (152 rows at once are 92 MB: without it, later
+// looks at the other rows missed L2; 256 rows with settings of their own 91 -> 87 us).
+template <bool kOnce = false>
 __device__ __forceinline__ float4 load_whole_quad(const float* row, int qd) {
-    return clean(__ldg(reinterpret_cast<const float4*>(row) + qd));
+    const float4* at = reinterpret_cast<const float4*>(row) + qd;
+    return clean(kOnce ? __ldcs(at) : __ldg(at));
 }
 __device__ __forceinline__ float4 load_columns(const float* row, int qd, int vocab) {
     const int col = qd * 4;
@@ -336,7 +340,7 @@ __device__ __forceinline__ float4 load_columns(const float* row, int qd, int voc
 __device__ __forceinline__ float max_of(const float4& v) { return fmaxf(fmax3(v.x, v.y, v.z), v.w); }
 
 // f(quad, its logits) over quads [q0, q1) of a row by whole warps, N loads in flight; lanes without a quad get -inf.
-template <int THREADS, int N, typename F>
+template <int THREADS, int N, bool kOnce = false, typename F>
 __device__ __forceinline__ void sweep_warps(const float* row, int q0, int q1, int whole, int vocab, F f) {
     const float4 none = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
     const int tid = threadIdx.x;
@@ -344,7 +348,7 @@ __device__ __forceinline__ void sweep_warps(const float* row, int q0, int q1, in
     for (; base + N * THREADS <= min(q1, whole); base += N * THREADS) {
         float4 v[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = load_whole_quad(row, base + i * THREADS + tid);
+        for (int i = 0; i < N; ++i) v[i] = load_whole_quad<kOnce>(row, base + i * THREADS + tid);
 #pragma unroll
         for (int i = 0; i < N; ++i) f(base + i * THREADS + tid, v[i]);
     }
@@ -353,7 +357,7 @@ __device__ __forceinline__ void sweep_warps(const float* row, int q0, int q1, in
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int qd = base + i * THREADS + tid;
-            v[i] = whole > 0 ? load_whole_quad(row, min(qd, whole - 1)) : none;
+            v[i] = whole > 0 ? load_whole_quad<kOnce>(row, min(qd, whole - 1)) : none;
             if (qd >= q1) v[i] = none;
             else if (qd >= whole) v[i] = load_columns(row, qd, vocab);
         }
@@ -381,7 +385,7 @@ __device__ __noinline__ RaceAll race_all_of(const float* row, int q0, int q1, in
     const float l2 = fminf(inv_t * LOG2E, 3.4028235e38f);
     const RoundKeys unused = {};
     float ref_end = -INFINITY, bar = -INFINITY;
-    sweep_warps<THREADS, RACE_LOADS>(row, q0, q1, whole, vocab, [&](int qd, const float4& v) {
+    sweep_warps<THREADS, RACE_LOADS, !kSum>(row, q0, q1, whole, vocab, [&](int qd, const float4& v) {
         const float m4 = max_of(v);
         if (m4 > r.mx) { r.mx = m4; r.mx_quad = qd; }
         if (__any_sync(0xffffffffu, m4 > ref_end)) {
@@ -679,21 +683,22 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
     auto load_whole = [&](int qd) -> float4 { return load_whole_quad(lrow, qd); };
     auto load_quad = [&](int qd) -> float4 { return qd < whole ? load_whole(qd) : load_columns(lrow, qd, a.vocab); };
     // f(quad, its logits) over the slice, LOADS loads in flight per thread
-    auto sweep_quads_by = [&](auto in_flight, auto f) {
+    auto sweep_quads_by = [&](auto in_flight, auto f, auto once) {
         constexpr int N = decltype(in_flight)::value;
+        constexpr bool kOnce = decltype(once)::value;
         int qd = q0 + tid;
         const int end = min(q1, whole);
         for (; qd + (N - 1) * THREADS < end; qd += N * THREADS) {
             float4 v[N];
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = load_whole(qd + i * THREADS);
+            for (int i = 0; i < N; ++i) v[i] = load_whole_quad<kOnce>(lrow, qd + i * THREADS);
 #pragma unroll
             for (int i = 0; i < N; ++i) f(qd + i * THREADS, v[i]);
         }
         if (qd < end) {                                   // the rest of the whole quads, together as well
             float4 v[N];
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = load_whole(min(qd + i * THREADS, end - 1));
+            for (int i = 0; i < N; ++i) v[i] = load_whole_quad<kOnce>(lrow, min(qd + i * THREADS, end - 1));
 #pragma unroll
             for (int i = 0; i < N; ++i)
                 if (qd + i * THREADS < end) f(qd + i * THREADS, v[i]);
@@ -701,7 +706,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
         }
         for (; qd < q1; qd += THREADS) f(qd, load_quad(qd));
     };
-    auto sweep_quads = [&](auto f) { sweep_quads_by(std::integral_constant<int, LOADS>{}, f); };
+    auto sweep_quads = [&](auto f) { sweep_quads_by(std::integral_constant<int, LOADS>{}, f, std::false_type{}); };
     const int iters = (q1 - q0 + THREADS - 1) / THREADS;  // uniform
     // f(column, logit) for every logit of the slice from x_min up, and above -inf
     auto sweep_from = [&](float x_min, auto f) {
@@ -788,7 +793,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
             }
             if (mx > -INFINITY)
                 zs += (ex2_ftz((v.x - mx) * l2) + ex2_ftz((v.y - mx) * l2)) + (ex2_ftz((v.z - mx) * l2) + ex2_ftz((v.w - mx) * l2));
-        });
+        }, std::false_type{});
     } else if (fast_k) {
         sweep_quads_by(std::integral_constant<int, LOADS1>{}, [&](int qd, const float4& v) {
             const float m4 = max_of(v);
@@ -798,12 +803,12 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
             m2 = a1 ? mx : a2 ? m4 : m2;
             mx_quad = a1 ? qd : mx_quad;
             mx = a1 ? m4 : mx;
-        });
+        }, std::true_type{});
     } else {
         sweep_quads_by(std::integral_constant<int, LOADS1>{}, [&](int qd, const float4& v) {
             const float m4 = max_of(v);
             if (m4 > mx) { mx = m4; mx_quad = qd; }
-        });
+        }, std::false_type{});
     }
     uint64_t top = 0;                                     // the first token: largest logit, lowest column
     if (mx > -INFINITY) {
@@ -1426,7 +1431,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
             Before sums = {};                             // before each of them; and the tokens before that one
             sweep_quads_by(std::integral_constant<int, CHECK_LOADS>{}, [&](int qd, const float4& v) {
                 if (max_of(v) >= x_low) sums = add_before(sums, sh, v, qd, M, per_logit, top_c);
-            });
+            }, std::false_type{});
             const uint32_t before = __reduce_add_sync(0xffffffffu, sums.count);
 #pragma unroll
             for (int j = 0; j < TRIED; ++j) {
