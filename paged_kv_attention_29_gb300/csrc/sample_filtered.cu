@@ -110,8 +110,7 @@ struct Shared {
         uint64_t parts[MAX_CLUSTER * 8][2];          // races: the two best of every part
     };
     uint64_t sorted[RANK_MAX];
-    uint64_t slot[2][MAX_CLUSTER];             // cluster-wide sums and counts, alternating
-    uint32_t slot_n[2][MAX_CLUSTER];
+    uint64_t slot[2][MAX_CLUSTER];             // cluster-wide sums, alternating
     uint64_t lo[2][MAX_CLUSTER], hi[2][MAX_CLUSTER];   // cluster-wide ranges, alternating
     uint64_t top[MAX_CLUSTER];   // pass 1: first token of each CTA, and its sum of weights relative to it
     float z[MAX_CLUSTER];
@@ -872,24 +871,20 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
 
     // ---- cluster-wide reductions; every CTA ends with the same values
     int phase = 0;
-    uint32_t summed = 0;                                  // the counts given with the last sum
-    auto cluster_sum = [&](uint64_t v, uint32_t cnt = 0) -> uint64_t {
+    auto cluster_sum = [&](uint64_t v) -> uint64_t {
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) v += shfl_xor64(v, off);
-        cnt = __reduce_add_sync(0xffffffffu, cnt);
-        if (lane == 0) { sh.wred[warp] = v; sh.wlo[warp] = cnt; }
+        if (lane == 0) sh.wred[warp] = v;
         __syncthreads();
         if (tid < CLUSTER) {
-            uint64_t s = 0, n = 0;
-            for (int w = 0; w < WARPS; ++w) { s += sh.wred[w]; n += sh.wlo[w]; }
+            uint64_t s = 0;
+            for (int w = 0; w < WARPS; ++w) s += sh.wred[w];
             *cluster.map_shared_rank(&sh.slot[phase][rank], tid) = s;
-            *cluster.map_shared_rank(&sh.slot_n[phase][rank], tid) = static_cast<uint32_t>(n);
         }
         cluster.sync();
         uint64_t s = 0;
-        summed = 0;
 #pragma unroll
-        for (int r = 0; r < CLUSTER; ++r) { s += sh.slot[phase][r]; summed += sh.slot_n[phase][r]; }
+        for (int r = 0; r < CLUSTER; ++r) s += sh.slot[phase][r];
         phase ^= 1;
         return s;
     };
@@ -1477,7 +1472,9 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
                 uint32_t n = 0;
                 for (int r = 0; r < CLUSTER; ++r) n += sh.ccnt[r];
                 keep = out + 1;
-                if (out == top_c && n <= CAP) {           // the first CTA ends it
+                // (decided by what every CTA has from the same exchange, so that a row that is written under the call
+                // cannot part them)
+                if (first < 0 && n <= CAP) {              // out is top_c: the first CTA ends it
                     sweep_from(composite_x(out), [&](int other, float x) {
                         if (composite(x, other) > out) collect(composite(x, other));
                     });
