@@ -8,6 +8,11 @@ fallback: if ``libpkv.so`` has not been built, :func:`load` raises.
 
 Build the library with ``python -m paged_kv_attention_29_gb300.build``.
 
+A call runs on ``stream``, by default the current one, and what it allocates
+itself (an output or a workspace that is not given) comes from that stream's
+pool.  A caller that names another stream orders its inputs before and the
+reading of the result after the call, as for any work on two streams.
+
 Functions carry the C names:
 
 =========================  ================================================
@@ -161,6 +166,20 @@ def _check(t: torch.Tensor, name: str, dtype, ndim=None, contiguous=True):
         raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _allocated(stream, make, *args, result=False, **kw):
+    """make(*args, **kw), a tensor that a call on `stream` (None: the current one) allocates itself, from that
+    stream's pool: a block of the current stream's could still be in use by work queued there, which `stream` does
+    not wait for.  A result is read on the caller's own stream, so that one's work holds its memory too."""
+    if stream is None:
+        return make(*args, **kw)
+    caller = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        t = make(*args, **kw)
+    if result and caller != stream:
+        t.record_stream(caller)
+    return t
 
 
 class _on_device:
@@ -606,15 +625,6 @@ def _launch(name: str, fn, stream, tensors, args):
         raise PkvError(status, name)
 
 
-def _used_on(stream, *tensors):
-    """Tensors a call allocated itself, on the current stream, and used on another: the allocator hands their
-    memory on only after that stream's work."""
-    if stream is not None and stream != torch.cuda.current_stream(stream.device):
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
-
-
 def _pools_fp8(k_cache, v_cache, k_scale, v_scale):
     """Shape (num_blocks, block_size, num_kv_heads, head_dim) of an 8-bit cache, checked."""
     _check(k_cache, "k_cache", torch.float8_e4m3fn, 4)
@@ -671,7 +681,6 @@ def pkv_rope_store_kvcache_fp8(q: Optional[torch.Tensor], k: torch.Tensor, v: to
         raise ValueError("positions and slot_mapping disagree on the token count")
     ks, vs = _rows(k, "k", n, hkv, d), _rows(v, "v", n, hkv, d)
     tensors = (k, v, positions, slot_mapping, k_cache, v_cache, k_scale, v_scale)
-    own = None
     if q is None:
         if q_out is not None:
             raise ValueError("q_out given without q")
@@ -683,14 +692,13 @@ def pkv_rope_store_kvcache_fp8(q: Optional[torch.Tensor], k: torch.Tensor, v: to
         hq = q.shape[1]
         qs = _rows(q, "q", n, hq, d)
         if q_out is None:
-            q_out = own = torch.empty(n, hq, d, dtype=torch.bfloat16, device=q.device)
+            q_out = _allocated(stream, torch.empty, n, hq, d, dtype=torch.bfloat16, device=q.device, result=True)
         head = (q.data_ptr(), qs, q_out.data_ptr(), _rows(q_out, "q_out", n, hq, d))
         tensors += (q, q_out)
     _launch("pkv_rope_store_kvcache_fp8", load().pkv_rope_store_kvcache_fp8, stream, tensors,
             head + (k.data_ptr(), ks, v.data_ptr(), vs, positions.data_ptr(), n, hq, hkv, d, float(rope_base),
                     slot_mapping.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
                     v_scale.data_ptr(), nb, bs))
-    _used_on(stream, own)
     return q_out
 
 
@@ -721,21 +729,19 @@ def pkv_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     rows, width = block_tables.shape
     if dq != d or context_lens.shape[0] != batch or rows != batch:
         raise ValueError("q, context_lens and block_tables disagree")
-    own_out = own_ws = None
     if out is None:
-        out = own_out = torch.empty_like(q)
+        out = _allocated(stream, torch.empty_like, q, result=True)
     _want(out, "out", torch.bfloat16, 3)
     if out.shape != (batch, hq, d):
         raise ValueError("out must have q's shape")
     if workspace is None:
-        workspace = own_ws = decode_fp8_workspace(batch, hq, hkv, d, k_cache.device)
+        workspace = _allocated(stream, decode_fp8_workspace, batch, hq, hkv, d, k_cache.device)
     _want(workspace, "workspace", torch.uint8, 1)
     _launch("pkv_decode_fp8", load().pkv_decode_fp8, stream,
             (q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, out, workspace),
             (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
              block_tables.data_ptr(), width, context_lens.data_ptr(), batch, int(max_context_len), hq, hkv, d, bs, nb,
              float(softmax_scale), out.data_ptr(), workspace.data_ptr(), workspace.numel()))
-    _used_on(stream, own_out, own_ws)
     return out
 
 
@@ -773,14 +779,14 @@ def pkv_prefill_varlen_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
     num_seqs, width = block_tables.shape
     if cu_seqlens_q.shape[0] != num_seqs + 1 or cu_seqlens_k.shape[0] != num_seqs + 1:
         raise ValueError("cu_seqlens_q, cu_seqlens_k and block_tables disagree on the sequence count")
-    own_out = own_ws = None
     if out is None:
-        out = own_out = torch.empty_like(q)
+        out = _allocated(stream, torch.empty_like, q, result=True)
     _want(out, "out", torch.bfloat16, 3)
     if out.shape != (total_q, hq, d):
         raise ValueError("out must have q's shape")
     if workspace is None:
-        workspace = own_ws = prefill_fp8_workspace(num_seqs, hq, hkv, d, max_seqlen_q, max_seqlen_k, total_k, k_cache.device)
+        workspace = _allocated(stream, prefill_fp8_workspace, num_seqs, hq, hkv, d, max_seqlen_q, max_seqlen_k, total_k,
+                               k_cache.device)
     _want(workspace, "workspace", torch.uint8, 1)
     _launch("pkv_prefill_varlen_fp8", load().pkv_prefill_varlen_fp8, stream,
             (q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, cu_seqlens_k, block_tables, out, workspace),
@@ -788,7 +794,6 @@ def pkv_prefill_varlen_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
              cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), block_tables.data_ptr(), width, num_seqs, total_q,
              int(max_seqlen_q), int(max_seqlen_k), int(total_k), hq, hkv, d, bs, nb, float(softmax_scale),
              out.data_ptr(), workspace.data_ptr(), workspace.numel()))
-    _used_on(stream, own_out, own_ws)
     return out
 
 
@@ -803,9 +808,8 @@ def _sample_filtered(name, logits, temperatures, top_k, top_p, min_p, noise, out
     row, element = logits.stride()
     if element != 1 and vocab > 1:
         raise ValueError("logits rows must be contiguous")
-    own = None
     if out_ids is None:
-        out_ids = own = torch.empty(batch, dtype=torch.int64, device=logits.device)
+        out_ids = _allocated(stream, torch.empty, batch, dtype=torch.int64, device=logits.device, result=True)
     tensors, filters = [logits, temperatures, out_ids], []
     _want(temperatures, "temperatures", torch.float32, 1)
     _want(out_ids, "out_ids", torch.int64, 1)
@@ -825,7 +829,6 @@ def _sample_filtered(name, logits, temperatures, top_k, top_p, min_p, noise, out
     _launch(name, getattr(load(), name), stream, tensors,
             (logits.data_ptr(), batch, vocab, row if batch > 1 else vocab, temperatures.data_ptr(), *filters, *noise,
              out_ids.data_ptr()))
-    _used_on(stream, own)
     return out_ids
 
 
