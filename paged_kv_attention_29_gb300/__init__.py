@@ -314,7 +314,7 @@ def pkv_rope_store_kvcache(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.
         if q.shape[0] != n or q.shape[2] != d or q.stride(2) != 1 or q.stride(1) != d:
             raise ValueError(f"q must be [n, Hq, {d}] with contiguous rows")
         if q_out is None:
-            q_out = torch.empty(n, hq, d, dtype=torch.bfloat16, device=q.device)
+            q_out = _allocated(stream, torch.empty, n, hq, d, dtype=torch.bfloat16, device=q.device, result=True)
         _check(q_out, "q_out", torch.bfloat16, 3, contiguous=False)
         if tuple(q_out.shape) != tuple(q.shape) or q_out.stride(2) != 1 or q_out.stride(1) != d:
             raise ValueError("q_out must match q's shape with contiguous rows")
@@ -350,13 +350,13 @@ def _prefill(entry: str, q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, block_
     if cu_seqlens_k.shape[0] != num_seqs + 1 or block_tables.shape[0] != num_seqs:
         raise ValueError("cu_seqlens_q, cu_seqlens_k and block_tables disagree on the sequence count")
     if out is None:
-        out = torch.empty_like(q)
+        out = _allocated(stream, torch.empty_like, q, result=True)
     _check(out, "out", torch.bfloat16, 3)
     if workspace is None:
         if entry == "pkv_prefill_varlen_planned":
             raise ValueError("a planned prefill needs the workspace its plan was written to")
         n = pkv_prefill_workspace_size(num_seqs, hq, hkv, d, int(max_seqlen_q))
-        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+        workspace = _allocated(stream, torch.empty, max(n, 1), dtype=torch.uint8, device=q.device)
     ws_bytes = workspace.numel() * workspace.element_size()
     with _on_device(q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, block_tables, out, workspace, stream=stream):
         _raise(getattr(load(), entry)(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k),
@@ -388,7 +388,7 @@ def pkv_prefill_plan(cu_seqlens_q: torch.Tensor, cu_seqlens_k: torch.Tensor, tot
         raise ValueError("cu_seqlens_q and cu_seqlens_k disagree on the sequence count")
     if workspace is None:
         n = pkv_prefill_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, int(max_seqlen_q))
-        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=cu_seqlens_q.device)
+        workspace = _allocated(stream, torch.empty, max(n, 1), dtype=torch.uint8, device=cu_seqlens_q.device, result=True)
     ws_bytes = workspace.numel() * workspace.element_size()
     with _on_device(cu_seqlens_q, cu_seqlens_k, workspace, stream=stream):
         _raise(load().pkv_prefill_plan(_ptr(cu_seqlens_q), _ptr(cu_seqlens_k), int(max_blocks_per_seq), num_seqs,
@@ -433,10 +433,10 @@ def pkv_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, bl
     if dq != d or context_lens.shape[0] != batch or block_tables.shape[0] != batch:
         raise ValueError("q, context_lens and block_tables disagree")
     if out is None:
-        out = torch.empty_like(q)
+        out = _allocated(stream, torch.empty_like, q, result=True)
     _check(out, "out", torch.bfloat16, 3)
     if workspace is None:
-        workspace = decode_workspace(batch, hq, hkv, d, q.device)
+        workspace = _allocated(stream, decode_workspace, batch, hq, hkv, d, q.device)
     _check(workspace, "workspace", torch.uint8, 1)
     with _on_device(q, k_cache, v_cache, block_tables, context_lens, out, workspace, stream=stream):
         _raise(load().pkv_decode(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), block_tables.shape[1],
@@ -466,12 +466,12 @@ def pkv_decode_append(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
     if tuple(k_new.shape) != (batch, hkv, d) or tuple(v_new.shape) != (batch, hkv, d):
         raise ValueError(f"k_new / v_new must be [{batch}, {hkv}, {d}]")
     if out is None:
-        out = torch.empty_like(q)
+        out = _allocated(stream, torch.empty_like, q, result=True)
     _check(out, "out", torch.bfloat16, 3)
     if slot_mapping is not None:
         _check(slot_mapping, "slot_mapping", torch.int32, 1)
     if workspace is None:
-        workspace = decode_workspace(batch, hq, hkv, d, q.device)
+        workspace = _allocated(stream, decode_workspace, batch, hq, hkv, d, q.device)
     _check(workspace, "workspace", torch.uint8, 1)
     with _on_device(q, k_new, v_new, k_cache, v_cache, block_tables, context_lens, out, slot_mapping, workspace,
                     stream=stream):
@@ -489,7 +489,9 @@ class DecodeAppendCall:
     A serving loop calls the same step on the same buffers (inputs copied into
     them) every iteration; this object does the argument checks and the ctypes
     marshalling at construction, so each call is one C-ABI call.  The buffers
-    must stay alive and keep their shapes; their contents may change freely."""
+    must stay alive and keep their shapes; their contents may change freely.
+    A call on another stream than the construction's is ordered behind the
+    construction by the caller."""
 
     def __init__(self, q, k_new, v_new, k_cache, v_cache, block_tables, context_lens, max_context_len,
                  softmax_scale, out, slot_mapping=None, workspace=None, stream=None):
@@ -499,7 +501,7 @@ class DecodeAppendCall:
         nb, bs, hkv, d = _pool_shape(k_cache)
         batch, hq, _ = q.shape
         if workspace is None:
-            workspace = decode_workspace(batch, hq, hkv, d, q.device)
+            workspace = _allocated(stream, decode_workspace, batch, hq, hkv, d, q.device)
         self._keep = (q, k_new, v_new, k_cache, v_cache, block_tables, context_lens, out, slot_mapping, workspace)
         self._fn = load().pkv_decode_append
         self._args = (_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
@@ -554,7 +556,7 @@ def pkv_sample(logits: torch.Tensor, temperatures: torch.Tensor, seed: int, offs
     _check(temperatures, "temperatures", torch.float32, 1)
     batch, vocab = logits.shape
     if out_ids is None:
-        out_ids = torch.empty(batch, dtype=torch.int64, device=logits.device)
+        out_ids = _allocated(stream, torch.empty, batch, dtype=torch.int64, device=logits.device, result=True)
     _check(out_ids, "out_ids", torch.int64, 1)
     with _on_device(logits, temperatures, out_ids, stream=stream):
         _raise(load().pkv_sample(_ptr(logits), batch, vocab, _row_stride(logits), _ptr(temperatures),
@@ -576,7 +578,7 @@ def pkv_sample_dev(logits: torch.Tensor, temperatures: torch.Tensor, seed_offset
         raise ValueError("seed_offset holds {seed, offset}")
     batch, vocab = logits.shape
     if out_ids is None:
-        out_ids = torch.empty(batch, dtype=torch.int64, device=logits.device)
+        out_ids = _allocated(stream, torch.empty, batch, dtype=torch.int64, device=logits.device, result=True)
     _check(out_ids, "out_ids", torch.int64, 1)
     with _on_device(logits, temperatures, seed_offset, out_ids, stream=stream):
         _raise(load().pkv_sample_dev(_ptr(logits), batch, vocab, _row_stride(logits), _ptr(temperatures),

@@ -89,10 +89,41 @@ def test_8_bit_and_filtered_calls_allocate_on_their_stream(pkv, name, allocation
     check_call(pkv, CALLS_8_BIT[name], allocations, monkeypatch)
 
 
+CALLS = {
+    "rope_store": lambda p, a, s: p.pkv_rope_store_kvcache(a["q"], a["k"], a["v"], a["pos"], a["slots"], a["k16"], a["v16"], 1e4, stream=s),
+    "decode": lambda p, a, s: p.pkv_decode(a["q"], a["k16"], a["v16"], a["tables"], a["lens"], 45, 0.1, stream=s),
+    "decode_append": lambda p, a, s: p.pkv_decode_append(a["q"], a["k"], a["v"], a["k16"], a["v16"], a["tables"], a["lens"], 45, 0.1, stream=s),
+    "prefill": lambda p, a, s: p.pkv_prefill_varlen(a["q"], a["k16"], a["v16"], a["cu_q"], a["cu_k"], a["tables"], 1, 45, 0.1, stream=s),
+    "sample": lambda p, a, s: p.pkv_sample(a["x"], a["T"], 1, stream=s),
+    "sample_dev": lambda p, a, s: p.pkv_sample_dev(a["x"], a["T"], a["so"], stream=s),
+}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_bf16_cache_calls_allocate_on_their_stream(pkv, name, allocations, monkeypatch):
+    check_call(pkv, CALLS[name], allocations, monkeypatch)
+
+
+def test_plans_and_call_objects_allocate_on_their_stream(pkv, allocations):
+    a = inputs()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    ws = pkv.pkv_prefill_plan(a["cu_q"], a["cu_k"], 2, 1, 45, 16, 8, D, 256, 1, stream=side)
+    assert pool_of(ws) == side.cuda_stream
+    out = torch.empty_like(a["q"])
+    torch.cuda.synchronize()
+    allocations.clear()
+    call = pkv.DecodeAppendCall(a["q"], a["k"], a["v"], a["k16"], a["v16"], a["tables"], a["lens"], 45, 0.1, out, stream=side)
+    call()
+    assert allocations and set(allocations) == {side.cuda_stream}
+    side.synchronize()
+    assert torch.equal(out, pkv.pkv_decode(a["q"], a["k16"], a["v16"], a["tables"], a["lens"], 45, 0.1))
+
+
 def test_calls_on_a_forked_stream_are_captured(pkv):
     """A call on a stream that a capture has forked to, with everything it allocates."""
     a = inputs()
-    for name, call in CALLS_8_BIT.items():
+    for name, call in {**CALLS_8_BIT, **CALLS}.items():
         ref = call(pkv, a, None)
         torch.cuda.synchronize()
         side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
