@@ -392,8 +392,9 @@ PKV_API pkv_status pkv_rope_store_kvcache_fp8(const pkv_bf16 *q, int64_t q_token
  * workspace rules as pkv_decode, with a workspace of
  * pkv_decode_fp8_workspace_size bytes, 256-byte aligned.  Results are
  * deterministic.  Scores and the softmax sum are fp32; the weight of each key,
- * times its value's scale relative to the largest such product seen, is rounded
- * to f16 (relative error 2^-11) for the product with the values.
+ * times its value's scale, is rounded to f16 for the product with the values: to
+ * 2^-11 of itself, and to no less than 2^-38 of the largest such product among the
+ * keys that are summed together (a run of a sequence's keys).
  */
 PKV_API size_t pkv_decode_fp8_workspace_size(int32_t batch, int32_t num_heads, int32_t num_kv_heads,
                                      int32_t head_dim);

@@ -20,12 +20,16 @@
 //   is exact in f16 down to 2^-28 of that element (and to within 2^-39 of it below).
 // * With s_j the scores in the log2 domain and m a running maximum of them, the softmax sum is
 //   l = sum 2^(s_j - m) in fp32, and the weight of key j in the second product is 2^(t_j - T),
-//   t_j = s_j - m + ev_j, T a running maximum of t: the largest weight is about 1 whatever the
-//   scales are, so f16 (11 bits, down to 2^-24) costs an error of 2^-11 relative to each term, an
-//   eighth of the output's bf16 rounding.  A piece is written as o * 2^T.  (t is taken relative to
-//   m, not s + ev, which would lose ev's bits beside a large score.)
-// * Both references move only when a score exceeds them by a margin (w <= 2^8 stays far below
-//   f16's 65504, l's terms below 2^64), found by one vote per chunk; the rescale is a rare branch.
+//   t_j = s_j - m + ev_j, T a reference that follows the largest t: the largest weight seen is held
+//   in [2^kTopT, 2^kMarginT], near the top of f16 (65504), whatever the scales are.  Rounding to f16
+//   costs 2^-11 of each term, an eighth of the output's bf16 rounding, so long as a weight is at least
+//   2^-14; below, an absolute 2^-25, which is 2^-(25 + kTopT) = 2^-38 of the largest: what thousands
+//   of light keys behind a heavy one add to a channel in which that one holds 0 is kept.  (With
+//   the largest weight at 1, keys below 2^-25 of it were lost, though l counted them.)  A piece is
+//   written as o * 2^T.  (t is taken relative to m, not s + ev, which would lose ev's bits beside a
+//   large score.)
+// * Both references move only when a score exceeds them by a margin (weights stay below 2^15,
+//   l's terms below 2^64), found by one vote per chunk; the rescale is a rare branch.
 //
 // Work split: the batch's tokens in 32-token chunks, sequence after sequence, are cut into equal
 // contiguous runs, one for each group of num_kv_heads warps of a persistent grid; warp h of the
@@ -60,8 +64,9 @@ constexpr int STAGE_BYTES = 2 * TILE_BYTES;  // K, V
 constexpr int SCALE_BYTES = 2 * CHUNK;       // a stage's K scales, V scales
 constexpr int MAX_BATCH = 4096;
 constexpr int KMIN = 2;                      // chunks a warp takes at least, where the batch allows it
-constexpr float kMarginT = 8.f;              // log2 headroom of the weights over their reference
-constexpr float kMarginM = 64.f;             // and of the softmax terms over theirs
+constexpr float kTopT = 13.f;                // log2 of the largest weight, when its reference moves
+constexpr float kMarginT = 15.f;             // and what moves it
+constexpr float kMarginM = 64.f;             // the same of the softmax terms, which move to 0
 static_assert(TILE_BYTES % 1024 == 0, "swizzled tiles start on 1 KiB");
 
 struct Params {
@@ -404,6 +409,7 @@ decode_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 float up = fmaxf(fmaxf(w[0][h], w[1][h]), fmaxf(w[2][h], w[3][h]));
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, x));
+                up -= kTopT;
                 if (!fresh) up = fmaxf(up, 0.f);
                 if (!(fabsf(up) < INFINITY)) up = 0.f;
                 T[h] += up;
@@ -458,11 +464,13 @@ decode_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 for (int off = 4; off < 32; off <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], off);
                 const int hq = 2 * t + h;                      // query head of the group
                 if (hq < G) {
-                    const float f = ex2_ftz(T[h]);             // from the weights' reference to the sum's
+                    // from the weights' reference to the sum's; the smallest scales' T alone is below 2^-126
+                    const float top = __uint_as_float((127u - static_cast<uint32_t>(kTopT)) << 23), f = ex2_ftz(T[h] + kTopT);
                     float4* dst = reinterpret_cast<float4*>(p.part_o + (piece * G + hq) * D + 16 * g);
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
-                        dst[u] = make_float4(o[2 * u][h] * f, o[2 * u][2 + h] * f, o[2 * u + 1][h] * f, o[2 * u + 1][2 + h] * f);
+                        dst[u] = make_float4(o[2 * u][h] * top * f, o[2 * u][2 + h] * top * f, o[2 * u + 1][h] * top * f,
+                                             o[2 * u + 1][2 + h] * top * f);
                     if (g == 0) {
                         p.part_ml[(piece * G + hq) * 2] = m[h];
                         p.part_ml[(piece * G + hq) * 2 + 1] = l[h];
