@@ -26,8 +26,10 @@
 //   2^-14; below, an absolute 2^-25, which is 2^-(25 + kTopT) = 2^-38 of the largest: what thousands
 //   of light keys behind a heavy one add to a channel in which that one holds 0 is kept.  (With
 //   the largest weight at 1, keys below 2^-25 of it were lost, though l counted them.)  A piece is
-//   written as o * 2^T.  (t is taken relative to m, not s + ev, which would lose ev's bits beside a
-//   large score.)
+//   written as o * 2^T; where values or l's terms (up to 2^64) are so large that this may leave
+//   fp32's range, relative to m + lg l + 12, which makes it an average of values and leaves the merge
+//   room for its sum.  (t is taken relative to m, not s + ev, which would lose ev's bits beside a large
+//   score.)
 // * Both references move only when a score exceeds them by a margin (weights stay below 2^15,
 //   l's terms below 2^64), found by one vote per chunk; the rescale is a rare branch.
 //
@@ -464,16 +466,17 @@ decode_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 for (int off = 4; off < 32; off <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], off);
                 const int hq = 2 * t + h;                      // query head of the group
                 if (hq < G) {
-                    // from the weights' reference to the sum's; the smallest scales' T alone is below 2^-126
-                    const float top = __uint_as_float((127u - static_cast<uint32_t>(kTopT)) << 23), f = ex2_ftz(T[h] + kTopT);
+                    // |o| is below 2^48 (weights, codes, keys); 2^(T - e) may be out of range where its product with o is not
+                    const float e = T[h] > 64.f && l[h] < INFINITY ? static_cast<float>(static_cast<int>(__float_as_uint(l[h]) >> 23) - 115) : 0.f;
+                    const float f = ex2_ftz(0.5f * (T[h] - e));
                     float4* dst = reinterpret_cast<float4*>(p.part_o + (piece * G + hq) * D + 16 * g);
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
-                        dst[u] = make_float4(o[2 * u][h] * top * f, o[2 * u][2 + h] * top * f, o[2 * u + 1][h] * top * f,
-                                             o[2 * u + 1][2 + h] * top * f);
+                        dst[u] = make_float4(o[2 * u][h] * f * f, o[2 * u][2 + h] * f * f, o[2 * u + 1][h] * f * f,
+                                             o[2 * u + 1][2 + h] * f * f);
                     if (g == 0) {
-                        p.part_ml[(piece * G + hq) * 2] = m[h];
-                        p.part_ml[(piece * G + hq) * 2 + 1] = l[h];
+                        p.part_ml[(piece * G + hq) * 2] = m[h] + e;
+                        p.part_ml[(piece * G + hq) * 2 + 1] = l[h] * ex2_ftz(-e);
                     }
                 }
             }

@@ -1,4 +1,4 @@
-"""Decode over an 8-bit cache where few keys outweigh many.
+"""Decode over an 8-bit cache where few keys outweigh many, and where values are of any size the format holds.
 
 Tolerance.  A key's weight times its value's scale is rounded to f16 relative to W, the largest such product
 its warp has seen: to 2^-11 of itself, and to no less than 2^-38 of W (f16's smallest step is 2^-24, half of
@@ -73,3 +73,13 @@ def test_heavy_keys_late_and_in_between(pkv):
     v[:, 1::4] *= (score < 1)[:, None]
     for batch in (1, 200):
         within(*decode(pkv, score, v, ev, batch))
+
+
+@pytest.mark.parametrize("exponent", [-126, -110, -60, 0, 60, 110, 118])
+def test_values_of_every_size(pkv, exponent):
+    """V of one size throughout, from the smallest scales to bf16's largest numbers, with scores that rise by 60 octaves."""
+    n, rng = 300, np.random.default_rng(7)
+    score = np.where(np.arange(n) < 32, 0.0, np.where(np.arange(n) < 250, 60.0, 56.0))
+    v = fc.E4M3[fc.round_e4m3(rng.choice([-1, 1], (n, D)) * rng.uniform(64, 400, (n, D)))]
+    for batch in (1, 160):
+        within(*decode(pkv, score, v, np.full(n, exponent), batch))
