@@ -494,7 +494,9 @@ PKV_API pkv_status pkv_sample_dev(const float *logits, int32_t batch, int32_t vo
  * Weights and a thread's sums of them are fp32, joined across threads in a fixed
  * order or in 64-bit fixed point: a token is decided as in exact arithmetic unless
  * top_p * sum lies within about 1e-6 of a running sum (of vocabularies up to some
- * 200,000 tokens; a thread's share, and with it the error, grows with larger ones).
+ * 200,000 tokens; a thread's share, and with it the error, grows with larger ones)
+ * or its z within 2^-22 |ln(min_p)| of ln(min_p) (the logarithm and its product with T
+ * are fp32; logits of any size are compared with the limit exactly).
  * Results do not depend on timing.
  */
 PKV_API pkv_status pkv_sample_filtered(const float *logits, int32_t batch, int32_t vocab, int64_t row_stride,

@@ -186,6 +186,15 @@ struct Best {
     __device__ __forceinline__ float key() const { return b1 ? composite_x(b1) : -INFINITY; }
 };
 
+// The smallest fp32 number not below M + c in exact arithmetic (c <= 0): the sum rounded to nearest and, where the
+// rounding took it down (its error is exact in fp32), the next one.  A limit on logits, compared as it would be on
+// their differences from M: M + c rounded to nearest is off by half a step of M, 3e-5 for logits near 1000.
+__device__ __forceinline__ float not_below(float M, float c) {
+    const float s = __fadd_rn(M, c), b = __fsub_rn(s, M);
+    const float low = __fadd_rn(__fsub_rn(M, __fsub_rn(s, b)), __fsub_rn(c, b));      // M + c - s
+    return low > 0.f ? nextafterf(s, INFINITY) : s;
+}
+
 // Steps that several ways share are functions, not inlined: a row runs most of this kernel's code once, so its
 // time is in good part that of fetching it.
 
@@ -861,7 +870,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(THREADS, MIN_C
         Z = fixed_of(z);
     }
     // the smallest logit in the race: min-p's limit, and the race's reach
-    const float min_x = fmaxf(mp > 0.f ? fmaf(T, logf(mp), M) : -INFINITY, M - RACE_Z * T);
+    const float min_x = fmaxf(mp > 0.f ? not_below(M, T * logf(mp)) : -INFINITY, M - RACE_Z * T);
     auto depth = [&](float x) { return (M - x) * per_logit; };
     // a logit not above any whose bin is <= b: M minus b + 1 bins and a margin for its own rounding
     auto x_at_end_of = [&](int b) {
