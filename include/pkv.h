@@ -420,7 +420,9 @@ PKV_API pkv_status pkv_decode_fp8(const pkv_bf16 *q, const pkv_e4m3 *k_cache, co
  * A sequence that does not fit total_k or max_seqlen_k records
  * PKV_DEVERR_SEQLENS; its output rows are unspecified.  The result is bit for
  * bit that of pkv_prefill_varlen over a bf16 cache that holds the values read
- * (exact for exponents e >= -117; below that bf16 is subnormal and rounds).
+ * (exact for exponents e >= -117; below that bf16 is subnormal and rounds): fp32
+ * scores and sums, probabilities rounded to bf16 for the product with the values,
+ * 2^-8 of each term at most, where pkv_decode_fp8 rounds to 2^-11.
  */
 PKV_API size_t pkv_prefill_fp8_workspace_size(int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads,
                                       int32_t head_dim, int32_t max_seqlen_q, int32_t max_seqlen_k,
@@ -493,8 +495,9 @@ PKV_API pkv_status pkv_sample_dev(const float *logits, int32_t batch, int32_t vo
  * {seed, offset} from device memory as pkv_sample_dev does.
  * Weights and a thread's sums of them are fp32, joined across threads in a fixed
  * order or in 64-bit fixed point: a token is decided as in exact arithmetic unless
- * top_p * sum lies within about 1e-6 of a running sum (of vocabularies up to some
- * 200,000 tokens; a thread's share, and with it the error, grows with larger ones)
+ * top_p * sum lies within about 1e-6 of a running sum (of vocabularies up to 200,000
+ * tokens in batches of any size; a thread's share, and with it the error, grows with
+ * larger ones, and is largest in batches of more than about 190 rows)
  * or its z within 2^-22 |ln(min_p)| of ln(min_p) (the logarithm and its product with T
  * are fp32; logits of any size are compared with the limit exactly).
  * Results do not depend on timing.

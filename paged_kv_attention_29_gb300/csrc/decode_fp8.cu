@@ -40,10 +40,12 @@
 // alone is 128 bytes at a stride of a token.  A run that crosses a sequence border writes a piece
 // (m, l, o) for each side, and a second kernel merges each head's pieces in run order, so results
 // do not depend on timing.
-// Measured (8 KV heads, groups of 2): batch 64 with 512 to 4096 tokens, 320 MB, 55 us = 5.8 TB/s; 8
-// contexts of 16k to 40k tokens, 461 MB, 75 us = 6.15 TB/s; DRAM reads 1.006 of the bytes.  Taking one
+// Measured (8 KV heads, groups of 2): batch 64 with 512 to 4096 tokens, 320 MB, 56 us = 5.7 TB/s; 8
+// contexts of 16k to 40k tokens, 461 MB, 76.5 us = 6.0 TB/s; DRAM reads 1.006 of the bytes.  Taking one
 // head after the other instead of side by side: 64 and 89 us; with 256-byte L2 promotion on top: 77 and
-// 109.  12 warps x 2 stages: 57 and 78.  530 instructions per chunk, 37% of issue slots.
+// 109.  12 warps x 2 stages: 57 and 78.  535 instructions per chunk, 35% of issue slots.  Where the largest
+// weight is held costs nothing there and, in a graph, 0.5 of 20.5 us with groups of 8 and 14 chunks to a
+// run (37 sequences of 0 to 2999 tokens: 20.0 us at 2^0 with a margin of 2^8, 20.2 at 2^7, 20.3 at 2^11).
 //
 // Each warp owns a ring of shared-memory stages, each holding a chunk's K and V codes (TMA tiles
 // with 128-byte swizzle: conflict-free 16-byte loads below) and its 2 x 32 scale bytes, all

@@ -47,8 +47,8 @@
 //
 // Counts are integers, the weights of every thread are summed in a fixed tree (Z) or in 64-bit fixed
 // point (2^-38), so neither atomics nor the order of the list can change a result.  A thread's share
-// of a sum (37 to 148 weights of a row of 151,936) is fp32: a running sum is within about 1e-6 of
-// itself, and the token at the border is decided as in exact arithmetic except when a border lies
+// of a sum (19, 74 or 148 weights of a row of 151,936, in clusters of 16 x 512, 8 x 256 and 4 x 256
+// threads) is fp32: a running sum is within about 1e-6 of itself at up to 200,000 logits, and the token at the border is decided as in exact arithmetic except when a border lies
 // that near to it.
 //
 // Rows that cannot all run at once are taken in an order that starts the longest first (row_in_order).
@@ -1537,7 +1537,10 @@ pkv_status launch_sample_filtered(const SampleFilteredArgs& a, int* err, cudaStr
     // an SM), as many rows as SMs on clusters of 4.  Rows of 151,936 with settings of their own, us: 8 rows 22 on 16 and
     // 28 on 8, 10 rows 22 and 28, 12 rows 35 and 29; 120 rows 53 on 8 and 70 on 4, 228 rows 84 and 78, 512 rows 162 and
     // 119 (256 rows without filters 109 and 82).  Their order: 120 rows 61 without it, 512 rows 136; equal rows lose
-    // 3 us to it.
+    // 3 us to it.  Other vocabularies, L2 flushed before each call: 262,144 logits 8 rows 29 on 16 and 42 on 8, 12 rows 33
+    // and 40, 190 rows 87 on 8 and 115 on 4, 300 rows 122 and 142; 32,000 logits 8 rows 25 and 24, 10 rows 28 and 24, 120
+    // rows 36 on 8 and 34 on 4, 300 rows 73 and 50.  So the limits, which go by rows alone, are right within a few
+    // us around 151,936 logits, and at 262,144 clusters of 8 would win past 300 rows still.
     constexpr int kWideRows = 10;
     const int sms = sm_count();
     const bool wide = a.batch <= kWideRows, some = 4 * a.batch <= 5 * sms;

@@ -16,7 +16,9 @@
 //
 // Measured on 10,814 tokens of 16 Q and 8 KV heads, 155 MB: 31.3 us = 4.97 TB/s through the ring of
 // bulk copies, 38 us with the next item's loads in registers, 50 us without (one item per warp).
-// 3 stages 33.2 us, 3 CTAs per SM 33.0, items of 8 rows 39.8, of 32 rows 37.0.
+// 3 stages 33.2 us, 3 CTAs per SM 33.0, items of 8 rows 39.8, of 32 rows 37.0.  Issue slots are 53% busy, so
+// they are not the bound.  With two items to a token and an even stride a warp's items are all Q rows or all K
+// and V rows, which do not take equally long: the likely rest.
 #include <cuda_fp8.h>
 
 #include <algorithm>
