@@ -204,3 +204,27 @@ def test_slices_beyond_the_warps_lists(pkv, B, over):
                 k[b], p[b], m[b] = ((0, 1.0, 0.05), (0, 0.9, 0.01), (2000, 0.8, 0.0), (50, 1.0, 0.0), (0, 0.5, 0.2), (30000, 0.95, 0.02),
                                     (0, 1.0, 0.0), (0, 0.999, 0.0))[i - 4]
         check_rows(pkv, x, 0.9, k, p, m, 31, rows)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,vocab", [(5, 7), (40, 3001), (200, 3001), (200, 5)])
+def test_masks_of_the_lowest_finite_value(pkv, B, vocab):
+    """A row that holds nothing but the lowest finite value is a flat row; beside other logits such tokens weigh
+    nothing, like ones at -inf."""
+    r = np.arange(B)
+    lowest = torch.finfo(torch.float32).min
+    T = torch.from_numpy(np.array([0.05, 0.9, 3.0], np.float32)[r % 3]).cuda()
+    k = torch.from_numpy(np.array([0, 0, 2, 3, 1025], np.int32)[r % 5]).cuda()
+    p = torch.from_numpy(np.array([1.0, 0.9, 0.5, 1e-6], np.float32)[r % 4]).cuda()
+    m = torch.from_numpy(np.array([0.0, 0.0, 0.2], np.float32)[r // 2 % 3]).cuda()
+    flat = torch.zeros(B, vocab, device="cuda")
+    args = (T, k, p, m, 51)
+    assert torch.equal(pkv.pkv_sample_filtered(flat, *args), pkv.pkv_sample_filtered(flat + lowest, *args))
+    g = torch.Generator().manual_seed(52)
+    x = torch.randn(B, vocab, generator=g) * 2
+    out = torch.rand(B, vocab, generator=g) < 0.9
+    out[r, r % vocab] = False
+    args = (T, k, p, m, 53)
+    a, b = (pkv.pkv_sample_filtered(x.masked_fill(out, v).cuda(), *args) for v in (lowest, -float("inf")))
+    assert torch.equal(a, b)
+    expect_no_device_error(pkv)
