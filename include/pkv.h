@@ -12,8 +12,9 @@
  *   f2  pkv_rope_store_kvcache  rotary embedding of Q/K fused into the a2 write
  *
  * and, beside them, the same writes and attentions on an 8-bit KV cache
- * (pkv_*_fp8) and sampling among the tokens that top-k, top-p and min-p keep
- * (pkv_sample_filtered).
+ * (pkv_*_fp8), sampling among the tokens that top-k, top-p and min-p keep
+ * (pkv_sample_filtered), and decoding along trees of drafted tokens
+ * (pkv_tree_*) with the block copies of sequences that fork (pkv_copy_blocks).
  *
  * Conventions shared by every call
  * --------------------------------
@@ -82,7 +83,8 @@ enum {
     PKV_DEVERR_TIMEOUT = 5,      /* an mbarrier wait exceeded its limit */
     PKV_DEVERR_BLOCK_TABLE = 6,  /* a position past max_blocks_per_seq * block_size */
     PKV_DEVERR_PLAN = 7,         /* the prefill workspace holds no plan for these arguments */
-    PKV_DEVERR_FILTER = 8        /* top_p outside (0, 1], min_p outside [0, 1], or either NaN */
+    PKV_DEVERR_FILTER = 8,       /* top_p outside (0, 1], min_p outside [0, 1], or either NaN */
+    PKV_DEVERR_TREE = 9          /* an accepted path that does not ascend or leaves its tree */
 };
 
 /* ABI version; bumped on any signature change. */
@@ -511,6 +513,136 @@ PKV_API pkv_status pkv_sample_filtered_dev(const float *logits, int32_t batch, i
                                    const float *temperatures, const int32_t *top_k, const float *top_p,
                                    const float *min_p, const uint64_t *seed_offset, int64_t *out_ids,
                                    pkv_stream_t stream);
+
+/*
+ * Trees of drafted tokens (speculative decoding).  A step drafts n_b tokens for
+ * sequence b, arranged in a tree: node 0 is the token that is certain (the last one
+ * sampled, whose K/V row is new), every other node a guess at what follows its
+ * parent, and a parent comes before its children.  The nodes' K/V rows are
+ * the sequence's last n_b positions in the cache, in node order: with
+ * P_b = context_lens[b] - n_b, node i sits at position P_b + i, whatever its depth.
+ * pkv_slot_mapping (cu_seqlens_q = cu_nodes, context_lens) gives the slots and the
+ * appending calls write them, rotated by P_b + depth, which the caller knows.
+ * One step is: append, pkv_tree_decode per layer, a sampled token per node
+ * (pkv_sample), pkv_tree_accept, pkv_tree_compact.
+ *
+ *   cu_nodes     int32 [batch + 1] running node counts; n_b may be 0 (a sequence
+ *                without drafts, left out)
+ *   context_lens int32 [batch] keys per sequence, its nodes among them
+ *   tree_mask    uint64 [total_nodes, mask_words]: bit j % 64 of word j / 64 of a
+ *                node's row says that the node sees node j of its tree.  For a tree
+ *                these are its ancestors and itself.  Bits at or above n_b have no
+ *                meaning.
+ *   max_nodes    bound on n_b (host-known), at most PKV_MAX_TREE_NODES and at most
+ *                64 * mask_words
+ * A sequence whose counts or lengths break these bounds, or with n_b > context_lens[b],
+ * is left out and PKV_DEVERR_SEQLENS recorded.
+ */
+#define PKV_MAX_TREE_NODES 256
+
+/*
+ * Attention of the nodes: for node i of sequence b,
+ *
+ *   out[i, h] = softmax_j(scale * q[i,h] . k_j) v_j
+ *
+ * over the keys j < P_b and the nodes j of its mask, K/V head
+ * h / (num_heads / num_kv_heads).  A node that sees nothing (P_b = 0 and no bit set)
+ * gets a zero row.  A key that a node does not see has no effect on its row, whatever
+ * its K and V hold, infinities and NaN included.
+ *
+ *   q, out  bf16 [total_nodes, num_heads, head_dim], packed in the order of cu_nodes;
+ *           rows of out behind cu_nodes[batch] and of sequences left out stay as they are
+ *   max_context_len  bound on context_lens (host-known)
+ *   workspace  >= pkv_tree_decode_workspace_size(batch, max_nodes, num_heads, num_kv_heads,
+ *           head_dim) bytes on the current device, 256-byte aligned, no initialisation needed,
+ *           scratch after the call; calls that may overlap need one each
+ * batch <= 4096.  fp32 scores and sums; a key's weight is rounded to bf16 for the product
+ * with the values (2^-8 of itself at most), the output once to bf16.  Deterministic.
+ * pkv_tree_decode_fp8 is the same over an 8-bit cache, bit for bit what pkv_tree_decode gives
+ * over a bf16 cache that holds the values read (scale exponents >= -117).
+ */
+PKV_API size_t pkv_tree_decode_workspace_size(int32_t batch, int32_t max_nodes, int32_t num_heads,
+                                      int32_t num_kv_heads, int32_t head_dim);
+
+PKV_API pkv_status pkv_tree_decode(const pkv_bf16 *q, const pkv_bf16 *k_cache, const pkv_bf16 *v_cache,
+                           const int32_t *block_tables, int32_t max_blocks_per_seq,
+                           const int32_t *context_lens, const int32_t *cu_nodes, const uint64_t *tree_mask,
+                           int32_t mask_words, int32_t batch, int32_t total_nodes, int32_t max_nodes,
+                           int32_t max_context_len, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                           int32_t block_size, int32_t num_blocks, float softmax_scale, pkv_bf16 *out,
+                           void *workspace, size_t workspace_bytes, pkv_stream_t stream);
+
+PKV_API pkv_status pkv_tree_decode_fp8(const pkv_bf16 *q, const pkv_e4m3 *k_cache, const pkv_e4m3 *v_cache,
+                               const pkv_e8m0 *k_scale, const pkv_e8m0 *v_scale, const int32_t *block_tables,
+                               int32_t max_blocks_per_seq, const int32_t *context_lens, const int32_t *cu_nodes,
+                               const uint64_t *tree_mask, int32_t mask_words, int32_t batch, int32_t total_nodes,
+                               int32_t max_nodes, int32_t max_context_len, int32_t num_heads, int32_t num_kv_heads,
+                               int32_t head_dim, int32_t block_size, int32_t num_blocks, float softmax_scale,
+                               pkv_bf16 *out, void *workspace, size_t workspace_bytes, pkv_stream_t stream);
+
+/*
+ * The accepted path: from node 0, as long as a child of the node holds the token that the
+ * model sampled at the node, go to that child (the lowest of several).  A node's parent is
+ * the highest node below it in its mask; a node other than 0 without one is never reached.
+ * With tokens sampled from the model's own distribution at every node (at any temperature) the
+ * accepted tokens are distributed as those of one-by-one decoding.
+ *
+ *   target        int64 [total_nodes] the token sampled at each node (pkv_sample's ids)
+ *   draft         int64 [total_nodes] the token each node stands for
+ *   path          int32 [batch, max_path] output: the path's nodes, node 0 first, cut at
+ *                 max_path >= 1 nodes, -1 behind them
+ *   path_lens     int32 [batch] output: nodes of the path (0 for a sequence without nodes)
+ *   next_tokens   int64 [batch] output: the target of the path's last node, -1 without nodes
+ *   new_context_lens  int32 [batch] output: P_b + path_lens[b], the keys of the sequence once
+ *                 the path's rows are moved together; may not be context_lens itself
+ * A sequence left out for its bounds gets path_lens 0, next_tokens -1 and its old length.
+ */
+PKV_API pkv_status pkv_tree_accept(const int64_t *target, const int64_t *draft, const uint64_t *tree_mask,
+                           int32_t mask_words, const int32_t *cu_nodes, const int32_t *context_lens,
+                           int32_t batch, int32_t total_nodes, int32_t max_nodes, int32_t max_path,
+                           int32_t *path, int32_t *path_lens, int64_t *next_tokens,
+                           int32_t *new_context_lens, pkv_stream_t stream);
+
+/*
+ * Every layer's pools in one call.  k_caches, v_caches, k_scales and v_scales are HOST arrays
+ * of num_layers device pointers (at most PKV_MAX_LAYERS), read before the call returns; all pools
+ * have the same shape.  k_scales and v_scales are both NULL for bf16 pools and both given for 8-bit
+ * ones.  All pools 16-byte aligned, no two the same or overlapping; head_dim = 128.
+ */
+#define PKV_MAX_LAYERS 128
+
+/*
+ * Move the accepted nodes' rows together: the row of node path[b, d] goes to position P_b + d, for
+ * d < path_lens[b], in K and V (and their scales) of every layer.  context_lens and cu_nodes are
+ * those of the step.  A path that does not ascend, or leaves its tree, is not moved and
+ * PKV_DEVERR_TREE recorded (info = sequence).  A block id outside the pool records
+ * PKV_DEVERR_BLOCK_ID and its row stays.  Exact copies.  No two sequences of a call may have a
+ * block of their nodes' rows in common.  batch <= 65535.
+ */
+PKV_API pkv_status pkv_tree_compact(void *const *k_caches, void *const *v_caches, pkv_e8m0 *const *k_scales,
+                            pkv_e8m0 *const *v_scales, int32_t num_layers, const int32_t *block_tables,
+                            int32_t max_blocks_per_seq, const int32_t *context_lens, const int32_t *cu_nodes,
+                            const int32_t *path, const int32_t *path_lens, int32_t batch, int32_t max_path,
+                            int32_t num_blocks, int32_t block_size, int32_t num_kv_heads, int32_t head_dim,
+                            pkv_stream_t stream);
+
+/*
+ * Copy rows of blocks to other blocks in K and V (and their scales) of every layer: a
+ * sequence that forks shares its full blocks and needs a copy of the last, partly filled one;
+ * a pool that is put in order moves blocks.
+ *
+ *   src_blocks, dst_blocks  int32 [num_pairs] block ids; src < 0 skips the pair (padding)
+ *   num_rows  int32 [num_pairs] rows of each block to copy (the first ones), or NULL: all.
+ *             Rows behind them stay as they are in the destination.
+ * A destination may be no other pair's source or destination.  Ids outside the pool record
+ * PKV_DEVERR_BLOCK_ID, row counts outside [0, block_size] PKV_DEVERR_SEQLENS, info = pair, and the
+ * pair is skipped.  Exact copies.  num_pairs <= 65535.
+ */
+PKV_API pkv_status pkv_copy_blocks(void *const *k_caches, void *const *v_caches, pkv_e8m0 *const *k_scales,
+                           pkv_e8m0 *const *v_scales, int32_t num_layers, const int32_t *src_blocks,
+                           const int32_t *dst_blocks, const int32_t *num_rows, int32_t num_pairs,
+                           int32_t num_blocks, int32_t block_size, int32_t num_kv_heads, int32_t head_dim,
+                           pkv_stream_t stream);
 
 /*
  * Read (and optionally clear) the current device's error word.  HOST output

@@ -24,5 +24,7 @@ fp8_cache
     the 8-bit cache's row format (e4m3 codes, a power-of-two scale) and its scatter.
 filtered
     top-k, top-p and min-p before the race.
+tree
+    a step along a tree of drafted tokens: its attention and the accepted path.
 """
-from . import filtered, fp8_cache, paged_attention, rope, sampler  # noqa: F401
+from . import filtered, fp8_cache, paged_attention, rope, sampler, tree  # noqa: F401

@@ -25,6 +25,9 @@ Functions carry the C names:
 ``pkv_*_fp8``              the writes and attentions on an 8-bit KV cache: e4m3
                            pools (``torch.float8_e4m3fn``) with one power-of-two
                            scale per row (``torch.float8_e8m0fnu``)
+``pkv_tree_*``             decoding along a tree of drafted tokens: its attention,
+                           the accepted path, that path's rows moved together
+``pkv_copy_blocks``        rows of blocks copied in every layer (a fork)
 =========================  ================================================
 """
 from __future__ import annotations
@@ -45,6 +48,8 @@ __all__ = [
     "pkv_store_kvcache_fp8", "pkv_rope_store_kvcache_fp8", "pkv_decode_fp8_workspace_size", "decode_fp8_workspace",
     "pkv_decode_fp8", "pkv_prefill_fp8_workspace_size", "prefill_fp8_workspace", "pkv_prefill_varlen_fp8",
     "pkv_sample_filtered", "pkv_sample_filtered_dev",
+    "MAX_TREE_NODES", "MAX_LAYERS", "pkv_tree_decode_workspace_size", "tree_decode_workspace", "pkv_tree_decode",
+    "pkv_tree_decode_fp8", "pkv_tree_accept", "KvPools", "pkv_tree_compact", "pkv_copy_blocks",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -53,7 +58,7 @@ _lib: Optional[ctypes.CDLL] = None
 
 DEVERR = {0: "none", 1: "block id outside pool", 2: "slot outside pool", 3: "sequence lengths",
           4: "temperature", 5: "pipeline wait timed out", 6: "position past block table",
-          7: "no prefill plan for these arguments in the workspace", 8: "sampling filter"}
+          7: "no prefill plan for these arguments in the workspace", 8: "sampling filter", 9: "accepted path"}
 
 _c_int32 = ctypes.c_int32
 _c_int64 = ctypes.c_int64
@@ -131,6 +136,15 @@ def load() -> ctypes.CDLL:
                                                _c_u64, _c_u64, _c_ptr, _c_ptr]),
         "pkv_sample_filtered_dev": (ctypes.c_int, [_c_ptr, _c_int32, _c_int32, _c_int64, _c_ptr, _c_ptr, _c_ptr, _c_ptr,
                                                    _c_ptr, _c_ptr, _c_ptr]),
+        "pkv_tree_decode_workspace_size": (_c_size, [_c_int32] * 5),
+        "pkv_tree_decode": (ctypes.c_int, [_c_ptr] * 4 + [_c_int32] + [_c_ptr] * 3 + [_c_int32] * 10 +
+                            [_c_float, _c_ptr, _c_ptr, _c_size, _c_ptr]),
+        "pkv_tree_decode_fp8": (ctypes.c_int, [_c_ptr] * 6 + [_c_int32] + [_c_ptr] * 3 + [_c_int32] * 10 +
+                                [_c_float, _c_ptr, _c_ptr, _c_size, _c_ptr]),
+        "pkv_tree_accept": (ctypes.c_int, [_c_ptr] * 3 + [_c_int32, _c_ptr, _c_ptr] + [_c_int32] * 4 + [_c_ptr] * 5),
+        "pkv_tree_compact": (ctypes.c_int, [_c_ptr] * 4 + [_c_int32, _c_ptr, _c_int32] + [_c_ptr] * 4 + [_c_int32] * 6 +
+                             [_c_ptr]),
+        "pkv_copy_blocks": (ctypes.c_int, [_c_ptr] * 4 + [_c_int32] + [_c_ptr] * 3 + [_c_int32] * 5 + [_c_ptr]),
         "pkv_get_device_error": (ctypes.c_int, [ctypes.POINTER(_c_int32), ctypes.POINTER(_c_int32), _c_int32]),
         "pkv_check_wait_timeout": (ctypes.c_int, [ctypes.c_void_p]),
     }
@@ -862,6 +876,197 @@ def pkv_check_wait_timeout(stream=None) -> None:
     (about 2 s) and records (DEVERR timeout, WAIT_CHECK_INFO); read it with pkv_get_device_error."""
     with _on_device(stream=stream):
         _raise(load().pkv_check_wait_timeout(_stream(stream)), "pkv_check_wait_timeout")
+
+
+# ---------------------------------------------------------------------------
+# trees of drafted tokens
+# ---------------------------------------------------------------------------
+
+MAX_TREE_NODES = 256
+MAX_LAYERS = 128
+
+
+def pkv_tree_decode_workspace_size(batch: int, max_nodes: int, num_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    return int(load().pkv_tree_decode_workspace_size(batch, max_nodes, num_heads, num_kv_heads, head_dim))
+
+
+def tree_decode_workspace(batch: int, max_nodes: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                          device=None) -> torch.Tensor:
+    """A uint8 device buffer of the size the tree attentions need (256-byte aligned by the allocator)."""
+    device = torch.device(device or "cuda")
+    with torch.cuda.device(device):
+        n = pkv_tree_decode_workspace_size(batch, max_nodes, num_heads, num_kv_heads, head_dim)
+    if n == 0:
+        raise PkvError(2, "pkv_tree_decode_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _tree_call(name, fn, pools, shape, q, block_tables, context_lens, cu_nodes, tree_mask, max_nodes, max_context_len,
+               softmax_scale, out, workspace, stream):
+    nb, bs, hkv, d = shape
+    _want(q, "q", torch.bfloat16, 3)
+    _want(block_tables, "block_tables", torch.int32, 2)
+    _want(context_lens, "context_lens", torch.int32, 1)
+    _want(cu_nodes, "cu_nodes", torch.int32, 1)
+    _want(tree_mask, "tree_mask", torch.int64, 2)
+    total, hq, dq = q.shape
+    batch = context_lens.shape[0]
+    if dq != d or block_tables.shape[0] != batch or cu_nodes.shape[0] != batch + 1 or tree_mask.shape[0] != total:
+        raise ValueError("q, block_tables, context_lens, cu_nodes and tree_mask disagree")
+    if out is None:
+        out = _allocated(stream, torch.empty_like, q, result=True)
+    else:
+        _want(out, "out", torch.bfloat16, 3)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    if workspace is None:
+        workspace = _allocated(stream, tree_decode_workspace, batch, max_nodes, hq, hkv, d, q.device)
+    else:
+        _want(workspace, "workspace", torch.uint8, 1)
+    _launch(name, fn, stream, (q, *pools, block_tables, context_lens, cu_nodes, tree_mask, out, workspace),
+            (q.data_ptr(), *[t.data_ptr() for t in pools], block_tables.data_ptr(), block_tables.shape[1],
+             context_lens.data_ptr(), cu_nodes.data_ptr(), tree_mask.data_ptr(), tree_mask.shape[1], batch, total,
+             int(max_nodes), int(max_context_len), hq, hkv, d, bs, nb, float(softmax_scale), out.data_ptr(),
+             workspace.data_ptr(), workspace.numel()))
+    return out
+
+
+def pkv_tree_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                    context_lens: torch.Tensor, cu_nodes: torch.Tensor, tree_mask: torch.Tensor, max_nodes: int,
+                    max_context_len: int, softmax_scale: float, out: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of drafted tokens, a tree per sequence, whose K/V rows are the sequence's last positions.
+
+    q [total_nodes, num_heads, 128] holds the nodes of all sequences, ``cu_nodes`` (int32 [batch + 1]) apart;
+    ``tree_mask`` (int64 [total_nodes, words]) has bit j of a node set where it sees node j of its own tree.
+    Rows behind cu_nodes[-1] are left as they were in ``out``."""
+    _check(k_cache, "k_cache", torch.bfloat16, 4)
+    _want(v_cache, "v_cache", torch.bfloat16, 4)
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache shapes differ")
+    return _tree_call("pkv_tree_decode", load().pkv_tree_decode, (k_cache, v_cache), k_cache.shape, q, block_tables,
+                      context_lens, cu_nodes, tree_mask, max_nodes, max_context_len, softmax_scale, out, workspace, stream)
+
+
+def pkv_tree_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                        v_scale: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                        cu_nodes: torch.Tensor, tree_mask: torch.Tensor, max_nodes: int, max_context_len: int,
+                        softmax_scale: float, out: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """pkv_tree_decode over an 8-bit cache."""
+    shape = _pools_fp8(k_cache, v_cache, k_scale, v_scale)
+    return _tree_call("pkv_tree_decode_fp8", load().pkv_tree_decode_fp8, (k_cache, v_cache, k_scale, v_scale), shape, q,
+                      block_tables, context_lens, cu_nodes, tree_mask, max_nodes, max_context_len, softmax_scale, out,
+                      workspace, stream)
+
+
+def pkv_tree_accept(target: torch.Tensor, draft: torch.Tensor, tree_mask: torch.Tensor, cu_nodes: torch.Tensor,
+                    context_lens: torch.Tensor, max_nodes: int, max_path: int, path: Optional[torch.Tensor] = None,
+                    path_lens: Optional[torch.Tensor] = None, next_tokens: Optional[torch.Tensor] = None,
+                    new_context_lens: Optional[torch.Tensor] = None, stream=None):
+    """The path of each tree along which every draft is the token sampled at its parent.
+
+    ``target`` (what pkv_sample returned for the nodes' logits) and ``draft`` are int64 [total_nodes].  Returns
+    (path int32 [batch, max_path] padded with -1, path_lens int32, next_tokens int64, new_context_lens int32)."""
+    _check(target, "target", torch.int64, 1)
+    _want(draft, "draft", torch.int64, 1)
+    _want(tree_mask, "tree_mask", torch.int64, 2)
+    _want(cu_nodes, "cu_nodes", torch.int32, 1)
+    _want(context_lens, "context_lens", torch.int32, 1)
+    total, batch, max_path = target.shape[0], context_lens.shape[0], int(max_path)
+    if draft.shape[0] != total or tree_mask.shape[0] != total or cu_nodes.shape[0] != batch + 1:
+        raise ValueError("target, draft, tree_mask, cu_nodes and context_lens disagree")
+    if max_path < 1:
+        raise ValueError("max_path must be at least 1")
+    outs = []
+    for name, t, dtype, shape in (("path", path, torch.int32, (batch, max_path)), ("path_lens", path_lens, torch.int32, (batch,)),
+                                  ("next_tokens", next_tokens, torch.int64, (batch,)),
+                                  ("new_context_lens", new_context_lens, torch.int32, (batch,))):
+        if t is None:
+            t = _allocated(stream, torch.empty, shape, dtype=dtype, device=target.device, result=True)
+        else:
+            _want(t, name, dtype, len(shape))
+            if t.shape != shape:
+                raise ValueError(f"{name} must be {list(shape)}")
+        outs.append(t)
+    _launch("pkv_tree_accept", load().pkv_tree_accept, stream, (target, draft, tree_mask, cu_nodes, context_lens, *outs),
+            (target.data_ptr(), draft.data_ptr(), tree_mask.data_ptr(), tree_mask.shape[1], cu_nodes.data_ptr(),
+             context_lens.data_ptr(), batch, total, int(max_nodes), max_path, *[t.data_ptr() for t in outs]))
+    return tuple(outs)
+
+
+class KvPools:
+    """Every layer's pools, checked and marshalled once, for the calls that work on all layers.
+
+    ``k_caches`` and ``v_caches`` are lists of a layer's pools each, bf16 or (with ``k_scales`` and ``v_scales``)
+    8-bit, all of one shape, on one device and without overlap.  The object keeps the tensors alive."""
+
+    def __init__(self, k_caches, v_caches, k_scales=None, v_scales=None):
+        if (k_scales is None) != (v_scales is None):
+            raise ValueError("k_scales and v_scales are given together or not at all")
+        lists = [list(x) for x in (k_caches, v_caches, k_scales, v_scales) if x is not None]
+        n = len(lists[0])
+        if n == 0 or n > MAX_LAYERS or any(len(x) != n for x in lists):
+            raise ValueError(f"every list must hold one pool per layer, 1 to {MAX_LAYERS} layers")
+        for i in range(n):
+            if k_scales is None:
+                shape = _pool_shape(lists[0][i])
+                _check(lists[1][i], "v_cache", torch.bfloat16, 4)
+                if lists[1][i].shape != shape:
+                    raise ValueError("k_cache and v_cache shapes differ")
+            else:
+                shape = _pools_fp8(*(x[i] for x in lists))
+            if i and tuple(shape) != self.shape:
+                raise ValueError("all layers' pools must have one shape")
+            self.shape = tuple(shape)
+        every = [t for x in lists for t in x]
+        if any(t.device != every[0].device for t in every):
+            raise ValueError("all pools must be on one device")
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in every)
+        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+            raise ValueError("pools overlap")
+        self.num_layers = n
+        self.tensors = every
+        self._arrays = [(ctypes.c_void_p * n)(*[t.data_ptr() for t in x]) for x in lists]
+        self._args = tuple(ctypes.addressof(x) for x in self._arrays) + (None,) * (4 - len(lists)) + (n,)
+
+
+def pkv_tree_compact(pools: KvPools, block_tables: torch.Tensor, context_lens: torch.Tensor, cu_nodes: torch.Tensor,
+                     path: torch.Tensor, path_lens: torch.Tensor, stream=None) -> None:
+    """Move the accepted nodes' rows together, in every layer: node path[b, d] to the d-th position behind the
+    context.  ``context_lens`` and ``cu_nodes`` are those of the step whose nodes they are."""
+    _want(block_tables, "block_tables", torch.int32, 2)
+    _want(context_lens, "context_lens", torch.int32, 1)
+    _want(cu_nodes, "cu_nodes", torch.int32, 1)
+    _want(path, "path", torch.int32, 2)
+    _want(path_lens, "path_lens", torch.int32, 1)
+    batch = context_lens.shape[0]
+    if block_tables.shape[0] != batch or cu_nodes.shape[0] != batch + 1 or path.shape[0] != batch or path_lens.shape[0] != batch:
+        raise ValueError("block_tables, context_lens, cu_nodes, path and path_lens disagree")
+    nb, bs, hkv, d = pools.shape
+    _launch("pkv_tree_compact", load().pkv_tree_compact, stream,
+            (pools.tensors[0], block_tables, context_lens, cu_nodes, path, path_lens),
+            (*pools._args, block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), cu_nodes.data_ptr(),
+             path.data_ptr(), path_lens.data_ptr(), batch, path.shape[1], nb, bs, hkv, d))
+
+
+def pkv_copy_blocks(pools: KvPools, src_blocks: torch.Tensor, dst_blocks: torch.Tensor,
+                    num_rows: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Copy the first num_rows[i] rows (None: all) of block src_blocks[i] to block dst_blocks[i], in every layer;
+    a negative source skips the pair.  No destination may be another pair's source or destination."""
+    _want(src_blocks, "src_blocks", torch.int32, 1)
+    _want(dst_blocks, "dst_blocks", torch.int32, 1)
+    tensors = (pools.tensors[0], src_blocks, dst_blocks)
+    n = src_blocks.shape[0]
+    if num_rows is not None:
+        _want(num_rows, "num_rows", torch.int32, 1)
+        tensors += (num_rows,)
+    if dst_blocks.shape[0] != n or (num_rows is not None and num_rows.shape[0] != n):
+        raise ValueError("src_blocks, dst_blocks and num_rows disagree on the number of pairs")
+    nb, bs, hkv, d = pools.shape
+    _launch("pkv_copy_blocks", load().pkv_copy_blocks, stream, tensors,
+            (*pools._args, src_blocks.data_ptr(), dst_blocks.data_ptr(), None if num_rows is None else num_rows.data_ptr(),
+             n, nb, bs, hkv, d))
 
 
 def pkv_get_device_error(clear: bool = True):

@@ -712,6 +712,198 @@ pkv_status pkv_check_wait_timeout(pkv_stream_t stream) {
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
+namespace {
+
+// Host checks and argument packing shared by the two tree attentions; scales are the 8-bit one's.
+pkv_status tree_decode_call(const pkv_bf16* q, const void* k_cache, const void* v_cache, bool fp8, const pkv_e8m0* k_scale,
+                            const pkv_e8m0* v_scale, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                            const int32_t* context_lens, const int32_t* cu_nodes, const uint64_t* tree_mask,
+                            int32_t mask_words, int32_t batch, int32_t total_nodes, int32_t max_nodes,
+                            int32_t max_context_len, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                            int32_t block_size, int32_t num_blocks, float softmax_scale, pkv_bf16* out, void* workspace,
+                            size_t workspace_bytes, pkv_stream_t stream) {
+    if (batch < 0 || total_nodes < 0 || max_nodes < 0 || mask_words < 0 || max_blocks_per_seq <= 0 || num_blocks <= 0 ||
+        max_context_len < 0 || !(softmax_scale > 0.f) || softmax_scale == INFINITY)
+        return PKV_ERR_INVALID_ARG;
+    if (!supported_shape(num_heads, num_kv_heads, head_dim, block_size)) return PKV_ERR_UNSUPPORTED;
+    if (max_nodes > kMaxTreeNodes || batch > 4096) return PKV_ERR_UNSUPPORTED;
+    if (max_nodes > 64 * static_cast<int64_t>(mask_words)) return PKV_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(max_blocks_per_seq) * block_size > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
+    if (batch == 0 || total_nodes == 0 || max_nodes == 0) return PKV_OK;
+    if (!q || !k_cache || !v_cache || (fp8 && (!k_scale || !v_scale)) || !block_tables || !context_lens || !cu_nodes || !tree_mask || !out)
+        return PKV_ERR_INVALID_ARG;
+    if (misaligned16(q, out, k_cache, v_cache) || misaligned16(k_scale, v_scale)) return PKV_ERR_UNSUPPORTED;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255) return PKV_ERR_WORKSPACE;
+    int* err = device_error_word();
+    if (!err) return PKV_ERR_CUDA;
+    TreeDecodeArgs a;
+    a.q = q;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.cu_nodes = cu_nodes;
+    a.tree_mask = tree_mask;
+    a.out = out;
+    a.max_blocks = max_blocks_per_seq;
+    a.batch = batch;
+    a.total_nodes = total_nodes;
+    a.max_nodes = max_nodes;
+    a.mask_words = mask_words;
+    a.max_context = max_context_len;
+    a.num_heads = num_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.block_size = block_size;
+    a.num_blocks = num_blocks;
+    a.softmax_scale = softmax_scale;
+    a.workspace = workspace;
+    a.workspace_bytes = workspace_bytes;
+    return launch_tree_decode(a, err, as_stream(stream));
+}
+
+// Fills the table of every layer's pools; PKV_OK, or what is wrong with them.
+pkv_status pool_table(void* const* k_caches, void* const* v_caches, pkv_e8m0* const* k_scales, pkv_e8m0* const* v_scales,
+                      int32_t num_layers, int32_t num_blocks, int32_t block_size, int32_t num_kv_heads, int32_t head_dim,
+                      PoolTable& t, int& row_bytes) {
+    if (num_layers < 0 || num_blocks <= 0 || block_size <= 0 || num_kv_heads <= 0 || head_dim <= 0) return PKV_ERR_INVALID_ARG;
+    if ((k_scales == nullptr) != (v_scales == nullptr)) return PKV_ERR_INVALID_ARG;
+    if (head_dim != kHeadDim || block_size % kBlockQuantum || num_layers > kMaxLayers || num_kv_heads > 4096) return PKV_ERR_UNSUPPORTED;
+    if (num_layers > 0 && (!k_caches || !v_caches)) return PKV_ERR_INVALID_ARG;
+    t = PoolTable{};
+    t.layers = num_layers;
+    for (int i = 0; i < num_layers; ++i) {
+        t.k[i] = k_caches[i];
+        t.v[i] = v_caches[i];
+        t.k_scale[i] = k_scales ? k_scales[i] : nullptr;
+        t.v_scale[i] = v_scales ? v_scales[i] : nullptr;
+        if (!t.k[i] || !t.v[i] || (k_scales && (!t.k_scale[i] || !t.v_scale[i]))) return PKV_ERR_INVALID_ARG;
+        if (misaligned16(t.k[i], t.v[i], t.k_scale[i], t.v_scale[i])) return PKV_ERR_UNSUPPORTED;
+    }
+    row_bytes = num_kv_heads * head_dim * (k_scales ? 1 : 2);
+    return PKV_OK;
+}
+
+}  // namespace
+
+size_t pkv_tree_decode_workspace_size(int32_t batch, int32_t max_nodes, int32_t num_heads, int32_t num_kv_heads,
+                                      int32_t head_dim) {
+    if (batch < 0 || max_nodes < 0 || max_nodes > kMaxTreeNodes || !supported_shape(num_heads, num_kv_heads, head_dim, kBlockQuantum))
+        return 0;
+    if (sm_count() <= 0) return 0;
+    return tree_decode_workspace_bytes();
+}
+
+pkv_status pkv_tree_decode(const pkv_bf16* q, const pkv_bf16* k_cache, const pkv_bf16* v_cache, const int32_t* block_tables,
+                           int32_t max_blocks_per_seq, const int32_t* context_lens, const int32_t* cu_nodes,
+                           const uint64_t* tree_mask, int32_t mask_words, int32_t batch, int32_t total_nodes,
+                           int32_t max_nodes, int32_t max_context_len, int32_t num_heads, int32_t num_kv_heads,
+                           int32_t head_dim, int32_t block_size, int32_t num_blocks, float softmax_scale, pkv_bf16* out,
+                           void* workspace, size_t workspace_bytes, pkv_stream_t stream) {
+    return tree_decode_call(q, k_cache, v_cache, false, nullptr, nullptr, block_tables, max_blocks_per_seq, context_lens, cu_nodes,
+                            tree_mask, mask_words, batch, total_nodes, max_nodes, max_context_len, num_heads, num_kv_heads, head_dim,
+                            block_size, num_blocks, softmax_scale, out, workspace, workspace_bytes, stream);
+}
+
+pkv_status pkv_tree_decode_fp8(const pkv_bf16* q, const pkv_e4m3* k_cache, const pkv_e4m3* v_cache, const pkv_e8m0* k_scale,
+                               const pkv_e8m0* v_scale, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                               const int32_t* context_lens, const int32_t* cu_nodes, const uint64_t* tree_mask,
+                               int32_t mask_words, int32_t batch, int32_t total_nodes, int32_t max_nodes,
+                               int32_t max_context_len, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                               int32_t block_size, int32_t num_blocks, float softmax_scale, pkv_bf16* out, void* workspace,
+                               size_t workspace_bytes, pkv_stream_t stream) {
+    return tree_decode_call(q, k_cache, v_cache, true, k_scale, v_scale, block_tables, max_blocks_per_seq, context_lens, cu_nodes,
+                            tree_mask, mask_words, batch, total_nodes, max_nodes, max_context_len, num_heads, num_kv_heads, head_dim,
+                            block_size, num_blocks, softmax_scale, out, workspace, workspace_bytes, stream);
+}
+
+pkv_status pkv_tree_accept(const int64_t* target, const int64_t* draft, const uint64_t* tree_mask, int32_t mask_words,
+                           const int32_t* cu_nodes, const int32_t* context_lens, int32_t batch, int32_t total_nodes,
+                           int32_t max_nodes, int32_t max_path, int32_t* path, int32_t* path_lens, int64_t* next_tokens,
+                           int32_t* new_context_lens, pkv_stream_t stream) {
+    if (batch < 0 || total_nodes < 0 || max_nodes < 0 || mask_words < 0 || max_path <= 0) return PKV_ERR_INVALID_ARG;
+    if (max_nodes > kMaxTreeNodes) return PKV_ERR_UNSUPPORTED;
+    if (max_nodes > 64 * static_cast<int64_t>(mask_words)) return PKV_ERR_INVALID_ARG;
+    if (batch == 0) return PKV_OK;
+    if (!cu_nodes || !context_lens || !path || !path_lens || !next_tokens || !new_context_lens) return PKV_ERR_INVALID_ARG;
+    if (total_nodes > 0 && (!target || !draft || !tree_mask)) return PKV_ERR_INVALID_ARG;
+    if (new_context_lens == context_lens) return PKV_ERR_INVALID_ARG;
+    int* err = device_error_word();
+    if (!err) return PKV_ERR_CUDA;
+    TreeAcceptArgs a;
+    a.target = target;
+    a.draft = draft;
+    a.tree_mask = tree_mask;
+    a.cu_nodes = cu_nodes;
+    a.context_lens = context_lens;
+    a.path = path;
+    a.path_lens = path_lens;
+    a.next_tokens = next_tokens;
+    a.new_context_lens = new_context_lens;
+    a.batch = batch;
+    a.total_nodes = total_nodes;
+    a.max_nodes = max_nodes;
+    a.mask_words = mask_words;
+    a.max_path = max_path;
+    return launch_tree_accept(a, err, as_stream(stream)) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status pkv_tree_compact(void* const* k_caches, void* const* v_caches, pkv_e8m0* const* k_scales, pkv_e8m0* const* v_scales,
+                            int32_t num_layers, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                            const int32_t* context_lens, const int32_t* cu_nodes, const int32_t* path, const int32_t* path_lens,
+                            int32_t batch, int32_t max_path, int32_t num_blocks, int32_t block_size, int32_t num_kv_heads,
+                            int32_t head_dim, pkv_stream_t stream) {
+    if (batch < 0 || max_path < 0 || max_blocks_per_seq <= 0) return PKV_ERR_INVALID_ARG;
+    PoolTable pools;
+    TreeCompactArgs a;
+    const pkv_status s = pool_table(k_caches, v_caches, k_scales, v_scales, num_layers, num_blocks, block_size, num_kv_heads, head_dim,
+                                    pools, a.row_bytes);
+    if (s != PKV_OK) return s;
+    if (batch > 65535) return PKV_ERR_UNSUPPORTED;
+    if (batch == 0 || num_layers == 0 || max_path == 0) return PKV_OK;
+    if (!block_tables || !context_lens || !cu_nodes || !path || !path_lens) return PKV_ERR_INVALID_ARG;
+    int* err = device_error_word();
+    if (!err) return PKV_ERR_CUDA;
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.cu_nodes = cu_nodes;
+    a.path = path;
+    a.path_lens = path_lens;
+    a.max_blocks = max_blocks_per_seq;
+    a.batch = batch;
+    a.max_path = max_path;
+    a.block_size = block_size;
+    a.num_blocks = num_blocks;
+    a.num_kv_heads = num_kv_heads;
+    return launch_tree_compact(pools, a, err, as_stream(stream)) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status pkv_copy_blocks(void* const* k_caches, void* const* v_caches, pkv_e8m0* const* k_scales, pkv_e8m0* const* v_scales,
+                           int32_t num_layers, const int32_t* src_blocks, const int32_t* dst_blocks, const int32_t* num_rows,
+                           int32_t num_pairs, int32_t num_blocks, int32_t block_size, int32_t num_kv_heads, int32_t head_dim,
+                           pkv_stream_t stream) {
+    if (num_pairs < 0) return PKV_ERR_INVALID_ARG;
+    PoolTable pools;
+    CopyBlocksArgs a;
+    const pkv_status s = pool_table(k_caches, v_caches, k_scales, v_scales, num_layers, num_blocks, block_size, num_kv_heads, head_dim,
+                                    pools, a.row_bytes);
+    if (s != PKV_OK) return s;
+    if (num_pairs > 65535) return PKV_ERR_UNSUPPORTED;
+    if (num_pairs == 0 || num_layers == 0) return PKV_OK;
+    if (!src_blocks || !dst_blocks) return PKV_ERR_INVALID_ARG;
+    int* err = device_error_word();
+    if (!err) return PKV_ERR_CUDA;
+    a.src = src_blocks;
+    a.dst = dst_blocks;
+    a.rows = num_rows;
+    a.pairs = num_pairs;
+    a.block_size = block_size;
+    a.num_blocks = num_blocks;
+    a.num_kv_heads = num_kv_heads;
+    return launch_copy_blocks(pools, a, err, as_stream(stream)) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
 pkv_status pkv_get_device_error(int32_t* code, int32_t* info, int32_t clear) {
     if (!code || !info) return PKV_ERR_INVALID_ARG;
     if (cudaDeviceSynchronize() != cudaSuccess) return PKV_ERR_CUDA;

@@ -4,6 +4,7 @@
 
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <stdint.h>
 
 #include "../../include/pkv.h"
@@ -406,6 +407,15 @@ __device__ __forceinline__ void f16_of_codes(uint32_t w, uint32_t& lo, uint32_t&
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
         "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
         : "=r"(lo), "=r"(hi) : "r"(w));
+}
+
+// Four e4m3 codes times f (a power of two), as four bf16.
+__device__ __forceinline__ uint2 bf16_of_codes(uint32_t w, float f) {
+    uint32_t a, b;
+    f16_of_codes(w, a, b);
+    const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&a));
+    const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&b));
+    return make_uint2(pack_bf16x2(lo.x * f, lo.y * f), pack_bf16x2(hi.x * f, hi.y * f));
 }
 
 // An E8M0 byte's exponent as fp32 (NaN for 255), and its value 2^exponent.

@@ -27,7 +27,7 @@ int sm_count();
 // current device once (thread-safe; a failed set-up is retried on the next
 // call) and returns whether the set-up for `key` has succeeded on this device.
 enum SetupKey { kSetupDecode = 0, kSetupPrefill, kSetupRopeStore, kSetupDecodeFp8, kSetupSampleFiltered, kSetupStoreFp8,
-                kSetupStoreFp8Rope, kNumSetupKeys };
+                kSetupStoreFp8Rope, kSetupTreeDecode, kNumSetupKeys };
 bool setup_once(SetupKey key, bool (*setup)());
 
 // cuTensorMapEncodeTiled through the runtime's driver entry point.
@@ -217,5 +217,80 @@ struct SampleFilteredArgs {
     int batch, vocab;
 };
 pkv_status launch_sample_filtered(const SampleFilteredArgs& a, int* err, cudaStream_t stream);
+
+// ---- trees of drafted tokens ------------------------------------------------------
+constexpr int kMaxTreeNodes = 256;
+constexpr int kMaxLayers = PKV_MAX_LAYERS;
+
+struct TreeDecodeArgs {
+    const uint16_t* q;
+    const void* k_cache;
+    const void* v_cache;
+    const uint8_t* k_scale;       // nullptr: bf16 cache
+    const uint8_t* v_scale;
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    const int32_t* cu_nodes;
+    const uint64_t* tree_mask;
+    uint16_t* out;
+    int max_blocks;
+    int batch;
+    int total_nodes;
+    int max_nodes;
+    int mask_words;
+    int max_context;
+    int num_heads;
+    int num_kv_heads;
+    int block_size;
+    int num_blocks;
+    float softmax_scale;
+    void* workspace;
+    size_t workspace_bytes;
+};
+size_t tree_decode_workspace_bytes();
+pkv_status launch_tree_decode(const TreeDecodeArgs& a, int* err, cudaStream_t stream);
+
+struct TreeAcceptArgs {
+    const int64_t* target;
+    const int64_t* draft;
+    const uint64_t* tree_mask;
+    const int32_t* cu_nodes;
+    const int32_t* context_lens;
+    int32_t* path;
+    int32_t* path_lens;
+    int64_t* next_tokens;
+    int32_t* new_context_lens;
+    int batch, total_nodes, max_nodes, mask_words, max_path;
+};
+cudaError_t launch_tree_accept(const TreeAcceptArgs& a, int* err, cudaStream_t stream);
+
+// Every layer's pools, as a kernel argument.
+struct PoolTable {
+    void* k[kMaxLayers];
+    void* v[kMaxLayers];
+    uint8_t* k_scale[kMaxLayers];
+    uint8_t* v_scale[kMaxLayers];
+    int layers;
+};
+
+struct TreeCompactArgs {
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    const int32_t* cu_nodes;
+    const int32_t* path;
+    const int32_t* path_lens;
+    int max_blocks, batch, max_path, block_size, num_blocks, num_kv_heads;
+    int row_bytes;                // K or V of one token, all KV heads
+};
+cudaError_t launch_tree_compact(const PoolTable& pools, const TreeCompactArgs& a, int* err, cudaStream_t stream);
+
+struct CopyBlocksArgs {
+    const int32_t* src;
+    const int32_t* dst;
+    const int32_t* rows;          // nullptr: whole blocks
+    int pairs, block_size, num_blocks, num_kv_heads;
+    int row_bytes;
+};
+cudaError_t launch_copy_blocks(const PoolTable& pools, const CopyBlocksArgs& a, int* err, cudaStream_t stream);
 
 }  // namespace pkv

@@ -65,15 +65,6 @@ __device__ __forceinline__ int keys_of(const DecodeTilesParams& p, const int32_t
     return within && need <= p.max_tiles && first + need <= p.num_tiles ? static_cast<int>(kl) : -1;
 }
 
-// Four e4m3 codes times f (a power of two), as four bf16.
-__device__ __forceinline__ uint2 bf16_of_codes(uint32_t w, float f) {
-    uint32_t a, b;
-    f16_of_codes(w, a, b);
-    const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&a));
-    const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&b));
-    return make_uint2(pack_bf16x2(lo.x * f, lo.y * f), pack_bf16x2(hi.x * f, hi.y * f));
-}
-
 // Started beside the plan (which it does not read) by programmatic launch; it ends after the plan has, so
 // the attention kernel, which waits for this one, finds both done.
 __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) decode_tiles_kernel(const DecodeTilesParams p) {

@@ -1,0 +1,880 @@
+// Attention of a tree of drafted tokens over the paged KV cache, on tcgen05
+// tensor cores: the verification step of tree-structured speculative decoding,
+// on the bf16 cache and on the 8-bit one.
+//
+// Sequence b has n_b nodes; their K/V rows are its last n_b positions, behind the
+// P_b = L_b - n_b positions every node sees.  Node i also sees node j iff bit j of its
+// mask is set:
+//
+//   out[i] = softmax_j(scale q_i . k_j) v_j   over j < P_b and the nodes of i's mask
+//
+// Unit: one sequence, one KV head and one tile of 128 / G nodes x the G query heads
+// that share it (row r of the tile: node r / G, head G g + r % G).  Its keys go by in
+// tiles of 64:
+//
+//   S = Q K^T   tcgen05.mma M=128 N=64, fp32 in TMEM, two buffers
+//   P           masked online softmax by the warpgroup, bf16 over S
+//   O += P V    tcgen05.mma with P from TMEM
+//
+// All units' tiles, in order, are cut into equal runs, one per CTA (two CTAs per SM, so
+// that one's loads and products fill the other's waits): a unit that a run does not
+// hold whole leaves fp32 partial sums with their maxima in the workspace, and a second
+// kernel joins them in the order of the runs.  Results are deterministic.
+//
+// A node's row is as if masked keys were not there, whatever they hold: scores are
+// selected, not added to, and infinities and NaN among the nodes' V rows, which a
+// product with a weight of 0 would spread, are taken out of the tile and given back
+// to the rows that see them.
+//
+// Warps 0-3: softmax and epilogue (TMEM lanes 0-127).  bf16 cache: warp 4 TMA producer,
+// warp 5 TMEM allocation and MMA issue.  8-bit cache: warps 4-7 load codes into
+// registers and write them, as the bf16 values they stand for, to the tiles in shared
+// memory; warp 8 issues.
+#include <algorithm>
+
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+
+namespace pkv {
+namespace {
+
+constexpr int D = kHeadDim;
+constexpr int ROWS = 128;                    // MMA M
+constexpr int KT = 64;                       // keys per tile
+constexpr int Q_HALF = ROWS * 64 * 2;        // 128B-swizzled box of 64 dims: 16 KiB of Q
+constexpr int KV_HALF = KT * 64 * 2;         // 8 KiB of K or V
+constexpr int KV_TILE = 2 * KV_HALF;
+constexpr int SLOTS = 5;                     // ring of K and V tiles
+constexpr int TMEM_COLS = 256;
+constexpr int O_COL = 128;                   // S / P buffers at columns 0 and 64
+constexpr float kRescaleLog2 = 8.0f;
+constexpr int MIN_RUN = 4;                   // tiles a CTA takes at least
+constexpr int CTAS_PER_SM = 2;
+
+constexpr int SM_Q = 0;
+constexpr int SM_KV = 2 * Q_HALF;
+constexpr int SM_BAR = SM_KV + SLOTS * KV_TILE;
+enum {
+    BAR_FULL = 0, BAR_EMPTY = BAR_FULL + SLOTS, BAR_QF = BAR_EMPTY + SLOTS, BAR_QE, BAR_SF, BAR_PF = BAR_SF + 2,
+    BAR_PV = BAR_PF + 2, BAR_OF, BAR_OE, BAR_WG, BAR_DRAIN, NUM_BARS
+};
+constexpr int SM_MISC = (SM_BAR + NUM_BARS * 8 + 15) & ~15;      // [0] TMEM base, [1] abort, [2..9] nodes with infinities or NaN in V
+constexpr int SM_SCAN = SM_MISC + 48;                            // 16 x int64: set-up sums; then the run's start
+constexpr int SMEM_BYTES = SM_SCAN + 16 * 8;
+static_assert(CTAS_PER_SM * (SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs share an SM's shared memory");
+
+struct Params {
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    const int32_t* cu_nodes;
+    const unsigned long long* mask;
+    uint16_t* out;
+    float4* part_o;           // [CTA][2][32][128]: four columns of each row
+    float2* part_ml;          // [CTA][2][128]: maximum (log2) and sum
+    int4* meta;               // [CTA]: {last CTA of the unit that continues behind this one's run or -1, first row's node, nodes, KV head}
+    const uint8_t* k_codes;   // 8-bit cache
+    const uint8_t* v_codes;
+    const uint8_t* k_scale;
+    const uint8_t* v_scale;
+    const uint16_t* v_cache;  // bf16 cache, for the values taken out of a tile
+    int batch, max_blocks, num_heads, num_kv_heads, lg, block_size, num_blocks;
+    int max_nodes, max_context, mask_words, total_nodes;
+    float scale_log2;
+    int* err;
+};
+
+struct Ctl {
+    volatile uint32_t* abort;
+    int* err;
+};
+
+// Waits for a phase, asleep between tries; gives up when another warp has, or after the limit.
+__device__ __forceinline__ bool wait_phase(const Ctl& c, uint32_t bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = global_ns();
+    while (true) {
+        if (mbar_try_wait_sleep(bar, parity, 500000u)) return true;
+        if (*c.abort) return false;
+        if (global_ns() - t0 > kWaitLimitNs) {
+            *c.abort = 1u;
+            record_error(c.err, PKV_DEVERR_TIMEOUT, static_cast<int>(blockIdx.x));
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ bool wait_warp(const Ctl& c, uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait_phase(c, bar, parity));
+}
+__device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity) {
+    const unsigned long long t0 = global_ns();
+    while (!mbar_try_wait_sleep(bar, parity, 500000u))
+        if (global_ns() - t0 > kWaitLimitNs) return false;
+    return true;
+}
+
+struct Seq {
+    int q0, n, len;       // first node's row, nodes (0: nothing to do), keys
+    bool bad;
+};
+__device__ __forceinline__ Seq sequence(const Params& p, int b) {
+    Seq s;
+    s.q0 = __ldg(p.cu_nodes + b);
+    const int q1 = __ldg(p.cu_nodes + b + 1);
+    s.len = __ldg(p.context_lens + b);
+    const long long n = static_cast<long long>(q1) - s.q0;
+    const bool fits = s.q0 >= 0 && n > 0 && q1 <= p.total_nodes && n <= p.max_nodes && n <= s.len && s.len <= p.max_context &&
+                      s.len <= static_cast<long long>(p.max_blocks) * p.block_size;
+    s.bad = n != 0 && !fits;
+    s.n = fits ? static_cast<int>(n) : 0;
+    return s;
+}
+__device__ __forceinline__ long long tiles_of(const Params& p, const Seq& s) {
+    const int qtok = ROWS >> p.lg;
+    return s.n ? static_cast<long long>((s.len + KT - 1) / KT) * ((s.n + qtok - 1) / qtok) * p.num_kv_heads : 0;
+}
+
+// A CTA's run of tiles, segment by segment: tiles [j0, j1) of the unit (sequence b, KV head g, row tile rt).
+// Every role walks by itself.
+struct Walk {
+    const Params& p;
+    Seq s;
+    int b, g, rt, nt, nrt, j0, j1;
+    long long left;
+
+    __device__ __forceinline__ Walk(const Params& params, int b0, long long off, long long count) : p(params), b(b0), left(count) {
+        g = rt = j0 = j1 = nt = nrt = 0;
+        if (left <= 0) return;
+        enter();
+        const int unit = static_cast<int>(off / nt);
+        j0 = static_cast<int>(off - static_cast<long long>(unit) * nt);
+        g = unit / nrt;
+        rt = unit - g * nrt;
+        clip();
+    }
+    __device__ __forceinline__ void enter() {
+        s = sequence(p, b);
+        const int qtok = ROWS >> p.lg;
+        nt = (s.len + KT - 1) / KT;
+        nrt = (s.n + qtok - 1) / qtok;
+    }
+    __device__ __forceinline__ void clip() { j1 = static_cast<int>(min(static_cast<long long>(nt), j0 + left)); }
+    __device__ __forceinline__ bool more() const { return left > 0; }
+    __device__ __forceinline__ void next() {
+        left -= j1 - j0;
+        if (left <= 0) return;
+        j0 = 0;
+        if (++rt == nrt) {
+            rt = 0;
+            if (++g == p.num_kv_heads) {
+                g = 0;
+                do {
+                    if (++b >= p.batch) {
+                        left = 0;
+                        return;
+                    }
+                    enter();
+                } while (s.n == 0);
+            }
+        }
+        clip();
+    }
+    __device__ __forceinline__ int tokens() const { return min(ROWS >> p.lg, s.n - rt * (ROWS >> p.lg)); }
+    // row of the pool (block * block_size + offset) where the keys of tile j start; negative: no such block
+    __device__ __forceinline__ int block_of(int j, int& off) const {
+        const int key0 = j * KT, lb = key0 / p.block_size;
+        off = key0 - lb * p.block_size;
+        const int phys = __ldg(p.block_tables + static_cast<int64_t>(b) * p.max_blocks + lb);
+        if (phys >= 0 && phys < p.num_blocks) return phys;
+        record_error(p.err, PKV_DEVERR_BLOCK_ID, b);
+        return -1;
+    }
+};
+
+// Sequence numbers of the tiles in the ring, for a run of T tiles: K(0), then K(t + 1) and V(t) for each t.
+__device__ __forceinline__ int k_seq(int t) { return t == 0 ? 0 : 2 * t - 1; }
+__device__ __forceinline__ int v_seq(int t, int T) { return t == T - 1 ? 2 * T - 1 : 2 * t + 2; }
+
+// Which of a tile's keys a node sees: bit e for key 64 j + e.
+__device__ __forceinline__ unsigned long long visible(const unsigned long long (&w)[4], int rel, int keys) {
+    // rel: node of the tile's first key (negative before the tree); keys: keys of the sequence in this tile
+    unsigned long long m;
+    if (rel < 0) {
+        m = rel <= -64 ? ~0ull : (w[0] << -rel) | ((1ull << -rel) - 1ull);
+    } else {
+        const int i = rel >> 6, sh = rel & 63;
+        const unsigned long long lo = i == 0 ? w[0] : i == 1 ? w[1] : i == 2 ? w[2] : w[3];
+        const unsigned long long hi = i == 0 ? w[1] : i == 1 ? w[2] : i == 2 ? w[3] : 0ull;
+        m = sh ? (lo >> sh) | (hi << (64 - sh)) : lo;
+    }
+    return keys >= 64 ? m : m & ((1ull << keys) - 1ull);
+}
+
+// Two bf16 of which at least one is an infinity or a NaN.
+__device__ __forceinline__ bool wild2(uint32_t w) { return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u; }
+
+__device__ __forceinline__ uint4 ld_stream(const void* p) {
+    return __ldcs(reinterpret_cast<const uint4*>(p));
+}
+
+template <bool FP8>
+__global__ void __launch_bounds__(FP8 ? 288 : 192, CTAS_PER_SM)
+tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v, const Params p) {
+    constexpr int THREADS = FP8 ? 288 : 192, LOAD_WARP = 4, MMA_WARP = FP8 ? 8 : 5;
+    extern __shared__ __align__(1024) uint8_t gbase[];
+    const uint32_t base = smem_u32(gbase);
+    const uint32_t sQ = base + SM_Q, sKV = base + SM_KV, bars = base + SM_BAR;
+    auto bar = [&](int i) { return bars + 8u * i; };
+    uint32_t* misc = reinterpret_cast<uint32_t*>(gbase + SM_MISC);
+    long long* scan = reinterpret_cast<long long*>(gbase + SM_SCAN);
+    Ctl ctl{reinterpret_cast<volatile uint32_t*>(misc + 1), p.err};
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (tid == 0) {
+        for (int i = 0; i < NUM_BARS; ++i) {
+            const bool per_warp = i == BAR_PF || i == BAR_PF + 1 || i == BAR_OE || i == BAR_WG || (FP8 && i >= BAR_FULL && i < BAR_FULL + SLOTS);
+            mbar_init(bar(i), per_warp ? 4 : 1);
+        }
+        misc[1] = 0u;
+        fence_barrier_init();
+        tma_prefetch_desc(&tm_q);
+        if (!FP8) {
+            tma_prefetch_desc(&tm_k);
+            tma_prefetch_desc(&tm_v);
+        }
+    }
+    if (warp == MMA_WARP) {
+        tmem_alloc(base + SM_MISC, TMEM_COLS);
+        tmem_relinquish();
+    }
+    // The run: all tiles are counted, then the sequence in which this CTA's share starts is searched, a
+    // block of sequences at a time.
+    constexpr int WARPS = THREADS / 32;
+    auto block_scan = [&](long long v, long long& total) {      // inclusive sums over the CTA's threads
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += y;
+        }
+        __syncthreads();
+        if (lane == 31) scan[warp] = v;
+        __syncthreads();
+        long long before = 0;
+        total = 0;
+        for (int i = 0; i < WARPS; ++i) {
+            const long long x = scan[i];
+            before += i < warp ? x : 0;
+            total += x;
+        }
+        return before + v;
+    };
+    long long mine = 0, first = 0;
+    for (int b = tid; b < p.batch; b += THREADS) {
+        const Seq s = sequence(p, b);
+        if (s.bad && blockIdx.x == 0) record_error(p.err, PKV_DEVERR_SEQLENS, b);
+        const long long t = tiles_of(p, s);
+        if (b < THREADS) first = t;
+        mine += t;
+    }
+    long long W;
+    long long upto = block_scan(mine, W);
+    const long long C = max(1ll, min(static_cast<long long>(gridDim.x), (W + MIN_RUN - 1) / MIN_RUN));
+    const long long c = blockIdx.x;
+    const long long t0 = c < C ? c * W / C : 0, t1 = c < C ? (c + 1) * W / C : 0;
+    if (t1 > t0) {
+        long long before = 0;
+        for (int base_b = 0; base_b < p.batch; base_b += THREADS) {
+            const int b = base_b + tid;
+            long long v = 0, total = W;
+            if (p.batch <= THREADS) {
+                v = first;                                   // one block: its sums are known
+            } else {
+                if (b < p.batch) v = tiles_of(p, sequence(p, b));
+                upto = block_scan(v, total);
+            }
+            const long long at = before + upto;
+            if (t0 >= at - v && t0 < at) {
+                scan[14] = b;
+                scan[15] = t0 - (at - v);
+            }
+            before += total;
+            if (before > t0) break;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc[0];
+    const int T = static_cast<int>(t1 - t0);
+    Walk w(p, T > 0 ? static_cast<int>(scan[14]) : 0, T > 0 ? scan[15] : 0, T);
+
+    if (warp >= LOAD_WARP && warp < MMA_WARP) {
+        if (!FP8) {
+            // ------------------------------------------------------------ TMA producer
+            if (lane == 0 && T > 0) {
+                int seq = 0;                                  // tiles issued
+                bool ok = true;
+                auto load = [&](const CUtensorMap* map, int phys, int off, int g) {
+                    const int slot = seq % SLOTS;
+                    if (seq >= SLOTS && !(ok = wait_phase(ctl, bar(BAR_EMPTY + slot), ((seq / SLOTS) - 1) & 1))) return;
+                    mbar_arrive_expect_tx(bar(BAR_FULL + slot), KV_TILE);
+                    const uint32_t dst = sKV + slot * KV_TILE;
+                    tma_load_4d(dst, map, bar(BAR_FULL + slot), 0, g, off, phys);
+                    tma_load_4d(dst + KV_HALF, map, bar(BAR_FULL + slot), 64, g, off, phys);
+                    ++seq;
+                };
+                int segs = 0;
+                auto load_q = [&] {
+                    if (segs >= 1 && !(ok = wait_phase(ctl, bar(BAR_QE), (segs - 1) & 1))) return;
+                    mbar_arrive_expect_tx(bar(BAR_QF), 2 * Q_HALF);
+                    const int row = w.s.q0 + w.rt * (ROWS >> p.lg), head = w.g << p.lg;
+                    tma_load_3d(sQ, &tm_q, bar(BAR_QF), 0, head, row);
+                    tma_load_3d(sQ + Q_HALF, &tm_q, bar(BAR_QF), 64, head, row);
+                    ++segs;
+                };
+                load_q();
+                int j = w.j0, k_off, k_phys = w.block_of(j, k_off), k_g = w.g;
+                load(&tm_k, k_phys, k_off, k_g);
+                for (int t = 0; t < T && ok; ++t) {
+                    const int v_phys = k_phys, v_off = k_off, v_g = k_g;
+                    bool fresh = false;
+                    if (t + 1 < T) {
+                        if (++j == w.j1) {
+                            w.next();
+                            if (!w.more()) break;
+                            j = w.j0;
+                            fresh = true;
+                        }
+                        k_phys = w.block_of(j, k_off);
+                        k_g = w.g;
+                        load(&tm_k, k_phys, k_off, k_g);
+                        if (!ok) break;
+                    }
+                    load(&tm_v, v_phys, v_off, v_g);
+                    if (ok && fresh) load_q();
+                }
+                if (*ctl.abort) {
+                    // copies in flight land before shared memory is released
+                    if (segs > 0) wait_drain(bar(BAR_QF), (segs - 1) & 1);
+                    for (int i = max(0, seq - SLOTS); i < seq; ++i) wait_drain(bar(BAR_FULL + i % SLOTS), (i / SLOTS) & 1);
+                }
+            }
+        } else if (T > 0) {
+            // ------------------------------------------------------------ 8-bit rows: load, decode, store
+            const int lt = tid - LOAD_WARP * 32;              // 0..127
+            const int vec = lt & 7, row0 = lt >> 3;           // 16 codes of rows row0, row0 + 16, ...
+            struct Tile {
+                uint4 c[4];
+                uint32_t s[4];
+            };
+            auto fetch = [&](Tile& x, bool k, int phys, int off, int g) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int64_t blk = max(phys, 0);
+                    const int64_t row = blk * p.block_size + off + row0 + 16 * i;
+                    x.c[i] = ld_stream((k ? p.k_codes : p.v_codes) + (row * p.num_kv_heads + g) * D + vec * 16);
+                    x.s[i] = __ldg((k ? p.k_scale : p.v_scale) + (blk * p.num_kv_heads + g) * p.block_size + off + row0 + 16 * i);
+                }
+                if (phys < 0) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        x.c[i] = make_uint4(0, 0, 0, 0);
+                        x.s[i] = 127u;
+                    }
+                }
+            };
+            int seq = 0;
+            bool ok = true;
+            auto put = [&](const Tile& x) {
+                const int slot = seq % SLOTS;
+                if (seq >= SLOTS && !(ok = wait_warp(ctl, bar(BAR_EMPTY + slot), ((seq / SLOTS) - 1) & 1))) return;
+                uint8_t* dst = gbase + SM_KV + slot * KV_TILE + (vec >> 2) * KV_HALF;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = row0 + 16 * i, ch = (vec & 3) * 2;
+                    const float f = e8m0_value(x.s[i]);
+                    const uint2 a = bf16_of_codes(x.c[i].x, f), b = bf16_of_codes(x.c[i].y, f);
+                    const uint2 e = bf16_of_codes(x.c[i].z, f), h = bf16_of_codes(x.c[i].w, f);
+                    *reinterpret_cast<uint4*>(dst + row * 128 + ((ch ^ (row & 7)) * 16)) = make_uint4(a.x, a.y, b.x, b.y);
+                    *reinterpret_cast<uint4*>(dst + row * 128 + (((ch + 1) ^ (row & 7)) * 16)) = make_uint4(e.x, e.y, h.x, h.y);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(BAR_FULL + slot));
+                ++seq;
+            };
+            int segs = 0;
+            auto load_q = [&] {
+                if (warp == LOAD_WARP) {
+                    if (segs >= 1) ok = wait_warp(ctl, bar(BAR_QE), (segs - 1) & 1);
+                    if (ok && lane == 0) {
+                        mbar_arrive_expect_tx(bar(BAR_QF), 2 * Q_HALF);
+                        const int row = w.s.q0 + w.rt * (ROWS >> p.lg), head = w.g << p.lg;
+                        tma_load_3d(sQ, &tm_q, bar(BAR_QF), 0, head, row);
+                        tma_load_3d(sQ + Q_HALF, &tm_q, bar(BAR_QF), 64, head, row);
+                    }
+                    __syncwarp();
+                }
+                if (ok) ++segs;
+            };
+            // one tile of K and one of V ahead, in registers: K(t + 1) and V(t) are written while K(t + 2) and V(t + 1) load
+            Tile kx, vx;
+            int j = w.j0, off;
+            int phys = w.block_of(j, off);
+            fetch(kx, true, phys, off, w.g);
+            fetch(vx, false, phys, off, w.g);
+            load_q();
+            put(kx);
+            bool fresh = false;
+            auto advance = [&] {
+                fresh = ++j == w.j1;
+                if (fresh) {
+                    w.next();
+                    j = w.j0;
+                }
+                phys = w.block_of(j, off);
+            };
+            if (T > 1) {
+                advance();
+                fetch(kx, true, phys, off, w.g);
+            }
+            for (int t = 0; t < T && ok; ++t) {
+                const bool load_next_q = fresh && t + 1 < T;
+                const int v_phys = phys, v_off = off, v_g = w.g;     // tile t + 1
+                if (t + 1 < T) {
+                    put(kx);
+                    if (!ok) break;
+                }
+                put(vx);
+                if (!ok) break;
+                if (load_next_q) load_q();
+                if (t + 1 < T) fetch(vx, false, v_phys, v_off, v_g);
+                if (t + 2 < T) {
+                    advance();
+                    fetch(kx, true, phys, off, w.g);
+                } else {
+                    fresh = false;
+                }
+            }
+            if (warp == LOAD_WARP && *ctl.abort && segs > 0) wait_drain(bar(BAR_QF), (segs - 1) & 1);
+        }
+        __syncwarp();
+        tc_fence_before();
+        __syncthreads();
+    } else if (warp == MMA_WARP) {
+        // ---------------------------------------------------------------- MMA
+        // The whole warp runs this loop in step; each tcgen05 instruction is issued by one elected lane.
+        constexpr uint32_t idesc_qk = idesc_bf16_f32(ROWS, KT, 0, 0);
+        constexpr uint32_t idesc_pv = idesc_bf16_f32(ROWS, D, 0, 1);
+        const uint64_t dq = smem_desc(sQ, 16, 1024, 2);
+        int segs = 0;                                         // segments whose S has begun
+        int oseg = 0;                                         // segments whose O has begun
+        bool ok = T > 0;
+        auto issue_s = [&](int t, bool seg_first, bool seg_last) {
+            if (seg_first) {
+                if (!(ok = wait_warp(ctl, bar(BAR_QF), segs & 1))) return;
+                ++segs;
+            }
+            const int sq = k_seq(t), slot = sq % SLOTS;
+            if (!(ok = wait_warp(ctl, bar(BAR_FULL + slot), (sq / SLOTS) & 1))) return;
+            tc_fence_after();
+            const uint64_t dk = smem_desc(sKV + slot * KV_TILE, 16, 1024, 2);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+                mma_ss_warp(tmem + (t & 1) * KT, dq + (((ks >> 2) * Q_HALF + (ks & 3) * 32) >> 4),
+                            dk + (((ks >> 2) * KV_HALF + (ks & 3) * 32) >> 4), idesc_qk, ks > 0 ? 1u : 0u);
+            mma_commit_warp(bar(BAR_SF + (t & 1)));
+            mma_commit_warp(bar(BAR_EMPTY + slot));
+            if (seg_last) mma_commit_warp(bar(BAR_QE));
+        };
+        int j = w.j0;
+        if (ok) issue_s(0, true, w.j0 + 1 == w.j1);
+        for (int t = 0; t < T && ok; ++t) {
+            const bool first_here = j == w.j0, last_here = j + 1 == w.j1;
+            const int keys = min(KT, w.s.len - j * KT);
+            if (!last_here && t + 1 < T) {
+                issue_s(t + 1, false, j + 2 == w.j1);
+                if (!ok) break;
+            }
+            if (first_here) {
+                if (oseg >= 1 && !(ok = wait_warp(ctl, bar(BAR_OE), (oseg - 1) & 1))) break;
+                ++oseg;
+            }
+            const int sq = v_seq(t, T), slot = sq % SLOTS;
+            if (!(ok = wait_warp(ctl, bar(BAR_FULL + slot), (sq / SLOTS) & 1))) break;
+            if (!(ok = wait_warp(ctl, bar(BAR_PF + (t & 1)), (t >> 1) & 1))) break;
+            tc_fence_after();
+            const uint64_t dv = smem_desc(sKV + slot * KV_TILE, KV_HALF, 1024, 2);
+            for (int ks = 0; ks < (keys + 15) >> 4; ++ks)
+                mma_ts_warp(tmem + O_COL, tmem + (t & 1) * KT + ks * 8, dv + ks * (16 * 128 >> 4), idesc_pv,
+                            (!first_here || ks > 0) ? 1u : 0u);
+            mma_commit_warp(bar(BAR_PV));
+            mma_commit_warp(bar(BAR_EMPTY + slot));
+            if (last_here) mma_commit_warp(bar(BAR_OF));
+            if (last_here) {
+                w.next();
+                j = w.j0;
+                if (t + 1 < T) issue_s(t + 1, true, w.j0 + 1 == w.j1);
+            } else {
+                ++j;
+            }
+        }
+        mma_commit_warp(bar(BAR_DRAIN));
+        wait_drain(bar(BAR_DRAIN), 0);
+        __syncwarp();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        tmem_dealloc(tmem, TMEM_COLS);
+    } else {
+        // ---------------------------------------------------------------- softmax and epilogue
+        const int row = tid;                                  // TMEM lane
+        const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
+        const float sc = p.scale_log2;
+        const int qtok = ROWS >> p.lg;
+        int t = 0, seg = 0;
+        bool ok = true;
+        int4 meta = make_int4(-1, 0, 0, 0);
+        uint32_t meets = 0;
+        auto meet = [&] {                                     // a barrier of the four warps that gives up with the others
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(BAR_WG));
+            ok = wait_warp(ctl, bar(BAR_WG), meets++ & 1u);
+            return ok;
+        };
+        for (; w.more() && ok; w.next(), ++seg) {
+            const int tokens = w.tokens();
+            const int tok = row >> p.lg;
+            const bool live = tok < tokens;                   // rows behind are computed by nobody
+            const bool warp_live = (warp * 32) >> p.lg < tokens;
+            const int tree0 = w.s.len - w.s.n;                // position of the first node
+            const int node_row = w.s.q0 + w.rt * qtok + tok;
+            unsigned long long words[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                words[i] = live && i < p.mask_words ? __ldg(p.mask + static_cast<int64_t>(node_row) * p.mask_words + i) : 0ull;
+            float m_used = -INFINITY, l = 0.f;
+            bool had_tree = false;
+            for (int j = w.j0; j < w.j1; ++j, ++t) {
+                const int keys = min(KT, w.s.len - j * KT), rel = j * KT - tree0;
+                const bool tree = rel + KT > 0;               // nodes among the keys: on no more than the last few tiles
+                if (tree) {
+                    // Infinities and NaN among the nodes' V rows leave the tile, and so does what the block holds
+                    // behind the last key: weights of 0 would spread them.
+                    const int sq = v_seq(t, T), slot = sq % SLOTS;
+                    ok = wait_warp(ctl, bar(BAR_FULL + slot), (sq / SLOTS) & 1);
+                    if (!ok) break;
+                    if (!had_tree) {
+                        if (!meet()) break;                   // the last segment's bits are read
+                        if (tid < 8) misc[2 + tid] = 0u;
+                        if (!meet()) break;
+                        had_tree = true;
+                    }
+                    uint8_t* vt = gbase + SM_KV + slot * KV_TILE;
+                    const int lo = max(0, -rel), hi = (keys + 15) & ~15;
+                    for (int i = lo * 16 + tid; i < hi * 16; i += 128) {
+                        const int r = i >> 4;
+                        uint4* at = reinterpret_cast<uint4*>(vt + ((i >> 3) & 1) * KV_HALF + r * 128 + (i & 7) * 16);
+                        if (r >= keys) {
+                            *at = make_uint4(0, 0, 0, 0);
+                        } else {
+                            const uint4 x = *at;
+                            if (wild2(x.x) || wild2(x.y) || wild2(x.z) || wild2(x.w)) {
+                                uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    if ((y[e] & 0x7f80u) == 0x7f80u) y[e] &= 0xffff0000u;
+                                    if ((y[e] & 0x7f800000u) == 0x7f800000u) y[e] &= 0x0000ffffu;
+                                }
+                                *at = make_uint4(y[0], y[1], y[2], y[3]);
+                                atomicOr(misc + 2 + ((rel + r) >> 5), 1u << ((rel + r) & 31));
+                            }
+                        }
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
+                ok = wait_warp(ctl, bar(BAR_SF + (t & 1)), (t >> 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                if (warp_live) {
+                    const uint32_t s_tmem = tmem + lane_off + (t & 1) * KT;
+                    uint32_t sr[2][32];
+                    tmem_ld32(s_tmem, sr[0]);
+                    tmem_ld32(s_tmem + 32, sr[1]);
+                    tmem_ld_wait();
+                    float s[KT];
+#pragma unroll
+                    for (int e = 0; e < KT; ++e) s[e] = __uint_as_float(sr[e >> 5][e & 31]);
+                    if (tree) {
+                        const unsigned long long see = visible(words, rel, keys);
+                        const uint32_t lo = static_cast<uint32_t>(see), hi = static_cast<uint32_t>(see >> 32);
+#pragma unroll
+                        for (int e = 0; e < KT; ++e) s[e] = ((e < 32 ? lo : hi) >> (e & 31)) & 1u ? s[e] : -INFINITY;
+                    }
+                    float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+                    for (int e = 0; e < KT; e += 4) {
+                        mx0 = fmax3(mx0, s[e + 0], s[e + 1]);
+                        mx1 = fmax3(mx1, s[e + 2], s[e + 3]);
+                    }
+                    const float m_new = fmaxf(mx0, mx1) * sc;
+                    if (j == w.j0) {
+                        m_used = m_new;
+                    } else if (__any_sync(0xffffffffu, m_new > m_used + kRescaleLog2)) {
+                        // O is rescaled only when a maximum grows by 2^8; PV(t - 1) has to be through
+                        ok = wait_warp(ctl, bar(BAR_PV), (t - 1) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const float m_tgt = fmaxf(m_used, m_new);
+                        const float alpha = m_tgt == m_used ? 1.f : ex2_ftz(m_used - m_tgt);
+#pragma unroll 1
+                        for (int cc = 0; cc < 4; ++cc) {
+                            uint32_t o[32];
+                            tmem_ld32(tmem + lane_off + O_COL + 32 * cc, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tmem_st32(tmem + lane_off + O_COL + 32 * cc, o);
+                        }
+                        tmem_st_wait();
+                        l *= alpha;
+                        m_used = m_tgt;
+                    }
+                    const float neg_m = m_used == -INFINITY ? 0.f : -m_used;      // a row that has seen nothing yet
+                    float r0 = 0.f, r1 = 0.f, r2 = 0.f, r3 = 0.f;
+#pragma unroll
+                    for (int cc = 0; cc < 2; ++cc) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const int x = 32 * cc + e;
+                            float a0, a1, a2, a3;
+                            ffma2(a0, a1, s[x], s[x + 1], sc, sc, neg_m, neg_m);
+                            ffma2(a2, a3, s[x + 2], s[x + 3], sc, sc, neg_m, neg_m);
+                            const float p0 = ex2_ftz(a0), p1 = ex2_ftz(a1), p2 = ex2_ftz(a2), p3 = ex2_ftz(a3);
+                            fadd2(r0, r1, r0, r1, p0, p1);
+                            fadd2(r2, r3, r2, r3, p2, p3);
+                            pk[e >> 1] = pack_bf16x2(p0, p1);
+                            pk[(e >> 1) + 1] = pack_bf16x2(p2, p3);
+                        }
+                        tmem_st16(s_tmem + 16 * cc, pk);
+                    }
+                    l += (r0 + r1) + (r2 + r3);
+                    tmem_st_wait();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(BAR_PF + (t & 1)));
+            }
+            if (!ok) break;
+            ok = wait_warp(ctl, bar(BAR_OF), seg & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (had_tree && !meet()) break;                   // every warp's bits are there
+            const bool whole = w.j0 == 0 && w.j1 == w.nt;
+            const int part = w.j0 > 0 ? 0 : 1;                // 0: the unit began before this run, 1: it goes on behind it
+            if (!whole && part == 1) {
+                // its last run: that of the unit's last tile, which lies nt - 1 tiles behind its first one here
+                const long long end = t1 + (w.nt - w.j1);
+                meta = make_int4(static_cast<int>((end * C - 1) / W), w.s.q0 + w.rt * qtok, tokens, w.g);
+            }
+            if (warp_live) {
+                uint32_t any = 0u;
+                if (had_tree)
+                    for (int i = 0; i < 8; ++i) any |= misc[2 + i];
+                const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+                const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + part;
+                uint16_t* orow = p.out + (static_cast<int64_t>(node_row) * p.num_heads + (w.g << p.lg) + (row & ((1 << p.lg) - 1))) * D;
+                if (!whole) p.part_ml[slot * ROWS + row] = make_float2(m_used, l);
+#pragma unroll 1
+                for (int cc = 0; cc < 4; ++cc) {
+                    uint32_t o[32];
+                    tmem_ld32(tmem + lane_off + O_COL + 32 * cc, o);
+                    tmem_ld_wait();
+                    if (any != 0u && live) {
+                        // what was taken out of the tiles, to the rows that see it
+#pragma unroll 1
+                        for (int i = 0; i < w.s.n; ++i) {
+                            const unsigned long long word = i < 64 ? words[0] : i < 128 ? words[1] : i < 192 ? words[2] : words[3];
+                            const int j = (tree0 + i) / KT;
+                            if (!((misc[2 + (i >> 5)] >> (i & 31)) & 1u) || !((word >> (i & 63)) & 1ull) || j < w.j0 || j >= w.j1) continue;
+                            int off;
+                            const int phys = w.block_of(j, off);
+                            if (phys < 0) continue;
+                            const int64_t at = static_cast<int64_t>(phys) * p.block_size + off + (tree0 + i - j * KT);
+                            const int64_t first_v = (at * p.num_kv_heads + w.g) * D + 32 * cc;
+                            const float f = FP8 ? e8m0_value(__ldg(p.v_scale + (static_cast<int64_t>(phys) * p.num_kv_heads + w.g) * p.block_size + off +
+                                                                   (tree0 + i - j * KT))) : 1.f;
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                const uint2 v = FP8 ? bf16_of_codes(__ldg(reinterpret_cast<const uint32_t*>(p.v_codes + first_v + e)), f)
+                                                    : __ldg(reinterpret_cast<const uint2*>(p.v_cache + first_v + e));
+                                const float x[4] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)};
+#pragma unroll
+                                for (int d = 0; d < 4; ++d)
+                                    if (!(fabsf(x[d]) <= 3.4028235e38f)) o[e + d] = __float_as_uint(__uint_as_float(o[e + d]) + x[d]);
+                            }
+                        }
+                    }
+                    if (whole) {
+                        if (live) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                uint4 x;
+                                x.x = pack_bf16x2(__uint_as_float(o[8 * q + 0]) * inv, __uint_as_float(o[8 * q + 1]) * inv);
+                                x.y = pack_bf16x2(__uint_as_float(o[8 * q + 2]) * inv, __uint_as_float(o[8 * q + 3]) * inv);
+                                x.z = pack_bf16x2(__uint_as_float(o[8 * q + 4]) * inv, __uint_as_float(o[8 * q + 5]) * inv);
+                                x.w = pack_bf16x2(__uint_as_float(o[8 * q + 6]) * inv, __uint_as_float(o[8 * q + 7]) * inv);
+                                *reinterpret_cast<uint4*>(orow + 32 * cc + 8 * q) = x;
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            p.part_o[(slot * 32 + 8 * cc + q) * ROWS + row] =
+                                make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]), __uint_as_float(o[4 * q + 2]),
+                                            __uint_as_float(o[4 * q + 3]));
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(BAR_OE));
+        }
+        if (tid == 0) p.meta[blockIdx.x] = ok ? meta : make_int4(-1, 0, 0, 0);
+        tc_fence_before();
+        __syncthreads();
+    }
+}
+
+// The units that several runs share: block (c, y) joins columns 8 y .. 8 y + 7 of the unit that starts in run c and
+// goes on behind it.
+constexpr int JOIN_THREADS = 256, JOIN_SPLIT = 16;
+__global__ void __launch_bounds__(JOIN_THREADS) tree_join_kernel(const float4* __restrict__ part_o, const float2* __restrict__ part_ml,
+                                                                 const int4* __restrict__ meta, uint16_t* __restrict__ out, int num_heads, int lg) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int c = blockIdx.x;
+    const int4 u = meta[c];
+    if (u.x < 0) return;
+    const int row = threadIdx.x & (ROWS - 1), c4 = blockIdx.y * 2 + (threadIdx.x >> 7);
+    if ((row >> lg) >= u.z) return;
+    auto slot = [&](int i) { return static_cast<int64_t>(i) * 2 + (i == c ? 1 : 0); };
+    float M = -INFINITY;
+    for (int i = c; i <= u.x; ++i) M = fmaxf(M, part_ml[slot(i) * ROWS + row].x);
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = c; i <= u.x; ++i) {
+        const float2 ml = part_ml[slot(i) * ROWS + row];
+        const float4 x = part_o[(slot(i) * 32 + c4) * ROWS + row];
+        const float w = ml.x == M ? 1.f : ex2_ftz(ml.x - M);
+        l += ml.y * w;
+        o.x += x.x * w;
+        o.y += x.y * w;
+        o.z += x.z * w;
+        o.w += x.w * w;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t at = (static_cast<int64_t>(u.y + (row >> lg)) * num_heads + (u.w << lg) + (row & ((1 << lg) - 1))) * D + 4 * c4;
+    *reinterpret_cast<uint2*>(out + at) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+}
+
+constexpr size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+int64_t grid_of(int batch, int max_nodes, int max_context, int num_kv_heads, int lg) {
+    const int qtok = ROWS >> lg;
+    const int64_t tiles = static_cast<int64_t>(batch) * ((static_cast<int64_t>(max_context) + KT - 1) / KT) * ((max_nodes + qtok - 1) / qtok) *
+                          num_kv_heads;
+    return std::max<int64_t>(1, std::min<int64_t>(CTAS_PER_SM * sm_count(), (tiles + MIN_RUN - 1) / MIN_RUN));
+}
+
+}  // namespace
+
+size_t tree_decode_workspace_bytes() {
+    const size_t ctas = static_cast<size_t>(CTAS_PER_SM) * sm_count();
+    return align256(ctas * 2 * ROWS * D * 4) + align256(ctas * 2 * ROWS * 8) + align256(ctas * 16);
+}
+
+pkv_status launch_tree_decode(const TreeDecodeArgs& a, int* err, cudaStream_t stream) {
+    const bool fp8 = a.k_scale != nullptr;
+    const int lg = group_log2(a.num_heads, a.num_kv_heads);
+    if (lg < 0) return PKV_ERR_UNSUPPORTED;
+    if (a.workspace == nullptr || a.workspace_bytes < tree_decode_workspace_bytes()) return PKV_ERR_WORKSPACE;
+    if (!setup_once(kSetupTreeDecode, [] {
+            return cudaFuncSetAttribute(tree_decode_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) == cudaSuccess &&
+                   cudaFuncSetAttribute(tree_decode_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) == cudaSuccess;
+        }))
+        return PKV_ERR_CUDA;
+    CUtensorMap tm_q, tm_k, tm_v;
+    {
+        const uint64_t dims[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(a.num_heads), static_cast<uint64_t>(a.total_nodes)};
+        const uint64_t strides[2] = {static_cast<uint64_t>(D) * 2, static_cast<uint64_t>(a.num_heads) * D * 2};
+        const uint32_t box[3] = {64u, static_cast<uint32_t>(1 << lg), static_cast<uint32_t>(ROWS >> lg)};
+        if (encode_tiled(&tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(a.q), dims, strides, box,
+                         CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+            return PKV_ERR_INVALID_ARG;
+    }
+    tm_k = tm_v = tm_q;                                       // the 8-bit kernel reads its pools itself
+    if (!fp8) {
+        const uint64_t dims[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(a.num_kv_heads), static_cast<uint64_t>(a.block_size),
+                                  static_cast<uint64_t>(a.num_blocks)};
+        const uint64_t strides[3] = {static_cast<uint64_t>(D) * 2, static_cast<uint64_t>(a.num_kv_heads) * D * 2,
+                                     static_cast<uint64_t>(a.block_size) * a.num_kv_heads * D * 2};
+        const uint32_t box[4] = {64u, 1u, static_cast<uint32_t>(KT), 1u};
+        if (encode_tiled(&tm_k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(a.k_cache), dims, strides, box,
+                         CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
+            encode_tiled(&tm_v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(a.v_cache), dims, strides, box,
+                         CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+            return PKV_ERR_INVALID_ARG;
+    }
+    const size_t ctas = static_cast<size_t>(CTAS_PER_SM) * sm_count();
+    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+    Params p{};
+    p.part_o = reinterpret_cast<float4*>(ws);
+    p.part_ml = reinterpret_cast<float2*>(ws + align256(ctas * 2 * ROWS * D * 4));
+    p.meta = reinterpret_cast<int4*>(ws + align256(ctas * 2 * ROWS * D * 4) + align256(ctas * 2 * ROWS * 8));
+    p.block_tables = a.block_tables;
+    p.context_lens = a.context_lens;
+    p.cu_nodes = a.cu_nodes;
+    p.mask = reinterpret_cast<const unsigned long long*>(a.tree_mask);
+    p.out = a.out;
+    p.k_codes = static_cast<const uint8_t*>(a.k_cache);
+    p.v_codes = static_cast<const uint8_t*>(a.v_cache);
+    p.v_cache = static_cast<const uint16_t*>(a.v_cache);
+    p.k_scale = a.k_scale;
+    p.v_scale = a.v_scale;
+    p.batch = a.batch;
+    p.max_blocks = a.max_blocks;
+    p.num_heads = a.num_heads;
+    p.num_kv_heads = a.num_kv_heads;
+    p.lg = lg;
+    p.block_size = a.block_size;
+    p.num_blocks = a.num_blocks;
+    p.max_nodes = a.max_nodes;
+    p.max_context = a.max_context;
+    p.mask_words = a.mask_words;
+    p.total_nodes = a.total_nodes;
+    p.scale_log2 = a.softmax_scale * 1.4426950408889634f;
+    p.err = err;
+    const int grid = static_cast<int>(grid_of(a.batch, a.max_nodes, a.max_context, a.num_kv_heads, lg));
+    if (fp8)
+        tree_decode_kernel<true><<<grid, 288, SMEM_BYTES, stream>>>(tm_q, tm_k, tm_v, p);
+    else
+        tree_decode_kernel<false><<<grid, 192, SMEM_BYTES, stream>>>(tm_q, tm_k, tm_v, p);
+    if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, JOIN_SPLIT);
+    cfg.blockDim = dim3(JOIN_THREADS);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_join_kernel, static_cast<const float4*>(p.part_o), static_cast<const float2*>(p.part_ml),
+                                             static_cast<const int4*>(p.meta), a.out, a.num_heads, lg);
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+}  // namespace pkv
