@@ -27,9 +27,9 @@
 // to the rows that see them.
 //
 // Warps 0-3: softmax and epilogue (TMEM lanes 0-127).  bf16 cache: warp 4 TMA producer,
-// warp 5 TMEM allocation and MMA issue.  8-bit cache: warps 4-7 load codes into
-// registers and write them, as the bf16 values they stand for, to the tiles in shared
-// memory; warp 8 issues.
+// warp 5 TMEM allocation and MMA issue.  8-bit cache: warps 4-7 turn the codes that TMA
+// has put into a slot of the ring into the bf16 values they stand for, in place; warp 8
+// issues, warp 9 is the producer.
 #include <algorithm>
 
 #include "pkv_device.cuh"
@@ -48,14 +48,18 @@ constexpr int SLOTS = 5;                     // ring of K and V tiles
 constexpr int TMEM_COLS = 256;
 constexpr int O_COL = 128;                   // S / P buffers at columns 0 and 64
 constexpr float kRescaleLog2 = 8.0f;
-constexpr int MIN_RUN = 4;                   // tiles a CTA takes at least
+constexpr int UNIT_COST = 2;                 // what starting and ending a unit costs, in tiles
+constexpr int MIN_RUN = 4;                   // cost a CTA takes at least; above UNIT_COST, so that every run has a tile
+static_assert(MIN_RUN > UNIT_COST, "a run has a tile");
 constexpr int CTAS_PER_SM = 2;
+constexpr int THREADS_BF16 = 192, THREADS_FP8 = 320;
 
 constexpr int SM_Q = 0;
 constexpr int SM_KV = 2 * Q_HALF;
-constexpr int SM_BAR = SM_KV + SLOTS * KV_TILE;
+constexpr int SM_SCALE = SM_KV + SLOTS * KV_TILE;               // 8-bit cache: a scale byte per row of each slot
+constexpr int SM_BAR = SM_SCALE + SLOTS * KT;
 enum {
-    BAR_FULL = 0, BAR_EMPTY = BAR_FULL + SLOTS, BAR_QF = BAR_EMPTY + SLOTS, BAR_QE, BAR_SF, BAR_PF = BAR_SF + 2,
+    BAR_FULL = 0, BAR_EMPTY = BAR_FULL + SLOTS, BAR_RAW = BAR_EMPTY + SLOTS, BAR_QF = BAR_RAW + SLOTS, BAR_QE, BAR_SF, BAR_PF = BAR_SF + 2,
     BAR_PV = BAR_PF + 2, BAR_OF, BAR_OE, BAR_WG, BAR_DRAIN, NUM_BARS
 };
 constexpr int SM_MISC = (SM_BAR + NUM_BARS * 8 + 15) & ~15;      // [0] TMEM base, [1] abort, [2..9] nodes with infinities or NaN in V
@@ -72,8 +76,7 @@ struct Params {
     float4* part_o;           // [CTA][2][32][128]: four columns of each row
     float2* part_ml;          // [CTA][2][128]: maximum (log2) and sum
     int4* meta;               // [CTA]: {last CTA of the unit that continues behind this one's run or -1, first row's node, nodes, KV head}
-    const uint8_t* k_codes;   // 8-bit cache
-    const uint8_t* v_codes;
+    const uint8_t* v_codes;   // 8-bit cache, for the values taken out of a tile
     const uint8_t* k_scale;
     const uint8_t* v_scale;
     const uint16_t* v_cache;  // bf16 cache, for the values taken out of a tile
@@ -128,28 +131,31 @@ __device__ __forceinline__ Seq sequence(const Params& p, int b) {
     s.n = fits ? static_cast<int>(n) : 0;
     return s;
 }
-__device__ __forceinline__ long long tiles_of(const Params& p, const Seq& s) {
+__device__ __forceinline__ long long cost_of(const Params& p, const Seq& s) {
     const int qtok = ROWS >> p.lg;
-    return s.n ? static_cast<long long>((s.len + KT - 1) / KT) * ((s.n + qtok - 1) / qtok) * p.num_kv_heads : 0;
+    return s.n ? static_cast<long long>((s.len + KT - 1) / KT + UNIT_COST) * ((s.n + qtok - 1) / qtok) * p.num_kv_heads : 0;
 }
 
-// A CTA's run of tiles, segment by segment: tiles [j0, j1) of the unit (sequence b, KV head g, row tile rt).
-// Every role walks by itself.
+// A CTA's run, segment by segment: tiles [j0, j1) of the unit (sequence b, KV head g, row tile rt).  Runs are cut in
+// cost: a unit is UNIT_COST steps without a tile and then a step per tile.  Every role walks by itself.
 struct Walk {
     const Params& p;
     Seq s;
     int b, g, rt, nt, nrt, j0, j1;
-    long long left;
+    long long left;                          // cost of the run behind this segment
 
-    __device__ __forceinline__ Walk(const Params& params, int b0, long long off, long long count) : p(params), b(b0), left(count) {
+    __device__ __forceinline__ Walk(const Params& params, int b0, long long off, long long count) : p(params), b(b0) {
         g = rt = j0 = j1 = nt = nrt = 0;
-        if (left <= 0) return;
+        left = count;
+        if (count <= 0) return;
         enter();
-        const int unit = static_cast<int>(off / nt);
-        j0 = static_cast<int>(off - static_cast<long long>(unit) * nt);
+        const int per = nt + UNIT_COST;
+        const int unit = static_cast<int>(off / per), at = static_cast<int>(off - static_cast<long long>(unit) * per);
         g = unit / nrt;
         rt = unit - g * nrt;
-        clip();
+        j0 = max(0, at - UNIT_COST);
+        clip(max(0, UNIT_COST - at));
+        if (j0 == j1) next();                // nothing of the last unit's steps but its first ones
     }
     __device__ __forceinline__ void enter() {
         s = sequence(p, b);
@@ -157,26 +163,26 @@ struct Walk {
         nt = (s.len + KT - 1) / KT;
         nrt = (s.n + qtok - 1) / qtok;
     }
-    __device__ __forceinline__ void clip() { j1 = static_cast<int>(min(static_cast<long long>(nt), j0 + left)); }
-    __device__ __forceinline__ bool more() const { return left > 0; }
+    __device__ __forceinline__ void clip(int before) {
+        j1 = static_cast<int>(min(static_cast<long long>(nt), max(static_cast<long long>(j0), j0 + left - before)));
+        left -= before + (j1 - j0);
+    }
+    __device__ __forceinline__ bool last() const { return left <= UNIT_COST; }     // no tile of this run lies behind this segment
+    __device__ __forceinline__ bool more() const { return j1 > j0; }
     __device__ __forceinline__ void next() {
-        left -= j1 - j0;
-        if (left <= 0) return;
-        j0 = 0;
+        j1 = j0 = 0;
+        if (last()) return;
         if (++rt == nrt) {
             rt = 0;
             if (++g == p.num_kv_heads) {
                 g = 0;
                 do {
-                    if (++b >= p.batch) {
-                        left = 0;
-                        return;
-                    }
+                    if (++b >= p.batch) return;
                     enter();
                 } while (s.n == 0);
             }
         }
-        clip();
+        clip(UNIT_COST);
     }
     __device__ __forceinline__ int tokens() const { return min(ROWS >> p.lg, s.n - rt * (ROWS >> p.lg)); }
     // row of the pool (block * block_size + offset) where the keys of tile j start; negative: no such block
@@ -190,9 +196,9 @@ struct Walk {
     }
 };
 
-// Sequence numbers of the tiles in the ring, for a run of T tiles: K(0), then K(t + 1) and V(t) for each t.
+// Sequence numbers in the ring of the K and V tiles of a run's tile t: K(0), then K(t + 1) and V(t) for each t.
 __device__ __forceinline__ int k_seq(int t) { return t == 0 ? 0 : 2 * t - 1; }
-__device__ __forceinline__ int v_seq(int t, int T) { return t == T - 1 ? 2 * T - 1 : 2 * t + 2; }
+__device__ __forceinline__ int v_seq(int t, bool last) { return last ? 2 * t + 1 : 2 * t + 2; }
 
 // Which of a tile's keys a node sees: bit e for key 64 j + e.
 __device__ __forceinline__ unsigned long long visible(const unsigned long long (&w)[4], int rel, int keys) {
@@ -212,15 +218,62 @@ __device__ __forceinline__ unsigned long long visible(const unsigned long long (
 // Two bf16 of which at least one is an infinity or a NaN.
 __device__ __forceinline__ bool wild2(uint32_t w) { return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u; }
 
-__device__ __forceinline__ uint4 ld_stream(const void* p) {
-    return __ldcs(reinterpret_cast<const uint4*>(p));
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// Two bytes of w, each as 16 bits with its sign in the upper eight: bytes 0 and 1 by the selector 0x9180, 2 and 3 by 0xb3a2.
+template <uint32_t SEL>
+__device__ __forceinline__ uint32_t widen(uint32_t w) {
+    uint32_t d;
+    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(d) : "r"(w), "n"(SEL));
+    return d;
+}
+
+// 16 e4m3 codes and their row's scale byte as 16 bf16.  A code's bits, set one exponent field further, read as a bf16
+// 2^-120 times its value (its subnormals as bf16's), so a product with 2^120 times the scale, in two factors where one
+// would not fit, is exact; only the NaN code needs to be seen.
+// The rest, out of line: rows with a NaN code, and scales for which one factor does not do.
+__device__ __noinline__ void bf16_of_odd_row(const uint32_t (&w)[4], uint32_t byte, uint32_t (&o)[8]) {
+    const float f = e8m0_value(byte);
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        const uint2 x = bf16_of_codes(w[i], f);
+        o[2 * i] = x.x;
+        o[2 * i + 1] = x.y;
+    }
+}
+
+__device__ __forceinline__ void bf16_of_row(const uint4& c, uint32_t byte, uint4& lo, uint4& hi) {
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    uint32_t nan = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) nan |= (w[i] & 0x7f7f7f7fu) + 0x01010101u;
+    uint32_t o[8];
+    if ((nan & 0x80808080u) != 0u || byte - 8u > 126u) {             // a NaN, or a scale outside 2^-119 .. 2^7
+        uint32_t odd[8];
+        bf16_of_odd_row(w, byte, odd);
+        lo = make_uint4(odd[0], odd[1], odd[2], odd[3]);
+        hi = make_uint4(odd[4], odd[5], odd[6], odd[7]);
+        return;
+    }
+    const uint32_t f = (byte + 120u) * 0x00800080u;                  // 2^(120 + e) twice
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        o[2 * i] = hmul2((widen<0x9180u>(w[i]) << 4) & 0x87f087f0u, f);
+        o[2 * i + 1] = hmul2((widen<0xb3a2u>(w[i]) << 4) & 0x87f087f0u, f);
+    }
+    lo = make_uint4(o[0], o[1], o[2], o[3]);
+    hi = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
 template <bool FP8>
-__global__ void __launch_bounds__(FP8 ? 288 : 192, CTAS_PER_SM)
+__global__ void __launch_bounds__(FP8 ? THREADS_FP8 : THREADS_BF16, CTAS_PER_SM)
 tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const Params p) {
-    constexpr int THREADS = FP8 ? 288 : 192, LOAD_WARP = 4, MMA_WARP = FP8 ? 8 : 5;
+    constexpr int THREADS = FP8 ? THREADS_FP8 : THREADS_BF16, LOAD_WARP = FP8 ? 9 : 4, MMA_WARP = FP8 ? 8 : 5;
     extern __shared__ __align__(1024) uint8_t gbase[];
     const uint32_t base = smem_u32(gbase);
     const uint32_t sQ = base + SM_Q, sKV = base + SM_KV, bars = base + SM_BAR;
@@ -239,10 +292,8 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         misc[1] = 0u;
         fence_barrier_init();
         tma_prefetch_desc(&tm_q);
-        if (!FP8) {
-            tma_prefetch_desc(&tm_k);
-            tma_prefetch_desc(&tm_v);
-        }
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
     }
     if (warp == MMA_WARP) {
         tmem_alloc(base + SM_MISC, TMEM_COLS);
@@ -273,13 +324,13 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     for (int b = tid; b < p.batch; b += THREADS) {
         const Seq s = sequence(p, b);
         if (s.bad && blockIdx.x == 0) record_error(p.err, PKV_DEVERR_SEQLENS, b);
-        const long long t = tiles_of(p, s);
+        const long long t = cost_of(p, s);
         if (b < THREADS) first = t;
         mine += t;
     }
     long long W;
     long long upto = block_scan(mine, W);
-    const long long C = max(1ll, min(static_cast<long long>(gridDim.x), (W + MIN_RUN - 1) / MIN_RUN));
+    const long long C = max(1ll, min(static_cast<long long>(gridDim.x), W / MIN_RUN));
     const long long c = blockIdx.x;
     const long long t0 = c < C ? c * W / C : 0, t1 = c < C ? (c + 1) * W / C : 0;
     if (t1 > t0) {
@@ -290,7 +341,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (p.batch <= THREADS) {
                 v = first;                                   // one block: its sums are known
             } else {
-                if (b < p.batch) v = tiles_of(p, sequence(p, b));
+                if (b < p.batch) v = cost_of(p, sequence(p, b));
                 upto = block_scan(v, total);
             }
             const long long at = before + upto;
@@ -306,160 +357,101 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = misc[0];
-    const int T = static_cast<int>(t1 - t0);
-    Walk w(p, T > 0 ? static_cast<int>(scan[14]) : 0, T > 0 ? scan[15] : 0, T);
+    const bool busy = t1 > t0;
+    Walk w(p, busy ? static_cast<int>(scan[14]) : 0, busy ? scan[15] : 0, t1 - t0);
 
-    if (warp >= LOAD_WARP && warp < MMA_WARP) {
-        if (!FP8) {
-            // ------------------------------------------------------------ TMA producer
-            if (lane == 0 && T > 0) {
-                int seq = 0;                                  // tiles issued
-                bool ok = true;
-                auto load = [&](const CUtensorMap* map, int phys, int off, int g) {
-                    const int slot = seq % SLOTS;
-                    if (seq >= SLOTS && !(ok = wait_phase(ctl, bar(BAR_EMPTY + slot), ((seq / SLOTS) - 1) & 1))) return;
-                    mbar_arrive_expect_tx(bar(BAR_FULL + slot), KV_TILE);
-                    const uint32_t dst = sKV + slot * KV_TILE;
-                    tma_load_4d(dst, map, bar(BAR_FULL + slot), 0, g, off, phys);
-                    tma_load_4d(dst + KV_HALF, map, bar(BAR_FULL + slot), 64, g, off, phys);
-                    ++seq;
-                };
-                int segs = 0;
-                auto load_q = [&] {
-                    if (segs >= 1 && !(ok = wait_phase(ctl, bar(BAR_QE), (segs - 1) & 1))) return;
-                    mbar_arrive_expect_tx(bar(BAR_QF), 2 * Q_HALF);
-                    const int row = w.s.q0 + w.rt * (ROWS >> p.lg), head = w.g << p.lg;
-                    tma_load_3d(sQ, &tm_q, bar(BAR_QF), 0, head, row);
-                    tma_load_3d(sQ + Q_HALF, &tm_q, bar(BAR_QF), 64, head, row);
-                    ++segs;
-                };
-                load_q();
-                int j = w.j0, k_off, k_phys = w.block_of(j, k_off), k_g = w.g;
-                load(&tm_k, k_phys, k_off, k_g);
-                for (int t = 0; t < T && ok; ++t) {
-                    const int v_phys = k_phys, v_off = k_off, v_g = k_g;
-                    bool fresh = false;
-                    if (t + 1 < T) {
-                        if (++j == w.j1) {
-                            w.next();
-                            if (!w.more()) break;
-                            j = w.j0;
-                            fresh = true;
-                        }
-                        k_phys = w.block_of(j, k_off);
-                        k_g = w.g;
-                        load(&tm_k, k_phys, k_off, k_g);
-                        if (!ok) break;
-                    }
-                    load(&tm_v, v_phys, v_off, v_g);
-                    if (ok && fresh) load_q();
-                }
-                if (*ctl.abort) {
-                    // copies in flight land before shared memory is released
-                    if (segs > 0) wait_drain(bar(BAR_QF), (segs - 1) & 1);
-                    for (int i = max(0, seq - SLOTS); i < seq; ++i) wait_drain(bar(BAR_FULL + i % SLOTS), (i / SLOTS) & 1);
-                }
-            }
-        } else if (T > 0) {
-            // ------------------------------------------------------------ 8-bit rows: load, decode, store
-            const int lt = tid - LOAD_WARP * 32;              // 0..127
-            const int vec = lt & 7, row0 = lt >> 3;           // 16 codes of rows row0, row0 + 16, ...
-            struct Tile {
-                uint4 c[4];
-                uint32_t s[4];
-            };
-            auto fetch = [&](Tile& x, bool k, int phys, int off, int g) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int64_t blk = max(phys, 0);
-                    const int64_t row = blk * p.block_size + off + row0 + 16 * i;
-                    x.c[i] = ld_stream((k ? p.k_codes : p.v_codes) + (row * p.num_kv_heads + g) * D + vec * 16);
-                    x.s[i] = __ldg((k ? p.k_scale : p.v_scale) + (blk * p.num_kv_heads + g) * p.block_size + off + row0 + 16 * i);
-                }
-                if (phys < 0) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        x.c[i] = make_uint4(0, 0, 0, 0);
-                        x.s[i] = 127u;
-                    }
-                }
-            };
-            int seq = 0;
+    if (warp == LOAD_WARP) {
+        // ---------------------------------------------------------------- TMA producer
+        if (lane == 0 && busy) {
+            int seq = 0, segs = 0;                            // tiles and Q tiles issued
             bool ok = true;
-            auto put = [&](const Tile& x) {
+            auto load = [&](bool k, int phys, int off, int g) {
                 const int slot = seq % SLOTS;
-                if (seq >= SLOTS && !(ok = wait_warp(ctl, bar(BAR_EMPTY + slot), ((seq / SLOTS) - 1) & 1))) return;
-                uint8_t* dst = gbase + SM_KV + slot * KV_TILE + (vec >> 2) * KV_HALF;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = row0 + 16 * i, ch = (vec & 3) * 2;
-                    const float f = e8m0_value(x.s[i]);
-                    const uint2 a = bf16_of_codes(x.c[i].x, f), b = bf16_of_codes(x.c[i].y, f);
-                    const uint2 e = bf16_of_codes(x.c[i].z, f), h = bf16_of_codes(x.c[i].w, f);
-                    *reinterpret_cast<uint4*>(dst + row * 128 + ((ch ^ (row & 7)) * 16)) = make_uint4(a.x, a.y, b.x, b.y);
-                    *reinterpret_cast<uint4*>(dst + row * 128 + (((ch + 1) ^ (row & 7)) * 16)) = make_uint4(e.x, e.y, h.x, h.y);
+                if (seq >= SLOTS && !(ok = wait_phase(ctl, bar(BAR_EMPTY + slot), ((seq / SLOTS) - 1) & 1))) return;
+                const uint32_t dst = sKV + slot * KV_TILE, full = bar((FP8 ? BAR_RAW : BAR_FULL) + slot);
+                const CUtensorMap* map = k ? &tm_k : &tm_v;
+                if (FP8) {
+                    // codes to the slot's second half, where the warp that decodes a row finds and overwrites it
+                    const int64_t at = (static_cast<int64_t>(max(phys, 0)) * p.num_kv_heads + g) * p.block_size + off;
+                    mbar_arrive_expect_tx(full, KV_HALF + KT);
+                    tma_load_4d(dst + KV_HALF, map, full, 0, g, off, phys);
+                    bulk_load(base + SM_SCALE + slot * KT, (k ? p.k_scale : p.v_scale) + at, KT, full);
+                } else {
+                    mbar_arrive_expect_tx(full, KV_TILE);
+                    tma_load_4d(dst, map, full, 0, g, off, phys);
+                    tma_load_4d(dst + KV_HALF, map, full, 64, g, off, phys);
                 }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(BAR_FULL + slot));
                 ++seq;
             };
-            int segs = 0;
             auto load_q = [&] {
-                if (warp == LOAD_WARP) {
-                    if (segs >= 1) ok = wait_warp(ctl, bar(BAR_QE), (segs - 1) & 1);
-                    if (ok && lane == 0) {
-                        mbar_arrive_expect_tx(bar(BAR_QF), 2 * Q_HALF);
-                        const int row = w.s.q0 + w.rt * (ROWS >> p.lg), head = w.g << p.lg;
-                        tma_load_3d(sQ, &tm_q, bar(BAR_QF), 0, head, row);
-                        tma_load_3d(sQ + Q_HALF, &tm_q, bar(BAR_QF), 64, head, row);
-                    }
-                    __syncwarp();
-                }
-                if (ok) ++segs;
+                if (segs >= 1 && !(ok = wait_phase(ctl, bar(BAR_QE), (segs - 1) & 1))) return;
+                mbar_arrive_expect_tx(bar(BAR_QF), 2 * Q_HALF);
+                const int row = w.s.q0 + w.rt * (ROWS >> p.lg), head = w.g << p.lg;
+                tma_load_3d(sQ, &tm_q, bar(BAR_QF), 0, head, row);
+                tma_load_3d(sQ + Q_HALF, &tm_q, bar(BAR_QF), 64, head, row);
+                ++segs;
             };
-            // one tile of K and one of V ahead, in registers: K(t + 1) and V(t) are written while K(t + 2) and V(t + 1) load
-            Tile kx, vx;
-            int j = w.j0, off;
-            int phys = w.block_of(j, off);
-            fetch(kx, true, phys, off, w.g);
-            fetch(vx, false, phys, off, w.g);
             load_q();
-            put(kx);
-            bool fresh = false;
-            auto advance = [&] {
-                fresh = ++j == w.j1;
-                if (fresh) {
-                    w.next();
-                    j = w.j0;
-                }
-                phys = w.block_of(j, off);
-            };
-            if (T > 1) {
-                advance();
-                fetch(kx, true, phys, off, w.g);
-            }
-            for (int t = 0; t < T && ok; ++t) {
-                const bool load_next_q = fresh && t + 1 < T;
-                const int v_phys = phys, v_off = off, v_g = w.g;     // tile t + 1
-                if (t + 1 < T) {
-                    put(kx);
+            int j = w.j0, k_off, k_phys = w.block_of(j, k_off), k_g = w.g;
+            load(true, k_phys, k_off, k_g);
+            while (ok) {
+                const int v_phys = k_phys, v_off = k_off, v_g = k_g;
+                const bool fresh = j + 1 == w.j1, end = fresh && w.last();
+                if (!end) {
+                    if (fresh) w.next();
+                    j = fresh ? w.j0 : j + 1;
+                    k_phys = w.block_of(j, k_off);
+                    k_g = w.g;
+                    load(true, k_phys, k_off, k_g);
                     if (!ok) break;
                 }
-                put(vx);
-                if (!ok) break;
-                if (load_next_q) load_q();
-                if (t + 1 < T) fetch(vx, false, v_phys, v_off, v_g);
-                if (t + 2 < T) {
-                    advance();
-                    fetch(kx, true, phys, off, w.g);
-                } else {
-                    fresh = false;
-                }
+                load(false, v_phys, v_off, v_g);
+                if (!ok || end) break;
+                if (fresh) load_q();
             }
-            if (warp == LOAD_WARP && *ctl.abort && segs > 0) wait_drain(bar(BAR_QF), (segs - 1) & 1);
+            if (*ctl.abort) {
+                // copies in flight land before shared memory is released
+                if (segs > 0) wait_drain(bar(BAR_QF), (segs - 1) & 1);
+                for (int i = max(0, seq - SLOTS); i < seq; ++i) wait_drain(bar((FP8 ? BAR_RAW : BAR_FULL) + i % SLOTS), (i / SLOTS) & 1);
+            }
         }
         __syncwarp();
+        tc_fence_before();
+        __syncthreads();
+    } else if (FP8 && warp >= 4 && warp < 8) {
+        // ---------------------------------------------------------------- 8-bit rows to bf16 tiles
+        // Warp x decodes rows 16 x .. 16 x + 15 of each tile.  Their codes lie where the second half of their values
+        // will, so a warp that has read its rows may write them.
+        const int vec = lane & 7, row0 = (warp - 4) * 16 + (lane >> 3);
+        int tiles = 0;                                        // of K and V in this run
+        for (; w.more(); w.next()) tiles += 2 * (w.j1 - w.j0);
+#pragma unroll 1
+        for (int seq = 0; seq < tiles; ++seq) {
+            const int slot = seq % SLOTS;
+            if (!wait_warp(ctl, bar(BAR_RAW + slot), (seq / SLOTS) & 1)) break;
+            uint8_t* tile = gbase + SM_KV + slot * KV_TILE;
+            const uint8_t* scales = gbase + SM_SCALE + slot * KT;
+            uint4 c[4];
+            uint32_t byte[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                c[i] = *reinterpret_cast<const uint4*>(tile + KV_HALF + (row0 + 4 * i) * 128 + vec * 16);
+                byte[i] = scales[row0 + 4 * i];
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = row0 + 4 * i, ch = (vec & 3) * 2;
+                uint4 lo, hi;
+                bf16_of_row(c[i], byte[i], lo, hi);
+                uint8_t* dst = tile + (vec >> 2) * KV_HALF + row * 128;
+                *reinterpret_cast<uint4*>(dst + ((ch ^ (row & 7)) * 16)) = lo;
+                *reinterpret_cast<uint4*>(dst + (((ch + 1) ^ (row & 7)) * 16)) = hi;
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(BAR_FULL + slot));
+        }
         tc_fence_before();
         __syncthreads();
     } else if (warp == MMA_WARP) {
@@ -470,7 +462,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const uint64_t dq = smem_desc(sQ, 16, 1024, 2);
         int segs = 0;                                         // segments whose S has begun
         int oseg = 0;                                         // segments whose O has begun
-        bool ok = T > 0;
+        bool ok = busy;
         auto issue_s = [&](int t, bool seg_first, bool seg_last) {
             if (seg_first) {
                 if (!(ok = wait_warp(ctl, bar(BAR_QF), segs & 1))) return;
@@ -490,10 +482,10 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         };
         int j = w.j0;
         if (ok) issue_s(0, true, w.j0 + 1 == w.j1);
-        for (int t = 0; t < T && ok; ++t) {
-            const bool first_here = j == w.j0, last_here = j + 1 == w.j1;
+        for (int t = 0; ok; ++t) {
+            const bool first_here = j == w.j0, last_here = j + 1 == w.j1, end = last_here && w.last();
             const int keys = min(KT, w.s.len - j * KT);
-            if (!last_here && t + 1 < T) {
+            if (!last_here) {
                 issue_s(t + 1, false, j + 2 == w.j1);
                 if (!ok) break;
             }
@@ -501,7 +493,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (oseg >= 1 && !(ok = wait_warp(ctl, bar(BAR_OE), (oseg - 1) & 1))) break;
                 ++oseg;
             }
-            const int sq = v_seq(t, T), slot = sq % SLOTS;
+            const int sq = v_seq(t, end), slot = sq % SLOTS;
             if (!(ok = wait_warp(ctl, bar(BAR_FULL + slot), (sq / SLOTS) & 1))) break;
             if (!(ok = wait_warp(ctl, bar(BAR_PF + (t & 1)), (t >> 1) & 1))) break;
             tc_fence_after();
@@ -512,10 +504,11 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             mma_commit_warp(bar(BAR_PV));
             mma_commit_warp(bar(BAR_EMPTY + slot));
             if (last_here) mma_commit_warp(bar(BAR_OF));
+            if (end) break;
             if (last_here) {
                 w.next();
                 j = w.j0;
-                if (t + 1 < T) issue_s(t + 1, true, w.j0 + 1 == w.j1);
+                issue_s(t + 1, true, w.j0 + 1 == w.j1);
             } else {
                 ++j;
             }
@@ -562,7 +555,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (tree) {
                     // Infinities and NaN among the nodes' V rows leave the tile, and so does what the block holds
                     // behind the last key: weights of 0 would spread them.
-                    const int sq = v_seq(t, T), slot = sq % SLOTS;
+                    const int sq = v_seq(t, j + 1 == w.j1 && w.last()), slot = sq % SLOTS;
                     ok = wait_warp(ctl, bar(BAR_FULL + slot), (sq / SLOTS) & 1);
                     if (!ok) break;
                     if (!had_tree) {
@@ -599,24 +592,39 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 tc_fence_after();
                 if (warp_live) {
                     const uint32_t s_tmem = tmem + lane_off + (t & 1) * KT;
-                    uint32_t sr[2][32];
-                    tmem_ld32(s_tmem, sr[0]);
-                    tmem_ld32(s_tmem + 32, sr[1]);
-                    tmem_ld_wait();
-                    float s[KT];
+                    const unsigned long long see = tree ? visible(words, rel, keys) : ~0ull;
+                    // 32 columns of S; the 8-bit kernel, whose threads have fewer registers, reads them again for P
+                    float s[FP8 ? 1 : 2][32];
+                    auto read = [&](int cc, float (&x)[32]) {
+                        uint32_t r[32];
+                        tmem_ld32(s_tmem + 32 * cc, r);
+                        tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < KT; ++e) s[e] = __uint_as_float(sr[e >> 5][e & 31]);
-                    if (tree) {
-                        const unsigned long long see = visible(words, rel, keys);
-                        const uint32_t lo = static_cast<uint32_t>(see), hi = static_cast<uint32_t>(see >> 32);
-#pragma unroll
-                        for (int e = 0; e < KT; ++e) s[e] = ((e < 32 ? lo : hi) >> (e & 31)) & 1u ? s[e] : -INFINITY;
-                    }
+                        for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(r[e]);
+                    };
                     float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
-                    for (int e = 0; e < KT; e += 4) {
-                        mx0 = fmax3(mx0, s[e + 0], s[e + 1]);
-                        mx1 = fmax3(mx1, s[e + 2], s[e + 3]);
+                    for (int cc = 0; cc < 2; ++cc) {
+                        float (&x)[32] = s[FP8 ? 0 : cc];
+                        read(cc, x);
+                        if (tree) {
+                            const uint32_t bits = static_cast<uint32_t>(see >> (32 * cc));
+                            uint32_t r[32];
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                x[e] = (bits >> e) & 1u ? x[e] : -INFINITY;
+                                r[e] = __float_as_uint(x[e]);
+                            }
+                            if (FP8) {
+                                tmem_st32(s_tmem + 32 * cc, r);
+                                tmem_st_wait();
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            mx0 = fmax3(mx0, x[e + 0], x[e + 1]);
+                            mx1 = fmax3(mx1, x[e + 2], x[e + 3]);
+                        }
                     }
                     const float m_new = fmaxf(mx0, mx1) * sc;
                     if (j == w.j0) {
@@ -646,12 +654,13 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
                     for (int cc = 0; cc < 2; ++cc) {
                         uint32_t pk[16];
+                        float (&x)[32] = s[FP8 ? 0 : cc];
+                        if (FP8) read(cc, x);
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
-                            const int x = 32 * cc + e;
                             float a0, a1, a2, a3;
-                            ffma2(a0, a1, s[x], s[x + 1], sc, sc, neg_m, neg_m);
-                            ffma2(a2, a3, s[x + 2], s[x + 3], sc, sc, neg_m, neg_m);
+                            ffma2(a0, a1, x[e], x[e + 1], sc, sc, neg_m, neg_m);
+                            ffma2(a2, a3, x[e + 2], x[e + 3], sc, sc, neg_m, neg_m);
                             const float p0 = ex2_ftz(a0), p1 = ex2_ftz(a1), p2 = ex2_ftz(a2), p3 = ex2_ftz(a3);
                             fadd2(r0, r1, r0, r1, p0, p1);
                             fadd2(r2, r3, r2, r3, p2, p3);
@@ -675,7 +684,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const bool whole = w.j0 == 0 && w.j1 == w.nt;
             const int part = w.j0 > 0 ? 0 : 1;                // 0: the unit began before this run, 1: it goes on behind it
             if (!whole && part == 1) {
-                // its last run: that of the unit's last tile, which lies nt - 1 tiles behind its first one here
+                // its last run: that of the unit's last tile, which lies nt - j1 steps behind this run's end
                 const long long end = t1 + (w.nt - w.j1);
                 meta = make_int4(static_cast<int>((end * C - 1) / W), w.s.q0 + w.rt * qtok, tokens, w.g);
             }
@@ -748,45 +757,56 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     }
 }
 
-// The units that several runs share: block (c, y) joins columns 8 y .. 8 y + 7 of the unit that starts in run c and
-// goes on behind it.
-constexpr int JOIN_THREADS = 256, JOIN_SPLIT = 16;
+// The units that several runs share: block (c, y) joins 32 columns of the unit that starts in run c and goes on behind
+// it, a thread 16 columns of one row.
+constexpr int JOIN_THREADS = 2 * ROWS, JOIN_SPLIT = 4;
 __global__ void __launch_bounds__(JOIN_THREADS) tree_join_kernel(const float4* __restrict__ part_o, const float2* __restrict__ part_ml,
                                                                  const int4* __restrict__ meta, uint16_t* __restrict__ out, int num_heads, int lg) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int c = blockIdx.x;
     const int4 u = meta[c];
     if (u.x < 0) return;
-    const int row = threadIdx.x & (ROWS - 1), c4 = blockIdx.y * 2 + (threadIdx.x >> 7);
+    const int row = threadIdx.x & (ROWS - 1), c4 = (blockIdx.y * 2 + (threadIdx.x >> 7)) * 4;
     if ((row >> lg) >= u.z) return;
+    // the unit's first part is its run's second slot, all others are their runs' first
     auto slot = [&](int i) { return static_cast<int64_t>(i) * 2 + (i == c ? 1 : 0); };
     float M = -INFINITY;
-    for (int i = c; i <= u.x; ++i) M = fmaxf(M, part_ml[slot(i) * ROWS + row].x);
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
+    for (int i = c; i <= u.x; ++i) M = fmaxf(M, part_ml[slot(i) * ROWS + row].x);
+    float l = 0.f, o[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[e] = 0.f;
+#pragma unroll 2
     for (int i = c; i <= u.x; ++i) {
         const float2 ml = part_ml[slot(i) * ROWS + row];
-        const float4 x = part_o[(slot(i) * 32 + c4) * ROWS + row];
         const float w = ml.x == M ? 1.f : ex2_ftz(ml.x - M);
         l += ml.y * w;
-        o.x += x.x * w;
-        o.y += x.y * w;
-        o.z += x.z * w;
-        o.w += x.w * w;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float4 x = part_o[(slot(i) * 32 + c4 + k) * ROWS + row];
+            o[4 * k] += x.x * w;
+            o[4 * k + 1] += x.y * w;
+            o[4 * k + 2] += x.z * w;
+            o[4 * k + 3] += x.w * w;
+        }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int64_t at = (static_cast<int64_t>(u.y + (row >> lg)) * num_heads + (u.w << lg) + (row & ((1 << lg) - 1))) * D + 4 * c4;
-    *reinterpret_cast<uint2*>(out + at) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    uint4* to = reinterpret_cast<uint4*>(out + (static_cast<int64_t>(u.y + (row >> lg)) * num_heads + (u.w << lg) + (row & ((1 << lg) - 1))) * D + 4 * c4);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        to[k] = make_uint4(pack_bf16x2(o[8 * k] * inv, o[8 * k + 1] * inv), pack_bf16x2(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                           pack_bf16x2(o[8 * k + 4] * inv, o[8 * k + 5] * inv), pack_bf16x2(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
 }
 
 constexpr size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
+// As many CTAs as the bounds allow runs: never fewer than the lengths themselves ask for, so that how a batch is cut, and
+// with it every rounding, does not depend on how tight the bounds are.
 int64_t grid_of(int batch, int max_nodes, int max_context, int num_kv_heads, int lg) {
     const int qtok = ROWS >> lg;
-    const int64_t tiles = static_cast<int64_t>(batch) * ((static_cast<int64_t>(max_context) + KT - 1) / KT) * ((max_nodes + qtok - 1) / qtok) *
-                          num_kv_heads;
-    return std::max<int64_t>(1, std::min<int64_t>(CTAS_PER_SM * sm_count(), (tiles + MIN_RUN - 1) / MIN_RUN));
+    const int64_t cost = static_cast<int64_t>(batch) * ((static_cast<int64_t>(max_context) + KT - 1) / KT + UNIT_COST) *
+                         ((max_nodes + qtok - 1) / qtok) * num_kv_heads;
+    return std::max<int64_t>(1, std::min<int64_t>(CTAS_PER_SM * sm_count(), cost / MIN_RUN));
 }
 
 }  // namespace
@@ -815,17 +835,16 @@ pkv_status launch_tree_decode(const TreeDecodeArgs& a, int* err, cudaStream_t st
                          CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
             return PKV_ERR_INVALID_ARG;
     }
-    tm_k = tm_v = tm_q;                                       // the 8-bit kernel reads its pools itself
-    if (!fp8) {
+    {
+        const uint64_t row = static_cast<uint64_t>(D) * (fp8 ? 1 : 2);
         const uint64_t dims[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(a.num_kv_heads), static_cast<uint64_t>(a.block_size),
                                   static_cast<uint64_t>(a.num_blocks)};
-        const uint64_t strides[3] = {static_cast<uint64_t>(D) * 2, static_cast<uint64_t>(a.num_kv_heads) * D * 2,
-                                     static_cast<uint64_t>(a.block_size) * a.num_kv_heads * D * 2};
-        const uint32_t box[4] = {64u, 1u, static_cast<uint32_t>(KT), 1u};
-        if (encode_tiled(&tm_k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(a.k_cache), dims, strides, box,
-                         CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
-            encode_tiled(&tm_v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(a.v_cache), dims, strides, box,
-                         CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+        const uint64_t strides[3] = {row, a.num_kv_heads * row, static_cast<uint64_t>(a.block_size) * a.num_kv_heads * row};
+        const uint32_t box[4] = {fp8 ? 128u : 64u, 1u, static_cast<uint32_t>(KT), 1u};
+        const CUtensorMapDataType type = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+        const CUtensorMapSwizzle swizzle = fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
+        if (encode_tiled(&tm_k, type, 4, const_cast<void*>(a.k_cache), dims, strides, box, swizzle) != CUDA_SUCCESS ||
+            encode_tiled(&tm_v, type, 4, const_cast<void*>(a.v_cache), dims, strides, box, swizzle) != CUDA_SUCCESS)
             return PKV_ERR_INVALID_ARG;
     }
     const size_t ctas = static_cast<size_t>(CTAS_PER_SM) * sm_count();
@@ -839,7 +858,6 @@ pkv_status launch_tree_decode(const TreeDecodeArgs& a, int* err, cudaStream_t st
     p.cu_nodes = a.cu_nodes;
     p.mask = reinterpret_cast<const unsigned long long*>(a.tree_mask);
     p.out = a.out;
-    p.k_codes = static_cast<const uint8_t*>(a.k_cache);
     p.v_codes = static_cast<const uint8_t*>(a.v_cache);
     p.v_cache = static_cast<const uint16_t*>(a.v_cache);
     p.k_scale = a.k_scale;
@@ -859,9 +877,9 @@ pkv_status launch_tree_decode(const TreeDecodeArgs& a, int* err, cudaStream_t st
     p.err = err;
     const int grid = static_cast<int>(grid_of(a.batch, a.max_nodes, a.max_context, a.num_kv_heads, lg));
     if (fp8)
-        tree_decode_kernel<true><<<grid, 288, SMEM_BYTES, stream>>>(tm_q, tm_k, tm_v, p);
+        tree_decode_kernel<true><<<grid, THREADS_FP8, SMEM_BYTES, stream>>>(tm_q, tm_k, tm_v, p);
     else
-        tree_decode_kernel<false><<<grid, 192, SMEM_BYTES, stream>>>(tm_q, tm_k, tm_v, p);
+        tree_decode_kernel<false><<<grid, THREADS_BF16, SMEM_BYTES, stream>>>(tm_q, tm_k, tm_v, p);
     if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid, JOIN_SPLIT);
