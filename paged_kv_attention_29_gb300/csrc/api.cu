@@ -792,7 +792,7 @@ size_t pkv_tree_decode_workspace_size(int32_t batch, int32_t max_nodes, int32_t 
     if (batch < 0 || max_nodes < 0 || max_nodes > kMaxTreeNodes || !supported_shape(num_heads, num_kv_heads, head_dim, kBlockQuantum))
         return 0;
     if (sm_count() <= 0) return 0;
-    return tree_decode_workspace_bytes();
+    return tree_decode_workspace_bytes(num_kv_heads);
 }
 
 pkv_status pkv_tree_decode(const pkv_bf16* q, const pkv_bf16* k_cache, const pkv_bf16* v_cache, const int32_t* block_tables,

@@ -247,7 +247,7 @@ struct TreeDecodeArgs {
     void* workspace;
     size_t workspace_bytes;
 };
-size_t tree_decode_workspace_bytes();
+size_t tree_decode_workspace_bytes(int num_kv_heads);
 pkv_status launch_tree_decode(const TreeDecodeArgs& a, int* err, cudaStream_t stream);
 
 struct TreeAcceptArgs {

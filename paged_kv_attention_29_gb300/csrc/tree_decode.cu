@@ -16,10 +16,12 @@
 //   P           masked online softmax by the warpgroup, bf16 over S
 //   O += P V    tcgen05.mma with P from TMEM
 //
-// All units' tiles, in order, are cut into equal runs, one per CTA (two CTAs per SM, so
-// that one's loads and products fill the other's waits): a unit that a run does not
-// hold whole leaves fp32 partial sums with their maxima in the workspace, and a second
-// kernel joins them in the order of the runs.  Results are deterministic.
+// The tiles of all sequences, in order, are cut into runs of equal cost, and each run is
+// taken by a CTA per KV head (two CTAs per SM, so that one's loads and products fill the
+// other's waits; a run's CTAs are neighbours, so that the heads' rows of a token, which
+// lie side by side in memory, are read at about the same time): a unit that a run does
+// not hold whole leaves fp32 partial sums with their maxima in the workspace, and a
+// second kernel joins them in the order of the runs.  Results are deterministic.
 //
 // A node's row is as if masked keys were not there, whatever they hold: scores are
 // selected, not added to, and infinities and NaN among the nodes' V rows, which a
@@ -29,8 +31,9 @@
 // Warps 0-3: softmax and epilogue (TMEM lanes 0-127).  bf16 cache: warp 4 TMA producer,
 // warp 5 TMEM allocation and MMA issue.  8-bit cache: warps 4-7 turn the codes that TMA
 // has put into a slot of the ring into the bf16 values they stand for, in place; warp 8
-// issues, warp 9 is the producer.
+// issues, warp 9 is the producer, warps 10-11 only complete the third warpgroup.
 #include <algorithm>
+#include <type_traits>
 
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
@@ -44,7 +47,6 @@ constexpr int KT = 64;                       // keys per tile
 constexpr int Q_HALF = ROWS * 64 * 2;        // 128B-swizzled box of 64 dims: 16 KiB of Q
 constexpr int KV_HALF = KT * 64 * 2;         // 8 KiB of K or V
 constexpr int KV_TILE = 2 * KV_HALF;
-constexpr int SLOTS = 5;                     // ring of K and V tiles
 constexpr int TMEM_COLS = 256;
 constexpr int O_COL = 128;                   // S / P buffers at columns 0 and 64
 constexpr float kRescaleLog2 = 8.0f;
@@ -52,20 +54,29 @@ constexpr int UNIT_COST = 2;                 // what starting and ending a unit 
 constexpr int MIN_RUN = 4;                   // cost a CTA takes at least; above UNIT_COST, so that every run has a tile
 static_assert(MIN_RUN > UNIT_COST, "a run has a tile");
 constexpr int CTAS_PER_SM = 2;
-constexpr int THREADS_BF16 = 192, THREADS_FP8 = 320;
+constexpr int THREADS_BF16 = 192, THREADS_FP8 = 384;
+// The 8-bit kernel's warpgroups (softmax; decoding; producer, MMA and two warps that only complete it) split the
+// registers that the launch must provide, checked on the host before every launch: 136 + 56 + 48 = 3 * 80.
+constexpr uint32_t kSoftmaxRegs = 136, kDecodeRegs = 56, kControlRegs = 48, kMinLaunchRegs = 80;
+static_assert(kSoftmaxRegs + kDecodeRegs + kControlRegs <= 3 * kMinLaunchRegs, "setmaxnreg draws on the launch's registers");
 
-constexpr int SM_Q = 0;
-constexpr int SM_KV = 2 * Q_HALF;
-constexpr int SM_SCALE = SM_KV + SLOTS * KV_TILE;               // 8-bit cache: a scale byte per row of each slot
-constexpr int SM_BAR = SM_SCALE + SLOTS * KT;
-enum {
-    BAR_FULL = 0, BAR_EMPTY = BAR_FULL + SLOTS, BAR_RAW = BAR_EMPTY + SLOTS, BAR_QF = BAR_RAW + SLOTS, BAR_QE, BAR_SF, BAR_PF = BAR_SF + 2,
-    BAR_PV = BAR_PF + 2, BAR_OF, BAR_OE, BAR_WG, BAR_DRAIN, NUM_BARS
+// Shared memory.  bf16: rings of 2 K and 3 V tiles.  8 bits: 3 tiles of K codes and 3 V tiles, the row scales beside
+// them (K's are read as late as the softmax of their tile, when K tiles up to four behind may be in flight).
+template <bool FP8>
+struct Layout {
+    static constexpr int K_SLOTS = FP8 ? 3 : 2, V_SLOTS = 3, K_TILE = FP8 ? KT * D : KV_TILE, KS_SLOTS = FP8 ? 8 : 0;
+    static constexpr int Q = 0, K = 2 * Q_HALF, V = K + K_SLOTS * K_TILE, VS = V + V_SLOTS * KV_TILE, KS = VS + (FP8 ? V_SLOTS * KT : 0);
+    static constexpr int KSF = KS + KS_SLOTS * KT;                // K scales as floats, a copy for each softmax warp
+    static constexpr int BAR = KSF + (FP8 ? 4 * KT * 4 : 0);
+    static constexpr int KF = 0, KE = KF + K_SLOTS, VF = KE + K_SLOTS, VE = VF + V_SLOTS, VRAW = VE + V_SLOTS, KSB = VRAW + V_SLOTS, QF = KSB + KS_SLOTS,
+                         QR = QF + 1, QE = QR + 1, SF = QE + 1, PF = SF + 2, PV = PF + 2, OF = PV + 1, OE = OF + 1, WG = OE + 1, DRAIN = WG + 1,
+                         NUM_BARS = DRAIN + 1;
+    static constexpr int MISC = (BAR + NUM_BARS * 8 + 15) & ~15;  // [0] TMEM base, [1] abort, [2..9] nodes with infinities or NaN in V
+    static constexpr int SCAN = MISC + 48;                        // 16 x int64: set-up sums; then the run's start
+    static constexpr int BYTES = SCAN + 16 * 8;
+    static_assert(K % 1024 == 0 && V % 1024 == 0 && KSF % 16 == 0 && BAR % 8 == 0, "operand tiles and vectors need their alignment");
+    static_assert(CTAS_PER_SM * (BYTES + 1024) <= 228 * 1024, "two CTAs share an SM's shared memory");
 };
-constexpr int SM_MISC = (SM_BAR + NUM_BARS * 8 + 15) & ~15;      // [0] TMEM base, [1] abort, [2..9] nodes with infinities or NaN in V
-constexpr int SM_SCAN = SM_MISC + 48;                            // 16 x int64: set-up sums; then the run's start
-constexpr int SMEM_BYTES = SM_SCAN + 16 * 8;
-static_assert(CTAS_PER_SM * (SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs share an SM's shared memory");
 
 struct Params {
     const int32_t* block_tables;
@@ -75,7 +86,7 @@ struct Params {
     uint16_t* out;
     float4* part_o;           // [CTA][2][32][128]: four columns of each row
     float2* part_ml;          // [CTA][2][128]: maximum (log2) and sum
-    int4* meta;               // [CTA]: {last CTA of the unit that continues behind this one's run or -1, first row's node, nodes, KV head}
+    int4* meta;               // [CTA]: {last run of the unit that continues behind this one's or -1, first row's node, nodes, 0}
     const uint8_t* v_codes;   // 8-bit cache, for the values taken out of a tile
     const uint8_t* k_scale;
     const uint8_t* v_scale;
@@ -133,26 +144,25 @@ __device__ __forceinline__ Seq sequence(const Params& p, int b) {
 }
 __device__ __forceinline__ long long cost_of(const Params& p, const Seq& s) {
     const int qtok = ROWS >> p.lg;
-    return s.n ? static_cast<long long>((s.len + KT - 1) / KT + UNIT_COST) * ((s.n + qtok - 1) / qtok) * p.num_kv_heads : 0;
+    return s.n ? static_cast<long long>((s.len + KT - 1) / KT + UNIT_COST) * ((s.n + qtok - 1) / qtok) : 0;
 }
 
-// A CTA's run, segment by segment: tiles [j0, j1) of the unit (sequence b, KV head g, row tile rt).  Runs are cut in
+// A CTA's run, segment by segment: tiles [j0, j1) of the unit (sequence b, row tile rt).  Runs are cut in
 // cost: a unit is UNIT_COST steps without a tile and then a step per tile.  Every role walks by itself.
 struct Walk {
     const Params& p;
     Seq s;
-    int b, g, rt, nt, nrt, j0, j1;
+    int b, rt, nt, nrt, j0, j1;
     long long left;                          // cost of the run behind this segment
 
     __device__ __forceinline__ Walk(const Params& params, int b0, long long off, long long count) : p(params), b(b0) {
-        g = rt = j0 = j1 = nt = nrt = 0;
+        rt = j0 = j1 = nt = nrt = 0;
         left = count;
         if (count <= 0) return;
         enter();
         const int per = nt + UNIT_COST;
-        const int unit = static_cast<int>(off / per), at = static_cast<int>(off - static_cast<long long>(unit) * per);
-        g = unit / nrt;
-        rt = unit - g * nrt;
+        rt = static_cast<int>(off / per);
+        const int at = static_cast<int>(off - static_cast<long long>(rt) * per);
         j0 = max(0, at - UNIT_COST);
         clip(max(0, UNIT_COST - at));
         if (j0 == j1) next();                // nothing of the last unit's steps but its first ones
@@ -174,13 +184,10 @@ struct Walk {
         if (last()) return;
         if (++rt == nrt) {
             rt = 0;
-            if (++g == p.num_kv_heads) {
-                g = 0;
-                do {
-                    if (++b >= p.batch) return;
-                    enter();
-                } while (s.n == 0);
-            }
+            do {
+                if (++b >= p.batch) return;
+                enter();
+            } while (s.n == 0);
         }
         clip(UNIT_COST);
     }
@@ -195,10 +202,6 @@ struct Walk {
         return -1;
     }
 };
-
-// Sequence numbers in the ring of the K and V tiles of a run's tile t: K(0), then K(t + 1) and V(t) for each t.
-__device__ __forceinline__ int k_seq(int t) { return t == 0 ? 0 : 2 * t - 1; }
-__device__ __forceinline__ int v_seq(int t, bool last) { return last ? 2 * t + 1 : 2 * t + 2; }
 
 // Which of a tile's keys a node sees: bit e for key 64 j + e.
 __device__ __forceinline__ unsigned long long visible(const unsigned long long (&w)[4], int rel, int keys) {
@@ -224,6 +227,14 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     return d;
 }
 
+// Four numbers rounded to e4m3, the first in the lowest byte.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+    uint32_t w;
+    asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\tmov.b32 %0, {lo, hi};\n\t}"
+        : "=r"(w) : "f"(a), "f"(b), "f"(c), "f"(d));
+    return w;
+}
+
 // Two bytes of w, each as 16 bits with its sign in the upper eight: bytes 0 and 1 by the selector 0x9180, 2 and 3 by 0xb3a2.
 template <uint32_t SEL>
 __device__ __forceinline__ uint32_t widen(uint32_t w) {
@@ -235,38 +246,71 @@ __device__ __forceinline__ uint32_t widen(uint32_t w) {
 // 16 e4m3 codes and their row's scale byte as 16 bf16.  A code's bits, set one exponent field further, read as a bf16
 // 2^-120 times its value (its subnormals as bf16's), so a product with 2^120 times the scale, in two factors where one
 // would not fit, is exact; only the NaN code needs to be seen.
-// The rest, out of line: rows with a NaN code, and scales for which one factor does not do.
-__device__ __noinline__ void bf16_of_odd_row(const uint32_t (&w)[4], uint32_t byte, uint32_t (&o)[8]) {
-    const float f = e8m0_value(byte);
-#pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
-        const uint2 x = bf16_of_codes(w[i], f);
-        o[2 * i] = x.x;
-        o[2 * i + 1] = x.y;
-    }
+__device__ __forceinline__ bool odd_row(const uint4& c, uint32_t byte) {      // a NaN code, or a scale outside 2^-119 .. 2^7
+    const uint32_t nan = ((c.x & 0x7f7f7f7fu) + 0x01010101u) | ((c.y & 0x7f7f7f7fu) + 0x01010101u) | ((c.z & 0x7f7f7f7fu) + 0x01010101u) |
+                         ((c.w & 0x7f7f7f7fu) + 0x01010101u);
+    return (nan & 0x80808080u) != 0u || byte - 8u > 126u;
 }
-
+template <bool ODD>
 __device__ __forceinline__ void bf16_of_row(const uint4& c, uint32_t byte, uint4& lo, uint4& hi) {
     const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-    uint32_t nan = 0u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) nan |= (w[i] & 0x7f7f7f7fu) + 0x01010101u;
-    uint32_t o[8];
-    if ((nan & 0x80808080u) != 0u || byte - 8u > 126u) {             // a NaN, or a scale outside 2^-119 .. 2^7
-        uint32_t odd[8];
-        bf16_of_odd_row(w, byte, odd);
-        lo = make_uint4(odd[0], odd[1], odd[2], odd[3]);
-        hi = make_uint4(odd[4], odd[5], odd[6], odd[7]);
-        return;
-    }
     const uint32_t f = (byte + 120u) * 0x00800080u;                  // 2^(120 + e) twice
+    uint32_t o[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        o[2 * i] = hmul2((widen<0x9180u>(w[i]) << 4) & 0x87f087f0u, f);
-        o[2 * i + 1] = hmul2((widen<0xb3a2u>(w[i]) << 4) & 0x87f087f0u, f);
+        if (ODD) {
+            const uint2 x = bf16_of_codes(w[i], e8m0_value(byte));
+            o[2 * i] = x.x;
+            o[2 * i + 1] = x.y;
+        } else {
+            o[2 * i] = hmul2((widen<0x9180u>(w[i]) << 4) & 0x87f087f0u, f);
+            o[2 * i + 1] = hmul2((widen<0xb3a2u>(w[i]) << 4) & 0x87f087f0u, f);
+        }
     }
     lo = make_uint4(o[0], o[1], o[2], o[3]);
     hi = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// A query row for the product with codes.  With f the power of two that takes the row's largest |q| to [128, 256), q f
+// is a sum of two e4m3 numbers, the nearest one and what is left: exactly where |q| is 2^-10 of the largest or more (8
+// bits are 4 + 4), and to 2^-18 of the largest otherwise.  The row is replaced by its two parts, each laid out as 128
+// bytes of a K-major tile; returns 1 / f, or NaN for a row with an infinity or a NaN.
+__device__ __forceinline__ float split_row(uint8_t* q, int row) {
+    uint32_t x[64];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const uint4 v = *reinterpret_cast<const uint4*>(q + (i >> 3) * Q_HALF + row * 128 + (((i & 7) ^ (row & 7)) * 16));
+        x[4 * i] = v.x;
+        x[4 * i + 1] = v.y;
+        x[4 * i + 2] = v.z;
+        x[4 * i + 3] = v.w;
+    }
+    uint32_t most = 0u;
+#pragma unroll
+    for (int i = 0; i < 64; ++i) {
+        const uint32_t a = x[i] & 0x7fff7fffu;
+        asm("max.u16x2 %0, %0, %1;" : "+r"(most) : "r"(a));
+    }
+    const uint32_t e = max(8u, max(most & 0xffffu, most >> 16) >> 7);            // exponent field of the largest
+    const float f = __uint_as_float((261u - e) << 23);                           // 2^(134 - e)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t a = x[8 * i + 2 * k], b = x[8 * i + 2 * k + 1];
+            const float y0 = bf16_lo(a) * f, y1 = bf16_hi(a) * f, y2 = bf16_lo(b) * f, y3 = bf16_hi(b) * f;
+            hi[k] = e4m3x4(y0, y1, y2, y3);
+            uint32_t h0, h1;
+            f16_of_codes(hi[k], h0, h1);
+            const float2 z0 = __half22float2(*reinterpret_cast<const __half2*>(&h0)), z1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+            lo[k] = e4m3x4(y0 - z0.x, y1 - z0.y, y2 - z1.x, y3 - z1.y);
+        }
+        uint8_t* at = q + row * 128 + ((i ^ (row & 7)) * 16);
+        *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(at + Q_HALF) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    return e == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float((e - 7u) << 23);
 }
 
 template <bool FP8>
@@ -276,17 +320,18 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     constexpr int THREADS = FP8 ? THREADS_FP8 : THREADS_BF16, LOAD_WARP = FP8 ? 9 : 4, MMA_WARP = FP8 ? 8 : 5;
     extern __shared__ __align__(1024) uint8_t gbase[];
     const uint32_t base = smem_u32(gbase);
-    const uint32_t sQ = base + SM_Q, sKV = base + SM_KV, bars = base + SM_BAR;
+    using L = Layout<FP8>;
+    const uint32_t sQ = base + L::Q, bars = base + L::BAR;
     auto bar = [&](int i) { return bars + 8u * i; };
-    uint32_t* misc = reinterpret_cast<uint32_t*>(gbase + SM_MISC);
-    long long* scan = reinterpret_cast<long long*>(gbase + SM_SCAN);
+    uint32_t* misc = reinterpret_cast<uint32_t*>(gbase + L::MISC);
+    long long* scan = reinterpret_cast<long long*>(gbase + L::SCAN);
     Ctl ctl{reinterpret_cast<volatile uint32_t*>(misc + 1), p.err};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid == 0) {
-        for (int i = 0; i < NUM_BARS; ++i) {
-            const bool per_warp = i == BAR_PF || i == BAR_PF + 1 || i == BAR_OE || i == BAR_WG || (FP8 && i >= BAR_FULL && i < BAR_FULL + SLOTS);
+        for (int i = 0; i < L::NUM_BARS; ++i) {
+            const bool per_warp = i == L::PF || i == L::PF + 1 || i == L::OE || i == L::WG || i == L::QR || (FP8 && i >= L::VF && i < L::VE);
             mbar_init(bar(i), per_warp ? 4 : 1);
         }
         misc[1] = 0u;
@@ -296,7 +341,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         tma_prefetch_desc(&tm_v);
     }
     if (warp == MMA_WARP) {
-        tmem_alloc(base + SM_MISC, TMEM_COLS);
+        tmem_alloc(base + L::MISC, TMEM_COLS);
         tmem_relinquish();
     }
     // The run: all tiles are counted, then the sequence in which this CTA's share starts is searched, a
@@ -330,8 +375,9 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     }
     long long W;
     long long upto = block_scan(mine, W);
-    const long long C = max(1ll, min(static_cast<long long>(gridDim.x), W / MIN_RUN));
-    const long long c = blockIdx.x;
+    const long long C = max(1ll, min(static_cast<long long>(gridDim.x / p.num_kv_heads), W / MIN_RUN));
+    const long long c = blockIdx.x / p.num_kv_heads;
+    const int g = static_cast<int>(blockIdx.x - c * p.num_kv_heads);
     const long long t0 = c < C ? c * W / C : 0, t1 = c < C ? (c + 1) * W / C : 0;
     if (t1 > t0) {
         long long before = 0;
@@ -361,100 +407,133 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     Walk w(p, busy ? static_cast<int>(scan[14]) : 0, busy ? scan[15] : 0, t1 - t0);
 
     if (warp == LOAD_WARP) {
+        if (FP8) regs_dec<kControlRegs>();
         // ---------------------------------------------------------------- TMA producer
         if (lane == 0 && busy) {
-            int seq = 0, segs = 0;                            // tiles and Q tiles issued
+            int kt = 0, vt = 0, segs = 0;                     // K, V and Q tiles issued
             bool ok = true;
-            auto load = [&](bool k, int phys, int off, int g) {
-                const int slot = seq % SLOTS;
-                if (seq >= SLOTS && !(ok = wait_phase(ctl, bar(BAR_EMPTY + slot), ((seq / SLOTS) - 1) & 1))) return;
-                const uint32_t dst = sKV + slot * KV_TILE, full = bar((FP8 ? BAR_RAW : BAR_FULL) + slot);
-                const CUtensorMap* map = k ? &tm_k : &tm_v;
+            auto load_k = [&](int phys, int off) {
+                const int slot = kt % L::K_SLOTS;
+                if (kt >= L::K_SLOTS && !(ok = wait_phase(ctl, bar(L::KE + slot), ((kt / L::K_SLOTS) - 1) & 1))) return;
+                const uint32_t dst = base + L::K + slot * L::K_TILE, full = bar(L::KF + slot);
+                mbar_arrive_expect_tx(full, L::K_TILE);
+                tma_load_4d(dst, &tm_k, full, 0, g, off, phys);
+                if (FP8) {
+                    const int64_t at = (static_cast<int64_t>(max(phys, 0)) * p.num_kv_heads + g) * p.block_size + off;
+                    const int s = kt % max(1, L::KS_SLOTS);
+                    mbar_arrive_expect_tx(bar(L::KSB + s), KT);
+                    bulk_load(base + L::KS + s * KT, p.k_scale + at, KT, bar(L::KSB + s));
+                } else {
+                    tma_load_4d(dst + KV_HALF, &tm_k, full, 64, g, off, phys);
+                }
+                ++kt;
+            };
+            auto load_v = [&](int phys, int off) {
+                const int slot = vt % L::V_SLOTS;
+                if (vt >= L::V_SLOTS && !(ok = wait_phase(ctl, bar(L::VE + slot), ((vt / L::V_SLOTS) - 1) & 1))) return;
+                const uint32_t dst = base + L::V + slot * KV_TILE, full = bar((FP8 ? L::VRAW : L::VF) + slot);
                 if (FP8) {
                     // codes to the slot's second half, where the warp that decodes a row finds and overwrites it
                     const int64_t at = (static_cast<int64_t>(max(phys, 0)) * p.num_kv_heads + g) * p.block_size + off;
                     mbar_arrive_expect_tx(full, KV_HALF + KT);
-                    tma_load_4d(dst + KV_HALF, map, full, 0, g, off, phys);
-                    bulk_load(base + SM_SCALE + slot * KT, (k ? p.k_scale : p.v_scale) + at, KT, full);
+                    tma_load_4d(dst + KV_HALF, &tm_v, full, 0, g, off, phys);
+                    bulk_load(base + L::VS + slot * KT, p.v_scale + at, KT, full);
                 } else {
                     mbar_arrive_expect_tx(full, KV_TILE);
-                    tma_load_4d(dst, map, full, 0, g, off, phys);
-                    tma_load_4d(dst + KV_HALF, map, full, 64, g, off, phys);
+                    tma_load_4d(dst, &tm_v, full, 0, g, off, phys);
+                    tma_load_4d(dst + KV_HALF, &tm_v, full, 64, g, off, phys);
                 }
-                ++seq;
+                ++vt;
             };
             auto load_q = [&] {
-                if (segs >= 1 && !(ok = wait_phase(ctl, bar(BAR_QE), (segs - 1) & 1))) return;
-                mbar_arrive_expect_tx(bar(BAR_QF), 2 * Q_HALF);
-                const int row = w.s.q0 + w.rt * (ROWS >> p.lg), head = w.g << p.lg;
-                tma_load_3d(sQ, &tm_q, bar(BAR_QF), 0, head, row);
-                tma_load_3d(sQ + Q_HALF, &tm_q, bar(BAR_QF), 64, head, row);
+                if (segs >= 1 && !(ok = wait_phase(ctl, bar(L::QE), (segs - 1) & 1))) return;
+                mbar_arrive_expect_tx(bar(L::QF), 2 * Q_HALF);
+                const int row = w.s.q0 + w.rt * (ROWS >> p.lg), head = g << p.lg;
+                tma_load_3d(sQ, &tm_q, bar(L::QF), 0, head, row);
+                tma_load_3d(sQ + Q_HALF, &tm_q, bar(L::QF), 64, head, row);
                 ++segs;
             };
             load_q();
-            int j = w.j0, k_off, k_phys = w.block_of(j, k_off), k_g = w.g;
-            load(true, k_phys, k_off, k_g);
+            int j = w.j0, k_off, k_phys = w.block_of(j, k_off);
+            load_k(k_phys, k_off);
             while (ok) {
-                const int v_phys = k_phys, v_off = k_off, v_g = k_g;
+                const int v_phys = k_phys, v_off = k_off;
                 const bool fresh = j + 1 == w.j1, end = fresh && w.last();
                 if (!end) {
                     if (fresh) w.next();
                     j = fresh ? w.j0 : j + 1;
                     k_phys = w.block_of(j, k_off);
-                    k_g = w.g;
-                    load(true, k_phys, k_off, k_g);
+                    load_k(k_phys, k_off);
                     if (!ok) break;
                 }
-                load(false, v_phys, v_off, v_g);
+                load_v(v_phys, v_off);
                 if (!ok || end) break;
                 if (fresh) load_q();
             }
             if (*ctl.abort) {
                 // copies in flight land before shared memory is released
-                if (segs > 0) wait_drain(bar(BAR_QF), (segs - 1) & 1);
-                for (int i = max(0, seq - SLOTS); i < seq; ++i) wait_drain(bar((FP8 ? BAR_RAW : BAR_FULL) + i % SLOTS), (i / SLOTS) & 1);
+                if (segs > 0) wait_drain(bar(L::QF), (segs - 1) & 1);
+                for (int i = max(0, kt - L::K_SLOTS); i < kt; ++i) wait_drain(bar(L::KF + i % L::K_SLOTS), (i / L::K_SLOTS) & 1);
+                for (int i = max(0, vt - L::V_SLOTS); i < vt; ++i) wait_drain(bar((FP8 ? L::VRAW : L::VF) + i % L::V_SLOTS), (i / L::V_SLOTS) & 1);
+                if (FP8)
+                    for (int i = max(0, kt - L::KS_SLOTS); i < kt; ++i)
+                        wait_drain(bar(L::KSB + i % max(1, L::KS_SLOTS)), (i / max(1, L::KS_SLOTS)) & 1);
             }
         }
         __syncwarp();
         tc_fence_before();
         __syncthreads();
     } else if (FP8 && warp >= 4 && warp < 8) {
-        // ---------------------------------------------------------------- 8-bit rows to bf16 tiles
+        // ---------------------------------------------------------------- 8-bit V rows to bf16 tiles
         // Warp x decodes rows 16 x .. 16 x + 15 of each tile.  Their codes lie where the second half of their values
-        // will, so a warp that has read its rows may write them.
-        const int vec = lane & 7, row0 = (warp - 4) * 16 + (lane >> 3);
-        int tiles = 0;                                        // of K and V in this run
-        for (; w.more(); w.next()) tiles += 2 * (w.j1 - w.j0);
+        // will, so a warp that has read its rows may write them.  Eight lanes take half of two rows whose numbers
+        // differ in bits 0 and 2: with the chunks of the codes (as TMA has put them) and of the values at an exclusive
+        // or with the row, neither the loads nor the stores meet in a bank.
+        regs_dec<kDecodeRegs>();
+        const int half = (lane >> 3) & 1, vec = half * 4 + (lane & 3);
+        int tiles = 0;                                        // in this run
+        for (; w.more(); w.next()) tiles += w.j1 - w.j0;
 #pragma unroll 1
-        for (int seq = 0; seq < tiles; ++seq) {
-            const int slot = seq % SLOTS;
-            if (!wait_warp(ctl, bar(BAR_RAW + slot), (seq / SLOTS) & 1)) break;
-            uint8_t* tile = gbase + SM_KV + slot * KV_TILE;
-            const uint8_t* scales = gbase + SM_SCALE + slot * KT;
+        for (int t = 0; t < tiles; ++t) {
+            const int slot = t % L::V_SLOTS;
+            if (!wait_warp(ctl, bar(L::VRAW + slot), (t / L::V_SLOTS) & 1)) break;
+            uint8_t* tile = gbase + L::V + slot * KV_TILE;
+            const uint8_t* scales = gbase + L::VS + slot * KT;
             uint4 c[4];
             uint32_t byte[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                c[i] = *reinterpret_cast<const uint4*>(tile + KV_HALF + (row0 + 4 * i) * 128 + vec * 16);
-                byte[i] = scales[row0 + 4 * i];
+                const int row = (warp - 4) * 16 + ((2 * (lane >> 4) + 4 * i) ^ (lane & 4 ? 5 : 0));
+                c[i] = *reinterpret_cast<const uint4*>(tile + KV_HALF + row * 128 + ((vec ^ (row & 7)) * 16));
+                byte[i] = scales[row];
             }
             __syncwarp();
+            bool odd = false;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = row0 + 4 * i, ch = (vec & 3) * 2;
-                uint4 lo, hi;
-                bf16_of_row(c[i], byte[i], lo, hi);
-                uint8_t* dst = tile + (vec >> 2) * KV_HALF + row * 128;
-                *reinterpret_cast<uint4*>(dst + ((ch ^ (row & 7)) * 16)) = lo;
-                *reinterpret_cast<uint4*>(dst + (((ch + 1) ^ (row & 7)) * 16)) = hi;
-            }
+            for (int i = 0; i < 4; ++i) odd |= odd_row(c[i], byte[i]);
+            auto put = [&](auto rare) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = (warp - 4) * 16 + ((2 * (lane >> 4) + 4 * i) ^ (lane & 4 ? 5 : 0)), ch = (lane & 3) * 2;
+                    uint4 lo, hi;
+                    bf16_of_row<decltype(rare)::value>(c[i], byte[i], lo, hi);
+                    uint8_t* dst = tile + half * KV_HALF + row * 128;
+                    *reinterpret_cast<uint4*>(dst + ((ch ^ (row & 7)) * 16)) = lo;
+                    *reinterpret_cast<uint4*>(dst + (((ch + 1) ^ (row & 7)) * 16)) = hi;
+                }
+            };
+            if (__any_sync(0xffffffffu, odd))
+                put(std::true_type{});
+            else
+                put(std::false_type{});
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(BAR_FULL + slot));
+            if (lane == 0) mbar_arrive(bar(L::VF + slot));
         }
         tc_fence_before();
         __syncthreads();
     } else if (warp == MMA_WARP) {
+        if (FP8) regs_dec<kControlRegs>();
         // ---------------------------------------------------------------- MMA
         // The whole warp runs this loop in step; each tcgen05 instruction is issued by one elected lane.
         constexpr uint32_t idesc_qk = idesc_bf16_f32(ROWS, KT, 0, 0);
@@ -465,20 +544,28 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         bool ok = busy;
         auto issue_s = [&](int t, bool seg_first, bool seg_last) {
             if (seg_first) {
-                if (!(ok = wait_warp(ctl, bar(BAR_QF), segs & 1))) return;
+                if (!(ok = wait_warp(ctl, bar(FP8 ? L::QR : L::QF), segs & 1))) return;
                 ++segs;
             }
-            const int sq = k_seq(t), slot = sq % SLOTS;
-            if (!(ok = wait_warp(ctl, bar(BAR_FULL + slot), (sq / SLOTS) & 1))) return;
+            const int slot = t % L::K_SLOTS;
+            if (!(ok = wait_warp(ctl, bar(L::KF + slot), (t / L::K_SLOTS) & 1))) return;
             tc_fence_after();
-            const uint64_t dk = smem_desc(sKV + slot * KV_TILE, 16, 1024, 2);
+            const uint64_t dk = smem_desc(base + L::K + slot * L::K_TILE, 16, 1024, 2);
+            if (FP8) {
+                // the codes themselves: Q's two parts, 32 dims a step
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-                mma_ss_warp(tmem + (t & 1) * KT, dq + (((ks >> 2) * Q_HALF + (ks & 3) * 32) >> 4),
-                            dk + (((ks >> 2) * KV_HALF + (ks & 3) * 32) >> 4), idesc_qk, ks > 0 ? 1u : 0u);
-            mma_commit_warp(bar(BAR_SF + (t & 1)));
-            mma_commit_warp(bar(BAR_EMPTY + slot));
-            if (seg_last) mma_commit_warp(bar(BAR_QE));
+                for (int ks = 0; ks < 2 * D / 32; ++ks)
+                    mma_f8_warp(tmem + (t & 1) * KT, dq + (((ks >> 2) * Q_HALF + (ks & 3) * 32) >> 4), dk + ((ks & 3) * 32 >> 4), idesc_e4m3_f32(ROWS, KT),
+                                ks > 0 ? 1u : 0u);
+            } else {
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    mma_ss_warp(tmem + (t & 1) * KT, dq + (((ks >> 2) * Q_HALF + (ks & 3) * 32) >> 4),
+                                dk + (((ks >> 2) * KV_HALF + (ks & 3) * 32) >> 4), idesc_qk, ks > 0 ? 1u : 0u);
+            }
+            mma_commit_warp(bar(L::SF + (t & 1)));
+            mma_commit_warp(bar(L::KE + slot));
+            if (seg_last) mma_commit_warp(bar(L::QE));
         };
         int j = w.j0;
         if (ok) issue_s(0, true, w.j0 + 1 == w.j1);
@@ -490,20 +577,20 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (!ok) break;
             }
             if (first_here) {
-                if (oseg >= 1 && !(ok = wait_warp(ctl, bar(BAR_OE), (oseg - 1) & 1))) break;
+                if (oseg >= 1 && !(ok = wait_warp(ctl, bar(L::OE), (oseg - 1) & 1))) break;
                 ++oseg;
             }
-            const int sq = v_seq(t, end), slot = sq % SLOTS;
-            if (!(ok = wait_warp(ctl, bar(BAR_FULL + slot), (sq / SLOTS) & 1))) break;
-            if (!(ok = wait_warp(ctl, bar(BAR_PF + (t & 1)), (t >> 1) & 1))) break;
+            const int slot = t % L::V_SLOTS;
+            if (!(ok = wait_warp(ctl, bar(L::VF + slot), (t / L::V_SLOTS) & 1))) break;
+            if (!(ok = wait_warp(ctl, bar(L::PF + (t & 1)), (t >> 1) & 1))) break;
             tc_fence_after();
-            const uint64_t dv = smem_desc(sKV + slot * KV_TILE, KV_HALF, 1024, 2);
+            const uint64_t dv = smem_desc(base + L::V + slot * KV_TILE, KV_HALF, 1024, 2);
             for (int ks = 0; ks < (keys + 15) >> 4; ++ks)
                 mma_ts_warp(tmem + O_COL, tmem + (t & 1) * KT + ks * 8, dv + ks * (16 * 128 >> 4), idesc_pv,
                             (!first_here || ks > 0) ? 1u : 0u);
-            mma_commit_warp(bar(BAR_PV));
-            mma_commit_warp(bar(BAR_EMPTY + slot));
-            if (last_here) mma_commit_warp(bar(BAR_OF));
+            mma_commit_warp(bar(L::PV));
+            mma_commit_warp(bar(L::VE + slot));
+            if (last_here) mma_commit_warp(bar(L::OF));
             if (end) break;
             if (last_here) {
                 w.next();
@@ -513,18 +600,21 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 ++j;
             }
         }
-        mma_commit_warp(bar(BAR_DRAIN));
-        wait_drain(bar(BAR_DRAIN), 0);
+        mma_commit_warp(bar(L::DRAIN));
+        wait_drain(bar(L::DRAIN), 0);
         __syncwarp();
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
         tmem_dealloc(tmem, TMEM_COLS);
+    } else if (FP8 && warp >= 10) {
+        regs_dec<kControlRegs>();
+        __syncthreads();
     } else {
         // ---------------------------------------------------------------- softmax and epilogue
+        if (FP8) regs_inc<kSoftmaxRegs>();
         const int row = tid;                                  // TMEM lane
         const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
-        const float sc = p.scale_log2;
         const int qtok = ROWS >> p.lg;
         int t = 0, seg = 0;
         bool ok = true;
@@ -532,8 +622,8 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         uint32_t meets = 0;
         auto meet = [&] {                                     // a barrier of the four warps that gives up with the others
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(BAR_WG));
-            ok = wait_warp(ctl, bar(BAR_WG), meets++ & 1u);
+            if (lane == 0) mbar_arrive(bar(L::WG));
+            ok = wait_warp(ctl, bar(L::WG), meets++ & 1u);
             return ok;
         };
         for (; w.more() && ok; w.next(), ++seg) {
@@ -547,16 +637,24 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 words[i] = live && i < p.mask_words ? __ldg(p.mask + static_cast<int64_t>(node_row) * p.mask_words + i) : 0ull;
-            float m_used = -INFINITY, l = 0.f;
+            float m_used = -INFINITY, l = 0.f, sc = p.scale_log2;
             bool had_tree = false;
+            if (FP8) {
+                ok = wait_warp(ctl, bar(L::QF), seg & 1);
+                if (!ok) break;
+                if (warp_live) sc *= split_row(gbase + L::Q, row);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::QR));
+            }
             for (int j = w.j0; j < w.j1; ++j, ++t) {
                 const int keys = min(KT, w.s.len - j * KT), rel = j * KT - tree0;
                 const bool tree = rel + KT > 0;               // nodes among the keys: on no more than the last few tiles
                 if (tree) {
                     // Infinities and NaN among the nodes' V rows leave the tile, and so does what the block holds
                     // behind the last key: weights of 0 would spread them.
-                    const int sq = v_seq(t, j + 1 == w.j1 && w.last()), slot = sq % SLOTS;
-                    ok = wait_warp(ctl, bar(BAR_FULL + slot), (sq / SLOTS) & 1);
+                    const int slot = t % L::V_SLOTS;
+                    ok = wait_warp(ctl, bar(L::VF + slot), (t / L::V_SLOTS) & 1);
                     if (!ok) break;
                     if (!had_tree) {
                         if (!meet()) break;                   // the last segment's bits are read
@@ -564,7 +662,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         if (!meet()) break;
                         had_tree = true;
                     }
-                    uint8_t* vt = gbase + SM_KV + slot * KV_TILE;
+                    uint8_t* vt = gbase + L::V + slot * KV_TILE;
                     const int lo = max(0, -rel), hi = (keys + 15) & ~15;
                     for (int i = lo * 16 + tid; i < hi * 16; i += 128) {
                         const int r = i >> 4;
@@ -587,7 +685,17 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
-                ok = wait_warp(ctl, bar(BAR_SF + (t & 1)), (t >> 1) & 1);
+                float* ksf = reinterpret_cast<float*>(gbase + L::KSF) + warp * KT;
+                if (FP8 && warp_live) {
+                    const int s = t % max(1, L::KS_SLOTS);
+                    ok = wait_warp(ctl, bar(L::KSB + s), (t / max(1, L::KS_SLOTS)) & 1);
+                    if (!ok) break;
+                    const uint8_t* ks = gbase + L::KS + s * KT;
+                    ksf[lane] = e8m0_value(ks[lane]);
+                    ksf[lane + 32] = e8m0_value(ks[lane + 32]);
+                    __syncwarp();
+                }
+                ok = wait_warp(ctl, bar(L::SF + (t & 1)), (t >> 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
                 if (warp_live) {
@@ -601,6 +709,14 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         tmem_ld_wait();
 #pragma unroll
                         for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(r[e]);
+                        if (FP8) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                const float4 f = *reinterpret_cast<const float4*>(ksf + 32 * cc + e);
+                                fmul2(x[e], x[e + 1], x[e], x[e + 1], f.x, f.y);
+                                fmul2(x[e + 2], x[e + 3], x[e + 2], x[e + 3], f.z, f.w);
+                            }
+                        }
                     };
                     float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
@@ -609,16 +725,14 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         read(cc, x);
                         if (tree) {
                             const uint32_t bits = static_cast<uint32_t>(see >> (32 * cc));
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[e] = (bits >> e) & 1u ? x[e] : -INFINITY;
+                        }
+                        if (FP8) {
                             uint32_t r[32];
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                x[e] = (bits >> e) & 1u ? x[e] : -INFINITY;
-                                r[e] = __float_as_uint(x[e]);
-                            }
-                            if (FP8) {
-                                tmem_st32(s_tmem + 32 * cc, r);
-                                tmem_st_wait();
-                            }
+                            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(x[e]);
+                            tmem_st32(s_tmem + 32 * cc, r);
                         }
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
@@ -626,12 +740,13 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             mx1 = fmax3(mx1, x[e + 2], x[e + 3]);
                         }
                     }
+                    if (FP8) tmem_st_wait();
                     const float m_new = fmaxf(mx0, mx1) * sc;
                     if (j == w.j0) {
                         m_used = m_new;
                     } else if (__any_sync(0xffffffffu, m_new > m_used + kRescaleLog2)) {
                         // O is rescaled only when a maximum grows by 2^8; PV(t - 1) has to be through
-                        ok = wait_warp(ctl, bar(BAR_PV), (t - 1) & 1);
+                        ok = wait_warp(ctl, bar(L::PV), (t - 1) & 1);
                         if (!ok) break;
                         tc_fence_after();
                         const float m_tgt = fmaxf(m_used, m_new);
@@ -655,7 +770,13 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     for (int cc = 0; cc < 2; ++cc) {
                         uint32_t pk[16];
                         float (&x)[32] = s[FP8 ? 0 : cc];
-                        if (FP8) read(cc, x);
+                        if (FP8) {                            // scaled and masked above
+                            uint32_t r[32];
+                            tmem_ld32(s_tmem + 32 * cc, r);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(r[e]);
+                        }
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
                             float a0, a1, a2, a3;
@@ -674,10 +795,10 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(BAR_PF + (t & 1)));
+                if (lane == 0) mbar_arrive(bar(L::PF + (t & 1)));
             }
             if (!ok) break;
-            ok = wait_warp(ctl, bar(BAR_OF), seg & 1);
+            ok = wait_warp(ctl, bar(L::OF), seg & 1);
             if (!ok) break;
             tc_fence_after();
             if (had_tree && !meet()) break;                   // every warp's bits are there
@@ -686,7 +807,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (!whole && part == 1) {
                 // its last run: that of the unit's last tile, which lies nt - j1 steps behind this run's end
                 const long long end = t1 + (w.nt - w.j1);
-                meta = make_int4(static_cast<int>((end * C - 1) / W), w.s.q0 + w.rt * qtok, tokens, w.g);
+                meta = make_int4(static_cast<int>((end * C - 1) / W), w.s.q0 + w.rt * qtok, tokens, 0);
             }
             if (warp_live) {
                 uint32_t any = 0u;
@@ -694,7 +815,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     for (int i = 0; i < 8; ++i) any |= misc[2 + i];
                 const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
                 const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + part;
-                uint16_t* orow = p.out + (static_cast<int64_t>(node_row) * p.num_heads + (w.g << p.lg) + (row & ((1 << p.lg) - 1))) * D;
+                uint16_t* orow = p.out + (static_cast<int64_t>(node_row) * p.num_heads + (g << p.lg) + (row & ((1 << p.lg) - 1))) * D;
                 if (!whole) p.part_ml[slot * ROWS + row] = make_float2(m_used, l);
 #pragma unroll 1
                 for (int cc = 0; cc < 4; ++cc) {
@@ -712,8 +833,8 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             const int phys = w.block_of(j, off);
                             if (phys < 0) continue;
                             const int64_t at = static_cast<int64_t>(phys) * p.block_size + off + (tree0 + i - j * KT);
-                            const int64_t first_v = (at * p.num_kv_heads + w.g) * D + 32 * cc;
-                            const float f = FP8 ? e8m0_value(__ldg(p.v_scale + (static_cast<int64_t>(phys) * p.num_kv_heads + w.g) * p.block_size + off +
+                            const int64_t first_v = (at * p.num_kv_heads + g) * D + 32 * cc;
+                            const float f = FP8 ? e8m0_value(__ldg(p.v_scale + (static_cast<int64_t>(phys) * p.num_kv_heads + g) * p.block_size + off +
                                                                    (tree0 + i - j * KT))) : 1.f;
 #pragma unroll
                             for (int e = 0; e < 32; e += 4) {
@@ -749,7 +870,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(BAR_OE));
+            if (lane == 0) mbar_arrive(bar(L::OE));
         }
         if (tid == 0) p.meta[blockIdx.x] = ok ? meta : make_int4(-1, 0, 0, 0);
         tc_fence_before();
@@ -757,19 +878,20 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     }
 }
 
-// The units that several runs share: block (c, y) joins 32 columns of the unit that starts in run c and goes on behind
-// it, a thread 16 columns of one row.
+// The units that several runs share: block (CTA, y) joins 32 columns of the unit that starts in the CTA's run and goes on
+// behind it, a thread 16 columns of one row.
 constexpr int JOIN_THREADS = 2 * ROWS, JOIN_SPLIT = 4;
 __global__ void __launch_bounds__(JOIN_THREADS) tree_join_kernel(const float4* __restrict__ part_o, const float2* __restrict__ part_ml,
-                                                                 const int4* __restrict__ meta, uint16_t* __restrict__ out, int num_heads, int lg) {
+                                                                 const int4* __restrict__ meta, uint16_t* __restrict__ out, int num_heads, int num_kv_heads,
+                                                                 int lg) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int c = blockIdx.x;
-    const int4 u = meta[c];
+    const int4 u = meta[blockIdx.x];
     if (u.x < 0) return;
+    const int c = blockIdx.x / num_kv_heads, g = blockIdx.x - c * num_kv_heads;
     const int row = threadIdx.x & (ROWS - 1), c4 = (blockIdx.y * 2 + (threadIdx.x >> 7)) * 4;
     if ((row >> lg) >= u.z) return;
     // the unit's first part is its run's second slot, all others are their runs' first
-    auto slot = [&](int i) { return static_cast<int64_t>(i) * 2 + (i == c ? 1 : 0); };
+    auto slot = [&](int i) { return (static_cast<int64_t>(i) * num_kv_heads + g) * 2 + (i == c ? 1 : 0); };
     float M = -INFINITY;
 #pragma unroll 4
     for (int i = c; i <= u.x; ++i) M = fmaxf(M, part_ml[slot(i) * ROWS + row].x);
@@ -791,7 +913,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) tree_join_kernel(const float4* _
         }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint4* to = reinterpret_cast<uint4*>(out + (static_cast<int64_t>(u.y + (row >> lg)) * num_heads + (u.w << lg) + (row & ((1 << lg) - 1))) * D + 4 * c4);
+    uint4* to = reinterpret_cast<uint4*>(out + (static_cast<int64_t>(u.y + (row >> lg)) * num_heads + (g << lg) + (row & ((1 << lg) - 1))) * D + 4 * c4);
 #pragma unroll
     for (int k = 0; k < 2; ++k)
         to[k] = make_uint4(pack_bf16x2(o[8 * k] * inv, o[8 * k + 1] * inv), pack_bf16x2(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
@@ -802,17 +924,19 @@ constexpr size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(25
 
 // As many CTAs as the bounds allow runs: never fewer than the lengths themselves ask for, so that how a batch is cut, and
 // with it every rounding, does not depend on how tight the bounds are.
+int64_t max_ctas(int num_kv_heads) {
+    return std::max(1, CTAS_PER_SM * sm_count() / num_kv_heads) * static_cast<int64_t>(num_kv_heads);
+}
 int64_t grid_of(int batch, int max_nodes, int max_context, int num_kv_heads, int lg) {
     const int qtok = ROWS >> lg;
-    const int64_t cost = static_cast<int64_t>(batch) * ((static_cast<int64_t>(max_context) + KT - 1) / KT + UNIT_COST) *
-                         ((max_nodes + qtok - 1) / qtok) * num_kv_heads;
-    return std::max<int64_t>(1, std::min<int64_t>(CTAS_PER_SM * sm_count(), cost / MIN_RUN));
+    const int64_t cost = static_cast<int64_t>(batch) * ((static_cast<int64_t>(max_context) + KT - 1) / KT + UNIT_COST) * ((max_nodes + qtok - 1) / qtok);
+    return std::min<int64_t>(max_ctas(num_kv_heads), std::max<int64_t>(1, cost / MIN_RUN) * num_kv_heads);
 }
 
 }  // namespace
 
-size_t tree_decode_workspace_bytes() {
-    const size_t ctas = static_cast<size_t>(CTAS_PER_SM) * sm_count();
+size_t tree_decode_workspace_bytes(int num_kv_heads) {
+    const size_t ctas = static_cast<size_t>(max_ctas(num_kv_heads));
     return align256(ctas * 2 * ROWS * D * 4) + align256(ctas * 2 * ROWS * 8) + align256(ctas * 16);
 }
 
@@ -820,10 +944,10 @@ pkv_status launch_tree_decode(const TreeDecodeArgs& a, int* err, cudaStream_t st
     const bool fp8 = a.k_scale != nullptr;
     const int lg = group_log2(a.num_heads, a.num_kv_heads);
     if (lg < 0) return PKV_ERR_UNSUPPORTED;
-    if (a.workspace == nullptr || a.workspace_bytes < tree_decode_workspace_bytes()) return PKV_ERR_WORKSPACE;
+    if (a.workspace == nullptr || a.workspace_bytes < tree_decode_workspace_bytes(a.num_kv_heads)) return PKV_ERR_WORKSPACE;
     if (!setup_once(kSetupTreeDecode, [] {
-            return cudaFuncSetAttribute(tree_decode_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) == cudaSuccess &&
-                   cudaFuncSetAttribute(tree_decode_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) == cudaSuccess;
+            return cudaFuncSetAttribute(tree_decode_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<false>::BYTES) == cudaSuccess &&
+                   cudaFuncSetAttribute(tree_decode_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<true>::BYTES) == cudaSuccess;
         }))
         return PKV_ERR_CUDA;
     CUtensorMap tm_q, tm_k, tm_v;
@@ -841,13 +965,19 @@ pkv_status launch_tree_decode(const TreeDecodeArgs& a, int* err, cudaStream_t st
                                   static_cast<uint64_t>(a.num_blocks)};
         const uint64_t strides[3] = {row, a.num_kv_heads * row, static_cast<uint64_t>(a.block_size) * a.num_kv_heads * row};
         const uint32_t box[4] = {fp8 ? 128u : 64u, 1u, static_cast<uint32_t>(KT), 1u};
+        // a head's row of codes is 128 bytes: wider fetches would bring the next head's too
+        const CUtensorMapL2promotion promotion = fp8 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
         const CUtensorMapDataType type = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-        const CUtensorMapSwizzle swizzle = fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
-        if (encode_tiled(&tm_k, type, 4, const_cast<void*>(a.k_cache), dims, strides, box, swizzle) != CUDA_SUCCESS ||
-            encode_tiled(&tm_v, type, 4, const_cast<void*>(a.v_cache), dims, strides, box, swizzle) != CUDA_SUCCESS)
+        if (encode_tiled(&tm_k, type, 4, const_cast<void*>(a.k_cache), dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B, promotion) != CUDA_SUCCESS ||
+            encode_tiled(&tm_v, type, 4, const_cast<void*>(a.v_cache), dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B, promotion) != CUDA_SUCCESS)
             return PKV_ERR_INVALID_ARG;
     }
-    const size_t ctas = static_cast<size_t>(CTAS_PER_SM) * sm_count();
+    static const int launch_regs = [] {
+        cudaFuncAttributes fa;
+        return cudaFuncGetAttributes(&fa, tree_decode_kernel<true>) == cudaSuccess ? fa.numRegs : -1;
+    }();
+    if (fp8 && launch_regs < static_cast<int>(kMinLaunchRegs)) return PKV_ERR_UNSUPPORTED;
+    const size_t ctas = static_cast<size_t>(max_ctas(a.num_kv_heads));
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     Params p{};
     p.part_o = reinterpret_cast<float4*>(ws);
@@ -877,9 +1007,9 @@ pkv_status launch_tree_decode(const TreeDecodeArgs& a, int* err, cudaStream_t st
     p.err = err;
     const int grid = static_cast<int>(grid_of(a.batch, a.max_nodes, a.max_context, a.num_kv_heads, lg));
     if (fp8)
-        tree_decode_kernel<true><<<grid, THREADS_FP8, SMEM_BYTES, stream>>>(tm_q, tm_k, tm_v, p);
+        tree_decode_kernel<true><<<grid, THREADS_FP8, Layout<true>::BYTES, stream>>>(tm_q, tm_k, tm_v, p);
     else
-        tree_decode_kernel<false><<<grid, THREADS_BF16, SMEM_BYTES, stream>>>(tm_q, tm_k, tm_v, p);
+        tree_decode_kernel<false><<<grid, THREADS_BF16, Layout<false>::BYTES, stream>>>(tm_q, tm_k, tm_v, p);
     if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid, JOIN_SPLIT);
@@ -891,7 +1021,7 @@ pkv_status launch_tree_decode(const TreeDecodeArgs& a, int* err, cudaStream_t st
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_join_kernel, static_cast<const float4*>(p.part_o), static_cast<const float2*>(p.part_ml),
-                                             static_cast<const int4*>(p.meta), a.out, a.num_heads, lg);
+                                             static_cast<const int4*>(p.meta), a.out, a.num_heads, a.num_kv_heads, lg);
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 

@@ -2,8 +2,8 @@
 
 Tolerances.  With A = sum_j p_j |v_j| per output element: a key's weight is rounded to bf16
 (2^-8 A), scores and sums are fp32 (a score error of 2^-13 would be 1000 roundings of a score near 1;
-2^-13 A), the output is rounded once to bf16 (2^-8 |ref|).  The 8-bit attention equals the bf16 one
-over the values read, bit for bit.  Paths, moved rows and copied blocks are exact."""
+2^-13 A), the output is rounded once to bf16 (2^-8 |ref|).  The 8-bit attention multiplies the codes
+themselves by two e4m3 parts of each query, off by 2^-18 of the row's largest at most.  Paths, moved rows and copied blocks are exact."""
 import numpy as np
 import pytest
 import torch
@@ -126,8 +126,6 @@ def test_attention(pkv, name, hq, hkv, fp8):
     out = b.gpu(pkv)
     expect_no_device_error(pkv)
     b.check(out)
-    if fp8:
-        assert torch.equal(out, b.gpu(pkv, as_bf16=True))
 
 
 @pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "8 bits"])
@@ -240,6 +238,21 @@ def test_large_scores_and_values(pkv):
     b = Trees([25], [333], 8, 2, seed=12)
     b.q *= 30
     b.v *= 2.0 ** 100
+    b.check(b.gpu(pkv))
+
+
+@pytest.mark.parametrize("power", [-100, 0, 3, 12])
+def test_large_and_small_queries_8_bits(pkv, power):
+    """Scores of any size up to some hundreds: a query's two parts and the codes' products lose nothing that counts
+    (2^-18 of the row's largest |q| in each of 128 products with |k| < 4 is below 2^-9 q_max / sqrt(128), on a
+    score that such a row's own keys put near q_max sqrt(128))."""
+    b = Trees([25, 64], [333, 2000], 8, 2, seed=12, fp8=True)
+    b.q *= 2.0 ** power / 12
+    b.ks[:] = np.where(b.ks == 255, 255, b.ks - 4)
+    b.k = torch.from_numpy(fc.read_pool(b.kc, b.ks)).bfloat16()
+    if power == -100:
+        b.ks[:] = np.where(b.ks == 255, 255, b.ks + 100)
+        b.k = torch.from_numpy(fc.read_pool(b.kc, b.ks)).bfloat16()
     b.check(b.gpu(pkv))
 
 
