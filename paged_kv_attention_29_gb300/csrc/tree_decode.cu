@@ -60,19 +60,23 @@ constexpr int THREADS_BF16 = 192, THREADS_FP8 = 384;
 constexpr uint32_t kSoftmaxRegs = 136, kDecodeRegs = 56, kControlRegs = 48, kMinLaunchRegs = 80;
 static_assert(kSoftmaxRegs + kDecodeRegs + kControlRegs <= 3 * kMinLaunchRegs, "setmaxnreg draws on the launch's registers");
 
-// Shared memory.  bf16: rings of 2 K and 3 V tiles.  8 bits: 3 tiles of K codes and 3 V tiles, the row scales beside
-// them (K's are read as late as the softmax of their tile, when K tiles up to four behind may be in flight).
+// Shared memory.  bf16: rings of 3 K and 2 V tiles (a K tile is asked for two steps before its product, a V tile's
+// product comes a step later).  8 bits: 3 tiles of K codes and 3 V tiles; the row scales of K as bytes and as floats, in
+// rings so long that those of a tile are read before K's copies come round again; each query row's factor, of two
+// segments.
 template <bool FP8>
 struct Layout {
-    static constexpr int K_SLOTS = FP8 ? 3 : 2, V_SLOTS = 3, K_TILE = FP8 ? KT * D : KV_TILE, KS_SLOTS = FP8 ? 8 : 0;
+    static constexpr int K_SLOTS = 3, V_SLOTS = FP8 ? 3 : 2, K_TILE = FP8 ? KT * D : KV_TILE, KS_SLOTS = 8;
     static constexpr int Q = 0, K = 2 * Q_HALF, V = K + K_SLOTS * K_TILE, VS = V + V_SLOTS * KV_TILE, KS = VS + (FP8 ? V_SLOTS * KT : 0);
-    static constexpr int KSF = KS + KS_SLOTS * KT;                // K scales as floats, a copy for each softmax warp
-    static constexpr int BAR = KSF + (FP8 ? 4 * KT * 4 : 0);
-    static constexpr int KF = 0, KE = KF + K_SLOTS, VF = KE + K_SLOTS, VE = VF + V_SLOTS, VRAW = VE + V_SLOTS, KSB = VRAW + V_SLOTS, QF = KSB + KS_SLOTS,
-                         QR = QF + 1, QE = QR + 1, SF = QE + 1, PF = SF + 2, PV = PF + 2, OF = PV + 1, OE = OF + 1, WG = OE + 1, DRAIN = WG + 1,
-                         NUM_BARS = DRAIN + 1;
-    static constexpr int MISC = (BAR + NUM_BARS * 8 + 15) & ~15;  // [0] TMEM base, [1] abort, [2..9] nodes with infinities or NaN in V
-    static constexpr int SCAN = MISC + 48;                        // 16 x int64: set-up sums; then the run's start
+    static constexpr int KSF = KS + (FP8 ? KS_SLOTS * KT : 0), QS = KSF + (FP8 ? KS_SLOTS * KT * 4 : 0);
+    static constexpr int BAR = QS + (FP8 ? 2 * ROWS * 4 : 0);
+    static constexpr int KF = 0, KE = KF + K_SLOTS, VF = KE + K_SLOTS, VE = VF + V_SLOTS, QF = VE + V_SLOTS, QE = QF + 1, SF = QE + 1, PF = SF + 2,
+                         PV = PF + 2, OF = PV + 1, OE = OF + 1, WG = OE + 1, DRAIN = WG + 1, BF16_BARS = DRAIN + 1;
+    static constexpr int VRAW = BF16_BARS, KSB = VRAW + V_SLOTS, KSR = KSB + KS_SLOTS, QR = KSR + KS_SLOTS, QG = QR + 1, FP8_BARS = QG + 1;
+    static constexpr int NUM_BARS = FP8 ? FP8_BARS : BF16_BARS;
+    static constexpr int MISC = (BAR + NUM_BARS * 8 + 15) & ~15;  // [0] TMEM base, [1] abort
+    static constexpr int WILD = MISC + 16;                        // [2][4 warps][8]: nodes with infinities or NaN in V
+    static constexpr int SCAN = WILD + 2 * 4 * 8 * 4;             // 16 x int64: set-up sums; then the run's start
     static constexpr int BYTES = SCAN + 16 * 8;
     static_assert(K % 1024 == 0 && V % 1024 == 0 && KSF % 16 == 0 && BAR % 8 == 0, "operand tiles and vectors need their alignment");
     static_assert(CTAS_PER_SM * (BYTES + 1024) <= 228 * 1024, "two CTAs share an SM's shared memory");
@@ -105,6 +109,7 @@ struct Ctl {
 // Waits for a phase, asleep between tries; gives up when another warp has, or after the limit.
 __device__ __forceinline__ bool wait_phase(const Ctl& c, uint32_t bar, uint32_t parity) {
     if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait_sleep(bar, parity, 100000u)) return true;     // the clock is read by waits that last, and only by them
     const unsigned long long t0 = global_ns();
     while (true) {
         if (mbar_try_wait_sleep(bar, parity, 500000u)) return true;
@@ -274,43 +279,44 @@ __device__ __forceinline__ void bf16_of_row(const uint4& c, uint32_t byte, uint4
 // A query row for the product with codes.  With f the power of two that takes the row's largest |q| to [128, 256), q f
 // is a sum of two e4m3 numbers, the nearest one and what is left: exactly where |q| is 2^-10 of the largest or more (8
 // bits are 4 + 4), and to 2^-18 of the largest otherwise.  The row is replaced by its two parts, each laid out as 128
-// bytes of a K-major tile; returns 1 / f, or NaN for a row with an infinity or a NaN.
-__device__ __forceinline__ float split_row(uint8_t* q, int row) {
-    uint32_t x[64];
+// bytes of a K-major tile; *factor gets 1 / f, or NaN for a row with an infinity or a NaN.  Eight lanes take a row, lane v
+// dims 16 v .. 16 v + 15; all of a warp's lanes call.
+__device__ __forceinline__ void split_row(uint8_t* q, int row, int v, float* factor) {
+    uint32_t x[8];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const uint4 v = *reinterpret_cast<const uint4*>(q + (i >> 3) * Q_HALF + row * 128 + (((i & 7) ^ (row & 7)) * 16));
-        x[4 * i] = v.x;
-        x[4 * i + 1] = v.y;
-        x[4 * i + 2] = v.z;
-        x[4 * i + 3] = v.w;
+    for (int i = 0; i < 2; ++i) {
+        const uint4 c = *reinterpret_cast<const uint4*>(q + (v >> 2) * Q_HALF + row * 128 + ((((2 * v + i) & 7) ^ (row & 7)) * 16));
+        x[4 * i] = c.x;
+        x[4 * i + 1] = c.y;
+        x[4 * i + 2] = c.z;
+        x[4 * i + 3] = c.w;
     }
     uint32_t most = 0u;
 #pragma unroll
-    for (int i = 0; i < 64; ++i) {
+    for (int i = 0; i < 8; ++i) {
         const uint32_t a = x[i] & 0x7fff7fffu;
         asm("max.u16x2 %0, %0, %1;" : "+r"(most) : "r"(a));
     }
-    const uint32_t e = max(8u, max(most & 0xffffu, most >> 16) >> 7);            // exponent field of the largest
+    most = max(most & 0xffffu, most >> 16);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));      // the row is read, too
+    const uint32_t e = max(8u, most >> 7);                                       // exponent field of the largest
     const float f = __uint_as_float((261u - e) << 23);                           // 2^(134 - e)
+    uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint32_t a = x[8 * i + 2 * k], b = x[8 * i + 2 * k + 1];
-            const float y0 = bf16_lo(a) * f, y1 = bf16_hi(a) * f, y2 = bf16_lo(b) * f, y3 = bf16_hi(b) * f;
-            hi[k] = e4m3x4(y0, y1, y2, y3);
-            uint32_t h0, h1;
-            f16_of_codes(hi[k], h0, h1);
-            const float2 z0 = __half22float2(*reinterpret_cast<const __half2*>(&h0)), z1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
-            lo[k] = e4m3x4(y0 - z0.x, y1 - z0.y, y2 - z1.x, y3 - z1.y);
-        }
-        uint8_t* at = q + row * 128 + ((i ^ (row & 7)) * 16);
-        *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(at + Q_HALF) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t a = x[2 * k], b = x[2 * k + 1];
+        const float y0 = bf16_lo(a) * f, y1 = bf16_hi(a) * f, y2 = bf16_lo(b) * f, y3 = bf16_hi(b) * f;
+        hi[k] = e4m3x4(y0, y1, y2, y3);
+        uint32_t h0, h1;
+        f16_of_codes(hi[k], h0, h1);
+        const float2 z0 = __half22float2(*reinterpret_cast<const __half2*>(&h0)), z1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+        lo[k] = e4m3x4(y0 - z0.x, y1 - z0.y, y2 - z1.x, y3 - z1.y);
     }
-    return e == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float((e - 7u) << 23);
+    uint8_t* at = q + row * 128 + ((v ^ (row & 7)) * 16);
+    *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(at + Q_HALF) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    if (v == 0) *factor = e == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float((e - 7u) << 23);
 }
 
 template <bool FP8>
@@ -331,8 +337,8 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid == 0) {
         for (int i = 0; i < L::NUM_BARS; ++i) {
-            const bool per_warp = i == L::PF || i == L::PF + 1 || i == L::OE || i == L::WG || i == L::QR || (FP8 && i >= L::VF && i < L::VE);
-            mbar_init(bar(i), per_warp ? 4 : 1);
+            const bool per_warp = i == L::PF || i == L::PF + 1 || i == L::OE || i == L::WG || (FP8 && ((i >= L::VF && i < L::VE) || i == L::QR));
+            mbar_init(bar(i), per_warp ? 4 : FP8 && i >= L::KSR && i < L::QR ? 2 : 1);
         }
         misc[1] = 0u;
         fence_barrier_init();
@@ -420,7 +426,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 tma_load_4d(dst, &tm_k, full, 0, g, off, phys);
                 if (FP8) {
                     const int64_t at = (static_cast<int64_t>(max(phys, 0)) * p.num_kv_heads + g) * p.block_size + off;
-                    const int s = kt % max(1, L::KS_SLOTS);
+                    const int s = kt % L::KS_SLOTS;
                     mbar_arrive_expect_tx(bar(L::KSB + s), KT);
                     bulk_load(base + L::KS + s * KT, p.k_scale + at, KT, bar(L::KSB + s));
                 } else {
@@ -477,7 +483,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 for (int i = max(0, vt - L::V_SLOTS); i < vt; ++i) wait_drain(bar((FP8 ? L::VRAW : L::VF) + i % L::V_SLOTS), (i / L::V_SLOTS) & 1);
                 if (FP8)
                     for (int i = max(0, kt - L::KS_SLOTS); i < kt; ++i)
-                        wait_drain(bar(L::KSB + i % max(1, L::KS_SLOTS)), (i / max(1, L::KS_SLOTS)) & 1);
+                        wait_drain(bar(L::KSB + i % L::KS_SLOTS), (i / L::KS_SLOTS) & 1);
             }
         }
         __syncwarp();
@@ -491,44 +497,55 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // or with the row, neither the loads nor the stores meet in a bank.
         regs_dec<kDecodeRegs>();
         const int half = (lane >> 3) & 1, vec = half * 4 + (lane & 3);
-        int tiles = 0;                                        // in this run
-        for (; w.more(); w.next()) tiles += w.j1 - w.j0;
+        // a tile's K scales to floats, by the first two warps
+        auto expand = [&](int t) {
+            if (warp >= 6) return true;
+            const int s = t % L::KS_SLOTS;
+            if (!wait_warp(ctl, bar(L::KSB + s), (t / L::KS_SLOTS) & 1)) return false;
+            const int key = tid - 4 * 32;
+            reinterpret_cast<float*>(gbase + L::KSF)[s * KT + key] = e8m0_value(gbase[L::KS + s * KT + key]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(L::KSR + s));
+            return true;
+        };
+        int t = 0, seg = 0;
+        bool ok = busy && expand(0);
+        for (; w.more() && ok; w.next(), ++seg) {
+          // the segment's queries, as soon as they are there; then its V tiles, each behind the K scales of the next
+          if (!(ok = wait_warp(ctl, bar(L::QF), seg & 1))) break;
+          const int rows = w.tokens() << p.lg;
 #pragma unroll 1
-        for (int t = 0; t < tiles; ++t) {
+          for (int r0 = (warp - 4) * 4; r0 < rows; r0 += 16)
+              split_row(gbase + L::Q, r0 + (lane >> 3), lane & 7, reinterpret_cast<float*>(gbase + L::QS) + (seg & 1) * ROWS + r0 + (lane >> 3));
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::QR));
+#pragma unroll 1
+          for (int j = w.j0; j < w.j1; ++j, ++t) {
+            if (!(j + 1 == w.j1 && w.last()) && !(ok = expand(t + 1))) break;
             const int slot = t % L::V_SLOTS;
-            if (!wait_warp(ctl, bar(L::VRAW + slot), (t / L::V_SLOTS) & 1)) break;
+            if (!(ok = wait_warp(ctl, bar(L::VRAW + slot), (t / L::V_SLOTS) & 1))) break;
             uint8_t* tile = gbase + L::V + slot * KV_TILE;
             const uint8_t* scales = gbase + L::VS + slot * KT;
-            uint4 c[4];
-            uint32_t byte[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = (warp - 4) * 16 + ((2 * (lane >> 4) + 4 * i) ^ (lane & 4 ? 5 : 0));
-                c[i] = *reinterpret_cast<const uint4*>(tile + KV_HALF + row * 128 + ((vec ^ (row & 7)) * 16));
-                byte[i] = scales[row];
+            // rolled, four rows at a time: this code and the softmax's share the schedulers' instruction caches
+#pragma unroll 1
+            for (int i = 0; i < 16; i += 4) {
+                const int row = (warp - 4) * 16 + ((2 * (lane >> 4) + i) ^ (lane & 4 ? 5 : 0)), ch = (lane & 3) * 2;
+                const uint4 c = *reinterpret_cast<const uint4*>(tile + KV_HALF + row * 128 + ((vec ^ (row & 7)) * 16));
+                const uint32_t byte = scales[row];
+                uint4 lo, hi;
+                if (__any_sync(0xffffffffu, odd_row(c, byte)))       // and every lane has read its part of these rows
+                    bf16_of_row<true>(c, byte, lo, hi);
+                else
+                    bf16_of_row<false>(c, byte, lo, hi);
+                uint8_t* dst = tile + half * KV_HALF + row * 128;
+                *reinterpret_cast<uint4*>(dst + ((ch ^ (row & 7)) * 16)) = lo;
+                *reinterpret_cast<uint4*>(dst + (((ch + 1) ^ (row & 7)) * 16)) = hi;
             }
-            __syncwarp();
-            bool odd = false;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) odd |= odd_row(c[i], byte[i]);
-            auto put = [&](auto rare) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = (warp - 4) * 16 + ((2 * (lane >> 4) + 4 * i) ^ (lane & 4 ? 5 : 0)), ch = (lane & 3) * 2;
-                    uint4 lo, hi;
-                    bf16_of_row<decltype(rare)::value>(c[i], byte[i], lo, hi);
-                    uint8_t* dst = tile + half * KV_HALF + row * 128;
-                    *reinterpret_cast<uint4*>(dst + ((ch ^ (row & 7)) * 16)) = lo;
-                    *reinterpret_cast<uint4*>(dst + (((ch + 1) ^ (row & 7)) * 16)) = hi;
-                }
-            };
-            if (__any_sync(0xffffffffu, odd))
-                put(std::true_type{});
-            else
-                put(std::false_type{});
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(L::VF + slot));
+          }
         }
         tc_fence_before();
         __syncthreads();
@@ -545,6 +562,8 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         auto issue_s = [&](int t, bool seg_first, bool seg_last) {
             if (seg_first) {
                 if (!(ok = wait_warp(ctl, bar(FP8 ? L::QR : L::QF), segs & 1))) return;
+                if (FP8 && lane == 0) mbar_arrive(bar(L::QG));        // the rows' factors, to the softmax
+                __syncwarp();
                 ++segs;
             }
             const int slot = t % L::K_SLOTS;
@@ -619,6 +638,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         int t = 0, seg = 0;
         bool ok = true;
         int4 meta = make_int4(-1, 0, 0, 0);
+        uint32_t* wild = reinterpret_cast<uint32_t*>(gbase + L::WILD);
         uint32_t meets = 0;
         auto meet = [&] {                                     // a barrier of the four warps that gives up with the others
             __syncwarp();
@@ -640,60 +660,17 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             float m_used = -INFINITY, l = 0.f, sc = p.scale_log2;
             bool had_tree = false;
             if (FP8) {
-                ok = wait_warp(ctl, bar(L::QF), seg & 1);
+                ok = wait_warp(ctl, bar(L::QG), seg & 1);
                 if (!ok) break;
-                if (warp_live) sc *= split_row(gbase + L::Q, row);
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(L::QR));
+                sc *= reinterpret_cast<const float*>(gbase + L::QS)[(seg & 1) * ROWS + row];
             }
             for (int j = w.j0; j < w.j1; ++j, ++t) {
                 const int keys = min(KT, w.s.len - j * KT), rel = j * KT - tree0;
                 const bool tree = rel + KT > 0;               // nodes among the keys: on no more than the last few tiles
-                if (tree) {
-                    // Infinities and NaN among the nodes' V rows leave the tile, and so does what the block holds
-                    // behind the last key: weights of 0 would spread them.
-                    const int slot = t % L::V_SLOTS;
-                    ok = wait_warp(ctl, bar(L::VF + slot), (t / L::V_SLOTS) & 1);
-                    if (!ok) break;
-                    if (!had_tree) {
-                        if (!meet()) break;                   // the last segment's bits are read
-                        if (tid < 8) misc[2 + tid] = 0u;
-                        if (!meet()) break;
-                        had_tree = true;
-                    }
-                    uint8_t* vt = gbase + L::V + slot * KV_TILE;
-                    const int lo = max(0, -rel), hi = (keys + 15) & ~15;
-                    for (int i = lo * 16 + tid; i < hi * 16; i += 128) {
-                        const int r = i >> 4;
-                        uint4* at = reinterpret_cast<uint4*>(vt + ((i >> 3) & 1) * KV_HALF + r * 128 + (i & 7) * 16);
-                        if (r >= keys) {
-                            *at = make_uint4(0, 0, 0, 0);
-                        } else {
-                            const uint4 x = *at;
-                            if (wild2(x.x) || wild2(x.y) || wild2(x.z) || wild2(x.w)) {
-                                uint32_t y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    if ((y[e] & 0x7f80u) == 0x7f80u) y[e] &= 0xffff0000u;
-                                    if ((y[e] & 0x7f800000u) == 0x7f800000u) y[e] &= 0x0000ffffu;
-                                }
-                                *at = make_uint4(y[0], y[1], y[2], y[3]);
-                                atomicOr(misc + 2 + ((rel + r) >> 5), 1u << ((rel + r) & 31));
-                            }
-                        }
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                }
-                float* ksf = reinterpret_cast<float*>(gbase + L::KSF) + warp * KT;
+                const float* ksf = reinterpret_cast<const float*>(gbase + L::KSF) + (t % L::KS_SLOTS) * KT;
                 if (FP8 && warp_live) {
-                    const int s = t % max(1, L::KS_SLOTS);
-                    ok = wait_warp(ctl, bar(L::KSB + s), (t / max(1, L::KS_SLOTS)) & 1);
+                    ok = wait_warp(ctl, bar(L::KSR + t % L::KS_SLOTS), (t / L::KS_SLOTS) & 1);
                     if (!ok) break;
-                    const uint8_t* ks = gbase + L::KS + s * KT;
-                    ksf[lane] = e8m0_value(ks[lane]);
-                    ksf[lane + 32] = e8m0_value(ks[lane + 32]);
-                    __syncwarp();
                 }
                 ok = wait_warp(ctl, bar(L::SF + (t & 1)), (t >> 1) & 1);
                 if (!ok) break;
@@ -701,46 +678,45 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (warp_live) {
                     const uint32_t s_tmem = tmem + lane_off + (t & 1) * KT;
                     const unsigned long long see = tree ? visible(words, rel, keys) : ~0ull;
-                    // 32 columns of S; the 8-bit kernel, whose threads have fewer registers, reads them again for P
-                    float s[FP8 ? 1 : 2][32];
-                    auto read = [&](int cc, float (&x)[32]) {
-                        uint32_t r[32];
-                        tmem_ld32(s_tmem + 32 * cc, r);
-                        tmem_ld_wait();
+                    float mx0 = -INFINITY, mx1 = -INFINITY;
+                    // bf16: all of S in registers.  8 bits: S is read twice, CH columns at a time, in rolled loops.
+                    constexpr int CH = FP8 ? 16 : KT;
+                    float s[CH];
+                    auto read = [&](int c0) {
+                        if constexpr (FP8) {
+                            uint32_t r[16];
+                            tmem_ld16(s_tmem + c0, r);
+                            tmem_ld_wait();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(r[e]);
-                        if (FP8) {
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
-                                const float4 f = *reinterpret_cast<const float4*>(ksf + 32 * cc + e);
-                                fmul2(x[e], x[e + 1], x[e], x[e + 1], f.x, f.y);
-                                fmul2(x[e + 2], x[e + 3], x[e + 2], x[e + 3], f.z, f.w);
+                            for (int e = 0; e < 16; e += 4) {
+                                const float4 f = *reinterpret_cast<const float4*>(ksf + c0 + e);
+                                fmul2(s[e], s[e + 1], __uint_as_float(r[e]), __uint_as_float(r[e + 1]), f.x, f.y);
+                                fmul2(s[e + 2], s[e + 3], __uint_as_float(r[e + 2]), __uint_as_float(r[e + 3]), f.z, f.w);
                             }
+                        } else {
+                            uint32_t r[2][32];
+                            tmem_ld32(s_tmem, r[0]);
+                            tmem_ld32(s_tmem + 32, r[1]);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < KT; ++e) s[e] = __uint_as_float(r[e >> 5][e & 31]);
+                        }
+                        if (tree) {
+                            const unsigned long long m = see >> c0;
+                            const uint32_t lo = static_cast<uint32_t>(m), hi = static_cast<uint32_t>(m >> 32);
+#pragma unroll
+                            for (int e = 0; e < CH; ++e) s[e] = ((e < 32 ? lo : hi) >> (e & 31)) & 1u ? s[e] : -INFINITY;
                         }
                     };
-                    float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < KT; c0 += CH) {
+                        read(c0);
 #pragma unroll
-                    for (int cc = 0; cc < 2; ++cc) {
-                        float (&x)[32] = s[FP8 ? 0 : cc];
-                        read(cc, x);
-                        if (tree) {
-                            const uint32_t bits = static_cast<uint32_t>(see >> (32 * cc));
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) x[e] = (bits >> e) & 1u ? x[e] : -INFINITY;
-                        }
-                        if (FP8) {
-                            uint32_t r[32];
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(x[e]);
-                            tmem_st32(s_tmem + 32 * cc, r);
-                        }
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            mx0 = fmax3(mx0, x[e + 0], x[e + 1]);
-                            mx1 = fmax3(mx1, x[e + 2], x[e + 3]);
+                        for (int e = 0; e < CH; e += 4) {
+                            mx0 = fmax3(mx0, s[e + 0], s[e + 1]);
+                            mx1 = fmax3(mx1, s[e + 2], s[e + 3]);
                         }
                     }
-                    if (FP8) tmem_st_wait();
                     const float m_new = fmaxf(mx0, mx1) * sc;
                     if (j == w.j0) {
                         m_used = m_new;
@@ -766,32 +742,62 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     }
                     const float neg_m = m_used == -INFINITY ? 0.f : -m_used;      // a row that has seen nothing yet
                     float r0 = 0.f, r1 = 0.f, r2 = 0.f, r3 = 0.f;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < KT; c0 += CH) {
+                        if (FP8) read(c0);
+                        uint32_t pk[CH / 2];
 #pragma unroll
-                    for (int cc = 0; cc < 2; ++cc) {
-                        uint32_t pk[16];
-                        float (&x)[32] = s[FP8 ? 0 : cc];
-                        if (FP8) {                            // scaled and masked above
-                            uint32_t r[32];
-                            tmem_ld32(s_tmem + 32 * cc, r);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(r[e]);
-                        }
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
+                        for (int e = 0; e < CH; e += 4) {
                             float a0, a1, a2, a3;
-                            ffma2(a0, a1, x[e], x[e + 1], sc, sc, neg_m, neg_m);
-                            ffma2(a2, a3, x[e + 2], x[e + 3], sc, sc, neg_m, neg_m);
+                            ffma2(a0, a1, s[e], s[e + 1], sc, sc, neg_m, neg_m);
+                            ffma2(a2, a3, s[e + 2], s[e + 3], sc, sc, neg_m, neg_m);
                             const float p0 = ex2_ftz(a0), p1 = ex2_ftz(a1), p2 = ex2_ftz(a2), p3 = ex2_ftz(a3);
                             fadd2(r0, r1, r0, r1, p0, p1);
                             fadd2(r2, r3, r2, r3, p2, p3);
                             pk[e >> 1] = pack_bf16x2(p0, p1);
                             pk[(e >> 1) + 1] = pack_bf16x2(p2, p3);
                         }
-                        tmem_st16(s_tmem + 16 * cc, pk);
+                        // P's columns end before the ones of S that are still to be read
+                        if constexpr (FP8)
+                            tmem_st8(s_tmem + c0 / 2, pk);
+                        else
+                            tmem_st32(s_tmem, pk);
                     }
                     l += (r0 + r1) + (r2 + r3);
                     tmem_st_wait();
+                }
+                if (tree) {
+                    // Infinities and NaN among the nodes' V rows leave the tile, and so does what the block holds
+                    // behind the last key: weights of 0 would spread them.
+                    const int slot = t % L::V_SLOTS;
+                    ok = wait_warp(ctl, bar(L::VF + slot), (t / L::V_SLOTS) & 1);
+                    if (!ok) break;
+                    uint32_t* mine = wild + ((seg & 1) * 4 + warp) * 8;
+                    if (!had_tree && lane < 8) mine[lane] = 0u;
+                    __syncwarp();
+                    had_tree = true;
+                    uint8_t* vt = gbase + L::V + slot * KV_TILE;
+                    const int lo = max(0, -rel), hi = (keys + 15) & ~15;
+                    for (int i = lo * 16 + tid; i < hi * 16; i += 128) {
+                        const int r = i >> 4;
+                        uint4* at = reinterpret_cast<uint4*>(vt + ((i >> 3) & 1) * KV_HALF + r * 128 + (i & 7) * 16);
+                        if (r >= keys) {
+                            *at = make_uint4(0, 0, 0, 0);
+                        } else {
+                            const uint4 x = *at;
+                            if (wild2(x.x) || wild2(x.y) || wild2(x.z) || wild2(x.w)) {
+                                uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    if ((y[e] & 0x7f80u) == 0x7f80u) y[e] &= 0xffff0000u;
+                                    if ((y[e] & 0x7f800000u) == 0x7f800000u) y[e] &= 0x0000ffffu;
+                                }
+                                *at = make_uint4(y[0], y[1], y[2], y[3]);
+                                atomicOr(mine + ((rel + r) >> 5), 1u << ((rel + r) & 31));
+                            }
+                        }
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -801,7 +807,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             ok = wait_warp(ctl, bar(L::OF), seg & 1);
             if (!ok) break;
             tc_fence_after();
-            if (had_tree && !meet()) break;                   // every warp's bits are there
+            if (had_tree && !meet()) break;                   // every warp's bits are there; those of the segment before are read
             const bool whole = w.j0 == 0 && w.j1 == w.nt;
             const int part = w.j0 > 0 ? 0 : 1;                // 0: the unit began before this run, 1: it goes on behind it
             if (!whole && part == 1) {
@@ -810,9 +816,14 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 meta = make_int4(static_cast<int>((end * C - 1) / W), w.s.q0 + w.rt * qtok, tokens, 0);
             }
             if (warp_live) {
+                // nodes of which something was taken out, by any of the warps
+                auto taken = [&](int i) {
+                    const uint32_t* x = wild + (seg & 1) * 32 + i;
+                    return x[0] | x[8] | x[16] | x[24];
+                };
                 uint32_t any = 0u;
                 if (had_tree)
-                    for (int i = 0; i < 8; ++i) any |= misc[2 + i];
+                    for (int i = 0; i < 32; ++i) any |= wild[(seg & 1) * 32 + i];
                 const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
                 const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + part;
                 uint16_t* orow = p.out + (static_cast<int64_t>(node_row) * p.num_heads + (g << p.lg) + (row & ((1 << p.lg) - 1))) * D;
@@ -828,7 +839,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         for (int i = 0; i < w.s.n; ++i) {
                             const unsigned long long word = i < 64 ? words[0] : i < 128 ? words[1] : i < 192 ? words[2] : words[3];
                             const int j = (tree0 + i) / KT;
-                            if (!((misc[2 + (i >> 5)] >> (i & 31)) & 1u) || !((word >> (i & 63)) & 1ull) || j < w.j0 || j >= w.j1) continue;
+                            if (!((taken(i >> 5) >> (i & 31)) & 1u) || !((word >> (i & 63)) & 1ull) || j < w.j0 || j >= w.j1) continue;
                             int off;
                             const int phys = w.block_of(j, off);
                             if (phys < 0) continue;
