@@ -31,7 +31,7 @@
 // Warps 0-3: softmax and epilogue (TMEM lanes 0-127).  bf16 cache: warp 4 TMA producer,
 // warp 5 TMEM allocation and MMA issue.  8-bit cache: warps 4-7 turn the codes that TMA
 // has put into a slot of the ring into the bf16 values they stand for, in place; warp 8
-// issues, warp 9 is the producer, warps 10-11 only complete the third warpgroup.
+// issues, warp 9 is the producer.
 #include <algorithm>
 #include <type_traits>
 
@@ -54,11 +54,7 @@ constexpr int UNIT_COST = 2;                 // what starting and ending a unit 
 constexpr int MIN_RUN = 4;                   // cost a CTA takes at least; above UNIT_COST, so that every run has a tile
 static_assert(MIN_RUN > UNIT_COST, "a run has a tile");
 constexpr int CTAS_PER_SM = 2;
-constexpr int THREADS_BF16 = 192, THREADS_FP8 = 384;
-// The 8-bit kernel's warpgroups (softmax; decoding; producer, MMA and two warps that only complete it) split the
-// registers that the launch must provide, checked on the host before every launch: 136 + 56 + 48 = 3 * 80.
-constexpr uint32_t kSoftmaxRegs = 136, kDecodeRegs = 56, kControlRegs = 48, kMinLaunchRegs = 80;
-static_assert(kSoftmaxRegs + kDecodeRegs + kControlRegs <= 3 * kMinLaunchRegs, "setmaxnreg draws on the launch's registers");
+constexpr int THREADS_BF16 = 192, THREADS_FP8 = 320;
 
 // Shared memory.  bf16: rings of 3 K and 2 V tiles (a K tile is asked for two steps before its product, a V tile's
 // product comes a step later).  8 bits: 3 tiles of K codes and 3 V tiles; the row scales of K as bytes and as floats, in
@@ -106,30 +102,34 @@ struct Ctl {
     int* err;
 };
 
-// Waits for a phase, asleep between tries; gives up when another warp has, or after the limit.
-__device__ __forceinline__ bool wait_phase(const Ctl& c, uint32_t bar, uint32_t parity) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (mbar_try_wait_sleep(bar, parity, 100000u)) return true;     // the clock is read by waits that last, and only by them
+// Waits for a phase, asleep between tries; gives up when another warp has, or after the limit.  What a wait that lasts
+// does is out of line: the roles' loops share small instruction caches.
+__device__ __noinline__ bool wait_long(volatile uint32_t* abort, int* err, uint32_t bar, uint32_t parity) {
     const unsigned long long t0 = global_ns();
     while (true) {
         if (mbar_try_wait_sleep(bar, parity, 500000u)) return true;
-        if (*c.abort) return false;
+        if (*abort) return false;
         if (global_ns() - t0 > kWaitLimitNs) {
-            *c.abort = 1u;
-            record_error(c.err, PKV_DEVERR_TIMEOUT, static_cast<int>(blockIdx.x));
+            *abort = 1u;
+            record_error(err, PKV_DEVERR_TIMEOUT, static_cast<int>(blockIdx.x));
             return false;
         }
     }
 }
+__device__ __forceinline__ bool wait_phase(const Ctl& c, uint32_t bar, uint32_t parity) {
+    return mbar_try_wait(bar, parity) || mbar_try_wait_sleep(bar, parity, 100000u) || wait_long(c.abort, c.err, bar, parity);
+}
 __device__ __forceinline__ bool wait_warp(const Ctl& c, uint32_t bar, uint32_t parity) {
     return __all_sync(0xffffffffu, wait_phase(c, bar, parity));
 }
-__device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity) {
+__device__ __noinline__ bool wait_drain(uint32_t bar, uint32_t parity) {
     const unsigned long long t0 = global_ns();
     while (!mbar_try_wait_sleep(bar, parity, 500000u))
         if (global_ns() - t0 > kWaitLimitNs) return false;
     return true;
 }
+
+__device__ __noinline__ void complain(int* err, int code, int info) { record_error(err, code, info); }
 
 struct Seq {
     int q0, n, len;       // first node's row, nodes (0: nothing to do), keys
@@ -197,13 +197,11 @@ struct Walk {
         clip(UNIT_COST);
     }
     __device__ __forceinline__ int tokens() const { return min(ROWS >> p.lg, s.n - rt * (ROWS >> p.lg)); }
-    // row of the pool (block * block_size + offset) where the keys of tile j start; negative: no such block
-    __device__ __forceinline__ int block_of(int j, int& off) const {
-        const int key0 = j * KT, lb = key0 / p.block_size;
-        off = key0 - lb * p.block_size;
+    // the physical block of logical block lb; negative: no such block
+    __device__ __forceinline__ int block_of(int lb) const {
         const int phys = __ldg(p.block_tables + static_cast<int64_t>(b) * p.max_blocks + lb);
         if (phys >= 0 && phys < p.num_blocks) return phys;
-        record_error(p.err, PKV_DEVERR_BLOCK_ID, b);
+        complain(p.err, PKV_DEVERR_BLOCK_ID, b);
         return -1;
     }
 };
@@ -319,6 +317,33 @@ __device__ __forceinline__ void split_row(uint8_t* q, int row, int v, float* fac
     if (v == 0) *factor = e == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float((e - 7u) << 23);
 }
 
+// The infinities and NaN that were taken out of the V rows of a segment's nodes, added to O in the rows that see the
+// node: wild holds a bit for every node of which something was taken, four sets that the warps found.
+template <bool FP8>
+__device__ __noinline__ void give_back(const Params& p, int seq, int n, int len, int j0, int j1, int g, const uint32_t* wild, unsigned long long m0, unsigned long long m1,
+                                       unsigned long long m2, unsigned long long m3, bool live, uint32_t o_tmem) {
+    for (int i = 0; i < n; ++i) {
+        const uint32_t* x = wild + (i >> 5);
+        if (!(((x[0] | x[8] | x[16] | x[24]) >> (i & 31)) & 1u)) continue;
+        const int pos = len - n + i, lb = pos / p.block_size;
+        const int phys = __ldg(p.block_tables + static_cast<int64_t>(seq) * p.max_blocks + lb);
+        if (pos / KT < j0 || pos / KT >= j1 || phys < 0 || phys >= p.num_blocks) continue;
+        const bool sees = live && ((i < 64 ? m0 : i < 128 ? m1 : i < 192 ? m2 : m3) >> (i & 63)) & 1ull;
+        const int64_t head = static_cast<int64_t>(phys) * p.num_kv_heads + g;
+        const int64_t row = (static_cast<int64_t>(phys) * p.block_size + (pos - lb * p.block_size)) * p.num_kv_heads + g;
+        const float f = FP8 ? e8m0_value(__ldg(p.v_scale + head * p.block_size + (pos - lb * p.block_size))) : 1.f;
+        for (int d = 0; d < D; ++d) {
+            const float v = FP8 ? bf16_lo(bf16_of_codes(__ldg(p.v_codes + row * D + d), f).x)
+                                : __uint_as_float(static_cast<uint32_t>(__ldg(p.v_cache + row * D + d)) << 16);
+            if (fabsf(v) <= 3.4028235e38f) continue;
+            const float o = __uint_as_float(tmem_ld1(o_tmem + d));
+            tmem_ld_wait();
+            tmem_st1(o_tmem + d, __float_as_uint(sees ? o + v : o));
+            tmem_st_wait();
+        }
+    }
+}
+
 template <bool FP8>
 __global__ void __launch_bounds__(FP8 ? THREADS_FP8 : THREADS_BF16, CTAS_PER_SM)
 tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -336,6 +361,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid == 0) {
+#pragma unroll 1
         for (int i = 0; i < L::NUM_BARS; ++i) {
             const bool per_warp = i == L::PF || i == L::PF + 1 || i == L::OE || i == L::WG || (FP8 && ((i >= L::VF && i < L::VE) || i == L::QR));
             mbar_init(bar(i), per_warp ? 4 : FP8 && i >= L::KSR && i < L::QR ? 2 : 1);
@@ -364,6 +390,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         __syncthreads();
         long long before = 0;
         total = 0;
+#pragma unroll 1
         for (int i = 0; i < WARPS; ++i) {
             const long long x = scan[i];
             before += i < warp ? x : 0;
@@ -372,9 +399,10 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         return before + v;
     };
     long long mine = 0, first = 0;
+#pragma unroll 1
     for (int b = tid; b < p.batch; b += THREADS) {
         const Seq s = sequence(p, b);
-        if (s.bad && blockIdx.x == 0) record_error(p.err, PKV_DEVERR_SEQLENS, b);
+        if (s.bad && blockIdx.x == 0) complain(p.err, PKV_DEVERR_SEQLENS, b);
         const long long t = cost_of(p, s);
         if (b < THREADS) first = t;
         mine += t;
@@ -387,6 +415,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     const long long t0 = c < C ? c * W / C : 0, t1 = c < C ? (c + 1) * W / C : 0;
     if (t1 > t0) {
         long long before = 0;
+#pragma unroll 1
         for (int base_b = 0; base_b < p.batch; base_b += THREADS) {
             const int b = base_b + tid;
             long long v = 0, total = W;
@@ -413,7 +442,6 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     Walk w(p, busy ? static_cast<int>(scan[14]) : 0, busy ? scan[15] : 0, t1 - t0);
 
     if (warp == LOAD_WARP) {
-        if (FP8) regs_dec<kControlRegs>();
         // ---------------------------------------------------------------- TMA producer
         if (lane == 0 && busy) {
             int kt = 0, vt = 0, segs = 0;                     // K, V and Q tiles issued
@@ -459,22 +487,30 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 tma_load_3d(sQ + Q_HALF, &tm_q, bar(L::QF), 64, head, row);
                 ++segs;
             };
-            load_q();
-            int j = w.j0, k_off, k_phys = w.block_of(j, k_off);
-            load_k(k_phys, k_off);
-            while (ok) {
-                const int v_phys = k_phys, v_off = k_off;
-                const bool fresh = j + 1 == w.j1, end = fresh && w.last();
-                if (!end) {
-                    if (fresh) w.next();
-                    j = fresh ? w.j0 : j + 1;
-                    k_phys = w.block_of(j, k_off);
-                    load_k(k_phys, k_off);
-                    if (!ok) break;
+            // K of a tile, then V of the one before; a segment's queries behind the first K.  Tile j lies in logical
+            // block lb, at key off.
+            int j = w.j0, lb = j * KT / p.block_size, off = j * KT - lb * p.block_size, phys = w.block_of(lb), v_phys = 0, v_off = 0;
+            bool more = true;
+#pragma unroll 1
+            for (int t = 0; ok; ++t) {
+                if (more) load_k(phys, off);
+                if (ok && t > 0) load_v(v_phys, v_off);
+                if (!ok || !more) break;
+                if (j == w.j0) load_q();
+                v_phys = phys;
+                v_off = off;
+                off += KT;
+                if (++j == w.j1) {
+                    more = !w.last();
+                    if (more) {                               // every segment behind a run's first starts at its first key
+                        w.next();
+                        j = lb = off = 0;
+                        phys = w.block_of(0);
+                    }
+                } else if (off == p.block_size) {
+                    off = 0;
+                    phys = w.block_of(++lb);
                 }
-                load_v(v_phys, v_off);
-                if (!ok || end) break;
-                if (fresh) load_q();
             }
             if (*ctl.abort) {
                 // copies in flight land before shared memory is released
@@ -495,62 +531,66 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // will, so a warp that has read its rows may write them.  Eight lanes take half of two rows whose numbers
         // differ in bits 0 and 2: with the chunks of the codes (as TMA has put them) and of the values at an exclusive
         // or with the row, neither the loads nor the stores meet in a bank.
-        regs_dec<kDecodeRegs>();
         const int half = (lane >> 3) & 1, vec = half * 4 + (lane & 3);
-        // a tile's K scales to floats, by the first two warps
-        auto expand = [&](int t) {
-            if (warp >= 6) return true;
-            const int s = t % L::KS_SLOTS;
-            if (!wait_warp(ctl, bar(L::KSB + s), (t / L::KS_SLOTS) & 1)) return false;
-            const int key = tid - 4 * 32;
-            reinterpret_cast<float*>(gbase + L::KSF)[s * KT + key] = e8m0_value(gbase[L::KS + s * KT + key]);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(L::KSR + s));
-            return true;
-        };
-        int t = 0, seg = 0;
-        bool ok = busy && expand(0);
-        for (; w.more() && ok; w.next(), ++seg) {
-          // the segment's queries, as soon as they are there; then its V tiles, each behind the K scales of the next
-          if (!(ok = wait_warp(ctl, bar(L::QF), seg & 1))) break;
-          const int rows = w.tokens() << p.lg;
+        // per tile: its K scales to floats, by the first two warps; V of the tile before; and, where it is a segment's
+        // first, the segment's queries
+        int j = w.j0, seg = 0;
+        bool more = busy, ok = true;
 #pragma unroll 1
-          for (int r0 = (warp - 4) * 4; r0 < rows; r0 += 16)
-              split_row(gbase + L::Q, r0 + (lane >> 3), lane & 7, reinterpret_cast<float*>(gbase + L::QS) + (seg & 1) * ROWS + r0 + (lane >> 3));
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(L::QR));
-#pragma unroll 1
-          for (int j = w.j0; j < w.j1; ++j, ++t) {
-            if (!(j + 1 == w.j1 && w.last()) && !(ok = expand(t + 1))) break;
-            const int slot = t % L::V_SLOTS;
-            if (!(ok = wait_warp(ctl, bar(L::VRAW + slot), (t / L::V_SLOTS) & 1))) break;
-            uint8_t* tile = gbase + L::V + slot * KV_TILE;
-            const uint8_t* scales = gbase + L::VS + slot * KT;
-            // rolled, four rows at a time: this code and the softmax's share the schedulers' instruction caches
-#pragma unroll 1
-            for (int i = 0; i < 16; i += 4) {
-                const int row = (warp - 4) * 16 + ((2 * (lane >> 4) + i) ^ (lane & 4 ? 5 : 0)), ch = (lane & 3) * 2;
-                const uint4 c = *reinterpret_cast<const uint4*>(tile + KV_HALF + row * 128 + ((vec ^ (row & 7)) * 16));
-                const uint32_t byte = scales[row];
-                uint4 lo, hi;
-                if (__any_sync(0xffffffffu, odd_row(c, byte)))       // and every lane has read its part of these rows
-                    bf16_of_row<true>(c, byte, lo, hi);
-                else
-                    bf16_of_row<false>(c, byte, lo, hi);
-                uint8_t* dst = tile + half * KV_HALF + row * 128;
-                *reinterpret_cast<uint4*>(dst + ((ch ^ (row & 7)) * 16)) = lo;
-                *reinterpret_cast<uint4*>(dst + (((ch + 1) ^ (row & 7)) * 16)) = hi;
+        for (int t = 0; ok; ++t) {
+            if (more && warp < 6) {
+                const int s = t % L::KS_SLOTS, key = tid - 4 * 32;
+                if (!(ok = wait_warp(ctl, bar(L::KSB + s), (t / L::KS_SLOTS) & 1))) break;
+                reinterpret_cast<float*>(gbase + L::KSF)[s * KT + key] = e8m0_value(gbase[L::KS + s * KT + key]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::KSR + s));
             }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(L::VF + slot));
-          }
+            if (t > 0) {
+                const int u = t - 1;
+                const int slot = u % L::V_SLOTS;
+                if (!(ok = wait_warp(ctl, bar(L::VRAW + slot), (u / L::V_SLOTS) & 1))) break;
+                uint8_t* tile = gbase + L::V + slot * KV_TILE;
+                const uint8_t* scales = gbase + L::VS + slot * KT;
+                // rolled, four rows at a time: this code and the softmax's share the schedulers' instruction caches
+#pragma unroll 1
+                for (int i = 0; i < 16; i += 4) {
+                    const int row = (warp - 4) * 16 + ((2 * (lane >> 4) + i) ^ (lane & 4 ? 5 : 0)), ch = (lane & 3) * 2;
+                    const uint4 c = *reinterpret_cast<const uint4*>(tile + KV_HALF + row * 128 + ((vec ^ (row & 7)) * 16));
+                    const uint32_t byte = scales[row];
+                    uint4 lo, hi;
+                    if (__any_sync(0xffffffffu, odd_row(c, byte)))       // and every lane has read its part of these rows
+                        bf16_of_row<true>(c, byte, lo, hi);
+                    else
+                        bf16_of_row<false>(c, byte, lo, hi);
+                    uint8_t* dst = tile + half * KV_HALF + row * 128;
+                    *reinterpret_cast<uint4*>(dst + ((ch ^ (row & 7)) * 16)) = lo;
+                    *reinterpret_cast<uint4*>(dst + (((ch + 1) ^ (row & 7)) * 16)) = hi;
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::VF + slot));
+            }
+            if (!more) break;
+            if (j == w.j0) {
+                if (!(ok = wait_warp(ctl, bar(L::QF), seg & 1))) break;
+                const int rows = w.tokens() << p.lg;
+                float* factors = reinterpret_cast<float*>(gbase + L::QS) + (seg & 1) * ROWS;
+#pragma unroll 1
+                for (int r = (warp - 4) * 4 + (lane >> 3); r - (lane >> 3) < rows; r += 16) split_row(gbase + L::Q, r, lane & 7, factors + r);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::QR));
+                ++seg;
+            }
+            if (++j == w.j1) {
+                more = !w.last();
+                if (more) w.next();
+                j = w.j0;
+            }
         }
         tc_fence_before();
         __syncthreads();
     } else if (warp == MMA_WARP) {
-        if (FP8) regs_dec<kControlRegs>();
         // ---------------------------------------------------------------- MMA
         // The whole warp runs this loop in step; each tcgen05 instruction is issued by one elected lane.
         constexpr uint32_t idesc_qk = idesc_bf16_f32(ROWS, KT, 0, 0);
@@ -572,7 +612,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const uint64_t dk = smem_desc(base + L::K + slot * L::K_TILE, 16, 1024, 2);
             if (FP8) {
                 // the codes themselves: Q's two parts, 32 dims a step
-#pragma unroll
+#pragma unroll 1
                 for (int ks = 0; ks < 2 * D / 32; ++ks)
                     mma_f8_warp(tmem + (t & 1) * KT, dq + (((ks >> 2) * Q_HALF + (ks & 3) * 32) >> 4), dk + ((ks & 3) * 32 >> 4), idesc_e4m3_f32(ROWS, KT),
                                 ks > 0 ? 1u : 0u);
@@ -586,15 +626,17 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             mma_commit_warp(bar(L::KE + slot));
             if (seg_last) mma_commit_warp(bar(L::QE));
         };
-        int j = w.j0;
-        if (ok) issue_s(0, true, w.j0 + 1 == w.j1);
-        for (int t = 0; ok; ++t) {
+        // S of a tile goes ahead of the product with V of the tile before it, as long as both are of one segment
+        int j = w.j0, t = 0, s = 0;
+#pragma unroll 1
+        while (ok) {
+            if (s == t || (s == t + 1 && j + 1 < w.j1)) {
+                issue_s(s, s == t, j + (s - t) + 1 == w.j1);
+                ++s;
+                continue;
+            }
             const bool first_here = j == w.j0, last_here = j + 1 == w.j1, end = last_here && w.last();
             const int keys = min(KT, w.s.len - j * KT);
-            if (!last_here) {
-                issue_s(t + 1, false, j + 2 == w.j1);
-                if (!ok) break;
-            }
             if (first_here) {
                 if (oseg >= 1 && !(ok = wait_warp(ctl, bar(L::OE), (oseg - 1) & 1))) break;
                 ++oseg;
@@ -604,6 +646,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (!(ok = wait_warp(ctl, bar(L::PF + (t & 1)), (t >> 1) & 1))) break;
             tc_fence_after();
             const uint64_t dv = smem_desc(base + L::V + slot * KV_TILE, KV_HALF, 1024, 2);
+#pragma unroll 1
             for (int ks = 0; ks < (keys + 15) >> 4; ++ks)
                 mma_ts_warp(tmem + O_COL, tmem + (t & 1) * KT + ks * 8, dv + ks * (16 * 128 >> 4), idesc_pv,
                             (!first_here || ks > 0) ? 1u : 0u);
@@ -611,13 +654,9 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             mma_commit_warp(bar(L::VE + slot));
             if (last_here) mma_commit_warp(bar(L::OF));
             if (end) break;
-            if (last_here) {
-                w.next();
-                j = w.j0;
-                issue_s(t + 1, true, w.j0 + 1 == w.j1);
-            } else {
-                ++j;
-            }
+            if (last_here) w.next();
+            j = last_here ? w.j0 : j + 1;
+            ++t;
         }
         mma_commit_warp(bar(L::DRAIN));
         wait_drain(bar(L::DRAIN), 0);
@@ -626,12 +665,8 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         __syncthreads();
         tc_fence_after();
         tmem_dealloc(tmem, TMEM_COLS);
-    } else if (FP8 && warp >= 10) {
-        regs_dec<kControlRegs>();
-        __syncthreads();
     } else {
         // ---------------------------------------------------------------- softmax and epilogue
-        if (FP8) regs_inc<kSoftmaxRegs>();
         const int row = tid;                                  // TMEM lane
         const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
         const int qtok = ROWS >> p.lg;
@@ -816,14 +851,13 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 meta = make_int4(static_cast<int>((end * C - 1) / W), w.s.q0 + w.rt * qtok, tokens, 0);
             }
             if (warp_live) {
-                // nodes of which something was taken out, by any of the warps
-                auto taken = [&](int i) {
-                    const uint32_t* x = wild + (seg & 1) * 32 + i;
-                    return x[0] | x[8] | x[16] | x[24];
-                };
-                uint32_t any = 0u;
-                if (had_tree)
+                if (had_tree) {
+                    // what was taken out of the tiles, to the rows that see it
+                    uint32_t any = 0u;
+#pragma unroll 1
                     for (int i = 0; i < 32; ++i) any |= wild[(seg & 1) * 32 + i];
+                    if (any != 0u) give_back<FP8>(p, w.b, w.s.n, w.s.len, w.j0, w.j1, g, wild + (seg & 1) * 32, words[0], words[1], words[2], words[3], live, tmem + lane_off + O_COL);
+                }
                 const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
                 const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + part;
                 uint16_t* orow = p.out + (static_cast<int64_t>(node_row) * p.num_heads + (g << p.lg) + (row & ((1 << p.lg) - 1))) * D;
@@ -833,31 +867,6 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     uint32_t o[32];
                     tmem_ld32(tmem + lane_off + O_COL + 32 * cc, o);
                     tmem_ld_wait();
-                    if (any != 0u && live) {
-                        // what was taken out of the tiles, to the rows that see it
-#pragma unroll 1
-                        for (int i = 0; i < w.s.n; ++i) {
-                            const unsigned long long word = i < 64 ? words[0] : i < 128 ? words[1] : i < 192 ? words[2] : words[3];
-                            const int j = (tree0 + i) / KT;
-                            if (!((taken(i >> 5) >> (i & 31)) & 1u) || !((word >> (i & 63)) & 1ull) || j < w.j0 || j >= w.j1) continue;
-                            int off;
-                            const int phys = w.block_of(j, off);
-                            if (phys < 0) continue;
-                            const int64_t at = static_cast<int64_t>(phys) * p.block_size + off + (tree0 + i - j * KT);
-                            const int64_t first_v = (at * p.num_kv_heads + g) * D + 32 * cc;
-                            const float f = FP8 ? e8m0_value(__ldg(p.v_scale + (static_cast<int64_t>(phys) * p.num_kv_heads + g) * p.block_size + off +
-                                                                   (tree0 + i - j * KT))) : 1.f;
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
-                                const uint2 v = FP8 ? bf16_of_codes(__ldg(reinterpret_cast<const uint32_t*>(p.v_codes + first_v + e)), f)
-                                                    : __ldg(reinterpret_cast<const uint2*>(p.v_cache + first_v + e));
-                                const float x[4] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)};
-#pragma unroll
-                                for (int d = 0; d < 4; ++d)
-                                    if (!(fabsf(x[d]) <= 3.4028235e38f)) o[e + d] = __float_as_uint(__uint_as_float(o[e + d]) + x[d]);
-                            }
-                        }
-                    }
                     if (whole) {
                         if (live) {
 #pragma unroll
@@ -983,11 +992,6 @@ pkv_status launch_tree_decode(const TreeDecodeArgs& a, int* err, cudaStream_t st
             encode_tiled(&tm_v, type, 4, const_cast<void*>(a.v_cache), dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B, promotion) != CUDA_SUCCESS)
             return PKV_ERR_INVALID_ARG;
     }
-    static const int launch_regs = [] {
-        cudaFuncAttributes fa;
-        return cudaFuncGetAttributes(&fa, tree_decode_kernel<true>) == cudaSuccess ? fa.numRegs : -1;
-    }();
-    if (fp8 && launch_regs < static_cast<int>(kMinLaunchRegs)) return PKV_ERR_UNSUPPORTED;
     const size_t ctas = static_cast<size_t>(max_ctas(a.num_kv_heads));
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     Params p{};
