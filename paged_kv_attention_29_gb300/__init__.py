@@ -968,31 +968,48 @@ def pkv_tree_accept(target: torch.Tensor, draft: torch.Tensor, tree_mask: torch.
 
     ``target`` (what pkv_sample returned for the nodes' logits) and ``draft`` are int64 [total_nodes].  Returns
     (path int32 [batch, max_path] padded with -1, path_lens int32, next_tokens int64, new_context_lens int32)."""
-    _check(target, "target", torch.int64, 1)
+    if not target.is_cuda:
+        _check(target, "target", torch.int64, 1)
+    _want(target, "target", torch.int64, 1)
     _want(draft, "draft", torch.int64, 1)
     _want(tree_mask, "tree_mask", torch.int64, 2)
     _want(cu_nodes, "cu_nodes", torch.int32, 1)
     _want(context_lens, "context_lens", torch.int32, 1)
-    total, batch, max_path = target.shape[0], context_lens.shape[0], int(max_path)
-    if draft.shape[0] != total or tree_mask.shape[0] != total or cu_nodes.shape[0] != batch + 1:
+    (total,), (batch,), (rows, words) = target.shape, context_lens.shape, tree_mask.shape
+    if draft.shape[0] != total or rows != total or cu_nodes.shape[0] != batch + 1:
         raise ValueError("target, draft, tree_mask, cu_nodes and context_lens disagree")
+    max_path = int(max_path)
     if max_path < 1:
         raise ValueError("max_path must be at least 1")
-    outs = []
-    for name, t, dtype, shape in (("path", path, torch.int32, (batch, max_path)), ("path_lens", path_lens, torch.int32, (batch,)),
-                                  ("next_tokens", next_tokens, torch.int64, (batch,)),
-                                  ("new_context_lens", new_context_lens, torch.int32, (batch,))):
-        if t is None:
-            t = _allocated(stream, torch.empty, shape, dtype=dtype, device=target.device, result=True)
-        else:
-            _want(t, name, dtype, len(shape))
-            if t.shape != shape:
-                raise ValueError(f"{name} must be {list(shape)}")
-        outs.append(t)
-    _launch("pkv_tree_accept", load().pkv_tree_accept, stream, (target, draft, tree_mask, cu_nodes, context_lens, *outs),
-            (target.data_ptr(), draft.data_ptr(), tree_mask.data_ptr(), tree_mask.shape[1], cu_nodes.data_ptr(),
-             context_lens.data_ptr(), batch, total, int(max_nodes), max_path, *[t.data_ptr() for t in outs]))
-    return tuple(outs)
+    dev = target.device
+    if path is None:
+        path = _allocated(stream, torch.empty, (batch, max_path), dtype=torch.int32, device=dev, result=True)
+    else:
+        _shaped(path, "path", torch.int32, (batch, max_path))
+    if path_lens is None:
+        path_lens = _allocated(stream, torch.empty_like, context_lens, result=True)
+    else:
+        _shaped(path_lens, "path_lens", torch.int32, (batch,))
+    if next_tokens is None:
+        next_tokens = _allocated(stream, torch.empty, batch, dtype=torch.int64, device=dev, result=True)
+    else:
+        _shaped(next_tokens, "next_tokens", torch.int64, (batch,))
+    if new_context_lens is None:
+        new_context_lens = _allocated(stream, torch.empty_like, context_lens, result=True)
+    else:
+        _shaped(new_context_lens, "new_context_lens", torch.int32, (batch,))
+    _launch("pkv_tree_accept", load().pkv_tree_accept, stream,
+            (target, draft, tree_mask, cu_nodes, context_lens, path, path_lens, next_tokens, new_context_lens),
+            (target.data_ptr(), draft.data_ptr(), tree_mask.data_ptr(), words, cu_nodes.data_ptr(),
+             context_lens.data_ptr(), batch, total, int(max_nodes), max_path, path.data_ptr(), path_lens.data_ptr(),
+             next_tokens.data_ptr(), new_context_lens.data_ptr()))
+    return path, path_lens, next_tokens, new_context_lens
+
+
+def _shaped(t, name, dtype, shape):
+    _want(t, name, dtype, len(shape))
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
 
 
 class KvPools:

@@ -1,6 +1,7 @@
 // What follows the attention of a tree of drafted tokens: the accepted path, its rows
 // moved together in every layer's pools, and the rows of blocks copied for a fork.
 #include <algorithm>
+#include <type_traits>
 
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
@@ -78,77 +79,95 @@ __global__ void __launch_bounds__(32 * ACCEPT_WARPS) tree_accept_kernel(const Tr
 // ---------------------------------------------------------------------------
 // compaction of the accepted rows
 // ---------------------------------------------------------------------------
-// CTA (x, b): pool x (K and V of each layer) and sequence b.  The accepted node of depth d moves to the d-th row
+// CTA (x, b): some pools (a layer's K or V each) of sequence b.  The accepted node of depth d moves to the d-th row
 // behind the context.  A path's nodes ascend and node path[d] >= d, so a row that is written has been read before by
-// the same thread: each thread takes its 16-byte columns of all rows in order, BATCH rows at a time, loads first.
-constexpr int COMPACT_THREADS = 128, BATCH = 8;
+// the same thread: each thread takes columns of all rows in order, BATCH rows at a time, loads first.  What a call costs
+// beside its bytes is the chain of path, block table and rows, so the GPU is filled once: a CTA walks the chain for as
+// many pools as that takes, one warp lists the rows that move (and where their scales lie: a division by the block size
+// costs more than a move), and the 8-bit rows' scales have a warp of their own.
+constexpr int ROW_THREADS = 256, COMPACT_THREADS = ROW_THREADS + 32, COMPACT_CTAS = 5, BATCH = 4;
 
-__global__ void __launch_bounds__(COMPACT_THREADS) tree_compact_kernel(const __grid_constant__ PoolTable pools, const TreeCompactArgs a, int* err) {
-    __shared__ int64_t src[kMaxTreeNodes], dst[kMaxTreeNodes];     // rows (block * block_size + offset); src < 0: stays
-    const int b = blockIdx.y, pool = blockIdx.x >> 1, is_v = blockIdx.x & 1;
-    const int q0 = __ldg(a.cu_nodes + b), q1 = __ldg(a.cu_nodes + b + 1), len = __ldg(a.context_lens + b);
-    const int count = __ldg(a.path_lens + b);
-    const long long n = static_cast<long long>(q1) - q0;
+__global__ void __launch_bounds__(COMPACT_THREADS, COMPACT_CTAS)
+tree_compact_kernel(const __grid_constant__ PoolTable pools, const TreeCompactArgs a, int pools_per_cta, int* err) {
+    __shared__ int64_t src[kMaxTreeNodes], dst[kMaxTreeNodes];     // rows that move, block * block_size + offset
+    __shared__ int64_t src_scale[kMaxTreeNodes], dst_scale[kMaxTreeNodes];   // and the places of their first head's scales
+    __shared__ int moves;
+    const int b = blockIdx.y, tid = threadIdx.x;
+    if (tid < 32) {
+        const bool say = blockIdx.x == 0;
+        const int32_t* path = a.path + static_cast<int64_t>(b) * a.max_path;
+        int node = tid < a.max_path ? __ldg(path + tid) : -1;      // asked for before the lengths are known
+        const int q0 = __ldg(a.cu_nodes + b), q1 = __ldg(a.cu_nodes + b + 1), len = __ldg(a.context_lens + b), count = __ldg(a.path_lens + b);
+        const long long n = static_cast<long long>(q1) - q0;
+        const bool fits = n >= 0 && n <= kMaxTreeNodes && n <= len && len <= static_cast<long long>(a.max_blocks) * a.block_size;
+        bool good = fits && count >= 0 && count <= a.max_path && count <= n;
+        if (!good && count != 0 && say && tid == 0) record_error(err, fits ? PKV_DEVERR_TREE : PKV_DEVERR_SEQLENS, b);
+        int listed = 0, before = -1;                               // the last node of the 32 before
+        for (int d0 = 0; good && d0 < count; d0 += 32) {
+            const int d = d0 + tid;
+            if (d0) node = d < count ? __ldg(path + d) : -1;
+            int prev = __shfl_up_sync(0xffffffffu, node, 1);
+            if (tid == 0) prev = before;
+            before = __shfl_sync(0xffffffffu, node, 31);
+            // a path that does not ascend could be read after it is written
+            good = __all_sync(0xffffffffu, d >= count || (node > prev && node < n));
+            if (!good && say && tid == 0) record_error(err, PKV_DEVERR_TREE, b);
+            int64_t row[2] = {-1, -1}, scale[2];
+            if (good && d < count && node != d) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int pos = len - static_cast<int>(n) + (k ? d : node), lb = pos / a.block_size;
+                    const int phys = __ldg(a.block_tables + static_cast<int64_t>(b) * a.max_blocks + lb);
+                    const int off = pos - lb * a.block_size;
+                    scale[k] = static_cast<int64_t>(phys) * a.num_kv_heads * a.block_size + off;
+                    if (phys >= 0 && phys < a.num_blocks)
+                        row[k] = static_cast<int64_t>(phys) * a.block_size + off;
+                    else if (say)
+                        record_error(err, PKV_DEVERR_BLOCK_ID, b);
+                }
+            }
+            const bool moving = row[0] >= 0 && row[1] >= 0;
+            const unsigned who = __ballot_sync(0xffffffffu, moving);
+            if (moving) {
+                const int at = listed + __popc(who & ((1u << tid) - 1u));
+                src[at] = row[0];
+                dst[at] = row[1];
+                src_scale[at] = scale[0];
+                dst_scale[at] = scale[1];
+            }
+            listed += __popc(who);
+        }
+        if (tid == 0) moves = good ? listed : 0;
+    }
+    __syncthreads();
+    const int count = moves;
     if (count == 0) return;
-    const bool say = blockIdx.x == 0 && threadIdx.x == 0;
-    if (n < 0 || n > kMaxTreeNodes || n > len || len > static_cast<long long>(a.max_blocks) * a.block_size) {
-        if (say) record_error(err, PKV_DEVERR_SEQLENS, b);
-        return;
-    }
-    if (count < 0 || count > a.max_path || count > n) {
-        if (say) record_error(err, PKV_DEVERR_TREE, b);
-        return;
-    }
-    const int first = len - static_cast<int>(n);
-    const int32_t* path = a.path + static_cast<int64_t>(b) * a.max_path;
-    auto row_of = [&](int pos) -> int64_t {
-        const int lb = pos / a.block_size;
-        const int phys = __ldg(a.block_tables + static_cast<int64_t>(b) * a.max_blocks + lb);
-        if (phys < 0 || phys >= a.num_blocks) {
-            if (blockIdx.x == 0) record_error(err, PKV_DEVERR_BLOCK_ID, b);
-            return -1;
-        }
-        return static_cast<int64_t>(phys) * a.block_size + (pos - lb * a.block_size);
-    };
-    bool good = true;
-    for (int d = threadIdx.x; d < count; d += COMPACT_THREADS) {
-        const int node = __ldg(path + d), before = d ? __ldg(path + d - 1) : -1;
-        const bool fine = node > before && node < n;
-        good &= fine;
-        int64_t s = -1, t = -1;
-        if (fine && node != d) {
-            s = row_of(first + node);
-            t = row_of(first + d);
-        }
-        src[d] = t >= 0 ? s : -1;
-        dst[d] = t;
-    }
-    if (!__syncthreads_and(good)) {                            // a path that does not ascend could be read after it is written
-        if (say) record_error(err, PKV_DEVERR_TREE, b);
-        return;
-    }
-    uint8_t* rows = static_cast<uint8_t*>(is_v ? pools.v[pool] : pools.k[pool]);
-    const int vecs = a.row_bytes / 16;
-    for (int c = threadIdx.x; c < vecs; c += COMPACT_THREADS) {
+    const int pool0 = blockIdx.x * pools_per_cta, here = min(pools_per_cta, 2 * pools.layers - pool0);
+    // one column; from[d] * stride and to[d] * stride: its places in the listed rows
+    auto move = [&](auto* column, const int64_t* from, const int64_t* to, int64_t stride) {
         for (int d0 = 0; d0 < count; d0 += BATCH) {
-            uint4 x[BATCH];
+            std::remove_reference_t<decltype(*column)> x[BATCH];
 #pragma unroll
             for (int i = 0; i < BATCH; ++i)
-                if (d0 + i < count && src[d0 + i] >= 0) x[i] = reinterpret_cast<const uint4*>(rows)[src[d0 + i] * vecs + c];
+                if (d0 + i < count) x[i] = column[from[d0 + i] * stride];
 #pragma unroll
             for (int i = 0; i < BATCH; ++i)
-                if (d0 + i < count && src[d0 + i] >= 0) reinterpret_cast<uint4*>(rows)[dst[d0 + i] * vecs + c] = x[i];
+                if (d0 + i < count) column[to[d0 + i] * stride] = x[i];
+        }
+    };
+    if (tid < ROW_THREADS) {
+        const int vecs = a.row_bytes / 16;
+        for (int c = tid; c < here * vecs; c += ROW_THREADS) {
+            const int i = c / vecs, x = pool0 + i;
+            move(static_cast<uint4*>(x & 1 ? pools.v[x >> 1] : pools.k[x >> 1]) + (c - i * vecs), src, dst, vecs);
+        }
+    } else if (pools.k_scale[0] != nullptr) {
+        for (int c = tid - ROW_THREADS; c < here * a.num_kv_heads; c += 32) {
+            const int i = c / a.num_kv_heads, x = pool0 + i;
+            move((x & 1 ? pools.v_scale[x >> 1] : pools.k_scale[x >> 1]) + static_cast<int64_t>(c - i * a.num_kv_heads) * a.block_size, src_scale,
+                 dst_scale, 1);
         }
     }
-    uint8_t* scales = is_v ? pools.v_scale[pool] : pools.k_scale[pool];
-    if (scales == nullptr) return;
-    auto scale_at = [&](int64_t row, int h) {
-        const int64_t blk = row / a.block_size;
-        return (blk * a.num_kv_heads + h) * a.block_size + (row - blk * a.block_size);
-    };
-    for (int h = threadIdx.x; h < a.num_kv_heads; h += COMPACT_THREADS)
-        for (int d = 0; d < count; ++d)
-            if (src[d] >= 0) scales[scale_at(dst[d], h)] = scales[scale_at(src[d], h)];
 }
 
 // ---------------------------------------------------------------------------
@@ -208,7 +227,10 @@ cudaError_t launch_tree_accept(const TreeAcceptArgs& a, int* err, cudaStream_t s
 }
 
 cudaError_t launch_tree_compact(const PoolTable& pools, const TreeCompactArgs& a, int* err, cudaStream_t stream) {
-    tree_compact_kernel<<<dim3(2 * pools.layers, a.batch), COMPACT_THREADS, 0, stream>>>(pools, a, err);
+    // as many pools to a CTA as let all CTAs run at once
+    const int64_t all = 2ll * pools.layers * a.batch, room = static_cast<int64_t>(COMPACT_CTAS) * std::max(1, sm_count());
+    const int per = static_cast<int>(std::min<int64_t>(2 * pools.layers, (all + room - 1) / room));
+    tree_compact_kernel<<<dim3((2 * pools.layers + per - 1) / per, a.batch), COMPACT_THREADS, 0, stream>>>(pools, a, per, err);
     return cudaGetLastError();
 }
 
