@@ -66,17 +66,18 @@ constexpr int THREADS_BF16 = 192, THREADS_FP8 = 320;
 // Shared memory.  bf16: rings of 3 K and 2 V tiles (a K tile is asked for two steps before its product, a V tile's
 // product comes a step later).  8 bits: 3 tiles of K codes and 3 V tiles; the row scales of K as bytes and as floats, in
 // rings so long that those of a tile are read before K's copies come round again (K of tile t + 5 is asked for when
-// tile t is through); each query row's factor, of two segments.  Split tiles: the weights of 32 rows, in front of the K
+// tile t is through); each query row's factor, of two segments.  Split tiles: the weights of 32 rows (of two tiles, where there is room), in front of the K
 // tiles: the product's other 96 rows of weights are whatever lies there, and their sums are not read.
 template <bool FP8, bool SPLIT>
 struct Layout {
-    static constexpr int K_SLOTS = SPLIT && !FP8 ? 2 : 3, V_SLOTS = FP8 ? 3 : 2, K_TILE = FP8 ? KT * D : KV_TILE, KS_SLOTS = 6;
-    static constexpr int Q = 0, P = 2 * Q_HALF, K = P + (SPLIT ? SPLIT_ROWS * KT * 2 : 0), V = K + K_SLOTS * K_TILE, VS = V + V_SLOTS * KV_TILE, KS = VS + (FP8 ? V_SLOTS * KT : 0);
+    static constexpr int P_SLOTS = SPLIT ? (FP8 ? 2 : 1) : 0, P_TILE = SPLIT_ROWS * KT * 2;
+    static constexpr int K_SLOTS = SPLIT ? 2 : 3, V_SLOTS = FP8 ? 3 : 2, K_TILE = FP8 ? KT * D : KV_TILE, KS_SLOTS = 6;
+    static constexpr int Q = 0, P = 2 * Q_HALF, K = P + P_SLOTS * P_TILE, V = K + K_SLOTS * K_TILE, VS = V + V_SLOTS * KV_TILE, KS = VS + (FP8 ? V_SLOTS * KT : 0);
     static constexpr int KSF = KS + (FP8 ? KS_SLOTS * KT : 0), QS = KSF + (FP8 ? KS_SLOTS * KT * 4 : 0);
     static constexpr int Q_ROWS = SPLIT ? SPLIT_ROWS : ROWS, EX = QS + (FP8 ? 2 * Q_ROWS * 4 : 0);      // what the four warps tell each other, two rounds of it
     static constexpr int BAR = EX + (SPLIT ? 2 * 4 * 32 * 4 : 0);
     static constexpr int KF = 0, KE = KF + K_SLOTS, VF = KE + K_SLOTS, VE = VF + V_SLOTS, QF = VE + V_SLOTS, QE = QF + 1, SF = QE + 1, PF = SF + 2,
-                         PV = PF + 2, OF = PV + 1, OE = OF + 1, WG = OE + 1, DRAIN = WG + 1, BF16_BARS = DRAIN + 1;
+                         PV = PF + 2, OF = PV + 2, OE = OF + 1, WG = OE + 1, DRAIN = WG + 1, BF16_BARS = DRAIN + 1;
     static constexpr int VRAW = BF16_BARS, KSB = VRAW + V_SLOTS, KSR = KSB + KS_SLOTS, QR = KSR + KS_SLOTS, QG = QR + 1, FP8_BARS = QG + 1;
     static constexpr int NUM_BARS = FP8 ? FP8_BARS : BF16_BARS;
     static constexpr int MISC = (BAR + NUM_BARS * 8 + 15) & ~15;  // [0] TMEM base, [1] abort
@@ -213,6 +214,146 @@ struct Walk {
         return -1;
     }
 };
+
+// A tile's products, issued by one elected lane in one piece: chosen once for all of them, with the descriptors advanced by
+// constants, an instruction costs the issuing warp what it should, where a loop of single ones took 130 cycles each.
+// S = Q K^T, bf16: 8 steps of 16 dims, 64 dims to a half of each tile.
+__device__ __forceinline__ void issue_qk_bf16(uint32_t d, uint64_t q, uint64_t k, uint32_t idesc) {
+    static_assert(Q_HALF >> 4 == 1024 && KV_HALF >> 4 == 512, "offsets below");
+    asm volatile(
+        "{\n\t"
+        ".reg .pred e, f, t;\n\t"
+        ".reg .b32 r;\n\t"
+        ".reg .b64 a, b;\n\t"
+        "elect.sync r|e, 0xffffffff;\n\t"
+        "setp.ne.u32 f, 0, 0;\n\t"
+        "setp.eq.u32 t, 0, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n\t"
+        "add.u64 a, %1, 2;\n\t"
+        "add.u64 b, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "add.u64 a, %1, 4;\n\t"
+        "add.u64 b, %2, 4;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "add.u64 a, %1, 6;\n\t"
+        "add.u64 b, %2, 6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "add.u64 a, %1, 1024;\n\t"
+        "add.u64 b, %2, 512;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "add.u64 a, %1, 1026;\n\t"
+        "add.u64 b, %2, 514;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "add.u64 a, %1, 1028;\n\t"
+        "add.u64 b, %2, 516;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "add.u64 a, %1, 1030;\n\t"
+        "add.u64 b, %2, 518;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "}" :: "r"(d), "l"(q), "l"(k), "r"(idesc)
+        : "memory");
+}
+
+// S = (Q's two parts) K^T, e4m3: 4 steps of 32 dims for each part.
+__device__ __forceinline__ void issue_qk_e4m3(uint32_t d, uint64_t q, uint64_t k, uint32_t idesc) {
+    asm volatile(
+        "{\n\t"
+        ".reg .pred e, f, t;\n\t"
+        ".reg .b32 r;\n\t"
+        ".reg .b64 a, b;\n\t"
+        "elect.sync r|e, 0xffffffff;\n\t"
+        "setp.ne.u32 f, 0, 0;\n\t"
+        "setp.eq.u32 t, 0, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, f;\n\t"
+        "add.u64 a, %1, 2;\n\t"
+        "add.u64 b, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+        "add.u64 a, %1, 4;\n\t"
+        "add.u64 b, %2, 4;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+        "add.u64 a, %1, 6;\n\t"
+        "add.u64 b, %2, 6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+        "add.u64 a, %1, 1024;\n\t"
+        "add.u64 b, %2, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+        "add.u64 a, %1, 1026;\n\t"
+        "add.u64 b, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+        "add.u64 a, %1, 1028;\n\t"
+        "add.u64 b, %2, 4;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+        "add.u64 a, %1, 1030;\n\t"
+        "add.u64 b, %2, 6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+        "}" :: "r"(d), "l"(q), "l"(k), "r"(idesc)
+        : "memory");
+}
+
+// O (+)= P V, P in TMEM: `steps` (1 to 4) of 16 keys.
+__device__ __forceinline__ void issue_pv_ts(uint32_t d, uint32_t p, uint64_t v, uint32_t idesc, uint32_t accumulate, uint32_t steps) {
+    asm volatile(
+        "{\n\t"
+        ".reg .pred e, f, t;\n\t"
+        ".reg .b32 r, a;\n\t"
+        ".reg .b64 b;\n\t"
+        "elect.sync r|e, 0xffffffff;\n\t"
+        "setp.ne.u32 f, %4, 0;\n\t"
+        "setp.eq.u32 t, 0, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n\t"
+        "setp.gt.and.u32 e, %5, 1, e;\n\t"
+        "add.u32 a, %1, 8;\n\t"
+        "add.u64 b, %2, 128;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+        "setp.gt.and.u32 e, %5, 2, e;\n\t"
+        "add.u32 a, %1, 16;\n\t"
+        "add.u64 b, %2, 256;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+        "setp.gt.and.u32 e, %5, 3, e;\n\t"
+        "add.u32 a, %1, 24;\n\t"
+        "add.u64 b, %2, 384;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+        "}" :: "r"(d), "r"(p), "l"(v), "r"(idesc), "r"(accumulate), "r"(steps)
+        : "memory");
+}
+
+// O (+)= P V, P in shared memory: `steps` (1 to 4) of 16 keys.
+__device__ __forceinline__ void issue_pv_ss(uint32_t d, uint64_t p, uint64_t v, uint32_t idesc, uint32_t accumulate, uint32_t steps) {
+    asm volatile(
+        "{\n\t"
+        ".reg .pred e, f, t;\n\t"
+        ".reg .b32 r;\n\t"
+        ".reg .b64 b, a;\n\t"
+        "elect.sync r|e, 0xffffffff;\n\t"
+        "setp.ne.u32 f, %4, 0;\n\t"
+        "setp.eq.u32 t, 0, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n\t"
+        "setp.gt.and.u32 e, %5, 1, e;\n\t"
+        "add.u64 a, %1, 2;\n\t"
+        "add.u64 b, %2, 128;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "setp.gt.and.u32 e, %5, 2, e;\n\t"
+        "add.u64 a, %1, 4;\n\t"
+        "add.u64 b, %2, 256;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "setp.gt.and.u32 e, %5, 3, e;\n\t"
+        "add.u64 a, %1, 6;\n\t"
+        "add.u64 b, %2, 384;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "}" :: "r"(d), "l"(p), "l"(v), "r"(idesc), "r"(accumulate), "r"(steps)
+        : "memory");
+}
+
+// Arrive on two barriers, and on a third if it is not 0, once all products issued before are through.
+__device__ __forceinline__ void commit3(uint32_t a, uint32_t b, uint32_t c) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t.reg .b32 r;\n\telect.sync r|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t"
+        "setp.ne.and.u32 e, %2, 0, e;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%2];\n\t}" ::"r"(a), "r"(b), "r"(c)
+        : "memory");
+}
 
 // Which of a tile's keys a node sees: bit e for key 64 j + e.
 __device__ __forceinline__ unsigned long long visible(const unsigned long long (&w)[4], int rel, int keys) {
@@ -621,21 +762,11 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (!(ok = wait_warp(ctl, bar(L::KF + slot), (t / L::K_SLOTS) & 1))) return;
             tc_fence_after();
             const uint64_t dk = smem_desc(base + L::K + slot * L::K_TILE, 16, 1024, 2);
-            if (FP8) {
-                // the codes themselves: Q's two parts, 32 dims a step
-#pragma unroll 1
-                for (int ks = 0; ks < 2 * D / 32; ++ks)
-                    mma_f8_warp(tmem + (t & 1) * KT, dq + (((ks >> 2) * Q_HALF + (ks & 3) * 32) >> 4), dk + ((ks & 3) * 32 >> 4), idesc_e4m3_f32(ROWS, KT),
-                                ks > 0 ? 1u : 0u);
-            } else {
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-                    mma_ss_warp(tmem + (t & 1) * KT, dq + (((ks >> 2) * Q_HALF + (ks & 3) * 32) >> 4),
-                                dk + (((ks >> 2) * KV_HALF + (ks & 3) * 32) >> 4), idesc_qk, ks > 0 ? 1u : 0u);
-            }
-            mma_commit_warp(bar(L::SF + (t & 1)));
-            mma_commit_warp(bar(L::KE + slot));
-            if (seg_last) mma_commit_warp(bar(L::QE));
+            if (FP8)
+                issue_qk_e4m3(tmem + (t & 1) * KT, dq, dk, idesc_e4m3_f32(ROWS, KT));     // the codes themselves, and Q's two parts
+            else
+                issue_qk_bf16(tmem + (t & 1) * KT, dq, dk, idesc_qk);
+            commit3(bar(L::SF + (t & 1)), bar(L::KE + slot), seg_last ? bar(L::QE) : 0u);
         };
         // S of a tile goes ahead of the product with V of the tile before it, as long as both are of one segment
         int j = w.j0, t = 0, s = 0;
@@ -657,17 +788,11 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (!(ok = wait_warp(ctl, bar(L::PF + (t & 1)), (t >> 1) & 1))) break;
             tc_fence_after();
             const uint64_t dv = smem_desc(base + L::V + slot * KV_TILE, KV_HALF, 1024, 2);
-#pragma unroll 1
-            for (int ks = 0; ks < (keys + 15) >> 4; ++ks)
-                if constexpr (SPLIT)
-                    mma_ss_warp(tmem + O_COL, smem_desc(base + L::P, 16, 1024, 2) + ks * (32 >> 4), dv + ks * (16 * 128 >> 4), idesc_pv,
-                                (!first_here || ks > 0) ? 1u : 0u);
-                else
-                    mma_ts_warp(tmem + O_COL, tmem + (t & 1) * KT + ks * 8, dv + ks * (16 * 128 >> 4), idesc_pv,
-                            (!first_here || ks > 0) ? 1u : 0u);
-            mma_commit_warp(bar(L::PV));
-            mma_commit_warp(bar(L::VE + slot));
-            if (last_here) mma_commit_warp(bar(L::OF));
+            if constexpr (SPLIT)
+                issue_pv_ss(tmem + O_COL, smem_desc(base + L::P + (t % max(1, L::P_SLOTS)) * L::P_TILE, 16, 1024, 2), dv, idesc_pv, first_here ? 0u : 1u, (keys + 15) >> 4);
+            else
+                issue_pv_ts(tmem + O_COL, tmem + (t & 1) * KT, dv, idesc_pv, first_here ? 0u : 1u, (keys + 15) >> 4);
+            commit3(bar(L::PV + (t & 1)), bar(L::VE + slot), last_here ? bar(L::OF) : 0u);
             if (end) break;
             if (last_here) w.next();
             j = last_here ? w.j0 : j + 1;
@@ -792,7 +917,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         m_used = m_new;
                     } else if (__any_sync(0xffffffffu, m_new > m_used + kRescaleLog2)) {
                         // O is rescaled only when a maximum grows by 2^8; PV(t - 1) has to be through
-                        ok = wait_warp(ctl, bar(L::PV), (t - 1) & 1);
+                        ok = wait_warp(ctl, bar(L::PV + ((t - 1) & 1)), ((t - 1) >> 1) & 1);
                         if (!ok) break;
                         tc_fence_after();
                         const float m_tgt = fmaxf(m_used, m_new);
@@ -829,9 +954,9 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         }
                         // P's columns end before the ones of S that are still to be read
                         if constexpr (SPLIT) {
-                            // to shared memory, once the product with the weights of the tile before has read them
-                            if (t > 0 && !(ok = wait_warp(ctl, bar(L::PV), (t - 1) & 1))) break;
-                            uint8_t* prow = gbase + L::P + lane * 128;
+                            // to shared memory, once the product with the weights that lie there is through
+                            if (t >= L::P_SLOTS && !(ok = wait_warp(ctl, bar(L::PV + ((t - L::P_SLOTS) & 1)), ((t - L::P_SLOTS) >> 1) & 1))) break;
+                            uint8_t* prow = gbase + L::P + (t % L::P_SLOTS) * L::P_TILE + lane * 128;
                             *reinterpret_cast<uint4*>(prow + (((2 * warp) ^ (lane & 7)) * 16)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
                             *reinterpret_cast<uint4*>(prow + (((2 * warp + 1) ^ (lane & 7)) * 16)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
                             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
