@@ -726,7 +726,7 @@ pkv_status tree_decode_call(const pkv_bf16* q, const void* k_cache, const void* 
         max_context_len < 0 || !(softmax_scale > 0.f) || softmax_scale == INFINITY)
         return PKV_ERR_INVALID_ARG;
     if (!supported_shape(num_heads, num_kv_heads, head_dim, block_size)) return PKV_ERR_UNSUPPORTED;
-    if (max_nodes > kMaxTreeNodes || batch > 4096) return PKV_ERR_UNSUPPORTED;
+    if (max_nodes > kMaxTreeNodes || batch > kMaxTreeBatch) return PKV_ERR_UNSUPPORTED;
     if (max_nodes > 64 * static_cast<int64_t>(mask_words)) return PKV_ERR_INVALID_ARG;
     if (static_cast<int64_t>(max_blocks_per_seq) * block_size > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
     if (batch == 0 || total_nodes == 0 || max_nodes == 0) return PKV_OK;

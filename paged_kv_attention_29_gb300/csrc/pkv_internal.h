@@ -27,7 +27,7 @@ int sm_count();
 // current device once (thread-safe; a failed set-up is retried on the next
 // call) and returns whether the set-up for `key` has succeeded on this device.
 enum SetupKey { kSetupDecode = 0, kSetupPrefill, kSetupRopeStore, kSetupDecodeFp8, kSetupSampleFiltered, kSetupStoreFp8,
-                kSetupStoreFp8Rope, kSetupTreeDecode, kNumSetupKeys };
+                kSetupStoreFp8Rope, kSetupTreeDecode, kSetupTreeRows, kNumSetupKeys };
 bool setup_once(SetupKey key, bool (*setup)());
 
 // cuTensorMapEncodeTiled through the runtime's driver entry point.
@@ -220,6 +220,8 @@ pkv_status launch_sample_filtered(const SampleFilteredArgs& a, int* err, cudaStr
 
 // ---- trees of drafted tokens ------------------------------------------------------
 constexpr int kMaxTreeNodes = 256;
+constexpr int kMaxTreeBatch = 4096;
+constexpr int kTreeRows = 32;         // nodes x group of the trees that tree_decode_rows.cu takes
 constexpr int kMaxLayers = PKV_MAX_LAYERS;
 
 struct TreeDecodeArgs {
@@ -249,6 +251,10 @@ struct TreeDecodeArgs {
 };
 size_t tree_decode_workspace_bytes(int num_kv_heads);
 pkv_status launch_tree_decode(const TreeDecodeArgs& a, int* err, cudaStream_t stream);
+// Small trees on the 8-bit cache, to which launch_tree_decode hands over; lg = log2(num_heads / num_kv_heads).
+bool tree_rows_fits(const TreeDecodeArgs& a, int lg);
+size_t tree_rows_workspace_bytes(int num_kv_heads);
+pkv_status launch_tree_rows(const TreeDecodeArgs& a, int lg, int* err, cudaStream_t stream);
 
 struct TreeAcceptArgs {
     const int64_t* target;

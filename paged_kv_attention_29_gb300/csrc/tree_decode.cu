@@ -28,11 +28,7 @@
 // product with a weight of 0 would spread, are taken out of the tile and given back
 // to the rows that see them.
 //
-// Trees of 32 rows or fewer (nodes x G, bounded by max_nodes) take tiles of 32 rows that
-// lie in the query tile four times over: every warp of the softmax then has all rows'
-// scores in its own lanes, takes 16 of the tile's 64 keys, and leaves its weights in
-// shared memory for the product with V, which only the first 32 lanes' sums are read of.
-// With one warp at work on all 64 keys its chain of instructions set the time.
+// Trees of 32 rows or fewer on the 8-bit cache are another kernel's (tree_decode_rows.cu).
 //
 // Warps 0-3: softmax and epilogue (TMEM lanes 0-127).  bf16 cache: warp 4 TMA producer,
 // warp 5 TMEM allocation and MMA issue.  8-bit cache: warps 4-7 turn the codes that TMA
@@ -49,7 +45,6 @@ namespace {
 
 constexpr int D = kHeadDim;
 constexpr int ROWS = 128;                    // MMA M
-constexpr int SPLIT_ROWS = 32;               // rows of a split tile
 constexpr int KT = 64;                       // keys per tile
 constexpr int Q_HALF = ROWS * 64 * 2;        // 128B-swizzled box of 64 dims: 16 KiB of Q
 constexpr int KV_HALF = KT * 64 * 2;         // 8 KiB of K or V
@@ -66,16 +61,13 @@ constexpr int THREADS_BF16 = 192, THREADS_FP8 = 320;
 // Shared memory.  bf16: rings of 3 K and 2 V tiles (a K tile is asked for two steps before its product, a V tile's
 // product comes a step later).  8 bits: 3 tiles of K codes and 3 V tiles; the row scales of K as bytes and as floats, in
 // rings so long that those of a tile are read before K's copies come round again (K of tile t + 5 is asked for when
-// tile t is through); each query row's factor, of two segments.  Split tiles: the weights of 32 rows (of two tiles, where there is room), in front of the K
-// tiles: the product's other 96 rows of weights are whatever lies there, and their sums are not read.
-template <bool FP8, bool SPLIT>
+// tile t is through); each query row's factor, of two segments.
+template <bool FP8>
 struct Layout {
-    static constexpr int P_SLOTS = SPLIT ? (FP8 ? 2 : 1) : 0, P_TILE = SPLIT_ROWS * KT * 2;
-    static constexpr int K_SLOTS = SPLIT ? 2 : 3, V_SLOTS = FP8 ? 3 : 2, K_TILE = FP8 ? KT * D : KV_TILE, KS_SLOTS = 6;
-    static constexpr int Q = 0, P = 2 * Q_HALF, K = P + P_SLOTS * P_TILE, V = K + K_SLOTS * K_TILE, VS = V + V_SLOTS * KV_TILE, KS = VS + (FP8 ? V_SLOTS * KT : 0);
+    static constexpr int K_SLOTS = 3, V_SLOTS = FP8 ? 3 : 2, K_TILE = FP8 ? KT * D : KV_TILE, KS_SLOTS = 6;
+    static constexpr int Q = 0, K = 2 * Q_HALF, V = K + K_SLOTS * K_TILE, VS = V + V_SLOTS * KV_TILE, KS = VS + (FP8 ? V_SLOTS * KT : 0);
     static constexpr int KSF = KS + (FP8 ? KS_SLOTS * KT : 0), QS = KSF + (FP8 ? KS_SLOTS * KT * 4 : 0);
-    static constexpr int Q_ROWS = SPLIT ? SPLIT_ROWS : ROWS, EX = QS + (FP8 ? 2 * Q_ROWS * 4 : 0);      // what the four warps tell each other, two rounds of it
-    static constexpr int BAR = EX + (SPLIT ? 2 * 4 * 32 * 4 : 0);
+    static constexpr int BAR = QS + (FP8 ? 2 * ROWS * 4 : 0);
     static constexpr int KF = 0, KE = KF + K_SLOTS, VF = KE + K_SLOTS, VE = VF + V_SLOTS, QF = VE + V_SLOTS, QE = QF + 1, SF = QE + 1, PF = SF + 2,
                          PV = PF + 2, OF = PV + 2, OE = OF + 1, WG = OE + 1, DRAIN = WG + 1, BF16_BARS = DRAIN + 1;
     static constexpr int VRAW = BF16_BARS, KSB = VRAW + V_SLOTS, KSR = KSB + KS_SLOTS, QR = KSR + KS_SLOTS, QG = QR + 1, FP8_BARS = QG + 1;
@@ -84,7 +76,7 @@ struct Layout {
     static constexpr int WILD = MISC + 16;                        // [2][4 warps][8]: nodes with infinities or NaN in V
     static constexpr int SCAN = WILD + 2 * 4 * 8 * 4;             // 16 x int64: set-up sums; then the run's start
     static constexpr int BYTES = SCAN + 16 * 8;
-    static_assert(P % 1024 == 0 && K % 1024 == 0 && V % 1024 == 0 && KSF % 16 == 0 && BAR % 8 == 0, "operand tiles and vectors need their alignment");
+    static_assert(K % 1024 == 0 && V % 1024 == 0 && KSF % 16 == 0 && BAR % 8 == 0, "operand tiles and vectors need their alignment");
     static_assert(CTAS_PER_SM * (BYTES + 1024) <= 228 * 1024, "two CTAs share an SM's shared memory");
 };
 
@@ -103,7 +95,7 @@ struct Params {
     const uint16_t* v_cache;  // bf16 cache, for the values taken out of a tile
     int batch, max_blocks, num_heads, num_kv_heads, lg, block_size, num_blocks;
     int max_nodes, max_context, mask_words, total_nodes;
-    int qtok;                 // nodes of a tile: 128 / G, or 32 / G in split tiles
+    int qtok;                 // nodes of a tile: 128 / G
     float scale_log2;
     int* err;
 };
@@ -317,33 +309,6 @@ __device__ __forceinline__ void issue_pv_ts(uint32_t d, uint32_t p, uint64_t v, 
         : "memory");
 }
 
-// O (+)= P V, P in shared memory: `steps` (1 to 4) of 16 keys.
-__device__ __forceinline__ void issue_pv_ss(uint32_t d, uint64_t p, uint64_t v, uint32_t idesc, uint32_t accumulate, uint32_t steps) {
-    asm volatile(
-        "{\n\t"
-        ".reg .pred e, f, t;\n\t"
-        ".reg .b32 r;\n\t"
-        ".reg .b64 b, a;\n\t"
-        "elect.sync r|e, 0xffffffff;\n\t"
-        "setp.ne.u32 f, %4, 0;\n\t"
-        "setp.eq.u32 t, 0, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n\t"
-        "setp.gt.and.u32 e, %5, 1, e;\n\t"
-        "add.u64 a, %1, 2;\n\t"
-        "add.u64 b, %2, 128;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
-        "setp.gt.and.u32 e, %5, 2, e;\n\t"
-        "add.u64 a, %1, 4;\n\t"
-        "add.u64 b, %2, 256;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
-        "setp.gt.and.u32 e, %5, 3, e;\n\t"
-        "add.u64 a, %1, 6;\n\t"
-        "add.u64 b, %2, 384;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
-        "}" :: "r"(d), "l"(p), "l"(v), "r"(idesc), "r"(accumulate), "r"(steps)
-        : "memory");
-}
-
 // Arrive on two barriers, and on a third if it is not 0, once all products issued before are through.
 __device__ __forceinline__ void commit3(uint32_t a, uint32_t b, uint32_t c) {
     asm volatile(
@@ -493,14 +458,14 @@ __device__ __noinline__ void give_back(const Params& p, int seq, int n, int len,
     }
 }
 
-template <bool FP8, bool SPLIT>
+template <bool FP8>
 __global__ void __launch_bounds__(FP8 ? THREADS_FP8 : THREADS_BF16, CTAS_PER_SM)
 tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const Params p) {
     constexpr int THREADS = FP8 ? THREADS_FP8 : THREADS_BF16, LOAD_WARP = FP8 ? 9 : 4, MMA_WARP = FP8 ? 8 : 5;
     extern __shared__ __align__(1024) uint8_t gbase[];
     const uint32_t base = smem_u32(gbase);
-    using L = Layout<FP8, SPLIT>;
+    using L = Layout<FP8>;
     const uint32_t sQ = base + L::Q, bars = base + L::BAR;
     auto bar = [&](int i) { return bars + 8u * i; };
     uint32_t* misc = reinterpret_cast<uint32_t*>(gbase + L::MISC);
@@ -632,11 +597,8 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (segs >= 1 && !(ok = wait_phase(ctl, bar(L::QE), (segs - 1) & 1))) return;
                 mbar_arrive_expect_tx(bar(L::QF), 2 * Q_HALF);
                 const int row = w.s.q0 + w.rt * p.qtok, head = g << p.lg;
-#pragma unroll 1
-                for (int at = 0; at < Q_HALF; at += SPLIT ? SPLIT_ROWS * 128 : Q_HALF) {
-                    tma_load_3d(sQ + at, &tm_q, bar(L::QF), 0, head, row);
-                    tma_load_3d(sQ + Q_HALF + at, &tm_q, bar(L::QF), 64, head, row);
-                }
+                tma_load_3d(sQ, &tm_q, bar(L::QF), 0, head, row);
+                tma_load_3d(sQ + Q_HALF, &tm_q, bar(L::QF), 64, head, row);
                 ++segs;
             };
             // K of a tile, then V of the one before; a segment's queries behind the first K.  Tile j lies in logical
@@ -725,10 +687,10 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (!more) break;
             if (j == w.j0) {
                 if (!(ok = wait_warp(ctl, bar(L::QF), seg & 1))) break;
-                const int rows = SPLIT ? ROWS : w.tokens() << p.lg;
-                float* factors = reinterpret_cast<float*>(gbase + L::QS) + (seg & 1) * L::Q_ROWS;
+                const int rows = w.tokens() << p.lg;
+                float* factors = reinterpret_cast<float*>(gbase + L::QS) + (seg & 1) * ROWS;
 #pragma unroll 1
-                for (int r = (warp - 4) * 4 + (lane >> 3); r - (lane >> 3) < rows; r += 16) split_row(gbase + L::Q, r, lane & 7, factors + (r & (L::Q_ROWS - 1)));
+                for (int r = (warp - 4) * 4 + (lane >> 3); r - (lane >> 3) < rows; r += 16) split_row(gbase + L::Q, r, lane & 7, factors + r);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(L::QR));
@@ -788,10 +750,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (!(ok = wait_warp(ctl, bar(L::PF + (t & 1)), (t >> 1) & 1))) break;
             tc_fence_after();
             const uint64_t dv = smem_desc(base + L::V + slot * KV_TILE, KV_HALF, 1024, 2);
-            if constexpr (SPLIT)
-                issue_pv_ss(tmem + O_COL, smem_desc(base + L::P + (t % max(1, L::P_SLOTS)) * L::P_TILE, 16, 1024, 2), dv, idesc_pv, first_here ? 0u : 1u, (keys + 15) >> 4);
-            else
-                issue_pv_ts(tmem + O_COL, tmem + (t & 1) * KT, dv, idesc_pv, first_here ? 0u : 1u, (keys + 15) >> 4);
+            issue_pv_ts(tmem + O_COL, tmem + (t & 1) * KT, dv, idesc_pv, first_here ? 0u : 1u, (keys + 15) >> 4);
             commit3(bar(L::PV + (t & 1)), bar(L::VE + slot), last_here ? bar(L::OF) : 0u);
             if (end) break;
             if (last_here) w.next();
@@ -807,7 +766,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         tmem_dealloc(tmem, TMEM_COLS);
     } else {
         // ---------------------------------------------------------------- softmax and epilogue
-        const int row = SPLIT ? lane : tid;                   // of the tile
+        const int row = tid;                                  // TMEM lane
         const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
         const int qtok = p.qtok;
         int t = 0, seg = 0;
@@ -821,21 +780,11 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             ok = wait_warp(ctl, bar(L::WG), meets++ & 1u);
             return ok;
         };
-        uint32_t rounds = 0;
-        float told[4];
-        auto tell = [&](float x) {                            // every warp's x of this lane's row
-            float* ex = reinterpret_cast<float*>(gbase + L::EX) + (rounds++ & 1u) * 128;
-            ex[tid] = x;
-            if (!meet()) return false;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) told[i] = ex[32 * i + lane];
-            return true;
-        };
         for (; w.more() && ok; w.next(), ++seg) {
             const int tokens = w.tokens();
             const int tok = row >> p.lg;
             const bool live = tok < tokens;                   // rows behind are computed by nobody
-            const bool warp_live = SPLIT || (warp * 32) >> p.lg < tokens;
+            const bool warp_live = (warp * 32) >> p.lg < tokens;
             const int tree0 = w.s.len - w.s.n;                // position of the first node
             const int node_row = w.s.q0 + w.rt * qtok + tok;
             unsigned long long words[4];
@@ -847,7 +796,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (FP8) {
                 ok = wait_warp(ctl, bar(L::QG), seg & 1);
                 if (!ok) break;
-                sc *= reinterpret_cast<const float*>(gbase + L::QS)[(seg & 1) * L::Q_ROWS + row];
+                sc *= reinterpret_cast<const float*>(gbase + L::QS)[(seg & 1) * ROWS + row];
             }
             for (int j = w.j0; j < w.j1; ++j, ++t) {
                 const int keys = min(KT, w.s.len - j * KT), rel = j * KT - tree0;
@@ -865,21 +814,15 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     const unsigned long long see = tree ? visible(words, rel, keys) : ~0ull;
                     float mx0 = -INFINITY, mx1 = -INFINITY;
                     // bf16: all of S in registers.  8 bits: S is read twice, CH columns at a time, in rolled loops.
-                    // Split: the warp's 16 columns.
-                    constexpr int CH = FP8 || SPLIT ? 16 : KT, C_END = SPLIT ? CH : KT;
-                    const int own = SPLIT ? 16 * warp : 0;
+                    constexpr int CH = FP8 ? 16 : KT;
                     float s[CH];
                     auto read = [&](int c0) {
-                        if constexpr (CH == 16) {
+                        if constexpr (FP8) {
                             uint32_t r[16];
                             tmem_ld16(s_tmem + c0, r);
                             tmem_ld_wait();
-                            if (!FP8) {
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) s[e] = __uint_as_float(r[e]);
-                            }
-#pragma unroll
-                            for (int e = 0; FP8 && e < 16; e += 4) {
+                            for (int e = 0; e < 16; e += 4) {
                                 const float4 f = *reinterpret_cast<const float4*>(ksf + c0 + e);
                                 fmul2(s[e], s[e + 1], __uint_as_float(r[e]), __uint_as_float(r[e + 1]), f.x, f.y);
                                 fmul2(s[e + 2], s[e + 3], __uint_as_float(r[e + 2]), __uint_as_float(r[e + 3]), f.z, f.w);
@@ -900,19 +843,15 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         }
                     };
 #pragma unroll 1
-                    for (int c0 = 0; c0 < C_END; c0 += CH) {
-                        read(own + c0);
+                    for (int c0 = 0; c0 < KT; c0 += CH) {
+                        read(c0);
 #pragma unroll
                         for (int e = 0; e < CH; e += 4) {
                             mx0 = fmax3(mx0, s[e + 0], s[e + 1]);
                             mx1 = fmax3(mx1, s[e + 2], s[e + 3]);
                         }
                     }
-                    float m_new = fmaxf(mx0, mx1) * sc;
-                    if constexpr (SPLIT) {
-                        if (!tell(m_new)) break;
-                        m_new = fmaxf(fmaxf(told[0], told[1]), fmaxf(told[2], told[3]));
-                    }
+                    const float m_new = fmaxf(mx0, mx1) * sc;
                     if (j == w.j0) {
                         m_used = m_new;
                     } else if (__any_sync(0xffffffffu, m_new > m_used + kRescaleLog2)) {
@@ -923,7 +862,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         const float m_tgt = fmaxf(m_used, m_new);
                         const float alpha = m_tgt == m_used ? 1.f : ex2_ftz(m_used - m_tgt);
 #pragma unroll 1
-                        for (int cc = SPLIT && warp > 0 ? 4 : 0; cc < 4; ++cc) {
+                        for (int cc = 0; cc < 4; ++cc) {
                             uint32_t o[32];
                             tmem_ld32(tmem + lane_off + O_COL + 32 * cc, o);
                             tmem_ld_wait();
@@ -938,8 +877,8 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     const float neg_m = m_used == -INFINITY ? 0.f : -m_used;      // a row that has seen nothing yet
                     float r0 = 0.f, r1 = 0.f, r2 = 0.f, r3 = 0.f;
 #pragma unroll 1
-                    for (int c0 = 0; c0 < C_END; c0 += CH) {
-                        if (FP8 && !SPLIT) read(c0);
+                    for (int c0 = 0; c0 < KT; c0 += CH) {
+                        if (FP8) read(c0);
                         uint32_t pk[CH / 2];
 #pragma unroll
                         for (int e = 0; e < CH; e += 4) {
@@ -953,21 +892,13 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             pk[(e >> 1) + 1] = pack_bf16x2(p2, p3);
                         }
                         // P's columns end before the ones of S that are still to be read
-                        if constexpr (SPLIT) {
-                            // to shared memory, once the product with the weights that lie there is through
-                            if (t >= L::P_SLOTS && !(ok = wait_warp(ctl, bar(L::PV + ((t - L::P_SLOTS) & 1)), ((t - L::P_SLOTS) >> 1) & 1))) break;
-                            uint8_t* prow = gbase + L::P + (t % L::P_SLOTS) * L::P_TILE + lane * 128;
-                            *reinterpret_cast<uint4*>(prow + (((2 * warp) ^ (lane & 7)) * 16)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                            *reinterpret_cast<uint4*>(prow + (((2 * warp + 1) ^ (lane & 7)) * 16)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-                            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        } else if constexpr (FP8)
+                        if constexpr (FP8)
                             tmem_st8(s_tmem + c0 / 2, pk);
                         else
                             tmem_st32(s_tmem, pk);
                     }
-                    if (!ok) break;
                     l += (r0 + r1) + (r2 + r3);
-                    if (!SPLIT) tmem_st_wait();
+                    tmem_st_wait();
                 }
                 if (tree) {
                     // Infinities and NaN among the nodes' V rows leave the tile, and so does what the block holds
@@ -1010,13 +941,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             ok = wait_warp(ctl, bar(L::OF), seg & 1);
             if (!ok) break;
             tc_fence_after();
-            // every warp's bits are there; those of the segment before are read
-            if constexpr (SPLIT) {
-                if (!tell(l)) break;
-                l = (told[0] + told[1]) + (told[2] + told[3]);
-            } else if (had_tree && !meet()) {
-                break;
-            }
+            if (had_tree && !meet()) break;                   // every warp's bits are there; those of the segment before are read
             const bool whole = w.j0 == 0 && w.j1 == w.nt;
             const int part = w.j0 > 0 ? 0 : 1;                // 0: the unit began before this run, 1: it goes on behind it
             if (!whole && part == 1) {
@@ -1024,7 +949,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const long long end = t1 + (w.nt - w.j1);
                 meta = make_int4(static_cast<int>((end * C - 1) / W), w.s.q0 + w.rt * qtok, tokens, 0);
             }
-            if (SPLIT ? warp == 0 : warp_live) {
+            if (warp_live) {
                 if (had_tree) {
                     // what was taken out of the tiles, to the rows that see it
                     uint32_t any = 0u;
@@ -1126,13 +1051,13 @@ int64_t grid_of(int batch, int max_nodes, int max_context, int num_kv_heads, int
     return std::min<int64_t>(max_ctas(num_kv_heads), std::max<int64_t>(1, cost / MIN_RUN) * num_kv_heads);
 }
 
-template <bool FP8, bool SPLIT>
+template <bool FP8>
 bool allow_smem() {
-    return cudaFuncSetAttribute(tree_decode_kernel<FP8, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<FP8, SPLIT>::BYTES) == cudaSuccess;
+    return cudaFuncSetAttribute(tree_decode_kernel<FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<FP8>::BYTES) == cudaSuccess;
 }
-template <bool FP8, bool SPLIT>
+template <bool FP8>
 cudaError_t launch(int grid, cudaStream_t stream, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Params& p) {
-    tree_decode_kernel<FP8, SPLIT><<<grid, FP8 ? THREADS_FP8 : THREADS_BF16, Layout<FP8, SPLIT>::BYTES, stream>>>(tm_q, tm_k, tm_v, p);
+    tree_decode_kernel<FP8><<<grid, FP8 ? THREADS_FP8 : THREADS_BF16, Layout<FP8>::BYTES, stream>>>(tm_q, tm_k, tm_v, p);
     return cudaGetLastError();
 }
 
@@ -1140,19 +1065,19 @@ cudaError_t launch(int grid, cudaStream_t stream, const CUtensorMap& tm_q, const
 
 size_t tree_decode_workspace_bytes(int num_kv_heads) {
     const size_t ctas = static_cast<size_t>(max_ctas(num_kv_heads));
-    return align256(ctas * 2 * ROWS * D * 4) + align256(ctas * 2 * ROWS * 8) + align256(ctas * 16);
+    return std::max(align256(ctas * 2 * ROWS * D * 4) + align256(ctas * 2 * ROWS * 8) + align256(ctas * 16), tree_rows_workspace_bytes(num_kv_heads));
 }
 
 pkv_status launch_tree_decode(const TreeDecodeArgs& a, int* err, cudaStream_t stream) {
     const bool fp8 = a.k_scale != nullptr;
     const int lg = group_log2(a.num_heads, a.num_kv_heads);
     if (lg < 0) return PKV_ERR_UNSUPPORTED;
-    // by the bound, not by the trees: 32 rows or fewer in every tile
-    const bool split = (a.max_nodes << lg) <= SPLIT_ROWS;
-    const int qtok = (split ? SPLIT_ROWS : ROWS) >> lg;
+    const int qtok = ROWS >> lg;
     if (a.workspace == nullptr || a.workspace_bytes < tree_decode_workspace_bytes(a.num_kv_heads)) return PKV_ERR_WORKSPACE;
-    if (!setup_once(kSetupTreeDecode, [] { return allow_smem<false, false>() && allow_smem<false, true>() && allow_smem<true, false>() && allow_smem<true, true>(); }))
+    if (!setup_once(kSetupTreeDecode, [] { return allow_smem<false>() && allow_smem<true>(); }))
         return PKV_ERR_CUDA;
+    // by the bounds, not by the trees themselves
+    if (tree_rows_fits(a, lg)) return launch_tree_rows(a, lg, err, stream);
     CUtensorMap tm_q, tm_k, tm_v;
     {
         const uint64_t dims[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(a.num_heads), static_cast<uint64_t>(a.total_nodes)};
@@ -1205,9 +1130,7 @@ pkv_status launch_tree_decode(const TreeDecodeArgs& a, int* err, cudaStream_t st
     p.err = err;
     p.qtok = qtok;
     const int grid = static_cast<int>(grid_of(a.batch, a.max_nodes, a.max_context, a.num_kv_heads, qtok));
-    const cudaError_t first = fp8 ? (split ? launch<true, true>(grid, stream, tm_q, tm_k, tm_v, p) : launch<true, false>(grid, stream, tm_q, tm_k, tm_v, p))
-                                  : (split ? launch<false, true>(grid, stream, tm_q, tm_k, tm_v, p) : launch<false, false>(grid, stream, tm_q, tm_k, tm_v, p));
-    if (first != cudaSuccess) return PKV_ERR_CUDA;
+    if ((fp8 ? launch<true>(grid, stream, tm_q, tm_k, tm_v, p) : launch<false>(grid, stream, tm_q, tm_k, tm_v, p)) != cudaSuccess) return PKV_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid, JOIN_SPLIT);
     cfg.blockDim = dim3(JOIN_THREADS);
