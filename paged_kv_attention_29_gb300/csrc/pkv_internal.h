@@ -221,7 +221,7 @@ pkv_status launch_sample_filtered(const SampleFilteredArgs& a, int* err, cudaStr
 // ---- trees of drafted tokens ------------------------------------------------------
 constexpr int kMaxTreeNodes = 256;
 constexpr int kMaxTreeBatch = 4096;
-constexpr int kTreeRows = 32;         // nodes x group of the trees that tree_decode_rows.cu takes
+constexpr int kTreeRows = 16;         // nodes x group of the trees that tree_decode_rows.cu takes
 constexpr int kMaxLayers = PKV_MAX_LAYERS;
 
 struct TreeDecodeArgs {

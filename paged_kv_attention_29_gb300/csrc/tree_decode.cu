@@ -28,7 +28,7 @@
 // product with a weight of 0 would spread, are taken out of the tile and given back
 // to the rows that see them.
 //
-// Trees of 32 rows or fewer on the 8-bit cache are another kernel's (tree_decode_rows.cu).
+// Trees of 16 rows or fewer on the 8-bit cache are another kernel's (tree_decode_rows.cu).
 //
 // Warps 0-3: softmax and epilogue (TMEM lanes 0-127).  bf16 cache: warp 4 TMA producer,
 // warp 5 TMEM allocation and MMA issue.  8-bit cache: warps 4-7 turn the codes that TMA

@@ -1,4 +1,4 @@
-// Attention of small trees of drafted tokens over an 8-bit KV cache: no more than 32
+// Attention of small trees of drafted tokens over an 8-bit KV cache: no more than 16
 // rows (nodes x query heads of a KV head) to a sequence.
 //
 // For sequence b with n_b nodes, the last of its L_b keys, and KV head g, row r (node r / G,
@@ -7,17 +7,20 @@
 //   out_r = sum_j p_j 2^ev_j v_j,   p = softmax_j(scale 2^ek_j q_r . k_j)
 //
 // over the keys before the tree and the nodes that the node's mask names.  A key costs 258
-// bytes and 512 flops a row, so up to 32 rows the step is bound by HBM, if the codes are
-// turned into operands cheaply: both products run transposed on mma.m16n8k16 with the key
-// or value tile as the 16-row operand,
+// bytes and 512 flops a row, so the step is bound by HBM if the codes are turned into
+// operands cheaply.  Both products run transposed on mma.m16n8k16 with the key or value tile
+// as the 16-row operand,
 //
 //   S^T [16 keys x 8 rows] += K [16 x 16 dims] Q^T
 //   O^T [16 dims x 8 rows] += V^T [16 x 16 keys] P^T
 //
-// so that codes become f16 (exactly, two to an instruction) once for all NT = 1, 2 or 4
-// groups of 8 rows, in the registers of the warp that uses them.  (On tcgen05 the same trees
-// took 106 us against 57 at batch 64, 512 to 4096 keys: there the codes go through shared
-// memory as bf16, and a tile's steps, 64 keys at a time, wait on one another.)
+// so that codes become f16 (exactly, two to an instruction) once for all NT = 1 or 2 groups
+// of 8 rows, in the registers of the warp that uses them.
+//
+// Why 16 rows, measured at batch 64 with 512 to 4096 keys (8 KV heads): 8 rows 57 us, 16 rows
+// 75, against 112 on tcgen05 (tree_decode.cu) whatever the rows up to 32; 32 rows took 132 here, as
+// one warp with 255 registers or as two that share a stage: two or three warps a scheduler
+// do not hide the latencies of some 700 to 1100 instructions a chunk.
 //
 // Numbers as in the single-token kernel: a query row times a power of two is exact in f16
 // down to 2^-28 of its largest element; scores, their maximum m and the sum l are fp32; the
@@ -45,8 +48,6 @@ namespace {
 
 constexpr int D = kHeadDim;
 constexpr int CHUNK = 32;
-constexpr int WARPS = 8;
-constexpr int THREADS = WARPS * 32;
 constexpr int TILE_BYTES = CHUNK * D;
 constexpr int STAGE_BYTES = 2 * TILE_BYTES;  // K, V
 constexpr int SCALE_BYTES = 2 * CHUNK;       // K scales, V scales
@@ -55,13 +56,10 @@ constexpr float kTopT = 13.f;                // log2 of the largest weight, when
 constexpr float kMarginT = 15.f;             // and what moves it
 constexpr float kMarginM = 64.f;             // the same of the softmax terms, which move to 0
 
-// 32 rows: the query operand lies in shared memory (64 registers a lane beside O's 128 would be too many), in the place
-// of one of three stages.
-constexpr int stages(int nt) { return nt == 4 ? 2 : 3; }
-constexpr int q_bytes(int nt) { return nt == 4 ? nt * 16 * 32 * 4 : 0; }       // per warp
-constexpr size_t smem_bytes(int nt, int batch) {
-    return 1024 + WARPS * (stages(nt) * (STAGE_BYTES + SCALE_BYTES + 8) + q_bytes(nt)) + THREADS * 4 + static_cast<size_t>(batch + 1) * 4;
-}
+constexpr int WARPS = 8, THREADS = WARPS * 32, STAGES = 3;
+// shared memory: stages, then scales, a barrier for each stage, the running sums
+constexpr int SM_SCALES = WARPS * STAGES * STAGE_BYTES, SM_BARS = SM_SCALES + WARPS * STAGES * SCALE_BYTES, SM_SUMS = SM_BARS + WARPS * STAGES * 8;
+constexpr size_t smem_bytes(int batch) { return SM_SUMS + WARPS * 4 + static_cast<size_t>(batch + 1) * 4; }
 
 struct Params {
     const uint16_t* q;
@@ -142,37 +140,25 @@ __device__ __forceinline__ uint32_t ld_shared_u8(uint32_t addr) {
     return v;
 }
 
-// Which of a chunk's 32 keys a node sees: `first` is the node of the chunk's first key (negative before the tree), `keys`
-// the sequence's keys in the chunk.  mask: the node's words, nullptr for a row that is nobody's.
-__device__ __forceinline__ uint32_t visible(const unsigned long long* mask, int words, int first, int keys) {
-    uint32_t m = 0xffffffffu;
-    if (mask != nullptr) {
-        if (first < 0) {
-            const unsigned long long w = __ldg(mask);
-            m = first <= -CHUNK ? 0xffffffffu : (static_cast<uint32_t>(w) << -first) | ((1u << -first) - 1u);
-        } else {
-            const int i = first >> 6, sh = first & 63;
-            unsigned long long w = i < words ? __ldg(mask + i) >> sh : 0ull;
-            if (sh > 32 && i + 1 < words) w |= __ldg(mask + i + 1) << (64 - sh);
-            m = static_cast<uint32_t>(w);
-        }
-    }
+// Which of a chunk's 32 keys a row sees: w, its node's mask (no tree here has more than 32 nodes; all ones for a row that is
+// nobody's); `first` is the node of the chunk's first key (negative before the tree, above -32), `keys` the sequence's
+// keys in the chunk.
+__device__ __forceinline__ uint32_t visible(uint32_t w, int first, int keys) {
+    const uint32_t m = first < 0 ? (w << -first) | ((1u << -first) - 1u) : w >> first;
     return keys >= CHUNK ? m : m & ((1u << keys) - 1u);
 }
 
 __device__ __forceinline__ bool nan_codes(uint32_t w) { return (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0u; }
 
+// NT groups of 8 rows
 template <int NT>
 __global__ void __launch_bounds__(THREADS, 1)
 tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Params p) {
-    constexpr int STAGES = stages(NT), ROWS = 8 * NT;
+    constexpr int ROWS = 8 * NT;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ __align__(1024) uint8_t smem[];
-    uint8_t* q_all = smem + WARPS * STAGES * STAGE_BYTES;
-    uint8_t* scales = q_all + WARPS * q_bytes(NT);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(scales + WARPS * STAGES * SCALE_BYTES);
-    int32_t* tsum = reinterpret_cast<int32_t*>(bars + WARPS * STAGES);
-    int32_t* prefix = tsum + THREADS;
+    int32_t* tsum = reinterpret_cast<int32_t*>(smem + SM_SUMS);
+    int32_t* prefix = tsum + WARPS;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, hkv = p.num_kv_heads;
 
@@ -217,11 +203,9 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         if (lane == 0) p.meta[gw] = meta;
         return;
     }
-
     const uint32_t stage0 = smem_u32(smem) + warp * STAGES * STAGE_BYTES;
-    const uint32_t scale0 = smem_u32(scales) + warp * STAGES * SCALE_BYTES;
-    const uint32_t bar0 = smem_u32(bars + warp * STAGES);
-    uint32_t* q_mine = reinterpret_cast<uint32_t*>(q_all + warp * q_bytes(NT)) + 4 * lane;     // [group of 8 rows][4][lane][4]
+    const uint32_t scale0 = smem_u32(smem + SM_SCALES) + warp * STAGES * SCALE_BYTES;
+    const uint32_t bar0 = smem_u32(smem + SM_BARS) + warp * STAGES * 8;
     if (lane == 0) {
         for (int s = 0; s < STAGES; ++s) mbar_init(bar0 + 8 * s, 1);
         fence_barrier_init();
@@ -269,16 +253,22 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     const int g = lane >> 2, t = lane & 3;
     // swizzled 16-byte pieces: K row r (r % 8 = g): pieces 2t, 2t + 1; V row r: piece g
     const uint32_t k_piece0 = static_cast<uint32_t>(((2 * t) ^ g) << 4), k_piece1 = static_cast<uint32_t>(((2 * t + 1) ^ g) << 4);
-    uint32_t qb[NT == 4 ? 1 : NT][16];
+    uint32_t qb[NT][16];
     float qf[NT][2];
+    uint32_t mask[NT][2];            // of the rows of this lane's columns
     Seq s;
-    // The segment's query rows, f16, row 8 x + g of this lane's dims 32 t .. + 31, and for the rows 8 x + 2t, 8 x + 2t + 1 of
-    // its columns the factor that turns a raw product into log2-domain scores.
+    // The segment's query rows, f16, row 8 x + g of this lane's dims 32 t .. + 31, and for the rows 8 x + 2t and 8 x + 2t + 1
+    // of its columns the mask and the factor that turns a raw product into log2-domain scores.
     auto enter = [&]() {
         sequence(p, cc.b, s);
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
             const int r = 8 * x + g;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int col = 8 * x + 2 * t + h;
+                mask[x][h] = col < s.n << p.lg ? static_cast<uint32_t>(__ldg(p.mask + static_cast<int64_t>(s.q0 + (col >> p.lg)) * p.mask_words)) : 0xffffffffu;
+            }
             uint4 w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[i] = make_uint4(0, 0, 0, 0);
@@ -302,15 +292,8 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint32_t y[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-                uint32_t h[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) h[e] = pack_f16x2(bf16_lo(y[e]) * mul, bf16_hi(y[e]) * mul);
-                if (NT == 4) {
-                    *reinterpret_cast<uint4*>(q_mine + (4 * x + i) * 128) = make_uint4(h[0], h[1], h[2], h[3]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) qb[NT == 4 ? 0 : x][4 * i + e] = h[e];
-                }
+                for (int e = 0; e < 4; ++e) qb[x][4 * i + e] = pack_f16x2(bf16_lo(y[e]) * mul, bf16_hi(y[e]) * mul);
             }
             const float f = E == 255 ? mul : __uint_as_float(static_cast<uint32_t>(E - 14) << 23) * p.scale_log2;
             qf[x][0] = __shfl_sync(0xffffffffu, f, (lane & 3) * 8);        // row 2t sits in lanes 8t .. 8t + 3
@@ -355,20 +338,16 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 bool bad = false;
                 if (r < CHUNK) {
                     const uint32_t at = vb + r * D + (lane & 7) * 16;
-                    if (r >= valid) {
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
-                    } else {
-                        const uint4 c = ld_shared_v4(at);
+                    const uint4 c = ld_shared_v4(at);
+                    bad = r < valid && (nan_codes(c.x) || nan_codes(c.y) || nan_codes(c.z) || nan_codes(c.w));
+                    if (bad || r >= valid) {
                         uint32_t y[4] = {c.x, c.y, c.z, c.w};
-                        bad = nan_codes(c.x) || nan_codes(c.y) || nan_codes(c.z) || nan_codes(c.w);
-                        if (bad) {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
+                        for (int e = 0; e < 4; ++e)
 #pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    if ((y[e] >> (8 * i) & 0x7fu) == 0x7fu) y[e] &= ~(0xffu << (8 * i));
-                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
-                        }
+                            for (int i = 0; i < 4; ++i)
+                                if (r >= valid || (y[e] >> (8 * i) & 0x7fu) == 0x7fu) y[e] &= ~(0xffu << (8 * i));
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
                     }
                 }
                 hurt |= __reduce_or_sync(0xffffffffu, bad ? 1u << r : 0u);
@@ -389,18 +368,7 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 #pragma unroll
             for (int i = 0; i < 4; ++i) a[i] = ld_shared_v4(kb + (8 * i + g) * D + (half ? k_piece1 : k_piece0));
 #pragma unroll
-            for (int e2 = 0; e2 < 2; ++e2) {               // 8 dims: q words 4 (2 half + e2) ..
-                uint32_t q[NT][4];
-#pragma unroll
-                for (int x = 0; x < NT; ++x) {
-                    if (NT == 4) {
-                        const uint4 y = *reinterpret_cast<const uint4*>(q_mine + (4 * x + 2 * half + e2) * 128);
-                        q[x][0] = y.x, q[x][1] = y.y, q[x][2] = y.z, q[x][3] = y.w;
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) q[x][e] = qb[NT == 4 ? 0 : x][4 * (2 * half + e2) + e];
-                    }
-                }
+            for (int e2 = 0; e2 < 2; ++e2)                 // 8 dims: q words 4 (2 half + e2) ..
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -411,9 +379,8 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                         f16_of_codes(wu, a0, a2);
                         f16_of_codes(wv, a1, a3);
 #pragma unroll
-                        for (int x = 0; x < NT; ++x) mma_f16(c[x][i], a0, a1, a2, a3, q[x][2 * e], q[x][2 * e + 1]);
+                        for (int x = 0; x < NT; ++x) mma_f16(c[x][i], a0, a1, a2, a3, qb[x][8 * half + 4 * e2 + 2 * e], qb[x][8 * half + 4 * e2 + 2 * e + 1]);
                     }
-            }
         }
         // ---- weights, 8 rows at a time; this lane: keys g + 8 r, rows 8 x + 2t, 8 x + 2t + 1
         float kf[4], ev[4];
@@ -434,9 +401,7 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             if (tree) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int row = 8 * x + 2 * t + h;
-                    const bool live = row < s.n << p.lg;
-                    see[h] = visible(live ? p.mask + static_cast<int64_t>(s.q0 + (row >> p.lg)) * p.mask_words : nullptr, p.mask_words, first, valid) >> g;
+                    see[h] = visible(mask[x][h], first, valid) >> g;
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
                         if (!((see[h] >> (8 * r)) & 1u)) d[r][h] = -INFINITY;
@@ -544,9 +509,7 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 for (int x = 0; x < NT; ++x)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const int row = 8 * x + 2 * t + h;
-                        if (row >= s.n << p.lg) continue;
-                        const uint32_t see = visible(p.mask + static_cast<int64_t>(s.q0 + (row >> p.lg)) * p.mask_words, p.mask_words, first, valid);
+                        const uint32_t see = 8 * x + 2 * t + h < s.n << p.lg ? visible(mask[x][h], first, valid) : 0u;
                         if (!((see >> r) & 1u)) continue;
 #pragma unroll
                         for (int u = 0; u < 8; ++u) {
@@ -601,9 +564,7 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             if (k != n_mine - 1) {
                 cursor_next(cc, prefix, p.batch);
                 seg_begin = 0;
-                __syncwarp();
                 enter();
-                __syncwarp();
                 reset();
             }
         } else {
@@ -620,10 +581,9 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 }
 
 // The sequences that several runs share: CTA (run, head) joins the one that its run leaves open, a warp each row.
-template <int NT>
+template <int ROWS>
 __global__ void __launch_bounds__(256) tree_rows_join_kernel(const Params p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    constexpr int ROWS = 8 * NT;
     const int gw = blockIdx.x, hkv = p.num_kv_heads;
     const int4 u = p.meta[gw];
     if (u.x < 0) return;
@@ -672,14 +632,15 @@ int max_groups(int num_kv_heads) { return sm_count() * WARPS / num_kv_heads; }
 
 template <int NT>
 bool allow_smem() {
-    return cudaFuncSetAttribute(tree_rows_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem_bytes(NT, kMaxTreeBatch))) == cudaSuccess;
+    return cudaFuncSetAttribute(tree_rows_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem_bytes(kMaxTreeBatch))) == cudaSuccess;
 }
 
 template <int NT>
 cudaError_t launch_pair(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Params& p, cudaStream_t stream) {
     const int warps = p.groups * p.num_kv_heads;
-    tree_rows_kernel<NT><<<(warps + WARPS - 1) / WARPS, THREADS, smem_bytes(NT, p.batch), stream>>>(tm_k, tm_v, p);
-    if (cudaGetLastError() != cudaSuccess) return cudaErrorLaunchFailure;
+    tree_rows_kernel<NT><<<(warps + WARPS - 1) / WARPS, THREADS, smem_bytes(p.batch), stream>>>(tm_k, tm_v, p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(warps);
     cfg.blockDim = dim3(256);
@@ -689,7 +650,7 @@ cudaError_t launch_pair(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_rows_join_kernel<NT>, p);
+    return cudaLaunchKernelEx(&cfg, tree_rows_join_kernel<8 * NT>, p);
 }
 
 size_t part_slots(int num_kv_heads) { return static_cast<size_t>(2) * max_groups(num_kv_heads) * num_kv_heads; }
@@ -707,7 +668,7 @@ bool tree_rows_fits(const TreeDecodeArgs& a, int lg) {
 }
 
 pkv_status launch_tree_rows(const TreeDecodeArgs& a, int lg, int* err, cudaStream_t stream) {
-    if (!setup_once(kSetupTreeRows, [] { return allow_smem<1>() && allow_smem<2>() && allow_smem<4>(); })) return PKV_ERR_CUDA;
+    if (!setup_once(kSetupTreeRows, [] { return allow_smem<1>() && allow_smem<2>(); })) return PKV_ERR_CUDA;
     CUtensorMap tm_k, tm_v;
     const uint64_t dims[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(a.num_kv_heads), static_cast<uint64_t>(a.block_size),
                               static_cast<uint64_t>(a.num_blocks)};
@@ -751,9 +712,7 @@ pkv_status launch_tree_rows(const TreeDecodeArgs& a, int lg, int* err, cudaStrea
     // with it every rounding, does not depend on how tight the bounds are
     const int64_t chunks = static_cast<int64_t>(a.batch) * ((static_cast<int64_t>(a.max_context) + CHUNK - 1) / CHUNK);
     p.groups = static_cast<int>(std::min<int64_t>(max_groups(a.num_kv_heads), std::max<int64_t>(1, chunks / KMIN)));
-    const int rows = a.max_nodes << lg;
-    const cudaError_t e = rows <= 8 ? launch_pair<1>(tm_k, tm_v, p, stream) : rows <= 16 ? launch_pair<2>(tm_k, tm_v, p, stream)
-                                                                                           : launch_pair<4>(tm_k, tm_v, p, stream);
+    const cudaError_t e = a.max_nodes << lg <= 8 ? launch_pair<1>(tm_k, tm_v, p, stream) : launch_pair<2>(tm_k, tm_v, p, stream);
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
