@@ -552,14 +552,17 @@ PKV_API pkv_status pkv_sample_filtered_dev(const float *logits, int32_t batch, i
  *
  *   q, out  bf16 [total_nodes, num_heads, head_dim], packed in the order of cu_nodes;
  *           rows of out behind cu_nodes[batch] and of sequences left out stay as they are
+ *           (out may not overlap q)
  *   max_context_len  bound on context_lens (host-known)
  *   workspace  >= pkv_tree_decode_workspace_size(batch, max_nodes, num_heads, num_kv_heads,
  *           head_dim) bytes on the current device, 256-byte aligned, no initialisation needed,
  *           scratch after the call; calls that may overlap need one each
  * batch <= 4096.  fp32 scores and sums; a key's weight is rounded to bf16 for the product
  * with the values (2^-8 of itself at most), the output once to bf16.  Deterministic.
- * pkv_tree_decode_fp8 is the same over an 8-bit cache, bit for bit what pkv_tree_decode gives
- * over a bf16 cache that holds the values read (scale exponents >= -117).
+ * pkv_tree_decode_fp8 is the same over an 8-bit cache.  More than 16 rows to a KV head
+ * (max_nodes * num_heads / num_kv_heads): a query is split into two e4m3 parts, off by at most
+ * 2^-18 of the row's largest element, and weights are rounded to bf16 as above.  Up to 16: as
+ * pkv_decode_fp8, queries exact to 2^-28 of the row's largest element, weights rounded to f16.
  */
 PKV_API size_t pkv_tree_decode_workspace_size(int32_t batch, int32_t max_nodes, int32_t num_heads,
                                       int32_t num_kv_heads, int32_t head_dim);

@@ -732,6 +732,7 @@ pkv_status tree_decode_call(const pkv_bf16* q, const void* k_cache, const void* 
     if (batch == 0 || total_nodes == 0 || max_nodes == 0) return PKV_OK;
     if (!q || !k_cache || !v_cache || (fp8 && (!k_scale || !v_scale)) || !block_tables || !context_lens || !cu_nodes || !tree_mask || !out)
         return PKV_ERR_INVALID_ARG;
+    if (out == q) return PKV_ERR_INVALID_ARG;                  // other runs of a sequence read q when one is written
     if (misaligned16(q, out, k_cache, v_cache) || misaligned16(k_scale, v_scale)) return PKV_ERR_UNSUPPORTED;
     if (reinterpret_cast<uintptr_t>(workspace) & 255) return PKV_ERR_WORKSPACE;
     int* err = device_error_word();

@@ -854,8 +854,9 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     const float m_new = fmaxf(mx0, mx1) * sc;
                     if (j == w.j0) {
                         m_used = m_new;
-                    } else if (__any_sync(0xffffffffu, m_new > m_used + kRescaleLog2)) {
-                        // O is rescaled only when a maximum grows by 2^8; PV(t - 1) has to be through
+                    } else if (__any_sync(0xffffffffu, live && m_new > m_used + kRescaleLog2)) {
+                        // O is rescaled only when a maximum grows by 2^8 (of a row that is somebody's: what the others hold
+                        // may not decide when these are rounded); PV(t - 1) has to be through
                         ok = wait_warp(ctl, bar(L::PV + ((t - 1) & 1)), ((t - 1) >> 1) & 1);
                         if (!ok) break;
                         tc_fence_after();
@@ -1011,24 +1012,31 @@ __global__ void __launch_bounds__(JOIN_THREADS) tree_join_kernel(const float4* _
     if ((row >> lg) >= u.z) return;
     // the unit's first part is its run's second slot, all others are their runs' first
     auto slot = [&](int i) { return (static_cast<int64_t>(i) * num_kv_heads + g) * 2 + (i == c ? 1 : 0); };
-    float M = -INFINITY;
-#pragma unroll 4
-    for (int i = c; i <= u.x; ++i) M = fmaxf(M, part_ml[slot(i) * ROWS + row].x);
-    float l = 0.f, o[16];
+    // the maximum, the sum and the columns in one pass, two runs' loads at a time
+    float M = -INFINITY, l = 0.f, o[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[e] = 0.f;
-#pragma unroll 2
-    for (int i = c; i <= u.x; ++i) {
-        const float2 ml = part_ml[slot(i) * ROWS + row];
-        const float w = ml.x == M ? 1.f : ex2_ftz(ml.x - M);
-        l += ml.y * w;
+    for (int i0 = c; i0 <= u.x; i0 += 2) {
+        float2 ml[2];
+        float4 x[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int64_t at = slot(min(i0 + i, u.x));
+            ml[i] = i0 + i <= u.x ? part_ml[at * ROWS + row] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                x[i][k] = i0 + i <= u.x ? part_o[(at * 32 + c4 + k) * ROWS + row] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        const float now = fmax3(M, ml[0].x, ml[1].x), keep = M == now ? 1.f : ex2_ftz(M - now);
+        const float w0 = ml[0].x == now ? 1.f : ex2_ftz(ml[0].x - now), w1 = ml[1].x == now ? 1.f : ex2_ftz(ml[1].x - now);
+        M = now;
+        l = l * keep + ml[0].y * w0 + ml[1].y * w1;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const float4 x = part_o[(slot(i) * 32 + c4 + k) * ROWS + row];
-            o[4 * k] += x.x * w;
-            o[4 * k + 1] += x.y * w;
-            o[4 * k + 2] += x.z * w;
-            o[4 * k + 3] += x.w * w;
+            o[4 * k] = o[4 * k] * keep + x[0][k].x * w0 + x[1][k].x * w1;
+            o[4 * k + 1] = o[4 * k + 1] * keep + x[0][k].y * w0 + x[1][k].y * w1;
+            o[4 * k + 2] = o[4 * k + 2] * keep + x[0][k].z * w0 + x[1][k].z * w1;
+            o[4 * k + 3] = o[4 * k + 3] * keep + x[0][k].w * w0 + x[1][k].w * w1;
         }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;

@@ -128,6 +128,152 @@ def test_attention(pkv, name, hq, hkv, fp8):
     b.check(out)
 
 
+SMALL = {
+    "single nodes": ([1, 1, 1, 1, 1], [1, 31, 32, 33, 700]),
+    "chunk borders": ([2, 4, 3, 1, 4], [32, 64, 63, 65, 257]),
+    "no context": ([4, 1, 2], [4, 1, 2]),
+    "ragged": ([0, 3, 4, 0, 0, 1, 2], [5, 100, 36, 0, 40, 600, 255]),
+    "split over its length": ([3], [9001]),
+}
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "8 bits"])
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (4, 2), (8, 2), (16, 4), (6, 3)])
+@pytest.mark.parametrize("name", SMALL)
+def test_small_trees(pkv, name, hq, hkv, fp8):
+    """Up to 4 nodes: 4 to 16 rows."""
+    nodes, lens = SMALL[name]
+    b = Trees(nodes, lens, hq, hkv, seed=hq + hkv, fp8=fp8)
+    out = b.gpu(pkv)
+    expect_no_device_error(pkv)
+    b.check(out)
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "8 bits"])
+@pytest.mark.parametrize("most", [4, 8, 9, 16, 17, 32, 33])
+def test_results_do_not_depend_on_bounds(pkv, most, fp8):
+    """Loose bounds on the lengths give the same bits; a tree's rows do not depend on the rest of the batch's sizes."""
+    b = Trees([most, 2, most], [800, 2600, most + 1], 2, 2, seed=most, fp8=fp8)
+    tight = b.gpu(pkv)
+    assert torch.equal(tight, b.gpu(pkv, max_len=70000))
+    b.check(tight)
+
+
+@pytest.mark.parametrize("power", [-60, 0, 60])
+@pytest.mark.parametrize("nodes", [4, 12])
+def test_value_scales_far_apart_8_bits(pkv, nodes, power):
+    """Scales of V that differ by 2^80 from key to key: the large ones' rows are right, whatever the order they come in."""
+    b = Trees([nodes], [300], 2, 1, seed=3, fp8=True)
+    rng = np.random.default_rng(4)
+    owned = b.vs != 255
+    b.vs[owned] = 127 + power // 2 + rng.integers(-40, 41, int(owned.sum()))
+    b.v = torch.from_numpy(fc.read_pool(b.vc, b.vs)).bfloat16()
+    b.check(b.gpu(pkv))
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "8 bits"])
+@pytest.mark.parametrize("nodes", [4, 12, 40])
+@pytest.mark.parametrize("bad", [float("inf"), NAN])
+def test_bad_queries_stay_in_their_rows(pkv, bad, nodes, fp8):
+    b = Trees([nodes, 3], [500, 90], 4, 2, seed=6, fp8=fp8)
+    clean = b.gpu(pkv)
+    b.q[2, 1, 5] = bad
+    b.q[nodes + 1, 3] = bad
+    out = b.gpu(pkv)
+    hit = torch.zeros(nodes + 3, 4, dtype=torch.bool)
+    hit[2, 1] = hit[nodes + 1, 3] = True
+    assert torch.isnan(out[hit.cuda()]).all()
+    assert torch.equal(out[~hit.cuda()], clean[~hit.cuda()])
+
+
+def test_keys_first_seen_late(pkv):
+    """Rows that see nothing in the first tiles and then only keys with very low scores."""
+    n = 140
+    sees = np.zeros((n, n), bool)
+    sees[:, 100:] = np.random.default_rng(2).random((n, 40)) < 0.5
+    sees[7] = False
+    b = Trees([n], [n], 2, 1, seed=5, masks=[sees])
+    for i in range(100, n):
+        blk, off = b.at(0, i)
+        b.k[blk, off, 0] = -4 * b.q[7, 0]              # far below 0 for many rows
+    b.q[:] = b.q[7:8, :1]
+    out = b.gpu(pkv)
+    b.check(out)
+    assert not out[7].any()
+    c = Trees([4], [4], 2, 1, seed=5, masks=[np.array([[0, 0, 0, 1]] * 3 + [[0, 0, 0, 0]], bool)], fp8=True)
+    c.check(c.gpu(pkv))
+
+
+def test_codes_that_read_as_nan_8_bits(pkv):
+    """NaN codes of K and of V reach the rows that see them, on the kernels for few rows and for many."""
+    for nodes in (4, 30):
+        sees = np.tril(np.ones((nodes, nodes), bool))
+        sees[:, 1] = False
+        sees[[1, 3], 1] = True
+        b = Trees([nodes], [200], 4, 2, seed=8, masks=[sees], fp8=True)
+        clean = b.gpu(pkv)
+        blk, off = b.at(0, 200 - nodes + 1)
+        seen = torch.tensor([i in (1, 3) for i in range(nodes)]).cuda()
+        kept = b.vc[blk, off].copy()
+        b.vc[blk, off, :, 100] = 0xff
+        out = b.gpu(pkv)
+        others = torch.arange(D).cuda() != 100
+        assert torch.isnan(out[seen][..., 100]).all() and torch.equal(out[~seen], clean[~seen])
+        assert torch.equal(out[..., others], clean[..., others])
+        b.vc[blk, off] = kept
+        b.kc[blk, off, 0, 9] = 0x7f                    # KV head 0: query heads 0 and 1
+        out = b.gpu(pkv)
+        assert torch.isnan(out[seen][:, :2]).all() and torch.equal(out[~seen], clean[~seen]) and torch.equal(out[:, 2:], clean[:, 2:])
+        b.ks[blk, :, off] = 255                        # both heads' rows of K
+        out = b.gpu(pkv)
+        assert torch.isnan(out[seen]).all() and torch.equal(out[~seen], clean[~seen])
+
+
+def test_two_calls_at_once(pkv):
+    """Two streams, a workspace each."""
+    a, b = Trees([64, 40], [9000, 3000], 16, 8, seed=1), Trees([4, 3], [20000, 7000], 16, 8, seed=2, fp8=True)
+    wa, wb = a.gpu(pkv), b.gpu(pkv)
+    torch.cuda.synchronize()
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(3):
+        oa, ob = a.gpu(pkv, stream=sa), b.gpu(pkv, stream=sb)
+        torch.cuda.synchronize()
+        assert torch.equal(oa, wa) and torch.equal(ob, wb)
+
+
+def test_wrong_arguments(pkv):
+    b = Trees([4], [40], 4, 2, seed=1)
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    q, k, v = b.q.cuda(), b.k.cuda(), b.v.cuda()
+    tab, lens, cu, mask = dev(b.tables), torch.tensor(b.len, dtype=torch.int32).cuda(), dev(b.cu), dev(b.mask.view(np.int64))
+    call = lambda q=q, k=k, v=v, tab=tab, lens=lens, cu=cu, mask=mask, nodes=4, **kw: pkv.pkv_tree_decode(  # noqa: E731
+        q, k, v, tab, lens, cu, mask, nodes, 40, 0.1, **kw)
+    call()
+    for bad in ({"q": q.float()}, {"lens": lens.long()}, {"mask": mask.int()}):
+        with pytest.raises(TypeError):
+            call(**bad)
+    for bad in ({"q": q[:3]}, {"cu": cu[:1]}, {"mask": mask[:2]}, {"tab": tab.repeat(2, 1)}, {"v": v[:1]}, {"q": q.transpose(0, 1)},
+                {"out": torch.empty(5, 4, D, dtype=torch.bfloat16).cuda()}, {"mask": mask.cpu()}, {"q": q[..., :64].contiguous()}):
+        with pytest.raises(ValueError):
+            call(**bad)
+    for bad in ({"nodes": 65}, {"workspace": torch.empty(256, dtype=torch.uint8).cuda()}, {"out": q}):
+        with pytest.raises(pkv.PkvError):
+            call(**bad)
+    expect_no_device_error(pkv)
+    pool = lambda: torch.zeros(2, 256, 2, D, dtype=torch.bfloat16).cuda()  # noqa: E731
+    x = pool()
+    for k_list, v_list in (([x], [x]), ([x, x], [pool(), pool()]), ([x], [x[:1]]), ([x], [pool(), pool()]), ([pool(), pool()[:1]], [pool(), pool()])):
+        with pytest.raises(ValueError):
+            pkv.KvPools(k_list, v_list)
+    with pytest.raises(TypeError):
+        pkv.KvPools([x.half()], [pool()])
+    pools = pkv.KvPools([x], [pool()])
+    with pytest.raises(ValueError):
+        pkv.pkv_copy_blocks(pools, torch.zeros(2, dtype=torch.int32).cuda(), torch.zeros(1, dtype=torch.int32).cuda())
+    with pytest.raises(ValueError):
+        pkv.pkv_copy_blocks(pools, torch.zeros(1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
+
+
 @pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "8 bits"])
 def test_many_short_sequences(pkv, fp8):
     """More sequences than a CTA has threads, some of them empty; a run crosses many of them."""

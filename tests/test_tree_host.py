@@ -57,10 +57,11 @@ P = None
 X = ctypes.c_void_p(4096)        # non-null and aligned, never dereferenced: the checks return first
 
 
-def attend(lib, fp8=False, words=1, batch=2, total=10, nodes=9, ctx=100, hq=16, hkv=8, d=128, bs=256, nb=4, scale=0.1, ptr=P, width=4, ws=P):
+def attend(lib, fp8=False, words=1, batch=2, total=10, nodes=9, ctx=100, hq=16, hkv=8, d=128, bs=256, nb=4, scale=0.1, ptr=P, width=4, ws=P, out=None):
     pools = (ptr,) * (4 if fp8 else 2)
     fn = lib.pkv_tree_decode_fp8 if fp8 else lib.pkv_tree_decode
-    return fn(ptr, *pools, ptr, width, ptr, ptr, ptr, words, batch, total, nodes, ctx, hq, hkv, d, bs, nb, scale, ptr, ws, 0, P)
+    out = ctypes.c_void_p(ptr.value + 4096) if ptr is not P and out is None else ptr
+    return fn(ptr, *pools, ptr, width, ptr, ptr, ptr, words, batch, total, nodes, ctx, hq, hkv, d, bs, nb, scale, out, ws, 0, P)
 
 
 @pytest.mark.parametrize("fp8", [False, True])
@@ -73,6 +74,7 @@ def test_attention_refuses(lib, fp8):
                 {"width": 1 << 23, "bs": 256}, {"ptr": ctypes.c_void_p(4104)}):
         assert attend(lib, fp8, **{"ptr": X, **bad}) == 2, bad
     assert attend(lib, fp8, ptr=X, ws=ctypes.c_void_p(4096 + 128)) == 3
+    assert attend(lib, fp8, ptr=X, out=X) == 1                     # in place
     for none in ({"batch": 0}, {"total": 0}, {"nodes": 0}):
         assert attend(lib, fp8, **none) == 0, none
 
