@@ -74,7 +74,7 @@ struct Layout {
     static constexpr int NUM_BARS = FP8 ? FP8_BARS : BF16_BARS;
     static constexpr int MISC = (BAR + NUM_BARS * 8 + 15) & ~15;  // [0] TMEM base, [1] abort
     static constexpr int WILD = MISC + 16;                        // [2][4 warps][8]: nodes with infinities or NaN in V
-    static constexpr int SCAN = WILD + 2 * 4 * 8 * 4;             // 16 x int64: set-up sums; then the run's start
+    static constexpr int SCAN = WILD + 2 * 4 * 8 * 4;             // 16 x int64: set-up sums; what the run is; its start
     static constexpr int BYTES = SCAN + 16 * 8;
     static_assert(K % 1024 == 0 && V % 1024 == 0 && KSF % 16 == 0 && BAR % 8 == 0, "operand tiles and vectors need their alignment");
     static_assert(CTAS_PER_SM * (BYTES + 1024) <= 228 * 1024, "two CTAs share an SM's shared memory");
@@ -88,7 +88,7 @@ struct Params {
     uint16_t* out;
     float4* part_o;           // [CTA][2][32][128]: four columns of each row
     float2* part_ml;          // [CTA][2][128]: maximum (log2) and sum
-    int4* meta;               // [CTA]: {last run of the unit that continues behind this one's or -1, first row's node, nodes, 0}
+    int4* meta;               // [CTA]: {last run of the unit that continues behind this one's or -1, first row's node, nodes, CTAs of a run}
     const uint8_t* v_codes;   // 8-bit cache, for the values taken out of a tile
     const uint8_t* k_scale;
     const uint8_t* v_scale;
@@ -150,37 +150,34 @@ __device__ __forceinline__ Seq sequence(const Params& p, int b) {
     s.n = fits ? static_cast<int>(n) : 0;
     return s;
 }
-__device__ __forceinline__ long long cost_of(const Params& p, const Seq& s) {
-    return s.n ? static_cast<long long>((s.len + KT - 1) / KT + UNIT_COST) * ((s.n + p.qtok - 1) / p.qtok) : 0;
-}
+__device__ __forceinline__ int tiles_of(const Params& p, const Seq& s) { return (s.n + p.qtok - 1) / p.qtok; }      // of rows
+__device__ __forceinline__ int cost_of(const Seq& s) { return s.n ? (s.len + KT - 1) / KT + UNIT_COST : 0; }           // of each
 
 // A CTA's run, segment by segment: tiles [j0, j1) of the unit (sequence b, row tile rt).  Runs are cut in
 // cost: a unit is UNIT_COST steps without a tile and then a step per tile.  Every role walks by itself.
+// only: the one row tile of each sequence that is walked, or -1 for all of them.
 struct Walk {
     const Params& p;
     Seq s;
-    int b, rt, nt, nrt, j0, j1;
+    int b, rt, j0, j1, only;
     long long left;                          // cost of the run behind this segment
 
-    __device__ __forceinline__ Walk(const Params& params, int b0, long long off, long long count) : p(params), b(b0) {
-        rt = j0 = j1 = nt = nrt = 0;
-        left = count;
-        if (count <= 0) return;
-        enter();
-        const int per = nt + UNIT_COST;
-        rt = static_cast<int>(off / per);
-        const int at = static_cast<int>(off - static_cast<long long>(rt) * per);
+    __device__ __forceinline__ Walk(const Params& params, int b0, long long off, long long cost, int only_rt) : p(params), b(b0), only(only_rt) {
+        j0 = j1 = 0;
+        rt = max(0, only);
+        left = cost;
+        if (cost <= 0) return;
+        s = sequence(p, b);
+        const int per = nt() + UNIT_COST, before = static_cast<int>(off / per);
+        const int at = static_cast<int>(off - static_cast<long long>(before) * per);
+        rt += before;                        // 0 where one row tile is walked
         j0 = max(0, at - UNIT_COST);
         clip(max(0, UNIT_COST - at));
         if (j0 == j1) next();                // nothing of the last unit's steps but its first ones
     }
-    __device__ __forceinline__ void enter() {
-        s = sequence(p, b);
-        nt = (s.len + KT - 1) / KT;
-        nrt = (s.n + p.qtok - 1) / p.qtok;
-    }
+    __device__ __forceinline__ int nt() const { return (s.len + KT - 1) / KT; }        // tiles of the unit
     __device__ __forceinline__ void clip(int before) {
-        j1 = static_cast<int>(min(static_cast<long long>(nt), max(static_cast<long long>(j0), j0 + left - before)));
+        j1 = static_cast<int>(min(static_cast<long long>(nt()), max(static_cast<long long>(j0), j0 + left - before)));
         left -= before + (j1 - j0);
     }
     __device__ __forceinline__ bool last() const { return left <= UNIT_COST; }     // no tile of this run lies behind this segment
@@ -188,11 +185,11 @@ struct Walk {
     __device__ __forceinline__ void next() {
         j1 = j0 = 0;
         if (last()) return;
-        if (++rt == nrt) {
-            rt = 0;
+        if (only >= 0 || ++rt == tiles_of(p, s)) {
+            rt = max(0, only);
             do {
                 if (++b >= p.batch) return;
-                enter();
+                s = sequence(p, b);
             } while (s.n == 0);
         }
         clip(UNIT_COST);
@@ -512,20 +509,45 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         return before + v;
     };
-    long long mine = 0, first = 0;
+    // Sums over the sequences of a row tile's cost, alone (x) and times the row tiles (y).  Where every sequence has the same
+    // number of row tiles, more than one, they are taken side by side like the KV heads, by neighbouring CTAs: what one
+    // reads from memory the other finds in L2 (33 to 64 nodes of 4 heads, batch of 32: 403 MB read one after the other).
+    long long x = 0, y = 0, x_first = 0, y_first = 0;
+    int least = 0x7fffffff, most = 0;
 #pragma unroll 1
     for (int b = tid; b < p.batch; b += THREADS) {
         const Seq s = sequence(p, b);
         if (s.bad && blockIdx.x == 0) complain(p.err, PKV_DEVERR_SEQLENS, b);
-        const long long t = cost_of(p, s);
-        if (b < THREADS) first = t;
-        mine += t;
+        const long long cost = cost_of(s);
+        const int tiles = tiles_of(p, s);
+        if (tiles > 0) {
+            least = min(least, tiles);
+            most = max(most, tiles);
+        }
+        if (b < THREADS) {
+            x_first = cost;
+            y_first = cost * tiles;
+        }
+        x += cost;
+        y += cost * tiles;
     }
-    long long W;
-    long long upto = block_scan(mine, W);
-    const long long C = max(1ll, min(static_cast<long long>(gridDim.x / p.num_kv_heads), W / MIN_RUN));
-    const long long c = blockIdx.x / p.num_kv_heads;
-    const int g = static_cast<int>(blockIdx.x - c * p.num_kv_heads);
+    long long W, Wx;
+    long long upto = block_scan(y, W);
+    int rts = 1;                                              // row tiles side by side
+    if (p.max_nodes > p.qtok) {
+        const long long upto_x = block_scan(x, Wx);
+        const int r = Wx > 0 ? static_cast<int>(W / Wx) : 1;
+        if (r > 1 && static_cast<int>(gridDim.x) >= r * p.num_kv_heads && __syncthreads_and(most == 0 || (least == r && most == r))) {
+            rts = r;
+            W = Wx;
+            upto = upto_x;
+        }
+    }
+    const int lanes = rts * p.num_kv_heads;                   // CTAs that walk the same run
+    const long long C = max(1ll, min(static_cast<long long>(gridDim.x / lanes), W / MIN_RUN));
+    const long long c = blockIdx.x / lanes;
+    const int rt_mine = static_cast<int>(blockIdx.x - c * lanes) / p.num_kv_heads;
+    const int g = static_cast<int>(blockIdx.x - c * lanes) - rt_mine * p.num_kv_heads;
     const long long t0 = c < C ? c * W / C : 0, t1 = c < C ? (c + 1) * W / C : 0;
     if (t1 > t0) {
         long long before = 0;
@@ -534,9 +556,12 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const int b = base_b + tid;
             long long v = 0, total = W;
             if (p.batch <= THREADS) {
-                v = first;                                   // one block: its sums are known
+                v = rts > 1 ? x_first : y_first;             // one block: its sums are known
             } else {
-                if (b < p.batch) v = cost_of(p, sequence(p, b));
+                if (b < p.batch) {
+                    const Seq s = sequence(p, b);
+                    v = static_cast<long long>(cost_of(s)) * (rts > 1 ? 1 : tiles_of(p, s));
+                }
                 upto = block_scan(v, total);
             }
             const long long at = before + upto;
@@ -548,12 +573,18 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (before > t0) break;
         }
     }
+    if (tid == 0) {                                           // what the end of a unit asks for, out of the registers until then
+        scan[10] = lanes;
+        scan[11] = t1;
+        scan[12] = C;
+        scan[13] = W;
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = misc[0];
     const bool busy = t1 > t0;
-    Walk w(p, busy ? static_cast<int>(scan[14]) : 0, busy ? scan[15] : 0, t1 - t0);
+    Walk w(p, busy ? static_cast<int>(scan[14]) : 0, busy ? scan[15] : 0, t1 - t0, rts > 1 ? rt_mine : -1);
 
     if (warp == LOAD_WARP) {
         // ---------------------------------------------------------------- TMA producer
@@ -943,12 +974,12 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (!ok) break;
             tc_fence_after();
             if (had_tree && !meet()) break;                   // every warp's bits are there; those of the segment before are read
-            const bool whole = w.j0 == 0 && w.j1 == w.nt;
+            const bool whole = w.j0 == 0 && w.j1 == w.nt();
             const int part = w.j0 > 0 ? 0 : 1;                // 0: the unit began before this run, 1: it goes on behind it
             if (!whole && part == 1) {
                 // its last run: that of the unit's last tile, which lies nt - j1 steps behind this run's end
-                const long long end = t1 + (w.nt - w.j1);
-                meta = make_int4(static_cast<int>((end * C - 1) / W), w.s.q0 + w.rt * qtok, tokens, 0);
+                const long long end = scan[11] + (w.nt() - w.j1);
+                meta = make_int4(static_cast<int>((end * scan[12] - 1) / scan[13]), w.s.q0 + w.rt * qtok, tokens, static_cast<int>(scan[10]));
             }
             if (warp_live) {
                 if (had_tree) {
@@ -1007,11 +1038,11 @@ __global__ void __launch_bounds__(JOIN_THREADS) tree_join_kernel(const float4* _
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 u = meta[blockIdx.x];
     if (u.x < 0) return;
-    const int c = blockIdx.x / num_kv_heads, g = blockIdx.x - c * num_kv_heads;
+    const int lanes = u.w, c = blockIdx.x / lanes, in_run = blockIdx.x - c * lanes, g = in_run % num_kv_heads;
     const int row = threadIdx.x & (ROWS - 1), c4 = (blockIdx.y * 2 + (threadIdx.x >> 7)) * 4;
     if ((row >> lg) >= u.z) return;
     // the unit's first part is its run's second slot, all others are their runs' first
-    auto slot = [&](int i) { return (static_cast<int64_t>(i) * num_kv_heads + g) * 2 + (i == c ? 1 : 0); };
+    auto slot = [&](int i) { return (static_cast<int64_t>(i) * lanes + in_run) * 2 + (i == c ? 1 : 0); };
     // the maximum, the sum and the columns in one pass, two runs' loads at a time
     float M = -INFINITY, l = 0.f, o[16];
 #pragma unroll
