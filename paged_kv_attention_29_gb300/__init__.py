@@ -884,6 +884,7 @@ def pkv_check_wait_timeout(stream=None) -> None:
 
 MAX_TREE_NODES = 256
 MAX_LAYERS = 128
+_empty, _empty_like, _i32, _i64 = torch.empty, torch.empty_like, torch.int32, torch.int64
 
 
 def pkv_tree_decode_workspace_size(batch: int, max_nodes: int, num_heads: int, num_kv_heads: int, head_dim: int) -> int:
@@ -981,35 +982,29 @@ def pkv_tree_accept(target: torch.Tensor, draft: torch.Tensor, tree_mask: torch.
     max_path = int(max_path)
     if max_path < 1:
         raise ValueError("max_path must be at least 1")
-    dev = target.device
-    if path is None:
-        path = _allocated(stream, torch.empty, (batch, max_path), dtype=torch.int32, device=dev, result=True)
+    if path is None and path_lens is None and next_tokens is None and new_context_lens is None and stream is None:
+        dev = target.device          # what most calls are, at the cost of four allocations and nothing else
+        path, path_lens = _empty((batch, max_path), dtype=_i32, device=dev), _empty_like(context_lens)
+        next_tokens, new_context_lens = _empty(batch, dtype=_i64, device=dev), _empty_like(context_lens)
     else:
-        _shaped(path, "path", torch.int32, (batch, max_path))
-    if path_lens is None:
-        path_lens = _allocated(stream, torch.empty_like, context_lens, result=True)
-    else:
-        _shaped(path_lens, "path_lens", torch.int32, (batch,))
-    if next_tokens is None:
-        next_tokens = _allocated(stream, torch.empty, batch, dtype=torch.int64, device=dev, result=True)
-    else:
-        _shaped(next_tokens, "next_tokens", torch.int64, (batch,))
-    if new_context_lens is None:
-        new_context_lens = _allocated(stream, torch.empty_like, context_lens, result=True)
-    else:
-        _shaped(new_context_lens, "new_context_lens", torch.int32, (batch,))
+        outs = []
+        for name, t, dtype, shape in (("path", path, _i32, (batch, max_path)), ("path_lens", path_lens, _i32, (batch,)),
+                                      ("next_tokens", next_tokens, _i64, (batch,)),
+                                      ("new_context_lens", new_context_lens, _i32, (batch,))):
+            if t is None:
+                t = _allocated(stream, _empty, shape, dtype=dtype, device=target.device, result=True)
+            else:
+                _want(t, name, dtype, len(shape))
+                if t.shape != shape:
+                    raise ValueError(f"{name} must be {list(shape)}")
+            outs.append(t)
+        path, path_lens, next_tokens, new_context_lens = outs
     _launch("pkv_tree_accept", load().pkv_tree_accept, stream,
             (target, draft, tree_mask, cu_nodes, context_lens, path, path_lens, next_tokens, new_context_lens),
             (target.data_ptr(), draft.data_ptr(), tree_mask.data_ptr(), words, cu_nodes.data_ptr(),
              context_lens.data_ptr(), batch, total, int(max_nodes), max_path, path.data_ptr(), path_lens.data_ptr(),
              next_tokens.data_ptr(), new_context_lens.data_ptr()))
     return path, path_lens, next_tokens, new_context_lens
-
-
-def _shaped(t, name, dtype, shape):
-    _want(t, name, dtype, len(shape))
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}")
 
 
 class KvPools:
