@@ -212,8 +212,8 @@ struct Walk {
     }
 };
 
-// A tile's products, issued by one elected lane in one piece: chosen once for all of them, with the descriptors advanced by
-// constants, an instruction costs the issuing warp what it should, where a loop of single ones took 130 cycles each.
+// A tile's products, issued by one elected lane in one piece: with the descriptors advanced by constants (1% of a call against an
+// election for each).
 // S = Q K^T, bf16: 8 steps of 16 dims, 64 dims to a half of each tile.
 __device__ __forceinline__ void issue_qk_bf16(uint32_t d, uint64_t q, uint64_t k, uint32_t idesc) {
     static_assert(Q_HALF >> 4 == 1024 && KV_HALF >> 4 == 512, "offsets below");
