@@ -884,7 +884,7 @@ def pkv_check_wait_timeout(stream=None) -> None:
 
 MAX_TREE_NODES = 256
 MAX_LAYERS = 128
-_empty, _empty_like, _i32, _i64 = torch.empty, torch.empty_like, torch.int32, torch.int64
+_empty, _empty_like, _i32, _i64, _bf16 = torch.empty, torch.empty_like, torch.int32, torch.int64, torch.bfloat16
 
 
 def pkv_tree_decode_workspace_size(batch: int, max_nodes: int, num_heads: int, num_kv_heads: int, head_dim: int) -> int:
@@ -905,19 +905,26 @@ def tree_decode_workspace(batch: int, max_nodes: int, num_heads: int, num_kv_hea
 def _tree_call(name, fn, pools, shape, q, block_tables, context_lens, cu_nodes, tree_mask, max_nodes, max_context_len,
                softmax_scale, out, workspace, stream):
     nb, bs, hkv, d = shape
-    _want(q, "q", torch.bfloat16, 3)
-    _want(block_tables, "block_tables", torch.int32, 2)
-    _want(context_lens, "context_lens", torch.int32, 1)
-    _want(cu_nodes, "cu_nodes", torch.int32, 1)
-    _want(tree_mask, "tree_mask", torch.int64, 2)
+    # one expression when all is well; else tensor by tensor, for the message
+    if not (type(q) is type(block_tables) is type(context_lens) is type(cu_nodes) is type(tree_mask) is _Tensor
+            and q.dtype is _bf16 and q.ndim == 3 and q.is_cuda and q.is_contiguous()
+            and block_tables.dtype is _i32 and block_tables.ndim == 2 and block_tables.is_contiguous()
+            and context_lens.dtype is _i32 and context_lens.ndim == 1 and context_lens.is_contiguous()
+            and cu_nodes.dtype is _i32 and cu_nodes.ndim == 1 and cu_nodes.is_contiguous()
+            and tree_mask.dtype is _i64 and tree_mask.ndim == 2 and tree_mask.is_contiguous()):
+        _check(q, "q", _bf16, 3)
+        _want(block_tables, "block_tables", _i32, 2)
+        _want(context_lens, "context_lens", _i32, 1)
+        _want(cu_nodes, "cu_nodes", _i32, 1)
+        _want(tree_mask, "tree_mask", _i64, 2)
     total, hq, dq = q.shape
-    batch = context_lens.shape[0]
-    if dq != d or block_tables.shape[0] != batch or cu_nodes.shape[0] != batch + 1 or tree_mask.shape[0] != total:
+    (batch,), (tables, width), (rows, words) = context_lens.shape, block_tables.shape, tree_mask.shape
+    if dq != d or tables != batch or cu_nodes.shape[0] != batch + 1 or rows != total:
         raise ValueError("q, block_tables, context_lens, cu_nodes and tree_mask disagree")
     if out is None:
-        out = _allocated(stream, torch.empty_like, q, result=True)
+        out = _allocated(stream, _empty_like, q, result=True)
     else:
-        _want(out, "out", torch.bfloat16, 3)
+        _want(out, "out", _bf16, 3)
         if out.shape != q.shape:
             raise ValueError("out must have q's shape")
     if workspace is None:
@@ -925,10 +932,9 @@ def _tree_call(name, fn, pools, shape, q, block_tables, context_lens, cu_nodes, 
     else:
         _want(workspace, "workspace", torch.uint8, 1)
     _launch(name, fn, stream, (q, *pools, block_tables, context_lens, cu_nodes, tree_mask, out, workspace),
-            (q.data_ptr(), *[t.data_ptr() for t in pools], block_tables.data_ptr(), block_tables.shape[1],
-             context_lens.data_ptr(), cu_nodes.data_ptr(), tree_mask.data_ptr(), tree_mask.shape[1], batch, total,
-             int(max_nodes), int(max_context_len), hq, hkv, d, bs, nb, float(softmax_scale), out.data_ptr(),
-             workspace.data_ptr(), workspace.numel()))
+            (q.data_ptr(), *[t.data_ptr() for t in pools], block_tables.data_ptr(), width, context_lens.data_ptr(),
+             cu_nodes.data_ptr(), tree_mask.data_ptr(), words, batch, total, int(max_nodes), int(max_context_len), hq,
+             hkv, d, bs, nb, float(softmax_scale), out.data_ptr(), workspace.data_ptr(), workspace.numel()))
     return out
 
 
@@ -941,8 +947,8 @@ def pkv_tree_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     q [total_nodes, num_heads, 128] holds the nodes of all sequences, ``cu_nodes`` (int32 [batch + 1]) apart;
     ``tree_mask`` (int64 [total_nodes, words]) has bit j of a node set where it sees node j of its own tree.
     Rows behind cu_nodes[-1] are left as they were in ``out``."""
-    _check(k_cache, "k_cache", torch.bfloat16, 4)
-    _want(v_cache, "v_cache", torch.bfloat16, 4)
+    _want(k_cache, "k_cache", _bf16, 4)
+    _want(v_cache, "v_cache", _bf16, 4)
     if v_cache.shape != k_cache.shape:
         raise ValueError("k_cache and v_cache shapes differ")
     return _tree_call("pkv_tree_decode", load().pkv_tree_decode, (k_cache, v_cache), k_cache.shape, q, block_tables,
