@@ -219,6 +219,21 @@ struct SampleFilteredArgs {
 pkv_status launch_sample_filtered(const SampleFilteredArgs& a, int* err, cudaStream_t stream);
 
 // ---- trees of drafted tokens ------------------------------------------------------
+// A launch that may start before the kernel in front of it has ended (the kernel waits with griddepcontrol.wait before it
+// touches global memory); attr has to live until the launch.
+inline cudaLaunchConfig_t programmatic(dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, cudaLaunchAttribute* attr) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
 constexpr int kMaxTreeNodes = 256;
 constexpr int kMaxTreeBatch = 4096;
 constexpr int kTreeRows = 16;         // nodes x group of the trees that tree_decode_rows.cu takes

@@ -495,6 +495,8 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         tmem_alloc(base + L::MISC, TMEM_COLS);
         tmem_relinquish();
     }
+    // everything above overlaps the kernel before this one; global memory is read and written from here on
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     // The run: all tiles are counted, then the sequence in which this CTA's share starts is searched, a
     // block of sequences at a time.
     constexpr int WARPS = THREADS / 32;
@@ -1043,6 +1045,7 @@ constexpr int JOIN_THREADS = 2 * ROWS, JOIN_SPLIT = 4;
 __global__ void __launch_bounds__(JOIN_THREADS) tree_join_kernel(const float4* __restrict__ part_o, const float2* __restrict__ part_ml,
                                                                  const int4* __restrict__ meta, uint16_t* __restrict__ out, int num_heads, int num_kv_heads,
                                                                  int lg) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 u = meta[blockIdx.x];
     if (u.x < 0) return;
@@ -1104,8 +1107,9 @@ bool allow_smem() {
 }
 template <bool FP8>
 cudaError_t launch(int grid, cudaStream_t stream, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Params& p) {
-    tree_decode_kernel<FP8><<<grid, FP8 ? THREADS_FP8 : THREADS_BF16, Layout<FP8>::BYTES, stream>>>(tm_q, tm_k, tm_v, p);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = programmatic(dim3(grid), FP8 ? THREADS_FP8 : THREADS_BF16, Layout<FP8>::BYTES, stream, attr);
+    return cudaLaunchKernelEx(&cfg, tree_decode_kernel<FP8>, tm_q, tm_k, tm_v, p);
 }
 
 }  // namespace
@@ -1178,15 +1182,8 @@ pkv_status launch_tree_decode(const TreeDecodeArgs& a, int* err, cudaStream_t st
     p.qtok = qtok;
     const int grid = static_cast<int>(grid_of(a.batch, a.max_nodes, a.max_context, a.num_kv_heads, qtok));
     if ((fp8 ? launch<true>(grid, stream, tm_q, tm_k, tm_v, p) : launch<false>(grid, stream, tm_q, tm_k, tm_v, p)) != cudaSuccess) return PKV_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, JOIN_SPLIT);
-    cfg.blockDim = dim3(JOIN_THREADS);
-    cfg.stream = stream;
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    const cudaLaunchConfig_t cfg = programmatic(dim3(grid, JOIN_SPLIT), JOIN_THREADS, 0, stream, attr);
     const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_join_kernel, static_cast<const float4*>(p.part_o), static_cast<const float2*>(p.part_ml),
                                              static_cast<const int4*>(p.meta), a.out, a.num_heads, a.num_kv_heads, lg);
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;

@@ -161,6 +161,7 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     int32_t* prefix = tsum + WARPS;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, hkv = p.num_kv_heads;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 
     // ---- chunks of each sequence and their running sum (every CTA computes the same)
     const int per = (p.batch + THREADS - 1) / THREADS;
@@ -583,6 +584,7 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 // The sequences that several runs share: CTA (run, head) joins the one that its run leaves open, a warp each row.
 template <int ROWS>
 __global__ void __launch_bounds__(256) tree_rows_join_kernel(const Params p) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int gw = blockIdx.x, hkv = p.num_kv_heads;
     const int4 u = p.meta[gw];
@@ -638,18 +640,11 @@ bool allow_smem() {
 template <int NT>
 cudaError_t launch_pair(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Params& p, cudaStream_t stream) {
     const int warps = p.groups * p.num_kv_heads;
-    tree_rows_kernel<NT><<<(warps + WARPS - 1) / WARPS, THREADS, smem_bytes(p.batch), stream>>>(tm_k, tm_v, p);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(warps);
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cudaLaunchConfig_t cfg = programmatic(dim3((warps + WARPS - 1) / WARPS), THREADS, smem_bytes(p.batch), stream, attr);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_rows_kernel<NT>, tm_k, tm_v, p);
+    if (e != cudaSuccess) return e;
+    cfg = programmatic(dim3(warps), 256, 0, stream, attr);
     return cudaLaunchKernelEx(&cfg, tree_rows_join_kernel<8 * NT>, p);
 }
 
