@@ -476,6 +476,108 @@ def test_streams_workspaces_and_graphs(pkv):
     expect_no_device_error(pkv)
 
 
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "8 bits"])
+@pytest.mark.parametrize("nodes", [4, 30])
+def test_graphs_of_any_shape(pkv, nodes, fp8):
+    """Captured as a graph's first node, behind a memset, a copy and a join of two streams, and twice in a row on one workspace:
+    a call starts beside the end of the kernel before it, and reads nothing before that has ended."""
+    b = Trees([nodes, 2], [2000, 700], 8, 4, seed=31, fp8=fp8)
+    want = b.gpu(pkv)
+    dev = lambda x: torch.from_numpy(np.ascontiguousarray(x)).cuda()  # noqa: E731
+    q0, lens, cu, mask, tab = b.q.cuda(), torch.tensor(b.len, dtype=torch.int32).cuda(), dev(b.cu), dev(b.mask.view(np.int64)), dev(b.tables)
+    if fp8:
+        pools = (dev(b.kc).view(torch.float8_e4m3fn), dev(b.vc).view(torch.float8_e4m3fn), dev(b.ks).view(torch.float8_e8m0fnu), dev(b.vs).view(torch.float8_e8m0fnu))
+        attend = pkv.pkv_tree_decode_fp8
+    else:
+        pools, attend = (b.k.cuda(), b.v.cuda()), pkv.pkv_tree_decode
+    q, scratch, ws = torch.empty_like(q0), torch.empty(1 << 24, device="cuda"), pkv.tree_decode_workspace(2, nodes, 8, 4, D)
+    outs = [torch.empty_like(q0) for _ in range(5)]
+    call = lambda i: attend(q, *pools, tab, lens, cu, mask, nodes, 2000, b.scale, out=outs[i], workspace=ws)  # noqa: E731
+    q.copy_(q0)
+    other, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        call(0)
+        q.zero_()
+        scratch.zero_()
+        q.copy_(q0)                                    # a copy node
+        call(1)
+        other.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(other):
+            q.zero_()
+            scratch.add_(1.0)
+            q.add_(q0)                                 # of the stream that is joined
+        scratch2 = scratch.new_zeros(8)
+        torch.cuda.current_stream().wait_stream(other)
+        call(2)
+        call(3)
+        other.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(other):
+            call(4)                                    # the forked stream's first
+        torch.cuda.current_stream().wait_stream(other)
+        outs[0].add_(0.0)
+        scratch2.zero_()
+    for _ in range(3):
+        for o in outs:
+            o.fill_(9.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        for o in outs:
+            assert torch.equal(o, want)
+    expect_no_device_error(pkv)
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "8 bits"])
+def test_blocks_far_into_a_pool(pkv, fp8):
+    """Blocks more than 2^32 bytes (8 bits) or 2^31 elements (bf16) into their pools, for every call of a step."""
+    hkv, block = 8, 256
+    trees = [Trees([x, 1], [600, 40], 16, hkv, seed=41, fp8=fp8) for x in (4, 40)]
+    nb = max(b.nb for b in trees)
+    first = 2 ** 32 // (block * hkv * D * (1 if fp8 else 2)) + 1
+    dev = lambda x: torch.from_numpy(np.ascontiguousarray(x)).cuda()  # noqa: E731
+    byte = lambda *shape: torch.empty(*shape, dtype=torch.uint8, device="cuda")  # noqa: E731
+    if fp8:
+        raw = [byte(first + nb, block, hkv, D) for _ in "kv"] + [byte(first + nb, hkv, block) for _ in "kv"]
+        pools = [x.view(torch.float8_e4m3fn if i < 2 else torch.float8_e8m0fnu) for i, x in enumerate(raw)]
+    else:
+        raw = pools = [torch.empty(first + nb, block, hkv, D, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    assert pools[0].numel() > 2 ** 31 and pools[0].numel() * pools[0].element_size() > 2 ** 32
+    for b in trees:
+        for x, h in zip(raw, (b.kc, b.vc, b.ks, b.vs) if fp8 else (b.k, b.v)):
+            x[first:first + b.nb] = dev(h) if fp8 else h.cuda()
+        tab = dev(np.where(b.tables < 0, -1, b.tables + first).astype(np.int32))
+        lens, cu = torch.tensor(b.len, dtype=torch.int32).cuda(), dev(b.cu)
+        attend = pkv.pkv_tree_decode_fp8 if fp8 else pkv.pkv_tree_decode
+        out = attend(b.q.cuda(), *pools, tab, lens, cu, dev(b.mask.view(np.int64)), b.most, 600, b.scale)
+        assert torch.equal(out, b.gpu(pkv))
+        b.check(out)
+        layers = pkv.KvPools(*[[x] for x in pools])
+        n = b.n[0]
+        pkv.pkv_tree_compact(layers, tab, lens, cu, dev(np.array([[0, n - 1], [0, -1]], np.int32)), dev(np.array([2, 1], np.int32)))
+        spare = min(set(range(b.nb)) - set(b.tables[b.tables >= 0].tolist()))
+        i32 = lambda x: torch.tensor([x], dtype=torch.int32).cuda()  # noqa: E731
+        moved, to = b.at(0, 599), b.at(0, 600 - n + 1)
+        pkv.pkv_copy_blocks(layers, i32(first + to[0]), i32(first + spare), i32(to[1] + 1))
+        expect_no_device_error(pkv)
+        for i, x in enumerate(raw):
+            pick = (lambda at: x[at[0] + first, at[1]]) if i < 2 else (lambda at: x[at[0] + first, :, at[1]])  # noqa: B023
+            assert torch.equal(pick(to).view(torch.uint8), pick(moved).view(torch.uint8))
+            assert torch.equal(pick((spare, to[1])).view(torch.uint8), pick(moved).view(torch.uint8))
+
+
+@pytest.mark.parametrize("nodes", [4, 140])
+def test_queries_of_zero_8_bits(pkv, nodes):
+    """Zero rows weigh what they see evenly, behind tiles of which they see nothing."""
+    sees = np.zeros((nodes, nodes), bool)
+    sees[:, -2:] = True
+    sees[0] = False
+    b = Trees([nodes], [nodes], 2, 1, seed=51, masks=[sees], fp8=True)
+    b.q.zero_()
+    out = b.gpu(pkv)
+    b.check(out)
+    assert not out[0].any()
+
+
 def test_empty_calls(pkv):
     b = Trees([0, 0], [0, 30], 8, 2, seed=1, spare_rows=2)
     out = torch.full_like(b.q, 5.0).cuda()
