@@ -60,6 +60,7 @@ constexpr int KV_TILE = 2 * KV_HALF;
 constexpr int TMEM_COLS = 256;
 constexpr int O_COL = 128;                   // S / P buffers at columns 0 and 64
 constexpr float kRescaleLog2 = 8.0f;
+constexpr float kMostSum = 256.0f;
 constexpr int UNIT_COST = 2;                 // what starting and ending a unit costs, in tiles
 constexpr int MIN_RUN = 4;                   // cost a CTA takes at least; above UNIT_COST, so that every run has a tile
 static_assert(MIN_RUN > UNIT_COST, "a run has a tile");
@@ -132,6 +133,11 @@ __device__ __forceinline__ bool wait_phase(const Ctl& c, uint32_t bar, uint32_t 
 }
 __device__ __forceinline__ bool wait_warp(const Ctl& c, uint32_t bar, uint32_t parity) {
     return __all_sync(0xffffffffu, wait_phase(c, bar, parity));
+}
+// Both phases, asked for side by side: shared memory answers late beside the products' reads.
+__device__ __forceinline__ bool wait_both(const Ctl& c, uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1) {
+    const bool x = mbar_try_wait(bar0, parity0), y = mbar_try_wait(bar1, parity1);
+    return (x || wait_phase(c, bar0, parity0)) && (y || wait_phase(c, bar1, parity1));
 }
 __device__ __noinline__ bool wait_drain(uint32_t bar, uint32_t parity) {
     const unsigned long long t0 = global_ns();
@@ -833,6 +839,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             for (int i = 0; i < 4; ++i)
                 words[i] = live && i < p.mask_words ? __ldg(p.mask + static_cast<int64_t>(node_row) * p.mask_words + i) : 0ull;
             float m_used = -INFINITY, l = 0.f, sc = p.scale_log2;
+            bool fresh = true;                                // rows of this warp's that have seen nothing yet
             bool had_tree = false;
             if (FP8) {
                 ok = wait_warp(ctl, bar(L::QG), seg & 1);
@@ -842,19 +849,24 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             for (int j = w.j0; j < w.j1; ++j, ++t) {
                 const int keys = min(KT, w.s.len - j * KT), rel = j * KT - tree0;
                 const bool tree = rel + KT > 0;               // nodes among the keys: on no more than the last few tiles
-                const float* ksf = reinterpret_cast<const float*>(gbase + L::KSF) + (t % L::KS_SLOTS) * KT;
-                if (FP8 && warp_live) {
-                    ok = wait_warp(ctl, bar(L::KSR + t % L::KS_SLOTS), (t / L::KS_SLOTS) & 1);
-                    if (!ok) break;
-                }
-                ok = wait_warp(ctl, bar(L::SF + (t & 1)), (t >> 1) & 1);
+                const uint32_t ksf = base + L::KSF + (t % L::KS_SLOTS) * KT * 4;
+                // the K scales of the 16 columns that are read next: beside the products' own reads of shared memory a load
+                // takes some 180 cycles
+                uint4 kf[4];
+                auto fetch = [&](int c0) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) kf[e] = ld_shared_v4(ksf + 4 * ((c0 & (KT - 1)) + 4 * e));
+                };
+                if (FP8 && warp_live)
+                    ok = __all_sync(0xffffffffu, wait_both(ctl, bar(L::KSR + t % L::KS_SLOTS), (t / L::KS_SLOTS) & 1, bar(L::SF + (t & 1)), (t >> 1) & 1));
+                else
+                    ok = wait_warp(ctl, bar(L::SF + (t & 1)), (t >> 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
                 if (warp_live) {
                     const uint32_t s_tmem = tmem + lane_off + (t & 1) * KT;
                     const unsigned long long see = tree ? visible(words, rel, keys) : ~0ull;
-                    float mx0 = -INFINITY, mx1 = -INFINITY;
-                    // bf16: all of S in registers.  8 bits: S is read twice, CH columns at a time, in rolled loops.
+                    // bf16: all of S in registers.  8 bits: CH columns at a time, in rolled loops.
                     constexpr int CH = FP8 ? 16 : KT;
                     float s[CH];
                     auto read = [&](int c0) {
@@ -864,10 +876,11 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             tmem_ld_wait();
 #pragma unroll
                             for (int e = 0; e < 16; e += 4) {
-                                const float4 f = *reinterpret_cast<const float4*>(ksf + c0 + e);
-                                fmul2(s[e], s[e + 1], __uint_as_float(r[e]), __uint_as_float(r[e + 1]), f.x, f.y);
-                                fmul2(s[e + 2], s[e + 3], __uint_as_float(r[e + 2]), __uint_as_float(r[e + 3]), f.z, f.w);
+                                const uint4 f = kf[e >> 2];
+                                fmul2(s[e], s[e + 1], __uint_as_float(r[e]), __uint_as_float(r[e + 1]), __uint_as_float(f.x), __uint_as_float(f.y));
+                                fmul2(s[e + 2], s[e + 3], __uint_as_float(r[e + 2]), __uint_as_float(r[e + 3]), __uint_as_float(f.z), __uint_as_float(f.w));
                             }
+                            fetch(c0 + 16);
                         } else {
                             uint32_t r[2][32];
                             tmem_ld32(s_tmem, r[0]);
@@ -883,26 +896,20 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             for (int e = 0; e < CH; ++e) s[e] = ((e < 32 ? lo : hi) >> (e & 31)) & 1u ? s[e] : -INFINITY;
                         }
                     };
-#pragma unroll 1
-                    for (int c0 = 0; c0 < KT; c0 += CH) {
-                        read(c0);
+                    auto largest = [&] {
+                        float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
                         for (int e = 0; e < CH; e += 4) {
                             mx0 = fmax3(mx0, s[e + 0], s[e + 1]);
                             mx1 = fmax3(mx1, s[e + 2], s[e + 3]);
                         }
-                    }
-                    const float m_new = fmaxf(mx0, mx1) * sc;
-                    if (j == w.j0) {
-                        m_used = m_new;
-                    } else if (__any_sync(0xffffffffu, live && m_new > m_used + kRescaleLog2)) {
-                        // O is rescaled only when a maximum grows by 2^8 (of a row that is somebody's: what the others hold
-                        // may not decide when these are rounded); PV(t - 1) has to be through
+                        return fmaxf(mx0, mx1) * sc;
+                    };
+                    // O times alpha, once PV(t - 1) is through
+                    auto rescale = [&](float alpha) {
                         ok = wait_warp(ctl, bar(L::PV + ((t - 1) & 1)), ((t - 1) >> 1) & 1);
-                        if (!ok) break;
+                        if (!ok) return;
                         tc_fence_after();
-                        const float m_tgt = fmaxf(m_used, m_new);
-                        const float alpha = m_tgt == m_used ? 1.f : ex2_ftz(m_used - m_tgt);
 #pragma unroll 1
                         for (int cc = 0; cc < 4; ++cc) {
                             uint32_t o[32];
@@ -913,33 +920,97 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             tmem_st32(tmem + lane_off + O_COL + 32 * cc, o);
                         }
                         tmem_st_wait();
-                        l *= alpha;
-                        m_used = m_tgt;
+                    };
+                    // The reference of a row's weights is moved, and O rescaled, only when a score passes it by 2^8 (of a row that is
+                    // somebody's: what the others hold may not decide when these are rounded).
+                    float r0 = 0.f, r1 = 0.f, r2 = 0.f, r3 = 0.f, neg_m;
+                    if constexpr (!FP8) {
+                        read(0);
+                        const float m_new = largest();
+                        if (j == w.j0) {
+                            m_used = m_new;
+                        } else if (__any_sync(0xffffffffu, live && m_new > m_used + kRescaleLog2)) {
+                            const float m_tgt = fmaxf(m_used, m_new), alpha = m_tgt == m_used ? 1.f : ex2_ftz(m_used - m_tgt);
+                            rescale(alpha);
+                            if (!ok) break;
+                            l *= alpha;
+                            m_used = m_tgt;
+                        }
+                        neg_m = m_used == -INFINITY ? 0.f : -m_used;         // a row that has seen nothing yet
+                    } else {
+                        neg_m = m_used == -INFINITY ? 0.f : -m_used;
+                        fetch(0);
                     }
-                    const float neg_m = m_used == -INFINITY ? 0.f : -m_used;      // a row that has seen nothing yet
-                    float r0 = 0.f, r1 = 0.f, r2 = 0.f, r3 = 0.f;
 #pragma unroll 1
                     for (int c0 = 0; c0 < KT; c0 += CH) {
-                        if (FP8) read(c0);
+                        if constexpr (FP8) read(c0);
                         uint32_t pk[CH / 2];
+                        auto weigh = [&](float& x0, float& x1, float& x2, float& x3) {
 #pragma unroll
-                        for (int e = 0; e < CH; e += 4) {
-                            float a0, a1, a2, a3;
-                            ffma2(a0, a1, s[e], s[e + 1], sc, sc, neg_m, neg_m);
-                            ffma2(a2, a3, s[e + 2], s[e + 3], sc, sc, neg_m, neg_m);
-                            const float p0 = ex2_ftz(a0), p1 = ex2_ftz(a1), p2 = ex2_ftz(a2), p3 = ex2_ftz(a3);
-                            fadd2(r0, r1, r0, r1, p0, p1);
-                            fadd2(r2, r3, r2, r3, p2, p3);
-                            pk[e >> 1] = pack_bf16x2(p0, p1);
-                            pk[(e >> 1) + 1] = pack_bf16x2(p2, p3);
-                        }
-                        // P's columns end before the ones of S that are still to be read
-                        if constexpr (FP8)
-                            tmem_st8(s_tmem + c0 / 2, pk);
-                        else
+                            for (int e = 0; e < CH; e += 4) {
+                                float a0, a1, a2, a3;
+                                ffma2(a0, a1, s[e], s[e + 1], sc, sc, neg_m, neg_m);
+                                ffma2(a2, a3, s[e + 2], s[e + 3], sc, sc, neg_m, neg_m);
+                                const float p0 = ex2_ftz(a0), p1 = ex2_ftz(a1), p2 = ex2_ftz(a2), p3 = ex2_ftz(a3);
+                                if (FP8 && e == 0) {
+                                    x0 = p0, x1 = p1, x2 = p2, x3 = p3;
+                                } else {
+                                    fadd2(x0, x1, x0, x1, p0, p1);
+                                    fadd2(x2, x3, x2, x3, p2, p3);
+                                }
+                                pk[e >> 1] = pack_bf16x2(p0, p1);
+                                pk[(e >> 1) + 1] = pack_bf16x2(p2, p3);
+                            }
+                        };
+                        if constexpr (!FP8) {
+                            weigh(r0, r1, r2, r3);
                             tmem_st32(s_tmem, pk);
+                        } else {
+                            // One pass: the sum of 16 weights tells that one is beyond 2^4 times the reference, before the weights are
+                            // stored.  Then the rest of the tile is looked through for the new reference, a power of two, so that the
+                            // weights that lie over S by then are scaled exactly.
+                            float x0, x1, x2, x3;
+                            weigh(x0, x1, x2, x3);
+                            float x = (x0 + x1) + (x2 + x3);
+                            if (fresh || __any_sync(0xffffffffu, live && x > kMostSum)) {
+                                fetch(c0);
+                                float m_new = -INFINITY;
+#pragma unroll 1
+                                for (int c = c0; c < KT; c += CH) {
+                                    read(c);
+                                    m_new = fmaxf(m_new, largest());
+                                }
+                                const float m_tgt = fmaxf(m_used, ceilf(m_new)), d = m_used - m_tgt;
+                                const float alpha = m_tgt == m_used ? 1.f : d < -126.f ? 0.f : __uint_as_float(static_cast<uint32_t>(static_cast<int>(d) + 127) << 23);
+                                const uint32_t alpha2 = (__float_as_uint(alpha) >> 16) * 0x00010001u;
+                                if (j > w.j0) {
+                                    rescale(alpha);
+                                    if (!ok) break;
+                                }
+                                tmem_st_wait();
+#pragma unroll 1
+                                for (int c = 0; c < c0; c += CH) {
+                                    tmem_ld8(s_tmem + c / 2, pk);
+                                    tmem_ld_wait();
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e) pk[e] = hmul2(pk[e], alpha2);
+                                    tmem_st8(s_tmem + c / 2, pk);
+                                }
+                                l *= alpha;
+                                m_used = m_tgt;
+                                neg_m = m_used == -INFINITY ? 0.f : -m_used;
+                                fresh = __any_sync(0xffffffffu, live && m_used == -INFINITY);
+                                fetch(c0);
+                                read(c0);
+                                weigh(x0, x1, x2, x3);
+                                x = (x0 + x1) + (x2 + x3);
+                            }
+                            l += x;
+                            tmem_st8(s_tmem + c0 / 2, pk);         // P's columns end before the ones of S that are still to be read
+                        }
                     }
-                    l += (r0 + r1) + (r2 + r3);
+                    if (!ok) break;
+                    if (!FP8) l += (r0 + r1) + (r2 + r3);
                     tmem_st_wait();
                 }
                 if (tree) {
