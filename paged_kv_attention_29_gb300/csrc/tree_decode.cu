@@ -59,8 +59,8 @@ constexpr int KV_HALF = KT * 64 * 2;         // 8 KiB of K or V
 constexpr int KV_TILE = 2 * KV_HALF;
 constexpr int TMEM_COLS = 256;
 constexpr int O_COL = 128;                   // S / P buffers at columns 0 and 64
-constexpr float kRescaleLog2 = 8.0f;
-constexpr float kMostSum = 256.0f;
+constexpr float kRescaleLog2 = 8.0f;         // bf16: log2 of the weight that moves a row's reference
+constexpr float kMostSum = 256.0f;           // 8 bits: sum of 32 weights that does
 constexpr int UNIT_COST = 2;                 // what starting and ending a unit costs, in tiles
 constexpr int MIN_RUN = 4;                   // cost a CTA takes at least; above UNIT_COST, so that every run has a tile
 static_assert(MIN_RUN > UNIT_COST, "a run has a tile");
@@ -793,8 +793,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 ++oseg;
             }
             const int slot = t % L::V_SLOTS;
-            if (!(ok = wait_warp(ctl, bar(L::VF + slot), (t / L::V_SLOTS) & 1))) break;
-            if (!(ok = wait_warp(ctl, bar(L::PF + (t & 1)), (t >> 1) & 1))) break;
+            if (!(ok = __all_sync(0xffffffffu, wait_both(ctl, bar(L::VF + slot), (t / L::V_SLOTS) & 1, bar(L::PF + (t & 1)), (t >> 1) & 1)))) break;
             tc_fence_after();
             const uint64_t dv = smem_desc(base + L::V + slot * KV_TILE, KV_HALF, 1024, 2);
             issue_pv_ts(tmem + O_COL, tmem + (t & 1) * KT, dv, idesc_pv, first_here ? 0u : 1u, (keys + 15) >> 4);
@@ -835,11 +834,15 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const int tree0 = w.s.len - w.s.n;                // position of the first node
             const int node_row = w.s.q0 + w.rt * qtok + tok;
             unsigned long long words[4];
+            auto load_words = [&] {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                words[i] = live && i < p.mask_words ? __ldg(p.mask + static_cast<int64_t>(node_row) * p.mask_words + i) : 0ull;
+                for (int i = 0; i < 4; ++i)
+                    words[i] = live && i < p.mask_words ? __ldg(p.mask + static_cast<int64_t>(node_row) * p.mask_words + i) : 0ull;
+            };
+            if (!FP8) load_words();
             float m_used = -INFINITY, l = 0.f, sc = p.scale_log2;
-            bool fresh = true;                                // rows of this warp's that have seen nothing yet
+            // what the sum of 32 weights may be: more moves the reference, and so does anything where nothing has been seen yet
+            float most = live ? -1.f : INFINITY;
             bool had_tree = false;
             if (FP8) {
                 ok = wait_warp(ctl, bar(L::QG), seg & 1);
@@ -850,8 +853,8 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const int keys = min(KT, w.s.len - j * KT), rel = j * KT - tree0;
                 const bool tree = rel + KT > 0;               // nodes among the keys: on no more than the last few tiles
                 const uint32_t ksf = base + L::KSF + (t % L::KS_SLOTS) * KT * 4;
-                // the K scales of the 16 columns that are read next: beside the products' own reads of shared memory a load
-                // takes some 180 cycles
+                // K scales of the first 16 of the 32 columns that are read next: beside the products' own reads of shared
+                // memory a load takes some 180 cycles
                 uint4 kf[4];
                 auto fetch = [&](int c0) {
 #pragma unroll
@@ -865,22 +868,26 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 tc_fence_after();
                 if (warp_live) {
                     const uint32_t s_tmem = tmem + lane_off + (t & 1) * KT;
+                    if (FP8 && tree) load_words();
                     const unsigned long long see = tree ? visible(words, rel, keys) : ~0ull;
                     // bf16: all of S in registers.  8 bits: CH columns at a time, in rolled loops.
-                    constexpr int CH = FP8 ? 16 : KT;
+                    constexpr int CH = FP8 ? 32 : KT;
                     float s[CH];
                     auto read = [&](int c0) {
                         if constexpr (FP8) {
-                            uint32_t r[16];
-                            tmem_ld16(s_tmem + c0, r);
+                            uint32_t r[32];
+                            tmem_ld32(s_tmem + c0, r);
+                            uint4 k2[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) k2[e] = ld_shared_v4(ksf + 4 * (c0 + 16 + 4 * e));
                             tmem_ld_wait();
 #pragma unroll
-                            for (int e = 0; e < 16; e += 4) {
-                                const uint4 f = kf[e >> 2];
+                            for (int e = 0; e < 32; e += 4) {
+                                const uint4 f = e < 16 ? kf[(e >> 2) & 3] : k2[(e >> 2) & 3];
                                 fmul2(s[e], s[e + 1], __uint_as_float(r[e]), __uint_as_float(r[e + 1]), __uint_as_float(f.x), __uint_as_float(f.y));
                                 fmul2(s[e + 2], s[e + 3], __uint_as_float(r[e + 2]), __uint_as_float(r[e + 3]), __uint_as_float(f.z), __uint_as_float(f.w));
                             }
-                            fetch(c0 + 16);
+                            fetch(c0 + 32);
                         } else {
                             uint32_t r[2][32];
                             tmem_ld32(s_tmem, r[0]);
@@ -921,7 +928,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         }
                         tmem_st_wait();
                     };
-                    // The reference of a row's weights is moved, and O rescaled, only when a score passes it by 2^8 (of a row that is
+                    // The reference of a row's weights is moved, and O rescaled, only when weights become large (of a row that is
                     // somebody's: what the others hold may not decide when these are rounded).
                     float r0 = 0.f, r1 = 0.f, r2 = 0.f, r3 = 0.f, neg_m;
                     if constexpr (!FP8) {
@@ -966,13 +973,13 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             weigh(r0, r1, r2, r3);
                             tmem_st32(s_tmem, pk);
                         } else {
-                            // One pass: the sum of 16 weights tells that one is beyond 2^4 times the reference, before the weights are
-                            // stored.  Then the rest of the tile is looked through for the new reference, a power of two, so that the
-                            // weights that lie over S by then are scaled exactly.
+                            // One pass: the sum of 32 weights, beyond kMostSum, tells that one is more than 2^3, before they are
+                            // stored.  Then the rest of the tile is looked through for the new reference, a power of two, so
+                            // that the weights that lie over S by then are scaled exactly.
                             float x0, x1, x2, x3;
                             weigh(x0, x1, x2, x3);
                             float x = (x0 + x1) + (x2 + x3);
-                            if (fresh || __any_sync(0xffffffffu, live && x > kMostSum)) {
+                            if (__any_sync(0xffffffffu, x > most)) {
                                 fetch(c0);
                                 float m_new = -INFINITY;
 #pragma unroll 1
@@ -990,23 +997,23 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                 tmem_st_wait();
 #pragma unroll 1
                                 for (int c = 0; c < c0; c += CH) {
-                                    tmem_ld8(s_tmem + c / 2, pk);
+                                    tmem_ld16(s_tmem + c / 2, pk);
                                     tmem_ld_wait();
 #pragma unroll
-                                    for (int e = 0; e < 8; ++e) pk[e] = hmul2(pk[e], alpha2);
-                                    tmem_st8(s_tmem + c / 2, pk);
+                                    for (int e = 0; e < 16; ++e) pk[e] = hmul2(pk[e], alpha2);
+                                    tmem_st16(s_tmem + c / 2, pk);
                                 }
                                 l *= alpha;
                                 m_used = m_tgt;
                                 neg_m = m_used == -INFINITY ? 0.f : -m_used;
-                                fresh = __any_sync(0xffffffffu, live && m_used == -INFINITY);
+                                if (live && m_used != -INFINITY) most = kMostSum;
                                 fetch(c0);
                                 read(c0);
                                 weigh(x0, x1, x2, x3);
                                 x = (x0 + x1) + (x2 + x3);
                             }
                             l += x;
-                            tmem_st8(s_tmem + c0 / 2, pk);         // P's columns end before the ones of S that are still to be read
+                            tmem_st16(s_tmem + c0 / 2, pk);         // P's columns end before the ones of S that are still to be read
                         }
                     }
                     if (!ok) break;
@@ -1068,6 +1075,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     uint32_t any = 0u;
 #pragma unroll 1
                     for (int i = 0; i < 32; ++i) any |= wild[(seg & 1) * 32 + i];
+                    if (FP8 && any != 0u) load_words();
                     if (any != 0u) give_back<FP8>(p, w.b, w.s.n, w.s.len, w.j0, w.j1, g, wild + (seg & 1) * 32, words[0], words[1], words[2], words[3], live, tmem + lane_off + O_COL);
                 }
                 const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;

@@ -402,6 +402,24 @@ def test_large_and_small_queries_8_bits(pkv, power):
     b.check(b.gpu(pkv))
 
 
+@pytest.mark.parametrize("down", [False, True], ids=["up", "down"])
+@pytest.mark.parametrize("nodes", [3, 20, 70])
+def test_scores_that_grow_along_the_keys_8_bits(pkv, nodes, down):
+    """A row's reference moves again and again, in every part of a tile, and what has been weighed and summed moves with it.
+    The queries are 1 or -1 and a key's elements are one code, so that scores (up to 170) are exact but for fp32 roundings."""
+    b = Trees([nodes, 1], [900, 333], 4, 2, seed=61, fp8=True)
+    b.q[:] = 1.0
+    b.q[::3] = -1.0                                    # for these rows the scores fall
+    for s, n in enumerate(b.len):
+        for i in range(n):
+            blk, off = b.at(s, i)
+            code = min(126, 40 + 64 * (n - 1 - i if down else i) // n)
+            b.kc[blk, off], b.ks[blk, :, off] = code, 127 - 2
+    with np.errstate(invalid="ignore"):
+        b.k = torch.from_numpy(fc.read_pool(b.kc, b.ks)).bfloat16()
+    b.check(b.gpu(pkv))
+
+
 def test_rows_left_alone(pkv):
     """Rows behind the last sequence, and sequences that break the bounds, stay as they were."""
     b = Trees([5, 9, 4], [40, 70, 30], 8, 2, seed=13, spare_rows=3)
