@@ -781,10 +781,15 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         int j = w.j0, t = 0, s = 0;
 #pragma unroll 1
         while (ok) {
-            if (s == t || (s == t + 1 && j + 1 < w.j1)) {
-                issue_s(s, s == t, j + (s - t) + 1 == w.j1);
+            if (s == t) {
+                issue_s(s, true, j + 1 == w.j1);
                 ++s;
-                continue;
+                if (!ok) break;
+            }
+            if (j + 1 < w.j1) {
+                issue_s(s, false, j + 2 == w.j1);
+                ++s;
+                if (!ok) break;
             }
             const bool first_here = j == w.j0, last_here = j + 1 == w.j1, end = last_here && w.last();
             const int keys = min(KT, w.s.len - j * KT);
