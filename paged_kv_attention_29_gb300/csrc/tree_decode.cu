@@ -31,12 +31,14 @@
 // Trees of 16 rows or fewer on the 8-bit cache are another kernel's (tree_decode_rows.cu).
 //
 // Measured (calls in a graph, 8 KV heads): batch 64 with 512 to 4096 keys and 12 to 16
-// nodes, G = 2, 575 MB: 100 us, 5.7 TB/s; 8 sequences of 16k to 40k keys, 60 nodes, 964 MB:
-// 155 us, 6.2 TB/s: HBM.  32 sequences of 80 to 2999 keys, 33 to 64 nodes, G = 4, 46 GFLOP: 75
+// nodes, G = 2, 575 MB: 99 us, 5.8 TB/s; 8 sequences of 16k to 40k keys, 60 nodes, 964 MB:
+// 155 us, 6.2 TB/s: HBM.  32 sequences of 80 to 2999 keys, 33 to 64 nodes, G = 4, 46 GFLOP: 73
 // us, bound by the steps of a tile (S, softmax, P, O), which wait on one another.  8-bit cache: the
-// first case 111 us, bound by instructions, V's decoding and the softmax; its loops are kept rolled
-// and rare paths out of line, since the roles share the schedulers' instruction caches (the
-// softmax unrolled over 64 columns 160 us, over 32 126, over 16 111).
+// first case 101 us, 7 sequences of 16k to 40k keys, 13 to 29 nodes, G = 8: 129, bound by the same steps,
+// whose waits and loads shared memory answers late (some 180 cycles beside the products' reads).  So
+// each step of its softmax takes one pass over the scores, 32 at a time with their scales loaded a
+// step ahead (two passes of 16: 110 and 156 us; one of 16: 107 and 142).  Its loops are kept rolled and
+// rare paths out of line, since the roles share the schedulers' instruction caches.
 //
 // Warps 0-3: softmax and epilogue (TMEM lanes 0-127).  bf16 cache: warp 4 TMA producer,
 // warp 5 TMEM allocation and MMA issue.  8-bit cache: warps 4-7 turn the codes that TMA

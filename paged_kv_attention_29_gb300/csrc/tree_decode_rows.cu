@@ -18,7 +18,7 @@
 // of 8 rows, in the registers of the warp that uses them.
 //
 // Why 16 rows, measured at batch 64 with 512 to 4096 keys (8 KV heads): 8 rows 57 us, 16 rows
-// 73, against 111 on tcgen05 (tree_decode.cu) whatever the rows up to 32; 32 rows took 132 here, as
+// 73, against 101 on tcgen05 (tree_decode.cu) whatever the rows up to 32; 32 rows took 132 here, as
 // one warp with 255 registers or as two that share a stage: two or three warps a scheduler
 // do not hide the latencies of some 700 to 1100 instructions a chunk.
 //
