@@ -935,8 +935,9 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         }
                         tmem_st_wait();
                     };
-                    // The reference of a row's weights is moved, and O rescaled, only when weights become large (of a row that is
-                    // somebody's: what the others hold may not decide when these are rounded).
+                    // The reference of a row's weights is moved, and O rescaled, only when its own weights become large.  The warp
+                    // does it together, but each row decides for itself: what another row sees may not decide when this one is
+                    // rounded.  A row that is nobody's does not ask for it.
                     float r0 = 0.f, r1 = 0.f, r2 = 0.f, r3 = 0.f, neg_m;
                     if constexpr (!FP8) {
                         read(0);
@@ -944,7 +945,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         if (j == w.j0) {
                             m_used = m_new;
                         } else if (__any_sync(0xffffffffu, live && m_new > m_used + kRescaleLog2)) {
-                            const float m_tgt = fmaxf(m_used, m_new), alpha = m_tgt == m_used ? 1.f : ex2_ftz(m_used - m_tgt);
+                            const float m_tgt = m_new > m_used + kRescaleLog2 ? m_new : m_used, alpha = m_tgt == m_used ? 1.f : ex2_ftz(m_used - m_tgt);
                             rescale(alpha);
                             if (!ok) break;
                             l *= alpha;
@@ -994,7 +995,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                     read(c);
                                     m_new = fmaxf(m_new, largest());
                                 }
-                                const float m_tgt = fmaxf(m_used, ceilf(m_new)), d = m_used - m_tgt;
+                                const float m_tgt = x > most ? fmaxf(m_used, ceilf(m_new)) : m_used, d = m_used - m_tgt;
                                 const float alpha = m_tgt == m_used ? 1.f : d < -126.f ? 0.f : __uint_as_float(static_cast<uint32_t>(static_cast<int>(d) + 127) << 23);
                                 const uint32_t alpha2 = (__float_as_uint(alpha) >> 16) * 0x00010001u;
                                 if (j > w.j0) {

@@ -26,7 +26,8 @@
 // down to 2^-28 of its largest element; scores, their maximum m and the sum l are fp32; the
 // weight of a key in the second product is f16 of 2^(s - m + ev - T), T following the largest
 // of these exponents so that it is held between 2^kTopT and 2^kMarginT; both references move
-// only past a margin.  A row's references are set by the first key it sees.
+// only past a margin, each row's by what that row sees (the warp votes to look, no more).  A
+// row's references are set by the first key it sees.
 //
 // Work split: the sequences' 32-key chunks, one after the other, are cut into equal runs, one
 // for each group of num_kv_heads warps; warp h of a group walks its run for KV head h (a
@@ -422,7 +423,7 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                         none &= __shfl_xor_sync(0xffffffffu, static_cast<int>(none), y) != 0;
                     }
                     if (!none) seen |= 1u << (2 * x + h);
-                    if (!fresh) up = fmaxf(up, 0.f);
+                    if (!fresh && !(up > kMarginM)) up = 0.f;   // another row's reference moves, not this one's
                     if (!(fabsf(up) < INFINITY)) up = 0.f;   // no finite score: any reference does
                     m[x][h] += up;
                     l[x][h] *= fresh ? 1.f : ex2_ftz(-up);   // a fresh l is 0, and up may be any score
@@ -453,8 +454,7 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                     float up = fmaxf(fmaxf(w[0][h], w[1][h]), fmaxf(w[2][h], w[3][h]));
 #pragma unroll
                     for (int y = 4; y < 32; y <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, y));
-                    up -= kTopT;
-                    if (!fresh) up = fmaxf(up, 0.f);
+                    up = fresh || up > kMarginT ? up - kTopT : 0.f;
                     if (!(fabsf(up) < INFINITY)) up = 0.f;
                     T[x][h] += up;
                     const float f = fresh ? 1.f : ex2_ftz(-up);          // a fresh o is 0

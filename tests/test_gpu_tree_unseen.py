@@ -1,0 +1,36 @@
+"""A key that a node does not see has no effect on its row, and neither have the rows beside it: the same bits, whatever
+the keys of others hold and however a call's bounds are stated."""
+import numpy as np
+import pytest
+import torch
+
+from pkv_testutil import expect_no_device_error
+from test_gpu_tree import Trees
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "8 bits"])
+@pytest.mark.parametrize("nodes,context", [(4, 32), (4, 40), (8, 100), (30, 64), (30, 130), (100, 64)])
+def test_large_keys_that_others_do_not_see(pkv, nodes, context, fp8):
+    """A node that only it sees holds a K along its own query, large enough to move its row's reference: in every other row
+    (of which some meet their largest score among the nodes, a little above the context's) nothing changes."""
+    hidden = nodes // 2
+    for seed in range(6):
+        sees = np.tril(np.ones((nodes, nodes), bool))
+        sees[:, hidden] = False
+        sees[hidden, hidden] = True
+        b = Trees([nodes], [context + nodes], 4, 2, seed=seed, masks=[sees], fp8=fp8)
+        clean = b.gpu(pkv)
+        b.check(clean)
+        blk, off = b.at(0, context + hidden)
+        along = torch.sign(b.q[hidden, ::2].float())                       # a query head of each KV head
+        if fp8:
+            b.kc[blk, off] = np.where(along.numpy() < 0, 0xfe, 0x7e)       # -448 or 448
+            b.ks[blk, :, off] = 127
+        b.k[blk, off] = (448 * along).bfloat16()
+        out = b.gpu(pkv)
+        expect_no_device_error(pkv)
+        b.check(out)
+        others = [i for i in range(nodes) if i != hidden]
+        assert torch.equal(out[others], clean[others]), seed
