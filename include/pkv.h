@@ -558,7 +558,9 @@ PKV_API pkv_status pkv_sample_filtered_dev(const float *logits, int32_t batch, i
  *           head_dim) bytes on the current device, 256-byte aligned, no initialisation needed,
  *           scratch after the call; calls that may overlap need one each
  * batch <= 4096.  fp32 scores and sums; a key's weight is rounded to bf16 for the product
- * with the values (2^-8 of itself at most), the output once to bf16.  Deterministic.
+ * with the values (2^-8 of itself at most), the output once to bf16.  Deterministic.  Values that
+ * are finite in bf16 give finite results, whatever their number (one within 2^-8 of bf16's largest
+ * may be rounded to an infinity); results are right to 2^-128 where that is more than the roundings.
  * pkv_tree_decode_fp8 is the same over an 8-bit cache.  More than 16 rows to a KV head
  * (max_nodes * num_heads / num_kv_heads): a query is split into two e4m3 parts, off by at most
  * 2^-18 of the row's largest element, and weights are rounded to bf16 as above; k_scale up to 2^100

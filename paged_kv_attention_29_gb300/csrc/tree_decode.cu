@@ -20,8 +20,8 @@
 // taken by a CTA per KV head (two CTAs per SM, so that one's loads and products fill the
 // other's waits; a run's CTAs are neighbours, so that the heads' rows of a token, which
 // lie side by side in memory, are read at about the same time): a unit that a run does
-// not hold whole leaves fp32 partial sums with their maxima in the workspace, and a
-// second kernel joins them in the order of the runs.  Results are deterministic.
+// not hold whole leaves fp32 averages with their references and sums in the workspace, and
+// a second kernel joins them in the order of the runs.  Results are deterministic.
 //
 // A node's row is as if masked keys were not there, whatever they hold: scores are
 // selected, not added to, and infinities and NaN among the nodes' V rows, which a
@@ -61,8 +61,13 @@ constexpr int KV_HALF = KT * 64 * 2;         // 8 KiB of K or V
 constexpr int KV_TILE = 2 * KV_HALF;
 constexpr int TMEM_COLS = 256;
 constexpr int O_COL = 128;                   // S / P buffers at columns 0 and 64
-constexpr float kRescaleLog2 = 8.0f;         // bf16: log2 of the weight that moves a row's reference
-constexpr float kMostSum = 256.0f;           // 8 bits: sum of 32 weights that does
+// A row's reference is put 2^16 above its largest weight and moved again once the weights' sum has passed 1/4 (bf16: or one
+// of the tile's weights 2^-8, and 64 of those make another 1/4).  So the sum stays below 1/2, and with it |O| / 2^127 for any
+// finite V.  2^16, so that long contexts seldom move it (32768 equal keys); less than that leaves O more of fp32's range at
+// the lower end, where V of 2^-118 keeps 14 bits.
+constexpr float kLift = 16.0f;
+constexpr float kMostWeightLog2 = -8.0f;
+constexpr float kMostSum = 0.25f;
 constexpr int UNIT_COST = 2;                 // what starting and ending a unit costs, in tiles
 constexpr int MIN_RUN = 4;                   // cost a CTA takes at least; above UNIT_COST, so that every run has a tile
 static_assert(MIN_RUN > UNIT_COST, "a run has a tile");
@@ -97,8 +102,8 @@ struct Params {
     const int32_t* cu_nodes;
     const unsigned long long* mask;
     uint16_t* out;
-    float4* part_o;           // [CTA][2][32][128]: four columns of each row
-    float2* part_ml;          // [CTA][2][128]: maximum (log2) and sum
+    float4* part_o;           // [CTA][2][32][128]: four columns of each row, over the sum
+    float2* part_ml;          // [CTA][2][128]: reference (log2) and sum
     int4* meta;               // [CTA]: {last run of the unit that continues behind this one's or -1, first row's node, nodes, CTAs of a run}
     const uint8_t* v_codes;   // 8-bit cache, for the values taken out of a tile
     const uint8_t* k_scale;
@@ -848,7 +853,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             };
             if (!FP8) load_words();
             float m_used = -INFINITY, l = 0.f, sc = p.scale_log2;
-            // what the sum of 32 weights may be: more moves the reference, and so does anything where nothing has been seen yet
+            // 8 bits: what the sum of weights may be: more moves the reference, and so does anything where nothing has been seen yet
             float most = live ? -1.f : INFINITY;
             bool had_tree = false;
             if (FP8) {
@@ -942,10 +947,12 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     if constexpr (!FP8) {
                         read(0);
                         const float m_new = largest();
+                        const bool full = l > kMostSum, large = m_new > m_used + kMostWeightLog2;
                         if (j == w.j0) {
-                            m_used = m_new;
-                        } else if (__any_sync(0xffffffffu, live && m_new > m_used + kRescaleLog2)) {
-                            const float m_tgt = m_new > m_used + kRescaleLog2 ? m_new : m_used, alpha = m_tgt == m_used ? 1.f : ex2_ftz(m_used - m_tgt);
+                            m_used = m_new + kLift;
+                        } else if (__any_sync(0xffffffffu, live && (full || large))) {
+                            const float m_tgt = full ? fmaxf(m_used, m_new) + kLift : large ? m_new + kLift : m_used;
+                            const float alpha = m_tgt == m_used ? 1.f : ex2_ftz(m_used - m_tgt);
                             rescale(alpha);
                             if (!ok) break;
                             l *= alpha;
@@ -981,13 +988,14 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             weigh(r0, r1, r2, r3);
                             tmem_st32(s_tmem, pk);
                         } else {
-                            // One pass: the sum of 32 weights, beyond kMostSum, tells that one is more than 2^3, before they are
-                            // stored.  Then the rest of the tile is looked through for the new reference, a power of two, so
-                            // that the weights that lie over S by then are scaled exactly.
+                            // One pass: the sum with 32 more weights tells, before they are stored, that it has become too large.
+                            // Then the rest of the tile is looked through for the new reference, a power of two, so that the
+                            // weights that lie over S by then are scaled exactly.
                             float x0, x1, x2, x3;
                             weigh(x0, x1, x2, x3);
                             float x = (x0 + x1) + (x2 + x3);
-                            if (__any_sync(0xffffffffu, x > most)) {
+                            const bool full = l + x > most;
+                            if (__any_sync(0xffffffffu, full)) {
                                 fetch(c0);
                                 float m_new = -INFINITY;
 #pragma unroll 1
@@ -995,7 +1003,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                     read(c);
                                     m_new = fmaxf(m_new, largest());
                                 }
-                                const float m_tgt = x > most ? fmaxf(m_used, ceilf(m_new)) : m_used, d = m_used - m_tgt;
+                                const float m_tgt = full ? fmaxf(m_used, ceilf(m_new)) + kLift : m_used, d = m_used - m_tgt;
                                 const float alpha = m_tgt == m_used ? 1.f : d < -126.f ? 0.f : __uint_as_float(static_cast<uint32_t>(static_cast<int>(d) + 127) << 23);
                                 const uint32_t alpha2 = (__float_as_uint(alpha) >> 16) * 0x00010001u;
                                 if (j > w.j0) {
@@ -1086,7 +1094,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     if (FP8 && any != 0u) load_words();
                     if (any != 0u) give_back<FP8>(p, w.b, w.s.n, w.s.len, w.j0, w.j1, g, wild + (seg & 1) * 32, words[0], words[1], words[2], words[3], live, tmem + lane_off + O_COL);
                 }
-                const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+                const float inv = l == 0.f ? 0.f : 1.f / l;
                 const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + part;
                 uint16_t* orow = p.out + (static_cast<int64_t>(node_row) * p.num_heads + (g << p.lg) + (row & ((1 << p.lg) - 1))) * D;
                 if (!whole) p.part_ml[slot * ROWS + row] = make_float2(m_used, l);
@@ -1111,8 +1119,8 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
                         for (int q = 0; q < 8; ++q)
                             p.part_o[(slot * 32 + 8 * cc + q) * ROWS + row] =
-                                make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]), __uint_as_float(o[4 * q + 2]),
-                                            __uint_as_float(o[4 * q + 3]));
+                                make_float4(__uint_as_float(o[4 * q]) * inv, __uint_as_float(o[4 * q + 1]) * inv, __uint_as_float(o[4 * q + 2]) * inv,
+                                            __uint_as_float(o[4 * q + 3]) * inv);
                     }
                 }
             }
@@ -1141,7 +1149,8 @@ __global__ void __launch_bounds__(JOIN_THREADS) tree_join_kernel(const float4* _
     if ((row >> lg) >= u.z) return;
     // the unit's first part is its run's second slot, all others are their runs' first
     auto slot = [&](int i) { return (static_cast<int64_t>(i) * lanes + in_run) * 2 + (i == c ? 1 : 0); };
-    // the maximum, the sum and the columns in one pass, two runs' loads at a time
+    // The reference, the sum and the columns in one pass, two runs' loads at a time.  Parts are averages, and what is held is
+    // the average of those that have gone by: no sum of theirs leaves fp32's range.
     float M = -INFINITY, l = 0.f, o[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[e] = 0.f;
@@ -1156,10 +1165,12 @@ __global__ void __launch_bounds__(JOIN_THREADS) tree_join_kernel(const float4* _
             for (int k = 0; k < 4; ++k)
                 x[i][k] = i0 + i <= u.x ? part_o[(at * 32 + c4 + k) * ROWS + row] : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        const float now = fmax3(M, ml[0].x, ml[1].x), keep = M == now ? 1.f : ex2_ftz(M - now);
-        const float w0 = ml[0].x == now ? 1.f : ex2_ftz(ml[0].x - now), w1 = ml[1].x == now ? 1.f : ex2_ftz(ml[1].x - now);
+        const float now = fmax3(M, ml[0].x, ml[1].x);
+        const float l0 = ml[0].x == now ? ml[0].y : ml[0].y * ex2_ftz(ml[0].x - now), l1 = ml[1].x == now ? ml[1].y : ml[1].y * ex2_ftz(ml[1].x - now);
+        const float before = M == now ? l : l * ex2_ftz(M - now);
         M = now;
-        l = l * keep + ml[0].y * w0 + ml[1].y * w1;
+        l = before + l0 + l1;
+        const float inv = l == 0.f ? 0.f : __fdividef(1.f, l), keep = before * inv, w0 = l0 * inv, w1 = l1 * inv;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             o[4 * k] = o[4 * k] * keep + x[0][k].x * w0 + x[1][k].x * w1;
@@ -1168,12 +1179,11 @@ __global__ void __launch_bounds__(JOIN_THREADS) tree_join_kernel(const float4* _
             o[4 * k + 3] = o[4 * k + 3] * keep + x[0][k].w * w0 + x[1][k].w * w1;
         }
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
     uint4* to = reinterpret_cast<uint4*>(out + (static_cast<int64_t>(u.y + (row >> lg)) * num_heads + (g << lg) + (row & ((1 << lg) - 1))) * D + 4 * c4);
 #pragma unroll
     for (int k = 0; k < 2; ++k)
-        to[k] = make_uint4(pack_bf16x2(o[8 * k] * inv, o[8 * k + 1] * inv), pack_bf16x2(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
-                           pack_bf16x2(o[8 * k + 4] * inv, o[8 * k + 5] * inv), pack_bf16x2(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+        to[k] = make_uint4(pack_bf16x2(o[8 * k], o[8 * k + 1]), pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
+                           pack_bf16x2(o[8 * k + 4], o[8 * k + 5]), pack_bf16x2(o[8 * k + 6], o[8 * k + 7]));
 }
 
 constexpr size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
