@@ -1137,9 +1137,10 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 // The units that several runs share: block (CTA, y) joins 32 columns of the unit that starts in the CTA's run and goes on
 // behind it, a thread 16 columns of one row.
 constexpr int JOIN_THREADS = 2 * ROWS, JOIN_SPLIT = 4;
-__global__ void __launch_bounds__(JOIN_THREADS) tree_join_kernel(const float4* __restrict__ part_o, const float2* __restrict__ part_ml,
-                                                                 const int4* __restrict__ meta, uint16_t* __restrict__ out, int num_heads, int num_kv_heads,
-                                                                 int lg) {
+// The pointers promise nothing (no __restrict__): the kernel is resident while the one before it still writes what they point at,
+// and loads of memory that is constant as far as the compiler knows may be moved ahead of the wait.
+__global__ void __launch_bounds__(JOIN_THREADS) tree_join_kernel(const float4* part_o, const float2* part_ml, const int4* meta, uint16_t* out, int num_heads,
+                                                                 int num_kv_heads, int lg) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 u = meta[blockIdx.x];
