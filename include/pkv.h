@@ -565,7 +565,8 @@ PKV_API pkv_status pkv_sample_filtered_dev(const float *logits, int32_t batch, i
  * (max_nodes * num_heads / num_kv_heads): a query is split into two e4m3 parts, off by at most
  * 2^-18 of the row's largest element, and weights are rounded to bf16 as above; k_scale up to 2^100
  * (a product of codes times its key's scale is formed in fp32 before the query's factor).  Up to 16: as
- * pkv_decode_fp8, queries exact to 2^-28 of the row's largest element, weights rounded to f16.
+ * pkv_decode_fp8, queries exact to 2^-28 of the row's largest element, weights rounded to f16 (unless
+ * the batch's block tables hold 2^36 positions or more, padding included; max_context_len plays no part).
  */
 PKV_API size_t pkv_tree_decode_workspace_size(int32_t batch, int32_t max_nodes, int32_t num_heads,
                                       int32_t num_kv_heads, int32_t head_dim);

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <math.h>
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 
@@ -753,7 +754,7 @@ pkv_status tree_decode_call(const pkv_bf16* q, const void* k_cache, const void* 
     a.total_nodes = total_nodes;
     a.max_nodes = max_nodes;
     a.mask_words = mask_words;
-    a.max_context = max_context_len;
+    a.max_context = std::min(max_context_len, max_blocks_per_seq * block_size);      // no sequence has more; the product fits (above)
     a.num_heads = num_heads;
     a.num_kv_heads = num_kv_heads;
     a.block_size = block_size;

@@ -658,7 +658,9 @@ size_t tree_rows_workspace_bytes(int num_kv_heads) {
 }
 
 bool tree_rows_fits(const TreeDecodeArgs& a, int lg) {
-    const int64_t chunks = (static_cast<int64_t>(a.max_context) + CHUNK - 1) / CHUNK;
+    // what the tables can hold, not max_context: a batch's chunks are counted in 32 bits, and which kernel takes it does not
+    // depend on how tight that bound is
+    const int64_t chunks = (static_cast<int64_t>(a.max_blocks) * a.block_size + CHUNK - 1) / CHUNK;
     return a.k_scale != nullptr && (a.max_nodes << lg) <= kTreeRows && max_groups(a.num_kv_heads) >= 1 && a.batch * chunks <= 0x7fffffffLL;
 }
 

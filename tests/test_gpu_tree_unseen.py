@@ -34,3 +34,16 @@ def test_large_keys_that_others_do_not_see(pkv, nodes, context, fp8):
         b.check(out)
         others = [i for i in range(nodes) if i != hidden]
         assert torch.equal(out[others], clean[others]), seed
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "8 bits"])
+@pytest.mark.parametrize("nodes", [4, 30])
+def test_any_bound_on_the_lengths(pkv, nodes, fp8):
+    """The loosest bound there is, with so many sequences that their product passes 2^31 tiles: the same bits."""
+    rng = np.random.default_rng(nodes)
+    lens = nodes + rng.integers(0, 700, 130)
+    b = Trees([nodes] * 130, lens, 4, 2, seed=nodes, fp8=fp8)
+    tight = b.gpu(pkv)
+    assert torch.equal(tight, b.gpu(pkv, max_len=2 ** 31 - 1))
+    expect_no_device_error(pkv)
+    b.check(tight, range(0, 130, 17))
