@@ -68,6 +68,9 @@ constexpr int O_COL = 128;                   // S / P buffers at columns 0 and 6
 constexpr float kLift = 16.0f;
 constexpr float kMostWeightLog2 = -8.0f;
 constexpr float kMostSum = 0.25f;
+// 8 bits: the factor of a row whose query holds an infinity or a NaN.  Any number would do that is positive, finite and no
+// other row's: a score that is not seen is -inf times the factor, and so that this is -inf no factor may be 0 or NaN.
+constexpr float kBadRow = 0x1.000002p-126f;
 constexpr int UNIT_COST = 2;                 // what starting and ending a unit costs, in tiles
 constexpr int MIN_RUN = 4;                   // cost a CTA takes at least; above UNIT_COST, so that every run has a tile
 static_assert(MIN_RUN > UNIT_COST, "a run has a tile");
@@ -409,9 +412,9 @@ __device__ __forceinline__ void bf16_of_row(const uint4& c, uint32_t byte, uint4
 // A query row for the product with codes.  With f the power of two that takes the row's largest |q| to [128, 256), q f
 // is a sum of two e4m3 numbers, the nearest one and what is left: exactly where |q| is 2^-10 of the largest or more (8
 // bits are 4 + 4), and to 2^-18 of the largest otherwise.  The row is replaced by its two parts, each laid out as 128
-// bytes of a K-major tile; *factor gets 1 / f, or NaN for a row with an infinity or a NaN.  Eight lanes take a row, lane v
+// bytes of a K-major tile; *factor gets scale / f, or kBadRow for a row with an infinity or a NaN.  Eight lanes take a row, lane v
 // dims 16 v .. 16 v + 15; all of a warp's lanes call.
-__device__ __forceinline__ void split_row(uint8_t* q, int row, int v, float* factor) {
+__device__ __forceinline__ void split_row(uint8_t* q, int row, int v, float scale, float* factor) {
     uint32_t x[8];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -446,7 +449,11 @@ __device__ __forceinline__ void split_row(uint8_t* q, int row, int v, float* fac
     uint8_t* at = q + row * 128 + ((v ^ (row & 7)) * 16);
     *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4*>(at + Q_HALF) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    if (v == 0) *factor = e == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float((e - 7u) << 23);
+    if (v == 0) {
+        // a factor below fp32's range is one of scores next to 0 (the products are below 2^125): the smallest number does as well
+        const float x = fmaxf(scale * __uint_as_float((e - 7u) << 23), 0x1p-149f);
+        *factor = e == 255u ? kBadRow : x == kBadRow ? 0x1p-126f : x;
+    }
 }
 
 // The infinities and NaN that were taken out of the V rows of a segment's nodes, added to O in the rows that see the
@@ -744,7 +751,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const int rows = w.tokens() << p.lg;
                 float* factors = reinterpret_cast<float*>(gbase + L::QS) + (seg & 1) * ROWS;
 #pragma unroll 1
-                for (int r = (warp - 4) * 4 + (lane >> 3); r - (lane >> 3) < rows; r += 16) split_row(gbase + L::Q, r, lane & 7, factors + r);
+                for (int r = (warp - 4) * 4 + (lane >> 3); r - (lane >> 3) < rows; r += 16) split_row(gbase + L::Q, r, lane & 7, p.scale_log2, factors + r);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(L::QR));
@@ -859,7 +866,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (FP8) {
                 ok = wait_warp(ctl, bar(L::QG), seg & 1);
                 if (!ok) break;
-                sc *= reinterpret_cast<const float*>(gbase + L::QS)[(seg & 1) * ROWS + row];
+                sc = reinterpret_cast<const float*>(gbase + L::QS)[(seg & 1) * ROWS + row];
             }
             for (int j = w.j0; j < w.j1; ++j, ++t) {
                 const int keys = min(KT, w.s.len - j * KT), rel = j * KT - tree0;
@@ -1086,6 +1093,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 meta = make_int4(static_cast<int>((end * scan[12] - 1) / scan[13]), w.s.q0 + w.rt * qtok, tokens, static_cast<int>(scan[10]));
             }
             if (warp_live) {
+                if (FP8 && sc == kBadRow && l != 0.f) l = __uint_as_float(0x7fc00000u);      // it has seen a key
                 if (had_tree) {
                     // what was taken out of the tiles, to the rows that see it
                     uint32_t any = 0u;

@@ -47,3 +47,28 @@ def test_any_bound_on_the_lengths(pkv, nodes, fp8):
     assert torch.equal(tight, b.gpu(pkv, max_len=2 ** 31 - 1))
     expect_no_device_error(pkv)
     b.check(tight, range(0, 130, 17))
+
+
+@pytest.mark.parametrize("scale", [128 ** -0.5, 1e-9, 1e-30, 1e-44])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "8 bits"])
+@pytest.mark.parametrize("nodes", [4, 40, 140])
+def test_small_queries_and_scales(pkv, nodes, fp8, scale):
+    """Scores that are all next to 0 weigh evenly what a row sees, and a row that sees nothing is zero: with queries of
+    zero, of the smallest numbers and of none at all."""
+    rng = np.random.default_rng(nodes)
+    sees = rng.random((nodes, nodes)) < 0.4
+    sees[np.arange(nodes), np.arange(nodes)] = True
+    sees[[0, 3]] = False
+    for context in (0, 200):
+        b = Trees([nodes], [nodes + context], 4, 2, seed=nodes, masks=[sees], fp8=fp8)
+        b.scale = scale
+        b.q[::2] = 0.0
+        b.q[1::2] *= 2.0 ** -125
+        b.check(b.gpu(pkv))
+    b = Trees([nodes], [nodes], 4, 2, seed=nodes, masks=[sees], fp8=fp8)
+    b.scale = scale
+    clean = b.gpu(pkv)
+    b.q[0], b.q[3] = float("nan"), float("inf")        # they see nothing, themselves included
+    out = b.gpu(pkv)
+    assert not out[[0, 3]].any() and torch.equal(out, clean)
+    expect_no_device_error(pkv)
