@@ -562,11 +562,12 @@ PKV_API pkv_status pkv_sample_filtered_dev(const float *logits, int32_t batch, i
  * are finite in bf16 give finite results, whatever their number (one within 2^-8 of bf16's largest
  * may be rounded to an infinity); results are right to 2^-128 where that is more than the roundings.
  * pkv_tree_decode_fp8 is the same over an 8-bit cache.  More than 16 rows to a KV head
- * (max_nodes * num_heads / num_kv_heads): a query is split into two e4m3 parts, off by at most
- * 2^-18 of the row's largest element, and weights are rounded to bf16 as above; k_scale up to 2^100
- * (a product of codes times its key's scale is formed in fp32 before the query's factor).  Up to 16: as
- * pkv_decode_fp8, queries exact to 2^-28 of the row's largest element, weights rounded to f16 (unless
- * the batch's block tables hold 2^36 positions or more, padding included; max_context_len plays no part).
+ * (max_nodes * num_heads / num_kv_heads): a query is split into two e4m3 parts, exact from 2^-9 of
+ * the row's largest element and off by at most 2^-17 of it, and weights are rounded to bf16 as above;
+ * k_scale up to 2^100 (a product of codes times its key's scale is formed in fp32 before the query's
+ * factor).  Up to 16: as pkv_decode_fp8, queries exact to 2^-28 of the row's largest element, weights
+ * rounded to f16 (unless the batch's block tables hold 2^36 positions or more, padding included;
+ * max_context_len plays no part).
  */
 PKV_API size_t pkv_tree_decode_workspace_size(int32_t batch, int32_t max_nodes, int32_t num_heads,
                                       int32_t num_kv_heads, int32_t head_dim);

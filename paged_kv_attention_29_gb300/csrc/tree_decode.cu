@@ -410,8 +410,8 @@ __device__ __forceinline__ void bf16_of_row(const uint4& c, uint32_t byte, uint4
 }
 
 // A query row for the product with codes.  With f the power of two that takes the row's largest |q| to [128, 256), q f
-// is a sum of two e4m3 numbers, the nearest one and what is left: exactly where |q| is 2^-10 of the largest or more (8
-// bits are 4 + 4), and to 2^-18 of the largest otherwise.  The row is replaced by its two parts, each laid out as 128
+// is a sum of two e4m3 numbers, the nearest one and what is left: exactly where |q| is 2^-9 of the largest or more (8 bits
+// are 4 + 4, the last one 2^-9), and to 2^-17 of the largest otherwise (half of e4m3's smallest step, 2^-9, beside 128).  The row is replaced by its two parts, each laid out as 128
 // bytes of a K-major tile; *factor gets scale / f, or kBadRow for a row with an infinity or a NaN.  Eight lanes take a row, lane v
 // dims 16 v .. 16 v + 15; all of a warp's lanes call.
 __device__ __forceinline__ void split_row(uint8_t* q, int row, int v, float scale, float* factor) {
