@@ -592,8 +592,9 @@ PKV_API pkv_status pkv_tree_decode_fp8(const pkv_bf16 *q, const pkv_e4m3 *k_cach
  * The accepted path: from node 0, as long as a child of the node holds the token that the
  * model sampled at the node, go to that child (the lowest of several).  A node's parent is
  * the highest node below it in its mask; a node other than 0 without one is never reached.
- * With tokens sampled from the model's own distribution at every node (at any temperature) the
- * accepted tokens are distributed as those of one-by-one decoding.
+ * With tokens sampled from the model's own distribution at every node (at any temperature), each with
+ * noise that no other row has had (pkv_sample's offset a running count of the rows sampled with its
+ * seed), the accepted tokens are distributed as those of one-by-one decoding.
  *
  *   target        int64 [total_nodes] the token sampled at each node (pkv_sample's ids)
  *   draft         int64 [total_nodes] the token each node stands for
