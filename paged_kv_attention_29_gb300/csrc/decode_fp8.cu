@@ -50,28 +50,14 @@
 // Each warp owns a ring of shared-memory stages, each holding a chunk's K and V codes (TMA tiles
 // with 128-byte swizzle: conflict-free 16-byte loads below) and its 2 x 32 scale bytes, all
 // landing on one mbarrier.
-#include <cuda_fp16.h>
-
-#include "pkv_device.cuh"
-#include "pkv_internal.h"
+#include "fp8_rows.cuh"
 
 namespace pkv {
 namespace {
 
-constexpr int D = kHeadDim;
-constexpr int CHUNK = 32;                    // tokens per stage
-constexpr int WARPS = 8;
-constexpr int STAGES = 3;                    // per warp
-constexpr int THREADS = WARPS * 32;
-constexpr int TILE_BYTES = CHUNK * D;        // one e4m3 tile
-constexpr int STAGE_BYTES = 2 * TILE_BYTES;  // K, V
-constexpr int SCALE_BYTES = 2 * CHUNK;       // a stage's K scales, V scales
+using namespace fp8_rows;
+
 constexpr int MAX_BATCH = 4096;
-constexpr int KMIN = 2;                      // chunks a warp takes at least, where the batch allows it
-constexpr float kTopT = 13.f;                // log2 of the largest weight, when its reference moves
-constexpr float kMarginT = 15.f;             // and what moves it
-constexpr float kMarginM = 64.f;             // the same of the softmax terms, which move to 0
-static_assert(TILE_BYTES % 1024 == 0, "swizzled tiles start on 1 KiB");
 
 struct Params {
     const uint16_t* q;
@@ -97,56 +83,6 @@ __device__ __forceinline__ int runs_of(int groups, int total) {
     return max(1, min(groups, (total + KMIN - 1) / KMIN));
 }
 
-// First chunk of run r.
-__device__ __forceinline__ int run_begin(int r, int total, int runs) {
-    return static_cast<int>(static_cast<uint64_t>(r) * static_cast<uint32_t>(total) / static_cast<uint32_t>(runs));
-}
-
-struct Cursor {
-    int b, c, n;      // sequence, chunk within it, chunks of the sequence
-};
-
-__device__ __forceinline__ Cursor cursor_at(const int32_t* prefix, int batch, int i) {
-    int lo = 0, hi = batch;          // prefix[lo] <= i < prefix[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (prefix[mid] <= i) lo = mid; else hi = mid;
-    }
-    return Cursor{lo, i - prefix[lo], prefix[lo + 1] - prefix[lo]};
-}
-
-__device__ __forceinline__ void cursor_next(Cursor& cu, const int32_t* prefix, int batch) {
-    if (++cu.c < cu.n) return;
-    cu.c = 0;
-    do { ++cu.b; } while (cu.b < batch && prefix[cu.b + 1] == prefix[cu.b]);
-    cu.n = cu.b < batch ? prefix[cu.b + 1] - prefix[cu.b] : 0;
-}
-
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t transposed_8x8(uint32_t x) {
-    uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-__device__ __forceinline__ uint32_t ld_shared_u8(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
-    return v;
-}
-
 // The raw query words of this lane: head g = lane / 4 of the group, dims 32 (lane % 4) ... + 31.
 template <int G>
 __device__ __forceinline__ void load_q(const Params& p, int b, int kv_head, int lane, uint4 (&w)[4]) {
@@ -158,33 +94,6 @@ __device__ __forceinline__ void load_q(const Params& p, int b, int kv_head, int 
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(row) + i);
     }
-}
-
-// The query operand in f16 and, for the two heads 2t, 2t + 1 of this lane's columns, the factor
-// that turns a raw product into log2-domain scores.
-__device__ __forceinline__ void make_q(const uint4 (&w)[4], float scale_log2, int lane, uint32_t (&qb)[16], float (&qf)[2]) {
-    uint32_t amax = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) amax = max(amax, max((x[e] << 16) & 0x7fffffffu, x[e] & 0x7fff0000u));
-    }
-    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    // E: biased exponent of the row's largest magnitude, held where the factors stay normal (a row
-    // that is smaller than 2^-111 gives scores of 0 against any cache)
-    const int E = max(static_cast<int>(amax >> 23), 16);
-    const float mul = E == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float(static_cast<uint32_t>(268 - min(E, 254)) << 23);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) qb[4 * i + e] = pack_f16x2(bf16_lo(x[e]) * mul, bf16_hi(x[e]) * mul);
-    }
-    const float f = E == 255 ? mul : __uint_as_float(static_cast<uint32_t>(E - 14) << 23) * scale_log2;
-    qf[0] = __shfl_sync(0xffffffffu, f, (lane & 3) * 8);        // head 2t sits in lanes 8t .. 8t + 3
-    qf[1] = __shfl_sync(0xffffffffu, f, (lane & 3) * 8 + 4);
 }
 
 template <int G>
@@ -244,11 +153,9 @@ decode_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const int n_mine = run_begin(run_id + 1, total, W) - begin;
     if (n_mine <= 0) return;
 
-    const uint32_t stage0 = smem_u32(smem) + warp * STAGES * STAGE_BYTES;
-    const uint32_t scale0 = smem_u32(scales) + warp * STAGES * SCALE_BYTES;
-    const uint32_t bar0 = smem_u32(bars + warp * STAGES);
+    const Ring ring{smem_u32(smem) + warp * STAGES * STAGE_BYTES, smem_u32(scales) + warp * STAGES * SCALE_BYTES, smem_u32(bars + warp * STAGES)};
     if (lane == 0) {
-        for (int s = 0; s < STAGES; ++s) mbar_init(bar0 + 8 * s, 1);
+        for (int s = 0; s < STAGES; ++s) mbar_init(ring.bar0 + 8 * s, 1);
         fence_barrier_init();
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
@@ -256,40 +163,9 @@ decode_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     __syncwarp();
     const uint64_t policy = l2_policy_evict_first();
 
-    // ---- copies: a cursor of their own, the block it is in, and a window of 32 block-table entries
-    Cursor pc = cursor_at(prefix, p.batch, begin);
-    Cursor cc = pc;
-    int blk = pc.c * CHUNK / p.block_size, off = pc.c * CHUNK - blk * p.block_size;
-    int bt_b = -1, bt_base = 0, bt_lane = -1;
-    int issued = 0, put = 0;         // chunks issued; the stage the next one goes to
-    auto issue_next = [&]() {
-        if (pc.b != bt_b || blk < bt_base || blk >= bt_base + 32) {
-            bt_b = pc.b;
-            bt_base = blk;
-            const int at = bt_base + lane;
-            bt_lane = at < p.max_blocks ? __ldg(p.block_tables + static_cast<int64_t>(pc.b) * p.max_blocks + at) : -1;
-        }
-        const int phys = __shfl_sync(0xffffffffu, bt_lane, blk - bt_base);
-        if (lane == 0) {
-            const bool known = phys >= 0 && phys < p.num_blocks;
-            if (!known) record_error(p.err, PKV_DEVERR_BLOCK_ID, pc.b);
-            const uint32_t bar = bar0 + 8 * put;
-            const uint32_t dst = stage0 + put * STAGE_BYTES, sdst = scale0 + put * SCALE_BYTES;
-            // the tensor copies fill a block outside the pool with zeros; its scales come from block 0
-            const int64_t srow = (static_cast<int64_t>(known ? phys : 0) * hkv + head) * p.block_size + off;
-            mbar_arrive_expect_tx(bar, STAGE_BYTES + SCALE_BYTES);
-            tma_load_4d_hint(dst, &tm_k, bar, 0, head, off, phys, policy);
-            tma_load_4d_hint(dst + TILE_BYTES, &tm_v, bar, 0, head, off, phys, policy);
-            bulk_load(sdst, p.k_scale + srow, CHUNK, bar);
-            bulk_load(sdst + CHUNK, p.v_scale + srow, CHUNK, bar);
-        }
-        ++issued;
-        put = put + 1 == STAGES ? 0 : put + 1;
-        off += CHUNK;
-        if (off == p.block_size) { off = 0; ++blk; }
-        cursor_next(pc, prefix, p.batch);
-        if (pc.c == 0) blk = off = 0;
-    };
+    Cursor cc = cursor_at(prefix, p.batch, begin);
+    Copies copies(cc, p.block_size);
+    auto issue_next = [&]() { copies.next(tm_k, tm_v, p, ring, prefix, head, lane, policy); };
     for (int i = 0; i < min(n_mine, STAGES); ++i) issue_next();
 
     const int g = lane >> 2, t = lane & 3;
@@ -330,10 +206,10 @@ decode_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     uint32_t parity = 0;
     bool failed = false;
     for (; k < n_mine; ++k) {
-        const bool ok = mbar_wait(bar0 + 8 * st, parity, p.err, gw);
+        const bool ok = mbar_wait(ring.bar0 + 8 * st, parity, p.err, gw);
         if (__any_sync(0xffffffffu, !ok)) { failed = true; break; }
-        const uint32_t kb = stage0 + st * STAGE_BYTES, vb = kb + TILE_BYTES;
-        const uint32_t sb = scale0 + st * SCALE_BYTES;
+        const uint32_t kb = ring.stage0 + st * STAGE_BYTES, vb = kb + TILE_BYTES;
+        const uint32_t sb = ring.scale0 + st * SCALE_BYTES;
         if (++st == STAGES) { st = 0; parity ^= 1u; }
         const int valid = min(CHUNK, L - cc.c * CHUNK);
         if (valid < CHUNK) {
@@ -457,7 +333,7 @@ decode_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         }
         if (valid < CHUNK) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the cleared rows, before the stage's next copy
         __syncwarp();
-        if (issued < n_mine) issue_next();
+        if (copies.issued < n_mine) issue_next();
 
         // ---- end of the sequence or of the run: write the piece
         if (cc.c == cc.n - 1 || k == n_mine - 1) {
@@ -494,8 +370,8 @@ decode_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         }
     }
     if (failed)       // copies in flight land before the CTA's shared memory goes away
-        for (; k < issued; ++k) {
-            const bool ok = mbar_wait(bar0 + 8 * st, parity, p.err, gw);
+        for (; k < copies.issued; ++k) {
+            const bool ok = mbar_wait(ring.bar0 + 8 * st, parity, p.err, gw);
             if (++st == STAGES) { st = 0; parity ^= 1u; }
             if (__any_sync(0xffffffffu, !ok)) break;
         }

@@ -37,27 +37,15 @@
 //
 // Each warp owns a ring of stages in shared memory: a chunk's K and V codes (TMA, 128-byte
 // swizzle) and scale bytes, all landing on one mbarrier.
-#include <cuda_fp16.h>
-
 #include <algorithm>
 
-#include "pkv_device.cuh"
-#include "pkv_internal.h"
+#include "fp8_rows.cuh"
 
 namespace pkv {
 namespace {
 
-constexpr int D = kHeadDim;
-constexpr int CHUNK = 32;
-constexpr int TILE_BYTES = CHUNK * D;
-constexpr int STAGE_BYTES = 2 * TILE_BYTES;  // K, V
-constexpr int SCALE_BYTES = 2 * CHUNK;       // K scales, V scales
-constexpr int KMIN = 2;                      // chunks a run has at least, where the batch allows it
-constexpr float kTopT = 13.f;                // log2 of the largest weight, when its reference moves
-constexpr float kMarginT = 15.f;             // and what moves it
-constexpr float kMarginM = 64.f;             // the same of the softmax terms, which move to 0
+using namespace fp8_rows;
 
-constexpr int WARPS = 8, THREADS = WARPS * 32, STAGES = 3;
 // shared memory: stages, then scales, a barrier for each stage, the running sums
 constexpr int SM_SCALES = WARPS * STAGES * STAGE_BYTES, SM_BARS = SM_SCALES + WARPS * STAGES * SCALE_BYTES, SM_SUMS = SM_BARS + WARPS * STAGES * 8;
 constexpr size_t smem_bytes(int batch) { return SM_SUMS + WARPS * 4 + static_cast<size_t>(batch + 1) * 4; }
@@ -98,50 +86,7 @@ __device__ __forceinline__ bool sequence(const Params& p, int b, Seq& s) {
 __device__ __forceinline__ int chunks_of(const Seq& s) { return s.n ? (s.len + CHUNK - 1) / CHUNK : 0; }
 
 __device__ __forceinline__ int runs_of(int groups, int total) { return max(1, min(groups, total / KMIN)); }
-__device__ __forceinline__ int run_begin(int r, int total, int runs) {
-    return static_cast<int>(static_cast<uint64_t>(r) * static_cast<uint32_t>(total) / static_cast<uint32_t>(runs));
-}
-
-struct Cursor {
-    int b, c, n;      // sequence, chunk within it, chunks of the sequence
-};
-__device__ __forceinline__ Cursor cursor_at(const int32_t* prefix, int batch, int i) {
-    int lo = 0, hi = batch;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (prefix[mid] <= i) lo = mid; else hi = mid;
-    }
-    return Cursor{lo, i - prefix[lo], prefix[lo + 1] - prefix[lo]};
-}
-__device__ __forceinline__ void cursor_next(Cursor& cu, const int32_t* prefix, int batch) {
-    if (++cu.c < cu.n) return;
-    cu.c = 0;
-    do { ++cu.b; } while (cu.b < batch && prefix[cu.b + 1] == prefix[cu.b]);
-    cu.n = cu.b < batch ? prefix[cu.b + 1] - prefix[cu.b] : 0;
-}
-
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t transposed_8x8(uint32_t x) {
-    uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t ld_shared_u8(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
-    return v;
-}
-
-// Which of a chunk's 32 keys a row sees: w, its node's mask (no tree here has more than 32 nodes; all ones for a row that is
+// Which of a chunk's 32 keys a row sees: w, its node's mask (no tree here has more than 16 nodes; all ones for a row that is
 // nobody's); `first` is the node of the chunk's first key (negative before the tree, above -32), `keys` the sequence's
 // keys in the chunk.
 __device__ __forceinline__ uint32_t visible(uint32_t w, int first, int keys) {
@@ -205,11 +150,10 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         if (lane == 0) p.meta[gw] = meta;
         return;
     }
-    const uint32_t stage0 = smem_u32(smem) + warp * STAGES * STAGE_BYTES;
-    const uint32_t scale0 = smem_u32(smem + SM_SCALES) + warp * STAGES * SCALE_BYTES;
-    const uint32_t bar0 = smem_u32(smem + SM_BARS) + warp * STAGES * 8;
+    const Ring ring{smem_u32(smem) + warp * STAGES * STAGE_BYTES, smem_u32(smem + SM_SCALES) + warp * STAGES * SCALE_BYTES,
+                    smem_u32(smem + SM_BARS) + warp * STAGES * 8};
     if (lane == 0) {
-        for (int s = 0; s < STAGES; ++s) mbar_init(bar0 + 8 * s, 1);
+        for (int s = 0; s < STAGES; ++s) mbar_init(ring.bar0 + 8 * s, 1);
         fence_barrier_init();
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
@@ -217,39 +161,9 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     __syncwarp();
     const uint64_t policy = l2_policy_evict_first();
 
-    // ---- copies: a cursor of their own, the block it is in, and a window of 32 block-table entries
-    Cursor pc = cursor_at(prefix, p.batch, begin);
-    Cursor cc = pc;
-    int blk = pc.c * CHUNK / p.block_size, off = pc.c * CHUNK - blk * p.block_size;
-    int bt_b = -1, bt_base = 0, bt_lane = -1;
-    int issued = 0, put = 0;
-    auto issue_next = [&]() {
-        if (pc.b != bt_b || blk < bt_base || blk >= bt_base + 32) {
-            bt_b = pc.b;
-            bt_base = blk;
-            const int at = bt_base + lane;
-            bt_lane = at < p.max_blocks ? __ldg(p.block_tables + static_cast<int64_t>(pc.b) * p.max_blocks + at) : -1;
-        }
-        const int phys = __shfl_sync(0xffffffffu, bt_lane, blk - bt_base);
-        if (lane == 0) {
-            const bool known = phys >= 0 && phys < p.num_blocks;
-            if (!known) record_error(p.err, PKV_DEVERR_BLOCK_ID, pc.b);
-            const uint32_t bar = bar0 + 8 * put, dst = stage0 + put * STAGE_BYTES, sdst = scale0 + put * SCALE_BYTES;
-            // the tensor copies fill a block outside the pool with zeros; its scales come from block 0
-            const int64_t srow = (static_cast<int64_t>(known ? phys : 0) * hkv + head) * p.block_size + off;
-            mbar_arrive_expect_tx(bar, STAGE_BYTES + SCALE_BYTES);
-            tma_load_4d_hint(dst, &tm_k, bar, 0, head, off, phys, policy);
-            tma_load_4d_hint(dst + TILE_BYTES, &tm_v, bar, 0, head, off, phys, policy);
-            bulk_load(sdst, p.k_scale + srow, CHUNK, bar);
-            bulk_load(sdst + CHUNK, p.v_scale + srow, CHUNK, bar);
-        }
-        ++issued;
-        put = put + 1 == STAGES ? 0 : put + 1;
-        off += CHUNK;
-        if (off == p.block_size) { off = 0; ++blk; }
-        cursor_next(pc, prefix, p.batch);
-        if (pc.c == 0) blk = off = 0;
-    };
+    Cursor cc = cursor_at(prefix, p.batch, begin);
+    Copies copies(cc, p.block_size);
+    auto issue_next = [&]() { copies.next(tm_k, tm_v, p, ring, prefix, head, lane, policy); };
     for (int i = 0; i < min(n_mine, STAGES); ++i) issue_next();
 
     const int g = lane >> 2, t = lane & 3;
@@ -279,27 +193,7 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 #pragma unroll
                 for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(row) + i);
             }
-            uint32_t amax = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t y[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) amax = max(amax, max((y[e] << 16) & 0x7fffffffu, y[e] & 0x7fff0000u));
-            }
-            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            // E: biased exponent of the row's largest magnitude, held where the factors stay normal
-            const int E = max(static_cast<int>(amax >> 23), 16);
-            const float mul = E == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float(static_cast<uint32_t>(268 - min(E, 254)) << 23);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t y[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) qb[x][4 * i + e] = pack_f16x2(bf16_lo(y[e]) * mul, bf16_hi(y[e]) * mul);
-            }
-            const float f = E == 255 ? mul : __uint_as_float(static_cast<uint32_t>(E - 14) << 23) * p.scale_log2;
-            qf[x][0] = __shfl_sync(0xffffffffu, f, (lane & 3) * 8);        // row 2t sits in lanes 8t .. 8t + 3
-            qf[x][1] = __shfl_sync(0xffffffffu, f, (lane & 3) * 8 + 4);
+            make_q(w, p.scale_log2, lane, qb[x], qf[x]);
         }
     };
     enter();
@@ -325,10 +219,10 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     uint32_t parity = 0;
     bool failed = false;
     for (; k < n_mine; ++k) {
-        const bool ok = mbar_wait(bar0 + 8 * st, parity, p.err, gw);
+        const bool ok = mbar_wait(ring.bar0 + 8 * st, parity, p.err, gw);
         if (__any_sync(0xffffffffu, !ok)) { failed = true; break; }
-        const uint32_t kb = stage0 + st * STAGE_BYTES, vb = kb + TILE_BYTES;
-        const uint32_t sb = scale0 + st * SCALE_BYTES;
+        const uint32_t kb = ring.stage0 + st * STAGE_BYTES, vb = kb + TILE_BYTES;
+        const uint32_t sb = ring.scale0 + st * SCALE_BYTES;
         if (++st == STAGES) { st = 0; parity ^= 1u; }
         const int valid = min(CHUNK, s.len - cc.c * CHUNK), first = cc.c * CHUNK - (s.len - s.n);
         const bool tree = first + CHUNK > 0;               // nodes among the keys, in the last chunks
@@ -522,7 +416,7 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         }
         if (tree) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // what was cleared, before the stage's next copy
         __syncwarp();
-        if (issued < n_mine) issue_next();
+        if (copies.issued < n_mine) issue_next();
 
         // ---- end of the sequence or of the run: its rows, or what this run knows of them
         if (cc.c == cc.n - 1 || k == n_mine - 1) {
@@ -573,8 +467,8 @@ tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         }
     }
     if (failed)       // copies in flight land before the CTA's shared memory goes away
-        for (; k < issued; ++k) {
-            const bool ok = mbar_wait(bar0 + 8 * st, parity, p.err, gw);
+        for (; k < copies.issued; ++k) {
+            const bool ok = mbar_wait(ring.bar0 + 8 * st, parity, p.err, gw);
             if (++st == STAGES) { st = 0; parity ^= 1u; }
             if (__any_sync(0xffffffffu, !ok)) break;
         }
