@@ -560,7 +560,8 @@ PKV_API pkv_status pkv_sample_filtered_dev(const float *logits, int32_t batch, i
  * batch <= 4096.  fp32 scores and sums; a key's weight is rounded to bf16 for the product
  * with the values (2^-8 of itself at most), the output once to bf16.  Deterministic.  Values that
  * are finite in bf16 give finite results, whatever their number (one within 2^-8 of bf16's largest
- * may be rounded to an infinity); results are right to 2^-128 where that is more than the roundings.
+ * may be rounded to an infinity; scores are taken to be below 2^27, beyond which fp32 tells no weights
+ * apart); results are right to 2^-128 where that is more than the roundings.
  * pkv_tree_decode_fp8 is the same over an 8-bit cache.  More than 16 rows to a KV head
  * (max_nodes * num_heads / num_kv_heads): a query is split into two e4m3 parts, exact from 2^-9 of
  * the row's largest element and off by at most 2^-17 of it, and weights are rounded to bf16 as above;
@@ -625,8 +626,9 @@ PKV_API pkv_status pkv_tree_accept(const int64_t *target, const int64_t *draft, 
  * d < path_lens[b], in K and V (and their scales) of every layer.  context_lens and cu_nodes are
  * those of the step.  A path that does not ascend, or leaves its tree, is not moved and
  * PKV_DEVERR_TREE recorded (info = sequence).  A block id outside the pool records
- * PKV_DEVERR_BLOCK_ID and its row stays.  Exact copies.  No two sequences of a call may have a
- * block of their nodes' rows in common.  batch <= 65535.
+ * PKV_DEVERR_BLOCK_ID and its row stays.  A sequence with path_lens 0 is passed over, whatever its
+ * bounds.  Exact copies.  No two sequences of a call may have a block of their nodes' rows in common.
+ * batch <= 65535.
  */
 PKV_API pkv_status pkv_tree_compact(void *const *k_caches, void *const *v_caches, pkv_e8m0 *const *k_scales,
                             pkv_e8m0 *const *v_scales, int32_t num_layers, const int32_t *block_tables,
@@ -645,7 +647,7 @@ PKV_API pkv_status pkv_tree_compact(void *const *k_caches, void *const *v_caches
  *             Rows behind them stay as they are in the destination.
  * A destination may be no other pair's source or destination.  Ids outside the pool record
  * PKV_DEVERR_BLOCK_ID, row counts outside [0, block_size] PKV_DEVERR_SEQLENS, info = pair, and the
- * pair is skipped.  Exact copies.  num_pairs <= 65535.
+ * pair is skipped; one with no rows to copy is passed over, whatever its ids.  Exact copies.  num_pairs <= 65535.
  */
 PKV_API pkv_status pkv_copy_blocks(void *const *k_caches, void *const *v_caches, pkv_e8m0 *const *k_scales,
                            pkv_e8m0 *const *v_scales, int32_t num_layers, const int32_t *src_blocks,

@@ -31,10 +31,10 @@
 // Trees of 16 rows or fewer on the 8-bit cache are another kernel's (tree_decode_rows.cu).
 //
 // Measured (calls in a graph, 8 KV heads): batch 64 with 512 to 4096 keys and 12 to 16
-// nodes, G = 2, 575 MB: 99 us, 5.8 TB/s; 8 sequences of 16k to 40k keys, 60 nodes, 964 MB:
-// 155 us, 6.2 TB/s: HBM.  32 sequences of 80 to 2999 keys, 33 to 64 nodes, G = 4, 46 GFLOP: 73
+// nodes, G = 2, 575 MB: 98 us, 5.9 TB/s; 8 sequences of 16k to 40k keys, 60 nodes, 964 MB:
+// 156 us, 6.2 TB/s: HBM.  32 sequences of 80 to 2999 keys, 33 to 64 nodes, G = 4, 46 GFLOP: 73
 // us, bound by the steps of a tile (S, softmax, P, O), which wait on one another.  8-bit cache: the
-// first case 101 us, 7 sequences of 16k to 40k keys, 13 to 29 nodes, G = 8: 129, bound by the same steps,
+// first case 99 us, 7 sequences of 16k to 40k keys, 13 to 29 nodes, G = 8: 128, bound by the same steps,
 // whose waits and loads shared memory answers late (some 180 cycles beside the products' reads).  So
 // each step of its softmax takes one pass over the scores, 32 at a time with their scales loaded a
 // step ahead (two passes of 16: 110 and 156 us; one of 16: 107 and 142).  Its loops are kept rolled and
@@ -382,8 +382,8 @@ __device__ __forceinline__ uint32_t widen(uint32_t w) {
 }
 
 // 16 e4m3 codes and their row's scale byte as 16 bf16.  A code's bits, set one exponent field further, read as a bf16
-// 2^-120 times its value (its subnormals as bf16's), so a product with 2^120 times the scale, in two factors where one
-// would not fit, is exact; only the NaN code needs to be seen.
+// 2^-120 times its value (its subnormals as bf16's), so a product with 2^120 times the scale is exact where bf16 holds that
+// factor, scales of 2^-119 to 2^7.  Rows with other scales or with a NaN code (ODD) go by way of f16 and fp32.
 __device__ __forceinline__ bool odd_row(const uint4& c, uint32_t byte) {      // a NaN code, or a scale outside 2^-119 .. 2^7
     const uint32_t nan = ((c.x & 0x7f7f7f7fu) + 0x01010101u) | ((c.y & 0x7f7f7f7fu) + 0x01010101u) | ((c.z & 0x7f7f7f7fu) + 0x01010101u) |
                          ((c.w & 0x7f7f7f7fu) + 0x01010101u);
@@ -541,7 +541,8 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     };
     // Sums over the sequences of a row tile's cost, alone (x) and times the row tiles (y).  Where every sequence has the same
     // number of row tiles, more than one, they are taken side by side like the KV heads, by neighbouring CTAs: what one
-    // reads from memory the other finds in L2 (33 to 64 nodes of 4 heads, batch of 32: 403 MB read one after the other).
+    // reads from memory the other finds in L2 (33 to 64 nodes of 4 heads, batch of 32: 73 us and 270 MB read).  Elsewhere
+    // they go one after the other (the same with one tree of one node: 85 us and 398 MB).
     long long x = 0, y = 0, x_first = 0, y_first = 0;
     int least = 0x7fffffff, most = 0;
 #pragma unroll 1

@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(32 * ACCEPT_WARPS) tree_accept_kernel(const Tr
 // many pools as that takes, one warp lists the rows that move (and where their scales lie: a division by the block size
 // costs more than a move), and the 8-bit rows' scales have a warp of their own.
 // Measured in a graph: one sequence, 28 layers 2.4 us; 128 sequences on the 8-bit cache, 52 MB in rows of 1 KB and
-// single scale bytes, 16.9 us (3.1 TB/s); 128 on bf16, 103 MB, 23.7 us.
+// single scale bytes, 15.9 us (3.3 TB/s); 128 on bf16, 103 MB, 24.1 us.
 constexpr int ROW_THREADS = 256, COMPACT_THREADS = ROW_THREADS + 32, COMPACT_CTAS = 5, BATCH = 4;
 
 __global__ void __launch_bounds__(COMPACT_THREADS, COMPACT_CTAS)
