@@ -561,7 +561,8 @@ PKV_API pkv_status pkv_sample_filtered_dev(const float *logits, int32_t batch, i
  * with the values (2^-8 of itself at most), the output once to bf16.  Deterministic.  Values that
  * are finite in bf16 give finite results, whatever their number (one within 2^-8 of bf16's largest
  * may be rounded to an infinity; scores are taken to be below 2^27, beyond which fp32 tells no weights
- * apart); results are right to 2^-128 where that is more than the roundings.
+ * apart); results are right to 2^-128 where that is more than the roundings, and a key that weighs less
+ * than 2^-108 of its row's sum counts as nothing.
  * pkv_tree_decode_fp8 is the same over an 8-bit cache.  More than 16 rows to a KV head
  * (max_nodes * num_heads / num_kv_heads): a query is split into two e4m3 parts, exact from 2^-9 of
  * the row's largest element and off by at most 2^-17 of it, and weights are rounded to bf16 as above;

@@ -61,10 +61,10 @@ constexpr int KV_HALF = KT * 64 * 2;         // 8 KiB of K or V
 constexpr int KV_TILE = 2 * KV_HALF;
 constexpr int TMEM_COLS = 256;
 constexpr int O_COL = 128;                   // S / P buffers at columns 0 and 64
-// A row's reference is put 2^16 above its largest weight and moved again once the weights' sum has passed 1/4 (bf16: or one
-// of the tile's weights 2^-8, and 64 of those make another 1/4).  So the sum stays below 1/2, and with it |O| / 2^127 for any
-// finite V.  2^16, so that long contexts seldom move it (32768 equal keys); less than that leaves O more of fp32's range at
-// the lower end, where V of 2^-118 keeps 14 bits.
+// A row's reference is put 2^16 above its largest score and moved again once the weights' sum has passed 1/4 (bf16: or one
+// of the tile's weights 2^-8, and 64 of those make another 1/4).  So the sum stays below 1/2 and |O| below 2^127 for any
+// finite V.  2^16, so that long contexts seldom move it (16384 equal keys); a lower one would leave O more of fp32's range at
+// the lower end, where V of 2^-118 keeps 14 bits.  The sum is 2^-18 at least, and weights end at 2^-126: at 2^-108 of it.
 constexpr float kLift = 16.0f;
 constexpr float kMostWeightLog2 = -8.0f;
 constexpr float kMostSum = 0.25f;
